@@ -542,6 +542,114 @@ qd_status qd_batch_set_graphs(qd_batch_handle b, int enable);
  * step scratch.  Synchronises. */
 qd_status qd_batch_time_kernel(qd_batch_handle b, int which, int reps, float *avg_ms);
 
+/* ---- a batch of streams over cached keys and values ----
+ *
+ * Operators for callers that hold the streams' caches themselves (one layer at a time)
+ * and decode, with several new tokens a stream where tokens were drafted:
+ * qd_kv_append writes the new tokens' keys and values, qd_attn_cached attends over
+ * the caches, qd_verify_drafts accepts or replaces drafted tokens.  All of them take the same
+ * two arrays: lengths_dev (DEVICE int32 [n_streams]), the positions each stream holds
+ * INCLUDING its new tokens, and n_new_dev (DEVICE int32 [n_streams] or NULL: n_tokens
+ * for every stream), how many of the call's n_tokens rows the stream uses (values
+ * outside [0, n_tokens] are taken as the nearest end).  Row t < n_new[b] of stream b
+ * stands at position lengths[b] - n_new[b] + t; rows from n_new[b] on are neither read
+ * nor written.  Both arrays are read on the device, so a captured graph serves growing
+ * streams.  The calls are asynchronous on cuda_stream, allocate nothing and keep
+ * nothing between calls.  Every pointer is memory of the current device: QD_EINVAL
+ * otherwise. */
+enum { QD_KV_BF16 = 0, QD_KV_Q8 = 1 };
+
+/* One layer's cached keys and values (a view: the caller owns the memory).  Element
+ * (stream b, head h, position j, dim d) of K is k[b * stream_stride + h * head_stride +
+ * j * row_stride + d], the same for V; strides in elements.  QD_KV_BF16: bf16.
+ * QD_KV_Q8: int8 codes with one fp32 scale a row, k_scale[b * scale_stream_stride + h *
+ * scale_head_stride + j] (scales NULL and their strides unread for QD_KV_BF16); an
+ * element stands for code * scale.  k and v are 16-byte aligned, the strides multiples
+ * of 16 bytes and rows at least head_dim apart.  head_dim is 64 or 128. */
+typedef struct {
+    void *k, *v;
+    float *k_scale, *v_scale;
+    int format, n_streams, n_kv_heads, smax, head_dim;
+    int64_t stream_stride, head_stride, row_stride;
+    int64_t scale_stream_stride, scale_head_stride;
+} qd_kv_cache;
+
+/* qd_kv_append -- write the new tokens' rows into the cache.  k_rows_dev, v_rows_dev:
+ * DEVICE fp32 or bf16 (dtype), head h of row t of stream b at b * stream_stride + t *
+ * token_stride + h * head_stride elements (slices of a fused projection serve as they
+ * are), 16-byte aligned with strides of 16-byte multiples.  QD_KV_BF16 rounds to
+ * nearest even.  QD_KV_Q8, per row in fp32: scale = max|x| / 127, code = nearest integer
+ * (ties to even) to x * (127 / max|x|); a row below 2^-116 throughout is stored as zeros,
+ * and one that holds an infinity or a NaN as codes 0 with a NaN scale, so that it reads
+ * as NaN.  A row whose position falls outside [0, smax) is not written.  Errors:
+ * QD_EINVAL (arguments, alignment, memory), QD_EUNSUPPORTED (head_dim), QD_ECUDA. */
+qd_status qd_kv_append(const qd_kv_cache *cache, const void *k_rows_dev, const void *v_rows_dev, int dtype,
+                       int n_tokens, int64_t stream_stride, int64_t token_stride, int64_t head_stride,
+                       const int32_t *lengths_dev, const int32_t *n_new_dev, void *cuda_stream);
+
+/* qd_kv_read -- the inverse: the rows that qd_kv_append with the same lengths would
+ * write, read back into k_rows_dev and v_rows_dev as fp32 or bf16 (code * scale in fp32, rounded
+ * to nearest even).  A row whose position falls outside [0, smax) is left as it is.
+ * Layout and errors as qd_kv_append. */
+qd_status qd_kv_read(const qd_kv_cache *cache, void *k_rows_dev, void *v_rows_dev, int dtype, int n_tokens,
+                     int64_t stream_stride, int64_t token_stride, int64_t head_stride, const int32_t *lengths_dev,
+                     const int32_t *n_new_dev, void *cuda_stream);
+
+/* qd_attn_cached -- attention of every stream's new tokens over its own cache and, where
+ * `prefix` is given, over a prefix that all streams share:
+ *   out[b][t][h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q[b][t][h] . k_j - max)
+ * over the prefix's positions [0, prefix_length) and the stream's positions j <
+ * lengths[b] - (n_new[b] - 1 - t) (its own and the new tokens up to itself; lengths
+ * outside [0, max_length] are taken as the nearest end), with key/value head h /
+ * (n_q_heads / n_kv_heads).  A query that sees no position gives zeros.  What stands
+ * at positions a query does not see never reaches its result, NaN and infinity
+ * included; an infinite value that it does see makes its dim infinite or NaN,
+ * and an infinite key, or a product beyond fp32's range, may make it NaN where the query has
+ * parts (fp32).
+ * q_dev, out_dev: DEVICE fp32 or bf16 (dtype, the same for both), head h of row t of
+ * stream b at b * stream_stride + t * token_stride + h * head_dim elements, each with its own strides,
+ * 16-byte aligned with strides of 16-byte multiples; q and out must not overlap.
+ * Scores, softmax and sums are fp32; fp32 queries and their probabilities keep at
+ * least 22 bits through the products, bf16 ones at least 11.
+ * prefix: one stream of n_kv_heads heads in either format (its strides for streams are
+ * unread), read once for the whole batch; NULL or prefix_length 0: none.
+ * n_tokens <= 64, max_length in [1, cache->smax] bounds the lengths (it plans the launch).
+ * workspace_dev: DEVICE, 256-byte aligned, qd_attn_cached_workspace bytes (0 without a
+ * prefix: NULL is allowed).  It is scratch of one call: calls, or captured graphs, that
+ * may run at the same time need their own.  Errors: QD_EINVAL (arguments, alignment,
+ * memory, workspace), QD_EUNSUPPORTED (head_dim, n_tokens), QD_ECUDA. */
+qd_status qd_attn_cached(const qd_kv_cache *cache, const qd_kv_cache *prefix, int prefix_length, const void *q_dev,
+                         int64_t q_stream_stride, int64_t q_token_stride, void *out_dev, int64_t out_stream_stride,
+                         int64_t out_token_stride, int dtype, int n_tokens, int n_q_heads, float scale,
+                         const int32_t *lengths_dev, const int32_t *n_new_dev, int max_length, void *workspace_dev,
+                         size_t workspace_bytes, void *cuda_stream);
+
+/* Bytes of workspace that qd_attn_cached needs for these sizes (HOST *bytes). */
+qd_status qd_attn_cached_workspace(int n_streams, int n_tokens, int n_q_heads, int n_kv_heads, int head_dim,
+                                   int prefix_length, size_t *bytes);
+
+/* qd_verify_drafts -- speculative sampling's verification (the accepted and the drawn tokens
+ * follow the target's distribution).  target_probs_dev: DEVICE fp32, the target's
+ * probabilities p of position t < n_tokens + 1 of stream b at b * target_stream_stride +
+ * t * target_row_stride elements, vocab of them; draft_probs_dev: the drafter's q for t
+ * < n_tokens, likewise, or NULL for drafts that were not sampled (q is 1 at the drafted
+ * id).  draft_ids_dev: DEVICE int32 [n_streams][n_tokens]; n_draft_dev: DEVICE int32
+ * [n_streams] or NULL, how many of them the stream has.  u_dev: DEVICE fp32 [n_streams][n_tokens + 1],
+ * uniform in [0, 1): draft t passes if u[b][t] * q(x) < p(x), exactly; the last one is
+ * for the token drawn.  out_ids_dev: DEVICE int32 [n_streams][n_tokens + 1]: the drafts
+ * up to the first that fails, then one id drawn from max(p - q, 0) of the failing
+ * position (from p where that is zero throughout), or from p of the position after the
+ * last draft when all passed, then -1.  n_accepted_dev: DEVICE int32 [n_streams], the
+ * drafts that passed.  The draw takes each weight w as the whole number floor(w * 2^44)
+ * (below 0 and NaN as 0, above 1 as 1) and gives the first id whose running sum exceeds floor(u *
+ * sum) (the product in fp64), so the result does not depend on the order of
+ * summation; where every weight is 0 it gives -1.  A drafted id outside [0, vocab)
+ * fails.  vocab <= 524288, n_tokens in [1, 64].  Errors: QD_EINVAL, QD_ECUDA. */
+qd_status qd_verify_drafts(const float *target_probs_dev, int64_t target_stream_stride, int64_t target_row_stride,
+                           const float *draft_probs_dev, int64_t draft_stream_stride, int64_t draft_row_stride,
+                           const int32_t *draft_ids_dev, const int32_t *n_draft_dev, const float *u_dev, int n_streams,
+                           int n_tokens, int vocab, int32_t *out_ids_dev, int32_t *n_accepted_dev, void *cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -42,7 +42,8 @@ EXPORTS = ("qd_create", "qd_destroy", "qd_reset", "qd_prefill", "qd_prefill_mrop
            "qd_conv_transpose1d_causal_tc", "qd_batch_create", "qd_batch_destroy",
            "qd_batch_set_stream", "qd_batch_decode", "qd_batch_sync", "qd_batch_get_logits", "qd_batch_copy_kv",
            "qd_batch_get_pos", "qd_batch_get_launch_count", "qd_batch_set_graphs", "qd_batch_time_kernel", "qd_batch_prefill",
-           "qd_batch_set_sampling")
+           "qd_batch_set_sampling", "qd_kv_append", "qd_kv_read", "qd_attn_cached", "qd_attn_cached_workspace",
+           "qd_verify_drafts")
 
 
 class qd_config(ctypes.Structure):
@@ -62,6 +63,14 @@ class qd_layer_weights(ctypes.Structure):
 class qd_weights(ctypes.Structure):
     _fields_ = [("embed", ctypes.c_void_p), ("final_norm", ctypes.c_void_p),
                 ("lm_head", ctypes.c_void_p * QD_MAX_HEADS), ("layers", ctypes.POINTER(qd_layer_weights))]
+
+
+class qd_kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)] + [
+        (n, ctypes.c_int) for n in ("format", "n_streams", "n_kv_heads", "smax", "head_dim")] + [
+        (n, ctypes.c_int64) for n in ("stream_stride", "head_stride", "row_stride", "scale_stream_stride",
+                                      "scale_head_stride")]
 
 
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t
@@ -114,6 +123,12 @@ _SIGS = {
     "qd_batch_set_graphs": ([_vp, _i32], _i32),
     "qd_batch_time_kernel": ([_vp, _i32, _i32, _P(ctypes.c_float)], _i32),
     "qd_batch_prefill": ([_vp, _vp, _i32, _vp, _i32, _vp], _i32),
+    "qd_kv_append": ([_vp, _vp, _vp, _i32, _i32, _i64, _i64, _i64, _vp, _vp, _vp], _i32),
+    "qd_kv_read": ([_vp, _vp, _vp, _i32, _i32, _i64, _i64, _i64, _vp, _vp, _vp], _i32),
+    "qd_attn_cached": ([_vp, _vp, _i32, _vp, _i64, _i64, _vp, _i64, _i64, _i32, _i32, _i32, ctypes.c_float, _vp, _vp,
+                        _i32, _vp, _sz, _vp], _i32),
+    "qd_attn_cached_workspace": ([_i32, _i32, _i32, _i32, _i32, _i32, _P(_sz)], _i32),
+    "qd_verify_drafts": ([_vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp], _i32),
 }
 for _name, (_args, _res) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -594,3 +609,174 @@ def qd_conv_transpose1d_causal_tc(x_dev, w_dev, bias_dev=None, stride: int = 2, 
     if st != QD_OK:
         raise QDError(st, "qd_conv_transpose1d_causal_tc failed")
     return (y, ms.value) if time_reps > 0 else y
+
+
+QD_KV_BF16, QD_KV_Q8 = 0, 1
+
+
+class KvCache:
+    """View of one layer's cached keys and values held in the caller's device tensors
+    (``qd_kv_cache`` in qd.h; it keeps the tensors alive, copies nothing).
+
+    k, v: [streams, kv_heads, positions, head_dim] with equal strides, the last 1: bf16, or
+    int8 codes with k_scale, v_scale fp32 [streams, kv_heads, positions] (last stride 1).
+    Any order of the first three axes in memory serves: ``x.transpose(1, 2)`` of a
+    [streams, positions, kv_heads, head_dim] tensor is such a view."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        import torch
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or k.stride(3) != 1:
+            raise ValueError("k and v must be alike: [streams, kv_heads, positions, head_dim], rows contiguous")
+        if k.dtype == torch.bfloat16:
+            if k_scale is not None or v_scale is not None:
+                raise ValueError("a bf16 cache has no scales")
+            fmt, ss = QD_KV_BF16, (0, 0)
+        elif k.dtype == torch.int8:
+            if k_scale is None or v_scale is None:
+                raise ValueError("an 8-bit cache needs k_scale and v_scale")
+            for s in (k_scale, v_scale):
+                if s.dtype != torch.float32 or s.shape != k.shape[:3] or s.stride() != k_scale.stride():
+                    raise ValueError("scales must be alike: fp32 [streams, kv_heads, positions]")
+            if k.shape[2] > 1 and k_scale.stride(2) != 1:
+                raise ValueError("a head's scales must be contiguous")
+            fmt, ss = QD_KV_Q8, k_scale.stride()[:2]
+        else:
+            raise ValueError(f"unsupported cache type {k.dtype}")
+        self.tensors = (k, v, k_scale, v_scale)
+        self.shape = tuple(k.shape)
+        B, H, S, D = k.shape
+        st = k.stride()
+        # the stride of an axis of one is free: take one that passes as contiguous
+        row = st[2] if S > 1 else D
+        self.c = qd_kv_cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), fmt, B, H, S, D,
+                             st[0] if B > 1 else 0, st[1] if H > 1 else 0, row, ss[0] if B > 1 else 0,
+                             ss[1] if H > 1 else 0)
+        self.addr = ctypes.addressof(self.c)
+
+
+def _op_stream(stream):
+    """The caller's stream, by default the current one (memory of another device is refused)."""
+    import torch
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+
+
+def _op_dtype(t) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return QD_BF16
+    if t.dtype == torch.float32:
+        return QD_F32
+    raise ValueError(f"fp32 or bf16 wanted, got {t.dtype}")
+
+
+def _op_ints(t, n: int, what: str):
+    """A contiguous int32 tensor of n values (or None) as an address."""
+    import torch
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be {n} contiguous int32 values")
+    return t.data_ptr()
+
+
+def _kv_rows(fn, name, cache, k_rows, v_rows, lengths, n_new, stream):
+    B, H, _, D = cache.shape
+    if k_rows.dim() != 4 or k_rows.shape != v_rows.shape or k_rows.stride() != v_rows.stride() or \
+            k_rows.dtype != v_rows.dtype or k_rows.shape[0] != B or tuple(k_rows.shape[2:]) != (H, D) or \
+            k_rows.stride(3) != 1:
+        raise ValueError(f"k_rows and v_rows must be alike: [{B}, tokens, {H}, {D}], heads contiguous")
+    T = k_rows.shape[1]
+    s = k_rows.stride()
+    st = fn(cache.addr, k_rows.data_ptr(), v_rows.data_ptr(), _op_dtype(k_rows), T, s[0] if B > 1 else 0,
+            s[1] if T > 1 else 0, s[2] if H > 1 else 0, _op_ints(lengths, B, "lengths"),
+            _op_ints(n_new, B, "n_new"), _op_stream(stream))
+    if st != QD_OK:
+        raise QDError(st, f"{name} failed")
+
+
+def qd_kv_append(cache: KvCache, k_rows, v_rows, lengths, n_new=None, stream=None):
+    """Write the new tokens' rows (fp32 or bf16 [streams, tokens, kv_heads, head_dim], slices of
+    a fused projection as they are) into the cache; lengths (int32 [streams]) counts them in."""
+    _kv_rows(_lib.qd_kv_append, "qd_kv_append", cache, k_rows, v_rows, lengths, n_new, stream)
+
+
+def qd_kv_read(cache: KvCache, lengths, k_rows, v_rows, n_new=None, stream=None):
+    """Read the rows that qd_kv_append with the same lengths writes back into k_rows and v_rows."""
+    _kv_rows(_lib.qd_kv_read, "qd_kv_read", cache, k_rows, v_rows, lengths, n_new, stream)
+
+
+def qd_attn_cached_workspace(n_streams: int, n_tokens: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
+                             prefix_length: int) -> int:
+    n = ctypes.c_size_t(0)
+    st = _lib.qd_attn_cached_workspace(n_streams, n_tokens, n_q_heads, n_kv_heads, head_dim, prefix_length,
+                                       ctypes.byref(n))
+    if st != QD_OK:
+        raise QDError(st, "qd_attn_cached_workspace failed")
+    return n.value
+
+
+def qd_attn_cached(q, cache: KvCache, lengths, out, n_new=None, max_length: Optional[int] = None, scale=None,
+                   prefix: Optional[KvCache] = None, prefix_length: Optional[int] = None, workspace=None, stream=None):
+    """Attention of the new tokens q [streams, tokens, q_heads, head_dim] (fp32 or bf16) over
+    each stream's cache and the shared prefix (a KvCache of one stream) into out (same type
+    and shape).  max_length: bound of the lengths (default: the cache's positions); scale:
+    default head_dim ** -0.5; prefix_length: default all of the prefix.  workspace: uint8
+    tensor of qd_attn_cached_workspace bytes, of this call alone while it runs; by default
+    one is taken from torch's allocator, on the stream that the call runs on."""
+    import torch
+    B, H, S, D = cache.shape
+    if q.dim() != 4 or q.shape != out.shape or q.dtype != out.dtype or q.shape[0] != B or q.shape[3] != D:
+        raise ValueError(f"q and out must be [{B}, tokens, q_heads, {D}] of one type")
+    _, T, QH, _ = q.shape
+    qs, os_ = q.stride(), out.stride()
+    if qs[3] != 1 or os_[3] != 1 or (QH > 1 and (qs[2] != D or os_[2] != D)):
+        raise ValueError("the heads of q and out must be contiguous")
+    P, need = 0, 0
+    if prefix is not None:
+        P = prefix.shape[2] if prefix_length is None else int(prefix_length)
+        if prefix.shape[0] != 1:
+            raise ValueError("the prefix is a cache of one stream")
+    elif prefix_length:
+        raise ValueError("prefix_length without a prefix")
+    if P > 0 and workspace is None:
+        need = qd_attn_cached_workspace(B, T, QH, H, D, P)
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        else:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    st = _lib.qd_attn_cached(cache.addr, prefix.addr if P > 0 else None, P, q.data_ptr(), qs[0] if B > 1 else 0,
+                             qs[1] if T > 1 else 0, out.data_ptr(), os_[0] if B > 1 else 0, os_[1] if T > 1 else 0,
+                             _op_dtype(q), T, QH, D ** -0.5 if scale is None else float(scale),
+                             _op_ints(lengths, B, "lengths"), _op_ints(n_new, B, "n_new"),
+                             S if max_length is None else int(max_length), _ptr(workspace),
+                             0 if workspace is None else workspace.numel() * workspace.element_size(),
+                             _op_stream(stream))
+    if st != QD_OK:
+        raise QDError(st, "qd_attn_cached failed")
+
+
+def qd_verify_drafts(target_probs, draft_ids, u, out_ids, n_accepted, draft_probs=None, n_draft=None, stream=None):
+    """Verify draft_ids (int32 [streams, tokens]) against target_probs (fp32 [streams, tokens + 1,
+    vocab]) and the drafter's draft_probs (fp32 [streams, tokens, vocab], None: drafts that were
+    not sampled) with the uniforms u (fp32 [streams, tokens + 1]) into out_ids (int32 [streams,
+    tokens + 1]) and n_accepted (int32 [streams])."""
+    import torch
+    B, T = draft_ids.shape
+    V = target_probs.shape[2]
+    if tuple(target_probs.shape) != (B, T + 1, V) or target_probs.dtype != torch.float32 or target_probs.stride(2) != 1:
+        raise ValueError(f"target_probs must be fp32 [{B}, {T + 1}, vocab], rows contiguous")
+    qs = (0, 0)
+    if draft_probs is not None:
+        if tuple(draft_probs.shape) != (B, T, V) or draft_probs.dtype != torch.float32 or draft_probs.stride(2) != 1:
+            raise ValueError(f"draft_probs must be fp32 [{B}, {T}, {V}], rows contiguous")
+        qs = (draft_probs.stride(0) if B > 1 else 0, draft_probs.stride(1) if T > 1 else 0)
+    if u.dtype != torch.float32 or tuple(u.shape) != (B, T + 1) or not u.is_contiguous():
+        raise ValueError(f"u must be contiguous fp32 [{B}, {T + 1}]")
+    st = _lib.qd_verify_drafts(target_probs.data_ptr(), target_probs.stride(0) if B > 1 else 0, target_probs.stride(1),
+                               _ptr(draft_probs), qs[0], qs[1], _op_ints(draft_ids, B * T, "draft_ids"),
+                               _op_ints(n_draft, B, "n_draft"), u.data_ptr(), B, T, V,
+                               _op_ints(out_ids, B * (T + 1), "out_ids"), _op_ints(n_accepted, B, "n_accepted"),
+                               _op_stream(stream))
+    if st != QD_OK:
+        raise QDError(st, "qd_verify_drafts failed")
