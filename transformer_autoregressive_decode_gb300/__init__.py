@@ -654,10 +654,13 @@ class KvCache:
         self.addr = ctypes.addressof(self.c)
 
 
-def _op_stream(stream):
-    """The caller's stream, by default the current one (memory of another device is refused)."""
+def _op_stream(stream, t) -> int:
+    """The caller's stream, by default the current one of t's device (memory of a device that is
+    not the current one is refused by the call).  The raw handle: a Stream object costs 3 us."""
     import torch
-    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if t.is_cuda else 0
 
 
 def _op_dtype(t) -> int:
@@ -689,7 +692,7 @@ def _kv_rows(fn, name, cache, k_rows, v_rows, lengths, n_new, stream):
     s = k_rows.stride()
     st = fn(cache.addr, k_rows.data_ptr(), v_rows.data_ptr(), _op_dtype(k_rows), T, s[0] if B > 1 else 0,
             s[1] if T > 1 else 0, s[2] if H > 1 else 0, _op_ints(lengths, B, "lengths"),
-            _op_ints(n_new, B, "n_new"), _op_stream(stream))
+            _op_ints(n_new, B, "n_new"), _op_stream(stream, k_rows))
     if st != QD_OK:
         raise QDError(st, f"{name} failed")
 
@@ -751,7 +754,7 @@ def qd_attn_cached(q, cache: KvCache, lengths, out, n_new=None, max_length: Opti
                              _op_ints(lengths, B, "lengths"), _op_ints(n_new, B, "n_new"),
                              S if max_length is None else int(max_length), _ptr(workspace),
                              0 if workspace is None else workspace.numel() * workspace.element_size(),
-                             _op_stream(stream))
+                             _op_stream(stream, q))
     if st != QD_OK:
         raise QDError(st, "qd_attn_cached failed")
 
@@ -777,6 +780,6 @@ def qd_verify_drafts(target_probs, draft_ids, u, out_ids, n_accepted, draft_prob
                                _ptr(draft_probs), qs[0], qs[1], _op_ints(draft_ids, B * T, "draft_ids"),
                                _op_ints(n_draft, B, "n_draft"), u.data_ptr(), B, T, V,
                                _op_ints(out_ids, B * (T + 1), "out_ids"), _op_ints(n_accepted, B, "n_accepted"),
-                               _op_stream(stream))
+                               _op_stream(stream, target_probs))
     if st != QD_OK:
         raise QDError(st, "qd_verify_drafts failed")
