@@ -614,8 +614,8 @@ qd_status qd_kv_read(const qd_kv_cache *cache, void *k_rows_dev, void *v_rows_de
  * prefix: one stream of n_kv_heads heads in either format (its strides for streams are
  * unread), read once for the whole batch; NULL or prefix_length 0: none.
  * n_tokens <= 64, max_length in [1, cache->smax] bounds the lengths (it plans the launch).
- * workspace_dev: DEVICE, 256-byte aligned, qd_attn_cached_workspace bytes (0 without a
- * prefix: NULL is allowed).  It is scratch of one call: calls, or captured graphs, that
+ * workspace_dev: DEVICE, 256-byte aligned, qd_attn_cached_workspace bytes (0 for a small
+ * batch without a prefix: NULL is allowed).  It is scratch of one call: calls, or captured graphs, that
  * may run at the same time need their own.  Errors: QD_EINVAL (arguments, alignment,
  * memory, workspace), QD_EUNSUPPORTED (head_dim, n_tokens), QD_ECUDA. */
 qd_status qd_attn_cached(const qd_kv_cache *cache, const qd_kv_cache *prefix, int prefix_length, const void *q_dev,
@@ -624,9 +624,10 @@ qd_status qd_attn_cached(const qd_kv_cache *cache, const qd_kv_cache *prefix, in
                          const int32_t *lengths_dev, const int32_t *n_new_dev, int max_length, void *workspace_dev,
                          size_t workspace_bytes, void *cuda_stream);
 
-/* Bytes of workspace that qd_attn_cached needs for these sizes (HOST *bytes). */
-qd_status qd_attn_cached_workspace(int n_streams, int n_tokens, int n_q_heads, int n_kv_heads, int head_dim,
-                                   int prefix_length, size_t *bytes);
+/* Bytes of workspace that qd_attn_cached needs on the current device for these sizes
+ * (HOST *bytes); of the caches only the sizes, strides and formats are looked at.  Errors as qd_attn_cached. */
+qd_status qd_attn_cached_workspace(const qd_kv_cache *cache, const qd_kv_cache *prefix, int prefix_length, int dtype,
+                                   int n_tokens, int n_q_heads, int max_length, size_t *bytes);
 
 /* qd_verify_drafts -- speculative sampling's verification (the accepted and the drawn tokens
  * follow the target's distribution).  target_probs_dev: DEVICE fp32, the target's

@@ -469,7 +469,7 @@ def test_a_decode_loop_of_all_of_them_captured(qd):
     ids, u = torch.zeros((B, T), dtype=torch.int32, device="cuda"), torch.zeros((B, T + 1), device="cuda")
     outs = [torch.zeros((B, T, G * H, D), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
     oi, acc = torch.zeros((B, T + 1), dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")
-    need = qd.qd_attn_cached_workspace(B, T, G * H, H, D, P)
+    need = qd.qd_attn_cached_workspace(view, True, T, G * H, prefix=pre)
     ws = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in range(2)]
 
     def step(i):

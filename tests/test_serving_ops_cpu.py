@@ -81,17 +81,15 @@ def test_prefix_must_fit_the_cache(qd):
                                       None, 32, A, 1 << 20, None) == qd.QD_EINVAL
 
 
-@pytest.mark.parametrize("args,want", [((0, 1, 2, 2, 64, 5), "EINVAL"), ((1, 0, 2, 2, 64, 5), "EINVAL"), ((1, 1, 3, 2, 64, 5), "EINVAL"),
-                                       ((1, 1, 2, 2, 80, 5), "EUNSUPPORTED"), ((1, 65, 2, 2, 64, 5), "EUNSUPPORTED"),
-                                       ((1, 1, 2, 2, 64, -1), "EINVAL"), ((1 << 23, 2, 8, 2, 64, 5), "EUNSUPPORTED")])
-def test_workspace_refusals(qd, args, want):
-    n = ctypes.c_size_t(5)
-    assert qd._lib.qd_attn_cached_workspace(*args, ctypes.byref(n)) == getattr(qd, "QD_" + want)
-
-
-def test_workspace_holds_the_partials(qd):
-    assert qd.qd_attn_cached_workspace(4, 2, 8, 2, 64, 0) == 0
-    assert qd.qd_attn_cached_workspace(4, 2, 8, 2, 64, 1) >= 4 * 2 * 8 * (64 * 4 + 8)
+@pytest.mark.parametrize("kw,n,want", [({}, dict(T=0), "EINVAL"), ({}, dict(heads=3), "EINVAL"), ({}, dict(heads=1), "EINVAL"),
+                                       (dict(head_dim=80), {}, "EUNSUPPORTED"), ({}, dict(T=65), "EUNSUPPORTED"),
+                                       ({}, dict(plen=-1), "EINVAL"), ({}, dict(plen=5), "EINVAL"), ({}, dict(dtype=7), "EINVAL"),
+                                       ({}, dict(most=33), "EINVAL"), (dict(n_streams=1 << 23), dict(T=8), "EUNSUPPORTED")])
+def test_workspace_refusals(qd, kw, n, want):
+    f = dict(prefix=None, plen=0, dtype=1, T=1, heads=2, most=32)
+    f.update(n)
+    c, out = cache(qd, **kw), ctypes.c_size_t(5)
+    assert qd._lib.qd_attn_cached_workspace(ctypes.addressof(c), *f.values(), ctypes.byref(out)) == getattr(qd, "QD_" + want)
 
 
 VERIFY = [dict(p=None), dict(p=A + 2), dict(ids=None), dict(u=None), dict(out=None), dict(acc=None), dict(ps=-1), dict(pr=-1),

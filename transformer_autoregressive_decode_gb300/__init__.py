@@ -127,7 +127,7 @@ _SIGS = {
     "qd_kv_read": ([_vp, _vp, _vp, _i32, _i32, _i64, _i64, _i64, _vp, _vp, _vp], _i32),
     "qd_attn_cached": ([_vp, _vp, _i32, _vp, _i64, _i64, _vp, _i64, _i64, _i32, _i32, _i32, ctypes.c_float, _vp, _vp,
                         _i32, _vp, _sz, _vp], _i32),
-    "qd_attn_cached_workspace": ([_i32, _i32, _i32, _i32, _i32, _i32, _P(_sz)], _i32),
+    "qd_attn_cached_workspace": ([_vp, _vp, _i32, _i32, _i32, _i32, _i32, _P(_sz)], _i32),
     "qd_verify_drafts": ([_vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp], _i32),
 }
 for _name, (_args, _res) in _SIGS.items():
@@ -708,14 +708,20 @@ def qd_kv_read(cache: KvCache, lengths, k_rows, v_rows, n_new=None, stream=None)
     _kv_rows(_lib.qd_kv_read, "qd_kv_read", cache, k_rows, v_rows, lengths, n_new, stream)
 
 
-def qd_attn_cached_workspace(n_streams: int, n_tokens: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
-                             prefix_length: int) -> int:
+def qd_attn_cached_workspace(cache: KvCache, bf16: bool, n_tokens: int, n_q_heads: int, max_length: Optional[int] = None,
+                             prefix: Optional[KvCache] = None, prefix_length: Optional[int] = None) -> int:
+    """Bytes of workspace of a qd_attn_cached call of these sizes (0: none)."""
     n = ctypes.c_size_t(0)
-    st = _lib.qd_attn_cached_workspace(n_streams, n_tokens, n_q_heads, n_kv_heads, head_dim, prefix_length,
-                                       ctypes.byref(n))
+    P = 0 if prefix is None else prefix.shape[2] if prefix_length is None else int(prefix_length)
+    st = _lib.qd_attn_cached_workspace(cache.addr, prefix.addr if P else None, P, QD_BF16 if bf16 else QD_F32, n_tokens,
+                                       n_q_heads, cache.shape[2] if max_length is None else int(max_length), ctypes.byref(n))
     if st != QD_OK:
         raise QDError(st, "qd_attn_cached_workspace failed")
     return n.value
+
+
+# workspace bytes by the sizes they follow from
+_attn_bytes: Dict[tuple, int] = {}
 
 
 def qd_attn_cached(q, cache: KvCache, lengths, out, n_new=None, max_length: Optional[int] = None, scale=None,
@@ -734,25 +740,29 @@ def qd_attn_cached(q, cache: KvCache, lengths, out, n_new=None, max_length: Opti
     qs, os_ = q.stride(), out.stride()
     if qs[3] != 1 or os_[3] != 1 or (QH > 1 and (qs[2] != D or os_[2] != D)):
         raise ValueError("the heads of q and out must be contiguous")
-    P, need = 0, 0
+    P = 0
     if prefix is not None:
         P = prefix.shape[2] if prefix_length is None else int(prefix_length)
         if prefix.shape[0] != 1:
             raise ValueError("the prefix is a cache of one stream")
     elif prefix_length:
         raise ValueError("prefix_length without a prefix")
-    if P > 0 and workspace is None:
-        need = qd_attn_cached_workspace(B, T, QH, H, D, P)
-        if stream is not None:
+    dt = _op_dtype(q)
+    most = S if max_length is None else int(max_length)
+    if workspace is None:
+        key = (cache.shape, cache.c.format, P, P and prefix.c.format, dt, T, QH, most, q.get_device())
+        need = _attn_bytes.get(key)
+        if need is None:
+            need = _attn_bytes[key] = qd_attn_cached_workspace(cache, dt == QD_BF16, T, QH, most, prefix, P)
+        if need and stream is not None:
             with torch.cuda.stream(stream):
                 workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        else:
+        elif need:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     st = _lib.qd_attn_cached(cache.addr, prefix.addr if P > 0 else None, P, q.data_ptr(), qs[0] if B > 1 else 0,
                              qs[1] if T > 1 else 0, out.data_ptr(), os_[0] if B > 1 else 0, os_[1] if T > 1 else 0,
-                             _op_dtype(q), T, QH, D ** -0.5 if scale is None else float(scale),
-                             _op_ints(lengths, B, "lengths"), _op_ints(n_new, B, "n_new"),
-                             S if max_length is None else int(max_length), _ptr(workspace),
+                             dt, T, QH, D ** -0.5 if scale is None else float(scale),
+                             _op_ints(lengths, B, "lengths"), _op_ints(n_new, B, "n_new"), most, _ptr(workspace),
                              0 if workspace is None else workspace.numel() * workspace.element_size(),
                              _op_stream(stream, q))
     if st != QD_OK:

@@ -19,9 +19,9 @@
 // share of the A fragment, and q is laid out to match.  For the output, V^T is A:
 // a lane holds the same dims of the four positions its fragment pairs, and a byte
 // permutation pairs them up, the same that widens the codes.  The probabilities turn
-// from the accumulator's layout into the B fragment's with movmatrix.  Each lane reads only what it
-// copied itself (cp.async, 16 bytes), so the ring of tiles needs no barrier: it serves as
-// registers that the loads in flight do not occupy.
+// from the accumulator's layout into the B fragment's with movmatrix.  Each warp has a ring of tiles of its own
+// that it fills with cp.async (whole 128-byte lines, so that each line is one write into shared memory), the 16-byte
+// pieces of a row placed so that fragments read without bank conflicts; no barrier wider than the warp.
 //
 // A cluster of CTAs shares one (stream, key head, rows) item; its warps take the 16-position
 // tiles in turn and their partial results (ref, sum, output) meet in distributed shared
@@ -38,8 +38,6 @@ namespace qd {
 namespace {
 
 constexpr int kAcWarps = 4, kAcThreads = kAcWarps * 32;
-constexpr int kAcStages = 3;
-constexpr int kAcTile = 16;                 // positions per warp and step
 constexpr int kAcMaxCluster = 8;
 constexpr int kAcMaxTokens = 64;
 // Probabilities stand 2^10 above 1 at the running maximum and may grow to 2^15 before the
@@ -53,13 +51,16 @@ struct CachedArgs {
     uint8_t *out;
     int64_t q_stream, q_token, o_stream, o_token;   // bytes
     const int32_t *lengths, *n_new;
-    int T, G, kvh, groups, max_len;
+    int B, T, G, kvh, groups, max_len;
     int rows;                                       // rows of an item: T G, of the prefix B T G
     float scale2;                                   // softmax scale times log2(e)
     // partials over the prefix: [kvh][B T G][splits]
     float2 *p_ml;
     float *p_o;
     int splits;
+    // partials of attn_share_kernel: [slot][rows of a CTA]
+    float2 *s_ml;
+    float *s_o;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -74,9 +75,6 @@ __device__ __forceinline__ float lg2(float x) {
 }
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool live) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp8(uint32_t dst, const void *src, bool live) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(live ? 8 : 0) : "memory");
 }
 __device__ __forceinline__ void cp4(uint32_t dst, const void *src, bool live) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4 : 0) : "memory");
@@ -104,8 +102,10 @@ __device__ __forceinline__ float f16_of(float x) { return __half2float(__float2h
 __device__ __forceinline__ float bf16_of(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
 
 // Two code bytes (offset by 128) under the exponent of 1024: 1024 + u, less 1152 = code, exactly.
-__device__ __forceinline__ uint32_t codes_f16(uint32_t y, uint32_t sel) {
+// RAW: 1152 + code, for a sum that starts at the offset's share.
+template <bool RAW> __device__ __forceinline__ uint32_t codes_f16(uint32_t y, uint32_t sel) {
     const uint32_t h = __byte_perm(y, 0x64646464u, sel);
+    if constexpr (RAW) return h;
     const __half2 v = __hsub2(*reinterpret_cast<const __half2 *>(&h), __half2half2(__ushort_as_half(0x6480)));
     return *reinterpret_cast<const uint32_t *>(&v);
 }
@@ -117,17 +117,27 @@ template <bool Q8, bool F32, int D, int NT> struct AcCfg {
     static constexpr int KP = D * ES / 64;                         // 16-byte pieces of a K row per lane
     static constexpr int KW = Q8 ? 4 : 2;                          // k-steps per piece
     static constexpr int KS = D / 16, MT = D / 16;
-    static constexpr int VB = D * ES / 8 < 16 ? D * ES / 8 : 16;   // bytes of a V access (8 or 16)
-    static constexpr int VP = D * ES / 8 / VB;                     // V accesses per position and lane
-    static constexpr int kV = 2 * KP * 512;                        // byte offset of V in a tile
-    static constexpr int kS = kV + 4 * VP * VB * 32;               // of the scales
-    static constexpr int kTileBytes = kS + (Q8 ? 128 : 0);
-    static constexpr int kRing = kAcStages * kTileBytes;           // per warp
+    static constexpr int LB = D * ES;                              // bytes of a row
+    static constexpr int VP = LB / 128 > 0 ? LB / 128 : 1;         // V accesses per position and lane
+    static constexpr int CP = LB / 32;                             // 16-byte copies per lane and block, of K or V
+    static constexpr int CR = 512 / LB;                            // rows that one copy instruction covers
+    static constexpr int kTurn = 8 / CR;                           // copies after which the places repeat, 8 rows on
+    // A step's tile: two blocks of 16 positions where they take 8 KB at most (half the address arithmetic,
+    // votes and waits per position, and two independent chains), one of bf16 rows of 128.
+    static constexpr int SUB = D * ES <= 128 ? 2 : 1;
+    static constexpr int TP = 16 * SUB;                            // positions of a tile
+    static constexpr int kV = 16 * LB;                             // byte offset of V in a block
+    static constexpr int kBlock = 2 * kV;
+    static constexpr int kS = SUB * kBlock;                        // of the scales in a tile: [K, V][TP]
+    static constexpr int kTileBytes = kS + (Q8 ? TP * 8 : 0);
+    static constexpr int kStages = kTileBytes > 8192 ? 2 : 3;
+    static constexpr int kRing = kStages * kTileBytes;             // per warp
     // after the pass the rings' space holds the warps' partials, then the CTA's
     static constexpr int kPart = kAcWarps * RW * D * 4;
     static constexpr int kMl = kPart + RW * D * 4;
     static constexpr int kEnd = kMl + (kAcWarps + 1) * RW * 8;
     static constexpr int kSmem = kAcWarps * kRing > kEnd ? kAcWarps * kRing : kEnd;
+    static constexpr int kMinCtas = NT == 1 ? (kSmem > 72 * 1024 ? 2 : kSmem > 54 * 1024 ? 3 : 4) : kSmem > 72 * 1024 ? 2 : 3;
 };
 
 // (ref, sum) of one partial: its weight against the reference M
@@ -147,198 +157,237 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     return v;
 }
 
-// PREFIX: the rows of every stream over the shared prefix, partials to global memory.
-// Otherwise: a stream's rows over its own cache; joins the prefix's partials and writes
-// the output.  blockIdx.x = item * splits + split.
-template <bool Q8, bool F32, int D, int NT, bool PREFIX>
-__global__ void __launch_bounds__(kAcThreads, NT == 1 ? 4 : 3) attn_cached_kernel(const CachedArgs a, int nsplit) {
+// One warp's pass over some of an item's tiles: the item's rows as B fragments, the ring of
+// tiles, and the running reference, sums and output.
+template <bool Q8, bool F32, int D, int NT, bool PREFIX> struct WarpPass {
     using K = AcCfg<Q8, F32, D, NT>;
-    constexpr int C = K::C, HC = C == 1 ? 2 : 1;
-    extern __shared__ __align__(16) uint8_t sm[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int split = blockIdx.x % nsplit, item = blockIdx.x / nsplit;
-    const int grp = item % a.groups, hk = (item / a.groups) % a.kvh, b = PREFIX ? 0 : item / a.groups / a.kvh;
-
-    int len = a.max_len, nn = a.T;
-    if constexpr (!PREFIX) {
-        len = a.lengths[b];
-        len = len < 0 ? 0 : len > a.max_len ? a.max_len : len;
-        nn = a.n_new ? a.n_new[b] : a.T;
-        nn = nn < 0 ? 0 : nn > a.T ? a.T : nn;
-    }
-    const int r0 = grp * K::RW;
-
-    // ---- this item's rows as the B fragments of the scores: column 8 nt + g holds part
-    // (column % C) of row r0 + column / C; q scaled by a power of two per row for fp16
+    static constexpr int C = K::C, HC = C == 1 ? 2 : 1;
+    // bf16 rows over codes: K's codes enter as 1152 + code, and the scores start at -1152 sum q (fp32 sums of
+    // 8 steps: within 2^-20 of 1152 sum |q|, 2^-17 of max|k| sum |q|).  fp32 rows and V subtract it from each code.
+    static constexpr bool kFold = Q8 && !F32;
+    int lane, g, t;
     uint32_t qf[NT][K::KS][2];
-    float cs_g[NT];
-    int lim_g[NT];
-    int lim_lo = INT32_MAX, lim_hi = 0;             // over this item's rows
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int col = 8 * nt + g, r = r0 + col / C, part = col % C;
-        int bb = b, rr = r;
-        if constexpr (PREFIX) {
-            bb = r / (a.T * a.G);
-            rr = r - bb * (a.T * a.G);
-        }
-        const int tt = rr / a.G, gg = rr - tt * a.G;
-        const bool live = r < a.rows && (PREFIX || tt < nn);
-        const uint8_t *src = a.q + bb * a.q_stream + tt * a.q_token + (int64_t)(hk * a.G + gg) * D * (F32 ? 4 : 2);
-        constexpr int E = 16 / K::ES;               // dims of a piece
-        float x[K::KP * E];
-#pragma unroll
-        for (int i = 0; i < K::KP; ++i)
-#pragma unroll
-            for (int e = 0; e < E; e += F32 ? 4 : 8) {
-                const int d = i * 4 * E + t * E + e;
-                uint4 u = make_uint4(0, 0, 0, 0);
-                if (live) u = __ldg(reinterpret_cast<const uint4 *>(src + d * (F32 ? 4 : 2)));
-                if constexpr (F32)
-                    Elem<float>::unpack(u, x + i * E + e);
-                else
-                    Elem<__nv_bfloat16>::unpack(u, x + i * E + e);
-            }
-        float cs = a.scale2;
-        if constexpr (Q8) {
-            uint32_t m = 0;
-#pragma unroll
-            for (int e = 0; e < K::KP * E; ++e) m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
-            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            // the row's largest value to [2^14, 2^15)
-            int up = 268 - (int)(m >> 23);
-            up = up > 253 ? 253 : up;
-            const float f = __uint_as_float((uint32_t)up << 23);
-            cs *= __uint_as_float((uint32_t)(254 - up) << 23);
-#pragma unroll
-            for (int e = 0; e < K::KP * E; ++e) x[e] *= f;
-        }
-#pragma unroll
-        for (int e = 0; e < K::KP * E; ++e) {
-            if constexpr (Q8) {
-                if (part == 1) x[e] = x[e] - f16_of(x[e]);
-            } else {
-                if (part >= 1) x[e] = x[e] - bf16_of(x[e]);
-                if (part >= 2) x[e] = x[e] - bf16_of(x[e]);
-                if (part >= 3) x[e] = 0.f;
-            }
-        }
-#pragma unroll
-        for (int ks = 0; ks < K::KS; ++ks)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float lo = x[ks * 4 + 2 * k], hi = x[ks * 4 + 2 * k + 1];
-                qf[nt][ks][k] = Q8 ? pack_f16(lo, hi) : pack_bf16(lo, hi);
-            }
-        cs_g[nt] = cs;
-        lim_g[nt] = !live ? 0 : PREFIX ? len : max(0, len - (nn - 1 - tt));
-        lim_lo = min(lim_lo, __reduce_min_sync(0xffffffffu, live ? lim_g[nt] : INT32_MAX));
-        lim_hi = max(lim_hi, __reduce_max_sync(0xffffffffu, lim_g[nt]));
-    }
-    // the columns of this lane's accumulators
-    float cs[NT][2];
+    float cs[NT][2], s0[NT][2];                     // of this lane's columns: factor, the scores' start
     int lim[NT][HC];
+    int lim_lo, lim_hi;                             // the limits of the item's rows
+    float o[K::MT][NT][4], ref[NT][HC], l[NT][HC];
+    const uint8_t *kb, *vb, *kp, *vp;               // this lane's column of the item; of the next tile
+    const float *ksb, *vsb;
+    int64_t row, hop;
+    int n_pos, next, end, step;
+    uint8_t *ring;
+    uint32_t ring_s;
+    int put[K::kTurn], kget[2], vget[2];            // this lane's places: copies, K's pieces, V's positions
+
+    __device__ __forceinline__ void init(int lane_) {
+        lane = lane_, g = lane_ >> 2, t = lane_ & 3;
+        const int at = lane / (32 / K::CR), c = lane % (32 / K::CR);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+        for (int j = 0; j < K::kTurn; ++j) put[j] = place(K::CR * j + at, c);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) cs[nt][k] = __shfl_sync(0xffffffffu, cs_g[nt], (2 * t + k) * 4);
-#pragma unroll
-        for (int k = 0; k < HC; ++k) lim[nt][k] = __shfl_sync(0xffffffffu, lim_g[nt], (2 * t + k) * 4);
+        for (int i = 0; i < 2; ++i) {
+            kget[i] = K::LB == 64 ? place(g, t) : place(g, 4 * i + t);
+            vget[i] = K::LB == 64 ? place(2 * t + i, g >> 1) + 8 * (g & 1) : place(2 * t + i, g);
+        }
     }
-    const int n_pos = lim_hi;                       // positions that any row sees
-    const int n_tiles = (n_pos + kAcTile - 1) / kAcTile;
 
-    const uint8_t *kb = a.c.k + (PREFIX ? 0 : b * a.c.stream) + hk * a.c.head;
-    const uint8_t *vb = a.c.v + (PREFIX ? 0 : b * a.c.stream) + hk * a.c.head;
-    const float *ksb = Q8 ? a.c.ks + (PREFIX ? 0 : b * a.c.sstream) + hk * a.c.shead : nullptr;
-    const float *vsb = Q8 ? a.c.vs + (PREFIX ? 0 : b * a.c.sstream) + hk * a.c.shead : nullptr;
-    uint8_t *ring = sm + warp * K::kRing;
-    const uint32_t ring_s = smem_addr(ring);
+    // Where 16-byte piece c of position p stands in a block of K or V: rows in order, the pieces of
+    // a 128-byte line permuted by the position, such that the fragments' reads (8 lanes: two rows, four pieces of K;
+    // four rows two apart, two pieces of V) meet every bank once.
+    static __device__ __forceinline__ int place(int p, int c) {
+        const int f = ((p & 1) << 2) ^ (p & 6);
+        if constexpr (K::LB == 64) return (p >> 1) * 128 + (((((p & 1) << 2) + c) ^ (p & 6)) << 4);
+        return p * K::LB + ((c >> 3) << 7) + (((c & 7) ^ f) << 4);
+    }
 
-    // copy this lane's share of the tile into its stage; positions past n_pos become zeros
-    auto fetch = [&](int tile, int stage) {
-        const int p0 = tile * kAcTile;
+    // copy the next tile into a stage; positions past n_pos become zeros
+    template <bool FULL> __device__ __forceinline__ void fetch_as(int stage) {
         const uint32_t dst = ring_s + stage * K::kTileBytes;
+        const int left = n_pos - next * K::TP, at = lane / (32 / K::CR);   // positions of the tile; this lane's first
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int p = p0 + g + 8 * h;
-            const bool live = p < n_pos;
-            const uint8_t *src = kb + (int64_t)(live ? p : 0) * a.c.row + t * 16;
+        for (int u = 0; u < K::SUB; ++u)
 #pragma unroll
-            for (int i = 0; i < K::KP; ++i) cp16(dst + (h * K::KP + i) * 512 + lane * 16, src + 64 * i, live);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int p = p0 + 2 * t + (i & 1) + 8 * (i >> 1);
-            const bool live = p < n_pos;
-            const uint8_t *src = vb + (int64_t)(live ? p : 0) * a.c.row + g * K::VB;
-#pragma unroll
-            for (int j = 0; j < K::VP; ++j) {
-                const uint32_t d = dst + K::kV + (i * K::VP + j) * (32 * K::VB) + lane * K::VB;
-                if constexpr (K::VB == 16)
-                    cp16(d, src + 128 * j, live);
-                else
-                    cp8(d, src, live);
+            for (int j = 0; j < K::CP; ++j) {
+                const int p = K::CR * j;
+                const uint32_t d = dst + u * K::kBlock + put[j % K::kTurn] + (j / K::kTurn) * 8 * K::LB;
+                const bool live = FULL || 16 * u + p + at < left;
+                cp16(d, live ? kp + (16 * u + p) * row : kb, live);
+                cp16(d + K::kV, live ? vp + (16 * u + p) * row : vb, live);
             }
-        }
         if constexpr (Q8) {
-            const int p = p0 + (lane & 15);
-            const bool live = p < n_pos;
-            cp4(dst + K::kS + lane * 4, (lane < 16 ? ksb : vsb) + (live ? p : 0), live);
+            static_assert(K::TP == 32, "a lane per position's scales");
+            const int p = next * K::TP + lane;
+            const bool live = FULL || lane < left;
+            cp4(dst + K::kS + lane * 4, ksb + (live ? p : 0), live);
+            cp4(dst + K::kS + 128 + lane * 4, vsb + (live ? p : 0), live);
         }
-    };
-
-    float o[K::MT][NT][4];
-#pragma unroll
-    for (int mt = 0; mt < K::MT; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
-    float ref[NT][HC], l[NT][HC];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int k = 0; k < HC; ++k) ref[nt][k] = -INFINITY, l[nt][k] = 0.f;
-
-    const int step = nsplit * kAcWarps;
-    int next = split * kAcWarps + warp;             // tile to fetch
-#pragma unroll
-    for (int s = 0; s < kAcStages - 1; ++s) {
-        if (next < n_tiles) fetch(next, s);
-        cp_commit();
-        next += step;
     }
-    int stage = 0;
-    for (int tile = split * kAcWarps + warp; tile < n_tiles; tile += step) {
-        {
-            const int into = stage == 0 ? kAcStages - 1 : stage - 1;
-            if (next < n_tiles) fetch(next, into);
+    __device__ __forceinline__ void fetch(int stage) {
+        if ((next + 1) * K::TP <= n_pos)
+            fetch_as<true>(stage);
+        else
+            fetch_as<false>(stage);
+        kp += hop, vp += hop;
+    }
+
+    // the item's tiles first, first + step, ... below end: the first copies start here
+    __device__ __forceinline__ void start(const CachedArgs &a, int b, int hk, int len, uint8_t *ring_, int first, int end_,
+                                          int step_) {
+        const int at = lane / (32 / K::CR), c = lane % (32 / K::CR);
+        kb = a.c.k + (PREFIX ? 0 : b * a.c.stream) + hk * a.c.head + c * 16;
+        vb = a.c.v + (PREFIX ? 0 : b * a.c.stream) + hk * a.c.head + c * 16;
+        ksb = Q8 ? a.c.ks + (PREFIX ? 0 : b * a.c.sstream) + hk * a.c.shead : nullptr;
+        vsb = Q8 ? a.c.vs + (PREFIX ? 0 : b * a.c.sstream) + hk * a.c.shead : nullptr;
+        row = a.c.row;
+        n_pos = len;
+        ring = ring_;
+        ring_s = smem_addr(ring_);
+        next = first, end = end_, step = step_;
+        kp = kb + ((int64_t)first * K::TP + at) * row;
+        vp = vb + ((int64_t)first * K::TP + at) * row;
+        hop = (int64_t)step * K::TP * row;
+#pragma unroll
+        for (int s = 0; s < K::kStages - 1; ++s) {
+            if (next < end) fetch(s);
             cp_commit();
             next += step;
         }
-        cp_wait<kAcStages - 1>();
-        __syncwarp();                               // the scales come from other lanes
-        const uint8_t *st = ring + stage * K::kTileBytes;
-        const int p0 = tile * kAcTile;
+    }
 
-        // ---- scores: rows (positions) g and g + 8, columns 2t and 2t + 1
-        float s[NT][4];
+    // rows r0 .. of the item as B fragments: column 8 nt + g holds part (column % C) of row r0 +
+    // column / C; q scaled by a power of two per row for fp16
+    __device__ __forceinline__ void load_rows(const CachedArgs &a, int b, int hk, int r0, int len, int nn) {
+        float cs_g[NT], s0_g[NT];
+        int lim_g[NT];
+        lim_lo = INT32_MAX, lim_hi = 0;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+        for (int nt = 0; nt < NT; ++nt) {
+            const int col = 8 * nt + g, r = r0 + col / C, part = col % C;
+            int bb = b, rr = r;
+            if constexpr (PREFIX) {
+                bb = r / (a.T * a.G);
+                rr = r - bb * (a.T * a.G);
+            }
+            const int tt = rr / a.G, gg = rr - tt * a.G;
+            const bool live = r < a.rows && (PREFIX || tt < nn);
+            const uint8_t *src = a.q + bb * a.q_stream + tt * a.q_token + (int64_t)(hk * a.G + gg) * D * (F32 ? 4 : 2);
+            constexpr int E = 16 / K::ES;           // dims of a piece
+            float x[K::KP * E];
+#pragma unroll
+            for (int i = 0; i < K::KP; ++i)
+#pragma unroll
+                for (int e = 0; e < E; e += F32 ? 4 : 8) {
+                    const int d = i * 4 * E + t * E + e;
+                    uint4 u = make_uint4(0, 0, 0, 0);
+                    if (r < a.rows) u = __ldg(reinterpret_cast<const uint4 *>(src + d * (F32 ? 4 : 2)));
+                    if constexpr (F32)
+                        Elem<float>::unpack(u, x + i * E + e);
+                    else
+                        Elem<__nv_bfloat16>::unpack(u, x + i * E + e);
+                }
+            float c = a.scale2, sum = 0.f;
+            if constexpr (Q8) {
+                uint32_t m = 0;
+#pragma unroll
+                for (int e = 0; e < K::KP * E; ++e) m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
+                m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                // the row's largest value to [2^14, 2^15)
+                int up = 268 - (int)(m >> 23);
+                up = up > 253 ? 253 : up;
+                const float f = __uint_as_float((uint32_t)up << 23);
+                c *= __uint_as_float((uint32_t)(254 - up) << 23);
+#pragma unroll
+                for (int e = 0; e < K::KP * E; ++e) x[e] *= f;
+            }
+#pragma unroll
+            for (int e = 0; e < K::KP * E; ++e) {
+                if constexpr (Q8) {
+                    if (part == 1) x[e] = x[e] - f16_of(x[e]);
+                } else {
+                    if (part >= 1) x[e] = x[e] - bf16_of(x[e]);
+                    if (part >= 2) x[e] = x[e] - bf16_of(x[e]);
+                    if (part >= 3) x[e] = 0.f;
+                }
+            }
+#pragma unroll
+            for (int ks = 0; ks < K::KS; ++ks)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float lo = x[ks * 4 + 2 * k], hi = x[ks * 4 + 2 * k + 1];
+                    qf[nt][ks][k] = Q8 ? pack_f16(lo, hi) : pack_bf16(lo, hi);
+                    if constexpr (kFold) {
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&qf[nt][ks][k]));
+                        sum += f.x + f.y;
+                    }
+                }
+            if constexpr (kFold) {
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            }
+            s0_g[nt] = -1152.f * sum;
+            cs_g[nt] = c;
+            lim_g[nt] = !live ? 0 : PREFIX ? len : max(0, len - (nn - 1 - tt));
+            lim_lo = min(lim_lo, __reduce_min_sync(0xffffffffu, live ? lim_g[nt] : INT32_MAX));
+            lim_hi = max(lim_hi, __reduce_max_sync(0xffffffffu, lim_g[nt]));
+        }
+        // the columns of this lane's accumulators
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                cs[nt][k] = __shfl_sync(0xffffffffu, cs_g[nt], (2 * t + k) * 4);
+                s0[nt][k] = __shfl_sync(0xffffffffu, s0_g[nt], (2 * t + k) * 4);
+            }
+#pragma unroll
+            for (int k = 0; k < HC; ++k) lim[nt][k] = __shfl_sync(0xffffffffu, lim_g[nt], (2 * t + k) * 4);
+        }
+#pragma unroll
+        for (int mt = 0; mt < K::MT; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < HC; ++k) ref[nt][k] = -INFINITY, l[nt][k] = 0.f;
+    }
+
+    __device__ __forceinline__ void run() {
+        int stage = 0;
+        for (int tile = next - (K::kStages - 1) * step; tile < end; tile += step) {
+            if (next < end) fetch(stage == 0 ? K::kStages - 1 : stage - 1);
+            cp_commit();
+            next += step;
+            cp_wait<K::kStages - 1>();
+            __syncwarp();                           // other lanes' copies
+            one_tile(ring + stage * K::kTileBytes, tile * K::TP);
+            stage = stage == K::kStages - 1 ? 0 : stage + 1;
+            __syncwarp();                           // before the stage is written again
+        }
+        cp_wait<0>();
+    }
+
+    // Scores of one block of 16 positions: rows (positions) g and g + 8, columns 2t and 2t + 1
+    __device__ __forceinline__ void scores(const uint8_t *st, float (&s)[NT][4]) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[nt][e] = kFold ? s0[nt][e & 1] : 0.f;
 #pragma unroll
         for (int i = 0; i < K::KP; ++i) {
-            const uint4 ua = *reinterpret_cast<const uint4 *>(st + i * 512 + lane * 16);
-            const uint4 ub = *reinterpret_cast<const uint4 *>(st + (K::KP + i) * 512 + lane * 16);
+            const uint8_t *at = st + kget[i & 1] + (i >> 1) * 128;
+            const uint4 ua = *reinterpret_cast<const uint4 *>(at);
+            const uint4 ub = *reinterpret_cast<const uint4 *>(at + 8 * K::LB);
             const uint32_t wa[4] = {ua.x, ua.y, ua.z, ua.w}, wb[4] = {ub.x, ub.y, ub.z, ub.w};
 #pragma unroll
             for (int w = 0; w < K::KW; ++w) {
                 uint32_t f[4];
                 if constexpr (Q8) {
                     const uint32_t xa = wa[w] ^ 0x80808080u, xb = wb[w] ^ 0x80808080u;
-                    f[0] = codes_f16(xa, 0x4140), f[1] = codes_f16(xb, 0x4140);
-                    f[2] = codes_f16(xa, 0x4342), f[3] = codes_f16(xb, 0x4342);
+                    f[0] = codes_f16<kFold>(xa, 0x4140), f[1] = codes_f16<kFold>(xb, 0x4140);
+                    f[2] = codes_f16<kFold>(xa, 0x4342), f[3] = codes_f16<kFold>(xb, 0x4342);
                 } else {
                     f[0] = wa[2 * w], f[1] = wb[2 * w], f[2] = wa[2 * w + 1], f[3] = wb[2 * w + 1];
                 }
@@ -352,132 +401,51 @@ __global__ void __launch_bounds__(kAcThreads, NT == 1 ? 4 : 3) attn_cached_kerne
                 }
             }
         }
+    }
 
-        // ---- scores in log2 units, the mask, and z = s + log2(values' scale), which bounds
-        // the weight that enters the product
-        float kd[2] = {1.f, 1.f}, vd[2] = {1.f, 1.f}, vl[2] = {0.f, 0.f};
+    // Output: rows (dims) of V^T of one block against its probabilities
+    __device__ __forceinline__ void output(const uint8_t *sv, const uint32_t (&pb)[NT][2], int p0) {
         if constexpr (Q8) {
-            const float *sc = reinterpret_cast<const float *>(st + K::kS);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                kd[h] = sc[g + 8 * h], vd[h] = sc[16 + g + 8 * h];
-                vl[h] = fmaxf(lg2(vd[h]), -60.f);   // a row of zeros does not move the reference
-            }
-        }
-        float x[NT][2][HC];
-        bool over = false;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int p = p0 + g + 8 * h;
-#pragma unroll
-                for (int k = 0; k < HC; ++k) {
-                    float v = s[nt][2 * h + k];
-                    if constexpr (F32) v += s[nt][2 * h + 1];   // bf16 q has one part
-                    if constexpr (C == 4) v += __shfl_xor_sync(0xffffffffu, v, 1);
-                    v *= cs[nt][k];
-                    if constexpr (Q8) v *= kd[h];
-                    v = p < lim[nt][k] ? v : -INFINITY;
-                    x[nt][h][k] = v;
-                    over |= v + vl[h] > ref[nt][k] + kAcRoom;
-                }
-            }
-        if (__any_sync(0xffffffffu, over)) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float f[HC];
-#pragma unroll
-                for (int k = 0; k < HC; ++k) {
-                    float m = fmaxf(x[nt][0][k] + vl[0], x[nt][1][k] + vl[1]);
-#pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-                    f[k] = 1.f;
-                    if (m > ref[nt][k] + kAcRoom) {
-                        const float now = m - kAcUp;
-                        f[k] = ref[nt][k] == -INFINITY ? 0.f : ex2(ref[nt][k] - now);
-                        ref[nt][k] = now;
-                        l[nt][k] = l[nt][k] * f[k];
-                    }
-                }
-#pragma unroll
-                for (int mt = 0; mt < K::MT; ++mt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[mt][nt][e] *= f[HC == 2 ? (e & 1) : 0];
-            }
-        }
-
-        // ---- probabilities, their sums, and their parts as the B fragments of the output
-        uint32_t pb[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float w[HC];
-#pragma unroll
-                for (int k = 0; k < HC; ++k) {
-                    const float rf = ref[nt][k] == -INFINITY ? 0.f : ref[nt][k];
-                    w[k] = ex2(x[nt][h][k] - rf);
-                    l[nt][k] += w[k];
-                    if constexpr (Q8) w[k] = p0 + g + 8 * h < lim[nt][k] ? w[k] * vd[h] : 0.f;
-                }
-                uint32_t u;
-                if constexpr (C == 1) {
-                    u = pack_f16(w[0], w[1]);
-                } else if constexpr (Q8) {
-                    const float hi = f16_of(w[0]);
-                    u = pack_f16(hi, w[0] - hi);
-                } else if constexpr (C == 2) {
-                    const float hi = bf16_of(w[0]);
-                    u = pack_bf16(hi, w[0] - hi);
-                } else {
-                    const float hi = bf16_of(w[0]), mid = bf16_of(w[0] - hi);
-                    u = t & 1 ? pack_bf16(w[0] - hi - mid, 0.f) : pack_bf16(hi, mid);
-                }
-                pb[nt][h] = movmatrix(u);
-            }
-
-        // ---- output: rows (dims) of V^T against the probabilities
-        const uint8_t *sv = st + K::kV;
-        if constexpr (Q8) {
-            constexpr int VW = K::VB / 4;
+            constexpr int VW = D / 32;
             uint32_t v[4][VW];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
+                const uint8_t *at = sv + vget[i & 1] + (i >> 1) * 8 * K::LB;
                 if constexpr (VW == 4) {
-                    const uint4 u = *reinterpret_cast<const uint4 *>(sv + i * 512 + lane * 16);
+                    const uint4 u = *reinterpret_cast<const uint4 *>(at);
                     v[i][0] = u.x, v[i][1] = u.y, v[i][2] = u.z, v[i][3] = u.w;
                 } else {
-                    const uint2 u = *reinterpret_cast<const uint2 *>(sv + i * 256 + lane * 8);
+                    const uint2 u = *reinterpret_cast<const uint2 *>(at);
                     v[i][0] = u.x, v[i][1] = u.y;
                 }
-#pragma unroll
-                for (int w = 0; w < VW; ++w) v[i][w] ^= 0x80808080u;
             }
 #pragma unroll
-            for (int w = 0; w < VW; ++w)
+            for (int w = 0; w < VW; ++w) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i][w] ^= 0x80808080u;
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
                     const uint32_t y = __byte_perm(v[0][w], v[1][w], hh ? 0x7362 : 0x5140);
                     const uint32_t z = __byte_perm(v[2][w], v[3][w], hh ? 0x7362 : 0x5140);
-                    const uint32_t f[4] = {codes_f16(y, 0x4140), codes_f16(y, 0x4342), codes_f16(z, 0x4140),
-                                           codes_f16(z, 0x4342)};
+                    const uint32_t f[4] = {codes_f16<false>(y, 0x4140), codes_f16<false>(y, 0x4342),
+                                           codes_f16<false>(z, 0x4140), codes_f16<false>(z, 0x4342)};
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) mma16816_f16(o[2 * w + hh][nt], f, pb[nt][0], pb[nt][1]);
                 }
+            }
         } else {
             uint32_t v[4][4 * K::VP];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < K::VP; ++j) {
-                    const uint4 u = *reinterpret_cast<const uint4 *>(sv + (i * K::VP + j) * 512 + lane * 16);
+                    const uint4 u = *reinterpret_cast<const uint4 *>(sv + vget[i & 1] + (i >> 1) * 8 * K::LB + 128 * j);
                     v[i][4 * j] = u.x, v[i][4 * j + 1] = u.y, v[i][4 * j + 2] = u.z, v[i][4 * j + 3] = u.w;
                 }
             // A new token's V that is not finite must not reach the rows that do not see it (0 x
             // infinity is NaN): only tiles that some rows see further into than others can hold one.
             bool odd = false;
-            if (!PREFIX && p0 + kAcTile > lim_lo) {
+            if (!PREFIX && p0 + 16 > lim_lo) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -491,7 +459,7 @@ __global__ void __launch_bounds__(kAcThreads, NT == 1 ? 4 : 3) attn_cached_kerne
                                        __byte_perm(v[2][w], v[3][w], 0x5410), __byte_perm(v[2][w], v[3][w], 0x7632)};
                 if (!PREFIX && odd) {
                     // one limit after the other: V beyond it zeroed, the result kept by the columns it is theirs
-                    for (int cut = max(lim_lo, 0); cut <= lim_hi; ++cut) {
+                    for (int cut = lim_lo; cut <= lim_hi; ++cut) {
                         const int at = p0 + 2 * t;
                         const uint32_t m0 = (at < cut ? 0xffffu : 0u) | (at + 1 < cut ? 0xffff0000u : 0u);
                         const uint32_t m1 = (at + 8 < cut ? 0xffffu : 0u) | (at + 9 < cut ? 0xffff0000u : 0u);
@@ -512,10 +480,203 @@ __global__ void __launch_bounds__(kAcThreads, NT == 1 ? 4 : 3) attn_cached_kerne
                 }
             }
         }
-        stage = stage == kAcStages - 1 ? 0 : stage + 1;
-        __syncwarp();                               // before a lane's scales are written again
     }
-    cp_wait<0>();
+
+    // one tile from position p0 on, in its stage
+    __device__ __forceinline__ void one_tile(const uint8_t *st, int p0) {
+        constexpr int H = 2 * K::SUB;               // this lane's positions: p0 + g + 8 h
+        const bool edge = p0 + K::TP > lim_lo;      // some row does not see all of it
+        float x[NT][H][HC], vd[H], vl[H];
+#pragma unroll
+        for (int u = 0; u < K::SUB; ++u) {
+            float s[NT][4];
+            scores(st + u * K::kBlock, s);
+            // in log2 units
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                const int h = 2 * u + hh;
+                float kd = 1.f;
+                if constexpr (Q8) kd = reinterpret_cast<const float *>(st + K::kS)[g + 8 * h];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int k = 0; k < HC; ++k) {
+                        float v = s[nt][2 * hh + k];
+                        if constexpr (F32) v += s[nt][2 * hh + 1];   // bf16 q has one part
+                        if constexpr (C == 4) v += __shfl_xor_sync(0xffffffffu, v, 1);
+                        v *= cs[nt][k];
+                        if constexpr (Q8) v *= kd;
+                        x[nt][h][k] = v;
+                    }
+            }
+        }
+        // z = s + log2(values' scale) bounds the weight that enters the product; a row of zeros
+        // does not move the reference
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            vd[h] = 1.f, vl[h] = 0.f;
+            if constexpr (Q8) {
+                vd[h] = reinterpret_cast<const float *>(st + K::kS)[K::TP + g + 8 * h];
+                vl[h] = fmaxf(lg2(vd[h]), -60.f);
+            }
+        }
+        if (edge) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int h = 0; h < H; ++h)
+#pragma unroll
+                    for (int k = 0; k < HC; ++k)
+                        if (p0 + g + 8 * h >= lim[nt][k]) x[nt][h][k] = -INFINITY;
+        }
+        bool over = false;
+        float m[NT][HC];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < HC; ++k) {
+                m[nt][k] = x[nt][0][k] + vl[0];
+#pragma unroll
+                for (int h = 1; h < H; ++h) m[nt][k] = fmaxf(m[nt][k], x[nt][h][k] + vl[h]);
+                over |= m[nt][k] > ref[nt][k] + kAcRoom;
+            }
+        if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float f[HC];
+#pragma unroll
+                for (int k = 0; k < HC; ++k) {
+                    float top = m[nt][k];
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                    f[k] = 1.f;
+                    if (top > ref[nt][k] + kAcRoom) {
+                        const float now = top - kAcUp;
+                        f[k] = ref[nt][k] == -INFINITY ? 0.f : ex2(ref[nt][k] - now);
+                        ref[nt][k] = now;
+                        l[nt][k] = l[nt][k] * f[k];
+                    }
+                }
+#pragma unroll
+                for (int mt = 0; mt < K::MT; ++mt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[mt][nt][e] *= f[HC == 2 ? (e & 1) : 0];
+            }
+        }
+        // probabilities, their sums, and their parts as the B fragments of the output
+        float rf[NT][HC];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < HC; ++k) rf[nt][k] = ref[nt][k] == -INFINITY ? 0.f : ref[nt][k];
+#pragma unroll
+        for (int u = 0; u < K::SUB; ++u) {
+            uint32_t pb[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    const int h = 2 * u + hh;
+                    float w[HC];
+#pragma unroll
+                    for (int k = 0; k < HC; ++k) {
+                        w[k] = ex2(x[nt][h][k] - rf[nt][k]);
+                        l[nt][k] += w[k];
+                        if constexpr (Q8) {
+                            w[k] *= vd[h];
+                            if (edge && p0 + g + 8 * h >= lim[nt][k]) w[k] = 0.f;   // its scale may be NaN
+                        }
+                    }
+                    uint32_t y;
+                    if constexpr (C == 1) {
+                        y = pack_f16(w[0], w[1]);
+                    } else if constexpr (Q8) {
+                        const float hi = f16_of(w[0]);
+                        y = pack_f16(hi, w[0] - hi);
+                    } else if constexpr (C == 2) {
+                        const float hi = bf16_of(w[0]);
+                        y = pack_bf16(hi, w[0] - hi);
+                    } else {
+                        const float hi = bf16_of(w[0]), mid = bf16_of(w[0] - hi);
+                        y = t & 1 ? pack_bf16(w[0] - hi - mid, 0.f) : pack_bf16(hi, mid);
+                    }
+                    pb[nt][hh] = movmatrix(y);
+                }
+            output(st + u * K::kBlock + K::kV, pb, p0 + 16 * u);
+        }
+    }
+
+    // Row r of this lane's columns (k) and eight-column tile nt, its sum over the warp's positions.
+    __device__ __forceinline__ int row_of(int nt, int k) const { return (8 * nt + 2 * t + k) / C; }
+    __device__ __forceinline__ bool writes() const { return C != 4 || !(t & 1); }
+    __device__ __forceinline__ float sum_of(int nt, int k) const {
+        float v = l[nt][k];
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+        return v;
+    }
+    // Four consecutive dims of that row: quad j of this lane's D / 32, at dim_of(j); the parts' columns added.
+    static constexpr int kQuads = D / 32;
+    __device__ __forceinline__ int dim_of(int j) const {
+        return Q8 ? (D / 8) * g + 4 * j : 64 * (j / 2) + 8 * g + 4 * (j % 2);
+    }
+    __device__ __forceinline__ float4 quad(int nt, int k, int j) const {
+        float w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int mt = 2 * j + (e >> 1), h = e & 1;
+            w[e] = o[mt][nt][2 * h + k];
+            if constexpr (C >= 2) w[e] += o[mt][nt][2 * h + 1];
+            if constexpr (C == 4) w[e] += __shfl_xor_sync(0xffffffffu, w[e], 1);
+        }
+        return make_float4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+__device__ __forceinline__ int clamp_len(int len, int most) { return len < 0 ? 0 : len > most ? most : len; }
+__device__ __forceinline__ int clamp_new(const CachedArgs &a, int b) {
+    const int n = a.n_new ? __ldg(a.n_new + b) : a.T;
+    return n < 0 ? 0 : n > a.T ? a.T : n;
+}
+// A stream's tiles of tp positions (a power of two): none where it has no new token.
+__device__ __forceinline__ int tiles_of(const CachedArgs &a, int b, int tp) {
+    const int len = clamp_len(__ldg(a.lengths + b), a.max_len);
+    return clamp_new(a, b) > 0 ? (int)((unsigned)(len + tp - 1) / (unsigned)tp) : 0;
+}
+
+template <bool F32> __device__ __forceinline__ void store4(uint8_t *dst, float4 v, float by) {
+    if constexpr (F32)
+        *reinterpret_cast<float4 *>(dst) = make_float4(v.x * by, v.y * by, v.z * by, v.w * by);
+    else
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(v.x * by, v.y * by), pack_bf16(v.z * by, v.w * by));
+}
+__device__ __forceinline__ void add4(float4 &acc, float f, float4 v) {
+    acc.x = fmaf(f, v.x, acc.x), acc.y = fmaf(f, v.y, acc.y);
+    acc.z = fmaf(f, v.z, acc.z), acc.w = fmaf(f, v.w, acc.w);
+}
+
+// Small batches: an item per cluster, its warps taking the tiles in turn; the partials meet in
+// shared memory and the output is written here.  PREFIX: the rows of every stream over
+// the shared prefix, an item per `nsplit` CTAs, partials to global memory.
+// blockIdx.x = item * nsplit + split.
+template <bool Q8, bool F32, int D, int NT, bool PREFIX>
+__global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NT>::kMinCtas)
+    attn_cached_kernel(const CachedArgs a, int nsplit) {
+    using K = AcCfg<Q8, F32, D, NT>;
+    extern __shared__ __align__(16) uint8_t sm[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int split = blockIdx.x % nsplit, item = blockIdx.x / nsplit;
+    const int grp = item % a.groups, hk = (item / a.groups) % a.kvh, b = PREFIX ? 0 : item / a.groups / a.kvh;
+    const int len = PREFIX ? a.max_len : clamp_len(__ldg(a.lengths + b), a.max_len);
+    const int nn = PREFIX ? a.T : clamp_new(a, b);
+    const int r0 = grp * K::RW;
+
+    WarpPass<Q8, F32, D, NT, PREFIX> w;
+    w.init(lane);
+    w.start(a, b, hk, len, sm + warp * K::kRing, split * kAcWarps + warp,
+            PREFIX || nn > 0 ? (len + K::TP - 1) / K::TP : 0, nsplit * kAcWarps);
+    w.load_rows(a, b, hk, r0, len, nn);
+    w.run();
     __syncthreads();
 
     // ---- the warps' partials
@@ -526,48 +687,37 @@ __global__ void __launch_bounds__(kAcThreads, NT == 1 ? 4 : 3) attn_cached_kerne
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int k = 0; k < HC; ++k) {
-            float v = l[nt][k];
+        for (int k = 0; k < w.HC; ++k) {
+            const float sum = w.sum_of(nt, k);
+            const int row = w.row_of(nt, k);
+            if (w.g == 0 && w.writes()) ml[warp * K::RW + row] = make_float2(w.ref[nt][k], sum);
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-            const int row = (8 * nt + 2 * t + k) / C;
-            if (g == 0 && (C != 4 || !(t & 1))) ml[warp * K::RW + row] = make_float2(ref[nt][k], v);
-#pragma unroll
-            for (int mt = 0; mt < K::MT; ++mt)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float w = o[mt][nt][2 * h + k];
-                    if constexpr (C >= 2) w += o[mt][nt][2 * h + 1];
-                    if constexpr (C == 4) w += __shfl_xor_sync(0xffffffffu, w, 1);
-                    const int d = Q8 ? (D / 8) * g + 2 * mt + h : 64 * (mt / 4) + 8 * g + 2 * (mt % 4) + h;
-                    if (C != 4 || !(t & 1)) part[(warp * K::RW + row) * D + d] = w;
-                }
+            for (int j = 0; j < w.kQuads; ++j) {
+                const float4 v = w.quad(nt, k, j);
+                if (w.writes()) *reinterpret_cast<float4 *>(part + (warp * K::RW + row) * D + w.dim_of(j)) = v;
+            }
         }
     __syncthreads();
     for (int i = threadIdx.x; i < K::RW * D / 4; i += kAcThreads) {
         const int row = i / (D / 4);
+        if (r0 + row >= a.rows) continue;
         float M = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kAcWarps; ++w) M = fmaxf(M, ml[w * K::RW + row].x);
+        for (int u = 0; u < kAcWarps; ++u) M = fmaxf(M, ml[u * K::RW + row].x);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         float sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < kAcWarps; ++w) {
-            const float2 e = ml[w * K::RW + row];
+        for (int u = 0; u < kAcWarps; ++u) {
+            const float2 e = ml[u * K::RW + row];
             if (e.y == 0.f) continue;
             const float f = part_weight(e, M);
-            const float4 v = *reinterpret_cast<const float4 *>(part + w * K::RW * D + i * 4);
-            acc.x = fmaf(f, v.x, acc.x), acc.y = fmaf(f, v.y, acc.y);
-            acc.z = fmaf(f, v.z, acc.z), acc.w = fmaf(f, v.w, acc.w);
+            add4(acc, f, *reinterpret_cast<const float4 *>(part + u * K::RW * D + i * 4));
             sum = fmaf(f, e.y, sum);
         }
         if constexpr (PREFIX) {
-            const int r = r0 + row;
-            if (r < a.rows) {
-                const int64_t at = ((int64_t)hk * a.rows + r) * nsplit + split;
-                *reinterpret_cast<float4 *>(a.p_o + at * D + (i % (D / 4)) * 4) = acc;
-                if (i % (D / 4) == 0) a.p_ml[at] = make_float2(M, sum);
-            }
+            const int64_t at = ((int64_t)hk * a.rows + r0 + row) * nsplit + split;
+            *reinterpret_cast<float4 *>(a.p_o + at * D + (i % (D / 4)) * 4) = acc;
+            if (i % (D / 4) == 0) a.p_ml[at] = make_float2(M, sum);
         } else {
             *reinterpret_cast<float4 *>(mine + i * 4) = acc;
             if (i % (D / 4) == 0) ml_mine[row] = make_float2(M, sum);
@@ -585,7 +735,7 @@ __global__ void __launch_bounds__(kAcThreads, NT == 1 ? 4 : 3) attn_cached_kerne
             float M = -INFINITY;
             for (int s = 0; s < nsplit; ++s)
                 M = fmaxf(M, nsplit > 1 ? ld_cluster_f2(cluster_map(ml_mine + row, s)).x : ml_mine[row].x);
-            const int64_t at = ((int64_t)hk * (gridDim.x / (nsplit * a.groups * a.kvh)) * a.rows + (int64_t)b * a.rows + r) * a.splits;
+            const int64_t at = (((int64_t)hk * a.B + b) * a.rows + r) * a.splits;
             for (int s = 0; s < a.splits; ++s) M = fmaxf(M, a.p_ml[at + s].x);
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
             float sum = 0.f;
@@ -604,67 +754,269 @@ __global__ void __launch_bounds__(kAcThreads, NT == 1 ? 4 : 3) attn_cached_kerne
                 }
                 if (e.y == 0.f) continue;
                 const float f = part_weight(e, M);
-                acc.x = fmaf(f, v.x, acc.x), acc.y = fmaf(f, v.y, acc.y);
-                acc.z = fmaf(f, v.z, acc.z), acc.w = fmaf(f, v.w, acc.w);
+                add4(acc, f, v);
                 sum = fmaf(f, e.y, sum);
             }
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            uint8_t *dst = a.out + b * a.o_stream + tt * a.o_token +
-                           ((int64_t)(hk * a.G + (r - tt * a.G)) * D + (i % (D / 4)) * 4) * (F32 ? 4 : 2);
-            if constexpr (F32)
-                *reinterpret_cast<float4 *>(dst) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-            else
-                *reinterpret_cast<uint2 *>(dst) =
-                    make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+            store4<F32>(a.out + b * a.o_stream + tt * a.o_token +
+                            ((int64_t)(hk * a.G + (r - tt * a.G)) * D + (i % (D / 4)) * 4) * (F32 ? 4 : 2),
+                        acc, sum == 0.f ? 0.f : 1.f / sum);
         }
         if (nsplit > 1) cluster_sync();              // the others have read this CTA's part
     }
 }
 
+// Large batches: the streams' lengths differ and only the device knows them, so the tiles of all items
+// stand in one list (stream, key head, row group, tile) that the grid's warps share out in equal runs,
+// whatever the lengths.  A warp's run covers the end of one item, whole items, the beginning of another;
+// it leaves a partial for each in slot (warp + item), which no other pair has: along the
+// list both only grow.  attn_join_kernel finds them by the same arithmetic.
+struct Share {
+    unsigned total, run;                             // tiles; tiles of a warp (the last may have fewer)
+    __device__ __forceinline__ void use(unsigned all, unsigned grid_warps) {
+        total = all;
+        run = max(1u, (all + grid_warps - 1) / grid_warps);
+    }
+};
+
+// The tiles of streams before b (`upto`) and of all, times the items of a stream.
+__device__ __forceinline__ unsigned tiles_before(const CachedArgs &a, int upto, int tp, unsigned *total) {
+    const int lane = threadIdx.x & 31;
+    unsigned before = 0, all = 0;
+    for (int b = lane; b < a.B; b += 32) {
+        const unsigned n = (unsigned)tiles_of(a, b, tp);
+        all += n;
+        if (b < upto) before += n;
+    }
+    before = __reduce_add_sync(0xffffffffu, before);
+    all = __reduce_add_sync(0xffffffffu, all);
+    const unsigned per = (unsigned)(a.kvh * a.groups);
+    *total = all * per;
+    return before * per;
+}
+
+template <bool Q8, bool F32, int D, int NT>
+__global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NT>::kMinCtas)
+    attn_share_kernel(const CachedArgs a) {
+    using K = AcCfg<Q8, F32, D, NT>;
+    extern __shared__ __align__(16) uint8_t sm[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const unsigned wid = blockIdx.x * kAcWarps + warp;
+    pdl_launch_dependents();
+    unsigned total;
+    tiles_before(a, 0, K::TP, &total);
+    Share sh;
+    sh.use(total, gridDim.x * kAcWarps);
+    unsigned x = wid * sh.run;                       // the host bounds both products
+    if (x >= total) return;
+    const unsigned x1 = min(total, x + sh.run);
+
+    // the stream that holds tile x: 32 streams a step, the running sum across the lanes
+    const unsigned per = (unsigned)(a.kvh * a.groups);
+    int b = 0;
+    unsigned s_b = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+        const unsigned n = b0 + lane < a.B ? tiles_of(a, b0 + lane, K::TP) * per : 0u;
+        unsigned upto = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        const uint32_t over = __ballot_sync(0xffffffffu, s_b + upto > x);
+        if (over) {
+            const int at = __ffs(over) - 1;
+            b = b0 + at;
+            s_b += __shfl_sync(0xffffffffu, upto - n, at);
+            break;
+        }
+        s_b += __shfl_sync(0xffffffffu, upto, 31);
+    }
+
+    WarpPass<Q8, F32, D, NT, false> w;
+    w.init(lane);
+    while (x < x1) {
+        const unsigned tiles = (unsigned)tiles_of(a, b, K::TP);
+        if (x >= s_b + tiles * per) {                // (a stream without tiles, too)
+            s_b += tiles * per;
+            ++b;
+            continue;
+        }
+        const int in = (int)((x - s_b) / tiles), tile0 = (int)(x - s_b - in * tiles);
+        const int n = (int)min(tiles - tile0, x1 - x);
+        const int hk = in / a.groups, grp = in - hk * a.groups;
+        const int len = clamp_len(__ldg(a.lengths + b), a.max_len);
+        w.start(a, b, hk, len, sm + warp * K::kRing, tile0, tile0 + n, 1);
+        w.load_rows(a, b, hk, grp * K::RW, len, clamp_new(a, b));
+        w.run();
+        __syncwarp();
+        const int64_t slot = (int64_t)b * per + in + wid;   // x only grows: so does the pair
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < w.HC; ++k) {
+                const float sum = w.sum_of(nt, k);
+                const int r = w.row_of(nt, k);
+                const bool mine = w.writes() && grp * K::RW + r < a.rows;
+                if (w.g == 0 && mine) a.s_ml[slot * K::RW + r] = make_float2(w.ref[nt][k], sum);
+#pragma unroll
+                for (int j = 0; j < w.kQuads; ++j) {
+                    const float4 v = w.quad(nt, k, j);
+                    if (mine) *reinterpret_cast<float4 *>(a.s_o + (slot * K::RW + r) * D + w.dim_of(j)) = v;
+                }
+            }
+        x += n;
+    }
+}
+
+// One output row (stream, token, query head) per WPR warps: its partials from attn_share_kernel
+// and from the prefix, weighted to a common reference, added in the order of the list.
+constexpr int kJoinWarps = 8;
+template <bool F32, int D, int WPR>
+__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const CachedArgs a, int rw, int tp, unsigned warps) {
+    __shared__ float4 s_acc[kJoinWarps][32];
+    __shared__ float s_sum[kJoinWarps];
+    constexpr int LPR = D / 4;                      // lanes of a row's float4s
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const unsigned r_all = blockIdx.x * (kJoinWarps / WPR) + warp / WPR;   // (stream, key head, row)
+    const int part = warp % WPR;
+    const unsigned n_rows = (unsigned)(a.B * a.kvh * a.rows), rr = min(r_all, n_rows - 1);
+    const int bh = rr / (unsigned)a.rows, r = rr - bh * a.rows, b = bh / a.kvh, hk = bh - b * a.kvh;
+    const int tt = r / a.G, grp = r / rw, in_grp = r - grp * rw;
+    const int tiles = tiles_of(a, b, tp), nn = clamp_new(a, b);
+    unsigned total;
+    const unsigned s_b = tiles_before(a, b, tp, &total);
+    Share sh;
+    sh.use(total, warps);
+    const int in = hk * a.groups + grp;
+    const unsigned x = s_b + in * tiles;
+    const unsigned w0 = x / sh.run, w1 = tiles ? (x + tiles - 1) / sh.run + 1 : w0;
+    const int own = (int)(w1 - w0), all = own + a.splits;
+    const int64_t slot0 = (int64_t)b * a.kvh * a.groups + in + w0;
+    const int64_t p_at = (((int64_t)hk * a.B + b) * a.rows + r) * a.splits;
+    pdl_wait();                                     // the partials are written
+
+    float M = -INFINITY;
+    for (int i = lane; i < all; i += 32)
+        M = fmaxf(M, i < own ? a.s_ml[(slot0 + i) * rw + in_grp].x : a.p_ml[p_at + i - own].x);
+    M = warp_max(M);
+    // 32 / LPR partials at a time (one for head_dim 128), LPR lanes each
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+    const int d = (lane % LPR) * 4;
+#pragma unroll 4
+    for (int i = part * (32 / LPR) + lane / LPR; i < all; i += WPR * (32 / LPR)) {
+        const float2 e = i < own ? a.s_ml[(slot0 + i) * rw + in_grp] : a.p_ml[p_at + i - own];
+        const float4 v = *reinterpret_cast<const float4 *>(i < own ? a.s_o + ((slot0 + i) * rw + in_grp) * D + d
+                                                                   : a.p_o + (p_at + i - own) * D + d);
+        if (e.y != 0.f) {
+            const float f = part_weight(e, M);
+            add4(acc, f, v);
+            sum = fmaf(f, e.y, sum);
+        }
+    }
+    if constexpr (LPR == 16) {
+        acc.x += __shfl_xor_sync(0xffffffffu, acc.x, 16), acc.y += __shfl_xor_sync(0xffffffffu, acc.y, 16);
+        acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16), acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+    }
+    if constexpr (WPR > 1) {
+        s_acc[warp][lane] = acc;
+        if (lane == 0) s_sum[warp] = sum;
+        __syncthreads();
+        if (part) return;
+#pragma unroll
+        for (int i = 1; i < WPR; ++i) {
+            add4(acc, 1.f, s_acc[warp + i][lane]);
+            sum += s_sum[warp + i];
+        }
+    }
+    if (r_all < n_rows && tt < nn && lane < LPR)
+        store4<F32>(a.out + b * a.o_stream + tt * a.o_token + ((int64_t)(hk * a.G + (r - tt * a.G)) * D + d) * (F32 ? 4 : 2),
+                    acc, sum == 0.f ? 0.f : 1.f / sum);
+}
+
 // ------------------------------------------------------------------------- launches
 
 // CTAs that share the prefix's positions, per key head and row group.
-int prefix_splits(int rows, int kvh, int prefix_len, int rw, int sms) {
+int prefix_splits(int rows, int kvh, int prefix_len, int rw, int tp, int sms) {
     const int groups = (rows + rw - 1) / rw;
-    const int tiles = (prefix_len + kAcTile - 1) / kAcTile;
+    const int tiles = (prefix_len + tp - 1) / tp;
     const int most = std::max(1, tiles / (2 * kAcWarps));
     const int want = std::max(1, 4 * sms / std::max(1, groups * kvh));
     return std::max(1, std::min(std::min(most, want), 32));
 }
 
-template <bool Q8, bool F32, int D, int NT, bool PREFIX>
-cudaError_t launch(const CachedArgs &a, int items, int nsplit, int dev, cudaStream_t s) {
-    using K = AcCfg<Q8, F32, D, NT>;
-    auto fn = attn_cached_kernel<Q8, F32, D, NT, PREFIX>;
-    static bool ready[64] = {};                     // per device; setting it twice is harmless
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!ready[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, K::kSmem);
-        if (e != cudaSuccess) return e;
-        ready[dev] = true;
-    }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(items * nsplit));
-    cfg.blockDim = dim3(kAcThreads);
-    cfg.dynamicSmemBytes = K::kSmem;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = PREFIX ? 1 : (unsigned)nsplit;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fn, a, nsplit);
+enum : int { kPassCluster = 0, kPassPrefix = 1, kPassShare = 2 };
+
+// Shared-memory limit and resident CTAs per SM of a variant, looked up once per device.
+struct Ready {
+    bool done;
+    int per_sm;
+};
+template <typename F> cudaError_t make_ready(Ready *r, F fn, int smem) {
+    if (r->done) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&r->per_sm, fn, kAcThreads, smem);
+    if (e != cudaSuccess) return e;
+    r->done = r->per_sm > 0;
+    return r->done ? cudaSuccess : cudaErrorInvalidConfiguration;
 }
 
+template <typename F, typename... A>
+cudaError_t launch_ex(F fn, unsigned grid, int threads, int smem, unsigned cluster, bool pdl, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    int n = 0;
+    if (cluster > 1) {
+        at[n].id = cudaLaunchAttributeClusterDimension;
+        at[n].val.clusterDim.x = cluster;
+        at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (pdl) {
+        at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
+    cfg.attrs = at;
+    cfg.numAttrs = (unsigned)n;
+    return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+
+// kind Cluster or Prefix: `ctas` of clusters of nsplit; kind Share: every CTA the SMs hold, *ctas says how many.
+template <bool Q8, bool F32, int D, int NT>
+cudaError_t launch(int kind, const CachedArgs &a, unsigned *ctas, int nsplit, int dev, cudaStream_t s, bool plan) {
+    using K = AcCfg<Q8, F32, D, NT>;
+    static Ready ready[3][64] = {};
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    cudaError_t e;
+    if (kind == kPassShare) {
+        auto fn = attn_share_kernel<Q8, F32, D, NT>;
+        if ((e = make_ready(&ready[kind][dev], fn, K::kSmem)) != cudaSuccess) return e;
+        *ctas = (unsigned)(ready[kind][dev].per_sm * sms_of(dev));
+        return plan ? cudaSuccess : launch_ex(fn, *ctas, kAcThreads, K::kSmem, 1, false, s, a);
+    }
+    if (kind == kPassPrefix) {
+        auto fn = attn_cached_kernel<Q8, F32, D, NT, true>;
+        if ((e = make_ready(&ready[kind][dev], fn, K::kSmem)) != cudaSuccess) return e;
+        return launch_ex(fn, *ctas, kAcThreads, K::kSmem, 1, false, s, a, nsplit);
+    }
+    auto fn = attn_cached_kernel<Q8, F32, D, NT, false>;
+    if ((e = make_ready(&ready[kind][dev], fn, K::kSmem)) != cudaSuccess) return e;
+    return launch_ex(fn, *ctas, kAcThreads, K::kSmem, (unsigned)nsplit, false, s, a, nsplit);
+}
+
+constexpr int tile_positions(bool q8, int d) { return q8 || d == 64 ? 32 : 16; }   // AcCfg::TP
 constexpr int rows_per_tile(bool q8, bool f32) { return 8 / (q8 ? (f32 ? 2 : 1) : (f32 ? 4 : 2)); }
 
-template <bool PREFIX>
-cudaError_t dispatch(bool q8, bool f32, int d, int nt, const CachedArgs &a, int items, int nsplit, int dev,
-                     cudaStream_t s) {
+cudaError_t dispatch(int kind, bool q8, bool f32, int d, int nt, const CachedArgs &a, unsigned *ctas, int nsplit, int dev,
+                     cudaStream_t s, bool plan = false) {
 #define QD_AC(Q, F, DD, N) \
-    if (q8 == Q && f32 == F && d == DD && nt == N) return launch<Q, F, DD, N, PREFIX>(a, items, nsplit, dev, s);
+    if (q8 == Q && f32 == F && d == DD && nt == N) return launch<Q, F, DD, N>(kind, a, ctas, nsplit, dev, s, plan);
 #define QD_AC2(Q, F) QD_AC(Q, F, 64, 1) QD_AC(Q, F, 64, 2) QD_AC(Q, F, 128, 1) QD_AC(Q, F, 128, 2)
     QD_AC2(false, false) QD_AC2(false, true) QD_AC2(true, false) QD_AC2(true, true)
 #undef QD_AC2
@@ -672,8 +1024,89 @@ cudaError_t dispatch(bool q8, bool f32, int d, int nt, const CachedArgs &a, int 
     return cudaErrorInvalidValue;
 }
 
-// workspace: (ref, sum) of every partial, then its output row
-size_t ml_bytes(int kvh, int64_t rows, int splits) { return ((size_t)kvh * rows * splits * 8 + 255) / 256 * 256; }
+cudaError_t launch_join(bool f32, int d, const CachedArgs &a, int rw, int tp, unsigned warps, bool many, cudaStream_t s) {
+    const long long rows = (long long)a.B * a.kvh * a.rows;
+    const int wpr = many ? kJoinWarps : 1, per = kJoinWarps / wpr;
+    const unsigned grid = (unsigned)((rows + per - 1) / per);
+#define QD_JOIN(F, DD, W) \
+    if (f32 == F && d == DD && wpr == W) return launch_ex(attn_join_kernel<F, DD, W>, grid, kJoinWarps * 32, 0, 1, true, s, a, rw, tp, warps);
+    QD_JOIN(false, 64, 1) QD_JOIN(false, 128, 1) QD_JOIN(true, 64, 1) QD_JOIN(true, 128, 1)
+    QD_JOIN(false, 64, kJoinWarps) QD_JOIN(false, 128, kJoinWarps) QD_JOIN(true, 64, kJoinWarps) QD_JOIN(true, 128, kJoinWarps)
+#undef QD_JOIN
+    return cudaErrorInvalidValue;
+}
+
+// How a call runs, from its sizes alone.
+struct Plan {
+    int nt, rw, groups, tp;             // own caches: row tiles, rows per CTA, row groups, positions of a tile
+    int nsplit;                         // CTAs of a cluster (one cluster per item); 0: shared out
+    unsigned ctas;                      // of the shared-out pass
+    int64_t rows_all;
+    int p_nt, p_rw, p_groups, splits;   // the prefix
+    size_t p_ml, p_o, s_ml, s_o, bytes; // workspace offsets
+};
+
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+qd_status make_plan(const qd_kv_cache *cache, const qd_kv_cache *prefix, int prefix_length, bool f32, int T, int QH,
+                    int max_length, int dev, Plan *p) {
+    *p = {};
+    const int kvh = cache->n_kv_heads, d = cache->head_dim, B = cache->n_streams, G = QH / kvh;
+    const int sms = sms_of(dev);
+    const bool q8 = cache->format == QD_KV_Q8;
+    const int rows = T * G, per = rows_per_tile(q8, f32);
+    p->rows_all = (int64_t)rows * B;
+    p->nt = rows > per ? 2 : 1, p->rw = per * p->nt, p->groups = (rows + p->rw - 1) / p->rw;
+    const int64_t items = (int64_t)B * kvh * p->groups;
+    p->tp = tile_positions(q8, d);
+    const int tiles = (max_length + p->tp - 1) / p->tp;
+    if (items * tiles > (1ll << 31)) return QD_EUNSUPPORTED;
+    // A cluster per item while the grid is one wave and a warp's share short; longer or larger
+    // batches are shared out.
+    p->nsplit = 1;
+    while (p->nsplit < kAcMaxCluster && items * p->nsplit < 2 * sms && tiles > p->nsplit * kAcWarps) p->nsplit *= 2;
+    if (items * p->nsplit > 4 * sms || tiles > 4 * p->nsplit * kAcWarps) p->nsplit = 0;
+    size_t at = 0;
+    if (prefix && prefix_length > 0) {
+        const bool pq8 = prefix->format == QD_KV_Q8;
+        const int pper = rows_per_tile(pq8, f32);
+        p->p_nt = p->rows_all > pper ? 2 : 1, p->p_rw = pper * p->p_nt;
+        p->p_groups = (int)((p->rows_all + p->p_rw - 1) / p->p_rw);
+        p->splits = prefix_splits((int)p->rows_all, kvh, prefix_length, p->p_rw, tile_positions(pq8, d), sms);
+        p->p_ml = at, at = up256(at + (size_t)kvh * p->rows_all * p->splits * 8);
+        p->p_o = at, at = up256(at + (size_t)kvh * p->rows_all * p->splits * d * 4);
+    }
+    if (!p->nsplit) {
+        const CachedArgs none = {};
+        if (dispatch(kPassShare, q8, f32, d, p->nt, none, &p->ctas, 0, dev, nullptr, true) != cudaSuccess) return QD_ECUDA;
+        const size_t slots = (size_t)items + (size_t)p->ctas * kAcWarps;
+        p->s_ml = at, at = up256(at + slots * p->rw * 8);
+        p->s_o = at, at = up256(at + slots * p->rw * d * 4);
+    }
+    p->bytes = at;
+    return QD_OK;
+}
+
+// The checks of sizes that the call and its workspace query share.
+qd_status check_sizes(const qd_kv_cache *cache, const qd_kv_cache *prefix, int prefix_length, int dtype, int n_tokens,
+                      int n_q_heads, int max_length) {
+    qd_status st = check_cache(cache, -1, false);
+    if (st != QD_OK) return st;
+    if (prefix_length < 0 || (!prefix && prefix_length)) return QD_EINVAL;
+    if (prefix && prefix_length > 0) {
+        if ((st = check_cache(prefix, -1, true)) != QD_OK) return st;
+        if (prefix->n_kv_heads != cache->n_kv_heads || prefix->head_dim != cache->head_dim ||
+            prefix_length > prefix->smax)
+            return QD_EINVAL;
+    }
+    const int kvh = cache->n_kv_heads;
+    if ((dtype != QD_F32 && dtype != QD_BF16) || n_tokens < 1 || n_q_heads < kvh || n_q_heads % kvh) return QD_EINVAL;
+    if (max_length < 1 || max_length > cache->smax) return QD_EINVAL;
+    if (n_tokens > kAcMaxTokens) return QD_EUNSUPPORTED;
+    const int64_t all = (int64_t)n_tokens * (n_q_heads / kvh) * cache->n_streams;
+    if (all > (1 << 24) || all * kvh > (1 << 26)) return QD_EUNSUPPORTED;
+    return QD_OK;
+}
 
 }  // namespace
 
@@ -683,23 +1116,18 @@ using namespace qd;
 
 extern "C" {
 
-qd_status qd_attn_cached_workspace(int n_streams, int n_tokens, int n_q_heads, int n_kv_heads, int head_dim,
-                                   int prefix_length, size_t *bytes) {
+qd_status qd_attn_cached_workspace(const qd_kv_cache *cache, const qd_kv_cache *prefix, int prefix_length, int dtype,
+                                   int n_tokens, int n_q_heads, int max_length, size_t *bytes) {
     if (!bytes) return QD_EINVAL;
     *bytes = 0;
-    if (n_streams < 1 || n_tokens < 1 || n_kv_heads < 1 || n_q_heads < n_kv_heads || n_q_heads % n_kv_heads ||
-        prefix_length < 0)
-        return QD_EINVAL;
-    if ((head_dim != 64 && head_dim != 128) || n_tokens > kAcMaxTokens) return QD_EUNSUPPORTED;
-    if (!prefix_length) return QD_OK;
+    qd_status st = check_sizes(cache, prefix, prefix_length, dtype, n_tokens, n_q_heads, max_length);
+    if (st != QD_OK) return st;
     int dev = 0;
-    const int sms = cudaGetDevice(&dev) == cudaSuccess ? sms_of(dev) : 152;
-    const int64_t rows = (int64_t)n_streams * n_tokens * (n_q_heads / n_kv_heads);
-    if (rows > (1 << 24)) return QD_EUNSUPPORTED;
-    // the most splits of any type's tiling
-    int most = 1;
-    for (int rw = 2; rw <= 16; rw <<= 1) most = std::max(most, prefix_splits((int)rows, n_kv_heads, prefix_length, rw, sms));
-    *bytes = ml_bytes(n_kv_heads, rows, most) + (size_t)n_kv_heads * rows * most * head_dim * 4;
+    if (cudaGetDevice(&dev) != cudaSuccess) return QD_ECUDA;
+    Plan p;
+    if ((st = make_plan(cache, prefix, prefix_length, dtype == QD_F32, n_tokens, n_q_heads, max_length, dev, &p)) != QD_OK)
+        return st;
+    *bytes = p.bytes;
     return QD_OK;
 }
 
@@ -708,75 +1136,60 @@ qd_status qd_attn_cached(const qd_kv_cache *cache, const qd_kv_cache *prefix, in
                          int64_t out_token_stride, int dtype, int n_tokens, int n_q_heads, float scale,
                          const int32_t *lengths_dev, const int32_t *n_new_dev, int max_length, void *workspace_dev,
                          size_t workspace_bytes, void *cuda_stream) {
-    qd_status st = check_cache(cache, -1, false);
+    qd_status st = check_sizes(cache, prefix, prefix_length, dtype, n_tokens, n_q_heads, max_length);
     if (st != QD_OK) return st;
-    const bool with_prefix = prefix && prefix_length > 0;
-    if (prefix_length < 0 || (!prefix && prefix_length)) return QD_EINVAL;
-    if (with_prefix) {
-        if ((st = check_cache(prefix, -1, true)) != QD_OK) return st;
-        if (prefix->n_kv_heads != cache->n_kv_heads || prefix->head_dim != cache->head_dim ||
-            prefix_length > prefix->smax)
-            return QD_EINVAL;
-    }
-    const int kvh = cache->n_kv_heads, d = cache->head_dim, B = cache->n_streams;
-    if ((dtype != QD_F32 && dtype != QD_BF16) || n_tokens < 1 || n_q_heads < kvh || n_q_heads % kvh) return QD_EINVAL;
-    if (max_length < 1 || max_length > cache->smax || !(scale > -3e38f && scale < 3e38f)) return QD_EINVAL;
-    if (n_tokens > kAcMaxTokens) return QD_EUNSUPPORTED;
-    if (!q_dev || !out_dev || !lengths_dev) return QD_EINVAL;
-    const int64_t unit = dtype == QD_F32 ? 4 : 8, e = dtype == QD_F32 ? 4 : 2;
+    const bool with_prefix = prefix && prefix_length > 0, f32 = dtype == QD_F32;
+    if (!(scale > -3e38f && scale < 3e38f) || !q_dev || !out_dev || !lengths_dev) return QD_EINVAL;
+    const int64_t unit = f32 ? 4 : 8, e = f32 ? 4 : 2;
     for (int64_t v : {q_stream_stride, q_token_stride, out_stream_stride, out_token_stride})
         if (v < 0 || v % unit) return QD_EINVAL;
     if (!is_aligned(q_dev, 16) || !is_aligned(out_dev, 16) || !is_aligned(lengths_dev, 4) || !is_aligned(n_new_dev, 4))
         return QD_EINVAL;
-    const int G = n_q_heads / kvh;
-    const int64_t rows = (int64_t)n_tokens * G, all = rows * B;
-    if (all > (1 << 24) || all * kvh > (1 << 26)) return QD_EUNSUPPORTED;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return QD_ECUDA;
-    const int sms = sms_of(dev);
     if ((st = check_cache(cache, dev, false)) != QD_OK) return st;
     if (with_prefix && (st = check_cache(prefix, dev, true)) != QD_OK) return st;
     if (!on_device(q_dev, dev) || !on_device(out_dev, dev) || !on_device(lengths_dev, dev) ||
         (n_new_dev && !on_device(n_new_dev, dev)))
         return QD_EINVAL;
+    Plan p;
+    if ((st = make_plan(cache, prefix, prefix_length, f32, n_tokens, n_q_heads, max_length, dev, &p)) != QD_OK) return st;
+    if (p.bytes && (!workspace_dev || workspace_bytes < p.bytes || !is_aligned(workspace_dev, 256) ||
+                    !on_device(workspace_dev, dev)))
+        return QD_EINVAL;
 
-    const bool f32 = dtype == QD_F32;
+    const int kvh = cache->n_kv_heads, d = cache->head_dim, B = cache->n_streams;
+    uint8_t *ws = static_cast<uint8_t *>(workspace_dev);
     cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
     CachedArgs a = {};
     a.q = static_cast<const uint8_t *>(q_dev), a.out = static_cast<uint8_t *>(out_dev);
     a.q_stream = q_stream_stride * e, a.q_token = q_token_stride * e;
     a.o_stream = out_stream_stride * e, a.o_token = out_token_stride * e;
     a.lengths = lengths_dev, a.n_new = n_new_dev;
-    a.T = n_tokens, a.G = G, a.kvh = kvh;
+    a.B = B, a.T = n_tokens, a.G = n_q_heads / kvh, a.kvh = kvh;
     a.scale2 = scale * 1.4426950408889634f;
-
     if (with_prefix) {
-        size_t need = 0;
-        if ((st = qd_attn_cached_workspace(B, n_tokens, n_q_heads, kvh, d, prefix_length, &need)) != QD_OK) return st;
-        if (!workspace_dev || workspace_bytes < need || !is_aligned(workspace_dev, 256) || !on_device(workspace_dev, dev))
-            return QD_EINVAL;
-        const bool q8 = prefix->format == QD_KV_Q8;
-        const int per = rows_per_tile(q8, f32), nt = all > per ? 2 : 1, rw = per * nt;
-        CachedArgs p = a;
-        p.c = kv_view(prefix);
-        p.rows = (int)all, p.groups = (int)((all + rw - 1) / rw), p.max_len = prefix_length;
-        const int splits = prefix_splits((int)all, kvh, prefix_length, rw, sms);
-        p.p_ml = static_cast<float2 *>(workspace_dev);
-        p.p_o = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace_dev) + ml_bytes(kvh, all, splits));
-        p.splits = splits;
-        if (dispatch<true>(q8, f32, d, nt, p, p.groups * kvh, splits, dev, s) != cudaSuccess) return QD_ECUDA;
-        a.p_ml = p.p_ml, a.p_o = p.p_o, a.splits = splits;
+        a.p_ml = reinterpret_cast<float2 *>(ws + p.p_ml), a.p_o = reinterpret_cast<float *>(ws + p.p_o);
+        a.splits = p.splits;
+        CachedArgs x = a;
+        x.c = kv_view(prefix);
+        x.rows = (int)p.rows_all, x.groups = p.p_groups, x.max_len = prefix_length;
+        unsigned ctas = (unsigned)(p.p_groups * kvh * p.splits);
+        if (dispatch(kPassPrefix, prefix->format == QD_KV_Q8, f32, d, p.p_nt, x, &ctas, p.splits, dev, s) != cudaSuccess)
+            return QD_ECUDA;
     }
-
     const bool q8 = cache->format == QD_KV_Q8;
-    const int per = rows_per_tile(q8, f32), nt = rows > per ? 2 : 1, rw = per * nt;
     a.c = kv_view(cache);
-    a.rows = (int)rows, a.groups = (int)((rows + rw - 1) / rw), a.max_len = max_length;
-    const int64_t items = (int64_t)B * kvh * a.groups;
-    // split a stream until the CTAs fill the SMs, but leave every warp a tile
-    int nsplit = 1;
-    while (nsplit < kAcMaxCluster && items * nsplit < 3 * sms && max_length > nsplit * kAcWarps * kAcTile) nsplit *= 2;
-    return dispatch<false>(q8, f32, d, nt, a, (int)items, nsplit, dev, s) == cudaSuccess ? QD_OK : QD_ECUDA;
+    a.rows = n_tokens * a.G, a.groups = p.groups, a.max_len = max_length;
+    if (p.nsplit) {
+        unsigned ctas = (unsigned)((int64_t)B * kvh * p.groups * p.nsplit);
+        return dispatch(kPassCluster, q8, f32, d, p.nt, a, &ctas, p.nsplit, dev, s) == cudaSuccess ? QD_OK : QD_ECUDA;
+    }
+    a.s_ml = reinterpret_cast<float2 *>(ws + p.s_ml), a.s_o = reinterpret_cast<float *>(ws + p.s_o);
+    if (dispatch(kPassShare, q8, f32, d, p.nt, a, &p.ctas, 0, dev, s) != cudaSuccess) return QD_ECUDA;
+    // many partials a row (long streams, few of them): several warps per row
+    const unsigned warps = p.ctas * kAcWarps, items = (unsigned)((int64_t)B * kvh * p.groups);
+    return launch_join(f32, d, a, p.rw, p.tp, warps, warps / items + p.splits > 16, s) == cudaSuccess ? QD_OK : QD_ECUDA;
 }
 
 }  // extern "C"
