@@ -118,7 +118,6 @@ template <bool Q8, bool F32, int D, int NT> struct AcCfg {
     static constexpr int KW = Q8 ? 4 : 2;                          // k-steps per piece
     static constexpr int KS = D / 16, MT = D / 16;
     static constexpr int LB = D * ES;                              // bytes of a row
-    static constexpr int VP = LB / 128 > 0 ? LB / 128 : 1;         // V accesses per position and lane
     static constexpr int CP = LB / 32;                             // 16-byte copies per lane and block, of K or V
     static constexpr int CR = 512 / LB;                            // rows that one copy instruction covers
     static constexpr int kTurn = 8 / CR;                           // copies after which the places repeat, 8 rows on
@@ -130,6 +129,7 @@ template <bool Q8, bool F32, int D, int NT> struct AcCfg {
     static constexpr int kBlock = 2 * kV;
     static constexpr int kS = SUB * kBlock;                        // of the scales in a tile: [K, V][TP]
     static constexpr int kTileBytes = kS + (Q8 ? TP * 8 : 0);
+    
     static constexpr int kStages = kTileBytes > 8192 ? 2 : 3;
     static constexpr int kRing = kStages * kTileBytes;             // per warp
     // after the pass the rings' space holds the warps' partials, then the CTA's
@@ -434,11 +434,11 @@ template <bool Q8, bool F32, int D, int NT, bool PREFIX> struct WarpPass {
                 }
             }
         } else {
-            uint32_t v[4][4 * K::VP];
+            uint32_t v[4][4 * (K::LB / 128)];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < K::VP; ++j) {
+                for (int j = 0; j < (K::LB / 128); ++j) {
                     const uint4 u = *reinterpret_cast<const uint4 *>(sv + vget[i & 1] + (i >> 1) * 8 * K::LB + 128 * j);
                     v[i][4 * j] = u.x, v[i][4 * j + 1] = u.y, v[i][4 * j + 2] = u.z, v[i][4 * j + 3] = u.w;
                 }
@@ -449,12 +449,12 @@ template <bool Q8, bool F32, int D, int NT, bool PREFIX> struct WarpPass {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int w = 0; w < 4 * K::VP; ++w)
+                    for (int w = 0; w < 4 * (K::LB / 128); ++w)
                         odd |= (v[i][w] & 0x7f80u) == 0x7f80u || (v[i][w] & 0x7f800000u) == 0x7f800000u;
                 odd = __any_sync(0xffffffffu, odd);
             }
 #pragma unroll
-            for (int w = 0; w < 4 * K::VP; ++w) {
+            for (int w = 0; w < 4 * (K::LB / 128); ++w) {
                 const uint32_t f[4] = {__byte_perm(v[0][w], v[1][w], 0x5410), __byte_perm(v[0][w], v[1][w], 0x7632),
                                        __byte_perm(v[2][w], v[3][w], 0x5410), __byte_perm(v[2][w], v[3][w], 0x7632)};
                 if (!PREFIX && odd) {
@@ -664,6 +664,8 @@ __global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NT>::kMinCtas)
     attn_cached_kernel(const CachedArgs a, int nsplit) {
     using K = AcCfg<Q8, F32, D, NT>;
     extern __shared__ __align__(16) uint8_t sm[];
+    pdl_wait();
+    pdl_launch_dependents();                         // after the wait: see attn_join_kernel
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = blockIdx.x % nsplit, item = blockIdx.x / nsplit;
     const int grp = item % a.groups, hk = (item / a.groups) % a.kvh, b = PREFIX ? 0 : item / a.groups / a.kvh;
@@ -771,10 +773,15 @@ __global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NT>::kMinCtas)
 // it leaves a partial for each in slot (warp + item), which no other pair has: along the
 // list both only grow.  attn_join_kernel finds them by the same arithmetic.
 struct Share {
-    unsigned total, run;                             // tiles; tiles of a warp (the last may have fewer)
-    __device__ __forceinline__ void use(unsigned all, unsigned grid_warps) {
+    unsigned total, run, more;                       // tiles; a warp's run; the first `more` warps take one tile more
+    __device__ __forceinline__ void use(unsigned all, unsigned warps) {
         total = all;
-        run = max(1u, (all + grid_warps - 1) / grid_warps);
+        run = all / warps, more = all - run * warps;
+    }
+    __device__ __forceinline__ unsigned first(unsigned w) const { return w * run + min(w, more); }
+    __device__ __forceinline__ unsigned owner(unsigned x) const {   // x < total
+        const unsigned big = more * (run + 1);
+        return x < big ? x / (run + 1) : more + (x - big) / run;
     }
 };
 
@@ -782,6 +789,7 @@ struct Share {
 __device__ __forceinline__ unsigned tiles_before(const CachedArgs &a, int upto, int tp, unsigned *total) {
     const int lane = threadIdx.x & 31;
     unsigned before = 0, all = 0;
+#pragma unroll 4
     for (int b = lane; b < a.B; b += 32) {
         const unsigned n = (unsigned)tiles_of(a, b, tp);
         all += n;
@@ -801,14 +809,15 @@ __global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NT>::kMinCtas)
     extern __shared__ __align__(16) uint8_t sm[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned wid = blockIdx.x * kAcWarps + warp;
-    pdl_launch_dependents();
+    pdl_wait();
+    pdl_launch_dependents();                         // after the wait: see attn_join_kernel
     unsigned total;
     tiles_before(a, 0, K::TP, &total);
     Share sh;
     sh.use(total, gridDim.x * kAcWarps);
-    unsigned x = wid * sh.run;                       // the host bounds both products
-    if (x >= total) return;
-    const unsigned x1 = min(total, x + sh.run);
+    unsigned x = sh.first(wid);
+    const unsigned x1 = sh.first(wid + 1);
+    if (x >= x1) return;                             // more warps than tiles: those behind have none
 
     // the stream that holds tile x: 32 streams a step, the running sum across the lanes
     const unsigned per = (unsigned)(a.kvh * a.groups);
@@ -874,9 +883,11 @@ constexpr int kJoinWarps = 8;
 template <bool F32, int D, int WPR>
 __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const CachedArgs a, int rw, int tp, unsigned warps) {
     __shared__ float4 s_acc[kJoinWarps][32];
-    __shared__ float s_sum[kJoinWarps];
+    __shared__ float2 s_ml[kJoinWarps];
     constexpr int LPR = D / 4;                      // lanes of a row's float4s
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // lengths and n_new may be read before the wait: attn_share_kernel lets this kernel start only after
+    // its own wait for whatever wrote them
     const unsigned r_all = blockIdx.x * (kJoinWarps / WPR) + warp / WPR;   // (stream, key head, row)
     const int part = warp % WPR;
     const unsigned n_rows = (unsigned)(a.B * a.kvh * a.rows), rr = min(r_all, n_rows - 1);
@@ -889,30 +900,58 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const Cached
     sh.use(total, warps);
     const int in = hk * a.groups + grp;
     const unsigned x = s_b + in * tiles;
-    const unsigned w0 = x / sh.run, w1 = tiles ? (x + tiles - 1) / sh.run + 1 : w0;
-    const int own = (int)(w1 - w0), all = own + a.splits;
+    const unsigned w0 = tiles ? sh.owner(x) : 0u;
+    const int own = tiles ? (int)(sh.owner(x + tiles - 1) + 1 - w0) : 0, all = own + a.splits;
     const int64_t slot0 = (int64_t)b * a.kvh * a.groups + in + w0;
     const int64_t p_at = (((int64_t)hk * a.B + b) * a.rows + r) * a.splits;
     pdl_wait();                                     // the partials are written
 
-    float M = -INFINITY;
-    for (int i = lane; i < all; i += 32)
-        M = fmaxf(M, i < own ? a.s_ml[(slot0 + i) * rw + in_grp].x : a.p_ml[p_at + i - own].x);
-    M = warp_max(M);
-    // 32 / LPR partials at a time (one for head_dim 128), LPR lanes each
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
+    // 32 / LPR partials at a time (one for head_dim 128), LPR lanes each; kBatch of those are loaded
+    // together, (ref, sum) with their rows, then weighted to the running reference
+    constexpr int kBatch = 8, kStep = WPR * (32 / LPR);
     const int d = (lane % LPR) * 4;
-#pragma unroll 4
-    for (int i = part * (32 / LPR) + lane / LPR; i < all; i += WPR * (32 / LPR)) {
-        const float2 e = i < own ? a.s_ml[(slot0 + i) * rw + in_grp] : a.p_ml[p_at + i - own];
-        const float4 v = *reinterpret_cast<const float4 *>(i < own ? a.s_o + ((slot0 + i) * rw + in_grp) * D + d
-                                                                   : a.p_o + (p_at + i - own) * D + d);
-        if (e.y != 0.f) {
-            const float f = part_weight(e, M);
-            add4(acc, f, v);
-            sum = fmaf(f, e.y, sum);
+    float M = -INFINITY, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = part * (32 / LPR) + lane / LPR; i0 - lane / LPR < all; i0 += kBatch * kStep) {
+        float2 e[kBatch];
+        float4 v[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int i = i0 + j * kStep;
+            e[j] = make_float2(-INFINITY, 0.f);
+            v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i < own) {
+                const int64_t at = (slot0 + i) * rw + in_grp;
+                e[j] = a.s_ml[at];
+                v[j] = *reinterpret_cast<const float4 *>(a.s_o + at * D + d);
+            } else if (i < all) {
+                const int64_t at = p_at + i - own;
+                e[j] = a.p_ml[at];
+                v[j] = *reinterpret_cast<const float4 *>(a.p_o + at * D + d);
+            }
         }
+        float now = M;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) now = fmaxf(now, e[j].x);
+        const float keep = part_weight(make_float2(M, sum), now);
+        acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
+        sum *= keep;
+        M = now;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            if (e[j].y == 0.f) continue;
+            const float f = part_weight(e[j], M);
+            add4(acc, f, v[j]);
+            sum = fmaf(f, e[j].y, sum);
+        }
+    }
+    // the lanes' and the warps' own references meet
+    if constexpr (LPR == 16) {
+        const float now = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
+        const float f = part_weight(make_float2(M, sum), now);
+        acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+        sum *= f;
+        M = now;
     }
     if constexpr (LPR == 16) {
         acc.x += __shfl_xor_sync(0xffffffffu, acc.x, 16), acc.y += __shfl_xor_sync(0xffffffffu, acc.y, 16);
@@ -921,13 +960,19 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const Cached
     }
     if constexpr (WPR > 1) {
         s_acc[warp][lane] = acc;
-        if (lane == 0) s_sum[warp] = sum;
+        if (lane == 0) s_ml[warp] = make_float2(M, sum);
         __syncthreads();
         if (part) return;
 #pragma unroll
-        for (int i = 1; i < WPR; ++i) {
-            add4(acc, 1.f, s_acc[warp + i][lane]);
-            sum += s_sum[warp + i];
+        for (int i = 0; i < WPR; ++i) M = fmaxf(M, s_ml[warp + i].x);
+        acc = make_float4(0.f, 0.f, 0.f, 0.f), sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < WPR; ++i) {
+            const float2 e = s_ml[warp + i];
+            if (e.y == 0.f) continue;
+            const float f = part_weight(e, M);
+            add4(acc, f, s_acc[warp + i][lane]);
+            sum = fmaf(f, e.y, sum);
         }
     }
     if (r_all < n_rows && tt < nn && lane < LPR)
@@ -963,7 +1008,7 @@ template <typename F> cudaError_t make_ready(Ready *r, F fn, int smem) {
 }
 
 template <typename F, typename... A>
-cudaError_t launch_ex(F fn, unsigned grid, int threads, int smem, unsigned cluster, bool pdl, cudaStream_t s, A... args) {
+cudaError_t launch_ex(F fn, unsigned grid, int threads, int smem, unsigned cluster, cudaStream_t s, A... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3((unsigned)threads);
@@ -977,11 +1022,11 @@ cudaError_t launch_ex(F fn, unsigned grid, int threads, int smem, unsigned clust
         at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
         ++n;
     }
-    if (pdl) {
-        at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at[n].val.programmaticStreamSerializationAllowed = 1;
-        ++n;
-    }
+    // every kernel here waits for its predecessor (griddepcontrol.wait) before it reads or writes memory,
+    // so its CTAs may be placed while that one ends
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
     cfg.attrs = at;
     cfg.numAttrs = (unsigned)n;
     return cudaLaunchKernelEx(&cfg, fn, args...);
@@ -998,16 +1043,16 @@ cudaError_t launch(int kind, const CachedArgs &a, unsigned *ctas, int nsplit, in
         auto fn = attn_share_kernel<Q8, F32, D, NT>;
         if ((e = make_ready(&ready[kind][dev], fn, K::kSmem)) != cudaSuccess) return e;
         *ctas = (unsigned)(ready[kind][dev].per_sm * sms_of(dev));
-        return plan ? cudaSuccess : launch_ex(fn, *ctas, kAcThreads, K::kSmem, 1, false, s, a);
+        return plan ? cudaSuccess : launch_ex(fn, *ctas, kAcThreads, K::kSmem, 1, s, a);
     }
     if (kind == kPassPrefix) {
         auto fn = attn_cached_kernel<Q8, F32, D, NT, true>;
         if ((e = make_ready(&ready[kind][dev], fn, K::kSmem)) != cudaSuccess) return e;
-        return launch_ex(fn, *ctas, kAcThreads, K::kSmem, 1, false, s, a, nsplit);
+        return launch_ex(fn, *ctas, kAcThreads, K::kSmem, 1, s, a, nsplit);
     }
     auto fn = attn_cached_kernel<Q8, F32, D, NT, false>;
     if ((e = make_ready(&ready[kind][dev], fn, K::kSmem)) != cudaSuccess) return e;
-    return launch_ex(fn, *ctas, kAcThreads, K::kSmem, (unsigned)nsplit, false, s, a, nsplit);
+    return launch_ex(fn, *ctas, kAcThreads, K::kSmem, (unsigned)nsplit, s, a, nsplit);
 }
 
 constexpr int tile_positions(bool q8, int d) { return q8 || d == 64 ? 32 : 16; }   // AcCfg::TP
@@ -1029,7 +1074,7 @@ cudaError_t launch_join(bool f32, int d, const CachedArgs &a, int rw, int tp, un
     const int wpr = many ? kJoinWarps : 1, per = kJoinWarps / wpr;
     const unsigned grid = (unsigned)((rows + per - 1) / per);
 #define QD_JOIN(F, DD, W) \
-    if (f32 == F && d == DD && wpr == W) return launch_ex(attn_join_kernel<F, DD, W>, grid, kJoinWarps * 32, 0, 1, true, s, a, rw, tp, warps);
+    if (f32 == F && d == DD && wpr == W) return launch_ex(attn_join_kernel<F, DD, W>, grid, kJoinWarps * 32, 0, 1, s, a, rw, tp, warps);
     QD_JOIN(false, 64, 1) QD_JOIN(false, 128, 1) QD_JOIN(true, 64, 1) QD_JOIN(true, 128, 1)
     QD_JOIN(false, 64, kJoinWarps) QD_JOIN(false, 128, kJoinWarps) QD_JOIN(true, 64, kJoinWarps) QD_JOIN(true, 128, kJoinWarps)
 #undef QD_JOIN

@@ -38,111 +38,146 @@ __device__ __forceinline__ uint32_t pack2_bf16(float a, float b) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// grid (row blocks, streams, K and V); LPR lanes a row
-template <typename T, int D, bool Q8>
+// A CTA takes U sets of its threads' rows at a time, their loads first.  LPR lanes a row.
+template <typename T, int D, int U> struct RowSet {
+    static constexpr int E = Vec16<T>::E, LPR = D / E, RPB = kRowThreads / LPR;
+    int t[U], h[U], pos[U];
+    bool live[U];
+    __device__ __forceinline__ void at(const RowsArgs &a, const NewRows &nr, int first) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = first + u * RPB + (int)threadIdx.x / LPR;
+            t[u] = (int)((unsigned)r / (unsigned)a.kvh), h[u] = r - t[u] * a.kvh;
+            pos[u] = nr.first + t[u];
+            live[u] = t[u] < nr.n && pos[u] >= 0 && pos[u] < a.smax;
+        }
+    }
+};
+
+// grid (row blocks, streams, K and V)
+template <typename T, int D, bool Q8, int U>
 __global__ void __launch_bounds__(kRowThreads) kv_append_kernel(const RowsArgs a) {
-    constexpr int E = Vec16<T>::E, LPR = D / E, RPB = kRowThreads / LPR;
-    const int b = blockIdx.y, which = blockIdx.z;
+    using S = RowSet<T, D, U>;
+    constexpr int E = S::E, LPR = S::LPR;
+    const int b = blockIdx.y, which = blockIdx.z, lane = threadIdx.x % LPR;
     const NewRows nr = new_rows(a.lengths, a.n_new, b, a.n_tokens);
-    const int lane = threadIdx.x % LPR;
-    const long long n = (long long)nr.n * a.kvh;
-    for (long long r = (long long)blockIdx.x * RPB + threadIdx.x / LPR; r - threadIdx.x / LPR < n; r += (long long)gridDim.x * RPB) {
-        const int t = (int)(r / a.kvh), h = (int)(r - (long long)t * a.kvh);
-        const int pos = nr.first + t;
-        const bool live = r < n && pos >= 0 && pos < a.smax;
-        float x[E];
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (live)
-            u = *reinterpret_cast<const uint4 *>(a.rows[which] + b * a.stream + t * a.token + h * a.head + lane * 16);
-        Vec16<T>::unpack(u, x);
-        uint8_t *dst = const_cast<uint8_t *>(which ? a.c.v : a.c.k) + b * a.c.stream + h * a.c.head + (int64_t)pos * a.c.row;
-        if constexpr (Q8) {
-            uint32_t m = 0;
+    const uint8_t *rows = a.rows[which] + b * a.stream + lane * 16;
+    uint8_t *cache = const_cast<uint8_t *>(which ? a.c.v : a.c.k) + b * a.c.stream + lane * (Q8 ? E : 2 * E);
+    float *scales = Q8 ? const_cast<float *>(which ? a.c.vs : a.c.ks) + b * a.c.sstream : nullptr;
+    S s;
+    for (int r0 = blockIdx.x * (U * S::RPB); r0 < nr.n * a.kvh; r0 += gridDim.x * (U * S::RPB)) {
+        s.at(a, nr, r0);
+        uint4 in[U];
 #pragma unroll
-            for (int e = 0; e < E; ++e) m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
+        for (int u = 0; u < U; ++u) {
+            in[u] = make_uint4(0, 0, 0, 0);
+            if (s.live[u]) in[u] = __ldcs(reinterpret_cast<const uint4 *>(rows + s.t[u] * a.token + s.h[u] * a.head));
+        }
 #pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const bool finite = m < 0x7f800000u, zero = m < 0x05800000u;   // below 2^-116
-            const float top = __uint_as_float(m);
-            const float by = (zero || !finite) ? 0.f : __fdiv_rn(127.f, top);
-            const float scale = !finite ? __uint_as_float(0x7fc00000u) : zero ? 0.f : __fdiv_rn(top, 127.f);
-            uint32_t w[E / 4];
+        for (int u = 0; u < U; ++u) {
+            float x[E];
+            Vec16<T>::unpack(in[u], x);
+            uint8_t *dst = cache + s.h[u] * a.c.head + s.pos[u] * a.c.row;
+            if constexpr (Q8) {
+                uint32_t m = 0;
 #pragma unroll
-            for (int e = 0; e < E; e += 4) {
-                uint32_t p = 0;
+                for (int e = 0; e < E; ++e) m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int c = by != 0.f ? __float2int_rn(__fmul_rn(x[e + i], by)) : 0;
-                    p |= (uint32_t)(c & 0xff) << (8 * i);
+                for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+                const bool finite = m < 0x7f800000u, zero = m < 0x05800000u;   // below 2^-116
+                const float top = __uint_as_float(m);
+                const float by = (zero || !finite) ? 0.f : __fdiv_rn(127.f, top);
+                const float scale = !finite ? __uint_as_float(0x7fc00000u) : zero ? 0.f : __fdiv_rn(top, 127.f);
+                uint32_t w[E / 4];
+#pragma unroll
+                for (int e = 0; e < E; e += 4) {
+                    uint32_t p = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int c = by != 0.f ? __float2int_rn(__fmul_rn(x[e + i], by)) : 0;
+                        p |= (uint32_t)(c & 0xff) << (8 * i);
+                    }
+                    w[e / 4] = p;
                 }
-                w[e / 4] = p;
-            }
-            if (live) {
+                if (s.live[u]) {
+                    if constexpr (E == 8)
+                        *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+                    else
+                        *reinterpret_cast<uint32_t *>(dst) = w[0];
+                    if (lane == 0) scales[s.h[u] * a.c.shead + s.pos[u]] = scale;
+                }
+            } else if (s.live[u]) {
                 if constexpr (E == 8)
-                    *reinterpret_cast<uint2 *>(dst + lane * 8) = make_uint2(w[0], w[1]);
+                    *reinterpret_cast<uint4 *>(dst) = in[u];
                 else
-                    *reinterpret_cast<uint32_t *>(dst + lane * 4) = w[0];
-                if (lane == 0)
-                    const_cast<float *>(which ? a.c.vs : a.c.ks)[b * a.c.sstream + h * a.c.shead + pos] = scale;
+                    *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2_bf16(x[0], x[1]), pack2_bf16(x[2], x[3]));
             }
-        } else if (live) {
-            if constexpr (E == 8)
-                *reinterpret_cast<uint4 *>(dst + lane * 16) = u;
-            else
-                *reinterpret_cast<uint2 *>(dst + lane * 8) = make_uint2(pack2_bf16(x[0], x[1]), pack2_bf16(x[2], x[3]));
         }
     }
 }
 
-template <typename T, int D, bool Q8>
+template <typename T, int D, bool Q8, int U>
 __global__ void __launch_bounds__(kRowThreads) kv_read_kernel(const RowsArgs a) {
-    constexpr int E = Vec16<T>::E, LPR = D / E, RPB = kRowThreads / LPR;
-    const int b = blockIdx.y, which = blockIdx.z;
+    using S = RowSet<T, D, U>;
+    constexpr int E = S::E, LPR = S::LPR, W = Q8 ? E / 4 : E / 2;   // words a lane reads
+    const int b = blockIdx.y, which = blockIdx.z, lane = threadIdx.x % LPR;
     const NewRows nr = new_rows(a.lengths, a.n_new, b, a.n_tokens);
-    const int lane = threadIdx.x % LPR;
-    const long long n = (long long)nr.n * a.kvh;
-    for (long long r = (long long)blockIdx.x * RPB + threadIdx.x / LPR; r < n; r += (long long)gridDim.x * RPB) {
-        const int t = (int)(r / a.kvh), h = (int)(r - (long long)t * a.kvh);
-        const int pos = nr.first + t;
-        if (pos < 0 || pos >= a.smax) continue;
-        const uint8_t *src = (which ? a.c.v : a.c.k) + b * a.c.stream + h * a.c.head + (int64_t)pos * a.c.row;
-        float x[E];
-        if constexpr (Q8) {
-            const float s = (which ? a.c.vs : a.c.ks)[b * a.c.sstream + h * a.c.shead + pos];
-            uint32_t w[E / 4];
-            if constexpr (E == 8) {
-                const uint2 u = *reinterpret_cast<const uint2 *>(src + lane * 8);
-                w[0] = u.x, w[1] = u.y;
-            } else {
-                w[0] = *reinterpret_cast<const uint32_t *>(src + lane * 4);
-            }
+    uint8_t *rows = const_cast<uint8_t *>(a.rows[which]) + b * a.stream + lane * 16;
+    const uint8_t *cache = (which ? a.c.v : a.c.k) + b * a.c.stream + lane * (W * 4);
+    const float *scales = Q8 ? (which ? a.c.vs : a.c.ks) + b * a.c.sstream : nullptr;
+    S s;
+    for (int r0 = blockIdx.x * (U * S::RPB); r0 < nr.n * a.kvh; r0 += gridDim.x * (U * S::RPB)) {
+        s.at(a, nr, r0);
+        uint32_t w[U][W];
+        float scale[U];
 #pragma unroll
-            for (int e = 0; e < E; ++e) x[e] = __fmul_rn((float)(int8_t)(w[e / 4] >> (8 * (e & 3))), s);
-        } else if constexpr (E == 8) {
-            Vec16<T>::unpack(*reinterpret_cast<const uint4 *>(src + lane * 16), x);
-        } else {
-            const uint2 u = *reinterpret_cast<const uint2 *>(src + lane * 8);
-            x[0] = bf16lo(u.x), x[1] = bf16hi(u.x), x[2] = bf16lo(u.y), x[3] = bf16hi(u.y);
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int i = 0; i < W; ++i) w[u][i] = 0;
+            scale[u] = 0.f;
+            if (!s.live[u]) continue;
+            const uint8_t *src = cache + s.h[u] * a.c.head + s.pos[u] * a.c.row;
+            if constexpr (W == 4) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(src);
+                w[u][0] = v.x, w[u][1] = v.y, w[u][2] = v.z, w[u][3] = v.w;
+            } else if constexpr (W == 2) {
+                const uint2 v = *reinterpret_cast<const uint2 *>(src);
+                w[u][0] = v.x, w[u][1] = v.y;
+            } else {
+                w[u][0] = *reinterpret_cast<const uint32_t *>(src);
+            }
+            if constexpr (Q8) scale[u] = scales[s.h[u] * a.c.shead + s.pos[u]];
         }
-        uint4 *dst = reinterpret_cast<uint4 *>(const_cast<uint8_t *>(a.rows[which]) + b * a.stream + t * a.token +
-                                               h * a.head + lane * 16);
-        if constexpr (E == 8)
-            *dst = make_uint4(pack2_bf16(x[0], x[1]), pack2_bf16(x[2], x[3]), pack2_bf16(x[4], x[5]),
-                              pack2_bf16(x[6], x[7]));
-        else
-            *dst = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
-                              __float_as_uint(x[3]));
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (!s.live[u]) continue;
+            float x[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                x[e] = Q8 ? __fmul_rn((float)(int8_t)(w[u][e / 4] >> (8 * (e & 3))), scale[u])
+                          : (e & 1 ? bf16hi(w[u][(e / 2) % W]) : bf16lo(w[u][(e / 2) % W]));
+            uint4 o;
+            if constexpr (E == 8)
+                o = make_uint4(pack2_bf16(x[0], x[1]), pack2_bf16(x[2], x[3]), pack2_bf16(x[4], x[5]),
+                               pack2_bf16(x[6], x[7]));
+            else
+                o = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                               __float_as_uint(x[3]));
+            __stcs(reinterpret_cast<uint4 *>(rows + s.t[u] * a.token + s.h[u] * a.head), o);
+        }
     }
 }
+
+constexpr int kRowSets = 4;   // rows in flight a thread, where there are that many
 
 typedef void (*RowsFn)(const RowsArgs);
-template <typename T> RowsFn rows_fn(bool read, int d, bool q8) {
+template <typename T, int U> RowsFn rows_fn(bool read, int d, bool q8) {
     if (d == 64) {
-        if (read) return q8 ? kv_read_kernel<T, 64, true> : kv_read_kernel<T, 64, false>;
-        return q8 ? kv_append_kernel<T, 64, true> : kv_append_kernel<T, 64, false>;
+        if (read) return q8 ? kv_read_kernel<T, 64, true, U> : kv_read_kernel<T, 64, false, U>;
+        return q8 ? kv_append_kernel<T, 64, true, U> : kv_append_kernel<T, 64, false, U>;
     }
-    if (read) return q8 ? kv_read_kernel<T, 128, true> : kv_read_kernel<T, 128, false>;
-    return q8 ? kv_append_kernel<T, 128, true> : kv_append_kernel<T, 128, false>;
+    if (read) return q8 ? kv_read_kernel<T, 128, true, U> : kv_read_kernel<T, 128, false, U>;
+    return q8 ? kv_append_kernel<T, 128, true, U> : kv_append_kernel<T, 128, false, U>;
 }
 
 qd_status move_rows(bool read, const qd_kv_cache *cache, const void *k_rows, const void *v_rows, int dtype,
@@ -173,10 +208,15 @@ qd_status move_rows(bool read, const qd_kv_cache *cache, const void *k_rows, con
     a.n_tokens = n_tokens, a.kvh = cache->n_kv_heads, a.smax = cache->smax;
     const int rpb = kRowThreads / (cache->head_dim / (int)unit);
     const long long rows = (long long)n_tokens * cache->n_kv_heads;
+    if (rows > INT32_MAX / 2) return QD_EUNSUPPORTED;
+    const bool many = rows > rpb, q8 = cache->format == QD_KV_Q8;
+    const long long per = (long long)rpb * (many ? kRowSets : 1);
     const long long most = std::max(1, sms_of(dev) * 16 / cache->n_streams);
-    const dim3 grid((unsigned)std::min((rows + rpb - 1) / rpb, most), (unsigned)cache->n_streams, 2);
-    const RowsFn fn = dtype == QD_F32 ? rows_fn<float>(read, cache->head_dim, cache->format == QD_KV_Q8)
-                                      : rows_fn<__nv_bfloat16>(read, cache->head_dim, cache->format == QD_KV_Q8);
+    const dim3 grid((unsigned)std::min((rows + per - 1) / per, most), (unsigned)cache->n_streams, 2);
+    const int d = cache->head_dim;
+    const RowsFn fn = dtype == QD_F32 ? (many ? rows_fn<float, kRowSets>(read, d, q8) : rows_fn<float, 1>(read, d, q8))
+                                      : (many ? rows_fn<__nv_bfloat16, kRowSets>(read, d, q8)
+                                              : rows_fn<__nv_bfloat16, 1>(read, d, q8));
     fn<<<grid, kRowThreads, 0, static_cast<cudaStream_t>(cuda_stream)>>>(a);
     return cudaGetLastError() == cudaSuccess ? QD_OK : QD_ECUDA;
 }

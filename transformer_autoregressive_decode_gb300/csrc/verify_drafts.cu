@@ -3,9 +3,9 @@
 // pass the next token is drawn from p of the position behind them.
 //
 // Only one row of p and one of q are needed in full: those of the position that is drawn
-// from, which T pairs of scalars decide.  A cluster of CTAs per stream shares that row:
-// every CTA finds the position by itself, adds up its slice (one sum per warp), reads all
-// the cluster's warp sums through distributed shared memory, and the one warp whose slice holds
+// from, which T pairs of scalars decide.  A CTA, or a cluster of them, per stream shares that row:
+// every CTA finds the position by itself, adds up its slices (one per warp), reads all
+// the cluster's slice sums through distributed shared memory, and the one warp whose slice holds
 // the mark walks it.  One launch, no scratch memory; 8 bytes per vocabulary entry are read
 // once, which bounds large vocabularies by HBM and small ones by the launch and the
 // three dependent loads before the sum.
@@ -20,16 +20,20 @@ namespace qd {
 
 namespace {
 
-constexpr int kVfThreads = 512, kVfWarps = kVfThreads / 32;
-constexpr int kVfCluster = 8;
+constexpr int kVfThreads = 256, kVfWarps = kVfThreads / 32;
+constexpr int kVfMaxCluster = 8;
+constexpr int kVfStep = 128, kVfAhead = 4;    // entries of a warp's step (a float4 a lane); steps whose loads go out together
+constexpr int kVfRound = kVfStep * kVfAhead;
 constexpr int kVfMaxTokens = 64, kVfMaxVocab = 524288;
+constexpr int kVfRounds = kVfMaxVocab / (kVfMaxCluster * kVfWarps * kVfRound);   // of a slice, at most
+static_assert(kVfRounds <= 32, "a lane per round");
 
 struct VerifyArgs {
     const float *p, *q;
     int64_t p_stream, p_row, q_stream, q_row;   // elements
     const int32_t *ids, *n_draft;
     const float *u;
-    int T, V;
+    int T, V, per;                              // per: entries of a warp's slice
     int32_t *out, *accepted;
 };
 
@@ -44,149 +48,215 @@ __device__ __forceinline__ unsigned long long warp_sum_u64(unsigned long long v)
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
+__device__ __forceinline__ unsigned long long warp_scan_u64(unsigned long long v, int lane) {   // inclusive
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long x = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += x;
+    }
+    return v;
+}
 
-// The weights of entries [i, i + 4) of the row drawn from: p, p - q, or p without the drafted id.
+// The row drawn from: p, p - q, or p without the drafted id.
 struct Row {
     const float *p, *q;
-    int hole, V;
+    int hole;
     bool vec;
-    __device__ __forceinline__ float left(float a, float b) const { return q ? __fsub_rn(a, b) : a; }
-    __device__ __forceinline__ void load4(int i, unsigned long long *w) const {
-        float a[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
-        if (vec && i + 4 <= V) {
-            const float4 x = __ldg(reinterpret_cast<const float4 *>(p + i));
-            a[0] = x.x, a[1] = x.y, a[2] = x.z, a[3] = x.w;
-            if (q) {
-                const float4 y = __ldg(reinterpret_cast<const float4 *>(q + i));
-                b[0] = y.x, b[1] = y.y, b[2] = y.z, b[3] = y.w;
-            }
-        } else {
+    __device__ __forceinline__ void set(const float *p_, const float *q_, int hole_) {
+        p = p_, q = q_, hole = hole_;
+        vec = ((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q)) & 15) == 0;
+    }
+    // entries [i, i + 4) below `end` of one of the two
+    __device__ __forceinline__ float4 load4(const float *x, int i, int end) const {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (vec && i + 4 <= end) return __ldg(reinterpret_cast<const float4 *>(x + i));
+        if (i < end) v.x = __ldg(x + i);
+        if (i + 1 < end) v.y = __ldg(x + i + 1);
+        if (i + 2 < end) v.z = __ldg(x + i + 2);
+        if (i + 3 < end) v.w = __ldg(x + i + 3);
+        return v;
+    }
+    // what is left of entries [i, i + 4) of kVfAhead steps, all loads first
+    __device__ __forceinline__ void round(int i, int end, float (&v)[kVfAhead][4]) const {
+        float4 x[kVfAhead], y[kVfAhead];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (i + e < V) {
-                    a[e] = __ldg(p + i + e);
-                    if (q) b[e] = __ldg(q + i + e);
-                }
+        for (int k = 0; k < kVfAhead; ++k) x[k] = load4(p, i + k * kVfStep, end);
+        if (q) {
+#pragma unroll
+            for (int k = 0; k < kVfAhead; ++k) y[k] = load4(q, i + k * kVfStep, end);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = i + e == hole ? 0ull : weight(left(a[e], b[e]));
+        for (int k = 0; k < kVfAhead; ++k) {
+            v[k][0] = x[k].x, v[k][1] = x[k].y, v[k][2] = x[k].z, v[k][3] = x[k].w;
+            if (q) {
+                v[k][0] = __fsub_rn(v[k][0], y[k].x), v[k][1] = __fsub_rn(v[k][1], y[k].y);
+                v[k][2] = __fsub_rn(v[k][2], y[k].z), v[k][3] = __fsub_rn(v[k][3], y[k].w);
+            }
+            const int at = hole - i - k * kVfStep;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (at == e) v[k][e] = 0.f;
+        }
     }
 };
 
-__global__ void __cluster_dims__(kVfCluster, 1, 1) __launch_bounds__(kVfThreads) verify_kernel(const VerifyArgs a) {
-    __shared__ unsigned long long sums[kVfWarps];
-    __shared__ unsigned long long all[kVfCluster * kVfWarps];
+// One stream per cluster of CL CTAs.
+template <int CL> __global__ void __launch_bounds__(kVfThreads, 4) verify_kernel(const VerifyArgs a) {
+    constexpr int kParts = CL * kVfWarps, kPer = (kParts + 31) / 32;   // slices; of them, a lane's
+    __shared__ unsigned long long sums[kVfWarps], rounds[kVfWarps][kVfRounds];
+    __shared__ unsigned long long all[kPer * 32];
     __shared__ int s_pass;
-    const int b = blockIdx.x / kVfCluster, rank = (int)cluster_ctarank();
+    const int b = blockIdx.x / CL, rank = blockIdx.x % CL;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int n = a.n_draft ? a.n_draft[b] : a.T;
+    const int32_t *ids = a.ids + (int64_t)b * a.T;
+    const float *u = a.u + (int64_t)b * (a.T + 1);
+    int32_t *out = a.out + (int64_t)b * (a.T + 1);
+    int n = a.n_draft ? __ldg(a.n_draft + b) : a.T;
     n = n < 0 ? 0 : n > a.T ? a.T : n;
 
-    // the drafts that pass: each lane of warp 0 decides two of them
+    // the drafts that pass: a lane of warp 0 decides one (of up to 64)
     if (warp == 0) {
         int first = n;
-        for (int t0 = 0; t0 < n; t0 += 32) {
+        for (int t0 = 0; t0 < a.T; t0 += 32) {
             const int t = t0 + lane;
             bool ok = true;
-            if (t < n) {
-                const int x = a.ids[(int64_t)b * a.T + t];
+            if (t < a.T) {
+                const int x = __ldg(ids + t);
                 ok = x >= 0 && x < a.V;
                 if (ok) {
                     const float px = a.p[b * a.p_stream + t * a.p_row + x];
                     const float qx = a.q ? a.q[b * a.q_stream + t * a.q_row + x] : 1.f;
                     // 24-bit factors: the product is exact in fp64
-                    ok = (double)a.u[(int64_t)b * (a.T + 1) + t] * (double)qx < (double)px;
+                    ok = (double)u[t] * (double)qx < (double)px;
                 }
             }
             const uint32_t bad = ~__ballot_sync(0xffffffffu, ok);
             if (bad) {
-                first = t0 + __ffs(bad) - 1;
+                first = min(n, t0 + __ffs(bad) - 1);
                 break;
             }
         }
         if (lane == 0) s_pass = first;
     }
+    if (threadIdx.x < kPer * 32) all[threadIdx.x] = 0;
     __syncthreads();
     const int pass = s_pass;
     if (rank == 0) {
         for (int s = threadIdx.x; s <= a.T; s += kVfThreads)
-            if (s != pass) a.out[(int64_t)b * (a.T + 1) + s] = s < pass ? a.ids[(int64_t)b * a.T + s] : -1;
+            if (s != pass) out[s] = s < pass ? ids[s] : -1;
         if (threadIdx.x == 0) a.accepted[b] = pass;
     }
 
     Row row;
-    row.p = a.p + b * a.p_stream + pass * a.p_row;
-    row.q = (pass < n && a.q) ? a.q + b * a.q_stream + pass * a.q_row : nullptr;
-    row.hole = (pass < n && !a.q) ? a.ids[(int64_t)b * a.T + pass] : -1;
-    row.V = a.V;
-    row.vec = ((reinterpret_cast<uintptr_t>(row.p) | reinterpret_cast<uintptr_t>(row.q)) & 15) == 0;
-
-    // slices in multiples of 128 entries (one float4 a lane), one per warp of the cluster
-    const int parts = kVfCluster * kVfWarps;
-    const int per = ((a.V + parts - 1) / parts + 127) / 128 * 128;
+    row.set(a.p + b * a.p_stream + pass * a.p_row, pass < n && a.q ? a.q + b * a.q_stream + pass * a.q_row : nullptr,
+            pass < n && !a.q ? __ldg(ids + pass) : -1);
     const int me = rank * kVfWarps + warp;
-    const int i0 = min(me * per, a.V), i1 = min(i0 + per, a.V);
-    unsigned long long total = 0;
-    for (int round = 0; round < 2; ++round) {
+    const int i0 = min(me * a.per, a.V), i1 = min(i0 + a.per, a.V);
+    unsigned long long mine[kPer], upto = 0, total = 0;
+    for (int turn = 0; turn < 2; ++turn) {
         unsigned long long s = 0;
-        for (int i = i0 + lane * 4; i < i1; i += 128) {
-            unsigned long long w[4];
-            row.load4(i, w);
-            s += (w[0] + w[1]) + (w[2] + w[3]);
+        for (int i = i0; i < i1; i += kVfRound) {
+            float v[kVfAhead][4];
+            row.round(i + lane * 4, i1, v);
+            unsigned long long r = 0;
+#pragma unroll
+            for (int k = 0; k < kVfAhead; ++k)
+                r += (weight(v[k][0]) + weight(v[k][1])) + (weight(v[k][2]) + weight(v[k][3]));
+            r = warp_sum_u64(r);
+            if (lane == 0) rounds[warp][(i - i0) / kVfRound] = r;
+            s += r;
         }
-        s = warp_sum_u64(s);
-        if (lane == 0) sums[warp] = s;
-        cluster_sync();
-        if (threadIdx.x < parts) {
-            const uint32_t at = cluster_map(&sums[threadIdx.x % kVfWarps], threadIdx.x / kVfWarps);
-            unsigned long long v;
-            asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(at) : "memory");
-            all[threadIdx.x] = v;
+        __syncwarp();
+        if constexpr (CL == 1) {
+            if (lane == 0) all[warp] = s;
+            __syncthreads();
+        } else {
+            if (lane == 0) sums[warp] = s;
+            cluster_sync();
+            if (threadIdx.x < kParts) {
+                const uint32_t at = cluster_map(&sums[threadIdx.x % kVfWarps], threadIdx.x / kVfWarps);
+                unsigned long long v;
+                asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(at) : "memory");
+                all[threadIdx.x] = v;
+            }
+            cluster_sync();      // every CTA has read the sums: they may be written again, and CTAs may leave
         }
-        cluster_sync();      // every CTA has read the sums: they may be written again, and CTAs may leave
-        total = 0;
-        for (int i = 0; i < parts; ++i) total += all[i];
+        // every warp scans the slices by itself
+        unsigned long long lane_sum = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) lane_sum += mine[i] = all[lane * kPer + i];
+        upto = warp_scan_u64(lane_sum, lane);
+        total = __shfl_sync(0xffffffffu, upto, 31);
+        upto -= lane_sum;
         if (total != 0 || (!row.q && row.hole < 0)) break;
-        row.q = nullptr;     // nothing left of p - q: the draw is from p
-        row.hole = -1;
-        row.vec = (reinterpret_cast<uintptr_t>(row.p) & 15) == 0;
+        row.set(row.p, nullptr, -1);   // nothing left of p - q: the draw is from p
+        if constexpr (CL == 1) __syncthreads();
     }
 
     if (total == 0) {
-        if (rank == 0 && threadIdx.x == 0) a.out[(int64_t)b * (a.T + 1) + pass] = -1;
+        if (rank == 0 && threadIdx.x == 0) out[pass] = -1;
         return;
     }
-    const double u = (double)a.u[(int64_t)b * (a.T + 1) + a.T];
-    unsigned long long mark = (unsigned long long)floor(u * __ull2double_rn(total));
+    unsigned long long mark = (unsigned long long)floor((double)u[a.T] * __ull2double_rn(total));
     if (mark >= total) mark = total - 1;   // u in [0, 1) gives less
-    unsigned long long before = 0;
-    for (int i = 0; i < me; ++i) before += all[i];
-    if (mark < before || mark - before >= all[me]) return;
-
-    // this warp's slice holds the mark: 128 entries a step, then the lane, then the entry
-    for (int i = i0; i < i1; i += 128) {
-        unsigned long long w[4];
-        row.load4(i + lane * 4, w);
-        if (i + lane * 4 >= i1) w[0] = w[1] = w[2] = w[3] = 0;
-        const unsigned long long own = (w[0] + w[1]) + (w[2] + w[3]);
-        unsigned long long upto = own;
+    // the slice that holds the mark, and the sum before it
+    int slice = 0;
+    unsigned long long before = upto;
+    bool here = false;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const unsigned long long v = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += v;
+    for (int i = 0; i < kPer; ++i)
+        if (!here) {
+            if (mark >= before && mark - before < mine[i])
+                here = true, slice = lane * kPer + i;
+            else
+                before += mine[i];
         }
-        const uint32_t over = __ballot_sync(0xffffffffu, before + upto > mark);
+    const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+    if (__shfl_sync(0xffffffffu, slice, src) != me) return;
+    before = __shfl_sync(0xffffffffu, before, src);
+
+    // this warp finds the round of its slice, reads it again, and finds the step, the lane, the entry
+    const int n_rounds = (i1 - i0 + kVfRound - 1) / kVfRound;
+    const unsigned long long in_round = lane < n_rounds ? rounds[warp][lane] : 0;
+    const unsigned long long ends = warp_scan_u64(in_round, lane);
+    const int r = __ffs(__ballot_sync(0xffffffffu, lane < n_rounds && before + ends > mark)) - 1;
+    before += __shfl_sync(0xffffffffu, ends - in_round, r);
+    float v[kVfAhead][4];
+    row.round(i0 + r * kVfRound + lane * 4, i1, v);
+#pragma unroll
+    for (int k = 0; k < kVfAhead; ++k) {
+        unsigned long long w[4] = {weight(v[k][0]), weight(v[k][1]), weight(v[k][2]), weight(v[k][3])};
+        const unsigned long long own = (w[0] + w[1]) + (w[2] + w[3]), scan = warp_scan_u64(own, lane);
+        const uint32_t over = __ballot_sync(0xffffffffu, before + scan > mark);
         if (over) {
             if (lane == __ffs(over) - 1) {
-                unsigned long long c = before + upto - own;
+                unsigned long long c = before + scan - own;
                 int e = 0;
-                while (e < 3 && c + w[e] <= mark) c += w[e++];
-                a.out[(int64_t)b * (a.T + 1) + pass] = i + lane * 4 + e;
+#pragma unroll
+                for (int j = 0; j < 3; ++j)
+                    if (e == j && c + w[j] <= mark) c += w[j], ++e;
+                out[pass] = i0 + r * kVfRound + k * kVfStep + lane * 4 + e;
             }
             return;
         }
-        before += __shfl_sync(0xffffffffu, upto, 31);
+        before += __shfl_sync(0xffffffffu, scan, 31);
     }
+}
+
+template <int CL> cudaError_t launch_verify(VerifyArgs &a, int n_streams, cudaStream_t s) {
+    constexpr int parts = CL * kVfWarps;
+    a.per = ((a.V + parts - 1) / parts + kVfStep - 1) / kVfStep * kVfStep;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(n_streams * CL));
+    cfg.blockDim = dim3(kVfThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = CL;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = CL > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, verify_kernel<CL>, (const VerifyArgs)a);
 }
 
 }  // namespace
@@ -222,6 +292,12 @@ extern "C" qd_status qd_verify_drafts(const float *target_probs_dev, int64_t tar
     a.ids = draft_ids_dev, a.n_draft = n_draft_dev, a.u = u_dev;
     a.T = n_tokens, a.V = vocab;
     a.out = out_ids_dev, a.accepted = n_accepted_dev;
-    verify_kernel<<<n_streams * kVfCluster, kVfThreads, 0, static_cast<cudaStream_t>(cuda_stream)>>>(a);
-    return cudaGetLastError() == cudaSuccess ? QD_OK : QD_ECUDA;
+    // CTAs of a stream: a warp's slice at most a round, as far as a cluster goes
+    cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+    constexpr int kCta = kVfWarps * kVfRound;
+    const cudaError_t e = vocab <= kCta       ? launch_verify<1>(a, n_streams, s)
+                          : vocab <= 2 * kCta ? launch_verify<2>(a, n_streams, s)
+                          : vocab <= 4 * kCta ? launch_verify<4>(a, n_streams, s)
+                                              : launch_verify<kVfMaxCluster>(a, n_streams, s);
+    return e == cudaSuccess ? QD_OK : QD_ECUDA;
 }
