@@ -8,7 +8,9 @@
 // dependent loads for a decode step.  A row is spread over the lanes so that each
 // lane's 16-byte access is contiguous with its neighbours' (fp32: 4 elements, bf16: 8); the row
 // maximum is a butterfly over those lanes, taken on the bits of |x| (integers order like
-// the magnitudes, NaN above infinity, so one comparison finds a row that is not finite).
+// the magnitudes, NaN above infinity, so one comparison finds a row that is not finite).  The
+// issue rate comes next (20 instructions an element held the first form at half of HBM): the two IEEE quotients of a row are
+// taken by one lane each, and rounding to a whole number is an add of 1.5 * 2^23, whose low byte is the code.
 #include "kv_view.cuh"
 #include "qd_device.cuh"
 #include "qd_internal.h"
@@ -33,9 +35,27 @@ template <typename T> struct Vec16 {
     static __device__ void unpack(uint4 u, float *f) { Elem<T>::unpack(u, f); }
 };
 
+// The largest magnitude of 16 bytes as fp32 bits (NaN above infinity above all finite ones).
+template <typename T> __device__ __forceinline__ uint32_t top_of(uint4 u) {
+    if constexpr (sizeof(T) == 2) {
+        // pairs of bf16: 16-bit maxima of the magnitudes
+        const uint32_t a = __vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu), b = __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu);
+        const uint32_t m = __vmaxu2(a, b);
+        return max(m & 0xffff0000u, m << 16);
+    } else {
+        return max(max(u.x & 0x7fffffffu, u.y & 0x7fffffffu), max(u.z & 0x7fffffffu, u.w & 0x7fffffffu));
+    }
+}
+
 __device__ __forceinline__ uint32_t pack2_bf16(float a, float b) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// Byte i of a word of codes as a float: offset by 128 under the exponent of 2^23, less 2^23 + 128 (a
+// permutation and an add at full rate, where a conversion has a quarter of it).
+__device__ __forceinline__ float code_of(uint32_t w, int i) {
+    return __fsub_rn(__uint_as_float(__byte_perm(w ^ 0x80808080u, 0x4b000000u, 0x7440 + i)), 8388736.f);
 }
 
 // A CTA takes U sets of its threads' rows at a time, their loads first.  LPR lanes a row.
@@ -73,38 +93,51 @@ __global__ void __launch_bounds__(kRowThreads) kv_append_kernel(const RowsArgs a
             in[u] = make_uint4(0, 0, 0, 0);
             if (s.live[u]) in[u] = __ldcs(reinterpret_cast<const uint4 *>(rows + s.t[u] * a.token + s.h[u] * a.head));
         }
+        // the rows' largest magnitudes; then each lane of a row's group takes one of the U rows' two quotients
+        float by[U], scale[U];
+        bool finite[U];
+        if constexpr (Q8) {
+            static_assert(2 * U <= LPR, "a lane per quotient");
+            uint32_t mine = 0;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                uint32_t m = top_of<T>(in[u]);
+#pragma unroll
+                for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+                finite[u] = m < 0x7f800000u;
+                if (lane / 2 == u) mine = m;
+            }
+            const bool zero = mine < 0x05800000u;   // below 2^-116
+            const float t = __uint_as_float(mine), one = zero || mine >= 0x7f800000u ? 1.f : t;
+            const float quot = zero ? 0.f : lane & 1 ? __fdiv_rn(one, 127.f) : __fdiv_rn(127.f, one);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                by[u] = __shfl_sync(0xffffffffu, quot, 2 * u, LPR);
+                scale[u] = __shfl_sync(0xffffffffu, quot, 2 * u + 1, LPR);
+                if (!finite[u]) scale[u] = __uint_as_float(0x7fc00000u);
+            }
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             float x[E];
             Vec16<T>::unpack(in[u], x);
             uint8_t *dst = cache + s.h[u] * a.c.head + s.pos[u] * a.c.row;
             if constexpr (Q8) {
-                uint32_t m = 0;
-#pragma unroll
-                for (int e = 0; e < E; ++e) m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
-#pragma unroll
-                for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-                const bool finite = m < 0x7f800000u, zero = m < 0x05800000u;   // below 2^-116
-                const float top = __uint_as_float(m);
-                const float by = (zero || !finite) ? 0.f : __fdiv_rn(127.f, top);
-                const float scale = !finite ? __uint_as_float(0x7fc00000u) : zero ? 0.f : __fdiv_rn(top, 127.f);
                 uint32_t w[E / 4];
 #pragma unroll
                 for (int e = 0; e < E; e += 4) {
-                    uint32_t p = 0;
+                    uint32_t c[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int c = by != 0.f ? __float2int_rn(__fmul_rn(x[e + i], by)) : 0;
-                        p |= (uint32_t)(c & 0xff) << (8 * i);
-                    }
-                    w[e / 4] = p;
+                    for (int i = 0; i < 4; ++i)
+                        c[i] = __float_as_uint(__fadd_rn(__fmul_rn(finite[u] ? x[e + i] : 0.f, by[u]), 12582912.f));
+                    w[e / 4] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
                 }
                 if (s.live[u]) {
                     if constexpr (E == 8)
                         *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
                     else
                         *reinterpret_cast<uint32_t *>(dst) = w[0];
-                    if (lane == 0) scales[s.h[u] * a.c.shead + s.pos[u]] = scale;
+                    if (lane == 0) scales[s.h[u] * a.c.shead + s.pos[u]] = scale[u];
                 }
             } else if (s.live[u]) {
                 if constexpr (E == 8)
@@ -154,7 +187,7 @@ __global__ void __launch_bounds__(kRowThreads) kv_read_kernel(const RowsArgs a) 
             float x[E];
 #pragma unroll
             for (int e = 0; e < E; ++e)
-                x[e] = Q8 ? __fmul_rn((float)(int8_t)(w[u][e / 4] >> (8 * (e & 3))), scale[u])
+                x[e] = Q8 ? __fmul_rn(code_of(w[u][(e / 4) % W], e & 3), scale[u])
                           : (e & 1 ? bf16hi(w[u][(e / 2) % W]) : bf16lo(w[u][(e / 2) % W]));
             uint4 o;
             if constexpr (E == 8)

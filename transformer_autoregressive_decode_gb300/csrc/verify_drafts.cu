@@ -27,6 +27,7 @@ constexpr int kVfRound = kVfStep * kVfAhead;
 constexpr int kVfMaxTokens = 64, kVfMaxVocab = 524288;
 constexpr int kVfRounds = kVfMaxVocab / (kVfMaxCluster * kVfWarps * kVfRound);   // of a slice, at most
 static_assert(kVfRounds <= 32, "a lane per round");
+static_assert(kVfRound <= 512, "a round's sums fit 32 bits");
 
 struct VerifyArgs {
     const float *p, *q;
@@ -37,17 +38,24 @@ struct VerifyArgs {
     int32_t *out, *accepted;
 };
 
-// floor(w 2^44); fmaxf takes a NaN to 0
-__device__ __forceinline__ unsigned long long weight(float w) {
-    w = fminf(fmaxf(w, 0.f), 1.f);
-    return __float2ull_rz(__fmul_rn(w, 17592186044416.f));
+// floor(w 2^44) of w in [0, 1] as hi 2^23 + lo, lo < 2^23, both as the low bits of a float at 2^23
+// (adding 2^23 towards zero leaves the whole part there; every other step is exact).  fp32
+// adds, where a conversion to 64 bits runs at a small fraction of their rate.  fmaxf takes a NaN to 0.
+constexpr float kVfWhole = 8388608.f;
+constexpr uint32_t kVfWholeBits = 0x4b000000u;
+struct Weight {
+    uint32_t hi, lo;                            // with kVfWholeBits
+    __device__ __forceinline__ unsigned long long value() const {
+        return ((unsigned long long)(hi - kVfWholeBits) << 23) + (lo - kVfWholeBits);
+    }
+};
+__device__ __forceinline__ Weight weight(float w) {
+    const float x = __fmul_rn(fminf(fmaxf(w, 0.f), 1.f), 2097152.f);   // 2^21
+    const float h = __fadd_rz(x, kVfWhole);
+    const float rest = __fsub_rn(x, __fsub_rn(h, kVfWhole));
+    return {__float_as_uint(h), __float_as_uint(__fadd_rz(__fmul_rn(rest, kVfWhole), kVfWhole))};
 }
 
-__device__ __forceinline__ unsigned long long warp_sum_u64(unsigned long long v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
 __device__ __forceinline__ unsigned long long warp_scan_u64(unsigned long long v, int lane) {   // inclusive
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -158,11 +166,18 @@ template <int CL> __global__ void __launch_bounds__(kVfThreads, 4) verify_kernel
         for (int i = i0; i < i1; i += kVfRound) {
             float v[kVfAhead][4];
             row.round(i + lane * 4, i1, v);
-            unsigned long long r = 0;
+            // 512 entries: the whole parts stay below 2^30, the rest below 2^32
+            uint32_t hi = 0, lo = 0;
 #pragma unroll
             for (int k = 0; k < kVfAhead; ++k)
-                r += (weight(v[k][0]) + weight(v[k][1])) + (weight(v[k][2]) + weight(v[k][3]));
-            r = warp_sum_u64(r);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const Weight w = weight(v[k][e]);
+                    hi += w.hi, lo += w.lo;
+                }
+            hi = __reduce_add_sync(0xffffffffu, hi - 4 * kVfAhead * kVfWholeBits);
+            lo = __reduce_add_sync(0xffffffffu, lo - 4 * kVfAhead * kVfWholeBits);
+            const unsigned long long r = ((unsigned long long)hi << 23) + lo;
             if (lane == 0) rounds[warp][(i - i0) / kVfRound] = r;
             s += r;
         }
@@ -225,7 +240,8 @@ template <int CL> __global__ void __launch_bounds__(kVfThreads, 4) verify_kernel
     row.round(i0 + r * kVfRound + lane * 4, i1, v);
 #pragma unroll
     for (int k = 0; k < kVfAhead; ++k) {
-        unsigned long long w[4] = {weight(v[k][0]), weight(v[k][1]), weight(v[k][2]), weight(v[k][3])};
+        unsigned long long w[4] = {weight(v[k][0]).value(), weight(v[k][1]).value(), weight(v[k][2]).value(),
+                                   weight(v[k][3]).value()};
         const unsigned long long own = (w[0] + w[1]) + (w[2] + w[3]), scan = warp_scan_u64(own, lane);
         const uint32_t over = __ballot_sync(0xffffffffu, before + scan > mark);
         if (over) {
