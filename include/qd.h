@@ -582,8 +582,7 @@ typedef struct {
  * (ties to even) to x * (127 / max|x|); a row below 2^-116 throughout is stored as zeros,
  * and one that holds an infinity or a NaN as codes 0 with a NaN scale, so that it reads
  * as NaN.  A row whose position falls outside [0, smax) is not written.  Errors:
- * QD_EINVAL (arguments, alignment, memory), QD_EUNSUPPORTED (head_dim, more than 2^30 rows
- * a stream), QD_ECUDA. */
+ * QD_EINVAL (arguments, alignment, memory), QD_EUNSUPPORTED (head_dim), QD_ECUDA. */
 qd_status qd_kv_append(const qd_kv_cache *cache, const void *k_rows_dev, const void *v_rows_dev, int dtype,
                        int n_tokens, int64_t stream_stride, int64_t token_stride, int64_t head_stride,
                        const int32_t *lengths_dev, const int32_t *n_new_dev, void *cuda_stream);

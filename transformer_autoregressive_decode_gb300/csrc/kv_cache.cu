@@ -27,6 +27,7 @@ struct RowsArgs {
     int64_t stream, token, head;       // bytes
     const int32_t *lengths, *n_new;
     int n_tokens, kvh, smax;
+    int hp, tp, sets;                  // heads and tokens of a CTA's threads; of those sets, a CTA's share at a time
 };
 
 // 16 bytes of T as floats
@@ -52,46 +53,50 @@ __device__ __forceinline__ uint32_t pack2_bf16(float a, float b) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// Byte i of a word of codes as a float: offset by 128 under the exponent of 2^23, less 2^23 + 128 (a
-// permutation and an add at full rate, where a conversion has a quarter of it).
-__device__ __forceinline__ float code_of(uint32_t w, int i) {
-    return __fsub_rn(__uint_as_float(__byte_perm(w ^ 0x80808080u, 0x4b000000u, 0x7440 + i)), 8388736.f);
-}
-
-// A CTA takes U sets of its threads' rows at a time, their loads first.  LPR lanes a row.
-template <typename T, int D, int U> struct RowSet {
-    static constexpr int E = Vec16<T>::E, LPR = D / E, RPB = kRowThreads / LPR;
-    int t[U], h[U], pos[U];
-    bool live[U];
-    __device__ __forceinline__ void at(const RowsArgs &a, const NewRows &nr, int first) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int r = first + u * RPB + (int)threadIdx.x / LPR;
-            t[u] = (int)((unsigned)r / (unsigned)a.kvh), h[u] = r - t[u] * a.kvh;
-            pos[u] = nr.first + t[u];
-            live[u] = t[u] < nr.n && pos[u] >= 0 && pos[u] < a.smax;
-        }
+// A CTA's threads stand for hp heads (of one of ceil(kvh / hp) groups) times tp tokens, so that a thread keeps
+// its head and walks the tokens with its addresses growing by constants; U tokens at a time, their loads first.
+// LPR lanes a row.
+template <typename T, int D> struct RowWalk {
+    static constexpr int E = Vec16<T>::E, LPR = D / E;
+    int h, t, tp, n, first;
+    bool idle;
+    __device__ __forceinline__ RowWalk(const RowsArgs &a) {
+        const NewRows nr = new_rows(a.lengths, a.n_new, (int)blockIdx.y, a.n_tokens);
+        n = nr.n, first = nr.first;
+        const int slot = threadIdx.x / LPR, in = slot / a.hp;
+        tp = a.tp;
+        h = (blockIdx.z >> 1) * a.hp + slot - in * a.hp;
+        idle = in >= tp || h >= a.kvh;
+        if (idle) h = 0;
+        t = blockIdx.x * tp * a.sets + in;
+    }
+    __device__ __forceinline__ bool live(const RowsArgs &a, int tt) const {
+        const int pos = first + tt;
+        return !idle && tt < n && pos >= 0 && pos < a.smax;
     }
 };
 
-// grid (row blocks, streams, K and V)
+// grid (token blocks, streams, head groups x (K, V))
 template <typename T, int D, bool Q8, int U>
 __global__ void __launch_bounds__(kRowThreads) kv_append_kernel(const RowsArgs a) {
-    using S = RowSet<T, D, U>;
+    using S = RowWalk<T, D>;
     constexpr int E = S::E, LPR = S::LPR;
-    const int b = blockIdx.y, which = blockIdx.z, lane = threadIdx.x % LPR;
-    const NewRows nr = new_rows(a.lengths, a.n_new, b, a.n_tokens);
-    const uint8_t *rows = a.rows[which] + b * a.stream + lane * 16;
-    uint8_t *cache = const_cast<uint8_t *>(which ? a.c.v : a.c.k) + b * a.c.stream + lane * (Q8 ? E : 2 * E);
-    float *scales = Q8 ? const_cast<float *>(which ? a.c.vs : a.c.ks) + b * a.c.sstream : nullptr;
-    S s;
-    for (int r0 = blockIdx.x * (U * S::RPB); r0 < nr.n * a.kvh; r0 += gridDim.x * (U * S::RPB)) {
-        s.at(a, nr, r0);
+    const int b = blockIdx.y, which = blockIdx.z & 1, lane = threadIdx.x % LPR;
+    S s(a);
+    const uint8_t *src = a.rows[which] + b * a.stream + s.h * a.head + s.t * a.token + lane * 16;
+    uint8_t *dst = const_cast<uint8_t *>(which ? a.c.v : a.c.k) + b * a.c.stream + s.h * a.c.head +
+                   (s.first + s.t) * a.c.row + lane * (Q8 ? E : 2 * E);
+    float *scales = nullptr;
+    if constexpr (Q8)
+        scales = const_cast<float *>(which ? a.c.vs : a.c.ks) + b * a.c.sstream + s.h * a.c.shead + s.first + s.t;
+    const int64_t hop_in = s.tp * a.token, hop_out = s.tp * a.c.row;
+    // the same number of turns for every thread of the CTA
+    for (int t0 = blockIdx.x * s.tp * U; t0 < s.n; t0 += gridDim.x * s.tp * U) {
         uint4 in[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             in[u] = make_uint4(0, 0, 0, 0);
-            if (s.live[u]) in[u] = __ldcs(reinterpret_cast<const uint4 *>(rows + s.t[u] * a.token + s.h[u] * a.head));
+            if (s.live(a, s.t + u * s.tp)) in[u] = __ldcs(reinterpret_cast<const uint4 *>(src + u * hop_in));
         }
         // the rows' largest magnitudes; then each lane of a row's group takes one of the U rows' two quotients
         float by[U], scale[U];
@@ -121,7 +126,8 @@ __global__ void __launch_bounds__(kRowThreads) kv_append_kernel(const RowsArgs a
         for (int u = 0; u < U; ++u) {
             float x[E];
             Vec16<T>::unpack(in[u], x);
-            uint8_t *dst = cache + s.h[u] * a.c.head + s.pos[u] * a.c.row;
+            const bool live = s.live(a, s.t + u * s.tp);
+            uint8_t *to = dst + u * hop_out;
             if constexpr (Q8) {
                 uint32_t w[E / 4];
 #pragma unroll
@@ -132,35 +138,38 @@ __global__ void __launch_bounds__(kRowThreads) kv_append_kernel(const RowsArgs a
                         c[i] = __float_as_uint(__fadd_rn(__fmul_rn(finite[u] ? x[e + i] : 0.f, by[u]), 12582912.f));
                     w[e / 4] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
                 }
-                if (s.live[u]) {
+                if (live) {
                     if constexpr (E == 8)
-                        *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+                        *reinterpret_cast<uint2 *>(to) = make_uint2(w[0], w[1]);
                     else
-                        *reinterpret_cast<uint32_t *>(dst) = w[0];
-                    if (lane == 0) scales[s.h[u] * a.c.shead + s.pos[u]] = scale[u];
+                        *reinterpret_cast<uint32_t *>(to) = w[0];
+                    if (lane == 0) scales[u * s.tp] = scale[u];
                 }
-            } else if (s.live[u]) {
+            } else if (live) {
                 if constexpr (E == 8)
-                    *reinterpret_cast<uint4 *>(dst) = in[u];
+                    *reinterpret_cast<uint4 *>(to) = in[u];
                 else
-                    *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2_bf16(x[0], x[1]), pack2_bf16(x[2], x[3]));
+                    *reinterpret_cast<uint2 *>(to) = make_uint2(pack2_bf16(x[0], x[1]), pack2_bf16(x[2], x[3]));
             }
         }
+        s.t += gridDim.x * s.tp * U;
+        src += (int64_t)gridDim.x * U * hop_in, dst += (int64_t)gridDim.x * U * hop_out;
+        if constexpr (Q8) scales += gridDim.x * s.tp * U;
     }
 }
 
 template <typename T, int D, bool Q8, int U>
 __global__ void __launch_bounds__(kRowThreads) kv_read_kernel(const RowsArgs a) {
-    using S = RowSet<T, D, U>;
+    using S = RowWalk<T, D>;
     constexpr int E = S::E, LPR = S::LPR, W = Q8 ? E / 4 : E / 2;   // words a lane reads
-    const int b = blockIdx.y, which = blockIdx.z, lane = threadIdx.x % LPR;
-    const NewRows nr = new_rows(a.lengths, a.n_new, b, a.n_tokens);
-    uint8_t *rows = const_cast<uint8_t *>(a.rows[which]) + b * a.stream + lane * 16;
-    const uint8_t *cache = (which ? a.c.v : a.c.k) + b * a.c.stream + lane * (W * 4);
-    const float *scales = Q8 ? (which ? a.c.vs : a.c.ks) + b * a.c.sstream : nullptr;
-    S s;
-    for (int r0 = blockIdx.x * (U * S::RPB); r0 < nr.n * a.kvh; r0 += gridDim.x * (U * S::RPB)) {
-        s.at(a, nr, r0);
+    const int b = blockIdx.y, which = blockIdx.z & 1, lane = threadIdx.x % LPR;
+    S s(a);
+    uint8_t *dst = const_cast<uint8_t *>(a.rows[which]) + b * a.stream + s.h * a.head + s.t * a.token + lane * 16;
+    const uint8_t *src = (which ? a.c.v : a.c.k) + b * a.c.stream + s.h * a.c.head + (s.first + s.t) * a.c.row + lane * (W * 4);
+    const float *scales = nullptr;
+    if constexpr (Q8) scales = (which ? a.c.vs : a.c.ks) + b * a.c.sstream + s.h * a.c.shead + s.first + s.t;
+    const int64_t hop_in = s.tp * a.c.row, hop_out = s.tp * a.token;
+    for (; s.t < s.n; s.t += gridDim.x * s.tp * U) {
         uint32_t w[U][W];
         float scale[U];
 #pragma unroll
@@ -168,26 +177,26 @@ __global__ void __launch_bounds__(kRowThreads) kv_read_kernel(const RowsArgs a) 
 #pragma unroll
             for (int i = 0; i < W; ++i) w[u][i] = 0;
             scale[u] = 0.f;
-            if (!s.live[u]) continue;
-            const uint8_t *src = cache + s.h[u] * a.c.head + s.pos[u] * a.c.row;
+            if (!s.live(a, s.t + u * s.tp)) continue;
+            const uint8_t *at = src + u * hop_in;
             if constexpr (W == 4) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(src);
+                const uint4 v = *reinterpret_cast<const uint4 *>(at);
                 w[u][0] = v.x, w[u][1] = v.y, w[u][2] = v.z, w[u][3] = v.w;
             } else if constexpr (W == 2) {
-                const uint2 v = *reinterpret_cast<const uint2 *>(src);
+                const uint2 v = *reinterpret_cast<const uint2 *>(at);
                 w[u][0] = v.x, w[u][1] = v.y;
             } else {
-                w[u][0] = *reinterpret_cast<const uint32_t *>(src);
+                w[u][0] = *reinterpret_cast<const uint32_t *>(at);
             }
-            if constexpr (Q8) scale[u] = scales[s.h[u] * a.c.shead + s.pos[u]];
+            if constexpr (Q8) scale[u] = scales[u * s.tp];
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (!s.live[u]) continue;
+            if (!s.live(a, s.t + u * s.tp)) continue;
             float x[E];
 #pragma unroll
             for (int e = 0; e < E; ++e)
-                x[e] = Q8 ? __fmul_rn(code_of(w[u][(e / 4) % W], e & 3), scale[u])
+                x[e] = Q8 ? __fmul_rn((float)(int8_t)(w[u][(e / 4) % W] >> (8 * (e & 3))), scale[u])
                           : (e & 1 ? bf16hi(w[u][(e / 2) % W]) : bf16lo(w[u][(e / 2) % W]));
             uint4 o;
             if constexpr (E == 8)
@@ -196,21 +205,25 @@ __global__ void __launch_bounds__(kRowThreads) kv_read_kernel(const RowsArgs a) 
             else
                 o = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
                                __float_as_uint(x[3]));
-            __stcs(reinterpret_cast<uint4 *>(rows + s.t[u] * a.token + s.h[u] * a.head), o);
+            __stcs(reinterpret_cast<uint4 *>(dst + u * hop_out), o);
         }
+        src += (int64_t)gridDim.x * U * hop_in, dst += (int64_t)gridDim.x * U * hop_out;
+        if constexpr (Q8) scales += gridDim.x * s.tp * U;
     }
 }
 
-constexpr int kRowSets = 4;   // rows in flight a thread, where there are that many
+// Rows in flight a thread, where there are that many (64 x 1792 bf16 rows in and out: 2 and 2 241 us, 4 and 4 227, 4
+// and 8 226 against 210 for the bytes at HBM's rate).
+constexpr int kAppendSets = 4, kReadSets = 8;
 
 typedef void (*RowsFn)(const RowsArgs);
-template <typename T, int U> RowsFn rows_fn(bool read, int d, bool q8) {
-    if (d == 64) {
-        if (read) return q8 ? kv_read_kernel<T, 64, true, U> : kv_read_kernel<T, 64, false, U>;
-        return q8 ? kv_append_kernel<T, 64, true, U> : kv_append_kernel<T, 64, false, U>;
-    }
-    if (read) return q8 ? kv_read_kernel<T, 128, true, U> : kv_read_kernel<T, 128, false, U>;
-    return q8 ? kv_append_kernel<T, 128, true, U> : kv_append_kernel<T, 128, false, U>;
+template <typename T, int D, bool Q8> RowsFn rows_fn(bool read, bool many) {
+    if (read) return many ? kv_read_kernel<T, D, Q8, kReadSets> : kv_read_kernel<T, D, Q8, 1>;
+    return many ? kv_append_kernel<T, D, Q8, kAppendSets> : kv_append_kernel<T, D, Q8, 1>;
+}
+template <typename T> RowsFn rows_fn(bool read, bool many, int d, bool q8) {
+    if (d == 64) return q8 ? rows_fn<T, 64, true>(read, many) : rows_fn<T, 64, false>(read, many);
+    return q8 ? rows_fn<T, 128, true>(read, many) : rows_fn<T, 128, false>(read, many);
 }
 
 qd_status move_rows(bool read, const qd_kv_cache *cache, const void *k_rows, const void *v_rows, int dtype,
@@ -239,17 +252,16 @@ qd_status move_rows(bool read, const qd_kv_cache *cache, const void *k_rows, con
     a.stream = stream_stride * e, a.token = token_stride * e, a.head = head_stride * e;
     a.lengths = lengths, a.n_new = n_new;
     a.n_tokens = n_tokens, a.kvh = cache->n_kv_heads, a.smax = cache->smax;
-    const int rpb = kRowThreads / (cache->head_dim / (int)unit);
-    const long long rows = (long long)n_tokens * cache->n_kv_heads;
-    if (rows > INT32_MAX / 2) return QD_EUNSUPPORTED;
-    const bool many = rows > rpb, q8 = cache->format == QD_KV_Q8;
-    const long long per = (long long)rpb * (many ? kRowSets : 1);
-    const long long most = std::max(1, sms_of(dev) * 16 / cache->n_streams);
-    const dim3 grid((unsigned)std::min((rows + per - 1) / per, most), (unsigned)cache->n_streams, 2);
-    const int d = cache->head_dim;
-    const RowsFn fn = dtype == QD_F32 ? (many ? rows_fn<float, kRowSets>(read, d, q8) : rows_fn<float, 1>(read, d, q8))
-                                      : (many ? rows_fn<__nv_bfloat16, kRowSets>(read, d, q8)
-                                              : rows_fn<__nv_bfloat16, 1>(read, d, q8));
+    const int rpb = kRowThreads / (cache->head_dim / (int)unit), d = cache->head_dim;
+    a.hp = std::min(a.kvh, rpb), a.tp = rpb / a.hp;
+    const bool many = n_tokens > a.tp, q8 = cache->format == QD_KV_Q8;
+    a.sets = many ? (read ? kReadSets : kAppendSets) : 1;
+    const int64_t per = (int64_t)a.tp * a.sets, hgroups = (a.kvh + a.hp - 1) / a.hp;
+    if (hgroups > 32767) return QD_EUNSUPPORTED;
+    // about 16 CTAs' worth of turns per SM: a few waves, whatever the lengths
+    const int64_t most = std::max<int64_t>(1, sms_of(dev) * 16 / (cache->n_streams * hgroups));
+    const dim3 grid((unsigned)std::min((n_tokens + per - 1) / per, most), (unsigned)cache->n_streams, (unsigned)(2 * hgroups));
+    const RowsFn fn = dtype == QD_F32 ? rows_fn<float>(read, many, d, q8) : rows_fn<__nv_bfloat16>(read, many, d, q8);
     fn<<<grid, kRowThreads, 0, static_cast<cudaStream_t>(cuda_stream)>>>(a);
     return cudaGetLastError() == cudaSuccess ? QD_OK : QD_ECUDA;
 }
