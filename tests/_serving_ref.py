@@ -53,12 +53,13 @@ def attend(q, k, v, lengths, n_new, scale, pk=None, pv=None):
     return out, mag, spread
 
 
-def attend_bound(out, mag, spread, n, D, dtype, q8):
+def attend_bound(out, mag, spread, n, D, dtype, q8, one_part=False):
     """How far a result may be from `out`:
 
     - the output's rounding, half a step;
     - each probability's rounding, twice (it stands in both sums, or in one of them): parts of fp16
-      (half a step 2^-11 a part, 8-bit cache) or bf16 (2^-8 a part, bf16 cache);
+      (half a step 2^-11 a part, 8-bit cache) or bf16 (2^-8 a part, bf16 cache: two parts for bf16 rows, or
+      with `one_part`, many rows over a bf16 prefix, one);
     - q's parts and the fp32 sum of D products in the score (2^-23 a product, for a truncating adder), e-fold in p,
       in numerator and denominator; 4 more roundings for the scale factors, and the argument's
       own rounding is a part of the same;
@@ -73,7 +74,7 @@ def attend_bound(out, mag, spread, n, D, dtype, q8):
     if q8:
         part_p, part_q = (2.0 ** -11, 0.0) if bf16 else (2.0 ** -22, 2.0 ** -22)
     else:
-        part_p, part_q = (2.0 ** -16, 0.0) if bf16 else (2.0 ** -24, 2.0 ** -24)
+        part_p, part_q = (2.0 ** (-8 if one_part else -16), 0.0) if bf16 else (2.0 ** -24, 2.0 ** -24)
     ds = spread * (part_q + (D + 8) * 2.0 ** -23)
     rel = 2 * part_p + 2 * torch.expm1(2 * ds) + 2.0 ** -20 + 2 * (n + 64) * 2.0 ** -23
     floor = n * 2.0 ** -35 * top if q8 else 0.0

@@ -25,6 +25,9 @@ def qd():
     return m
 
 
+WIDE_ROWS = 48                                   # rows of a key head from which it does
+
+
 def ints(v):
     return torch.tensor(v, dtype=torch.int32, device="cuda")
 
@@ -158,9 +161,11 @@ def _check(qd, B, T, G, H, D, S, lengths, n_new, q8, dtype, P=0, p8=None, seed=0
     got = out.cpu().double()
     unused = torch.isnan(want)
     assert torch.equal(got[unused], torch.full_like(got[unused], 7.0))
-    tol = ref.attend_bound(want, mag, spread, max(lengths) + P, D, dtype, q8 or bool(P and p8))
-    if P and p8 is not None and p8 != q8:
-        tol = torch.maximum(tol, ref.attend_bound(want, mag, spread, max(lengths) + P, D, dtype, False))
+    pq = q8 if p8 is None else p8
+    wide = bool(P) and dtype == torch.bfloat16 and B * T * G >= WIDE_ROWS    # the prefix goes to the wide kernel
+    tol = ref.attend_bound(want, mag, spread, max(lengths) + P, D, dtype, q8)
+    if P:
+        tol = torch.maximum(tol, ref.attend_bound(want, mag, spread, max(lengths) + P, D, dtype, pq, wide and not pq))
     bad = ~((got - want).abs() <= tol) & ~unused
     assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} off, worst {float(((got - want).abs() / tol)[~unused].max()):.3g} of the bound"
     return got
@@ -195,6 +200,52 @@ def test_drafted_tokens(qd, dtype, q8, D, T, G):
 def test_shared_prefix(qd, dtype, q8, p8, D, P, T, G):
     lengths = [0, 1, 7, 40, 64]
     _check(qd, 5, T, G, 2, D, 64, lengths, [min(T, n) for n in lengths], q8, dtype, P=P, p8=p8, seed=P)
+
+
+@pytest.mark.parametrize("q8", [True, False])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,T,G,P", [(24, 1, 2, 1), (48, 1, 1, 127), (64, 1, 2, 128), (33, 1, 4, 129), (13, 5, 3, 700),
+                                     (10, 8, 8, 515), (50, 2, 3, 1300)])
+def test_many_rows_over_a_prefix(qd, q8, D, B, T, G, P):
+    """Tiles of 128 rows, one alone (every other chunk to each half) or in pairs, partly filled, with unused rows between."""
+    g = gen(P)
+    lengths = torch.randint(0, 20, (B,), generator=g).tolist()
+    n_new = torch.randint(0, T + 1, (B,), generator=g).tolist() if T > 1 else None
+    if n_new:
+        n_new = [min(a, b) for a, b in zip(n_new, lengths)]
+    _check(qd, B, T, G, 2, D, 20, lengths, n_new, q8, torch.bfloat16, P=P, p8=q8, seed=P)
+    if T > 1:
+        _check(qd, B, T, G, 2, D, 20, lengths, None, q8, torch.bfloat16, P=P, p8=q8, seed=P + 1, q_scale=4.0)
+
+
+def test_no_rows_in_use_over_a_prefix(qd):
+    _check(qd, 30, 2, 2, 2, 128, 20, [0] * 30, [0] * 30, True, torch.bfloat16, P=300, p8=True)
+    _check(qd, 30, 2, 2, 2, 128, 20, [3] * 30, [0] * 29 + [1], False, torch.bfloat16, P=300, p8=False)
+
+
+@pytest.mark.parametrize("q8", [True, False])
+def test_growing_scores_over_a_prefix(qd, q8):
+    """Keys in order of their score: the reference moves in every chunk, O with it."""
+    g = gen(17)
+    B, P, D = 64, 1000, 128
+    q = torch.randn((B, 1, 1, D), generator=g).bfloat16()
+    q[:] = q[:1]
+    ramp = torch.linspace(-30, 90, P)
+    k = (ramp[:, None] * q[0, 0, 0].float() / q[0, 0, 0].float().square().sum())[None, None]
+    v = torch.randn((1, 1, P, D), generator=g) * torch.linspace(3, 0.1, P)[:, None]
+    if q8:
+        (kc, ks), (vc, vs) = ref.quantise_rows(k.numpy()), ref.quantise_rows(v.numpy())
+        pre = [torch.from_numpy(x).cuda() for x in (kc, vc, ks, vs)]
+        k, v = (torch.from_numpy(c).double() * torch.from_numpy(s).double()[..., None] for c, s in ((kc, ks), (vc, vs)))
+    else:
+        pre = [k.bfloat16().cuda(), v.bfloat16().cuda(), None, None]
+        k, v = k.bfloat16().double(), v.bfloat16().double()
+    own, _ = _filled(g, B, 1, 4, D, q8)
+    out = torch.empty((B, 1, 1, D), dtype=torch.bfloat16, device="cuda")
+    qd.qd_attn_cached(q.cuda(), qd.KvCache(*own), ints([0] * B), out, prefix=qd.KvCache(*pre), scale=1.0)
+    want, mag, spread = ref.attend(q[:1], k, v, [P], [1], 1.0)
+    tol = ref.attend_bound(want, mag, spread, P, D, torch.bfloat16, q8, not q8)
+    assert ((out.cpu().double() - want).abs() <= tol).all()
 
 
 @pytest.mark.parametrize("q8", [True, False])

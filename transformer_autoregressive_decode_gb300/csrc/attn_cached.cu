@@ -26,11 +26,7 @@
 // A cluster of CTAs shares one (stream, key head, rows) item; its warps take the 16-position
 // tiles in turn and their partial results (ref, sum, output) meet in distributed shared
 // memory, in a fixed order.  Nothing is kept in global memory but the prefix's partials.
-#include <cuda_fp16.h>
-
-#include "kv_view.cuh"
-#include "mma_sync.cuh"
-#include "qd_device.cuh"
+#include "attn_cached.cuh"
 #include "qd_internal.h"
 
 namespace qd {
@@ -40,39 +36,7 @@ namespace {
 constexpr int kAcWarps = 4, kAcThreads = kAcWarps * 32;
 constexpr int kAcMaxCluster = 8;
 constexpr int kAcMaxTokens = 64;
-// Probabilities stand 2^10 above 1 at the running maximum and may grow to 2^15 before the
-// sums are rescaled: fp16 then keeps 11 (two parts: 22) bits of every weight down to 2^-24
-// (2^-10) of the largest, and small moves of the maximum cost nothing.
-constexpr float kAcUp = 10.f, kAcRoom = 15.f;
 
-struct CachedArgs {
-    KvView c;
-    const uint8_t *q;
-    uint8_t *out;
-    int64_t q_stream, q_token, o_stream, o_token;   // bytes
-    const int32_t *lengths, *n_new;
-    int B, T, G, kvh, groups, max_len;
-    int rows;                                       // rows of an item: T G, of the prefix B T G
-    float scale2;                                   // softmax scale times log2(e)
-    // partials over the prefix: [kvh][B T G][splits]
-    float2 *p_ml;
-    float *p_o;
-    int splits;
-    // partials of attn_share_kernel: [slot][rows of a CTA]
-    float2 *s_ml;
-    float *s_o;
-};
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float lg2(float x) {
-    float y;
-    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool live) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
@@ -94,22 +58,6 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
     return d;
 }
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    const __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&v);
-}
-__device__ __forceinline__ float f16_of(float x) { return __half2float(__float2half_rn(x)); }
-__device__ __forceinline__ float bf16_of(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
-
-// Two code bytes (offset by 128) under the exponent of 1024: 1024 + u, less 1152 = code, exactly.
-// RAW: 1152 + code, for a sum that starts at the offset's share.
-template <bool RAW> __device__ __forceinline__ uint32_t codes_f16(uint32_t y, uint32_t sel) {
-    const uint32_t h = __byte_perm(y, 0x64646464u, sel);
-    if constexpr (RAW) return h;
-    const __half2 v = __hsub2(*reinterpret_cast<const __half2 *>(&h), __half2half2(__ushort_as_half(0x6480)));
-    return *reinterpret_cast<const uint32_t *>(&v);
-}
-
 template <bool Q8, bool F32, int D, int NT> struct AcCfg {
     static constexpr int C = Q8 ? (F32 ? 2 : 1) : (F32 ? 4 : 2);   // columns per row
     static constexpr int RW = 8 * NT / C;                          // rows per CTA
@@ -139,9 +87,6 @@ template <bool Q8, bool F32, int D, int NT> struct AcCfg {
     static constexpr int kSmem = kAcWarps * kRing > kEnd ? kAcWarps * kRing : kEnd;
     static constexpr int kMinCtas = NT == 1 ? (kSmem > 72 * 1024 ? 2 : kSmem > 54 * 1024 ? 3 : 4) : kSmem > 72 * 1024 ? 2 : 3;
 };
-
-// (ref, sum) of one partial: its weight against the reference M
-__device__ __forceinline__ float part_weight(float2 ml, float M) { return ml.y == 0.f ? 0.f : ex2(ml.x - M); }
 
 __device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
     float2 v;
@@ -633,11 +578,6 @@ template <bool Q8, bool F32, int D, int NT, bool PREFIX> struct WarpPass {
     }
 };
 
-__device__ __forceinline__ int clamp_len(int len, int most) { return len < 0 ? 0 : len > most ? most : len; }
-__device__ __forceinline__ int clamp_new(const CachedArgs &a, int b) {
-    const int n = a.n_new ? __ldg(a.n_new + b) : a.T;
-    return n < 0 ? 0 : n > a.T ? a.T : n;
-}
 // A stream's tiles of tp positions (a power of two): none where it has no new token.
 __device__ __forceinline__ int tiles_of(const CachedArgs &a, int b, int tp) {
     const int len = clamp_len(__ldg(a.lengths + b), a.max_len);
@@ -772,19 +712,6 @@ __global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NT>::kMinCtas)
 // whatever the lengths.  A warp's run covers the end of one item, whole items, the beginning of another;
 // it leaves a partial for each in slot (warp + item), which no other pair has: along the
 // list both only grow.  attn_join_kernel finds them by the same arithmetic.
-struct Share {
-    unsigned total, run, more;                       // tiles; a warp's run; the first `more` warps take one tile more
-    __device__ __forceinline__ void use(unsigned all, unsigned warps) {
-        total = all;
-        run = all / warps, more = all - run * warps;
-    }
-    __device__ __forceinline__ unsigned first(unsigned w) const { return w * run + min(w, more); }
-    __device__ __forceinline__ unsigned owner(unsigned x) const {   // x < total
-        const unsigned big = more * (run + 1);
-        return x < big ? x / (run + 1) : more + (x - big) / run;
-    }
-};
-
 // The tiles of streams before b (`upto`) and of all, times the items of a stream.
 __device__ __forceinline__ unsigned tiles_before(const CachedArgs &a, int upto, int tp, unsigned *total) {
     const int lane = threadIdx.x & 31;
@@ -901,7 +828,29 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const Cached
     const int in = hk * a.groups + grp;
     const unsigned x = s_b + in * tiles;
     const unsigned w0 = tiles ? sh.owner(x) : 0u;
-    const int own = tiles ? (int)(sh.owner(x + tiles - 1) + 1 - w0) : 0, all = own + a.splits;
+    const int own = tiles ? (int)(sh.owner(x + tiles - 1) + 1 - w0) : 0;
+    // the prefix's partials: `splits` of them, or the records of attn_prefix_tc_kernel
+    int n_pre = a.splits, subs = 1, sub = 0, cr = 0;
+    int64_t rec0 = 0;
+    if (a.wide) {
+        int rows;
+        cr = wide_rows(a, b, &rows) + r;
+        n_pre = 0;
+        if (tt < nn) {                               // else the row has no place in the list
+            const WideItems items(rows);
+            Share ws;
+            items.share(a, &ws);
+            const int tile = cr / kWideRows, item = items.pairs ? hk * items.pairs + tile / 2 : hk;
+            const unsigned c0 = (unsigned)(item * a.wide_chunks), o0 = ws.owner(c0);
+            if (items.pairs)
+                sub = tile & 1;
+            else
+                subs = 2;
+            n_pre = (int)(ws.owner(c0 + a.wide_chunks - 1) + 1 - o0) * subs;
+            rec0 = 2 * ((int64_t)o0 + item);
+        }
+    }
+    const int all = own + n_pre;
     const int64_t slot0 = (int64_t)b * a.kvh * a.groups + in + w0;
     const int64_t p_at = (((int64_t)hk * a.B + b) * a.rows + r) * a.splits;
     pdl_wait();                                     // the partials are written
@@ -925,7 +874,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const Cached
                 e[j] = a.s_ml[at];
                 v[j] = *reinterpret_cast<const float4 *>(a.s_o + at * D + d);
             } else if (i < all) {
-                const int64_t at = p_at + i - own;
+                const int k = i - own;
+                const int64_t at = !a.wide ? p_at + k
+                                           : (rec0 + (subs == 2 ? k : 2 * k + sub)) * kWideRows + cr % kWideRows;
                 e[j] = a.p_ml[at];
                 v[j] = *reinterpret_cast<const float4 *>(a.p_o + at * D + d);
             }
@@ -1055,6 +1006,12 @@ cudaError_t launch(int kind, const CachedArgs &a, unsigned *ctas, int nsplit, in
     return launch_ex(fn, *ctas, kAcThreads, K::kSmem, (unsigned)nsplit, s, a, nsplit);
 }
 
+// Rows from which the prefix goes to the tcgen05 cores.
+#ifndef QD_WF
+#define QD_WF 48
+#endif
+constexpr int kWideFrom = QD_WF;
+
 constexpr int tile_positions(bool q8, int d) { return q8 || d == 64 ? 32 : 16; }   // AcCfg::TP
 constexpr int rows_per_tile(bool q8, bool f32) { return 8 / (q8 ? (f32 ? 2 : 1) : (f32 ? 4 : 2)); }
 
@@ -1087,7 +1044,8 @@ struct Plan {
     int nsplit;                         // CTAs of a cluster (one cluster per item); 0: shared out
     unsigned ctas;                      // of the shared-out pass
     int64_t rows_all;
-    int p_nt, p_rw, p_groups, splits;   // the prefix
+    int p_nt, p_rw, p_groups, splits;   // the prefix, a few rows at a time
+    int wide;                           // or its CTAs on the tcgen05 cores
     size_t p_ml, p_o, s_ml, s_o, bytes; // workspace offsets
 };
 
@@ -1114,12 +1072,22 @@ qd_status make_plan(const qd_kv_cache *cache, const qd_kv_cache *prefix, int pre
     size_t at = 0;
     if (prefix && prefix_length > 0) {
         const bool pq8 = prefix->format == QD_KV_Q8;
+        if (!f32 && p->rows_all >= kWideFrom) {
+            p->wide = sms, p->nsplit = 0;
+            const int64_t tiles = (p->rows_all + kWideRows - 1) / kWideRows, items = kvh * ((tiles + 1) / 2);
+            const int64_t chunks = (prefix_length + kWideKeys - 1) / kWideKeys;
+            if (items * chunks > (1ll << 30)) return QD_EUNSUPPORTED;
+            const size_t recs = 2 * (size_t)(p->wide + items);
+            p->p_ml = at, at = up256(at + recs * kWideRows * 8);
+            p->p_o = at, at = up256(at + recs * kWideRows * d * 4);
+        } else {
         const int pper = rows_per_tile(pq8, f32);
         p->p_nt = p->rows_all > pper ? 2 : 1, p->p_rw = pper * p->p_nt;
         p->p_groups = (int)((p->rows_all + p->p_rw - 1) / p->p_rw);
         p->splits = prefix_splits((int)p->rows_all, kvh, prefix_length, p->p_rw, tile_positions(pq8, d), sms);
         p->p_ml = at, at = up256(at + (size_t)kvh * p->rows_all * p->splits * 8);
         p->p_o = at, at = up256(at + (size_t)kvh * p->rows_all * p->splits * d * 4);
+        }
     }
     if (!p->nsplit) {
         const CachedArgs none = {};
@@ -1216,11 +1184,14 @@ qd_status qd_attn_cached(const qd_kv_cache *cache, const qd_kv_cache *prefix, in
     if (with_prefix) {
         a.p_ml = reinterpret_cast<float2 *>(ws + p.p_ml), a.p_o = reinterpret_cast<float *>(ws + p.p_o);
         a.splits = p.splits;
+        if (p.wide) a.wide = p.wide, a.wide_chunks = (prefix_length + kWideKeys - 1) / kWideKeys;
         CachedArgs x = a;
         x.c = kv_view(prefix);
         x.rows = (int)p.rows_all, x.groups = p.p_groups, x.max_len = prefix_length;
         unsigned ctas = (unsigned)(p.p_groups * kvh * p.splits);
-        if (dispatch(kPassPrefix, prefix->format == QD_KV_Q8, f32, d, p.p_nt, x, &ctas, p.splits, dev, s) != cudaSuccess)
+        if (p.wide) {
+            if (launch_attn_prefix_tc(prefix->format == QD_KV_Q8, d, x, p.wide, s) != cudaSuccess) return QD_ECUDA;
+        } else if (dispatch(kPassPrefix, prefix->format == QD_KV_Q8, f32, d, p.p_nt, x, &ctas, p.splits, dev, s) != cudaSuccess)
             return QD_ECUDA;
     }
     const bool q8 = cache->format == QD_KV_Q8;
