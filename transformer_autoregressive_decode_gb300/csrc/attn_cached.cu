@@ -805,55 +805,54 @@ __global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NT>::kMinCtas)
 }
 
 // One output row (stream, token, query head) per WPR warps: its partials from attn_share_kernel
-// and from the prefix, weighted to a common reference, added in the order of the list.
+// and from the prefix, weighted to a common reference, added in the order of the list.  blockIdx.x: the stream, whose
+// place in the lists a warp works out once; blockIdx.y: its share of the stream's rows in use.
 constexpr int kJoinWarps = 8;
 template <bool F32, int D, int WPR>
 __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const CachedArgs a, int rw, int tp, unsigned warps) {
     __shared__ float4 s_acc[kJoinWarps][32];
     __shared__ float2 s_ml[kJoinWarps];
     constexpr int LPR = D / 4;                      // lanes of a row's float4s
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % WPR;
     // lengths and n_new may be read before the wait: attn_share_kernel lets this kernel start only after
     // its own wait for whatever wrote them
-    const unsigned r_all = blockIdx.x * (kJoinWarps / WPR) + warp / WPR;   // (stream, key head, row)
-    const int part = warp % WPR;
-    const unsigned n_rows = (unsigned)(a.B * a.kvh * a.rows), rr = min(r_all, n_rows - 1);
-    const int bh = rr / (unsigned)a.rows, r = rr - bh * a.rows, b = bh / a.kvh, hk = bh - b * a.kvh;
-    const int tt = r / a.G, grp = r / rw, in_grp = r - grp * rw;
-    const int tiles = tiles_of(a, b, tp), nn = clamp_new(a, b);
+    const int b = blockIdx.x, nn = clamp_new(a, b), tiles = tiles_of(a, b, tp);
     unsigned total;
     const unsigned s_b = tiles_before(a, b, tp, &total);
-    Share sh;
+    Share sh, ws;
     sh.use(total, warps);
+    int rows_all = 0, cr0 = 0;
+    if (a.wide) cr0 = wide_rows(a, b, &rows_all);
+    const WideItems items(rows_all);
+    if (a.wide) items.share(a, &ws);
+    const int used = nn * a.G, n_rows = a.kvh * used;    // of the stream, key head by key head
+    pdl_wait();                                     // the partials are written
+
+    constexpr int kRows = kJoinWarps / WPR;         // rows of a CTA's turn
+    for (int i0 = blockIdx.y * kRows; i0 < n_rows; i0 += gridDim.y * kRows) {
+    const int row = i0 + warp / WPR, hk = min(row, n_rows - 1) / used, r = min(row, n_rows - 1) - hk * used;
+    const int tt = r / a.G, grp = r / rw, in_grp = r - grp * rw;
     const int in = hk * a.groups + grp;
     const unsigned x = s_b + in * tiles;
     const unsigned w0 = tiles ? sh.owner(x) : 0u;
     const int own = tiles ? (int)(sh.owner(x + tiles - 1) + 1 - w0) : 0;
-    // the prefix's partials: `splits` of them, or the records of attn_prefix_tc_kernel
-    int n_pre = a.splits, subs = 1, sub = 0, cr = 0;
-    int64_t rec0 = 0;
-    if (a.wide) {
-        int rows;
-        cr = wide_rows(a, b, &rows) + r;
-        n_pre = 0;
-        if (tt < nn) {                               // else the row has no place in the list
-            const WideItems items(rows);
-            Share ws;
-            items.share(a, &ws);
-            const int tile = cr / kWideRows, item = items.pairs ? hk * items.pairs + tile / 2 : hk;
-            const unsigned c0 = (unsigned)(item * a.wide_chunks), o0 = ws.owner(c0);
-            if (items.pairs)
-                sub = tile & 1;
-            else
-                subs = 2;
-            n_pre = (int)(ws.owner(c0 + a.wide_chunks - 1) + 1 - o0) * subs;
-            rec0 = 2 * ((int64_t)o0 + item);
-        }
-    }
-    const int all = own + n_pre;
     const int64_t slot0 = (int64_t)b * a.kvh * a.groups + in + w0;
     const int64_t p_at = (((int64_t)hk * a.B + b) * a.rows + r) * a.splits;
-    pdl_wait();                                     // the partials are written
+    // the prefix's partials: `splits` of them, or the records of attn_prefix_tc_kernel
+    int n_pre = a.splits, subs = 1, sub = 0;
+    int64_t rec0 = 0;
+    const int cr = cr0 + r;
+    if (a.wide) {
+        const int tile = cr / kWideRows, item = items.pairs ? hk * items.pairs + tile / 2 : hk;
+        const unsigned c0 = (unsigned)(item * a.wide_chunks), o0 = ws.owner(c0);
+        if (items.pairs)
+            sub = tile & 1;
+        else
+            subs = 2;
+        n_pre = (int)(ws.owner(c0 + a.wide_chunks - 1) + 1 - o0) * subs;
+        rec0 = 2 * ((int64_t)o0 + item);
+    }
+    const int all = own + n_pre;
 
     // 32 / LPR partials at a time (one for head_dim 128), LPR lanes each; kBatch of those are loaded
     // together, (ref, sum) with their rows, then weighted to the running reference
@@ -913,22 +912,24 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const Cached
         s_acc[warp][lane] = acc;
         if (lane == 0) s_ml[warp] = make_float2(M, sum);
         __syncthreads();
-        if (part) return;
+        const int w1 = warp - part;                 // this row's first warp
 #pragma unroll
-        for (int i = 0; i < WPR; ++i) M = fmaxf(M, s_ml[warp + i].x);
+        for (int i = 0; i < WPR; ++i) M = fmaxf(M, s_ml[w1 + i].x);
         acc = make_float4(0.f, 0.f, 0.f, 0.f), sum = 0.f;
 #pragma unroll
         for (int i = 0; i < WPR; ++i) {
-            const float2 e = s_ml[warp + i];
+            const float2 e = s_ml[w1 + i];
             if (e.y == 0.f) continue;
             const float f = part_weight(e, M);
-            add4(acc, f, s_acc[warp + i][lane]);
+            add4(acc, f, s_acc[w1 + i][lane]);
             sum = fmaf(f, e.y, sum);
         }
+        __syncthreads();                            // before the next turn's
     }
-    if (r_all < n_rows && tt < nn && lane < LPR)
+    if (row < n_rows && part == 0 && lane < LPR)
         store4<F32>(a.out + b * a.o_stream + tt * a.o_token + ((int64_t)(hk * a.G + (r - tt * a.G)) * D + d) * (F32 ? 4 : 2),
                     acc, sum == 0.f ? 0.f : 1.f / sum);
+    }
 }
 
 // ------------------------------------------------------------------------- launches
@@ -959,9 +960,9 @@ template <typename F> cudaError_t make_ready(Ready *r, F fn, int smem) {
 }
 
 template <typename F, typename... A>
-cudaError_t launch_ex(F fn, unsigned grid, int threads, int smem, unsigned cluster, cudaStream_t s, A... args) {
+cudaError_t launch_ex(F fn, dim3 grid, int threads, int smem, unsigned cluster, cudaStream_t s, A... args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = s;
@@ -1026,10 +1027,10 @@ cudaError_t dispatch(int kind, bool q8, bool f32, int d, int nt, const CachedArg
     return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_join(bool f32, int d, const CachedArgs &a, int rw, int tp, unsigned warps, bool many, cudaStream_t s) {
-    const long long rows = (long long)a.B * a.kvh * a.rows;
-    const int wpr = many ? kJoinWarps : 1, per = kJoinWarps / wpr;
-    const unsigned grid = (unsigned)((rows + per - 1) / per);
+cudaError_t launch_join(bool f32, int d, const CachedArgs &a, int rw, int tp, unsigned warps, bool many, int sms, cudaStream_t s) {
+    // a warp's turn or two per CTA: rows enough to fill the SMs, the stream's place worked out seldom
+    const int wpr = many ? kJoinWarps : 1, turns = (a.kvh * a.rows * wpr + kJoinWarps - 1) / kJoinWarps;
+    const dim3 grid((unsigned)a.B, (unsigned)std::min({turns, std::max(1, 8 * sms / a.B), 65535}));
 #define QD_JOIN(F, DD, W) \
     if (f32 == F && d == DD && wpr == W) return launch_ex(attn_join_kernel<F, DD, W>, grid, kJoinWarps * 32, 0, 1, s, a, rw, tp, warps);
     QD_JOIN(false, 64, 1) QD_JOIN(false, 128, 1) QD_JOIN(true, 64, 1) QD_JOIN(true, 128, 1)
@@ -1205,7 +1206,7 @@ qd_status qd_attn_cached(const qd_kv_cache *cache, const qd_kv_cache *prefix, in
     if (dispatch(kPassShare, q8, f32, d, p.nt, a, &p.ctas, 0, dev, s) != cudaSuccess) return QD_ECUDA;
     // many partials a row (long streams, few of them): several warps per row
     const unsigned warps = p.ctas * kAcWarps, items = (unsigned)((int64_t)B * kvh * p.groups);
-    return launch_join(f32, d, a, p.rw, p.tp, warps, warps / items + p.splits > 16, s) == cudaSuccess ? QD_OK : QD_ECUDA;
+    return launch_join(f32, d, a, p.rw, p.tp, warps, warps / items + p.splits > 16, sms_of(dev), s) == cudaSuccess ? QD_OK : QD_ECUDA;
 }
 
 }  // extern "C"

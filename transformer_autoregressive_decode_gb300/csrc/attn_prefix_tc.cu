@@ -74,6 +74,34 @@ __device__ __forceinline__ void ld32(uint32_t taddr, float *v) {
 #pragma unroll
     for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
 }
+// pairs of fp32 in one instruction
+__device__ __forceinline__ uint64_t pk(float x, float y) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+    return v;
+}
+__device__ __forceinline__ void unpk(uint64_t v, float &x, float &y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+// 32 columns without waiting; ld_done makes them usable
+__device__ __forceinline__ void ld32_start(uint32_t taddr, uint32_t *r) {
+    tc_ld16_nowait(taddr, r);
+    tc_ld16_nowait(taddr + 16, r + 16);
+}
+
 __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
     return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
            ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
@@ -188,17 +216,17 @@ __global__ void __launch_bounds__(kWtThreads, 1) attn_prefix_tc_kernel(const Cac
             const int hk = w.item / items.per_head();
             const uint8_t *base = (is_v ? a.c.v : a.c.k) + hk * a.c.head;
             if constexpr (Q8) {
-                constexpr int PPR = D / 16, RPI = kWtLoad / PPR, N = 128 / RPI;   // code pieces a row; rows, copies an instruction's
+                constexpr int RPI = kWtLoad / 4, N = 128 / RPI * KB;   // four lanes a row of one 64-wide block
                 const float *ks = a.c.ks + hk * a.c.shead, *vs = a.c.vs + hk * a.c.shead;
-                const int j = tid % PPR, r0 = tid / PPR;
+                const int j = tid & 3, r0 = tid >> 2;
                 uint4 u[N];                         // the next chunk's codes
                 float s[2][2];                      // V's warps: K's and V's scales of keys tid and tid + 64
                 auto load = [&](int c) {
 #pragma unroll
                     for (int i = 0; i < N; ++i) {
-                        const int key = c * kWideKeys + r0 + i * RPI;
+                        const int key = c * kWideKeys + r0 + (i / KB) * RPI;
                         u[i] = make_uint4(0, 0, 0, 0);
-                        if (key < P) u[i] = __ldg(reinterpret_cast<const uint4 *>(base + (int64_t)key * a.c.row + j * 16));
+                        if (key < P) u[i] = __ldg(reinterpret_cast<const uint4 *>(base + (int64_t)key * a.c.row + (i % KB) * 64 + j * 16));
                     }
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -214,18 +242,17 @@ __global__ void __launch_bounds__(kWtThreads, 1) attn_prefix_tc_kernel(const Cac
                     uint8_t *tile = tiles + (uint32_t)(st * KB) * kWtBox;
 #pragma unroll
                     for (int n = 0; n < N; ++n) {
-                        const int r = r0 + n * RPI;
+                        const int r = r0 + (n / KB) * RPI;
                         const uint32_t x[4] = {u[n].x ^ 0x80808080u, u[n].y ^ 0x80808080u, u[n].z ^ 0x80808080u,
                                                u[n].w ^ 0x80808080u};
-                        const uint4 p0 = make_uint4(codes_f16<false>(x[0], 0x4140), codes_f16<false>(x[0], 0x4342),
-                                                    codes_f16<false>(x[1], 0x4140), codes_f16<false>(x[1], 0x4342));
-                        const uint4 p1 = make_uint4(codes_f16<false>(x[2], 0x4140), codes_f16<false>(x[2], 0x4342),
-                                                    codes_f16<false>(x[3], 0x4140), codes_f16<false>(x[3], 0x4342));
-                        // the two blocks' lanes write alternate pieces, so that they meet different banks
-                        const int odd = (j >> 2) & 1, c = 2 * (j & 3);
-                        uint8_t *box = tile + (j >> 2) * kWtBox;
-                        *reinterpret_cast<uint4 *>(box + swz(r, c + odd)) = odd ? p1 : p0;
-                        *reinterpret_cast<uint4 *>(box + swz(r, c + 1 - odd)) = odd ? p0 : p1;
+                        // eight lanes: two rows, whose swizzles differ in the last bit, and four even (odd) pieces
+                        uint8_t *box = tile + (n % KB) * kWtBox;
+                        *reinterpret_cast<uint4 *>(box + swz(r, 2 * j)) =
+                            make_uint4(codes_f16<false>(x[0], 0x4140), codes_f16<false>(x[0], 0x4342),
+                                       codes_f16<false>(x[1], 0x4140), codes_f16<false>(x[1], 0x4342));
+                        *reinterpret_cast<uint4 *>(box + swz(r, 2 * j + 1)) =
+                            make_uint4(codes_f16<false>(x[2], 0x4140), codes_f16<false>(x[2], 0x4342),
+                                       codes_f16<false>(x[3], 0x4140), codes_f16<false>(x[3], 0x4342));
                     }
                     // the scales come with V, which is not given up before its softmax is done (K's tile is)
                     if (is_v) {
@@ -390,6 +417,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) attn_prefix_tc_kernel(const Cac
                 }
             }
             float ref = -INFINITY, l = 0.f;
+            const uint64_t cs2 = pk(cs, cs);
             const int N = pairs ? 2 * w.n : w.n;
             for (int i = h; i < N; i += 2) {
                 const int c = pairs ? i >> 1 : i, st = (kc + c) & 1;
@@ -399,31 +427,36 @@ __global__ void __launch_bounds__(kWtThreads, 1) attn_prefix_tc_kernel(const Cac
                 ++ns;
                 if constexpr (Q8) ok = ok && wt_wait(&v_full[st], (uint32_t)((kc + c) >> 1) & 1u, bad);
                 tc_fence_after();
-                // the chunk's largest score (with the values' scales: the largest weight)
+                // the chunk's largest score (with the values' scales: the largest weight), 64 keys at a time
                 float m = -INFINITY;
+#pragma unroll 1
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t u[64];
+                    ld32_start(tS + 64u * q, u);
+                    ld32_start(tS + 64u * q + 32u, u + 32);
+                    tc_wait_ld_u32<64>(u);
+                    float m2 = -INFINITY;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float s[32];
-                    ld32(tS + 32u * q, s);
-                    if constexpr (Q8) {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const float4 k = *reinterpret_cast<const float4 *>(sc + 32 * q + e);
-                            const float4 v = *reinterpret_cast<const float4 *>(sc + 256 + 32 * q + e);
-                            s[e] = fmaf(s[e] * k.x, cs, v.x), s[e + 1] = fmaf(s[e + 1] * k.y, cs, v.y);
-                            s[e + 2] = fmaf(s[e + 2] * k.z, cs, v.z), s[e + 3] = fmaf(s[e + 3] * k.w, cs, v.w);
+                    for (int e = 0; e < 64; e += 4) {
+                        float s0 = __uint_as_float(u[e]), s1 = __uint_as_float(u[e + 1]), s2 = __uint_as_float(u[e + 2]),
+                              s3 = __uint_as_float(u[e + 3]);
+                        if constexpr (Q8) {
+                            const ulonglong2 k = *reinterpret_cast<const ulonglong2 *>(sc + 64 * q + e);
+                            const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(sc + 256 + 64 * q + e);
+                            unpk(fma2(mul2(pk(s0, s1), k.x), cs2, v.x), s0, s1);
+                            unpk(fma2(mul2(pk(s2, s3), k.y), cs2, v.y), s2, s3);
+                        } else {
+                            unpk(mul2(pk(s0, s1), cs2), s0, s1);
+                            unpk(mul2(pk(s2, s3), cs2), s2, s3);
                         }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) s[e] *= cs;
+                        if (left < kWideKeys) {
+                            const int key = 64 * q + e;
+                            s0 = key < left ? s0 : -INFINITY, s1 = key + 1 < left ? s1 : -INFINITY;
+                            s2 = key + 2 < left ? s2 : -INFINITY, s3 = key + 3 < left ? s3 : -INFINITY;
+                        }
+                        m = fmaxf(m, fmaxf(s0, s1)), m2 = fmaxf(m2, fmaxf(s2, s3));
                     }
-                    if (left < kWideKeys) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (32 * q + e >= left) s[e] = -INFINITY;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) m = fmaxf(m, s[e]);
+                    m = fmaxf(m, m2);
                 }
                 if (__any_sync(0xffffffffu, m > ref + kAcRoom)) {
                     // this half's earlier O products are done: its next S, which came behind them, is
@@ -435,7 +468,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) attn_prefix_tc_kernel(const Cac
                         l *= f;
                     }
                     if (i >= 2) {
-#pragma unroll
+#pragma unroll 1
                         for (int q = 0; q < D / 32; ++q) {
                             float v[32];
                             uint32_t u[32];
@@ -448,32 +481,54 @@ __global__ void __launch_bounds__(kWtThreads, 1) attn_prefix_tc_kernel(const Cac
                     }
                 }
                 const float rf = ref == -INFINITY ? 0.f : ref;
+                const uint64_t rf2 = pk(-rf, -rf);
+                uint64_t l2 = pk(l, 0.f);
+                uint32_t u[2][32];                  // the next 32 keys' scores arrive while these are worked
+                ld32_start(tS, u[0]);
+                tc_wait_ld_u32<32>(u[0]);
+#pragma unroll 1
+                for (int q = 0; q < 4; q += 2) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float s[32];
-                    ld32(tS + 32u * q, s);
-                    uint32_t u[16];
+                    for (int z = 0; z < 2; ++z) {
+                        const int key0 = 32 * (q + z);
+                        if (z == 0 || q == 0) ld32_start(tS + key0 + 32u, u[z ^ 1]);
+                        uint32_t o[16];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        if constexpr (Q8) {
-                            const float4 k = *reinterpret_cast<const float4 *>(sc + 32 * q + e);
-                            s[e] *= k.x, s[e + 1] *= k.y, s[e + 2] *= k.z, s[e + 3] *= k.w;
+                        for (int e = 0; e < 32; e += 4) {
+                            uint64_t x0 = pk(__uint_as_float(u[z][e]), __uint_as_float(u[z][e + 1]));
+                            uint64_t x1 = pk(__uint_as_float(u[z][e + 2]), __uint_as_float(u[z][e + 3]));
+                            if constexpr (Q8) {
+                                const ulonglong2 k = *reinterpret_cast<const ulonglong2 *>(sc + key0 + e);
+                                x0 = mul2(x0, k.x), x1 = mul2(x1, k.y);
+                            }
+                            float s0, s1, s2, s3;
+                            unpk(fma2(x0, cs2, rf2), s0, s1);
+                            unpk(fma2(x1, cs2, rf2), s2, s3);
+                            s0 = ex2(s0), s1 = ex2(s1), s2 = ex2(s2), s3 = ex2(s3);
+                            if (left < kWideKeys) {
+                                const int key = key0 + e;
+                                s0 = key < left ? s0 : 0.f, s1 = key + 1 < left ? s1 : 0.f;
+                                s2 = key + 2 < left ? s2 : 0.f, s3 = key + 3 < left ? s3 : 0.f;
+                            }
+                            x0 = pk(s0, s1), x1 = pk(s2, s3);
+                            l2 = add2(l2, add2(x0, x1));
+                            if constexpr (Q8) {
+                                const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(sc + 128 + key0 + e);
+                                unpk(mul2(x0, v.x), s0, s1);
+                                unpk(mul2(x1, v.y), s2, s3);
+                            }
+                            o[e / 2] = Q8 ? pack_f16(s0, s1) : pack_bf16(s0, s1);
+                            o[e / 2 + 1] = Q8 ? pack_f16(s2, s3) : pack_bf16(s2, s3);
                         }
-#pragma unroll
-                        for (int z = e; z < e + 4; ++z) {
-                            s[z] = ex2(fmaf(s[z], cs, -rf));
-                            if (left < kWideKeys && 32 * q + z >= left) s[z] = 0.f;
-                            l += s[z];
-                        }
-                        if constexpr (Q8) {
-                            const float4 v = *reinterpret_cast<const float4 *>(sc + 128 + 32 * q + e);
-                            s[e] *= v.x, s[e + 1] *= v.y, s[e + 2] *= v.z, s[e + 3] *= v.w;
-                        }
-                        u[e / 2] = Q8 ? pack_f16(s[e], s[e + 1]) : pack_bf16(s[e], s[e + 1]);
-                        u[e / 2 + 1] = Q8 ? pack_f16(s[e + 2], s[e + 3]) : pack_bf16(s[e + 2], s[e + 3]);
+                        // these keys' columns lie in the first half of S's that have been read
+                        if (z == 0 || q == 0) tc_wait_ld_u32<32>(u[z ^ 1]);
+                        tc_st16(tS + key0 / 2, o);
                     }
-                    // keys 32 q ..: columns 16 q .. of the half's S, whose scores up to 32 q + 31 have been read
-                    tc_st16(tS + 16u * q, u);
+                }
+                {
+                    float l0, l1;
+                    unpk(l2, l0, l1);
+                    l = l0 + l1;
                 }
                 tc_wait_st();
                 tc_fence_before();
@@ -492,7 +547,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) attn_prefix_tc_kernel(const Cac
             if (row < rows) a.p_ml[rec * kWideRows + r] = make_float2(ref, l + fail);
             float *dst = a.p_o + (rec * kWideRows + r) * D;
             if (steps > 0) {
-#pragma unroll
+#pragma unroll 1
                 for (int q = 0; q < D / 32; ++q) {
                     float v[32];
                     ld32(tO + 32u * q, v);
