@@ -53,13 +53,13 @@ def attend(q, k, v, lengths, n_new, scale, pk=None, pv=None):
     return out, mag, spread
 
 
-def attend_bound(out, mag, spread, n, D, dtype, q8, one_part=False):
+def attend_bound(out, mag, spread, n, D, dtype, q8, wide=False):
     """How far a result may be from `out`:
 
     - the output's rounding, half a step;
     - each probability's rounding, twice (it stands in both sums, or in one of them): parts of fp16
       (half a step 2^-11 a part, 8-bit cache) or bf16 (2^-8 a part, bf16 cache: two parts for bf16 rows, or
-      with `one_part`, many rows over a bf16 prefix, one);
+      one where `wide`: many rows over a prefix);
     - q's parts and the fp32 sum of D products in the score (2^-23 a product, for a truncating adder), e-fold in p,
       in numerator and denominator; 4 more roundings for the scale factors, and the argument's
       own rounding is a part of the same;
@@ -67,17 +67,18 @@ def attend_bound(out, mag, spread, n, D, dtype, q8, one_part=False):
     - 8-bit cache: the weights p_j s_j (s_j the row's scale) go into the product as fp16 numbers, the largest
       at 2^10 or above, so the spacing 2^-24 of fp16's smallest numbers costs each of them up to 2^-25, which is
       2^-35 of the largest.  Times codes of at most 127 and n positions: n 2^-35 max(p_j s_j 127) / sum p, and
-      s_j 127 is the row's largest |v|.  Where the heavy positions hold zeros this is all that is left of an element."""
+      s_j 127 is the row's largest |v|.  Where the heavy positions hold zeros this is all that is left of an element.
+      `wide` sets the largest at 2^2 or above: 2^-27."""
     mag, top = mag[..., :D], mag[..., D:]
     bf16 = dtype == torch.bfloat16
     step = torch.finfo(dtype).eps / 2
     if q8:
         part_p, part_q = (2.0 ** -11, 0.0) if bf16 else (2.0 ** -22, 2.0 ** -22)
     else:
-        part_p, part_q = (2.0 ** (-8 if one_part else -16), 0.0) if bf16 else (2.0 ** -24, 2.0 ** -24)
+        part_p, part_q = (2.0 ** (-8 if wide else -16), 0.0) if bf16 else (2.0 ** -24, 2.0 ** -24)
     ds = spread * (part_q + (D + 8) * 2.0 ** -23)
     rel = 2 * part_p + 2 * torch.expm1(2 * ds) + 2.0 ** -20 + 2 * (n + 64) * 2.0 ** -23
-    floor = n * 2.0 ** -35 * top if q8 else 0.0
+    floor = n * 2.0 ** (-27 if wide else -35) * top if q8 else 0.0
     return step * (out.abs() + mag * rel) + mag * rel + floor * 1.01 + 1e-30
 
 

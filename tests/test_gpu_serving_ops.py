@@ -165,7 +165,7 @@ def _check(qd, B, T, G, H, D, S, lengths, n_new, q8, dtype, P=0, p8=None, seed=0
     wide = bool(P) and dtype == torch.bfloat16 and B * T * G >= WIDE_ROWS    # the prefix goes to the wide kernel
     tol = ref.attend_bound(want, mag, spread, max(lengths) + P, D, dtype, q8)
     if P:
-        tol = torch.maximum(tol, ref.attend_bound(want, mag, spread, max(lengths) + P, D, dtype, pq, wide and not pq))
+        tol = torch.maximum(tol, ref.attend_bound(want, mag, spread, max(lengths) + P, D, dtype, pq, wide))
     bad = ~((got - want).abs() <= tol) & ~unused
     assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} off, worst {float(((got - want).abs() / tol)[~unused].max()):.3g} of the bound"
     return got
@@ -223,6 +223,25 @@ def test_no_rows_in_use_over_a_prefix(qd):
     _check(qd, 30, 2, 2, 2, 128, 20, [3] * 30, [0] * 29 + [1], False, torch.bfloat16, P=300, p8=False)
 
 
+def test_a_prefix_that_begins_with_hidden_keys(qd):
+    """Keys of -infinity first, then scores far below zero: the reference comes from the first that count."""
+    g = gen(18)
+    B, P, D = 64, 300, 128
+    k = torch.full((1, 1, P, D), 0.0)
+    k[0, 0, :, 0] = -500.0 + torch.rand((P,), generator=g)
+    k[0, 0, :150] = -math.inf
+    v = torch.randn((1, 1, P, D), generator=g).bfloat16()
+    k = k.bfloat16()
+    own, _ = _filled(g, B, 1, 4, D, False)
+    q = torch.zeros((B, 1, 1, D)).bfloat16()
+    q[..., 0] = 1.0
+    q[...] = q + 2.0 ** -100                                        # nothing times an infinity
+    out = torch.empty((B, 1, 1, D), dtype=torch.bfloat16, device="cuda")
+    qd.qd_attn_cached(q.cuda(), qd.KvCache(*own), ints([0] * B), out, prefix=qd.KvCache(k.cuda(), v.cuda()), scale=1.0)
+    want, mag, spread = ref.attend(q[:1], k[:, :, 150:].double(), v[:, :, 150:].double(), [150], [1], 1.0)
+    assert ((out.cpu().double() - want).abs() <= ref.attend_bound(want, mag, spread, P, D, torch.bfloat16, False, True)).all()
+
+
 @pytest.mark.parametrize("q8", [True, False])
 def test_growing_scores_over_a_prefix(qd, q8):
     """Keys in order of their score: the reference moves in every chunk, O with it."""
@@ -244,7 +263,7 @@ def test_growing_scores_over_a_prefix(qd, q8):
     out = torch.empty((B, 1, 1, D), dtype=torch.bfloat16, device="cuda")
     qd.qd_attn_cached(q.cuda(), qd.KvCache(*own), ints([0] * B), out, prefix=qd.KvCache(*pre), scale=1.0)
     want, mag, spread = ref.attend(q[:1], k, v, [P], [1], 1.0)
-    tol = ref.attend_bound(want, mag, spread, P, D, torch.bfloat16, q8, not q8)
+    tol = ref.attend_bound(want, mag, spread, P, D, torch.bfloat16, q8, True)
     assert ((out.cpu().double() - want).abs() <= tol).all()
 
 

@@ -11,15 +11,19 @@
 // otherwise both take the one tile, every other chunk each.  The list (key head, tile pair, chunk) is cut into equal
 // runs, one per CTA; each leaves (ref, sum, O) of its rows for attn_join_kernel.
 //
-// ref follows the running maximum at a distance (kAcUp, kAcRoom), so O is rescaled in tensor memory only
-// when the maximum has moved far; the half's previous O product has finished when its next S has.
-//
 // bf16 prefix: P is one bf16 part (half a step 2^-8 of each probability, at random; a second part would add half the MMA
 // time again).  8-bit prefix: the codes are widened to fp16, exactly, on their way into shared
 // memory; the keys' scales multiply S's columns, the values' scales P's, and P is fp16 (2^-11).
 //
-// Roles (416 threads): warps 0-3 and 4-7 the softmax of the two halves (a row each, also Q and the results),
-// warps 8 and 9 load K, 10 and 11 V, warp 12 owns the tensor memory and its lane 0 issues the MMAs.  Every wait
+// A chunk's probabilities are formed with the reference as it stands, the scores left where they are, and written
+// over them only when none has outgrown its room; otherwise the maximum is taken first (rescaling O in tensor
+// memory: the half's previous O product has finished when its next S has).
+// So the scores are usually read once: the softmax is bound by the exponentials' rate (16 a clock and SM: 1024
+// clocks for 128 x 128, as long as their two products take).
+//
+// Roles (512 threads): warps 0-3 and 4-7 the softmax of the two halves (a row each, also Q and the results),
+// warps 8-11 load K and V, warp 12 owns the tensor memory and issues the MMAs, warps 13-15 only complete its
+// warpgroup.  Registers a thread: 128 at launch, then 184, 184, 88 and 56 (all of the 65,536).  Every wait
 // is bounded; where one expires the CTA's partials become NaN and the roles run to their ends.
 #include <cuda.h>
 
@@ -31,8 +35,10 @@ namespace qd {
 
 namespace {
 
-constexpr int kWtThreads = 416;
-constexpr int kWtSoft = 256, kWtLoad = 64;   // softmax threads, loading threads of K and of V
+constexpr int kWtThreads = 512;
+constexpr int kWtSoft = 256, kWtLoad = 128;   // softmax threads, loading threads
+constexpr int kWtRegsSoft = 184, kWtRegsLoad = 88, kWtRegsMma = 56;
+static_assert(128 * (2 * kWtRegsSoft + kWtRegsLoad + kWtRegsMma) <= kWtThreads * 128, "registers");
 constexpr uint32_t kWtBox = 128 * 128;        // 128 rows of 128 bytes, 128-byte swizzle
 constexpr uint32_t kWtS = 0, kWtO = 256;      // tensor memory columns: S (and P) of the halves, O
 
@@ -109,6 +115,103 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t lbo, uint32
 // Byte of 16-byte piece c (of 8) of row r in a swizzled box.
 __device__ __forceinline__ uint32_t swz(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 
+// The reference of a half's rows stands 2^kWtUp<> below 2^0.. of the largest weight when it is set, and moves when a
+// weight has passed kWtTop<>.  fp16 weights (8-bit prefix): from 2^2 to 2^15, the type's range less a factor of two; below
+// 2^-14 they lose bits, 2^-25 at most, 2^-27 of the largest.  bf16 weights have fp32's range: practically once.
+template <bool Q8> constexpr float kWtUp = Q8 ? 2.f : 0.f;
+template <bool Q8> constexpr float kWtTop = Q8 ? 32768.f : 1.e18f;
+
+// The largest score of a row's first keys (32 for a first guess, or all of a chunk) in log2 units, with the values' scales: the
+// largest weight.
+template <bool Q8> __device__ __forceinline__ float largest(uint32_t tS, const float *sc, float cs, int left, int keys) {
+    float m = -INFINITY;
+    const int n = min(left, keys);
+#pragma unroll 1
+    for (int q = 0; q < keys; q += 32) {
+        float s[32];
+        ld32(tS + q, s);
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+            if constexpr (Q8) {
+                const float4 k = *reinterpret_cast<const float4 *>(sc + q + e), v = *reinterpret_cast<const float4 *>(sc + 256 + q + e);
+                s[e] = fmaf(s[e] * k.x, cs, v.x), s[e + 1] = fmaf(s[e + 1] * k.y, cs, v.y);
+                s[e + 2] = fmaf(s[e + 2] * k.z, cs, v.z), s[e + 3] = fmaf(s[e + 3] * k.w, cs, v.w);
+            } else {
+                s[e] *= cs, s[e + 1] *= cs, s[e + 2] *= cs, s[e + 3] *= cs;
+            }
+        }
+        if (n - q < 32) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                if (q + e >= n) s[e] = -INFINITY;
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) m = fmaxf(m, s[e]);
+    }
+    return m;
+}
+
+// A row's chunk against its reference: the weights of the product packed to 16 bits, the largest of them, and the sum of the
+// probabilities.  A weight past kWtTop means that the reference has to move.
+template <bool Q8, bool EDGE>
+__device__ __forceinline__ void weigh(uint32_t tS, const float *sc, float cs, float ref, int left, uint32_t (&out)[64],
+                                      float &top, float &sum) {
+    const float rf = ref == -INFINITY ? 0.f : ref;
+    const uint64_t cs2 = pk(cs, cs), rf2 = pk(-rf, -rf);
+    uint64_t l2 = pk(0.f, 0.f);
+    float t0 = 0.f, t1 = 0.f;
+    uint32_t u[2][32];                              // the next 32 keys' scores arrive while these are worked
+    ld32_start(tS, u[0]);
+    tc_wait_ld_u32<32>(u[0]);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        if (q < 3) ld32_start(tS + 32u * (q + 1), u[(q + 1) & 1]);
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+            const uint32_t *x = u[q & 1] + e;
+            uint64_t x0 = pk(__uint_as_float(x[0]), __uint_as_float(x[1])), x1 = pk(__uint_as_float(x[2]), __uint_as_float(x[3]));
+            const int key = 32 * q + e;
+            if constexpr (Q8) {
+                const ulonglong2 k = *reinterpret_cast<const ulonglong2 *>(sc + key);
+                x0 = mul2(x0, k.x), x1 = mul2(x1, k.y);
+            }
+            float s0, s1, s2, s3;
+            unpk(fma2(x0, cs2, rf2), s0, s1);
+            unpk(fma2(x1, cs2, rf2), s2, s3);
+            s0 = ex2(s0), s1 = ex2(s1), s2 = ex2(s2), s3 = ex2(s3);
+            if constexpr (EDGE) {
+                s0 = key < left ? s0 : 0.f, s1 = key + 1 < left ? s1 : 0.f;
+                s2 = key + 2 < left ? s2 : 0.f, s3 = key + 3 < left ? s3 : 0.f;
+            }
+            x0 = pk(s0, s1), x1 = pk(s2, s3);
+            l2 = add2(l2, add2(x0, x1));
+            if constexpr (Q8) {
+                const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(sc + 128 + key);
+                unpk(mul2(x0, v.x), s0, s1);
+                unpk(mul2(x1, v.y), s2, s3);
+            }
+            t0 = fmaxf(t0, fmaxf(s0, s1)), t1 = fmaxf(t1, fmaxf(s2, s3));
+            out[key / 2] = Q8 ? pack_f16(s0, s1) : pack_bf16(s0, s1);
+            out[key / 2 + 1] = Q8 ? pack_f16(s2, s3) : pack_bf16(s2, s3);
+        }
+        if (q < 3) tc_wait_ld_u32<32>(u[(q + 1) & 1]);
+    }
+    float l0, l1;
+    unpk(l2, l0, l1);
+    sum = l0 + l1, top = fmaxf(t0, t1);
+}
+
+// One lane of a converged warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)::"memory");
+    return r != 0;
+}
+
 __device__ __forceinline__ void soft_sync() { named_sync(1, kWtSoft); }
 
 // Bounded wait; the flag ends all later ones at once.
@@ -154,7 +257,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) attn_prefix_tc_kernel(const Cac
     volatile int *bad = reinterpret_cast<volatile int *>(bars + 18);
     int *off = reinterpret_cast<int *>(sm + C::kOff);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 4), mbar_init(&q_full[i], 4), mbar_init(&o_done[i], 1);
@@ -205,150 +308,187 @@ __global__ void __launch_bounds__(kWtThreads, 1) attn_prefix_tc_kernel(const Cac
     const int P = a.max_len;
 
     if (warp >= 8 && warp < 12) {
-        // ---- K or V chunks into the operands' layout
-        const bool is_v = warp >= 10;
-        const int tid = (threadIdx.x - kWtSoft) & (kWtLoad - 1);
-        uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
-        uint8_t *tiles = sm + (is_v ? C::kV : C::kK);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWtRegsLoad));
+        // ---- K and V chunks into the operands' layout, 16 bytes of the cache a thread and turn
+        const int tid = threadIdx.x - kWtSoft;
         int kc = 0;                                 // chunks so far
         bool ok = true;
         while (w.next()) {
             const int hk = w.item / items.per_head();
-            const uint8_t *base = (is_v ? a.c.v : a.c.k) + hk * a.c.head;
+            const uint8_t *kb = a.c.k + hk * a.c.head, *vb = a.c.v + hk * a.c.head;
             if constexpr (Q8) {
-                constexpr int RPI = kWtLoad / 4, N = 128 / RPI * KB;   // four lanes a row of one 64-wide block
+                // this thread: piece j (16 codes) of rows r0, r0 + 32, .. of each 64-wide block
+                constexpr int N = 4 * KB;
                 const float *ks = a.c.ks + hk * a.c.shead, *vs = a.c.vs + hk * a.c.shead;
                 const int j = tid & 3, r0 = tid >> 2;
-                uint4 u[N];                         // the next chunk's codes
-                float s[2][2];                      // V's warps: K's and V's scales of keys tid and tid + 64
-                auto load = [&](int c) {
+                const int64_t hop = 32 * a.c.row;
+                kb += r0 * a.c.row + j * 16, vb += r0 * a.c.row + j * 16;
+                uint4 uk[N], uv[N];                 // the next chunk's codes
+                float sk, sv;                       // and scales, of key tid
+                auto load = [&](const uint8_t *base, int c, uint4 *to) {
+                    const uint8_t *at = base + (int64_t)c * kWideKeys * a.c.row;
+                    const int left = P - c * kWideKeys;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int k = 0; k < KB; ++k) {
+                            to[KB * i + k] = make_uint4(0, 0, 0, 0);
+                            if (r0 + 32 * i < left) to[KB * i + k] = __ldg(reinterpret_cast<const uint4 *>(at + i * hop + 64 * k));
+                        }
+                };
+                auto load_scales = [&](int c) {
+                    const int key = c * kWideKeys + tid;
+                    sk = key < P ? __ldg(ks + key) : 0.f, sv = key < P ? __ldg(vs + key) : 0.f;
+                };
+                const uint32_t put0 = swz(r0, 2 * j), put1 = swz(r0, 2 * j + 1);   // rows 32 apart swizzle alike
+                auto store = [&](uint8_t *tile, const uint4 *from) {
 #pragma unroll
                     for (int i = 0; i < N; ++i) {
-                        const int key = c * kWideKeys + r0 + (i / KB) * RPI;
-                        u[i] = make_uint4(0, 0, 0, 0);
-                        if (key < P) u[i] = __ldg(reinterpret_cast<const uint4 *>(base + (int64_t)key * a.c.row + (i % KB) * 64 + j * 16));
-                    }
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int key = c * kWideKeys + tid + i * kWtLoad;
-                        const bool live = is_v && key < P;
-                        s[i][0] = live ? __ldg(ks + key) : 0.f, s[i][1] = live ? __ldg(vs + key) : 0.f;
-                    }
-                };
-                load(w.c0);
-                for (int i = 0; i < w.n; ++i, ++kc) {
-                    const int st = kc & 1;
-                    if (kc >= 2) ok = ok && wt_wait(&empty[st], ((uint32_t)(kc >> 1) & 1u) ^ 1u, bad);
-                    uint8_t *tile = tiles + (uint32_t)(st * KB) * kWtBox;
-#pragma unroll
-                    for (int n = 0; n < N; ++n) {
-                        const int r = r0 + (n / KB) * RPI;
-                        const uint32_t x[4] = {u[n].x ^ 0x80808080u, u[n].y ^ 0x80808080u, u[n].z ^ 0x80808080u,
-                                               u[n].w ^ 0x80808080u};
+                        const uint32_t x[4] = {from[i].x ^ 0x80808080u, from[i].y ^ 0x80808080u, from[i].z ^ 0x80808080u,
+                                               from[i].w ^ 0x80808080u};
                         // eight lanes: two rows, whose swizzles differ in the last bit, and four even (odd) pieces
-                        uint8_t *box = tile + (n % KB) * kWtBox;
-                        *reinterpret_cast<uint4 *>(box + swz(r, 2 * j)) =
+                        uint8_t *box = tile + (i % KB) * kWtBox + (i / KB) * 32 * 128;
+                        *reinterpret_cast<uint4 *>(box + put0) =
                             make_uint4(codes_f16<false>(x[0], 0x4140), codes_f16<false>(x[0], 0x4342),
                                        codes_f16<false>(x[1], 0x4140), codes_f16<false>(x[1], 0x4342));
-                        *reinterpret_cast<uint4 *>(box + swz(r, 2 * j + 1)) =
+                        *reinterpret_cast<uint4 *>(box + put1) =
                             make_uint4(codes_f16<false>(x[2], 0x4140), codes_f16<false>(x[2], 0x4342),
                                        codes_f16<false>(x[3], 0x4140), codes_f16<false>(x[3], 0x4342));
                     }
-                    // the scales come with V, which is not given up before its softmax is done (K's tile is)
-                    if (is_v) {
-                        float *sc = reinterpret_cast<float *>(sm + C::kSc) + st * 384;
-#pragma unroll
-                        for (int n = 0; n < 2; ++n) {
-                            const int key = tid + n * kWtLoad;
-                            sc[key] = s[n][0], sc[128 + key] = s[n][1], sc[256 + key] = fmaxf(lg2(s[n][1]), -60.f);
-                        }
-                    }
-                    fence_proxy_async_smem();
-                    mbar_arrive(&full[st]);
-                    if (i + 1 < w.n) load(w.c0 + i + 1);
-                }
-            } else {
-                constexpr int PPR = D / 8, RPI = kWtLoad / PPR, N = 128 / RPI;
-                const int j = tid % PPR, r0 = tid / PPR;
+                };
+                load(kb, w.c0, uk);
+                load(vb, w.c0, uv);
+                load_scales(w.c0);
                 for (int i = 0; i < w.n; ++i, ++kc) {
                     const int st = kc & 1;
-                    if (kc >= 2) ok = ok && wt_wait(&empty[st], ((uint32_t)(kc >> 1) & 1u) ^ 1u, bad);
-                    const uint32_t box = smem_addr(tiles + (uint32_t)(st * KB) * kWtBox) + (uint32_t)(j >> 3) * kWtBox;
+                    const uint32_t was = ((uint32_t)(kc >> 1) & 1u) ^ 1u;
+                    if (kc >= 2) ok = ok && wt_wait(&k_empty[st], was, bad);
+                    store(sm + C::kK + (uint32_t)(st * KB) * kWtBox, uk);
+                    fence_proxy_async_smem();
+                    mbar_arrive(&k_full[st]);
+                    if (i + 1 < w.n) load(kb, w.c0 + i + 1, uk);
+                    if (kc >= 2) ok = ok && wt_wait(&v_empty[st], was, bad);
+                    store(sm + C::kV + (uint32_t)(st * KB) * kWtBox, uv);
+                    // the scales come with V, which is not given up before its softmax is done (K's tile is)
+                    float *sc = reinterpret_cast<float *>(sm + C::kSc) + st * 384;
+                    sc[tid] = sk, sc[128 + tid] = sv, sc[256 + tid] = fmaxf(lg2(sv), -60.f);
+                    fence_proxy_async_smem();
+                    mbar_arrive(&v_full[st]);
+                    if (i + 1 < w.n) {
+                        load(vb, w.c0 + i + 1, uv);
+                        load_scales(w.c0 + i + 1);
+                    }
+                }
+            } else {
+                // this thread: piece j (8 dims) of rows r0, r0 + RPI, ..
+                constexpr int PPR = 8 * KB, RPI = kWtLoad / PPR, N = 128 / RPI;
+                const int j = tid % PPR, r0 = tid / PPR;
+                const int64_t hop = RPI * a.c.row;
+                kb += r0 * a.c.row + j * 16, vb += r0 * a.c.row + j * 16;
+                auto copy = [&](const uint8_t *base, int c, uint8_t *tile) {
+                    const uint8_t *at = base + (int64_t)c * kWideKeys * a.c.row;
+                    const int left = P - c * kWideKeys;
+                    const uint32_t to = smem_addr(tile) + (uint32_t)(j >> 3) * kWtBox;
 #pragma unroll
                     for (int n = 0; n < N; ++n) {
-                        const int r = r0 + n * RPI, key = (w.c0 + i) * kWideKeys + r;
-                        const bool live = key < P;
-                        const uint8_t *src = base + (int64_t)(live ? key : 0) * a.c.row + j * 16;
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(box + swz(r, j & 7)), "l"(src),
-                                     "r"(live ? 16 : 0)
+                        const int r = r0 + n * RPI;
+                        const bool live = r < left;
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + swz(r, j & 7)),
+                                     "l"(live ? at + n * hop : a.c.k), "r"(live ? 16 : 0)
                                      : "memory");
                     }
-                    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+                };
+                for (int i = 0; i < w.n; ++i, ++kc) {
+                    const int st = kc & 1;
+                    const uint32_t was = ((uint32_t)(kc >> 1) & 1u) ^ 1u;
+                    if (kc >= 2) ok = ok && wt_wait(&k_empty[st], was, bad);
+                    copy(kb, w.c0 + i, sm + C::kK + (uint32_t)(st * KB) * kWtBox);
+                    if (kc >= 2) ok = ok && wt_wait(&v_empty[st], was, bad);
+                    copy(vb, w.c0 + i, sm + C::kV + (uint32_t)(st * KB) * kWtBox);
+                    asm volatile("cp.async.wait_group 1;" ::: "memory");
                     fence_proxy_async_smem();
-                    mbar_arrive(&full[st]);
+                    mbar_arrive(&k_full[st]);
+                    asm volatile("cp.async.wait_group 0;" ::: "memory");
+                    fence_proxy_async_smem();
+                    mbar_arrive(&v_full[st]);
                 }
             }
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
-    } else if (warp == 12) {
-        // ---- the MMAs: S of both halves, then always a half's O followed by its next S
-        if (lane == 0) {
-            constexpr uint32_t bf = Q8 ? 0u : (1u << 7) | (1u << 10);
-            constexpr uint32_t base = (1u << 4) | bf | ((uint32_t)(kWideRows >> 4) << 24);
-            constexpr uint32_t idesc_s = base | ((uint32_t)(kWideKeys >> 3) << 17);
-            constexpr uint32_t idesc_o = base | (1u << 16) | ((uint32_t)(D >> 3) << 17);
-            const uint32_t sQ = smem_addr(sm + C::kQ), sK = smem_addr(sm + C::kK), sV = smem_addr(sm + C::kV);
-            int kc = 0, seg = 0;
-            uint32_t np[2] = {0, 0};               // P's so far
-            bool ok = true;
-            for (; ok && w.next(); ++seg) {
-                const int N = pairs ? 2 * w.n : w.n;
-                ok = wt_wait(&q_full[0], (uint32_t)seg & 1u, bad) && (!pairs || wt_wait(&q_full[1], (uint32_t)seg & 1u, bad));
-                auto issue_s = [&](int i) {
-                    const int h = i & 1, c = kc + (pairs ? i >> 1 : i), st = c & 1;
-                    if (!pairs || !h) ok = ok && wt_wait(&k_full[st], (uint32_t)(c >> 1) & 1u, bad);
-                    if (!ok) return;
-                    tc_fence_after();
-                    const uint32_t d = tmem + kWtS + 128u * h, q = sQ + (uint32_t)(pairs ? h * KB : 0) * kWtBox;
-                    const uint32_t k = sK + (uint32_t)(st * KB) * kWtBox;
+    } else if (warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWtRegsMma));
+        if (warp == 12) {
+        // ---- the MMAs: S of both halves, then always a half's O followed by its next S.  The whole warp walks
+        // along, and one lane of its choosing issues (elect.sync always names the same): the operands then live in uniform
+        // registers.  A branch on lane 0 instead took 140 to 190 clocks for each MMA of 64.
+        constexpr uint32_t bf = Q8 ? 0u : (1u << 7) | (1u << 10);
+        constexpr uint32_t base = (1u << 4) | bf | ((uint32_t)(kWideRows >> 4) << 24);
+        constexpr uint32_t idesc_s = base | ((uint32_t)(kWideKeys >> 3) << 17);
+        constexpr uint32_t idesc_o = base | (1u << 16) | ((uint32_t)(D >> 3) << 17);
+        // descriptors of the first bytes; an offset of n bytes adds n / 16
+        const uint64_t dQ = sw128_desc(smem_addr(sm + C::kQ)), dK = sw128_desc(smem_addr(sm + C::kK));
+        const uint64_t dV = desc_mn(smem_addr(sm + C::kV), kWtBox, 1024u);
+        constexpr uint32_t kBox16 = kWtBox / 16;
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        int kc = 0, seg = 0;
+        uint32_t np[2] = {0, 0};                   // P's so far
+        bool ok = true;
+        for (; ok && w.next(); ++seg) {
+            const int N = pairs ? 2 * w.n : w.n;
+            ok = wt_wait(&q_full[0], (uint32_t)seg & 1u, bad) && (!pairs || wt_wait(&q_full[1], (uint32_t)seg & 1u, bad));
+            auto issue_s = [&](int i) {
+                const int h = i & 1, c = kc + (pairs ? i >> 1 : i), st = c & 1;
+                if (!pairs || !h) ok = ok && wt_wait(&k_full[st], (uint32_t)(c >> 1) & 1u, bad);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t d = tm + kWtS + 128u * h;
+                const uint64_t q = dQ + (pairs ? h * KB : 0) * kBox16, k = dK + st * KB * kBox16;
+                if (elect_one()) {
 #pragma unroll
                     for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
                         for (int s = 0; s < 4; ++s)
-                            tc_mma(d, sw128_desc(q + (uint32_t)kb * kWtBox + 32u * s),
-                                   sw128_desc(k + (uint32_t)kb * kWtBox + 32u * s), idesc_s, (kb | s) ? 1u : 0u);
+                            tc_mma(d, q + kb * kBox16 + 2 * s, k + kb * kBox16 + 2 * s, idesc_s, (kb | s) ? 1u : 0u);
                     tc_commit(&s_full[h]);
                     if (!pairs || h) tc_commit(&k_empty[st]);
-                };
-                auto issue_o = [&](int i) {
-                    const int h = i & 1, c = kc + (pairs ? i >> 1 : i), st = c & 1;
-                    ok = ok && wt_wait(&p_full[h], np[h] & 1u, bad);
-                    if (!pairs || !h) ok = ok && wt_wait(&v_full[st], (uint32_t)(c >> 1) & 1u, bad);
-                    if (!ok) return;
-                    ++np[h];
-                    tc_fence_after();
-                    const uint32_t d = tmem + kWtO + 128u * h, p = tmem + kWtS + 128u * h;
-                    const uint32_t v = sV + (uint32_t)(st * KB) * kWtBox;
+                }
+                __syncwarp();
+            };
+            auto issue_o = [&](int i) {
+                const int h = i & 1, c = kc + (pairs ? i >> 1 : i), st = c & 1;
+                ok = ok && wt_wait(&p_full[h], np[h] & 1u, bad);
+                if (!pairs || !h) ok = ok && wt_wait(&v_full[st], (uint32_t)(c >> 1) & 1u, bad);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) return;
+                ++np[h];
+                tc_fence_after();
+                const uint32_t d = tm + kWtO + 128u * h, p = tm + kWtS + 128u * h;
+                const uint64_t v = dV + st * KB * kBox16;
+                if (elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < kWideKeys / 16; ++ks)
-                        tc_mma_ts(d, p + 8u * ks, desc_mn(v + (uint32_t)ks * 2048u, kWtBox, 1024u), idesc_o,
-                                  (i >= 2 || ks) ? 1u : 0u);
+                        tc_mma_ts(d, p + 8u * ks, v + ks * 128, idesc_o, ks ? 1u : (i >= 2 ? 1u : 0u));
                     if (!pairs || h) tc_commit(&v_empty[st]);
                     if (i + 2 >= N) tc_commit(&o_done[h]);
-                };
-                for (int i = 0; ok && i < 2 && i < N; ++i) issue_s(i);
-                for (int i = 0; ok && i < N; ++i) {
-                    issue_o(i);
-                    if (i + 2 < N) issue_s(i + 2);
                 }
-                kc += w.n;
+                __syncwarp();
+            };
+            for (int i = 0; ok && i < 2 && i < N; ++i) issue_s(i);
+            for (int i = 0; ok && i < N; ++i) {
+                issue_o(i);
+                if (ok && i + 2 < N) issue_s(i + 2);
             }
-            // every MMA issued has completed before the tensor memory can be freed
-            tc_commit(drain);
-            (void)mbar_wait_bounded(drain, 0u, 20000000ull);
+            kc += w.n;
         }
+        // every MMA issued has completed before the tensor memory can be freed
+        if (elect_one()) tc_commit(drain);
+        (void)mbar_wait_bounded(drain, 0u, 20000000ull);
         __syncwarp();
+        }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWtRegsSoft));
         // ---- softmax: half h, row r of its tile
         const int h = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
@@ -417,7 +557,6 @@ __global__ void __launch_bounds__(kWtThreads, 1) attn_prefix_tc_kernel(const Cac
                 }
             }
             float ref = -INFINITY, l = 0.f;
-            const uint64_t cs2 = pk(cs, cs);
             const int N = pairs ? 2 * w.n : w.n;
             for (int i = h; i < N; i += 2) {
                 const int c = pairs ? i >> 1 : i, st = (kc + c) & 1;
@@ -427,109 +566,44 @@ __global__ void __launch_bounds__(kWtThreads, 1) attn_prefix_tc_kernel(const Cac
                 ++ns;
                 if constexpr (Q8) ok = ok && wt_wait(&v_full[st], (uint32_t)((kc + c) >> 1) & 1u, bad);
                 tc_fence_after();
-                // the chunk's largest score (with the values' scales: the largest weight), 64 keys at a time
-                float m = -INFINITY;
+                uint32_t pr[64];                    // the probabilities, packed
+                float top, sum;
+                const bool edge = left < kWideKeys;
+                // a half's first chunk sets the reference by its first 32 keys, which is near enough as a rule
+                for (int turn = i < 2 ? 0 : 1;; ++turn) {
+                    if (turn != 1) {
+                        const float m = largest<Q8>(tS, sc, cs, left, turn ? kWideKeys : 32);
+                        // this half's earlier O products are done: its next S, which came behind them, is
+                        float f = 1.f;
+                        if (m - kWtUp<Q8> > ref) {
+                            f = ref == -INFINITY ? 0.f : ex2(ref - (m - kWtUp<Q8>));
+                            ref = m - kWtUp<Q8>;
+                            l *= f;
+                        }
+                        if (i >= 2) {
 #pragma unroll 1
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t u[64];
-                    ld32_start(tS + 64u * q, u);
-                    ld32_start(tS + 64u * q + 32u, u + 32);
-                    tc_wait_ld_u32<64>(u);
-                    float m2 = -INFINITY;
+                            for (int q = 0; q < D / 32; ++q) {
+                                float v[32];
+                                uint32_t u[32];
+                                ld32(tO + 32u * q, v);
 #pragma unroll
-                    for (int e = 0; e < 64; e += 4) {
-                        float s0 = __uint_as_float(u[e]), s1 = __uint_as_float(u[e + 1]), s2 = __uint_as_float(u[e + 2]),
-                              s3 = __uint_as_float(u[e + 3]);
-                        if constexpr (Q8) {
-                            const ulonglong2 k = *reinterpret_cast<const ulonglong2 *>(sc + 64 * q + e);
-                            const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(sc + 256 + 64 * q + e);
-                            unpk(fma2(mul2(pk(s0, s1), k.x), cs2, v.x), s0, s1);
-                            unpk(fma2(mul2(pk(s2, s3), k.y), cs2, v.y), s2, s3);
-                        } else {
-                            unpk(mul2(pk(s0, s1), cs2), s0, s1);
-                            unpk(mul2(pk(s2, s3), cs2), s2, s3);
-                        }
-                        if (left < kWideKeys) {
-                            const int key = 64 * q + e;
-                            s0 = key < left ? s0 : -INFINITY, s1 = key + 1 < left ? s1 : -INFINITY;
-                            s2 = key + 2 < left ? s2 : -INFINITY, s3 = key + 3 < left ? s3 : -INFINITY;
-                        }
-                        m = fmaxf(m, fmaxf(s0, s1)), m2 = fmaxf(m2, fmaxf(s2, s3));
-                    }
-                    m = fmaxf(m, m2);
-                }
-                if (__any_sync(0xffffffffu, m > ref + kAcRoom)) {
-                    // this half's earlier O products are done: its next S, which came behind them, is
-                    float f = 1.f;
-                    if (m > ref + kAcRoom) {
-                        const float now = m - kAcUp;
-                        f = ref == -INFINITY ? 0.f : ex2(ref - now);
-                        ref = now;
-                        l *= f;
-                    }
-                    if (i >= 2) {
-#pragma unroll 1
-                        for (int q = 0; q < D / 32; ++q) {
-                            float v[32];
-                            uint32_t u[32];
-                            ld32(tO + 32u * q, v);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(v[e] * f);
-                            tc_st16(tO + 32u * q, u);
-                            tc_st16(tO + 32u * q + 16u, u + 16);
-                        }
-                    }
-                }
-                const float rf = ref == -INFINITY ? 0.f : ref;
-                const uint64_t rf2 = pk(-rf, -rf);
-                uint64_t l2 = pk(l, 0.f);
-                uint32_t u[2][32];                  // the next 32 keys' scores arrive while these are worked
-                ld32_start(tS, u[0]);
-                tc_wait_ld_u32<32>(u[0]);
-#pragma unroll 1
-                for (int q = 0; q < 4; q += 2) {
-#pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        const int key0 = 32 * (q + z);
-                        if (z == 0 || q == 0) ld32_start(tS + key0 + 32u, u[z ^ 1]);
-                        uint32_t o[16];
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            uint64_t x0 = pk(__uint_as_float(u[z][e]), __uint_as_float(u[z][e + 1]));
-                            uint64_t x1 = pk(__uint_as_float(u[z][e + 2]), __uint_as_float(u[z][e + 3]));
-                            if constexpr (Q8) {
-                                const ulonglong2 k = *reinterpret_cast<const ulonglong2 *>(sc + key0 + e);
-                                x0 = mul2(x0, k.x), x1 = mul2(x1, k.y);
+                                for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(v[e] * f);
+                                tc_st16(tO + 32u * q, u);
+                                tc_st16(tO + 32u * q + 16u, u + 16);
                             }
-                            float s0, s1, s2, s3;
-                            unpk(fma2(x0, cs2, rf2), s0, s1);
-                            unpk(fma2(x1, cs2, rf2), s2, s3);
-                            s0 = ex2(s0), s1 = ex2(s1), s2 = ex2(s2), s3 = ex2(s3);
-                            if (left < kWideKeys) {
-                                const int key = key0 + e;
-                                s0 = key < left ? s0 : 0.f, s1 = key + 1 < left ? s1 : 0.f;
-                                s2 = key + 2 < left ? s2 : 0.f, s3 = key + 3 < left ? s3 : 0.f;
-                            }
-                            x0 = pk(s0, s1), x1 = pk(s2, s3);
-                            l2 = add2(l2, add2(x0, x1));
-                            if constexpr (Q8) {
-                                const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(sc + 128 + key0 + e);
-                                unpk(mul2(x0, v.x), s0, s1);
-                                unpk(mul2(x1, v.y), s2, s3);
-                            }
-                            o[e / 2] = Q8 ? pack_f16(s0, s1) : pack_bf16(s0, s1);
-                            o[e / 2 + 1] = Q8 ? pack_f16(s2, s3) : pack_bf16(s2, s3);
                         }
-                        // these keys' columns lie in the first half of S's that have been read
-                        if (z == 0 || q == 0) tc_wait_ld_u32<32>(u[z ^ 1]);
-                        tc_st16(tS + key0 / 2, o);
                     }
+                    if (edge)
+                        weigh<Q8, true>(tS, sc, cs, ref, left, pr, top, sum);
+                    else
+                        weigh<Q8, false>(tS, sc, cs, ref, left, pr, top, sum);
+                    if (turn >= 2 || !__any_sync(0xffffffffu, top > kWtTop<Q8> || ref == -INFINITY)) break;
+                    if (turn == 0) turn = 1;         // next: the whole chunk's maximum
                 }
-                {
-                    float l0, l1;
-                    unpk(l2, l0, l1);
-                    l = l0 + l1;
-                }
+                l += sum;
+                // over the first half of the scores' columns, all of which have been read
+#pragma unroll
+                for (int q = 0; q < 4; ++q) tc_st16(tS + 16u * q, pr + 16 * q);
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
