@@ -599,3 +599,62 @@ def test_another_stream(qd):
     s.synchronize()
     want, mag, spread = ref.attend(q, k, v, [64, 9], [1, 1], 0.125, pk[0], pv[0])
     assert ((out.cpu().double() - want).abs() <= ref.attend_bound(want, mag, spread, 264, 64, torch.bfloat16, False)).all()
+
+
+def test_scratch_of_two_streams_and_of_a_capture(qd):
+    """Calls without a workspace at the same time on two streams, and a replayed capture beside them: each has memory
+    of its own, and the results stay bit for bit."""
+    g = gen(43)
+    B, P = 40, 900
+    dev, _ = _filled(g, B, 2, 300, 64, True)
+    pdev, _ = _filled(g, 1, 2, P, 64, True)
+    view, pre = qd.KvCache(*dev), qd.KvCache(*pdev)
+    ln = ints(torch.randint(1, 300, (B,), generator=g).tolist())
+    qs = [torch.randn((B, 1, 4, 64), generator=g).bfloat16().cuda() for _ in range(3)]
+    assert qd.qd_attn_cached_workspace(view, True, 1, 4, prefix=pre) > 0
+
+    def call(q, out):
+        qd.qd_attn_cached(q, view, ln, out, prefix=pre)
+    want = []
+    for q in qs:
+        o = torch.empty_like(q)
+        call(q, o)
+        want.append(o)
+    torch.cuda.synchronize()
+    outs = [torch.zeros_like(q) for q in qs]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(qs[2], outs[2])
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(30):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                call(qs[i], outs[i])
+        with torch.cuda.stream(streams[2]):
+            graph.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
+
+
+def test_two_host_threads_on_one_stream(qd):
+    import threading
+    g = gen(44)
+    dev, _ = _filled(g, 6, 2, 700, 64, False)
+    pdev, _ = _filled(g, 1, 2, 500, 64, False)
+    view, pre, ln = qd.KvCache(*dev), qd.KvCache(*pdev), ints([700, 1, 30, 444, 0, 64])
+    qs = [torch.randn((6, 1, 4, 64), generator=g).bfloat16().cuda() for _ in range(2)]
+    outs, want = [torch.zeros_like(q) for q in qs], [torch.zeros_like(q) for q in qs]
+    for q, o in zip(qs, want):
+        qd.qd_attn_cached(q, view, ln, o, prefix=pre)
+
+    def work(i):
+        for _ in range(200):
+            qd.qd_attn_cached(qs[i], view, ln, outs[i], prefix=pre)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])

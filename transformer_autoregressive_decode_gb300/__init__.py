@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 from typing import Dict, Optional, Sequence
 
 import numpy as np
@@ -651,45 +652,80 @@ class KvCache:
         self.c = qd_kv_cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), fmt, B, H, S, D,
                              st[0] if B > 1 else 0, st[1] if H > 1 else 0, row, ss[0] if B > 1 else 0,
                              ss[1] if H > 1 else 0)
+        self.format = fmt
         self.addr = ctypes.addressof(self.c)
+
+
+_torch = None
+
+
+def _T():
+    """torch, looked up once (the module itself imports without it)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
 
 
 def _op_stream(stream, t) -> int:
     """The caller's stream, by default the current one of t's device (memory of a device that is
     not the current one is refused by the call).  The raw handle: a Stream object costs 3 us."""
-    import torch
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(t.get_device()) if t.is_cuda else 0
+    return _T()._C._cuda_getCurrentRawStream(t.get_device()) if t.is_cuda else 0
 
 
 def _op_dtype(t) -> int:
-    import torch
-    if t.dtype == torch.bfloat16:
+    torch, d = _T(), t.dtype
+    if d is torch.bfloat16:
         return QD_BF16
-    if t.dtype == torch.float32:
+    if d is torch.float32:
         return QD_F32
-    raise ValueError(f"fp32 or bf16 wanted, got {t.dtype}")
+    raise ValueError(f"fp32 or bf16 wanted, got {d}")
 
 
 def _op_ints(t, n: int, what: str):
     """A contiguous int32 tensor of n values (or None) as an address."""
-    import torch
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
+    if t.dtype is not _T().int32 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{what} must be {n} contiguous int32 values")
     return t.data_ptr()
 
 
+# Scratch of the calls on torch's current stream outside of captures, one buffer per device and stream: they follow
+# one another there.  The lock keeps two host threads from interleaving their launches on one stream.  Larger needs,
+# streams passed in, and captures (whose replays may run beside anything) take fresh memory from torch's allocator.
+_scratch: Dict[tuple, "torch.Tensor"] = {}
+_scratch_lock = threading.Lock()
+_SCRATCH_MOST = 128 << 20
+
+
+def _fresh(need: int, t, stream):
+    torch = _T()
+    if stream is None:
+        return torch.empty(need, dtype=torch.uint8, device=t.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(need, dtype=torch.uint8, device=t.device)
+
+
+def _stream_scratch(need: int, t, raw: int):
+    """Under _scratch_lock: the current stream's buffer, grown to `need` bytes."""
+    key = (t.get_device(), raw)
+    buf = _scratch.get(key)
+    if buf is None or buf.numel() < need:
+        buf = _scratch[key] = _fresh(max(need, 1 << 20), t, None)
+    return buf
+
+
 def _kv_rows(fn, name, cache, k_rows, v_rows, lengths, n_new, stream):
     B, H, _, D = cache.shape
-    if k_rows.dim() != 4 or k_rows.shape != v_rows.shape or k_rows.stride() != v_rows.stride() or \
-            k_rows.dtype != v_rows.dtype or k_rows.shape[0] != B or tuple(k_rows.shape[2:]) != (H, D) or \
-            k_rows.stride(3) != 1:
+    shape, s = k_rows.shape, k_rows.stride()
+    if len(shape) != 4 or shape != v_rows.shape or s != v_rows.stride() or k_rows.dtype is not v_rows.dtype or \
+            shape[0] != B or shape[2] != H or shape[3] != D or s[3] != 1:
         raise ValueError(f"k_rows and v_rows must be alike: [{B}, tokens, {H}, {D}], heads contiguous")
-    T = k_rows.shape[1]
-    s = k_rows.stride()
+    T = shape[1]
     st = fn(cache.addr, k_rows.data_ptr(), v_rows.data_ptr(), _op_dtype(k_rows), T, s[0] if B > 1 else 0,
             s[1] if T > 1 else 0, s[2] if H > 1 else 0, _op_ints(lengths, B, "lengths"),
             _op_ints(n_new, B, "n_new"), _op_stream(stream, k_rows))
@@ -730,41 +766,44 @@ def qd_attn_cached(q, cache: KvCache, lengths, out, n_new=None, max_length: Opti
     each stream's cache and the shared prefix (a KvCache of one stream) into out (same type
     and shape).  max_length: bound of the lengths (default: the cache's positions); scale:
     default head_dim ** -0.5; prefix_length: default all of the prefix.  workspace: uint8
-    tensor of qd_attn_cached_workspace bytes, of this call alone while it runs; by default
-    one is taken from torch's allocator, on the stream that the call runs on."""
-    import torch
+    tensor of qd_attn_cached_workspace bytes, of this call alone while it runs; by default the
+    stream's own scratch (in a capture: fresh memory of the graph's)."""
     B, H, S, D = cache.shape
-    if q.dim() != 4 or q.shape != out.shape or q.dtype != out.dtype or q.shape[0] != B or q.shape[3] != D:
+    shape, qs, os_ = q.shape, q.stride(), out.stride()
+    if len(shape) != 4 or shape != out.shape or q.dtype is not out.dtype or shape[0] != B or shape[3] != D:
         raise ValueError(f"q and out must be [{B}, tokens, q_heads, {D}] of one type")
-    _, T, QH, _ = q.shape
-    qs, os_ = q.stride(), out.stride()
+    T, QH = shape[1], shape[2]
     if qs[3] != 1 or os_[3] != 1 or (QH > 1 and (qs[2] != D or os_[2] != D)):
         raise ValueError("the heads of q and out must be contiguous")
-    P = 0
+    P, pre = 0, None
     if prefix is not None:
         P = prefix.shape[2] if prefix_length is None else int(prefix_length)
         if prefix.shape[0] != 1:
             raise ValueError("the prefix is a cache of one stream")
+        pre = prefix.addr if P else None
     elif prefix_length:
         raise ValueError("prefix_length without a prefix")
     dt = _op_dtype(q)
     most = S if max_length is None else int(max_length)
-    if workspace is None:
-        key = (cache.shape, cache.c.format, P, P and prefix.c.format, dt, T, QH, most, q.get_device())
+    raw = _op_stream(stream, q)
+    args = (cache.addr, pre, P, q.data_ptr(), qs[0] if B > 1 else 0, qs[1] if T > 1 else 0, out.data_ptr(),
+            os_[0] if B > 1 else 0, os_[1] if T > 1 else 0, dt, T, QH, D ** -0.5 if scale is None else float(scale),
+            _op_ints(lengths, B, "lengths"), _op_ints(n_new, B, "n_new"), most)
+    if workspace is not None:
+        st = _lib.qd_attn_cached(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), raw)
+    else:
+        key = (cache.shape, cache.format, P, P and prefix.format, dt, T, QH, most, q.get_device())
         need = _attn_bytes.get(key)
         if need is None:
             need = _attn_bytes[key] = qd_attn_cached_workspace(cache, dt == QD_BF16, T, QH, most, prefix, P)
-        if need and stream is not None:
-            with torch.cuda.stream(stream):
-                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        elif need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    st = _lib.qd_attn_cached(cache.addr, prefix.addr if P > 0 else None, P, q.data_ptr(), qs[0] if B > 1 else 0,
-                             qs[1] if T > 1 else 0, out.data_ptr(), os_[0] if B > 1 else 0, os_[1] if T > 1 else 0,
-                             dt, T, QH, D ** -0.5 if scale is None else float(scale),
-                             _op_ints(lengths, B, "lengths"), _op_ints(n_new, B, "n_new"), most, _ptr(workspace),
-                             0 if workspace is None else workspace.numel() * workspace.element_size(),
-                             _op_stream(stream, q))
+        if not need:
+            st = _lib.qd_attn_cached(*args, None, 0, raw)
+        elif need > _SCRATCH_MOST or stream is not None or not q.is_cuda or _T()._C._cuda_isCurrentStreamCapturing():
+            ws = _fresh(need, q, stream)
+            st = _lib.qd_attn_cached(*args, ws.data_ptr(), need, raw)
+        else:
+            with _scratch_lock:
+                st = _lib.qd_attn_cached(*args, _stream_scratch(need, q, raw).data_ptr(), need, raw)
     if st != QD_OK:
         raise QDError(st, "qd_attn_cached failed")
 
@@ -774,20 +813,20 @@ def qd_verify_drafts(target_probs, draft_ids, u, out_ids, n_accepted, draft_prob
     vocab]) and the drafter's draft_probs (fp32 [streams, tokens, vocab], None: drafts that were
     not sampled) with the uniforms u (fp32 [streams, tokens + 1]) into out_ids (int32 [streams,
     tokens + 1]) and n_accepted (int32 [streams])."""
-    import torch
+    f32 = _T().float32
     B, T = draft_ids.shape
-    V = target_probs.shape[2]
-    if tuple(target_probs.shape) != (B, T + 1, V) or target_probs.dtype != torch.float32 or target_probs.stride(2) != 1:
+    ps, V = target_probs.stride(), target_probs.shape[2]
+    if target_probs.shape != (B, T + 1, V) or target_probs.dtype is not f32 or ps[2] != 1:
         raise ValueError(f"target_probs must be fp32 [{B}, {T + 1}, vocab], rows contiguous")
     qs = (0, 0)
     if draft_probs is not None:
-        if tuple(draft_probs.shape) != (B, T, V) or draft_probs.dtype != torch.float32 or draft_probs.stride(2) != 1:
+        qs = draft_probs.stride()
+        if draft_probs.shape != (B, T, V) or draft_probs.dtype is not f32 or qs[2] != 1:
             raise ValueError(f"draft_probs must be fp32 [{B}, {T}, {V}], rows contiguous")
-        qs = (draft_probs.stride(0) if B > 1 else 0, draft_probs.stride(1) if T > 1 else 0)
-    if u.dtype != torch.float32 or tuple(u.shape) != (B, T + 1) or not u.is_contiguous():
+    if u.dtype is not f32 or u.shape != (B, T + 1) or not u.is_contiguous():
         raise ValueError(f"u must be contiguous fp32 [{B}, {T + 1}]")
-    st = _lib.qd_verify_drafts(target_probs.data_ptr(), target_probs.stride(0) if B > 1 else 0, target_probs.stride(1),
-                               _ptr(draft_probs), qs[0], qs[1], _op_ints(draft_ids, B * T, "draft_ids"),
+    st = _lib.qd_verify_drafts(target_probs.data_ptr(), ps[0] if B > 1 else 0, ps[1], _ptr(draft_probs),
+                               qs[0] if B > 1 else 0, qs[1] if T > 1 else 0, _op_ints(draft_ids, B * T, "draft_ids"),
                                _op_ints(n_draft, B, "n_draft"), u.data_ptr(), B, T, V,
                                _op_ints(out_ids, B * (T + 1), "out_ids"), _op_ints(n_accepted, B, "n_accepted"),
                                _op_stream(stream, target_probs))

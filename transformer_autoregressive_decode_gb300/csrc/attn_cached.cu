@@ -1028,9 +1028,9 @@ cudaError_t dispatch(int kind, bool q8, bool f32, int d, int nt, const CachedArg
 }
 
 cudaError_t launch_join(bool f32, int d, const CachedArgs &a, int rw, int tp, unsigned warps, bool many, int sms, cudaStream_t s) {
-    // a warp's turn or two per CTA: rows enough to fill the SMs, the stream's place worked out seldom
+    // about two CTAs per SM: the stream's place is worked out once for several turns
     const int wpr = many ? kJoinWarps : 1, turns = (a.kvh * a.rows * wpr + kJoinWarps - 1) / kJoinWarps;
-    const dim3 grid((unsigned)a.B, (unsigned)std::min({turns, std::max(1, 8 * sms / a.B), 65535}));
+    const dim3 grid((unsigned)a.B, (unsigned)std::min({turns, std::max(1, 2 * sms / a.B), 65535}));
 #define QD_JOIN(F, DD, W) \
     if (f32 == F && d == DD && wpr == W) return launch_ex(attn_join_kernel<F, DD, W>, grid, kJoinWarps * 32, 0, 1, s, a, rw, tp, warps);
     QD_JOIN(false, 64, 1) QD_JOIN(false, 128, 1) QD_JOIN(true, 64, 1) QD_JOIN(true, 128, 1)
