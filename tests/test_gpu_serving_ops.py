@@ -218,6 +218,15 @@ def test_many_rows_over_a_prefix(qd, q8, D, B, T, G, P):
         _check(qd, B, T, G, 2, D, 20, lengths, None, q8, torch.bfloat16, P=P, p8=q8, seed=P + 1, q_scale=4.0)
 
 
+@pytest.mark.parametrize("q8,dtype,B,T,G,P", [(True, torch.float32, 24, 4, 2, 3000), (False, torch.float32, 9, 3, 3, 4100),
+                                             (False, torch.bfloat16, 5, 1, 3, 30000), (True, torch.bfloat16, 22, 1, 2, 3500)])
+def test_prefix_in_a_pass_of_its_own(qd, q8, dtype, B, T, G, P):
+    """Too long for every stream to read, and too few or too exact rows for the tcgen05 cores."""
+    g = gen(P)
+    lengths = torch.randint(0, 40, (B,), generator=g).tolist()
+    _check(qd, B, T, G, 2, 64, 40, lengths, [min(T, n) for n in lengths], q8, dtype, P=P, p8=q8, seed=P)
+
+
 def test_no_rows_in_use_over_a_prefix(qd):
     _check(qd, 30, 2, 2, 2, 128, 20, [0] * 30, [0] * 30, True, torch.bfloat16, P=300, p8=True)
     _check(qd, 30, 2, 2, 2, 128, 20, [3] * 30, [0] * 29 + [1], False, torch.bfloat16, P=300, p8=False)
@@ -499,7 +508,8 @@ def test_refusals(qd):
     assert status(lambda: qd.qd_attn_cached(many, view, ln, many.clone())) == qd.QD_EUNSUPPORTED
     three = torch.zeros((2, 1, 3, 64), dtype=torch.bfloat16, device="cuda")
     assert status(lambda: qd.qd_attn_cached(three, view, ln, three.clone())) == qd.QD_EINVAL    # 3 heads over 2
-    pre = qd.KvCache(k[:1], k[:1].clone(), s[:1], s[:1].clone())
+    b = torch.zeros((1, 2, 32, 64), dtype=torch.bfloat16, device="cuda")
+    pre = qd.KvCache(b, b.clone())                                # another format: a pass of its own
     small = torch.empty(64, dtype=torch.uint8, device="cuda")
     assert status(lambda: qd.qd_attn_cached(q, view, ln, out, prefix=pre, workspace=small)) == qd.QD_EINVAL
     assert status(lambda: qd.qd_attn_cached(q, view, ln, out, prefix=pre, prefix_length=33,
@@ -605,7 +615,7 @@ def test_scratch_of_two_streams_and_of_a_capture(qd):
     """Calls without a workspace at the same time on two streams, and a replayed capture beside them: each has memory
     of its own, and the results stay bit for bit."""
     g = gen(43)
-    B, P = 40, 900
+    B, P = 40, 4000
     dev, _ = _filled(g, B, 2, 300, 64, True)
     pdev, _ = _filled(g, 1, 2, P, 64, True)
     view, pre = qd.KvCache(*dev), qd.KvCache(*pdev)
@@ -641,8 +651,9 @@ def test_two_host_threads_on_one_stream(qd):
     import threading
     g = gen(44)
     dev, _ = _filled(g, 6, 2, 700, 64, False)
-    pdev, _ = _filled(g, 1, 2, 500, 64, False)
+    pdev, _ = _filled(g, 1, 2, 30000, 64, False)
     view, pre, ln = qd.KvCache(*dev), qd.KvCache(*pdev), ints([700, 1, 30, 444, 0, 64])
+    assert qd.qd_attn_cached_workspace(view, True, 1, 4, prefix=pre) > 0
     qs = [torch.randn((6, 1, 4, 64), generator=g).bfloat16().cuda() for _ in range(2)]
     outs, want = [torch.zeros_like(q) for q in qs], [torch.zeros_like(q) for q in qs]
     for q, o in zip(qs, want):

@@ -175,15 +175,15 @@ template <bool Q8, bool F32, int D, int NT, bool PREFIX> struct WarpPass {
         kp += hop, vp += hop;
     }
 
-    // the item's tiles first, first + step, ... below end: the first copies start here
-    __device__ __forceinline__ void start(const CachedArgs &a, int b, int hk, int len, uint8_t *ring_, int first, int end_,
+    // tiles first, first + step, ... below end of `len` positions of one stream and head: the first copies start here
+    __device__ __forceinline__ void start(const KvView &v, int b, int hk, int len, uint8_t *ring_, int first, int end_,
                                           int step_) {
         const int at = lane / (32 / K::CR), c = lane % (32 / K::CR);
-        kb = a.c.k + (PREFIX ? 0 : b * a.c.stream) + hk * a.c.head + c * 16;
-        vb = a.c.v + (PREFIX ? 0 : b * a.c.stream) + hk * a.c.head + c * 16;
-        ksb = Q8 ? a.c.ks + (PREFIX ? 0 : b * a.c.sstream) + hk * a.c.shead : nullptr;
-        vsb = Q8 ? a.c.vs + (PREFIX ? 0 : b * a.c.sstream) + hk * a.c.shead : nullptr;
-        row = a.c.row;
+        kb = v.k + b * v.stream + hk * v.head + c * 16;
+        vb = v.v + b * v.stream + hk * v.head + c * 16;
+        ksb = Q8 ? v.ks + b * v.sstream + hk * v.shead : nullptr;
+        vsb = Q8 ? v.vs + b * v.sstream + hk * v.shead : nullptr;
+        row = v.row;
         n_pos = len;
         ring = ring_;
         ring_s = smem_addr(ring_);
@@ -191,7 +191,7 @@ template <bool Q8, bool F32, int D, int NT, bool PREFIX> struct WarpPass {
         kp = kb + ((int64_t)first * K::TP + at) * row;
         vp = vb + ((int64_t)first * K::TP + at) * row;
         hop = (int64_t)step * K::TP * row;
-#pragma unroll
+#pragma unroll 1
         for (int s = 0; s < K::kStages - 1; ++s) {
             if (next < end) fetch(s);
             cp_commit();
@@ -297,6 +297,15 @@ template <bool Q8, bool F32, int D, int NT, bool PREFIX> struct WarpPass {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int k = 0; k < HC; ++k) ref[nt][k] = -INFINITY, l[nt][k] = 0.f;
+    }
+
+    // every row sees all `len` positions of the run that follows
+    __device__ __forceinline__ void see_all(int len) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < HC; ++k) lim[nt][k] = len;
+        lim_lo = lim_hi = len;
     }
 
     __device__ __forceinline__ void run() {
@@ -578,10 +587,10 @@ template <bool Q8, bool F32, int D, int NT, bool PREFIX> struct WarpPass {
     }
 };
 
-// A stream's tiles of tp positions (a power of two): none where it has no new token.
+// A stream's tiles of tp positions (a power of two), its own and then those of a short prefix: none where it has no new token.
 __device__ __forceinline__ int tiles_of(const CachedArgs &a, int b, int tp) {
     const int len = clamp_len(__ldg(a.lengths + b), a.max_len);
-    return clamp_new(a, b) > 0 ? (int)((unsigned)(len + tp - 1) / (unsigned)tp) : 0;
+    return clamp_new(a, b) > 0 ? (int)((unsigned)(len + tp - 1) / (unsigned)tp) + a.pre_tiles : 0;
 }
 
 template <bool F32> __device__ __forceinline__ void store4(uint8_t *dst, float4 v, float by) {
@@ -615,10 +624,24 @@ __global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NT>::kMinCtas)
 
     WarpPass<Q8, F32, D, NT, PREFIX> w;
     w.init(lane);
-    w.start(a, b, hk, len, sm + warp * K::kRing, split * kAcWarps + warp,
-            PREFIX || nn > 0 ? (len + K::TP - 1) / K::TP : 0, nsplit * kAcWarps);
-    w.load_rows(a, b, hk, r0, len, nn);
-    w.run();
+    {
+        const int own = (len + K::TP - 1) / K::TP, step = nsplit * kAcWarps, total = nn > 0 ? own + (PREFIX ? 0 : a.pre_tiles) : 0;
+        int tile = split * kAcWarps + warp;
+        bool first = true;
+        do {                                         // the stream's own tiles, then a short prefix's
+            const bool pre = !PREFIX && tile >= own && tile < total;
+            if (pre)
+                w.start(a.pc, 0, hk, a.pre_len, sm + warp * K::kRing, tile - own, a.pre_tiles, step);
+            else
+                w.start(a.c, b, hk, len, sm + warp * K::kRing, tile, min(own, total), step);
+            if (first) w.load_rows(a, b, hk, r0, len, nn);
+            if (pre) w.see_all(a.pre_len);
+            w.run();
+            first = false;
+            const int end = pre ? total : min(own, total);
+            if (tile < end) tile += (end - tile + step - 1) / step * step;
+        } while (tile < total);
+    }
     __syncthreads();
 
     // ---- the warps' partials
@@ -781,9 +804,18 @@ __global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NT>::kMinCtas)
         const int n = (int)min(tiles - tile0, x1 - x);
         const int hk = in / a.groups, grp = in - hk * a.groups;
         const int len = clamp_len(__ldg(a.lengths + b), a.max_len);
-        w.start(a, b, hk, len, sm + warp * K::kRing, tile0, tile0 + n, 1);
-        w.load_rows(a, b, hk, grp * K::RW, len, clamp_new(a, b));
-        w.run();
+        const int own = (int)tiles - a.pre_tiles;
+        for (int t = tile0; t < tile0 + n;) {        // its own tiles, then a short prefix's
+            const int end = t < own ? min(own, tile0 + n) : tile0 + n;
+            if (t < own)
+                w.start(a.c, b, hk, len, sm + warp * K::kRing, t, end, 1);
+            else
+                w.start(a.pc, 0, hk, a.pre_len, sm + warp * K::kRing, t - own, end - own, 1);
+            if (t == tile0) w.load_rows(a, b, hk, grp * K::RW, len, clamp_new(a, b));
+            if (t >= own) w.see_all(a.pre_len);
+            w.run();
+            t = end;
+        }
         __syncwarp();
         const int64_t slot = (int64_t)b * per + in + wid;   // x only grows: so does the pair
 #pragma unroll
@@ -1007,11 +1039,13 @@ cudaError_t launch(int kind, const CachedArgs &a, unsigned *ctas, int nsplit, in
     return launch_ex(fn, *ctas, kAcThreads, K::kSmem, (unsigned)nsplit, s, a, nsplit);
 }
 
+// Up to here (tiles that the streams would read between them) a prefix is read by every stream's own pass: a launch and
+// a pipeline's start less, where its positions cost little (64 streams, one token each, 8-bit: 1024 positions, 16384 tiles, 24 us
+// against 32 on the tcgen05 cores; 2048, 32768 tiles, 37 against 33; bf16: 512, 16384 tiles, 24 against 32).
+constexpr int64_t kInlineTiles = 20000;
+
 // Rows from which the prefix goes to the tcgen05 cores.
-#ifndef QD_WF
-#define QD_WF 48
-#endif
-constexpr int kWideFrom = QD_WF;
+constexpr int kWideFrom = 48;
 
 constexpr int tile_positions(bool q8, int d) { return q8 || d == 64 ? 32 : 16; }   // AcCfg::TP
 constexpr int rows_per_tile(bool q8, bool f32) { return 8 / (q8 ? (f32 ? 2 : 1) : (f32 ? 4 : 2)); }
@@ -1045,7 +1079,8 @@ struct Plan {
     int nsplit;                         // CTAs of a cluster (one cluster per item); 0: shared out
     unsigned ctas;                      // of the shared-out pass
     int64_t rows_all;
-    int p_nt, p_rw, p_groups, splits;   // the prefix, a few rows at a time
+    bool inline_prefix;                 // a short prefix: every stream's own pass reads it
+    int p_nt, p_rw, p_groups, splits;   // else a few rows of the batch at a time
     int wide;                           // or its CTAs on the tcgen05 cores
     size_t p_ml, p_o, s_ml, s_o, bytes; // workspace offsets
 };
@@ -1063,15 +1098,25 @@ qd_status make_plan(const qd_kv_cache *cache, const qd_kv_cache *prefix, int pre
     p->nt = rows > per ? 2 : 1, p->rw = per * p->nt, p->groups = (rows + p->rw - 1) / p->rw;
     const int64_t items = (int64_t)B * kvh * p->groups;
     p->tp = tile_positions(q8, d);
-    const int tiles = (max_length + p->tp - 1) / p->tp;
+    int tiles = (max_length + p->tp - 1) / p->tp;
+    if (prefix && prefix_length > 0 && prefix->format == cache->format) {
+        const int64_t pre = (prefix_length + p->tp - 1) / p->tp;
+        const int64_t own = items * pre;
+        if (f32 || p->rows_all < kWideFrom)
+            p->inline_prefix = own <= (p->rows_all + p->rw - 1) / p->rw * kvh * pre + kInlineTiles;
+        else
+            p->inline_prefix = own <= kInlineTiles;
+        if (p->inline_prefix) tiles += (int)pre;
+    }
     if (items * tiles > (1ll << 31)) return QD_EUNSUPPORTED;
-    // A cluster per item while the grid is one wave and a warp's share short; longer or larger
-    // batches are shared out.
+    // A cluster per item while the grid is one wave, or little more, and a warp's share short; longer or larger batches are
+    // shared out.  (72 items, a short prefix: 576 CTAs 13.8 us, 288 10.2; 592 items of one CTA 14.6 us, shared out 18.)
+    const int wave = (!q8 && d == 128 ? 2 : 3) * sms;
     p->nsplit = 1;
-    while (p->nsplit < kAcMaxCluster && items * p->nsplit < 2 * sms && tiles > p->nsplit * kAcWarps) p->nsplit *= 2;
-    if (items * p->nsplit > 4 * sms || tiles > 4 * p->nsplit * kAcWarps) p->nsplit = 0;
+    while (p->nsplit < kAcMaxCluster && items * p->nsplit * 2 <= wave && tiles > p->nsplit * kAcWarps) p->nsplit *= 2;
+    if (items * p->nsplit > wave + wave / 3 || tiles > 8 * p->nsplit * kAcWarps) p->nsplit = 0;
     size_t at = 0;
-    if (prefix && prefix_length > 0) {
+    if (prefix && prefix_length > 0 && !p->inline_prefix) {
         const bool pq8 = prefix->format == QD_KV_Q8;
         if (!f32 && p->rows_all >= kWideFrom) {
             p->wide = sms, p->nsplit = 0;
@@ -1182,7 +1227,10 @@ qd_status qd_attn_cached(const qd_kv_cache *cache, const qd_kv_cache *prefix, in
     a.lengths = lengths_dev, a.n_new = n_new_dev;
     a.B = B, a.T = n_tokens, a.G = n_q_heads / kvh, a.kvh = kvh;
     a.scale2 = scale * 1.4426950408889634f;
-    if (with_prefix) {
+    if (p.inline_prefix) {
+        a.pc = kv_view(prefix);
+        a.pre_len = prefix_length, a.pre_tiles = (prefix_length + p.tp - 1) / p.tp;
+    } else if (with_prefix) {
         a.p_ml = reinterpret_cast<float2 *>(ws + p.p_ml), a.p_o = reinterpret_cast<float *>(ws + p.p_o);
         a.splits = p.splits;
         if (p.wide) a.wide = p.wide, a.wide_chunks = (prefix_length + kWideKeys - 1) / kWideKeys;

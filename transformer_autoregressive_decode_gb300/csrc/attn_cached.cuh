@@ -18,6 +18,9 @@ struct CachedArgs {
     int B, T, G, kvh, groups, max_len;
     int rows;                                       // rows of an item: T G, of the prefix B T G
     float scale2;                                   // softmax scale times log2(e)
+    // a short prefix is read by every stream's own pass, behind its cache: its view, positions and tiles
+    KvView pc;
+    int pre_len, pre_tiles;
     // partials over the prefix: [kvh][B T G][splits]
     float2 *p_ml;
     float *p_o;
