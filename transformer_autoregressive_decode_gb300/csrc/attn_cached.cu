@@ -840,8 +840,11 @@ __global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NT>::kMinCtas)
 // and from the prefix, weighted to a common reference, added in the order of the list.  blockIdx.x: the stream, whose
 // place in the lists a warp works out once; blockIdx.y: its share of the stream's rows in use.
 constexpr int kJoinWarps = 8;
-template <bool F32, int D, int WPR>
-__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const CachedArgs a, int rw, int tp, unsigned warps) {
+// WPR 8: few rows of many partials.  WPR 1: a warp a row, BATCH partials in flight: 8 where the rows are few and the time is a
+// chain of loads, 4 (half the registers, four CTAs an SM) where they are many.  (64 x 16 rows: 34.2 us a call against 36;
+// 96 x 4 x 32: 143 against 137.)
+template <bool F32, int D, int WPR, int BATCH>
+__global__ void __launch_bounds__(kJoinWarps * 32, BATCH == 8 ? 2 : 4) attn_join_kernel(const CachedArgs a, int rw, int tp, unsigned warps) {
     __shared__ float4 s_acc[kJoinWarps][32];
     __shared__ float2 s_ml[kJoinWarps];
     constexpr int LPR = D / 4;                      // lanes of a row's float4s
@@ -888,7 +891,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const Cached
 
     // 32 / LPR partials at a time (one for head_dim 128), LPR lanes each; kBatch of those are loaded
     // together, (ref, sum) with their rows, then weighted to the running reference
-    constexpr int kBatch = 8, kStep = WPR * (32 / LPR);
+    constexpr int kBatch = BATCH, kStep = WPR * (32 / LPR);
     const int d = (lane % LPR) * 4;
     float M = -INFINITY, sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1062,13 +1065,16 @@ cudaError_t dispatch(int kind, bool q8, bool f32, int d, int nt, const CachedArg
 }
 
 cudaError_t launch_join(bool f32, int d, const CachedArgs &a, int rw, int tp, unsigned warps, bool many, int sms, cudaStream_t s) {
-    // about two CTAs per SM: the stream's place is worked out once for several turns
+    // about eight CTAs per SM, two waves: the stream's place is worked out once for a few turns
     const int wpr = many ? kJoinWarps : 1, turns = (a.kvh * a.rows * wpr + kJoinWarps - 1) / kJoinWarps;
-    const dim3 grid((unsigned)a.B, (unsigned)std::min({turns, std::max(1, 2 * sms / a.B), 65535}));
-#define QD_JOIN(F, DD, W) \
-    if (f32 == F && d == DD && wpr == W) return launch_ex(attn_join_kernel<F, DD, W>, grid, kJoinWarps * 32, 0, 1, s, a, rw, tp, warps);
-    QD_JOIN(false, 64, 1) QD_JOIN(false, 128, 1) QD_JOIN(true, 64, 1) QD_JOIN(true, 128, 1)
-    QD_JOIN(false, 64, kJoinWarps) QD_JOIN(false, 128, kJoinWarps) QD_JOIN(true, 64, kJoinWarps) QD_JOIN(true, 128, kJoinWarps)
+    const dim3 grid((unsigned)a.B, (unsigned)std::min({turns, std::max(1, 8 * sms / a.B), 65535}));
+    const int batch = many || (int64_t)a.B * a.kvh * a.rows <= 4096 ? 8 : 4;
+#define QD_JOIN(F, DD, W, N) \
+    if (f32 == F && d == DD && wpr == W && batch == N) \
+        return launch_ex(attn_join_kernel<F, DD, W, N>, grid, kJoinWarps * 32, 0, 1, s, a, rw, tp, warps);
+#define QD_JOIN2(F, DD) QD_JOIN(F, DD, 1, 4) QD_JOIN(F, DD, 1, 8) QD_JOIN(F, DD, kJoinWarps, 8)
+    QD_JOIN2(false, 64) QD_JOIN2(false, 128) QD_JOIN2(true, 64) QD_JOIN2(true, 128)
+#undef QD_JOIN2
 #undef QD_JOIN
     return cudaErrorInvalidValue;
 }

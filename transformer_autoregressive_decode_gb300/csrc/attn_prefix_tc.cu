@@ -274,9 +274,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) attn_prefix_tc_kernel(const Cac
     }
     pdl_wait();
     pdl_launch_dependents();
-    // rows in use, and where each stream's begin
-    int rows;
-    (void)wide_rows(a, 0, &rows);
+    // where each stream's rows in use begin, and how many there are
     const bool gaps = a.n_new && a.B <= kWideMaxStreams;
     if (gaps && warp == 0) {
         int sum = 0;
@@ -297,6 +295,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) attn_prefix_tc_kernel(const Cac
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    const int rows = gaps ? off[a.B] : a.B * a.T * a.G;
 
     const WideItems items(rows);
     const bool pairs = items.pairs > 0;
@@ -500,57 +499,61 @@ __global__ void __launch_bounds__(kWtThreads, 1) attn_prefix_tc_kernel(const Cac
             const int per = items.per_head(), hk = w.item / per, tile = pairs ? 2 * (w.item - hk * per) + h : 0;
             const int row = tile * kWideRows + r;
             // the row's query: compact row -> stream, token, head
+            const uint8_t *src = nullptr;
+            if (row < rows) {
+                int b, in;
+                if (gaps) {
+                    int lo = 0, hi = a.B;           // off[lo] <= row < off[hi]
+                    while (hi - lo > 1) {
+                        const int mid = (lo + hi) >> 1;
+                        if (off[mid] <= row)
+                            lo = mid;
+                        else
+                            hi = mid;
+                    }
+                    b = lo, in = row - off[lo];
+                } else {
+                    b = row / (a.T * a.G), in = row - b * (a.T * a.G);
+                }
+                const int tt = in / a.G, g = in - tt * a.G;
+                src = a.q + b * a.q_stream + tt * a.q_token + (int64_t)(hk * a.G + g) * D * 2;
+            }
+            // the warp's 32 rows, D / 8 lanes a row: whole lines, where a row a thread took a line for every 16 bytes
             float cs = a.scale2;
             {
-                uint4 u[D / 8];
+                constexpr int LPR = D / 8, RPI = 32 / LPR, N = LPR;   // lanes a row, rows a turn, turns
+                const int j = lane % LPR, in = lane / LPR;
+                uint4 u[N];
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) u[i] = make_uint4(0, 0, 0, 0);
-                if (row < rows) {
-                    int b, in;
-                    if (gaps) {
-                        int lo = 0, hi = a.B;       // off[lo] <= row < off[hi]
-                        while (hi - lo > 1) {
-                            const int mid = (lo + hi) >> 1;
-                            if (off[mid] <= row)
-                                lo = mid;
-                            else
-                                hi = mid;
-                        }
-                        b = lo, in = row - off[lo];
-                    } else {
-                        b = row / (a.T * a.G), in = row - b * (a.T * a.G);
-                    }
-                    const int tt = in / a.G, g = in - tt * a.G;
-                    const uint4 *src = reinterpret_cast<const uint4 *>(a.q + b * a.q_stream + tt * a.q_token +
-                                                                       (int64_t)(hk * a.G + g) * D * 2);
-#pragma unroll
-                    for (int i = 0; i < D / 8; ++i) u[i] = __ldg(src + i);
+                for (int i = 0; i < N; ++i) {
+                    const uint64_t at = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(src), RPI * i + in);
+                    u[i] = make_uint4(0, 0, 0, 0);
+                    if (at) u[i] = __ldg(reinterpret_cast<const uint4 *>(at) + j);
                 }
-                if constexpr (Q8) {
-                    // fp16, scaled by a power of two: the row's largest value to [2^14, 2^15)
-                    uint32_t m = 0;
+                uint8_t *q = sm + C::kQ + (uint32_t)((pairs ? h : 0) * KB + (j >> 3)) * kWtBox;
 #pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
-                        const uint32_t x = __vmaxu2(__vmaxu2(u[i].x & 0x7fff7fffu, u[i].y & 0x7fff7fffu),
-                                                    __vmaxu2(u[i].z & 0x7fff7fffu, u[i].w & 0x7fff7fffu));
-                        m = __vmaxu2(m, x);
-                    }
-                    m = max(m >> 16, m & 0xffffu) >> 7;             // the exponent
-                    const int up = min(268 - (int)m, 253);
-                    const float f = __uint_as_float((uint32_t)up << 23);
-                    cs *= __uint_as_float((uint32_t)(254 - up) << 23);
+                for (int i = 0; i < N; ++i) {
+                    const int rr = RPI * i + in;
+                    if constexpr (Q8) {
+                        // fp16, scaled by a power of two: the row's largest value to [2^14, 2^15)
+                        uint32_t m = __vmaxu2(__vmaxu2(u[i].x & 0x7fff7fffu, u[i].y & 0x7fff7fffu),
+                                              __vmaxu2(u[i].z & 0x7fff7fffu, u[i].w & 0x7fff7fffu));
+                        m = max(m >> 16, m & 0xffffu);
 #pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
+                        for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+                        const int up = min(268 - (int)(m >> 7), 253);   // from the exponent
+                        const float f = __uint_as_float((uint32_t)up << 23);
+                        // the row's own thread takes the inverse into its factor
+                        const int mine = __shfl_sync(0xffffffffu, up, (lane % RPI) * LPR);
+                        if (lane / RPI == i) cs = a.scale2 * __uint_as_float((uint32_t)(254 - mine) << 23);
                         u[i].x = pack_f16(bf16lo(u[i].x) * f, bf16hi(u[i].x) * f);
                         u[i].y = pack_f16(bf16lo(u[i].y) * f, bf16hi(u[i].y) * f);
                         u[i].z = pack_f16(bf16lo(u[i].z) * f, bf16hi(u[i].z) * f);
                         u[i].w = pack_f16(bf16lo(u[i].w) * f, bf16hi(u[i].w) * f);
                     }
+                    if (pairs || h == 0) *reinterpret_cast<uint4 *>(q + swz(quarter * 32 + rr, j & 7)) = u[i];
                 }
                 if (pairs || h == 0) {
-                    uint8_t *q = sm + C::kQ + (uint32_t)(h * KB) * kWtBox;
-#pragma unroll
-                    for (int i = 0; i < D / 8; ++i) *reinterpret_cast<uint4 *>(q + (uint32_t)(i >> 3) * kWtBox + swz(r, i & 7)) = u[i];
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&q_full[h]);
@@ -619,17 +622,34 @@ __global__ void __launch_bounds__(kWtThreads, 1) attn_prefix_tc_kernel(const Cac
             tc_fence_after();
             const float fail = ok && !*bad ? 0.f : __uint_as_float(0x7fc00000u);
             if (row < rows) a.p_ml[rec * kWideRows + r] = make_float2(ref, l + fail);
-            float *dst = a.p_o + (rec * kWideRows + r) * D;
+            // O by way of shared memory, so that the stores are whole lines: D / 4 columns of the warp's rows at a time, over Q
+            // (this half's own, all of whose products are done; with one tile for both halves, the unused second)
             if (steps > 0) {
+                constexpr int CW = D / 4, PC = CW / 4;   // columns a turn, 16-byte pieces of them
+                uint8_t *stage = sm + C::kQ + (pairs ? (uint32_t)(h * KB) * kWtBox : (uint32_t)KB * kWtBox + h * (32u * D * 4)) +
+                                 quarter * (8u * D * 4);
+                float *dst = a.p_o + (rec * kWideRows + quarter * 32) * D;
+                auto place = [&](int row32, int c) {
+                    return PC == 8 ? row32 * 128 + ((c ^ (row32 & 7)) << 4) : row32 * 64 + ((c ^ ((row32 >> 1) & 3)) << 4);
+                };
 #pragma unroll 1
-                for (int q = 0; q < D / 32; ++q) {
-                    float v[32];
-                    ld32(tO + 32u * q, v);
-                    if (row < rows) {
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t v[CW];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<float4 *>(dst + 32 * q + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                    for (int e = 0; e < CW; e += 16) tc_ld16_nowait(tO + (uint32_t)(CW * q + e), v + e);
+                    tc_wait_ld_u32<CW>(v);
+#pragma unroll
+                    for (int c = 0; c < PC; ++c)
+                        *reinterpret_cast<uint4 *>(stage + place(lane, c)) = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < PC; ++i) {
+                        const int row32 = i * (32 / PC) + lane / PC, c = lane % PC;
+                        const uint4 x = *reinterpret_cast<const uint4 *>(stage + place(row32, c));
+                        if (tile * kWideRows + quarter * 32 + row32 < rows)
+                            *reinterpret_cast<uint4 *>(dst + row32 * D + CW * q + 4 * c) = x;
                     }
+                    __syncwarp();
                 }
             }
             tc_fence_before();
