@@ -85,7 +85,9 @@ template <bool Q8, bool F32, int D, int NT> struct AcCfg {
     static constexpr int kMl = kPart + RW * D * 4;
     static constexpr int kEnd = kMl + (kAcWarps + 1) * RW * 8;
     static constexpr int kSmem = kAcWarps * kRing > kEnd ? kAcWarps * kRing : kEnd;
-    static constexpr int kMinCtas = NT == 1 ? (kSmem > 72 * 1024 ? 2 : kSmem > 54 * 1024 ? 3 : 4) : kSmem > 72 * 1024 ? 2 : 3;
+    // CTAs an SM: as many as shared memory holds, but two for two row tiles of 128 (three left 240 bytes a thread in
+    // memory: 96 streams of 16 rows 133 us against 128)
+    static constexpr int kMinCtas = kSmem > 72 * 1024 || (NT == 2 && D == 128) ? 2 : NT == 1 && kSmem <= 54 * 1024 ? 4 : 3;
 };
 
 __device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
@@ -626,21 +628,23 @@ __global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NT>::kMinCtas)
     w.init(lane);
     {
         const int own = (len + K::TP - 1) / K::TP, step = nsplit * kAcWarps, total = nn > 0 ? own + (PREFIX ? 0 : a.pre_tiles) : 0;
-        int tile = split * kAcWarps + warp;
-        bool first = true;
-        do {                                         // the stream's own tiles, then a short prefix's
-            const bool pre = !PREFIX && tile >= own && tile < total;
-            if (pre)
-                w.start(a.pc, 0, hk, a.pre_len, sm + warp * K::kRing, tile - own, a.pre_tiles, step);
-            else
-                w.start(a.c, b, hk, len, sm + warp * K::kRing, tile, min(own, total), step);
-            if (first) w.load_rows(a, b, hk, r0, len, nn);
-            if (pre) w.see_all(a.pre_len);
-            w.run();
-            first = false;
-            const int end = pre ? total : min(own, total);
-            if (tile < end) tile += (end - tile + step - 1) / step * step;
-        } while (tile < total);
+        const int tile = split * kAcWarps + warp;
+        bool pre = !PREFIX && tile >= own && tile < total;   // the stream's own tiles, then a short prefix's
+        if (pre)
+            w.start(a.pc, 0, hk, a.pre_len, sm + warp * K::kRing, tile - own, a.pre_tiles, step);
+        else
+            w.start(a.c, b, hk, len, sm + warp * K::kRing, tile, min(own, total), step);
+        w.load_rows(a, b, hk, r0, len, nn);
+        if (pre) w.see_all(a.pre_len);
+        w.run();
+        if constexpr (!PREFIX) {
+            const int then = tile + (own - tile + step - 1) / step * step;   // this warp's first tile past its own
+            if (!pre && tile < own && then < total) {
+                w.start(a.pc, 0, hk, a.pre_len, sm + warp * K::kRing, then - own, a.pre_tiles, step);
+                w.see_all(a.pre_len);
+                w.run();
+            }
+        }
     }
     __syncthreads();
 
@@ -804,17 +808,19 @@ __global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NT>::kMinCtas)
         const int n = (int)min(tiles - tile0, x1 - x);
         const int hk = in / a.groups, grp = in - hk * a.groups;
         const int len = clamp_len(__ldg(a.lengths + b), a.max_len);
-        const int own = (int)tiles - a.pre_tiles;
-        for (int t = tile0; t < tile0 + n;) {        // its own tiles, then a short prefix's
-            const int end = t < own ? min(own, tile0 + n) : tile0 + n;
-            if (t < own)
-                w.start(a.c, b, hk, len, sm + warp * K::kRing, t, end, 1);
-            else
-                w.start(a.pc, 0, hk, a.pre_len, sm + warp * K::kRing, t - own, end - own, 1);
-            if (t == tile0) w.load_rows(a, b, hk, grp * K::RW, len, clamp_new(a, b));
-            if (t >= own) w.see_all(a.pre_len);
+        // its own tiles, then a short prefix's (two copies of the pass: a loop around one held 250 bytes a thread in memory)
+        const int own = (int)tiles - a.pre_tiles, cut = min(max(own, tile0), tile0 + n);
+        if (tile0 < own)
+            w.start(a.c, b, hk, len, sm + warp * K::kRing, tile0, cut, 1);
+        else
+            w.start(a.pc, 0, hk, a.pre_len, sm + warp * K::kRing, tile0 - own, tile0 + n - own, 1);
+        w.load_rows(a, b, hk, grp * K::RW, len, clamp_new(a, b));
+        if (tile0 >= own) w.see_all(a.pre_len);
+        w.run();
+        if (tile0 < own && cut < tile0 + n) {
+            w.start(a.pc, 0, hk, a.pre_len, sm + warp * K::kRing, cut - own, tile0 + n - own, 1);
+            w.see_all(a.pre_len);
             w.run();
-            t = end;
         }
         __syncwarp();
         const int64_t slot = (int64_t)b * per + in + wid;   // x only grows: so does the pair
@@ -1117,7 +1123,8 @@ qd_status make_plan(const qd_kv_cache *cache, const qd_kv_cache *prefix, int pre
     if (items * tiles > (1ll << 31)) return QD_EUNSUPPORTED;
     // A cluster per item while the grid is one wave, or little more, and a warp's share short; longer or larger batches are
     // shared out.  (72 items, a short prefix: 576 CTAs 13.8 us, 288 10.2; 592 items of one CTA 14.6 us, shared out 18.)
-    const int wave = (!q8 && d == 128 ? 2 : 3) * sms;
+    // An SM holds three CTAs at least, two of the largest variants.
+    const int wave = (d == 128 && (!q8 || p->nt == 2) ? 2 : 3) * sms;
     p->nsplit = 1;
     while (p->nsplit < kAcMaxCluster && items * p->nsplit * 2 <= wave && tiles > p->nsplit * kAcWarps) p->nsplit *= 2;
     if (items * p->nsplit > wave + wave / 3 || tiles > 8 * p->nsplit * kAcWarps) p->nsplit = 0;
