@@ -581,7 +581,8 @@ typedef struct {
  * nearest even.  QD_KV_Q8, per row in fp32: scale = max|x| / 127, code = nearest integer
  * (ties to even) to x * (127 / max|x|); a row below 2^-116 throughout is stored as zeros,
  * and one that holds an infinity or a NaN as codes 0 with a NaN scale, so that it reads
- * as NaN.  A row whose position falls outside [0, smax) is not written.  Errors:
+ * as NaN.  A row whose position falls outside [0, smax) is not written.  At most 65535
+ * streams.  Errors:
  * QD_EINVAL (arguments, alignment, memory), QD_EUNSUPPORTED (head_dim), QD_ECUDA. */
 qd_status qd_kv_append(const qd_kv_cache *cache, const void *k_rows_dev, const void *v_rows_dev, int dtype,
                        int n_tokens, int64_t stream_stride, int64_t token_stride, int64_t head_stride,
@@ -609,15 +610,18 @@ qd_status qd_kv_read(const qd_kv_cache *cache, void *k_rows_dev, void *v_rows_de
  * q_dev, out_dev: DEVICE fp32 or bf16 (dtype, the same for both), head h of row t of
  * stream b at b * stream_stride + t * token_stride + h * head_dim elements, each with its own strides,
  * 16-byte aligned with strides of 16-byte multiples; q and out must not overlap.
- * Scores, softmax and sums are fp32; fp32 queries and their probabilities keep at
- * least 22 bits through the products, bf16 ones at least 11.
+ * Scores, softmax and sums are fp32.  fp32 queries and their probabilities keep at least
+ * 22 bits through the products; bf16 queries are exact, their probabilities keep 11
+ * bits over 8-bit rows, and over bf16 rows 16 bits up to 8 rows (tokens times query
+ * heads) a key head, 8 bits beyond.
  * prefix: one stream of n_kv_heads heads in either format (its strides for streams are
  * unread), read once for the whole batch; NULL or prefix_length 0: none.
  * n_tokens <= 64, max_length in [1, cache->smax] bounds the lengths (it plans the launch).
- * workspace_dev: DEVICE, 256-byte aligned, qd_attn_cached_workspace bytes (0 for a small
- * batch without a prefix: NULL is allowed).  It is scratch of one call: calls, or captured graphs, that
+ * workspace_dev: DEVICE, 256-byte aligned, qd_attn_cached_workspace bytes (0 for small
+ * batches: NULL is allowed).  It is scratch of one call: calls, or captured graphs, that
  * may run at the same time need their own.  Errors: QD_EINVAL (arguments, alignment,
- * memory, workspace), QD_EUNSUPPORTED (head_dim, n_tokens), QD_ECUDA. */
+ * memory, workspace), QD_EUNSUPPORTED (head_dim, n_tokens, more than 2^24 query rows a
+ * key head or 2^31 tiles of positions), QD_ECUDA. */
 qd_status qd_attn_cached(const qd_kv_cache *cache, const qd_kv_cache *prefix, int prefix_length, const void *q_dev,
                          int64_t q_stream_stride, int64_t q_token_stride, void *out_dev, int64_t out_stream_stride,
                          int64_t out_token_stride, int dtype, int n_tokens, int n_q_heads, float scale,

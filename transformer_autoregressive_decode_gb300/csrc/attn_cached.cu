@@ -58,8 +58,12 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
     return d;
 }
-template <bool Q8, bool F32, int D, int NT> struct AcCfg {
-    static constexpr int C = Q8 ? (F32 ? 2 : 1) : (F32 ? 4 : 2);   // columns per row
+// NTX: tiles of 8 columns, plus kOnePart for bf16 rows over a bf16 cache whose probabilities are one bf16 part
+// (half a step 2^-8 of each, at random): from 9 rows on, where it halves the passes over the cache.
+constexpr int kOnePart = 8;
+template <bool Q8, bool F32, int D, int NTX> struct AcCfg {
+    static constexpr int NT = NTX & 7;
+    static constexpr int C = Q8 ? (F32 ? 2 : 1) : F32 ? 4 : NTX & kOnePart ? 1 : 2;   // columns per row
     static constexpr int RW = 8 * NT / C;                          // rows per CTA
     static constexpr int ES = Q8 ? 1 : 2;
     static constexpr int KP = D * ES / 64;                         // 16-byte pieces of a K row per lane
@@ -87,7 +91,7 @@ template <bool Q8, bool F32, int D, int NT> struct AcCfg {
     static constexpr int kSmem = kAcWarps * kRing > kEnd ? kAcWarps * kRing : kEnd;
     // CTAs an SM: as many as shared memory holds, but two for two row tiles of 128 (three left 240 bytes a thread in
     // memory: 96 streams of 16 rows 133 us against 128)
-    static constexpr int kMinCtas = kSmem > 72 * 1024 || (NT == 2 && D == 128) ? 2 : NT == 1 && kSmem <= 54 * 1024 ? 4 : 3;
+    static constexpr int kMinCtas = kSmem > 72 * 1024 || (NT == 2 && D == 128) || NT == 4 ? 2 : NT == 1 && kSmem <= 54 * 1024 ? 4 : 3;
 };
 
 __device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
@@ -106,8 +110,9 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
 
 // One warp's pass over some of an item's tiles: the item's rows as B fragments, the ring of
 // tiles, and the running reference, sums and output.
-template <bool Q8, bool F32, int D, int NT, bool PREFIX> struct WarpPass {
-    using K = AcCfg<Q8, F32, D, NT>;
+template <bool Q8, bool F32, int D, int NTX, bool PREFIX> struct WarpPass {
+    using K = AcCfg<Q8, F32, D, NTX>;
+    static constexpr int NT = K::NT;
     static constexpr int C = K::C, HC = C == 1 ? 2 : 1;
     // bf16 rows over codes: K's codes enter as 1152 + code, and the scores start at -1152 sum q (fp32 sums of
     // 8 steps: within 2^-20 of 1152 sum |q|, 2^-17 of max|k| sum |q|).  fp32 rows and V subtract it from each code.
@@ -424,10 +429,9 @@ template <bool Q8, bool F32, int D, int NT, bool PREFIX> struct WarpPass {
                         for (int nt = 0; nt < NT; ++nt) {
                             float acc[4] = {o[w][nt][0], o[w][nt][1], o[w][nt][2], o[w][nt][3]};
                             mma16816(acc, fm, pb[nt][0], pb[nt][1]);
-                            if (lim[nt][0] == cut) {
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) o[w][nt][e] = acc[e];
-                            }
+                            for (int e = 0; e < 4; ++e)
+                                if (lim[nt][HC == 2 ? e & 1 : 0] == cut) o[w][nt][e] = acc[e];
                         }
                     }
                 } else {
@@ -545,7 +549,7 @@ template <bool Q8, bool F32, int D, int NT, bool PREFIX> struct WarpPass {
                     }
                     uint32_t y;
                     if constexpr (C == 1) {
-                        y = pack_f16(w[0], w[1]);
+                        y = Q8 ? pack_f16(w[0], w[1]) : pack_bf16(w[0], w[1]);
                     } else if constexpr (Q8) {
                         const float hi = f16_of(w[0]);
                         y = pack_f16(hi, w[0] - hi);
@@ -610,10 +614,11 @@ __device__ __forceinline__ void add4(float4 &acc, float f, float4 v) {
 // shared memory and the output is written here.  PREFIX: the rows of every stream over
 // the shared prefix, an item per `nsplit` CTAs, partials to global memory.
 // blockIdx.x = item * nsplit + split.
-template <bool Q8, bool F32, int D, int NT, bool PREFIX>
-__global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NT>::kMinCtas)
+template <bool Q8, bool F32, int D, int NTX, bool PREFIX>
+__global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NTX>::kMinCtas)
     attn_cached_kernel(const CachedArgs a, int nsplit) {
-    using K = AcCfg<Q8, F32, D, NT>;
+    using K = AcCfg<Q8, F32, D, NTX>;
+    constexpr int NT = K::NT;
     extern __shared__ __align__(16) uint8_t sm[];
     pdl_wait();
     pdl_launch_dependents();                         // after the wait: see attn_join_kernel
@@ -624,7 +629,7 @@ __global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NT>::kMinCtas)
     const int nn = PREFIX ? a.T : clamp_new(a, b);
     const int r0 = grp * K::RW;
 
-    WarpPass<Q8, F32, D, NT, PREFIX> w;
+    WarpPass<Q8, F32, D, NTX, PREFIX> w;
     w.init(lane);
     {
         const int own = (len + K::TP - 1) / K::TP, step = nsplit * kAcWarps, total = nn > 0 ? own + (PREFIX ? 0 : a.pre_tiles) : 0;
@@ -756,10 +761,11 @@ __device__ __forceinline__ unsigned tiles_before(const CachedArgs &a, int upto, 
     return before * per;
 }
 
-template <bool Q8, bool F32, int D, int NT>
-__global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NT>::kMinCtas)
+template <bool Q8, bool F32, int D, int NTX>
+__global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NTX>::kMinCtas)
     attn_share_kernel(const CachedArgs a) {
-    using K = AcCfg<Q8, F32, D, NT>;
+    using K = AcCfg<Q8, F32, D, NTX>;
+    constexpr int NT = K::NT;
     extern __shared__ __align__(16) uint8_t sm[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned wid = blockIdx.x * kAcWarps + warp;
@@ -795,7 +801,7 @@ __global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NT>::kMinCtas)
         s_b += __shfl_sync(0xffffffffu, upto, 31);
     }
 
-    WarpPass<Q8, F32, D, NT, false> w;
+    WarpPass<Q8, F32, D, NTX, false> w;
     w.init(lane);
     while (x < x1) {
         const unsigned tiles = (unsigned)tiles_of(a, b, K::TP);
@@ -1026,24 +1032,24 @@ cudaError_t launch_ex(F fn, dim3 grid, int threads, int smem, unsigned cluster, 
 }
 
 // kind Cluster or Prefix: `ctas` of clusters of nsplit; kind Share: every CTA the SMs hold, *ctas says how many.
-template <bool Q8, bool F32, int D, int NT>
+template <bool Q8, bool F32, int D, int NTX>
 cudaError_t launch(int kind, const CachedArgs &a, unsigned *ctas, int nsplit, int dev, cudaStream_t s, bool plan) {
-    using K = AcCfg<Q8, F32, D, NT>;
+    using K = AcCfg<Q8, F32, D, NTX>;
     static Ready ready[3][64] = {};
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     cudaError_t e;
     if (kind == kPassShare) {
-        auto fn = attn_share_kernel<Q8, F32, D, NT>;
+        auto fn = attn_share_kernel<Q8, F32, D, NTX>;
         if ((e = make_ready(&ready[kind][dev], fn, K::kSmem)) != cudaSuccess) return e;
         *ctas = (unsigned)(ready[kind][dev].per_sm * sms_of(dev));
         return plan ? cudaSuccess : launch_ex(fn, *ctas, kAcThreads, K::kSmem, 1, s, a);
     }
     if (kind == kPassPrefix) {
-        auto fn = attn_cached_kernel<Q8, F32, D, NT, true>;
+        auto fn = attn_cached_kernel<Q8, F32, D, NTX, true>;
         if ((e = make_ready(&ready[kind][dev], fn, K::kSmem)) != cudaSuccess) return e;
         return launch_ex(fn, *ctas, kAcThreads, K::kSmem, 1, s, a, nsplit);
     }
-    auto fn = attn_cached_kernel<Q8, F32, D, NT, false>;
+    auto fn = attn_cached_kernel<Q8, F32, D, NTX, false>;
     if ((e = make_ready(&ready[kind][dev], fn, K::kSmem)) != cudaSuccess) return e;
     return launch_ex(fn, *ctas, kAcThreads, K::kSmem, (unsigned)nsplit, s, a, nsplit);
 }
@@ -1057,14 +1063,27 @@ constexpr int64_t kInlineTiles = 20000;
 constexpr int kWideFrom = 48;
 
 constexpr int tile_positions(bool q8, int d) { return q8 || d == 64 ? 32 : 16; }   // AcCfg::TP
-constexpr int rows_per_tile(bool q8, bool f32) { return 8 / (q8 ? (f32 ? 2 : 1) : (f32 ? 4 : 2)); }
+// Column tiles (AcCfg's NTX) for `rows` rows of an item, and the rows that they hold.
+int column_tiles(bool q8, bool f32, int d, int64_t rows, int *rw) {
+    const int per = 8 / (q8 ? (f32 ? 2 : 1) : (f32 ? 4 : 2));   // rows of a tile
+    int nt = rows > per ? 2 : 1;
+    *rw = per * nt;
+    // more tiles, where their sums fit the registers (head_dim 64), or one part where two were
+    if (d == 64 && rows > *rw && (f32 || !q8) && rows > (f32 ? *rw : 16))
+        nt = f32 ? 4 : kOnePart + 4, *rw = f32 ? per * 4 : 32;
+    else if (!f32 && !q8 && rows > *rw)
+        nt = kOnePart + 2, *rw = 16;
+    return nt;
+}
 
 cudaError_t dispatch(int kind, bool q8, bool f32, int d, int nt, const CachedArgs &a, unsigned *ctas, int nsplit, int dev,
                      cudaStream_t s, bool plan = false) {
 #define QD_AC(Q, F, DD, N) \
-    if (q8 == Q && f32 == F && d == DD && nt == N) return launch<Q, F, DD, N>(kind, a, ctas, nsplit, dev, s, plan);
+    if (q8 == Q && f32 == F && d == DD && nt == (N)) return launch<Q, F, DD, (N)>(kind, a, ctas, nsplit, dev, s, plan);
 #define QD_AC2(Q, F) QD_AC(Q, F, 64, 1) QD_AC(Q, F, 64, 2) QD_AC(Q, F, 128, 1) QD_AC(Q, F, 128, 2)
     QD_AC2(false, false) QD_AC2(false, true) QD_AC2(true, false) QD_AC2(true, true)
+    QD_AC(false, false, 64, kOnePart + 2) QD_AC(false, false, 128, kOnePart + 2)
+    QD_AC(false, false, 64, kOnePart + 4) QD_AC(false, true, 64, 4) QD_AC(true, true, 64, 4)
 #undef QD_AC2
 #undef QD_AC
     return cudaErrorInvalidValue;
@@ -1105,9 +1124,9 @@ qd_status make_plan(const qd_kv_cache *cache, const qd_kv_cache *prefix, int pre
     const int kvh = cache->n_kv_heads, d = cache->head_dim, B = cache->n_streams, G = QH / kvh;
     const int sms = sms_of(dev);
     const bool q8 = cache->format == QD_KV_Q8;
-    const int rows = T * G, per = rows_per_tile(q8, f32);
+    const int rows = T * G;
     p->rows_all = (int64_t)rows * B;
-    p->nt = rows > per ? 2 : 1, p->rw = per * p->nt, p->groups = (rows + p->rw - 1) / p->rw;
+    p->nt = column_tiles(q8, f32, d, rows, &p->rw), p->groups = (rows + p->rw - 1) / p->rw;
     const int64_t items = (int64_t)B * kvh * p->groups;
     p->tp = tile_positions(q8, d);
     int tiles = (max_length + p->tp - 1) / p->tp;
@@ -1124,7 +1143,7 @@ qd_status make_plan(const qd_kv_cache *cache, const qd_kv_cache *prefix, int pre
     // A cluster per item while the grid is one wave, or little more, and a warp's share short; longer or larger batches are
     // shared out.  (72 items, a short prefix: 576 CTAs 13.8 us, 288 10.2; 592 items of one CTA 14.6 us, shared out 18.)
     // An SM holds three CTAs at least, two of the largest variants.
-    const int wave = (d == 128 && (!q8 || p->nt == 2) ? 2 : 3) * sms;
+    const int wave = ((d == 128 && (!q8 || p->nt == 2)) || (p->nt & 7) == 4 ? 2 : 3) * sms;
     p->nsplit = 1;
     while (p->nsplit < kAcMaxCluster && items * p->nsplit * 2 <= wave && tiles > p->nsplit * kAcWarps) p->nsplit *= 2;
     if (items * p->nsplit > wave + wave / 3 || tiles > 8 * p->nsplit * kAcWarps) p->nsplit = 0;
@@ -1140,12 +1159,11 @@ qd_status make_plan(const qd_kv_cache *cache, const qd_kv_cache *prefix, int pre
             p->p_ml = at, at = up256(at + recs * kWideRows * 8);
             p->p_o = at, at = up256(at + recs * kWideRows * d * 4);
         } else {
-        const int pper = rows_per_tile(pq8, f32);
-        p->p_nt = p->rows_all > pper ? 2 : 1, p->p_rw = pper * p->p_nt;
-        p->p_groups = (int)((p->rows_all + p->p_rw - 1) / p->p_rw);
-        p->splits = prefix_splits((int)p->rows_all, kvh, prefix_length, p->p_rw, tile_positions(pq8, d), sms);
-        p->p_ml = at, at = up256(at + (size_t)kvh * p->rows_all * p->splits * 8);
-        p->p_o = at, at = up256(at + (size_t)kvh * p->rows_all * p->splits * d * 4);
+            p->p_nt = column_tiles(pq8, f32, d, p->rows_all, &p->p_rw);
+            p->p_groups = (int)((p->rows_all + p->p_rw - 1) / p->p_rw);
+            p->splits = prefix_splits((int)p->rows_all, kvh, prefix_length, p->p_rw, tile_positions(pq8, d), sms);
+            p->p_ml = at, at = up256(at + (size_t)kvh * p->rows_all * p->splits * 8);
+            p->p_o = at, at = up256(at + (size_t)kvh * p->rows_all * p->splits * d * 4);
         }
     }
     if (!p->nsplit) {

@@ -268,11 +268,13 @@ __global__ void __launch_bounds__(kWtThreads, 1) attn_prefix_tc_kernel(const Cac
         *bad = 0;
         fence_barrier_init();
     }
+    // The predecessor first, the tensor memory then: held while waiting it could be what a predecessor's CTA on this SM
+    // waits for.
+    pdl_wait();
     if (warp == 12) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
-    pdl_wait();
     pdl_launch_dependents();
     // where each stream's rows in use begin, and how many there are
     const bool gaps = a.n_new && a.B <= kWideMaxStreams;
