@@ -852,13 +852,15 @@ __global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NTX>::kMinCtas)
 // and from the prefix, weighted to a common reference, added in the order of the list.  blockIdx.x: the stream, whose
 // place in the lists a warp works out once; blockIdx.y: its share of the stream's rows in use.
 constexpr int kJoinWarps = 8;
+constexpr int join_warps(int wpr) { return wpr == 1 ? 4 : kJoinWarps; }   // small CTAs find room while attn_share_kernel ends
 // WPR 8: few rows of many partials.  WPR 1: a warp a row, BATCH partials in flight: 8 where the rows are few and the time is a
-// chain of loads, 4 (half the registers, four CTAs an SM) where they are many.  (64 x 16 rows: 34.2 us a call against 36;
-// 96 x 4 x 32: 143 against 137.)
+// chain of loads, 4 (half the registers) where they are many.  (64 x 16 rows: 34.2 us a call against 36; 96 x 4 x 32: 143
+// against 137.)
 template <bool F32, int D, int WPR, int BATCH>
-__global__ void __launch_bounds__(kJoinWarps * 32, BATCH == 8 ? 2 : 4) attn_join_kernel(const CachedArgs a, int rw, int tp, unsigned warps) {
-    __shared__ float4 s_acc[kJoinWarps][32];
-    __shared__ float2 s_ml[kJoinWarps];
+__global__ void __launch_bounds__(join_warps(WPR) * 32, WPR > 1 ? 2 : BATCH == 8 ? 4 : 8) attn_join_kernel(const CachedArgs a, int rw, int tp, unsigned warps) {
+    constexpr int JW = join_warps(WPR);
+    __shared__ float4 s_acc[JW][32];
+    __shared__ float2 s_ml[JW];
     constexpr int LPR = D / 4;                      // lanes of a row's float4s
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % WPR;
     // lengths and n_new may be read before the wait: attn_share_kernel lets this kernel start only after
@@ -873,109 +875,123 @@ __global__ void __launch_bounds__(kJoinWarps * 32, BATCH == 8 ? 2 : 4) attn_join
     const WideItems items(rows_all);
     if (a.wide) items.share(a, &ws);
     const int used = nn * a.G, n_rows = a.kvh * used;    // of the stream, key head by key head
+    constexpr int kRows = JW / WPR;                 // rows of a CTA's turn
+    struct Place {
+        int row, hk, r, own, all, subs, sub, cr, in_grp;
+        int64_t slot0, p_at, rec0;
+    };
+    auto place = [&](int i0) {
+        Place p;
+        p.row = i0 + warp / WPR;
+        const int at = min(p.row, n_rows - 1);
+        p.hk = at / used, p.r = at - p.hk * used;
+        const int grp = p.r / rw, in = p.hk * a.groups + grp;
+        p.in_grp = p.r - grp * rw;
+        const unsigned x = s_b + in * tiles;
+        const unsigned w0 = tiles ? sh.owner(x) : 0u;
+        p.own = tiles ? (int)(sh.owner(x + tiles - 1) + 1 - w0) : 0;
+        p.slot0 = (int64_t)b * a.kvh * a.groups + in + w0;
+        p.p_at = (((int64_t)p.hk * a.B + b) * a.rows + p.r) * a.splits;
+        // the prefix's partials: `splits` of them, or the records of attn_prefix_tc_kernel
+        int n_pre = a.splits;
+        p.subs = 1, p.sub = 0, p.rec0 = 0, p.cr = cr0 + p.r;
+        if (a.wide) {
+            const int tile = p.cr / kWideRows, item = items.pairs ? p.hk * items.pairs + tile / 2 : p.hk;
+            const unsigned c0 = (unsigned)(item * a.wide_chunks), o0 = ws.owner(c0);
+            if (items.pairs)
+                p.sub = tile & 1;
+            else
+                p.subs = 2;
+            n_pre = (int)(ws.owner(c0 + a.wide_chunks - 1) + 1 - o0) * p.subs;
+            p.rec0 = 2 * ((int64_t)o0 + item);
+        }
+        p.all = p.own + n_pre;
+        return p;
+    };
+    Place p = {};
+    if ((int)blockIdx.y * kRows < n_rows) p = place(blockIdx.y * kRows);
     pdl_wait();                                     // the partials are written
 
-    constexpr int kRows = kJoinWarps / WPR;         // rows of a CTA's turn
-    for (int i0 = blockIdx.y * kRows; i0 < n_rows; i0 += gridDim.y * kRows) {
-    const int row = i0 + warp / WPR, hk = min(row, n_rows - 1) / used, r = min(row, n_rows - 1) - hk * used;
-    const int tt = r / a.G, grp = r / rw, in_grp = r - grp * rw;
-    const int in = hk * a.groups + grp;
-    const unsigned x = s_b + in * tiles;
-    const unsigned w0 = tiles ? sh.owner(x) : 0u;
-    const int own = tiles ? (int)(sh.owner(x + tiles - 1) + 1 - w0) : 0;
-    const int64_t slot0 = (int64_t)b * a.kvh * a.groups + in + w0;
-    const int64_t p_at = (((int64_t)hk * a.B + b) * a.rows + r) * a.splits;
-    // the prefix's partials: `splits` of them, or the records of attn_prefix_tc_kernel
-    int n_pre = a.splits, subs = 1, sub = 0;
-    int64_t rec0 = 0;
-    const int cr = cr0 + r;
-    if (a.wide) {
-        const int tile = cr / kWideRows, item = items.pairs ? hk * items.pairs + tile / 2 : hk;
-        const unsigned c0 = (unsigned)(item * a.wide_chunks), o0 = ws.owner(c0);
-        if (items.pairs)
-            sub = tile & 1;
-        else
-            subs = 2;
-        n_pre = (int)(ws.owner(c0 + a.wide_chunks - 1) + 1 - o0) * subs;
-        rec0 = 2 * ((int64_t)o0 + item);
-    }
-    const int all = own + n_pre;
-
-    // 32 / LPR partials at a time (one for head_dim 128), LPR lanes each; kBatch of those are loaded
-    // together, (ref, sum) with their rows, then weighted to the running reference
-    constexpr int kBatch = BATCH, kStep = WPR * (32 / LPR);
-    const int d = (lane % LPR) * 4;
-    float M = -INFINITY, sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = part * (32 / LPR) + lane / LPR; i0 - lane / LPR < all; i0 += kBatch * kStep) {
-        float2 e[kBatch];
-        float4 v[kBatch];
+    for (int i0 = blockIdx.y * kRows; i0 < n_rows;) {
+        // 32 / LPR partials at a time (one for head_dim 128), LPR lanes each; kBatch of those are loaded
+        // together, (ref, sum) with their rows, then weighted to the running reference
+        constexpr int kBatch = BATCH, kStep = WPR * (32 / LPR);
+        const int d = (lane % LPR) * 4;
+        float M = -INFINITY, sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j0 = part * (32 / LPR) + lane / LPR; j0 - lane / LPR < p.all; j0 += kBatch * kStep) {
+            float2 e[kBatch];
+            float4 v[kBatch];
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            const int i = i0 + j * kStep;
-            e[j] = make_float2(-INFINITY, 0.f);
-            v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (i < own) {
-                const int64_t at = (slot0 + i) * rw + in_grp;
-                e[j] = a.s_ml[at];
-                v[j] = *reinterpret_cast<const float4 *>(a.s_o + at * D + d);
-            } else if (i < all) {
-                const int k = i - own;
-                const int64_t at = !a.wide ? p_at + k
-                                           : (rec0 + (subs == 2 ? k : 2 * k + sub)) * kWideRows + cr % kWideRows;
-                e[j] = a.p_ml[at];
-                v[j] = *reinterpret_cast<const float4 *>(a.p_o + at * D + d);
+            for (int j = 0; j < kBatch; ++j) {
+                const int i = j0 + j * kStep;
+                e[j] = make_float2(-INFINITY, 0.f);
+                v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i < p.own) {
+                    const int64_t at = (p.slot0 + i) * rw + p.in_grp;
+                    e[j] = a.s_ml[at];
+                    v[j] = *reinterpret_cast<const float4 *>(a.s_o + at * D + d);
+                } else if (i < p.all) {
+                    const int k = i - p.own;
+                    const int64_t at = !a.wide ? p.p_at + k
+                                               : (p.rec0 + (p.subs == 2 ? k : 2 * k + p.sub)) * kWideRows + p.cr % kWideRows;
+                    e[j] = a.p_ml[at];
+                    v[j] = *reinterpret_cast<const float4 *>(a.p_o + at * D + d);
+                }
+            }
+            float now = M;
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) now = fmaxf(now, e[j].x);
+            const float keep = part_weight(make_float2(M, sum), now);
+            acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
+            sum *= keep;
+            M = now;
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                if (e[j].y == 0.f) continue;
+                const float f = part_weight(e[j], M);
+                add4(acc, f, v[j]);
+                sum = fmaf(f, e[j].y, sum);
             }
         }
-        float now = M;
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) now = fmaxf(now, e[j].x);
-        const float keep = part_weight(make_float2(M, sum), now);
-        acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
-        sum *= keep;
-        M = now;
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            if (e[j].y == 0.f) continue;
-            const float f = part_weight(e[j], M);
-            add4(acc, f, v[j]);
-            sum = fmaf(f, e[j].y, sum);
+        // the lanes' and the warps' own references meet
+        if constexpr (LPR == 16) {
+            const float now = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
+            const float f = part_weight(make_float2(M, sum), now);
+            acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+            sum *= f;
+            M = now;
         }
-    }
-    // the lanes' and the warps' own references meet
-    if constexpr (LPR == 16) {
-        const float now = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
-        const float f = part_weight(make_float2(M, sum), now);
-        acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
-        sum *= f;
-        M = now;
-    }
-    if constexpr (LPR == 16) {
-        acc.x += __shfl_xor_sync(0xffffffffu, acc.x, 16), acc.y += __shfl_xor_sync(0xffffffffu, acc.y, 16);
-        acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16), acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-    }
-    if constexpr (WPR > 1) {
-        s_acc[warp][lane] = acc;
-        if (lane == 0) s_ml[warp] = make_float2(M, sum);
-        __syncthreads();
-        const int w1 = warp - part;                 // this row's first warp
-#pragma unroll
-        for (int i = 0; i < WPR; ++i) M = fmaxf(M, s_ml[w1 + i].x);
-        acc = make_float4(0.f, 0.f, 0.f, 0.f), sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < WPR; ++i) {
-            const float2 e = s_ml[w1 + i];
-            if (e.y == 0.f) continue;
-            const float f = part_weight(e, M);
-            add4(acc, f, s_acc[w1 + i][lane]);
-            sum = fmaf(f, e.y, sum);
+        if constexpr (LPR == 16) {
+            acc.x += __shfl_xor_sync(0xffffffffu, acc.x, 16), acc.y += __shfl_xor_sync(0xffffffffu, acc.y, 16);
+            acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16), acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 16);
         }
-        __syncthreads();                            // before the next turn's
-    }
-    if (row < n_rows && part == 0 && lane < LPR)
-        store4<F32>(a.out + b * a.o_stream + tt * a.o_token + ((int64_t)(hk * a.G + (r - tt * a.G)) * D + d) * (F32 ? 4 : 2),
-                    acc, sum == 0.f ? 0.f : 1.f / sum);
+        if constexpr (WPR > 1) {
+            s_acc[warp][lane] = acc;
+            if (lane == 0) s_ml[warp] = make_float2(M, sum);
+            __syncthreads();
+            const int w1 = warp - part;                 // this row's first warp
+#pragma unroll
+            for (int i = 0; i < WPR; ++i) M = fmaxf(M, s_ml[w1 + i].x);
+            acc = make_float4(0.f, 0.f, 0.f, 0.f), sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < WPR; ++i) {
+                const float2 e = s_ml[w1 + i];
+                if (e.y == 0.f) continue;
+                const float f = part_weight(e, M);
+                add4(acc, f, s_acc[w1 + i][lane]);
+                sum = fmaf(f, e.y, sum);
+            }
+            __syncthreads();                            // before the next turn's
+        }
+        if (p.row < n_rows && part == 0 && lane < LPR) {
+            const int tt = p.r / a.G;
+            store4<F32>(a.out + b * a.o_stream + tt * a.o_token + ((int64_t)(p.hk * a.G + (p.r - tt * a.G)) * D + d) * (F32 ? 4 : 2),
+                        acc, sum == 0.f ? 0.f : 1.f / sum);
+        }
+        i0 += gridDim.y * kRows;
+        if (i0 < n_rows) p = place(i0);
     }
 }
 
@@ -1091,12 +1107,12 @@ cudaError_t dispatch(int kind, bool q8, bool f32, int d, int nt, const CachedArg
 
 cudaError_t launch_join(bool f32, int d, const CachedArgs &a, int rw, int tp, unsigned warps, bool many, int sms, cudaStream_t s) {
     // about eight CTAs per SM, two waves: the stream's place is worked out once for a few turns
-    const int wpr = many ? kJoinWarps : 1, turns = (a.kvh * a.rows * wpr + kJoinWarps - 1) / kJoinWarps;
-    const dim3 grid((unsigned)a.B, (unsigned)std::min({turns, std::max(1, 8 * sms / a.B), 65535}));
+    const int wpr = many ? kJoinWarps : 1, jw = join_warps(wpr), turns = (a.kvh * a.rows * wpr + jw - 1) / jw;
+    const dim3 grid((unsigned)a.B, (unsigned)std::min({turns, std::max(1, 64 / jw * sms / a.B), 65535}));
     const int batch = many || (int64_t)a.B * a.kvh * a.rows <= 4096 ? 8 : 4;
 #define QD_JOIN(F, DD, W, N) \
     if (f32 == F && d == DD && wpr == W && batch == N) \
-        return launch_ex(attn_join_kernel<F, DD, W, N>, grid, kJoinWarps * 32, 0, 1, s, a, rw, tp, warps);
+        return launch_ex(attn_join_kernel<F, DD, W, N>, grid, jw * 32, 0, 1, s, a, rw, tp, warps);
 #define QD_JOIN2(F, DD) QD_JOIN(F, DD, 1, 4) QD_JOIN(F, DD, 1, 8) QD_JOIN(F, DD, kJoinWarps, 8)
     QD_JOIN2(false, 64) QD_JOIN2(false, 128) QD_JOIN2(true, 64) QD_JOIN2(true, 128)
 #undef QD_JOIN2
