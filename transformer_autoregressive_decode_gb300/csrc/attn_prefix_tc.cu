@@ -23,7 +23,7 @@
 //
 // Roles (512 threads): warps 0-3 and 4-7 the softmax of the two halves (a row each, also Q and the results),
 // warps 8-11 load K and V, warp 12 owns the tensor memory and issues the MMAs, warps 13-15 only complete its
-// warpgroup.  Registers a thread: 128 at launch, then 184, 184, 88 and 56 (all of the 65,536).  Every wait
+// warpgroup.  Registers a thread: 128 at launch, then 176, 176, 104 and 56 (all of the 65,536).  Every wait
 // is bounded; where one expires the CTA's partials become NaN and the roles run to their ends.
 #include <cuda.h>
 
@@ -37,7 +37,7 @@ namespace {
 
 constexpr int kWtThreads = 512;
 constexpr int kWtSoft = 256, kWtLoad = 128;   // softmax threads, loading threads
-constexpr int kWtRegsSoft = 184, kWtRegsLoad = 88, kWtRegsMma = 56;
+constexpr int kWtRegsSoft = 176, kWtRegsLoad = 104, kWtRegsMma = 56;
 static_assert(128 * (2 * kWtRegsSoft + kWtRegsLoad + kWtRegsMma) <= kWtThreads * 128, "registers");
 constexpr uint32_t kWtBox = 128 * 128;        // 128 rows of 128 bytes, 128-byte swizzle
 constexpr uint32_t kWtS = 0, kWtO = 256;      // tensor memory columns: S (and P) of the halves, O
