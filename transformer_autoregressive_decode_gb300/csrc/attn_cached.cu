@@ -8,24 +8,34 @@
 // scale multiplies s_j, the values' scale multiplies p_j on its way into the product, so
 // the tensor cores work on the codes themselves (exact in fp16).
 //
-// Decoding has few rows and many positions, so the positions are the long side (M = 16) of m16n8k16
-// and the rows its N = 8 columns.  Where a value must keep more bits than the tensor
-// core's type has, it takes C columns, one per part (q and p alike; the parts' products
-// are added afterwards): 8-bit cache, fp16: bf16 rows 1 part, fp32 rows 2; bf16 cache: 2
-// parts (hi, lo of p), fp32 rows 3 of 4 columns.
+// Decoding has few rows and many positions, so the positions are the long side (M = 16) of
+// m16n8k16 and the rows its N = 8 columns.  Where a value must keep more bits than the
+// tensor core's type has, it takes C columns, one per part (q and p alike; the parts'
+// products are added afterwards): 8-bit cache, fp16: bf16 rows 1 part, fp32 rows 2; bf16
+// cache: 2 parts (hi, lo of p; one from 9 rows on), fp32 rows 3 of 4 columns.
 //
-// Neither K nor V passes through a layout in shared memory.  The products' sums run over
-// head_dim (scores) and positions (output) in any order, so each lane takes 16 contiguous bytes of a row as its
-// share of the A fragment, and q is laid out to match.  For the output, V^T is A:
-// a lane holds the same dims of the four positions its fragment pairs, and a byte
-// permutation pairs them up, the same that widens the codes.  The probabilities turn
-// from the accumulator's layout into the B fragment's with movmatrix.  Each warp has a ring of tiles of its own
-// that it fills with cp.async (whole 128-byte lines, so that each line is one write into shared memory), the 16-byte
-// pieces of a row placed so that fragments read without bank conflicts; no barrier wider than the warp.
+// Neither K nor V is laid out anew in shared memory.  The products' sums run over head_dim
+// (scores) and positions (output) in any order, so each lane takes 16 contiguous bytes of a
+// row as its share of the A fragment, and q is laid out to match.  For the output, V^T is
+// A: a lane holds the same dims of the four positions its fragment pairs, and a byte
+// permutation pairs them up, the same that widens the codes.  The probabilities turn from
+// the accumulator's layout into the B fragment's with movmatrix.  Each warp has a ring of
+// tiles of its own that it fills with cp.async, whole 128-byte lines at a time (a copy by
+// fragment made a write into shared memory of every 32-byte sector: 46 us against 37 for 64
+// ragged 8-bit streams), the 16-byte pieces of a row placed so that fragments read without
+// bank conflicts; no barrier is wider than the warp.
 //
-// A cluster of CTAs shares one (stream, key head, rows) item; its warps take the 16-position
-// tiles in turn and their partial results (ref, sum, output) meet in distributed shared
-// memory, in a fixed order.  Nothing is kept in global memory but the prefix's partials.
+// Three ways over a stream's cache, by the sizes alone (make_plan):
+//  - small batches: a cluster of CTAs per (stream, key head, rows) item, one wave of them; the
+//    warps take the tiles in turn and their partial results (ref, sum, output) meet in
+//    distributed shared memory, in a fixed order.  One launch, no scratch; bound by its
+//    chain of loads (1 x 600 positions 6.8 us, as many of them the launch).
+//  - larger ones: attn_share_kernel's equal runs over all warps and attn_join_kernel.  Bound by HBM:
+//    3 streams of up to 65536 8-bit positions, 334 MB, 57 us (0.86 of the measured rate); 64
+//    of 257 to 2048, 156 MB, 34 us (0.68: 23 for the bytes, the launches, a pipeline's start and
+//    the join the rest).
+//  - a prefix: read by every stream's own pass while that is cheap, else by
+//    attn_prefix_tc_kernel (bf16 rows) or once for every group of rows (PREFIX here).
 #include "attn_cached.cuh"
 #include "qd_internal.h"
 
