@@ -1,7 +1,9 @@
 """Python binding of the qd C-ABI (``include/qd.h``): argument marshalling only.
 
 Every step of the decode path runs in the CUDA kernels of ``libqd.so``; this
-module converts Python/torch arguments into the C types the library takes.
+module converts Python/torch arguments into the C types the library takes (by ctypes;
+for the operators over caller-held caches, whose smallest calls are short, by the
+CPython module ``_qd_ops``).
 PyTorch serves only to hold device memory and to name the caller's stream.
 There is no fallback: importing fails loudly when ``libqd.so`` has not been
 built (``python -c "import __graft_entry__ as g; g.build()"``).
@@ -10,7 +12,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import threading
 from typing import Dict, Optional, Sequence
 
 import numpy as np
@@ -668,37 +669,24 @@ def _T():
     return _torch
 
 
-def _op_stream(stream, t) -> int:
-    """The caller's stream, by default the current one of t's device (memory of a device that is
-    not the current one is refused by the call).  The raw handle: a Stream object costs 3 us."""
-    if stream is not None:
-        return stream.cuda_stream
-    return _T()._C._cuda_getCurrentRawStream(t.get_device()) if t.is_cuda else 0
+def _setup_ops():
+    """The marshalling module, handed the library's functions and torch's objects."""
+    global _ops
+    from . import _qd_ops
+    t = _T()
+    _qd_ops.setup(*(ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in (
+        "qd_kv_append", "qd_kv_read", "qd_attn_cached", "qd_attn_cached_workspace", "qd_verify_drafts")),
+        t.float32, t.bfloat16, t.int32, t._C._cuda_getCurrentRawStream, t._C._cuda_isCurrentStreamCapturing)
+    _ops = _qd_ops
+    return _ops
 
 
-def _op_dtype(t) -> int:
-    torch, d = _T(), t.dtype
-    if d is torch.bfloat16:
-        return QD_BF16
-    if d is torch.float32:
-        return QD_F32
-    raise ValueError(f"fp32 or bf16 wanted, got {d}")
+_ops = None
 
 
-def _op_ints(t, n: int, what: str):
-    """A contiguous int32 tensor of n values (or None) as an address."""
-    if t is None:
-        return None
-    if t.dtype is not _T().int32 or t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{what} must be {n} contiguous int32 values")
-    return t.data_ptr()
-
-
-# Scratch of the calls on torch's current stream outside of captures, one buffer per device and stream: they follow
-# one another there.  The lock keeps two host threads from interleaving their launches on one stream.  Larger needs,
-# streams passed in, and captures (whose replays may run beside anything) take fresh memory from torch's allocator.
+# Scratch of the calls on torch's current streams outside of captures (_qd_ops keeps the addresses and explains why that
+# is safe).  Larger needs, streams passed in, and captures take fresh memory from torch's allocator.
 _scratch: Dict[tuple, "torch.Tensor"] = {}
-_scratch_lock = threading.Lock()
 _SCRATCH_MOST = 128 << 20
 
 
@@ -710,38 +698,19 @@ def _fresh(need: int, t, stream):
         return torch.empty(need, dtype=torch.uint8, device=t.device)
 
 
-def _stream_scratch(need: int, t, raw: int):
-    """Under _scratch_lock: the current stream's buffer, grown to `need` bytes."""
-    key = (t.get_device(), raw)
-    buf = _scratch.get(key)
-    if buf is None or buf.numel() < need:
-        buf = _scratch[key] = _fresh(max(need, 1 << 20), t, None)
-    return buf
-
-
-def _kv_rows(fn, name, cache, k_rows, v_rows, lengths, n_new, stream):
-    B, H, _, D = cache.shape
-    shape, s = k_rows.shape, k_rows.stride()
-    if len(shape) != 4 or shape != v_rows.shape or s != v_rows.stride() or k_rows.dtype is not v_rows.dtype or \
-            shape[0] != B or shape[2] != H or shape[3] != D or s[3] != 1:
-        raise ValueError(f"k_rows and v_rows must be alike: [{B}, tokens, {H}, {D}], heads contiguous")
-    T = shape[1]
-    st = fn(cache.addr, k_rows.data_ptr(), v_rows.data_ptr(), _op_dtype(k_rows), T, s[0] if B > 1 else 0,
-            s[1] if T > 1 else 0, s[2] if H > 1 else 0, _op_ints(lengths, B, "lengths"),
-            _op_ints(n_new, B, "n_new"), _op_stream(stream, k_rows))
-    if st != QD_OK:
-        raise QDError(st, f"{name} failed")
-
-
 def qd_kv_append(cache: KvCache, k_rows, v_rows, lengths, n_new=None, stream=None):
     """Write the new tokens' rows (fp32 or bf16 [streams, tokens, kv_heads, head_dim], slices of
     a fused projection as they are) into the cache; lengths (int32 [streams]) counts them in."""
-    _kv_rows(_lib.qd_kv_append, "qd_kv_append", cache, k_rows, v_rows, lengths, n_new, stream)
+    st = (_ops or _setup_ops()).rows(False, cache.addr, k_rows, v_rows, lengths, n_new, stream)
+    if st != QD_OK:
+        raise QDError(st, "qd_kv_append failed")
 
 
 def qd_kv_read(cache: KvCache, lengths, k_rows, v_rows, n_new=None, stream=None):
     """Read the rows that qd_kv_append with the same lengths writes back into k_rows and v_rows."""
-    _kv_rows(_lib.qd_kv_read, "qd_kv_read", cache, k_rows, v_rows, lengths, n_new, stream)
+    st = (_ops or _setup_ops()).rows(True, cache.addr, k_rows, v_rows, lengths, n_new, stream)
+    if st != QD_OK:
+        raise QDError(st, "qd_kv_read failed")
 
 
 def qd_attn_cached_workspace(cache: KvCache, bf16: bool, n_tokens: int, n_q_heads: int, max_length: Optional[int] = None,
@@ -756,10 +725,6 @@ def qd_attn_cached_workspace(cache: KvCache, bf16: bool, n_tokens: int, n_q_head
     return n.value
 
 
-# workspace bytes by the sizes they follow from
-_attn_bytes: Dict[tuple, int] = {}
-
-
 def qd_attn_cached(q, cache: KvCache, lengths, out, n_new=None, max_length: Optional[int] = None, scale=None,
                    prefix: Optional[KvCache] = None, prefix_length: Optional[int] = None, workspace=None, stream=None):
     """Attention of the new tokens q [streams, tokens, q_heads, head_dim] (fp32 or bf16) over
@@ -768,42 +733,21 @@ def qd_attn_cached(q, cache: KvCache, lengths, out, n_new=None, max_length: Opti
     default head_dim ** -0.5; prefix_length: default all of the prefix.  workspace: uint8
     tensor of qd_attn_cached_workspace bytes, of this call alone while it runs; by default the
     stream's own scratch (in a capture: fresh memory of the graph's)."""
-    B, H, S, D = cache.shape
-    shape, qs, os_ = q.shape, q.stride(), out.stride()
-    if len(shape) != 4 or shape != out.shape or q.dtype is not out.dtype or shape[0] != B or shape[3] != D:
-        raise ValueError(f"q and out must be [{B}, tokens, q_heads, {D}] of one type")
-    T, QH = shape[1], shape[2]
-    if qs[3] != 1 or os_[3] != 1 or (QH > 1 and (qs[2] != D or os_[2] != D)):
-        raise ValueError("the heads of q and out must be contiguous")
-    P, pre = 0, None
-    if prefix is not None:
-        P = prefix.shape[2] if prefix_length is None else int(prefix_length)
-        if prefix.shape[0] != 1:
-            raise ValueError("the prefix is a cache of one stream")
-        pre = prefix.addr if P else None
-    elif prefix_length:
-        raise ValueError("prefix_length without a prefix")
-    dt = _op_dtype(q)
-    most = S if max_length is None else int(max_length)
-    raw = _op_stream(stream, q)
-    args = (cache.addr, pre, P, q.data_ptr(), qs[0] if B > 1 else 0, qs[1] if T > 1 else 0, out.data_ptr(),
-            os_[0] if B > 1 else 0, os_[1] if T > 1 else 0, dt, T, QH, D ** -0.5 if scale is None else float(scale),
-            _op_ints(lengths, B, "lengths"), _op_ints(n_new, B, "n_new"), most)
+    ops = _ops or _setup_ops()
+    args = (q, cache.addr, lengths, out, n_new, max_length, scale, None if prefix is None else prefix.addr, prefix_length)
     if workspace is not None:
-        st = _lib.qd_attn_cached(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), raw)
+        st = ops.attn(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream)
     else:
-        key = (cache.shape, cache.format, P, P and prefix.format, dt, T, QH, most, q.get_device())
-        need = _attn_bytes.get(key)
-        if need is None:
-            need = _attn_bytes[key] = qd_attn_cached_workspace(cache, dt == QD_BF16, T, QH, most, prefix, P)
-        if not need:
-            st = _lib.qd_attn_cached(*args, None, 0, raw)
-        elif need > _SCRATCH_MOST or stream is not None or not q.is_cuda or _T()._C._cuda_isCurrentStreamCapturing():
-            ws = _fresh(need, q, stream)
-            st = _lib.qd_attn_cached(*args, ws.data_ptr(), need, raw)
-        else:
-            with _scratch_lock:
-                st = _lib.qd_attn_cached(*args, _stream_scratch(need, q, raw).data_ptr(), need, raw)
+        st = ops.attn(*args, None, 0, stream)
+        if st > 0:                                  # the bytes of scratch that there is none of
+            need, torch = st, _T()
+            keep = need <= _SCRATCH_MOST and stream is None and q.is_cuda and not torch._C._cuda_isCurrentStreamCapturing()
+            ws = _fresh(max(need, 1 << 20) if keep else need, q, stream)
+            if keep:
+                key = (q.get_device(), torch._C._cuda_getCurrentRawStream(q.get_device()))
+                if ops.keep(*key, ws.data_ptr(), ws.numel()):
+                    _scratch[key] = ws              # a smaller one before it goes back to the stream's allocator
+            st = ops.attn(*args, ws.data_ptr(), ws.numel(), stream)
     if st != QD_OK:
         raise QDError(st, "qd_attn_cached failed")
 
@@ -813,22 +757,6 @@ def qd_verify_drafts(target_probs, draft_ids, u, out_ids, n_accepted, draft_prob
     vocab]) and the drafter's draft_probs (fp32 [streams, tokens, vocab], None: drafts that were
     not sampled) with the uniforms u (fp32 [streams, tokens + 1]) into out_ids (int32 [streams,
     tokens + 1]) and n_accepted (int32 [streams])."""
-    f32 = _T().float32
-    B, T = draft_ids.shape
-    ps, V = target_probs.stride(), target_probs.shape[2]
-    if target_probs.shape != (B, T + 1, V) or target_probs.dtype is not f32 or ps[2] != 1:
-        raise ValueError(f"target_probs must be fp32 [{B}, {T + 1}, vocab], rows contiguous")
-    qs = (0, 0)
-    if draft_probs is not None:
-        qs = draft_probs.stride()
-        if draft_probs.shape != (B, T, V) or draft_probs.dtype is not f32 or qs[2] != 1:
-            raise ValueError(f"draft_probs must be fp32 [{B}, {T}, {V}], rows contiguous")
-    if u.dtype is not f32 or u.shape != (B, T + 1) or not u.is_contiguous():
-        raise ValueError(f"u must be contiguous fp32 [{B}, {T + 1}]")
-    st = _lib.qd_verify_drafts(target_probs.data_ptr(), ps[0] if B > 1 else 0, ps[1], _ptr(draft_probs),
-                               qs[0] if B > 1 else 0, qs[1] if T > 1 else 0, _op_ints(draft_ids, B * T, "draft_ids"),
-                               _op_ints(n_draft, B, "n_draft"), u.data_ptr(), B, T, V,
-                               _op_ints(out_ids, B * (T + 1), "out_ids"), _op_ints(n_accepted, B, "n_accepted"),
-                               _op_stream(stream, target_probs))
+    st = (_ops or _setup_ops()).verify(target_probs, draft_ids, u, out_ids, n_accepted, draft_probs, n_draft, stream)
     if st != QD_OK:
         raise QDError(st, "qd_verify_drafts failed")

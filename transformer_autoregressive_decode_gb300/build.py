@@ -1,4 +1,5 @@
-"""Build ``libqd.so`` (the C-ABI decode library) in-tree with nvcc for sm_103a.
+"""Build ``libqd.so`` (the C-ABI decode library) in-tree with nvcc for sm_103a, and
+``_qd_ops.so`` (the CPython marshalling of the operators over caller-held caches) with gcc.
 
 Translation units compile in parallel; the library links the CUDA runtime
 statically so it loads without any Python package.  Outputs: ``libqd.so`` next
@@ -10,12 +11,14 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libqd.so")
+OPS = os.path.join(PKG, "_qd_ops.so")
 OBJDIR = os.path.join(ROOT, "_build", "qd")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -37,10 +40,25 @@ def _deps():
         glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
 
 
+def build_ops(force: bool = False) -> str:
+    """Compile the CPython module of the operators' marshalling next to the library."""
+    src = os.path.join(CSRC, "binding_ops.c")
+    deps = [src, os.path.join(INCLUDE, "qd.h"), os.path.abspath(__file__)]
+    if not force and os.path.exists(OPS) and os.path.getmtime(OPS) >= max(os.path.getmtime(p) for p in deps):
+        return OPS
+    tmp = OPS + f".tmp{os.getpid()}"
+    subprocess.check_call(["gcc", "-O2", "-shared", "-fPIC", "-std=c11", "-Wall", "-I", sysconfig.get_paths()["include"],
+                           "-I", INCLUDE, "-o", tmp, src])
+    os.replace(tmp, OPS)
+    return OPS
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=None, lib=None, objdir=None) -> str:
     """Compile every CUDA source for sm_103a and link ``libqd.so`` (or ``lib``, with its
     objects under ``objdir``: a variant build such as the phase-timeline one); returns
     the library's path."""
+    if lib is None:
+        build_ops(force)
     LIB_ = lib or LIB
     OBJDIR_ = objdir or OBJDIR
     newest = max(os.path.getmtime(p) for p in _deps())
