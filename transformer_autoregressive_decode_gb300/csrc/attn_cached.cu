@@ -94,29 +94,29 @@ template <bool Q8, bool F32, int D, int NTX> struct AcCfg {
     
     static constexpr int kStages = kTileBytes > 8192 ? 2 : 3;
     static constexpr int kRing = kStages * kTileBytes;             // per warp
-    // after the pass the rings' space holds the warps' partials, then the CTA's
-    static constexpr int kPart = kAcWarps * RW * D * 4;
-    static constexpr int kMl = kPart + RW * D * 4;
-    static constexpr int kEnd = kMl + (kAcWarps + 1) * RW * 8;
+    // after the pass the rings' space holds the warps' partials
+    static constexpr int kMl = kAcWarps * RW * D * 4;
+    static constexpr int kEnd = kMl + kAcWarps * RW * 8;
     static constexpr int kSmem = kAcWarps * kRing > kEnd ? kAcWarps * kRing : kEnd;
+    // behind them what a cluster's CTAs send each other: [source][slice], [source][rows]
+    static constexpr int kRecv = (kSmem + 15) / 16 * 16;
+    static constexpr int kRecvMl = kRecv + RW * D * 4 + kAcMaxCluster * 16;
+    static constexpr int kSmemCluster = kRecvMl + kAcMaxCluster * RW * 8;
     // CTAs an SM: as many as shared memory holds, but two for two row tiles of 128 (three left 240 bytes a thread in
     // memory: 96 streams of 16 rows 133 us against 128)
     static constexpr int kMinCtas = kSmem > 72 * 1024 || (NT == 2 && D == 128) || NT == 4 ? 2 : NT == 1 && kSmem <= 54 * 1024 ? 4 : 3;
 };
 
-__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
-    float2 v;
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
-    return v;
+__device__ __forceinline__ void st_cluster_f2(uint32_t addr, float2 v) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(v.x), "f"(v.y) : "memory");
 }
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
+__device__ __forceinline__ void st_cluster_f4(uint32_t addr, float4 v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
                  : "memory");
-    return v;
 }
+// The cluster barrier in two halves, the first without an order: the CTAs have started.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 
 // One warp's pass over some of an item's tiles: the item's rows as B fragments, the ring of
 // tiles, and the running reference, sums and output.
@@ -630,6 +630,7 @@ __global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NTX>::kMinCtas)
     using K = AcCfg<Q8, F32, D, NTX>;
     constexpr int NT = K::NT;
     extern __shared__ __align__(16) uint8_t sm[];
+    if (!PREFIX && nsplit > 1) cluster_arrive();
     pdl_wait();
     pdl_launch_dependents();                         // after the wait: see attn_join_kernel
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -665,9 +666,7 @@ __global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NTX>::kMinCtas)
 
     // ---- the warps' partials
     float *part = reinterpret_cast<float *>(sm);
-    float *mine = part + kAcWarps * K::RW * D;      // the CTA's
     float2 *ml = reinterpret_cast<float2 *>(sm + K::kMl);
-    float2 *ml_mine = ml + kAcWarps * K::RW;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -682,70 +681,90 @@ __global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NTX>::kMinCtas)
             }
         }
     __syncthreads();
-    for (int i = threadIdx.x; i < K::RW * D / 4; i += kAcThreads) {
-        const int row = i / (D / 4);
-        if (r0 + row >= a.rows) continue;
-        float M = -INFINITY;
+    // row `row`, dims 4 (i % (D / 4)) ..: the prefix's partials join, the output is written
+    auto finish = [&](int row, int i, float M, float4 acc, float sum) {
+        const int r = r0 + row, tt = r / a.G;
+        if (tt >= nn) return;
+        const int64_t at = (((int64_t)hk * a.B + b) * a.rows + r) * a.splits;
+        for (int s = 0; s < a.splits; ++s) {
+            const float2 e = a.p_ml[at + s];
+            if (e.y == 0.f) continue;
+            const float now = fmaxf(M, e.x), keep = part_weight(make_float2(M, sum), now), f = part_weight(e, now);
+            acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
+            add4(acc, f, *reinterpret_cast<const float4 *>(a.p_o + (at + s) * D + (i % (D / 4)) * 4));
+            sum = fmaf(f, e.y, sum * keep);
+            M = now;
+        }
+        store4<F32>(a.out + b * a.o_stream + tt * a.o_token +
+                        ((int64_t)(hk * a.G + (r - tt * a.G)) * D + (i % (D / 4)) * 4) * (F32 ? 4 : 2),
+                    acc, sum == 0.f ? 0.f : 1.f / sum);
+    };
+    // the CTA's (ref, sum) of a row
+    auto row_ml = [&](int row) {
+        float M = -INFINITY, sum = 0.f;
 #pragma unroll
         for (int u = 0; u < kAcWarps; ++u) M = fmaxf(M, ml[u * K::RW + row].x);
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float sum = 0.f;
 #pragma unroll
         for (int u = 0; u < kAcWarps; ++u) {
             const float2 e = ml[u * K::RW + row];
-            if (e.y == 0.f) continue;
-            const float f = part_weight(e, M);
-            add4(acc, f, *reinterpret_cast<const float4 *>(part + u * K::RW * D + i * 4));
-            sum = fmaf(f, e.y, sum);
+            if (e.y != 0.f) sum = fmaf(part_weight(e, M), e.y, sum);
+        }
+        return make_float2(M, sum);
+    };
+    // A cluster's CTAs send their partials to the one that owns the slice (a read of the others' memory instead took a round
+    // trip for every CTA, twice): buffers of their own, which no warp's ring uses.
+    constexpr int kAll = K::RW * D / 4;
+    const int per = (kAll + nsplit - 1) / nsplit;
+    float4 *recv = reinterpret_cast<float4 *>(sm + K::kRecv);           // [source][per]
+    float2 *recv_ml = reinterpret_cast<float2 *>(sm + K::kRecvMl);      // [source][rows]
+    if (!PREFIX && nsplit > 1) cluster_wait();       // every CTA of the cluster has started
+    for (int i = threadIdx.x; i < kAll; i += kAcThreads) {
+        const int row = i / (D / 4);
+        if (r0 + row >= a.rows) continue;
+        const float2 own = row_ml(row);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int u = 0; u < kAcWarps; ++u) {
+            const float2 e = ml[u * K::RW + row];
+            if (e.y != 0.f) add4(acc, part_weight(e, own.x), *reinterpret_cast<const float4 *>(part + u * K::RW * D + i * 4));
         }
         if constexpr (PREFIX) {
             const int64_t at = ((int64_t)hk * a.rows + r0 + row) * nsplit + split;
             *reinterpret_cast<float4 *>(a.p_o + at * D + (i % (D / 4)) * 4) = acc;
-            if (i % (D / 4) == 0) a.p_ml[at] = make_float2(M, sum);
+            if (i % (D / 4) == 0) a.p_ml[at] = own;
+        } else if (nsplit == 1) {
+            finish(row, i, own.x, acc, own.y);
         } else {
-            *reinterpret_cast<float4 *>(mine + i * 4) = acc;
-            if (i % (D / 4) == 0) ml_mine[row] = make_float2(M, sum);
+            const int to = i / per;
+            st_cluster_f4(cluster_map(recv + split * per + (i - to * per), (uint32_t)to), acc);
         }
     }
     if constexpr (!PREFIX) {
-        if (nsplit > 1)
-            cluster_sync();
-        else
-            __syncthreads();
-        // ---- the cluster's partials and the prefix's, each CTA a share of the output
-        for (int i = split * kAcThreads + threadIdx.x; i < K::RW * D / 4; i += nsplit * kAcThreads) {
-            const int row = i / (D / 4), r = r0 + row, tt = r / a.G;
-            if (r >= a.rows || tt >= nn) continue;
-            float M = -INFINITY;
-            for (int s = 0; s < nsplit; ++s)
-                M = fmaxf(M, nsplit > 1 ? ld_cluster_f2(cluster_map(ml_mine + row, s)).x : ml_mine[row].x);
-            const int64_t at = (((int64_t)hk * a.B + b) * a.rows + r) * a.splits;
-            for (int s = 0; s < a.splits; ++s) M = fmaxf(M, a.p_ml[at + s].x);
+        if (nsplit == 1) return;
+        for (int j = threadIdx.x; j < K::RW * nsplit; j += kAcThreads) {
+            const int row = j % K::RW;
+            st_cluster_f2(cluster_map(recv_ml + split * K::RW + row, (uint32_t)(j / K::RW)), row_ml(row));
+        }
+        cluster_sync();
+        for (int i = threadIdx.x; i < per && split * per + i < kAll; i += kAcThreads) {
+            const int row = (split * per + i) / (D / 4);
+            if (r0 + row >= a.rows) continue;
+            float M = -INFINITY, sum = 0.f;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            float sum = 0.f;
-            for (int s = 0; s < nsplit + a.splits; ++s) {
-                float2 e;
-                float4 v;
-                if (s >= nsplit) {
-                    e = a.p_ml[at + s - nsplit];
-                    v = *reinterpret_cast<const float4 *>(a.p_o + (at + s - nsplit) * D + (i % (D / 4)) * 4);
-                } else if (nsplit > 1) {
-                    e = ld_cluster_f2(cluster_map(ml_mine + row, s));
-                    v = ld_cluster_f4(cluster_map(mine + i * 4, s));
-                } else {
-                    e = ml_mine[row];
-                    v = *reinterpret_cast<const float4 *>(mine + i * 4);
-                }
+#pragma unroll
+            for (int s = 0; s < kAcMaxCluster; ++s)
+                if (s < nsplit) M = fmaxf(M, recv_ml[s * K::RW + row].x);
+#pragma unroll
+            for (int s = 0; s < kAcMaxCluster; ++s) {
+                if (s >= nsplit) break;
+                const float2 e = recv_ml[s * K::RW + row];
                 if (e.y == 0.f) continue;
                 const float f = part_weight(e, M);
-                add4(acc, f, v);
+                add4(acc, f, recv[s * per + i]);
                 sum = fmaf(f, e.y, sum);
             }
-            store4<F32>(a.out + b * a.o_stream + tt * a.o_token +
-                            ((int64_t)(hk * a.G + (r - tt * a.G)) * D + (i % (D / 4)) * 4) * (F32 ? 4 : 2),
-                        acc, sum == 0.f ? 0.f : 1.f / sum);
+            finish(row, split * per + i, M, acc, sum);
         }
-        if (nsplit > 1) cluster_sync();              // the others have read this CTA's part
     }
 }
 
@@ -1076,8 +1095,9 @@ cudaError_t launch(int kind, const CachedArgs &a, unsigned *ctas, int nsplit, in
         return launch_ex(fn, *ctas, kAcThreads, K::kSmem, 1, s, a, nsplit);
     }
     auto fn = attn_cached_kernel<Q8, F32, D, NTX, false>;
-    if ((e = make_ready(&ready[kind][dev], fn, K::kSmem)) != cudaSuccess) return e;
-    return launch_ex(fn, *ctas, kAcThreads, K::kSmem, (unsigned)nsplit, s, a, nsplit);
+    const int smem = nsplit > 1 ? K::kSmemCluster : K::kSmem;
+    if ((e = make_ready(&ready[kind][dev], fn, K::kSmemCluster)) != cudaSuccess) return e;
+    return launch_ex(fn, *ctas, kAcThreads, smem, (unsigned)nsplit, s, a, nsplit);
 }
 
 // Up to here (tiles that the streams would read between them) a prefix is read by every stream's own pass: a launch and
