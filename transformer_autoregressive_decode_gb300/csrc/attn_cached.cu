@@ -643,7 +643,7 @@ __global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NTX>::kMinCtas)
     WarpPass<Q8, F32, D, NTX, PREFIX> w;
     w.init(lane);
     {
-        const int own = (len + K::TP - 1) / K::TP, step = nsplit * kAcWarps, total = nn > 0 ? own + (PREFIX ? 0 : a.pre_tiles) : 0;
+        const int own = (len + K::TP - 1) / K::TP, step = nsplit * kAcWarps, total = PREFIX ? own : r0 < nn * a.G ? own + a.pre_tiles : 0;
         const int tile = split * kAcWarps + warp;
         bool pre = !PREFIX && tile >= own && tile < total;   // the stream's own tiles, then a short prefix's
         if (pre)
@@ -773,21 +773,24 @@ __global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NTX>::kMinCtas)
 // whatever the lengths.  A warp's run covers the end of one item, whole items, the beginning of another;
 // it leaves a partial for each in slot (warp + item), which no other pair has: along the
 // list both only grow.  attn_join_kernel finds them by the same arithmetic.
-// The tiles of streams before b (`upto`) and of all, times the items of a stream.
-__device__ __forceinline__ unsigned tiles_before(const CachedArgs &a, int upto, int tp, unsigned *total) {
+// A stream's row groups with a row in use (its first rows, token by token): those of tokens that n_new leaves out read
+// nothing (fp32, 77 streams of 1 to 3 tokens of 8 rows in groups of 4: 112 us, 149 with every group).
+__device__ __forceinline__ int groups_of(const CachedArgs &a, int b, int rw) {
+    return (int)((unsigned)(clamp_new(a, b) * a.G + rw - 1) / (unsigned)rw);
+}
+
+// The tiles of all items of the streams before b (`upto`), and of all streams.
+__device__ __forceinline__ unsigned tiles_before(const CachedArgs &a, int upto, int tp, int rw, unsigned *total) {
     const int lane = threadIdx.x & 31;
     unsigned before = 0, all = 0;
 #pragma unroll 4
     for (int b = lane; b < a.B; b += 32) {
-        const unsigned n = (unsigned)tiles_of(a, b, tp);
+        const unsigned n = (unsigned)(tiles_of(a, b, tp) * groups_of(a, b, rw));
         all += n;
         if (b < upto) before += n;
     }
-    before = __reduce_add_sync(0xffffffffu, before);
-    all = __reduce_add_sync(0xffffffffu, all);
-    const unsigned per = (unsigned)(a.kvh * a.groups);
-    *total = all * per;
-    return before * per;
+    *total = __reduce_add_sync(0xffffffffu, all) * (unsigned)a.kvh;
+    return __reduce_add_sync(0xffffffffu, before) * (unsigned)a.kvh;
 }
 
 template <bool Q8, bool F32, int D, int NTX>
@@ -801,7 +804,7 @@ __global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NTX>::kMinCtas)
     pdl_wait();
     pdl_launch_dependents();                         // after the wait: see attn_join_kernel
     unsigned total;
-    tiles_before(a, 0, K::TP, &total);
+    tiles_before(a, 0, K::TP, K::RW, &total);
     Share sh;
     sh.use(total, gridDim.x * kAcWarps);
     unsigned x = sh.first(wid);
@@ -809,11 +812,10 @@ __global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NTX>::kMinCtas)
     if (x >= x1) return;                             // more warps than tiles: those behind have none
 
     // the stream that holds tile x: 32 streams a step, the running sum across the lanes
-    const unsigned per = (unsigned)(a.kvh * a.groups);
     int b = 0;
     unsigned s_b = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
-        const unsigned n = b0 + lane < a.B ? tiles_of(a, b0 + lane, K::TP) * per : 0u;
+        const unsigned n = b0 + lane < a.B ? (unsigned)(tiles_of(a, b0 + lane, K::TP) * groups_of(a, b0 + lane, K::RW) * a.kvh) : 0u;
         unsigned upto = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -834,14 +836,16 @@ __global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NTX>::kMinCtas)
     w.init(lane);
     while (x < x1) {
         const unsigned tiles = (unsigned)tiles_of(a, b, K::TP);
-        if (x >= s_b + tiles * per) {                // (a stream without tiles, too)
-            s_b += tiles * per;
+        const int groups = groups_of(a, b, K::RW);
+        const unsigned of_b = tiles * (unsigned)(groups * a.kvh);
+        if (x >= s_b + of_b) {                       // (a stream without tiles, too)
+            s_b += of_b;
             ++b;
             continue;
         }
         const int in = (int)((x - s_b) / tiles), tile0 = (int)(x - s_b - in * tiles);
         const int n = (int)min(tiles - tile0, x1 - x);
-        const int hk = in / a.groups, grp = in - hk * a.groups;
+        const int hk = in / groups, grp = in - hk * groups;
         const int len = clamp_len(__ldg(a.lengths + b), a.max_len);
         // its own tiles, then a short prefix's (two copies of the pass: a loop around one held 250 bytes a thread in memory)
         const int own = (int)tiles - a.pre_tiles, cut = min(max(own, tile0), tile0 + n);
@@ -858,7 +862,7 @@ __global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NTX>::kMinCtas)
             w.run();
         }
         __syncwarp();
-        const int64_t slot = (int64_t)b * per + in + wid;   // x only grows: so does the pair
+        const int64_t slot = (int64_t)b * a.kvh * a.groups + in + wid;   // x only grows: so does the pair
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -896,7 +900,8 @@ __global__ void __launch_bounds__(join_warps(WPR) * 32, WPR > 1 ? 2 : BATCH == 8
     // its own wait for whatever wrote them
     const int b = blockIdx.x, nn = clamp_new(a, b), tiles = tiles_of(a, b, tp);
     unsigned total;
-    const unsigned s_b = tiles_before(a, b, tp, &total);
+    const unsigned s_b = tiles_before(a, b, tp, rw, &total);
+    const int groups = groups_of(a, b, rw);
     Share sh, ws;
     sh.use(total, warps);
     int rows_all = 0, cr0 = 0;
@@ -914,7 +919,7 @@ __global__ void __launch_bounds__(join_warps(WPR) * 32, WPR > 1 ? 2 : BATCH == 8
         p.row = i0 + warp / WPR;
         const int at = min(p.row, n_rows - 1);
         p.hk = at / used, p.r = at - p.hk * used;
-        const int grp = p.r / rw, in = p.hk * a.groups + grp;
+        const int grp = p.r / rw, in = p.hk * groups + grp;
         p.in_grp = p.r - grp * rw;
         const unsigned x = s_b + in * tiles;
         const unsigned w0 = tiles ? sh.owner(x) : 0u;
@@ -1114,7 +1119,8 @@ int column_tiles(bool q8, bool f32, int d, int64_t rows, int *rw) {
     const int per = 8 / (q8 ? (f32 ? 2 : 1) : (f32 ? 4 : 2));   // rows of a tile
     int nt = rows > per ? 2 : 1;
     *rw = per * nt;
-    // more tiles, where their sums fit the registers (head_dim 64), or one part where two were
+    // more tiles, where their sums fit the registers (head_dim 64), or one part where two were; four tiles of 128 kept 230
+    // bytes a thread in memory (fp32 rows, bf16 cache, 66 streams of 12 rows: 92 us against 74 on two, which read it three times)
     if (d == 64 && rows > *rw && (f32 || !q8) && rows > (f32 ? *rw : 16))
         nt = f32 ? 4 : kOnePart + 4, *rw = f32 ? per * 4 : 32;
     else if (!f32 && !q8 && rows > *rw)
