@@ -101,3 +101,24 @@ def test_bad_verification(qd, kw):
     f = dict(p=A, ps=16, pr=8, q=None, qs=0, qr=0, ids=A, nd=None, u=A, B=1, T=1, V=8, out=A, acc=A)
     f.update(kw)
     assert qd._lib.qd_verify_drafts(*f.values(), None) == qd.QD_EINVAL
+
+
+def test_scratch_lives_as_long_as_its_address_is_noted(qd):
+    """A stream's scratch goes only when another takes its place (no such device: no call finds it)."""
+    import gc
+    import weakref
+
+    class Memory:
+        pass
+
+    ops = qd._setup_ops()
+    a, b = Memory(), Memory()
+    wa, wb = weakref.ref(a), weakref.ref(b)
+    assert ops.keep(99, 7, a, A, 256)
+    del a
+    gc.collect()
+    assert wa() is not None
+    assert ops.keep(99, 7, b, 2 * A, 512)
+    del b
+    gc.collect()
+    assert wa() is None and wb() is not None

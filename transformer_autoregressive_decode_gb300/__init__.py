@@ -684,9 +684,8 @@ def _setup_ops():
 _ops = None
 
 
-# Scratch of the calls on torch's current streams outside of captures (_qd_ops keeps the addresses and explains why that
-# is safe).  Larger needs, streams passed in, and captures take fresh memory from torch's allocator.
-_scratch: Dict[tuple, "torch.Tensor"] = {}
+# Scratch of the calls on torch's current streams outside of captures is kept by _qd_ops (which explains why that is safe).
+# Larger needs, streams passed in, and captures take fresh memory from torch's allocator.
 _SCRATCH_MOST = 128 << 20
 
 
@@ -744,9 +743,7 @@ def qd_attn_cached(q, cache: KvCache, lengths, out, n_new=None, max_length: Opti
             keep = need <= _SCRATCH_MOST and stream is None and q.is_cuda and not torch._C._cuda_isCurrentStreamCapturing()
             ws = _fresh(max(need, 1 << 20) if keep else need, q, stream)
             if keep:
-                key = (q.get_device(), torch._C._cuda_getCurrentRawStream(q.get_device()))
-                if ops.keep(*key, ws.data_ptr(), ws.numel()):
-                    _scratch[key] = ws              # a smaller one before it goes back to the stream's allocator
+                ops.keep(q.get_device(), torch._C._cuda_getCurrentRawStream(q.get_device()), ws, ws.data_ptr(), ws.numel())
             st = ops.attn(*args, ws.data_ptr(), ws.numel(), stream)
     if st != QD_OK:
         raise QDError(st, "qd_attn_cached failed")

@@ -27,13 +27,13 @@ static PyObject *t_f32, *t_bf16, *t_i32;               /* torch's types */
 static PyObject *raw_stream, *capturing;               /* its current raw stream of a device; whether that is being captured */
 static PyObject *s_shape, *s_stride, *s_dtype, *s_ptr, *s_device, *s_stream;
 
-/* Scratch of torch's current streams, one buffer per device and stream (the binding holds the tensors).  Calls on one
- * stream follow one another, and the interpreter's lock is held from the look-up to the last launch, so two host threads cannot
+/* Scratch of torch's current streams, one tensor per device and stream, held here.  Calls on one stream follow one another, and the interpreter's lock is held from the look-up to the last launch, so two host threads cannot
  * interleave theirs. */
 static struct {
     long dev;
     void *stream, *ptr;
     size_t size;
+    PyObject *tensor;
 } scratch[64];
 static int n_scratch;
 
@@ -297,17 +297,25 @@ static PyObject *py_verify(PyObject *self, PyObject *const *a, Py_ssize_t nargs)
                                     (int)B, (int)T, (int)V, (int32_t *)out, (int32_t *)acc, s));
 }
 
-/* keep(device, stream, pointer, bytes): scratch of a stream from now on; whether there was room to note it */
+/* keep(device, stream, tensor, pointer, bytes): scratch of a stream from now on, where there is room to note it.  Address
+ * and tensor change together, so another thread's call between the two cannot leave an address of freed memory. */
 static PyObject *py_keep(PyObject *self, PyObject *args) {
     long dev;
     unsigned long long stream, ptr, size;
-    if (!PyArg_ParseTuple(args, "lKKK", &dev, &stream, &ptr, &size)) return NULL;
+    PyObject *tensor, *before = NULL;
+    if (!PyArg_ParseTuple(args, "lKOKK", &dev, &stream, &tensor, &ptr, &size)) return NULL;
     int i = 0;
     while (i < n_scratch && (scratch[i].dev != dev || scratch[i].stream != (void *)(uintptr_t)stream)) ++i;
     if (i == 64) Py_RETURN_FALSE;
     scratch[i].dev = dev, scratch[i].stream = (void *)(uintptr_t)stream;
     scratch[i].ptr = (void *)(uintptr_t)ptr, scratch[i].size = (size_t)size;
-    if (i == n_scratch) ++n_scratch;
+    if (i == n_scratch)
+        ++n_scratch;
+    else
+        before = scratch[i].tensor;
+    Py_INCREF(tensor);
+    scratch[i].tensor = tensor;
+    Py_XDECREF(before);                 /* to the stream's allocator, which hands it to later work of the stream only */
     Py_RETURN_TRUE;
 }
 
