@@ -582,8 +582,9 @@ typedef struct {
  * (ties to even) to x * (127 / max|x|); a row below 2^-116 throughout is stored as zeros,
  * and one that holds an infinity or a NaN as codes 0 with a NaN scale, so that it reads
  * as NaN.  A row whose position falls outside [0, smax) is not written.  At most 65535
- * streams.  Errors:
- * QD_EINVAL (arguments, alignment, memory), QD_EUNSUPPORTED (head_dim), QD_ECUDA. */
+ * streams.  Errors: QD_EINVAL (arguments, alignment, memory; a cache whose strides or
+ * pointers lay its streams, heads, keys and values over each other), QD_EUNSUPPORTED
+ * (head_dim), QD_ECUDA. */
 qd_status qd_kv_append(const qd_kv_cache *cache, const void *k_rows_dev, const void *v_rows_dev, int dtype,
                        int n_tokens, int64_t stream_stride, int64_t token_stride, int64_t head_stride,
                        const int32_t *lengths_dev, const int32_t *n_new_dev, void *cuda_stream);
@@ -591,7 +592,7 @@ qd_status qd_kv_append(const qd_kv_cache *cache, const void *k_rows_dev, const v
 /* qd_kv_read -- the inverse: the rows that qd_kv_append with the same lengths would
  * write, read back into k_rows_dev and v_rows_dev as fp32 or bf16 (code * scale in fp32, rounded
  * to nearest even).  A row whose position falls outside [0, smax) is left as it is.
- * Layout and errors as qd_kv_append. */
+ * Layout and errors as qd_kv_append (here the rows must not lie over each other). */
 qd_status qd_kv_read(const qd_kv_cache *cache, void *k_rows_dev, void *v_rows_dev, int dtype, int n_tokens,
                      int64_t stream_stride, int64_t token_stride, int64_t head_stride, const int32_t *lengths_dev,
                      const int32_t *n_new_dev, void *cuda_stream);
@@ -620,8 +621,8 @@ qd_status qd_kv_read(const qd_kv_cache *cache, void *k_rows_dev, void *v_rows_de
  * workspace_dev: DEVICE, 256-byte aligned, qd_attn_cached_workspace bytes (0 for small
  * batches: NULL is allowed).  It is scratch of one call: calls, or captured graphs, that
  * may run at the same time need their own.  Errors: QD_EINVAL (arguments, alignment,
- * memory, workspace), QD_EUNSUPPORTED (head_dim, n_tokens, more than 2^24 query rows a
- * key head or 2^31 tiles of positions), QD_ECUDA. */
+ * memory, workspace, q = out, an out whose rows lie over each other), QD_EUNSUPPORTED (head_dim,
+ * n_tokens, more than 2^24 query rows a key head or 2^26 in all, 2^30 tiles of positions), QD_ECUDA. */
 qd_status qd_attn_cached(const qd_kv_cache *cache, const qd_kv_cache *prefix, int prefix_length, const void *q_dev,
                          int64_t q_stream_stride, int64_t q_token_stride, void *out_dev, int64_t out_stream_stride,
                          int64_t out_token_stride, int dtype, int n_tokens, int n_q_heads, float scale,

@@ -709,3 +709,63 @@ def test_the_first_call_of_a_process_may_be_captured():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST_IN_A_CAPTURE], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
+
+
+# ------------------------------------------------------------------------ the ends of the arguments
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("q8", [True, False])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("P", [0, 33])
+def test_row_groups_without_a_row_in_use(qd, dtype, q8, D, P):
+    """Runs that skip the row groups of tokens that n_new leaves out: none, one or all of a stream's in use."""
+    B, T, G, H, S = 40, 6, 8, 4, 130
+    g = gen(P + D)
+    lengths = torch.randint(0, S + 1, (B,), generator=g).tolist()
+    n_new = torch.randint(0, T + 1, (B,), generator=g).tolist()
+    n_new[:2] = n_new[-2:] = [0] * 2
+    n_new[10:13], lengths[5] = [T, 1, 0], 0
+    _check(qd, B, T, G, H, D, S, lengths, n_new, q8, dtype, P=P, p8=q8, seed=P)
+
+
+INT_MIN, INT_MAX = -2 ** 31, 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("q8", [True, False])
+def test_counts_beyond_their_ends(qd, q8):
+    """Lengths and counts are taken as the nearest end; rows outside the cache are not written."""
+    B, T, H, D, S = 5, 4, 2, 64, 40
+    g = gen(77)
+    dev, _ = _filled(g, B, H, S, D, q8)
+    before = [None if x is None else x.clone() for x in dev]
+    view = qd.KvCache(*dev)
+    rows = torch.randn((B, T, H, D), generator=g).cuda()
+    far, nn = ints([INT_MIN, INT_MAX, INT_MIN + 2, -1, S + T]), ints([INT_MAX, INT_MAX, T, 2, INT_MAX])
+    qd.qd_kv_append(view, rows, rows, far, n_new=nn)
+    back = [torch.full((B, T, H, D), 7.0, device="cuda") for _ in range(2)]
+    qd.qd_kv_read(view, far, *back, n_new=nn)
+    assert all(x is None or torch.equal(x, y) for x, y in zip(dev, before))
+    assert all(bool((x == 7.0).all()) for x in back)
+    q = torch.randn((B, T, 2 * H, D), generator=g).cuda()
+    got, want = torch.full_like(q, 7.0), torch.full_like(q, 7.0)
+    qd.qd_attn_cached(q, view, far, got, n_new=ints([INT_MAX, INT_MIN, T, 2, INT_MAX]), max_length=S)
+    qd.qd_attn_cached(q, view, ints([0, S, 0, 0, S]), want, n_new=ints([T, 0, T, 2, T]), max_length=S)
+    assert torch.equal(got, want)
+    assert bool((got[[0, 2]] == 0).all()) and bool((got[1] == 7.0).all()) and bool((got[3, 2:] == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("q8", [True, False])
+def test_queries_and_caches_shared_by_streams(qd, q8, dtype):
+    """What is only read may be broadcast: one query for all streams, one cache for all."""
+    B, T, G, H, D, S = 6, 3, 2, 2, 128, 90
+    g = gen(78)
+    dev, _ = _filled(g, 1, H, S, D, q8)
+    one = [None if x is None else x.expand(B, *x.shape[1:]) for x in dev]
+    all_ = [None if x is None else x.contiguous() for x in one]
+    q = torch.randn((1, 1, G * H, D), generator=g).to(dtype).cuda().expand(B, T, G * H, D)
+    ln = ints([90, 17, 3, 64, 65, 0])
+    got, want = (torch.empty((B, T, G * H, D), dtype=dtype, device="cuda") for _ in range(2))
+    qd.qd_attn_cached(q, qd.KvCache(*one), ln, got)
+    qd.qd_attn_cached(q.contiguous(), qd.KvCache(*all_), ln, want)
+    assert torch.equal(got, want)

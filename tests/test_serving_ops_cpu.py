@@ -23,6 +23,11 @@ def cache(qd, **kw):
     return qd.qd_kv_cache(*(f[n] for n, _ in qd.qd_kv_cache._fields_))
 
 
+def _has_device():
+    import torch
+    return torch.cuda.is_available()
+
+
 BAD_CACHE = [(dict(k=None), "EINVAL"), (dict(v=None), "EINVAL"), (dict(k_scale=None), "EINVAL"), (dict(v_scale=2), "EINVAL"),
              (dict(k=A + 8), "EINVAL"), (dict(format=2), "EINVAL"), (dict(n_streams=0), "EINVAL"), (dict(smax=0), "EINVAL"),
              (dict(n_kv_heads=0), "EINVAL"), (dict(head_dim=96), "EUNSUPPORTED"), (dict(row_stride=48), "EINVAL"),
@@ -56,6 +61,27 @@ def test_bad_rows(qd, kw):
     c = cache(qd)
     for fn in (qd._lib.qd_kv_append, qd._lib.qd_kv_read):
         assert fn(ctypes.addressof(c), *f.values(), None) == qd.QD_EINVAL
+
+
+def test_rows_over_each_other(qd):
+    """What a call writes must have places of its own; what it only reads may be shared."""
+    f = dict(k_rows=A, v_rows=2 * A, dtype=1, n=2, stream=256, token=128, head=64, lengths=A, n_new=None)
+    for kw in (dict(v_rows=A), dict(stream=0), dict(token=0), dict(head=0), dict(token=32)):
+        assert qd._lib.qd_kv_read(ctypes.addressof(cache(qd)), *dict(f, **kw).values(), None) == qd.QD_EINVAL
+    for kw in (dict(stream_stride=0), dict(head_stride=0), dict(v=A), dict(v_scale=3 * A), dict(scale_head_stride=0),
+               dict(scale_stream_stride=0)):
+        assert qd._lib.qd_kv_append(ctypes.addressof(cache(qd, **kw)), *f.values(), None) == qd.QD_EINVAL
+    g = dict(prefix=None, plen=0, q=A, qs=256, qt=128, out=2 * A, os=256, ot=128, dtype=1, n=2, heads=2, scale=1.0, lengths=A,
+             n_new=None, most=32, ws=None, wb=0)
+    for kw in (dict(out=A), dict(os=0), dict(ot=0), dict(ot=64), dict(os=64)):
+        assert qd._lib.qd_attn_cached(ctypes.addressof(cache(qd)), *dict(g, **kw).values(), None) == qd.QD_EINVAL
+    if not _has_device():                       # these pass the checks of their arguments
+        for kw in (dict(), dict(qs=0), dict(qt=0), dict(qs=0, qt=0)):
+            assert qd._lib.qd_attn_cached(ctypes.addressof(cache(qd)), *dict(g, **kw).values(), None) == qd.QD_ECUDA
+        for kw in (dict(), dict(v_rows=A), dict(stream=0), dict(head=0)):
+            assert qd._lib.qd_kv_append(ctypes.addressof(cache(qd)), *dict(f, **kw).values(), None) == qd.QD_ECUDA
+        for kw in (dict(stream_stride=0), dict(head_stride=0), dict(v=A)):
+            assert qd._lib.qd_kv_read(ctypes.addressof(cache(qd, **kw)), *f.values(), None) == qd.QD_ECUDA
 
 
 ATTN = [(dict(q=None), "EINVAL"), (dict(out=None), "EINVAL"), (dict(q=A + 8), "EINVAL"), (dict(qt=4), "EINVAL"), (dict(os=-8), "EINVAL"),

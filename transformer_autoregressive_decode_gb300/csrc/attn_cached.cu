@@ -29,7 +29,7 @@
 //  - small batches: a cluster of CTAs per (stream, key head, rows) item, one wave of them; the
 //    warps take the tiles in turn and their partial results (ref, sum, output) meet in
 //    distributed shared memory, in a fixed order.  One launch, no scratch; bound by its
-//    chain of loads (1 x 600 positions 6.8 us, as many of them the launch).
+//    chain of loads (1 x 600 positions 5.4 us, as many of them the launch).
 //  - larger ones: attn_share_kernel's equal runs over all warps and attn_join_kernel.  Bound by HBM:
 //    3 streams of up to 65536 8-bit positions, 334 MB, 57 us (0.86 of the measured rate); 64
 //    of 257 to 2048, 156 MB, 34 us (0.68: 23 for the bytes, the launches, a pipeline's start and
@@ -785,7 +785,7 @@ __device__ __forceinline__ unsigned tiles_before(const CachedArgs &a, int upto, 
     unsigned before = 0, all = 0;
 #pragma unroll 4
     for (int b = lane; b < a.B; b += 32) {
-        const unsigned n = (unsigned)(tiles_of(a, b, tp) * groups_of(a, b, rw));
+        const unsigned n = (unsigned)tiles_of(a, b, tp) * (unsigned)groups_of(a, b, rw);
         all += n;
         if (b < upto) before += n;
     }
@@ -815,7 +815,7 @@ __global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NTX>::kMinCtas)
     int b = 0;
     unsigned s_b = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
-        const unsigned n = b0 + lane < a.B ? (unsigned)(tiles_of(a, b0 + lane, K::TP) * groups_of(a, b0 + lane, K::RW) * a.kvh) : 0u;
+        const unsigned n = b0 + lane < a.B ? (unsigned)tiles_of(a, b0 + lane, K::TP) * (unsigned)(groups_of(a, b0 + lane, K::RW) * a.kvh) : 0u;
         unsigned upto = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -1191,7 +1191,7 @@ qd_status make_plan(const qd_kv_cache *cache, const qd_kv_cache *prefix, int pre
             p->inline_prefix = own <= kInlineTiles;
         if (p->inline_prefix) tiles += (int)pre;
     }
-    if (items * tiles > (1ll << 31)) return QD_EUNSUPPORTED;
+    if (items * tiles > (1ll << 30)) return QD_EUNSUPPORTED;
     // A cluster per item while the grid is one wave, or little more, and a warp's share short; longer or larger batches are
     // shared out.  (72 items, a short prefix: 576 CTAs 13.8 us, 288 10.2; 592 items of one CTA 14.6 us, shared out 18.)
     // An SM holds three CTAs at least, two of the largest variants.
@@ -1286,6 +1286,9 @@ qd_status qd_attn_cached(const qd_kv_cache *cache, const qd_kv_cache *prefix, in
     for (int64_t v : {q_stream_stride, q_token_stride, out_stream_stride, out_token_stride})
         if (v < 0 || v % unit) return QD_EINVAL;
     if (!is_aligned(q_dev, 16) || !is_aligned(out_dev, 16) || !is_aligned(lengths_dev, 4) || !is_aligned(n_new_dev, 4))
+        return QD_EINVAL;
+    if (q_dev == out_dev || !apart((int64_t)n_q_heads * cache->head_dim, 1, 0, n_tokens, out_token_stride, cache->n_streams,
+                                   out_stream_stride))
         return QD_EINVAL;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return QD_ECUDA;

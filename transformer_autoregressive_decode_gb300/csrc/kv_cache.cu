@@ -239,6 +239,16 @@ qd_status move_rows(bool read, const qd_kv_cache *cache, const void *k_rows, con
         return QD_EINVAL;
     if (!is_aligned(k_rows, 16) || !is_aligned(v_rows, 16) || !is_aligned(lengths, 4) || !is_aligned(n_new, 4))
         return QD_EINVAL;
+    // the side that is written
+    const int64_t d64 = cache->head_dim;
+    if (read ? k_rows == v_rows || !apart(d64, cache->n_kv_heads, head_stride, n_tokens, token_stride, cache->n_streams, stream_stride)
+             : cache->k == cache->v || !apart(d64, cache->n_kv_heads, cache->head_stride, cache->smax, cache->row_stride,
+                                              cache->n_streams, cache->stream_stride))
+        return QD_EINVAL;
+    if (!read && cache->format == QD_KV_Q8 &&
+        (cache->k_scale == cache->v_scale ||
+         !apart(1, cache->n_kv_heads, cache->scale_head_stride, 1, 1, cache->n_streams, cache->scale_stream_stride)))
+        return QD_EINVAL;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return QD_ECUDA;
     if ((st = check_cache(cache, dev, false)) != QD_OK) return st;

@@ -25,7 +25,7 @@ struct NewRows {
 __device__ __forceinline__ NewRows new_rows(const int32_t *lengths, const int32_t *n_new, int b, int n_tokens) {
     int n = n_new ? n_new[b] : n_tokens;
     n = n < 0 ? 0 : n > n_tokens ? n_tokens : n;
-    return {n, lengths[b] - n};
+    return {n, max(lengths[b], 0) - n};   // (below 0 all positions are, with no overflow)
 }
 
 // Device (or managed) memory of the current device.
@@ -68,6 +68,12 @@ inline qd_status check_cache(const qd_kv_cache *c, int dev, bool one_stream) {
         if (c->format == QD_KV_Q8 && (!on_device(c->k_scale, dev) || !on_device(c->v_scale, dev))) return QD_EINVAL;
     }
     return QD_OK;
+}
+
+// Rows (of d elements, heads of a token, tokens, streams) that a call writes must not lie over each other.
+inline bool apart(int64_t d, int64_t heads, int64_t head_stride, int64_t tokens, int64_t token_stride, int64_t streams,
+                  int64_t stream_stride) {
+    return (heads == 1 || head_stride >= d) && (tokens == 1 || token_stride >= d) && (streams == 1 || stream_stride >= d);
 }
 
 inline KvView kv_view(const qd_kv_cache *c) {
