@@ -769,3 +769,44 @@ def test_queries_and_caches_shared_by_streams(qd, q8, dtype):
     qd.qd_attn_cached(q, qd.KvCache(*one), ln, got)
     qd.qd_attn_cached(q.contiguous(), qd.KvCache(*all_), ln, want)
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("q8,dtype", [(True, torch.bfloat16), (False, torch.bfloat16), (True, torch.float32)])
+@pytest.mark.parametrize("captured", [False, True])
+def test_the_streams_own_pass_sees_what_was_written_just_before(qd, q8, dtype, captured):
+    """Every step writes rows, lengths and queries directly before the call over a long prefix; the same call on
+    finished inputs gives the same bits (the pass beside the prefix's must not read anything older)."""
+    B, G, H, D, S, P = 48, 2, 4, 128, 96, 2900
+    g = gen(91)
+    dev, _ = _filled(g, B, H, S, D, q8)
+    pdev, _ = _filled(g, 1, H, P, D, q8)
+    view, pre = qd.KvCache(*dev), qd.KvCache(*pdev)
+    steps = 40
+    rows = torch.randn((steps, 2, B, 1, H, D), generator=g).to(dtype).cuda()
+    qs = torch.randn((steps, B, 1, G * H, D), generator=g).to(dtype).cuda()
+    row, q = torch.empty_like(rows[0]), torch.empty_like(qs[0])
+    ln = torch.zeros((B,), dtype=torch.int32, device="cuda")
+    out, again = torch.empty_like(q), torch.empty_like(q)
+    ws = torch.empty((qd.qd_attn_cached_workspace(view, dtype == torch.bfloat16, 1, G * H, prefix=pre),), dtype=torch.uint8, device="cuda")
+    assert ws.numel() > 0
+
+    def step():
+        ln.add_(1)
+        qd.qd_kv_append(view, row[0], row[1], ln)
+        qd.qd_attn_cached(q, view, ln, out, prefix=pre, workspace=ws)
+
+    if captured:
+        step()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        ln.zero_()
+    for i in range(steps):
+        row.copy_(rows[i])
+        q.copy_(qs[i])
+        graph.replay() if captured else step()
+        torch.cuda.synchronize()
+        qd.qd_attn_cached(q, view, ln, again, prefix=pre, workspace=ws)
+        torch.cuda.synchronize()
+        assert torch.equal(out, again), i
