@@ -1,0 +1,140 @@
+"""Attention over caller-held caches, path by path: every case says which way its prefix goes (read by the
+streams' own pass, in a pass of a few rows at a time, or on the tcgen05 cores) and checks it by the workspace that the
+call asks for, so that a moved threshold fails here instead of emptying the test.  A prefix of the other format
+than the cache's is never read by the streams' own pass, whatever its length."""
+import math
+
+import pytest
+import torch
+
+from tests import _serving_ref as ref
+from tests.test_gpu_serving_ops import _filled, _spoil, gen, ints
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda(cuda_ok):
+    import __graft_entry__
+    __graft_entry__.build()
+    yield
+
+
+@pytest.fixture(scope="module")
+def qd():
+    import transformer_autoregressive_decode_gb300 as m
+    return m
+
+
+def route(qd, view, pre, P, bf16, T, QH):
+    """'inline', 'narrow' or 'wide', from the workspace: the tcgen05 kernel keeps two records of 128 rows for every SM at
+    least, the narrow pass (ref, sum) and an fp32 row for each row of the batch, key head and split, and nothing else is added."""
+    H, D = view.shape[1], view.shape[3]
+    more = qd.qd_attn_cached_workspace(view, bf16, T, QH, prefix=pre, prefix_length=P)
+    none = qd.qd_attn_cached_workspace(view, bf16, T, QH)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    if more - none >= 2 * sms * 128 * (8 + 4 * D):
+        return "wide"
+
+    def up(n):
+        return (n + 255) // 256 * 256
+    rows = H * view.shape[0] * T * (QH // H)
+    if more - none in [up(rows * s * 8) + up(rows * s * 4 * D) for s in range(1, 33)]:
+        return "narrow"
+    return "inline"
+
+
+def bound(want, mag, spread, n, D, dtype, q8, wide=False):
+    """ref.attend_bound with the bits that qd.h promises for the probabilities at any number of rows: 16 over bf16
+    rows (two bf16 parts) and 22 over 8-bit rows (two fp16 parts) for bf16 queries.  The floor of 8-bit rows as there:
+    the spacing of fp16's smallest numbers, against a largest weight of 2^10, of 2^2 where `wide`."""
+    mag, top = mag[..., :D], mag[..., D:]
+    bf16 = dtype == torch.bfloat16
+    step = torch.finfo(dtype).eps / 2
+    part_p, part_q = (2.0 ** -22, 0.0 if bf16 else 2.0 ** -22) if q8 else (2.0 ** -16, 0.0) if bf16 else (2.0 ** -24, 2.0 ** -24)
+    ds = spread * (part_q + (D + 8) * 2.0 ** -23)
+    rel = 2 * part_p + 2 * torch.expm1(2 * ds) + 2.0 ** -20 + 2 * (n + 64) * 2.0 ** -23
+    floor = n * 2.0 ** (-27 if wide else -35) * top if q8 else 0.0
+    return step * (out_abs(want) + mag * rel) + mag * rel + floor * 1.01 + 1e-30
+
+
+def out_abs(x):
+    return torch.nan_to_num(x).abs()
+
+
+def run(qd, way, B, T, G, H, D, S, lengths, n_new, q8, dtype, P=0, p8=None, seed=0, q_scale=1.0, change=None):
+    """A call of this way against the 64-bit form; `change` may alter (dev, values) of cache and prefix."""
+    g = gen(seed)
+    dev, kv = _filled(g, B, H, S, D, q8)
+    pdev, pkv = _filled(g, 1, H, P + 3, D, p8) if P else (None, None)
+    if change:
+        change(dev, kv, pdev, pkv)
+    _spoil(dev, lengths, S)
+    nn = [min(n, T) for n in n_new] if n_new else [T] * B
+    q = (torch.randn((B, T, G * H, D), generator=g) * q_scale).to(dtype)
+    for b in range(B):
+        q[b, nn[b]:] = math.nan
+    view, pre, pk, pv = qd.KvCache(*dev), None, None, None
+    if P:
+        _spoil(pdev, [P], P + 3)
+        pre, pk, pv = qd.KvCache(*pdev), pkv[0][0, :, :P], pkv[1][0, :, :P]
+        assert route(qd, view, pre, P, dtype == torch.bfloat16, T, G * H) == way
+    out = torch.full((B, T, G * H, D), 7.0, dtype=dtype, device="cuda")
+    qd.qd_attn_cached(q.cuda(), view, ints(lengths), out, n_new=ints(n_new) if n_new else None, prefix=pre,
+                      prefix_length=P if P else None)
+    torch.cuda.synchronize()
+    want, mag, spread = ref.attend(q, kv[0], kv[1], lengths, nn, D ** -0.5, pk, pv)
+    got, unused = out.cpu().double(), torch.isnan(want)
+    assert torch.equal(got[unused], torch.full_like(got[unused], 7.0))
+    n = max(lengths) + P
+    tol = bound(want, mag, spread, n, D, dtype, q8)
+    if P:
+        tol = torch.maximum(tol, bound(want, mag, spread, n, D, dtype, p8, way == "wide"))
+    bad = ~((got - want).abs() <= tol) & ~unused
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} off, worst {float(((got - want).abs() / tol)[~unused].max()):.3g} of the bound"
+
+
+# ------------------------------------------------- the probabilities keep their bits at any number of rows
+
+def cancel(dev, kv, pdev, pkv):
+    """Position 2 i + 1's value is the negative of position 2 i's (codes, or bf16): every result is a small difference of large
+    terms, where it shows if probabilities were cut short."""
+    for parts, values in ((dev, kv), (pdev, pkv)):
+        if parts is None:
+            continue
+        n = parts[1].shape[2] // 2 * 2
+        parts[1][:, :, 1:n:2] = -parts[1][:, :, :n:2]
+        if parts[3] is not None:
+            parts[3][:, :, 1:n:2] = parts[3][:, :, :n:2]
+        values[1][:, :, 1:n:2] = -values[1][:, :, :n:2]
+
+
+@pytest.mark.parametrize("q8", [True, False])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T,G", [(1, 2), (1, 8), (4, 2), (3, 5), (9, 8)])
+def test_terms_that_cancel_over_own_caches(qd, q8, D, T, G):
+    lengths = [20, 8, 12, 2, 16, 10]
+    run(qd, None, 6, T, G, 2, D, 20, lengths, [min(T, n) for n in lengths], q8, torch.bfloat16, seed=T + 9, q_scale=0.05, change=cancel)
+
+
+@pytest.mark.parametrize("p8", [True, False])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("way,B,T,G", [("narrow", 3, 1, 2), ("narrow", 12, 1, 2)])
+def test_terms_that_cancel_over_a_prefix(qd, p8, D, way, B, T, G):
+    run(qd, way, B, T, G, 2, D, 8, [0] * B, None, not p8, torch.bfloat16, P=20, p8=p8, seed=B + 9, q_scale=0.05, change=cancel)
+
+
+@pytest.mark.parametrize("q8", [True, False])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T,G", [(1, 2), (4, 2), (3, 3), (4, 4), (5, 8), (9, 8)])
+def test_probabilities_over_own_caches(qd, q8, D, T, G):
+    """2 to 72 rows a key head, few positions: where an element's terms cancel, a part that was left out shows."""
+    lengths = [20, 7, 12, 2, 16, 9]
+    run(qd, None, 6, T, G, 2, D, 20, lengths, [min(T, n) for n in lengths], q8, torch.bfloat16, seed=T)
+
+
+@pytest.mark.parametrize("p8", [True, False])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,T,G", [(3, 1, 2), (12, 1, 2), (3, 3, 5)])
+def test_probabilities_over_a_prefix_of_few_rows(qd, p8, D, B, T, G):
+    run(qd, "narrow", B, T, G, 2, D, 8, [0] * B, None, not p8, torch.bfloat16, P=20, p8=p8, seed=B)

@@ -11,8 +11,9 @@
 // Decoding has few rows and many positions, so the positions are the long side (M = 16) of
 // m16n8k16 and the rows its N = 8 columns.  Where a value must keep more bits than the
 // tensor core's type has, it takes C columns, one per part (q and p alike; the parts'
-// products are added afterwards): 8-bit cache, fp16: bf16 rows 1 part, fp32 rows 2; bf16
-// cache: 2 parts (hi, lo of p; one from 9 rows on), fp32 rows 3 of 4 columns.
+// products are added afterwards): fp32 rows 2 fp16 parts over an 8-bit cache, 3 bf16 parts of 4 columns over
+// a bf16 one.  bf16 rows have one part of q and two of p (16 bits of bf16, 22 of fp16), in two columns for up to 8 rows of a
+// bf16 cache, else in one column each and two products (hi, then lo) into the same sums.
 //
 // Neither K nor V is laid out anew in shared memory.  The products' sums run over head_dim
 // (scores) and positions (output) in any order, so each lane takes 16 contiguous bytes of a
@@ -31,7 +32,7 @@
 //    distributed shared memory, in a fixed order.  One launch, no scratch; bound by its
 //    chain of loads (1 x 600 positions 5.4 us, as many of them the launch).
 //  - larger ones: attn_share_kernel's equal runs over all warps and attn_join_kernel.  Bound by HBM:
-//    3 streams of up to 65536 8-bit positions, 334 MB, 57 us (0.86 of the measured rate); 64
+//    3 streams of up to 65536 8-bit positions, 334 MB, 58 us (0.85 of the measured rate); 64
 //    of 257 to 2048, 156 MB, 34 us (0.68: 23 for the bytes, the launches, a pipeline's start and
 //    the join the rest).
 //  - a prefix: read by every stream's own pass while that is cheap, else by
@@ -68,12 +69,15 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
     return d;
 }
-// NTX: tiles of 8 columns, plus kOnePart for bf16 rows over a bf16 cache whose probabilities are one bf16 part
-// (half a step 2^-8 of each, at random): from 9 rows on, where it halves the passes over the cache.
-constexpr int kOnePart = 8;
+// NTX: tiles of 8 columns, plus kOneColumn for bf16 rows over a bf16 cache with a column a row: from 9 rows on, where it
+// halves the passes over the cache.  Where a row has one column (over 8-bit rows, too) each step makes two products for the
+// output, one per part of p: 16 streams of 64 rows over 4000 bf16 positions 71 us, 67 with the first part alone, which
+// keeps 8 bits (11 of fp16); of 16 rows over 8-bit positions 34.6 and 33.6; 64 ragged 8-bit streams 34.6 and 33.9.
+constexpr int kOneColumn = 8;
 template <bool Q8, bool F32, int D, int NTX> struct AcCfg {
     static constexpr int NT = NTX & 7;
-    static constexpr int C = Q8 ? (F32 ? 2 : 1) : F32 ? 4 : NTX & kOnePart ? 1 : 2;   // columns per row
+    static constexpr int C = Q8 ? (F32 ? 2 : 1) : F32 ? 4 : NTX & kOneColumn ? 1 : 2;   // columns per row
+    static constexpr int PP = C == 1 ? 2 : 1;                      // products of the output, one per part of p
     static constexpr int RW = 8 * NT / C;                          // rows per CTA
     static constexpr int ES = Q8 ? 1 : 2;
     static constexpr int KP = D * ES / 64;                         // 16-byte pieces of a K row per lane
@@ -374,8 +378,8 @@ template <bool Q8, bool F32, int D, int NTX, bool PREFIX> struct WarpPass {
         }
     }
 
-    // Output: rows (dims) of V^T of one block against its probabilities
-    __device__ __forceinline__ void output(const uint8_t *sv, const uint32_t (&pb)[NT][2], int p0) {
+    // Output: rows (dims) of V^T of one block against its probabilities (their parts)
+    __device__ __forceinline__ void output(const uint8_t *sv, const uint32_t (&pb)[K::PP][NT][2], int p0) {
         if constexpr (Q8) {
             constexpr int VW = D / 32;
             uint32_t v[4][VW];
@@ -401,7 +405,9 @@ template <bool Q8, bool F32, int D, int NTX, bool PREFIX> struct WarpPass {
                     const uint32_t f[4] = {codes_f16<false>(y, 0x4140), codes_f16<false>(y, 0x4342),
                                            codes_f16<false>(z, 0x4140), codes_f16<false>(z, 0x4342)};
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma16816_f16(o[2 * w + hh][nt], f, pb[nt][0], pb[nt][1]);
+                    for (int pp = 0; pp < K::PP; ++pp)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma16816_f16(o[2 * w + hh][nt], f, pb[pp][nt][0], pb[pp][nt][1]);
                 }
             }
         } else {
@@ -438,7 +444,8 @@ template <bool Q8, bool F32, int D, int NTX, bool PREFIX> struct WarpPass {
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             float acc[4] = {o[w][nt][0], o[w][nt][1], o[w][nt][2], o[w][nt][3]};
-                            mma16816(acc, fm, pb[nt][0], pb[nt][1]);
+#pragma unroll
+                            for (int pp = 0; pp < K::PP; ++pp) mma16816(acc, fm, pb[pp][nt][0], pb[pp][nt][1]);
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
                                 if (lim[nt][HC == 2 ? e & 1 : 0] == cut) o[w][nt][e] = acc[e];
@@ -446,7 +453,9 @@ template <bool Q8, bool F32, int D, int NTX, bool PREFIX> struct WarpPass {
                     }
                 } else {
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma16816(o[w][nt], f, pb[nt][0], pb[nt][1]);
+                    for (int pp = 0; pp < K::PP; ++pp)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma16816(o[w][nt], f, pb[pp][nt][0], pb[pp][nt][1]);
                 }
             }
         }
@@ -541,7 +550,7 @@ template <bool Q8, bool F32, int D, int NTX, bool PREFIX> struct WarpPass {
             for (int k = 0; k < HC; ++k) rf[nt][k] = ref[nt][k] == -INFINITY ? 0.f : ref[nt][k];
 #pragma unroll
         for (int u = 0; u < K::SUB; ++u) {
-            uint32_t pb[NT][2];
+            uint32_t pb[K::PP][NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -560,6 +569,9 @@ template <bool Q8, bool F32, int D, int NTX, bool PREFIX> struct WarpPass {
                     uint32_t y;
                     if constexpr (C == 1) {
                         y = Q8 ? pack_f16(w[0], w[1]) : pack_bf16(w[0], w[1]);
+                        const float2 hi = Q8 ? __half22float2(*reinterpret_cast<const __half2 *>(&y))
+                                             : make_float2(bf16lo(y), bf16hi(y));
+                        pb[K::PP - 1][nt][hh] = movmatrix(Q8 ? pack_f16(w[0] - hi.x, w[1] - hi.y) : pack_bf16(w[0] - hi.x, w[1] - hi.y));
                     } else if constexpr (Q8) {
                         const float hi = f16_of(w[0]);
                         y = pack_f16(hi, w[0] - hi);
@@ -570,7 +582,7 @@ template <bool Q8, bool F32, int D, int NTX, bool PREFIX> struct WarpPass {
                         const float hi = bf16_of(w[0]), mid = bf16_of(w[0] - hi);
                         y = t & 1 ? pack_bf16(w[0] - hi - mid, 0.f) : pack_bf16(hi, mid);
                     }
-                    pb[nt][hh] = movmatrix(y);
+                    pb[0][nt][hh] = movmatrix(y);
                 }
             output(st + u * K::kBlock + K::kV, pb, p0 + 16 * u);
         }
@@ -1131,12 +1143,12 @@ int column_tiles(bool q8, bool f32, int d, int64_t rows, int *rw) {
     const int per = 8 / (q8 ? (f32 ? 2 : 1) : (f32 ? 4 : 2));   // rows of a tile
     int nt = rows > per ? 2 : 1;
     *rw = per * nt;
-    // more tiles, where their sums fit the registers (head_dim 64), or one part where two were; four tiles of 128 kept 230
+    // more tiles, where their sums fit the registers (head_dim 64), or one column where two were; four tiles of 128 kept 230
     // bytes a thread in memory (fp32 rows, bf16 cache, 66 streams of 12 rows: 92 us against 74 on two, which read it three times)
     if (d == 64 && rows > *rw && (f32 || !q8) && rows > (f32 ? *rw : 16))
-        nt = f32 ? 4 : kOnePart + 4, *rw = f32 ? per * 4 : 32;
+        nt = f32 ? 4 : kOneColumn + 4, *rw = f32 ? per * 4 : 32;
     else if (!f32 && !q8 && rows > *rw)
-        nt = kOnePart + 2, *rw = 16;
+        nt = kOneColumn + 2, *rw = 16;
     return nt;
 }
 
@@ -1146,8 +1158,8 @@ cudaError_t dispatch(int kind, bool q8, bool f32, int d, int nt, const CachedArg
     if (q8 == Q && f32 == F && d == DD && nt == (N)) return launch<Q, F, DD, (N)>(kind, a, ctas, nsplit, dev, s, plan);
 #define QD_AC2(Q, F) QD_AC(Q, F, 64, 1) QD_AC(Q, F, 64, 2) QD_AC(Q, F, 128, 1) QD_AC(Q, F, 128, 2)
     QD_AC2(false, false) QD_AC2(false, true) QD_AC2(true, false) QD_AC2(true, true)
-    QD_AC(false, false, 64, kOnePart + 2) QD_AC(false, false, 128, kOnePart + 2)
-    QD_AC(false, false, 64, kOnePart + 4) QD_AC(false, true, 64, 4) QD_AC(true, true, 64, 4)
+    QD_AC(false, false, 64, kOneColumn + 2) QD_AC(false, false, 128, kOneColumn + 2)
+    QD_AC(false, false, 64, kOneColumn + 4) QD_AC(false, true, 64, 4) QD_AC(true, true, 64, 4)
 #undef QD_AC2
 #undef QD_AC
     return cudaErrorInvalidValue;
