@@ -119,7 +119,7 @@ def test_terms_that_cancel_over_own_caches(qd, q8, D, T, G):
 
 @pytest.mark.parametrize("p8", [True, False])
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("way,B,T,G", [("narrow", 3, 1, 2), ("narrow", 12, 1, 2)])
+@pytest.mark.parametrize("way,B,T,G", [("narrow", 3, 1, 2), ("narrow", 12, 1, 2), ("wide", 24, 1, 2), ("wide", 40, 4, 2)])
 def test_terms_that_cancel_over_a_prefix(qd, p8, D, way, B, T, G):
     run(qd, way, B, T, G, 2, D, 8, [0] * B, None, not p8, torch.bfloat16, P=20, p8=p8, seed=B + 9, q_scale=0.05, change=cancel)
 
@@ -138,3 +138,10 @@ def test_probabilities_over_own_caches(qd, q8, D, T, G):
 @pytest.mark.parametrize("B,T,G", [(3, 1, 2), (12, 1, 2), (3, 3, 5)])
 def test_probabilities_over_a_prefix_of_few_rows(qd, p8, D, B, T, G):
     run(qd, "narrow", B, T, G, 2, D, 8, [0] * B, None, not p8, torch.bfloat16, P=20, p8=p8, seed=B)
+
+
+@pytest.mark.parametrize("p8", [True, False])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,T,G", [(24, 1, 2), (64, 1, 2), (40, 4, 2)])
+def test_probabilities_over_a_prefix_of_many_rows(qd, p8, D, B, T, G):
+    run(qd, "wide", B, T, G, 2, D, 8, [0] * B, None, not p8, torch.bfloat16, P=20, p8=p8, seed=B)

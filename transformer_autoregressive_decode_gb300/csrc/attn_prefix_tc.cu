@@ -5,26 +5,25 @@
 // come in chunks of 128.  A CTA has two halves, each with a tile of its own in flight (S, P and O in tensor
 // memory), so that the tensor core works for one half while the other takes its softmax:
 //   S = Q K^T          128 x 128 fp32 in tensor memory; Q and K from shared memory
-//   softmax            thread = row: maximum, then P = 2^(s - ref) packed to 16 bits over S's own columns
-//   O += P V           P from tensor memory, V from shared memory (keys x dims: the MN-major operand)
+//   softmax            thread = row: P = 2^(s - ref) as two 16-bit parts over S's own columns, 32 keys at a time
+//   O += P V           P's parts from tensor memory, V from shared memory (keys x dims: the MN-major operand)
 // With more than 128 rows the halves take two tiles of rows over the same chunks (K and V are shared);
 // otherwise both take the one tile, every other chunk each.  The list (key head, tile pair, chunk) is cut into equal
 // runs, one per CTA; each leaves (ref, sum, O) of its rows for attn_join_kernel.
 //
-// bf16 prefix: P is one bf16 part (half a step 2^-8 of each probability, at random; a second part would add half the MMA
-// time again).  8-bit prefix: the codes are widened to fp16, exactly, on their way into shared
-// memory; the keys' scales multiply S's columns, the values' scales P's, and P is fp16 (2^-11).
+// bf16 prefix: P is two bf16 parts (16 bits).  8-bit prefix: the codes are widened to fp16, exactly, on their way into shared
+// memory; the keys' scales multiply S's columns, the values' scales P's, and P is two fp16 parts (22 bits).  32 keys'
+// scores stand in 32 columns, and so do their parts: 16 columns of the first, 16 of the second.
 //
-// A chunk's probabilities are formed with the reference as it stands, the scores left where they are, and written
-// over them only when none has outgrown its room; otherwise the maximum is taken first (rescaling O in tensor
-// memory: the half's previous O product has finished when its next S has).
-// So the scores are usually read once: the exponentials' rate (16 a clock and SM) allows 128 x 128 in 1024
-// clocks, as long as their two products take.
+// 64 keys' probabilities are formed with the reference as it stands and written over their scores when none has outgrown
+// its room (32 keys at a time, a vote each, took 150 us where this takes 142); otherwise the reference moves first, with O in
+// tensor memory (the half's previous O product has finished when its next S has) and what the chunk has written so
+// far.  So the scores are usually read once.
 //
-// Measured: 16384 8-bit positions under 768 of 1536 rows and 8 key heads, 52.7 GFLOP, 70 us (0.75 PFLOP/s, 0.39 of
-// the measured bf16 rate).  A pair of chunks takes 4900 clocks where the products need 2048: a half's
-// softmax (2000 to 2300 with two warps a scheduler) and its two products follow one another, and S and O of two
-// halves fill the tensor memory, so there is no third to put between.
+// Measured: 16384 8-bit positions under 768 of 1536 rows and 8 key heads, 52.7 GFLOP (79 with P's second part), 89 us a
+// call with next to no own caches, 71 with one part, which keeps 11 bits (8 of bf16).  A pair of chunks takes some 6000
+// clocks where the products need 3072 and the exponentials' units (16 a clock and SM) 2048: a half's softmax and its
+// two products follow one another, and S and O of two halves fill the tensor memory of head_dim 128.
 //
 // Roles (512 threads): warps 0-3 and 4-7 the softmax of the two halves (a row each, also Q and the results),
 // warps 8-11 load K and V, warp 12 owns the tensor memory and issues the MMAs, warps 13-15 only complete its
@@ -126,84 +125,73 @@ __device__ __forceinline__ uint32_t swz(int r, int c) { return (uint32_t)(r * 12
 template <bool Q8> constexpr float kWtUp = Q8 ? 2.f : 0.f;
 template <bool Q8> constexpr float kWtTop = Q8 ? 32768.f : 1.e18f;
 
-// The largest score of a row's first keys (32 for a first guess, or all of a chunk) in log2 units, with the values' scales: the
-// largest weight.
-template <bool Q8> __device__ __forceinline__ float largest(uint32_t tS, const float *sc, float cs, int left, int keys) {
+// The largest weight, in log2 units, that 32 keys (`left` of them there) have in a row.
+template <bool Q8> __device__ __forceinline__ float largest(const uint32_t (&x)[32], const float *sc, float cs, int left) {
     float m = -INFINITY;
-    const int n = min(left, keys);
-#pragma unroll 1
-    for (int q = 0; q < keys; q += 32) {
-        float s[32];
-        ld32(tS + q, s);
 #pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-            if constexpr (Q8) {
-                const float4 k = *reinterpret_cast<const float4 *>(sc + q + e), v = *reinterpret_cast<const float4 *>(sc + 256 + q + e);
-                s[e] = fmaf(s[e] * k.x, cs, v.x), s[e + 1] = fmaf(s[e + 1] * k.y, cs, v.y);
-                s[e + 2] = fmaf(s[e + 2] * k.z, cs, v.z), s[e + 3] = fmaf(s[e + 3] * k.w, cs, v.w);
-            } else {
-                s[e] *= cs, s[e + 1] *= cs, s[e + 2] *= cs, s[e + 3] *= cs;
-            }
-        }
-        if (n - q < 32) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-                if (q + e >= n) s[e] = -INFINITY;
-        }
-#pragma unroll
-        for (int e = 0; e < 32; ++e) m = fmaxf(m, s[e]);
+    for (int e = 0; e < 32; ++e) {
+        float s = __uint_as_float(x[e]);
+        s = Q8 ? fmaf(s * sc[e], cs, sc[256 + e]) : s * cs;
+        m = fmaxf(m, e < left ? s : -INFINITY);
     }
     return m;
 }
 
-// A row's chunk against its reference: the weights of the product packed to 16 bits, the largest of them, and the sum of the
+// 32 keys of a row against its reference: the weights of the product, the largest of them, and the sum of the
 // probabilities.  A weight past kWtTop means that the reference has to move.
 template <bool Q8, bool EDGE>
-__device__ __forceinline__ void weigh(uint32_t tS, const float *sc, float cs, float ref, int left, uint32_t (&out)[64],
+__device__ __forceinline__ void weigh(const uint32_t (&x)[32], const float *sc, float cs, float ref, int left, float (&w)[32],
                                       float &top, float &sum) {
     const float rf = ref == -INFINITY ? 0.f : ref;
     const uint64_t cs2 = pk(cs, cs), rf2 = pk(-rf, -rf);
     uint64_t l2 = pk(0.f, 0.f);
     float t0 = 0.f, t1 = 0.f;
-    uint32_t u[2][32];                              // the next 32 keys' scores arrive while these are worked
-    ld32_start(tS, u[0]);
-    tc_wait_ld_u32<32>(u[0]);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        if (q < 3) ld32_start(tS + 32u * (q + 1), u[(q + 1) & 1]);
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-            const uint32_t *x = u[q & 1] + e;
-            uint64_t x0 = pk(__uint_as_float(x[0]), __uint_as_float(x[1])), x1 = pk(__uint_as_float(x[2]), __uint_as_float(x[3]));
-            const int key = 32 * q + e;
-            if constexpr (Q8) {
-                const ulonglong2 k = *reinterpret_cast<const ulonglong2 *>(sc + key);
-                x0 = mul2(x0, k.x), x1 = mul2(x1, k.y);
-            }
-            float s0, s1, s2, s3;
-            unpk(fma2(x0, cs2, rf2), s0, s1);
-            unpk(fma2(x1, cs2, rf2), s2, s3);
-            s0 = ex2(s0), s1 = ex2(s1), s2 = ex2(s2), s3 = ex2(s3);
-            if constexpr (EDGE) {
-                s0 = key < left ? s0 : 0.f, s1 = key + 1 < left ? s1 : 0.f;
-                s2 = key + 2 < left ? s2 : 0.f, s3 = key + 3 < left ? s3 : 0.f;
-            }
-            x0 = pk(s0, s1), x1 = pk(s2, s3);
-            l2 = add2(l2, add2(x0, x1));
-            if constexpr (Q8) {
-                const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(sc + 128 + key);
-                unpk(mul2(x0, v.x), s0, s1);
-                unpk(mul2(x1, v.y), s2, s3);
-            }
-            t0 = fmaxf(t0, fmaxf(s0, s1)), t1 = fmaxf(t1, fmaxf(s2, s3));
-            out[key / 2] = Q8 ? pack_f16(s0, s1) : pack_bf16(s0, s1);
-            out[key / 2 + 1] = Q8 ? pack_f16(s2, s3) : pack_bf16(s2, s3);
+    for (int e = 0; e < 32; e += 4) {
+        uint64_t x0 = pk(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), x1 = pk(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+        if constexpr (Q8) {
+            const ulonglong2 k = *reinterpret_cast<const ulonglong2 *>(sc + e);
+            x0 = mul2(x0, k.x), x1 = mul2(x1, k.y);
         }
-        if (q < 3) tc_wait_ld_u32<32>(u[(q + 1) & 1]);
+        float s0, s1, s2, s3;
+        unpk(fma2(x0, cs2, rf2), s0, s1);
+        unpk(fma2(x1, cs2, rf2), s2, s3);
+        s0 = ex2(s0), s1 = ex2(s1), s2 = ex2(s2), s3 = ex2(s3);
+        if constexpr (EDGE) {
+            s0 = e < left ? s0 : 0.f, s1 = e + 1 < left ? s1 : 0.f;
+            s2 = e + 2 < left ? s2 : 0.f, s3 = e + 3 < left ? s3 : 0.f;
+        }
+        x0 = pk(s0, s1), x1 = pk(s2, s3);
+        l2 = add2(l2, add2(x0, x1));
+        if constexpr (Q8) {
+            const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(sc + 128 + e);
+            unpk(mul2(x0, v.x), s0, s1);
+            unpk(mul2(x1, v.y), s2, s3);
+        }
+        t0 = fmaxf(t0, fmaxf(s0, s1)), t1 = fmaxf(t1, fmaxf(s2, s3));
+        w[e] = s0, w[e + 1] = s1, w[e + 2] = s2, w[e + 3] = s3;
     }
     float l0, l1;
     unpk(l2, l0, l1);
     sum = l0 + l1, top = fmaxf(t0, t1);
+}
+
+// A pair of weights as two 16-bit parts each, and back.
+template <bool Q8> __device__ __forceinline__ float2 pair_of(uint32_t y) {
+    return Q8 ? __half22float2(*reinterpret_cast<const __half2 *>(&y)) : make_float2(bf16lo(y), bf16hi(y));
+}
+template <bool Q8> __device__ __forceinline__ void parts(float a, float b, uint32_t &hi, uint32_t &lo) {
+    hi = Q8 ? pack_f16(a, b) : pack_bf16(a, b);
+    const float2 h = pair_of<Q8>(hi);
+    lo = Q8 ? pack_f16(a - h.x, b - h.y) : pack_bf16(a - h.x, b - h.y);
+}
+// 32 weights over the columns of their scores
+template <bool Q8> __device__ __forceinline__ void put_weights(uint32_t taddr, const float (&w)[32]) {
+    uint32_t y[32];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) parts<Q8>(w[2 * e], w[2 * e + 1], y[e], y[16 + e]);
+    tc_st16(taddr, y);
+    tc_st16(taddr + 16u, y + 16);
 }
 
 // One lane of a converged warp, always the same.
@@ -475,7 +463,10 @@ __global__ void __launch_bounds__(kWtThreads, 1) attn_prefix_tc_kernel(const Cac
                 if (elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < kWideKeys / 16; ++ks)
-                        tc_mma_ts(d, p + 8u * ks, v + ks * 128, idesc_o, ks ? 1u : (i >= 2 ? 1u : 0u));
+#pragma unroll
+                        for (int part = 0; part < 2; ++part)
+                            tc_mma_ts(d, p + 32u * (ks >> 1) + 8u * (ks & 1) + 16u * part, v + ks * 128, idesc_o,
+                                      (ks | part) ? 1u : (i >= 2 ? 1u : 0u));
                     if (!pairs || h) tc_commit(&v_empty[st]);
                     if (i + 2 >= N) tc_commit(&o_done[h]);
                 }
@@ -576,13 +567,42 @@ __global__ void __launch_bounds__(kWtThreads, 1) attn_prefix_tc_kernel(const Cac
                 ++ns;
                 if constexpr (Q8) ok = ok && wt_wait(&v_full[st], (uint32_t)((kc + c) >> 1) & 1u, bad);
                 tc_fence_after();
-                uint32_t pr[64];                    // the probabilities, packed
-                float top, sum;
-                const bool edge = left < kWideKeys;
-                // a half's first chunk sets the reference by its first 32 keys, which is near enough as a rule
-                for (int turn = i < 2 ? 0 : 1;; ++turn) {
-                    if (turn != 1) {
-                        const float m = largest<Q8>(tS, sc, cs, left, turn ? kWideKeys : 32);
+                // 64 keys at a time; the next ones' scores arrive while these are packed
+                uint32_t x[2][2][32];
+                ld32_start(tS, x[0][0]);
+                ld32_start(tS + 32u, x[0][1]);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const uint32_t tq = tS + 64u * q;
+                    const int here = left - 64 * q; // keys there
+                    const float *scq = sc + 64 * q;
+                    float w[2][32], top, sum;
+                    auto weigh_all = [&](const uint32_t (&y)[2][32]) {
+                        float t1, s1;
+                        if (here < 64) {
+                            weigh<Q8, true>(y[0], scq, cs, ref, here, w[0], top, sum);
+                            weigh<Q8, true>(y[1], scq + 32, cs, ref, here - 32, w[1], t1, s1);
+                        } else {
+                            weigh<Q8, false>(y[0], scq, cs, ref, here, w[0], top, sum);
+                            weigh<Q8, false>(y[1], scq + 32, cs, ref, here, w[1], t1, s1);
+                        }
+                        top = fmaxf(top, t1), sum += s1;
+                    };
+                    tc_wait_ld_u32<32>(x[q][0]);
+                    tc_wait_ld_u32<32>(x[q][1]);
+                    // a half's first keys set the reference, which is near enough as a rule
+                    bool move = q == 0 && i < 2;
+                    if (!move) {
+                        weigh_all(x[q]);
+                        move = __any_sync(0xffffffffu, top > kWtTop<Q8> || ref == -INFINITY);
+                    }
+                    if (move) {
+                        uint32_t y[2][32];          // the scores again: they stand until their weights are written
+                        ld32_start(tq, y[0]);
+                        ld32_start(tq + 32u, y[1]);
+                        tc_wait_ld_u32<32>(y[0]);
+                        tc_wait_ld_u32<32>(y[1]);
+                        const float m = fmaxf(largest<Q8>(y[0], scq, cs, here), largest<Q8>(y[1], scq + 32, cs, here - 32));
                         // this half's earlier O products are done: its next S, which came behind them, is
                         float f = 1.f;
                         if (m - kWtUp<Q8> > ref) {
@@ -592,28 +612,39 @@ __global__ void __launch_bounds__(kWtThreads, 1) attn_prefix_tc_kernel(const Cac
                         }
                         if (i >= 2) {
 #pragma unroll 1
-                            for (int q = 0; q < D / 32; ++q) {
+                            for (int c = 0; c < D / 32; ++c) {
                                 float v[32];
                                 uint32_t u[32];
-                                ld32(tO + 32u * q, v);
+                                ld32(tO + 32u * c, v);
 #pragma unroll
                                 for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(v[e] * f);
-                                tc_st16(tO + 32u * q, u);
-                                tc_st16(tO + 32u * q + 16u, u + 16);
+                                tc_st16(tO + 32u * c, u);
+                                tc_st16(tO + 32u * c + 16u, u + 16);
                             }
                         }
-                    }
-                    if (edge)
-                        weigh<Q8, true>(tS, sc, cs, ref, left, pr, top, sum);
-                    else
-                        weigh<Q8, false>(tS, sc, cs, ref, left, pr, top, sum);
-                    if (turn >= 2 || !__any_sync(0xffffffffu, top > kWtTop<Q8> || ref == -INFINITY)) break;
-                    if (turn == 0) turn = 1;         // next: the whole chunk's maximum
-                }
-                l += sum;
-                // over the first half of the scores' columns, all of which have been read
+                        // and the chunk's weights so far
+                        if (q > 0) tc_wait_st();
+#pragma unroll 1
+                        for (int c = 0; c < 2 * q; ++c) {
+                            float v[32];
+                            uint32_t u[32];
+                            ld32(tS + 32u * c, v);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) tc_st16(tS + 16u * q, pr + 16 * q);
+                            for (int e = 0; e < 16; ++e) {
+                                const float2 a0 = pair_of<Q8>(__float_as_uint(v[e])), a1 = pair_of<Q8>(__float_as_uint(v[16 + e]));
+                                parts<Q8>((a0.x + a1.x) * f, (a0.y + a1.y) * f, u[e], u[16 + e]);
+                            }
+                            tc_st16(tS + 32u * c, u);
+                            tc_st16(tS + 32u * c + 16u, u + 16);
+                        }
+                        weigh_all(y);
+                    }
+                    l += sum;
+                    put_weights<Q8>(tq, w[0]);
+                    if (q == 0) ld32_start(tS + 64u, x[1][0]);
+                    put_weights<Q8>(tq + 32u, w[1]);
+                    if (q == 0) ld32_start(tS + 96u, x[1][1]);
+                }
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
