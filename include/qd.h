@@ -564,7 +564,7 @@ enum { QD_KV_BF16 = 0, QD_KV_Q8 = 1 };
  * j * row_stride + d], the same for V; strides in elements.  QD_KV_BF16: bf16.
  * QD_KV_Q8: int8 codes with one fp32 scale a row, k_scale[b * scale_stream_stride + h *
  * scale_head_stride + j] (scales NULL and their strides unread for QD_KV_BF16); an
- * element stands for code * scale.  k and v are 16-byte aligned, the strides multiples
+ * element stands for code * scale, of either sign.  k and v are 16-byte aligned, the strides multiples
  * of 16 bytes and rows at least head_dim apart.  head_dim is 64 or 128. */
 typedef struct {
     void *k, *v;

@@ -62,8 +62,9 @@ def out_abs(x):
     return torch.nan_to_num(x).abs()
 
 
-def run(qd, way, B, T, G, H, D, S, lengths, n_new, q8, dtype, P=0, p8=None, seed=0, q_scale=1.0, change=None):
-    """A call of this way against the 64-bit form; `change` may alter (dev, values) of cache and prefix."""
+def run(qd, way, B, T, G, H, D, S, lengths, n_new, q8, dtype, P=0, p8=None, seed=0, q_scale=1.0, change=None,
+        queries=None):
+    """A call of this way against the 64-bit form; `change` may alter (dev, values) of cache and prefix, `queries` the queries."""
     g = gen(seed)
     dev, kv = _filled(g, B, H, S, D, q8)
     pdev, pkv = _filled(g, 1, H, P + 3, D, p8) if P else (None, None)
@@ -72,6 +73,8 @@ def run(qd, way, B, T, G, H, D, S, lengths, n_new, q8, dtype, P=0, p8=None, seed
     _spoil(dev, lengths, S)
     nn = [min(n, T) for n in n_new] if n_new else [T] * B
     q = (torch.randn((B, T, G * H, D), generator=g) * q_scale).to(dtype)
+    if queries:
+        queries(q)
     for b in range(B):
         q[b, nn[b]:] = math.nan
     view, pre, pk, pv = qd.KvCache(*dev), None, None, None
@@ -145,3 +148,62 @@ def test_probabilities_over_a_prefix_of_few_rows(qd, p8, D, B, T, G):
 @pytest.mark.parametrize("B,T,G", [(24, 1, 2), (64, 1, 2), (40, 4, 2)])
 def test_probabilities_over_a_prefix_of_many_rows(qd, p8, D, B, T, G):
     run(qd, "wide", B, T, G, 2, D, 8, [0] * B, None, not p8, torch.bfloat16, P=20, p8=p8, seed=B)
+
+
+# ---------------------------------------------------------------- scores in fp32, scales of either sign
+
+def loud_channel(dev, kv, pdev, pkv):
+    """8-bit keys with one loud channel, as rotated and normalised keys have: the row's scale comes from it and the other
+    codes are small."""
+    for parts, values in ((dev, kv), (pdev, pkv)):
+        if parts is None or parts[2] is None:
+            continue
+        x = values[0].float()
+        x[..., 11] = 60.0 * x.abs().amax(-1)
+        c, s = ref.quantise_rows(x.numpy())
+        parts[0].copy_(torch.from_numpy(c))
+        parts[2].copy_(torch.from_numpy(s))
+        values[0] = torch.from_numpy(c).double() * torch.from_numpy(s).double()[..., None]
+
+
+def quiet_there(q):
+    """Queries that do not look at that channel."""
+    q[..., 11] = 0.0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("way,B,T,G", [(None, 6, 1, 2), (None, 6, 4, 4), ("narrow", 4, 1, 2), ("wide", 32, 1, 2)])
+def test_scores_beside_a_loud_channel(qd, dtype, D, way, B, T, G):
+    """The scores' error goes by the products that a query has, not by the row's largest key."""
+    if way == "wide" and dtype == torch.float32:
+        way = "narrow"
+    lengths = [20] * B if way is None else [0] * B
+    run(qd, way, B, T, G, 2, D, 20, lengths, None, way is None, dtype, P=20 if way else 0, p8=True, seed=B + T, q_scale=6.0,
+        change=loud_channel, queries=quiet_there)
+
+
+def negative_scales(dev, kv, pdev, pkv):
+    """An element stands for code * scale, whatever the scale's sign: values 2^12 loud with every other scale negative, the
+    keys' too."""
+    for parts, values in ((dev, kv), (pdev, pkv)):
+        if parts is None or parts[2] is None:
+            continue
+        for i in range(2):
+            sign = torch.ones(parts[2 + i].shape)
+            sign[..., i::2] = -1.0
+            if i == 1:
+                sign *= 4096.0
+            parts[2 + i].mul_(sign.cuda())
+            values[i] = values[i] * sign.double()[..., None]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("way,B,T,G", [(None, 6, 1, 2), (None, 6, 4, 4), ("narrow", 4, 1, 2), ("wide", 32, 1, 2)])
+def test_scales_of_either_sign(qd, dtype, D, way, B, T, G):
+    if way == "wide" and dtype == torch.float32:
+        way = "narrow"
+    lengths = [40, 1, 2, 33, 17, 9] if way is None else [0] * B
+    run(qd, way, B, T, G, 2, D, 40, lengths, [min(T, n) for n in lengths] if way is None else None, way is None, dtype,
+        P=150 if way else 0, p8=True, seed=B + T, change=negative_scales)

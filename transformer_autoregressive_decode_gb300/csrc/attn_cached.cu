@@ -489,14 +489,14 @@ template <bool Q8, bool F32, int D, int NTX, bool PREFIX> struct WarpPass {
                     }
             }
         }
-        // z = s + log2(values' scale) bounds the weight that enters the product; a row of zeros
+        // z = s + log2|values' scale| bounds the weight that enters the product; a row of zeros
         // does not move the reference
 #pragma unroll
         for (int h = 0; h < H; ++h) {
             vd[h] = 1.f, vl[h] = 0.f;
             if constexpr (Q8) {
                 vd[h] = reinterpret_cast<const float *>(st + K::kS)[K::TP + g + 8 * h];
-                vl[h] = fmaxf(lg2(vd[h]), -60.f);
+                vl[h] = fmaxf(lg2(fabsf(vd[h])), -60.f);
             }
         }
         if (edge) {

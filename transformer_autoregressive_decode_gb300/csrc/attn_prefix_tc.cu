@@ -51,7 +51,7 @@ template <int D> struct WtCfg {
     static constexpr uint32_t kQ = 0;                         // Q [half][KB]
     static constexpr uint32_t kK = kQ + 2 * KB * kWtBox;      // K [stage][KB]
     static constexpr uint32_t kV = kK + 2 * KB * kWtBox;      // V [stage][KB]
-    static constexpr uint32_t kSc = kV + 2 * KB * kWtBox;     // scales [stage][keys', values', log2 of values'][128]
+    static constexpr uint32_t kSc = kV + 2 * KB * kWtBox;     // scales [stage][keys', values', log2 of |values'|][128]
     static constexpr uint32_t kOff = kSc + 2 * 3 * 128 * 4;   // first row of each stream
     static constexpr uint32_t kBar = kOff + (kWideMaxStreams + 1) * 4 + 4;
     static constexpr uint32_t kSmem = 1024 + kBar + 32 * 8;
@@ -168,7 +168,7 @@ __device__ __forceinline__ void weigh(const uint32_t (&x)[32], const float *sc, 
             unpk(mul2(x0, v.x), s0, s1);
             unpk(mul2(x1, v.y), s2, s3);
         }
-        t0 = fmaxf(t0, fmaxf(s0, s1)), t1 = fmaxf(t1, fmaxf(s2, s3));
+        t0 = fmaxf(t0, fmaxf(fabsf(s0), fabsf(s1))), t1 = fmaxf(t1, fmaxf(fabsf(s2), fabsf(s3)));   // (a scale may be negative)
         w[e] = s0, w[e + 1] = s1, w[e + 2] = s2, w[e + 3] = s3;
     }
     float l0, l1;
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) attn_prefix_tc_kernel(const Cac
                     store(sm + C::kV + (uint32_t)(st * KB) * kWtBox, uv);
                     // the scales come with V, which is not given up before its softmax is done (K's tile is)
                     float *sc = reinterpret_cast<float *>(sm + C::kSc) + st * 384;
-                    sc[tid] = sk, sc[128 + tid] = sv, sc[256 + tid] = fmaxf(lg2(sv), -60.f);
+                    sc[tid] = sk, sc[128 + tid] = sv, sc[256 + tid] = fmaxf(lg2(fabsf(sv)), -60.f);
                     fence_proxy_async_smem();
                     mbar_arrive(&v_full[st]);
                     if (i + 1 < w.n) {
