@@ -1311,9 +1311,17 @@ qd_status qd_attn_cached(const qd_kv_cache *cache, const qd_kv_cache *prefix, in
         if (v < 0 || v % unit) return QD_EINVAL;
     if (!is_aligned(q_dev, 16) || !is_aligned(out_dev, 16) || !is_aligned(lengths_dev, 4) || !is_aligned(n_new_dev, 4))
         return QD_EINVAL;
-    if (q_dev == out_dev || !apart((int64_t)n_q_heads * cache->head_dim, 1, 0, n_tokens, out_token_stride, cache->n_streams,
-                                   out_stream_stride))
+    // out's rows must lie neither over each other nor over q's
+    const int64_t row = (int64_t)n_q_heads * cache->head_dim, B64 = cache->n_streams;
+    const bool alike = (n_tokens == 1 || q_token_stride == out_token_stride) && (B64 == 1 || q_stream_stride == out_stream_stride);
+    if (q_dev == out_dev || !apart(e, row, {{n_tokens, out_token_stride}, {B64, out_stream_stride}}, alike ? bytes_between(q_dev, out_dev) : 0))
         return QD_EINVAL;
+    if (!alike) {                                    // rows of two layouts: not in the same stretch of memory
+        const uintptr_t q0 = reinterpret_cast<uintptr_t>(q_dev), o0 = reinterpret_cast<uintptr_t>(out_dev);
+        const uintptr_t q1 = ((uintptr_t)(n_tokens - 1) * q_token_stride + (uintptr_t)(B64 - 1) * q_stream_stride + row) * e;
+        const uintptr_t o1 = ((uintptr_t)(n_tokens - 1) * out_token_stride + (uintptr_t)(B64 - 1) * out_stream_stride + row) * e;
+        if (q0 < o0 ? o0 - q0 < q1 : q0 - o0 < o1) return QD_EINVAL;
+    }
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return QD_ECUDA;
     if ((st = check_cache(cache, dev, false)) != QD_OK) return st;

@@ -240,14 +240,15 @@ qd_status move_rows(bool read, const qd_kv_cache *cache, const void *k_rows, con
     if (!is_aligned(k_rows, 16) || !is_aligned(v_rows, 16) || !is_aligned(lengths, 4) || !is_aligned(n_new, 4))
         return QD_EINVAL;
     // the side that is written
-    const int64_t d64 = cache->head_dim;
-    if (read ? k_rows == v_rows || !apart(d64, cache->n_kv_heads, head_stride, n_tokens, token_stride, cache->n_streams, stream_stride)
-             : cache->k == cache->v || !apart(d64, cache->n_kv_heads, cache->head_stride, cache->smax, cache->row_stride,
-                                              cache->n_streams, cache->stream_stride))
+    const int64_t d64 = cache->head_dim, B = cache->n_streams, H = cache->n_kv_heads, ce = cache->format == QD_KV_Q8 ? 1 : 2;
+    if (read ? k_rows == v_rows || !apart(e, d64, {{H, head_stride}, {n_tokens, token_stride}, {B, stream_stride}},
+                                          bytes_between(k_rows, v_rows))
+             : cache->k == cache->v || !apart(ce, d64, {{H, cache->head_stride}, {cache->smax, cache->row_stride}, {B, cache->stream_stride}},
+                                              bytes_between(cache->k, cache->v)))
         return QD_EINVAL;
     if (!read && cache->format == QD_KV_Q8 &&
-        (cache->k_scale == cache->v_scale ||
-         !apart(1, cache->n_kv_heads, cache->scale_head_stride, 1, 1, cache->n_streams, cache->scale_stream_stride)))
+        (cache->k_scale == cache->v_scale || !apart(4, cache->smax, {{H, cache->scale_head_stride}, {B, cache->scale_stream_stride}},
+                                                    bytes_between(cache->k_scale, cache->v_scale))))
         return QD_EINVAL;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return QD_ECUDA;

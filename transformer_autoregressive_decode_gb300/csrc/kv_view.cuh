@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <initializer_list>
 
 #include "qd.h"
 
@@ -70,10 +71,32 @@ inline qd_status check_cache(const qd_kv_cache *c, int dev, bool one_stream) {
     return QD_OK;
 }
 
-// Rows (of d elements, heads of a token, tokens, streams) that a call writes must not lie over each other.
-inline bool apart(int64_t d, int64_t heads, int64_t head_stride, int64_t tokens, int64_t token_stride, int64_t streams,
-                  int64_t stream_stride) {
-    return (heads == 1 || head_stride >= d) && (tokens == 1 || token_stride >= d) && (streams == 1 || stream_stride >= d);
+// What a call writes must have bytes of its own: pieces of `inner` elements of e bytes at every combination of the
+// axes' steps (in elements), in one array or in two `pair` bytes apart.  From the smallest step on, each has to pass over all that the
+// smaller ones span; axes that interleave without nesting are refused too.
+struct Axis {
+    int64_t n, stride;
+};
+inline bool apart(int64_t e, int64_t inner, std::initializer_list<Axis> axes, int64_t pair = 0) {
+    constexpr int64_t kMost = int64_t(1) << 62;   // no address is as far
+    Axis a[5];
+    int n = 0;
+    for (const Axis &x : axes)
+        if (x.n > 1) {
+            if (x.stride > kMost / e) return false;
+            a[n++] = {x.n, x.stride * e};
+        }
+    if (pair) a[n++] = {2, pair < 0 ? -pair : pair};
+    std::sort(a, a + n, [](const Axis &x, const Axis &y) { return x.stride < y.stride; });
+    int64_t span = inner * e;
+    for (int i = 0; i < n; ++i) {
+        if (a[i].stride < span || a[i].n - 1 > (kMost - span) / a[i].stride) return false;
+        span += (a[i].n - 1) * a[i].stride;
+    }
+    return true;
+}
+inline int64_t bytes_between(const void *a, const void *b) {
+    return (int64_t)(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
 }
 
 inline KvView kv_view(const qd_kv_cache *c) {
