@@ -585,7 +585,7 @@ typedef struct {
  * streams.  Errors: QD_EINVAL (arguments, alignment, memory; a cache whose strides or
  * pointers lay its streams, heads, positions, keys and values over each other; from the smallest stride on, each has to
  * pass over all that the smaller ones span), QD_EUNSUPPORTED
- * (head_dim), QD_ECUDA. */
+ * (head_dim, more than 2^31 - 2^20 - 1 tokens), QD_ECUDA. */
 qd_status qd_kv_append(const qd_kv_cache *cache, const void *k_rows_dev, const void *v_rows_dev, int dtype,
                        int n_tokens, int64_t stream_stride, int64_t token_stride, int64_t head_stride,
                        const int32_t *lengths_dev, const int32_t *n_new_dev, void *cuda_stream);
@@ -623,7 +623,8 @@ qd_status qd_kv_read(const qd_kv_cache *cache, void *k_rows_dev, void *v_rows_de
  * may run at the same time need their own.  Errors: QD_EINVAL (arguments, alignment,
  * memory, workspace, an out whose rows lie over each other or over q's; q and out
  * of different strides have to be apart as a whole), QD_EUNSUPPORTED (head_dim,
- * n_tokens, more than 2^24 query rows a key head or 2^26 in all, 2^30 tiles of positions), QD_ECUDA. */
+ * n_tokens, max_length or prefix_length above 2^31 - 1025, more than 2^24 query rows a key head or 2^26 in all, 2^30 tiles of
+ * positions), QD_ECUDA. */
 qd_status qd_attn_cached(const qd_kv_cache *cache, const qd_kv_cache *prefix, int prefix_length, const void *q_dev,
                          int64_t q_stream_stride, int64_t q_token_stride, void *out_dev, int64_t out_stream_stride,
                          int64_t out_token_stride, int dtype, int n_tokens, int n_q_heads, float scale,

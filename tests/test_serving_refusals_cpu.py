@@ -139,3 +139,29 @@ def test_results_over_each_other_or_the_queries(qd, accepted, kw, over):
     c = cache(qd)
     got = qd._lib.qd_attn_cached(ctypes.addressof(c), *f.values(), None)
     check(qd, accepted, got, over)
+
+
+# -------------------------------------------------------------------- sizes past the kernels' counters
+
+FAR = 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("most,plen", [(FAR, 0), (FAR - 1023, 0), (32, FAR), (32, FAR - 126), (FAR, FAR)])
+def test_positions_past_the_counters(qd, most, plen):
+    """A reader's cache may hold that many rows (K and V may be the same ones)."""
+    c = cache(qd, smax=FAR, stream_stride=0, head_stride=0)
+    p = cache(qd, smax=FAR, n_streams=1, stream_stride=0, head_stride=0)
+    n = ctypes.c_size_t(0)
+    at = (ctypes.addressof(c), ctypes.addressof(p) if plen else None, plen)
+    assert qd._lib.qd_attn_cached_workspace(*at, 1, 1, 3, most, ctypes.byref(n)) == qd.QD_EUNSUPPORTED
+    assert qd._lib.qd_attn_cached(*at, A, 192, 192, 2 * A, 192, 192, 1, 1, 3, 1.0, A, None, most, A, 1 << 30,
+                                  None) == qd.QD_EUNSUPPORTED
+
+
+@pytest.mark.parametrize("tokens", [FAR, FAR - 2 ** 20 + 1])
+def test_tokens_past_the_counters(qd, tokens):
+    """One row for all tokens (a stride of 0), as appending allows, and as many rows apart as reading asks for."""
+    c = cache(qd)
+    assert qd._lib.qd_kv_append(ctypes.addressof(c), A, A, 1, tokens, 0, 0, 64, A, None, None) == qd.QD_EUNSUPPORTED
+    c = cache(qd, n_streams=1, n_kv_heads=1)
+    assert qd._lib.qd_kv_read(ctypes.addressof(c), A, 1 << 50, 1, tokens, 0, 64, 0, A, None, None) == qd.QD_EUNSUPPORTED

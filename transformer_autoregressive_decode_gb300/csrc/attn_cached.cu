@@ -47,6 +47,7 @@ namespace {
 constexpr int kAcWarps = 4, kAcThreads = kAcWarps * 32;
 constexpr int kAcMaxCluster = 8;
 constexpr int kAcMaxTokens = 64;
+constexpr int kAcMaxPositions = INT32_MAX - 1024;    // rounded up to tiles or chunks they fit an int
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool live) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
@@ -1268,7 +1269,7 @@ qd_status check_sizes(const qd_kv_cache *cache, const qd_kv_cache *prefix, int p
     const int kvh = cache->n_kv_heads;
     if ((dtype != QD_F32 && dtype != QD_BF16) || n_tokens < 1 || n_q_heads < kvh || n_q_heads % kvh) return QD_EINVAL;
     if (max_length < 1 || max_length > cache->smax) return QD_EINVAL;
-    if (n_tokens > kAcMaxTokens) return QD_EUNSUPPORTED;
+    if (n_tokens > kAcMaxTokens || max_length > kAcMaxPositions || prefix_length > kAcMaxPositions) return QD_EUNSUPPORTED;
     const int64_t all = (int64_t)n_tokens * (n_q_heads / kvh) * cache->n_streams;
     if (all > (1 << 24) || all * kvh > (1 << 26)) return QD_EUNSUPPORTED;
     return QD_OK;

@@ -71,8 +71,7 @@ template <typename T, int D> struct RowWalk {
         t = blockIdx.x * tp * a.sets + in;
     }
     __device__ __forceinline__ bool live(const RowsArgs &a, int tt) const {
-        const int pos = first + tt;
-        return !idle && tt < n && pos >= 0 && pos < a.smax;
+        return !idle && tt < n && (unsigned)first + (unsigned)tt < (unsigned)a.smax;   // (past the last token it may wrap)
     }
 };
 
@@ -85,7 +84,7 @@ __global__ void __launch_bounds__(kRowThreads) kv_append_kernel(const RowsArgs a
     S s(a);
     const uint8_t *src = a.rows[which] + b * a.stream + s.h * a.head + s.t * a.token + lane * 16;
     uint8_t *dst = const_cast<uint8_t *>(which ? a.c.v : a.c.k) + b * a.c.stream + s.h * a.c.head +
-                   (s.first + s.t) * a.c.row + lane * (Q8 ? E : 2 * E);
+                   ((int64_t)s.first + s.t) * a.c.row + lane * (Q8 ? E : 2 * E);
     float *scales = nullptr;
     if constexpr (Q8)
         scales = const_cast<float *>(which ? a.c.vs : a.c.ks) + b * a.c.sstream + s.h * a.c.shead + s.first + s.t;
@@ -165,7 +164,7 @@ __global__ void __launch_bounds__(kRowThreads) kv_read_kernel(const RowsArgs a) 
     const int b = blockIdx.y, which = blockIdx.z & 1, lane = threadIdx.x % LPR;
     S s(a);
     uint8_t *dst = const_cast<uint8_t *>(a.rows[which]) + b * a.stream + s.h * a.head + s.t * a.token + lane * 16;
-    const uint8_t *src = (which ? a.c.v : a.c.k) + b * a.c.stream + s.h * a.c.head + (s.first + s.t) * a.c.row + lane * (W * 4);
+    const uint8_t *src = (which ? a.c.v : a.c.k) + b * a.c.stream + s.h * a.c.head + ((int64_t)s.first + s.t) * a.c.row + lane * (W * 4);
     const float *scales = nullptr;
     if constexpr (Q8) scales = (which ? a.c.vs : a.c.ks) + b * a.c.sstream + s.h * a.c.shead + s.first + s.t;
     const int64_t hop_in = s.tp * a.c.row, hop_out = s.tp * a.token;
@@ -232,6 +231,7 @@ qd_status move_rows(bool read, const qd_kv_cache *cache, const void *k_rows, con
     qd_status st = check_cache(cache, -1, false);
     if (st != QD_OK) return st;
     if ((dtype != QD_F32 && dtype != QD_BF16) || n_tokens < 1 || cache->n_streams > 65535) return QD_EINVAL;
+    if (n_tokens > INT32_MAX - (1 << 20)) return QD_EUNSUPPORTED;   // a turn past the last token has to fit the kernels' counters
     if (!k_rows || !v_rows || !lengths) return QD_EINVAL;
     const int64_t unit = dtype == QD_F32 ? 4 : 8, e = dtype == QD_F32 ? 4 : 2;
     if (stream_stride < 0 || token_stride < 0 || head_stride < 0 || stream_stride % unit || token_stride % unit ||
