@@ -165,3 +165,16 @@ def test_tokens_past_the_counters(qd, tokens):
     assert qd._lib.qd_kv_append(ctypes.addressof(c), A, A, 1, tokens, 0, 0, 64, A, None, None) == qd.QD_EUNSUPPORTED
     c = cache(qd, n_streams=1, n_kv_heads=1)
     assert qd._lib.qd_kv_read(ctypes.addressof(c), A, 1 << 50, 1, tokens, 0, 64, 0, A, None, None) == qd.QD_EUNSUPPORTED
+
+
+# --------------------------------------------------------------------------------- the binding
+
+def test_a_workspace_that_is_less_than_it_counts(qd):
+    """An expanded tensor counts bytes that it does not have."""
+    import torch
+    k = torch.zeros((2, 2, 32, 64), dtype=torch.bfloat16)
+    view = qd.KvCache(k, k.clone())
+    q = torch.zeros((2, 1, 4, 64), dtype=torch.bfloat16)
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(1 << 30), torch.zeros(1 << 12, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError):
+            qd.qd_attn_cached(q, view, torch.zeros(2, dtype=torch.int32), torch.zeros_like(q), workspace=ws)

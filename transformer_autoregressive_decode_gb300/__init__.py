@@ -729,12 +729,14 @@ def qd_attn_cached(q, cache: KvCache, lengths, out, n_new=None, max_length: Opti
     """Attention of the new tokens q [streams, tokens, q_heads, head_dim] (fp32 or bf16) over
     each stream's cache and the shared prefix (a KvCache of one stream) into out (same type
     and shape).  max_length: bound of the lengths (default: the cache's positions); scale:
-    default head_dim ** -0.5; prefix_length: default all of the prefix.  workspace: uint8
+    default head_dim ** -0.5; prefix_length: default all of the prefix.  workspace: contiguous uint8
     tensor of qd_attn_cached_workspace bytes, of this call alone while it runs; by default the
     stream's own scratch (in a capture: fresh memory of the graph's)."""
     ops = _ops or _setup_ops()
     args = (q, cache.addr, lengths, out, n_new, max_length, scale, None if prefix is None else prefix.addr, prefix_length)
     if workspace is not None:
+        if not workspace.is_contiguous():       # an expanded one has fewer bytes than it counts
+            raise ValueError("workspace must be contiguous")
         st = ops.attn(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream)
     else:
         st = ops.attn(*args, None, 0, stream)
