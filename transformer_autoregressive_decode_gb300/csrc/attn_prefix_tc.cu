@@ -431,6 +431,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) attn_prefix_tc_kernel(const Cac
         for (; ok && w.next(); ++seg) {
             const int N = pairs ? 2 * w.n : w.n;
             ok = wt_wait(&q_full[0], (uint32_t)seg & 1u, bad) && (!pairs || wt_wait(&q_full[1], (uint32_t)seg & 1u, bad));
+            ok = __all_sync(0xffffffffu, ok);       // a wait may expire for some lanes alone: all leave together
             auto issue_s = [&](int i) {
                 const int h = i & 1, c = kc + (pairs ? i >> 1 : i), st = c & 1;
                 if (!pairs || !h) ok = ok && wt_wait(&k_full[st], (uint32_t)(c >> 1) & 1u, bad);
