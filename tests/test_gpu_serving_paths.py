@@ -207,3 +207,42 @@ def test_scales_of_either_sign(qd, dtype, D, way, B, T, G):
     lengths = [40, 1, 2, 33, 17, 9] if way is None else [0] * B
     run(qd, way, B, T, G, 2, D, 40, lengths, [min(T, n) for n in lengths] if way is None else None, way is None, dtype,
         P=150 if way else 0, p8=True, seed=B + T, change=negative_scales)
+
+
+# ------------------------------------------------------------------------------------- host threads
+
+FIRST_CALLS_MEET = """
+import ctypes, threading, torch
+import transformer_autoregressive_decode_gb300 as qd
+# ctypes lets go of the interpreter's lock, so the library's first calls run at the same time; head_dim 64 and 128, both formats
+torch.zeros(1, device="cuda")
+jobs = []
+for d in (64, 128):
+    for dt in (torch.int8, torch.bfloat16):
+        # long enough that the workspace goes by the SMs and the CTAs that each holds
+        k = torch.zeros((1, 2, 4000, d), dtype=dt, device="cuda").expand(300, 2, 4000, d)
+        s = [torch.ones((1, 2, 4000), device="cuda").expand(300, 2, 4000) for _ in range(2)] if dt == torch.int8 else []
+        jobs.append(qd.KvCache(k, k, *s))
+got = [[] for _ in range(8)]
+gate = threading.Barrier(8)
+def work(i):
+    n = ctypes.c_size_t(0)
+    gate.wait()
+    for v in jobs:
+        st = qd._lib.qd_attn_cached_workspace(v.addr, None, 0, 1, 1, 4, 4000, ctypes.byref(n))
+        got[i].append((st, n.value))
+t = [threading.Thread(target=work, args=(i,)) for i in range(8)]
+[x.start() for x in t]
+[x.join() for x in t]
+assert all(g == got[0] for g in got) and all(st == 0 and n > 0 for st, n in got[0]), got
+print("alike")
+"""
+
+
+def test_first_calls_of_host_threads():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS_MEET], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "alike" in r.stdout, r.stdout[-2000:] + r.stderr[-2000:]

@@ -37,6 +37,8 @@
 //    the join the rest).
 //  - a prefix: read by every stream's own pass while that is cheap, else by
 //    attn_prefix_tc_kernel (bf16 rows) or once for every group of rows (PREFIX here).
+#include <atomic>
+
 #include "attn_cached.cuh"
 #include "qd_internal.h"
 
@@ -1067,18 +1069,18 @@ int prefix_splits(int rows, int kvh, int prefix_len, int rw, int tp, int sms) {
 
 enum : int { kPassCluster = 0, kPassPrefix = 1, kPassShare = 2 };
 
-// Shared-memory limit and resident CTAs per SM of a variant, looked up once per device.
-struct Ready {
-    bool done;
-    int per_sm;
-};
+// Shared-memory limit set and resident CTAs per SM (0: not yet) of a variant, looked up once per device.  Host threads
+// whose first calls meet look it up twice; none sees the one without the other.
+using Ready = std::atomic<int>;
 template <typename F> cudaError_t make_ready(Ready *r, F fn, int smem) {
-    if (r->done) return cudaSuccess;
+    if (r->load(std::memory_order_acquire)) return cudaSuccess;
+    int per_sm = 0;
     cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&r->per_sm, fn, kAcThreads, smem);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, kAcThreads, smem);
     if (e != cudaSuccess) return e;
-    r->done = r->per_sm > 0;
-    return r->done ? cudaSuccess : cudaErrorInvalidConfiguration;
+    if (per_sm < 1) return cudaErrorInvalidConfiguration;
+    r->store(per_sm, std::memory_order_release);
+    return cudaSuccess;
 }
 
 template <typename F, typename... A>
@@ -1116,7 +1118,7 @@ cudaError_t launch(int kind, const CachedArgs &a, unsigned *ctas, int nsplit, in
     if (kind == kPassShare) {
         auto fn = attn_share_kernel<Q8, F32, D, NTX>;
         if ((e = make_ready(&ready[kind][dev], fn, K::kSmem)) != cudaSuccess) return e;
-        *ctas = (unsigned)(ready[kind][dev].per_sm * sms_of(dev));
+        *ctas = (unsigned)(ready[kind][dev].load(std::memory_order_acquire) * sms_of(dev));
         return plan ? cudaSuccess : launch_ex(fn, *ctas, kAcThreads, K::kSmem, 1, s, a);
     }
     if (kind == kPassPrefix) {

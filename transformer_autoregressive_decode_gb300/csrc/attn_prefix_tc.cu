@@ -31,6 +31,8 @@
 // is bounded; where one expires the CTA's partials become NaN and the roles run to their ends.
 #include <cuda.h>
 
+#include <atomic>
+
 #include "attn_cached.cuh"
 #include "qd_internal.h"
 #include "tc_common.cuh"
@@ -703,7 +705,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) attn_prefix_tc_kernel(const Cac
 }
 
 template <bool Q8, int D> cudaError_t launch(const CachedArgs &a, int ctas, int dev, cudaStream_t s) {
-    static bool ready[64] = {};
+    static std::atomic<bool> ready[64] = {};
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     auto fn = attn_prefix_tc_kernel<Q8, D>;
     if (!ready[dev]) {

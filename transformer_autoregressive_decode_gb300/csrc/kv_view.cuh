@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 #include <initializer_list>
 
 #include "qd.h"
@@ -42,10 +43,13 @@ inline bool on_device(const void *p, int dev) {
 
 // SMs of the current device (152 on a GB300), looked up once per device.
 inline int sms_of(int dev) {
-    static int n[64] = {};
+    static std::atomic<int> known[64] = {};
     if (dev < 0 || dev >= 64) return 152;
-    if (!n[dev] && cudaDeviceGetAttribute(&n[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 152;
-    return n[dev];
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 152;
+    known[dev].store(n, std::memory_order_relaxed);
+    return n;
 }
 
 inline bool is_aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
