@@ -246,3 +246,154 @@ def test_first_calls_of_host_threads():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST_CALLS_MEET], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "alike" in r.stdout, r.stdout[-2000:] + r.stderr[-2000:]
+
+
+# --------------------------------------------------------------- a prefix's own passes, shape by shape
+
+@pytest.mark.parametrize("p8", [True, False])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,T,G,P", [(24, 1, 2, 1), (48, 1, 1, 127), (33, 1, 2, 129), (64, 1, 2, 128), (43, 1, 3, 700), (64, 2, 2, 257),
+                                     (50, 2, 3, 1300), (13, 5, 3, 515), (10, 8, 8, 64)])
+def test_wide_prefix(qd, p8, D, B, T, G, P):
+    """48 to 640 rows a key head: a tile of 128 rows alone (every other chunk of 128 keys to each half), full, one row into the
+    next, an odd number of tiles; unused rows left out, or all in use; the streams' caches in the other format beside it."""
+    g = gen(P)
+    lengths = torch.randint(0, 20, (B,), generator=g).tolist()
+    n_new = [min(int(a), b) for a, b in zip(torch.randint(0, T + 1, (B,), generator=g), lengths)] if T > 1 else None
+    run(qd, "wide", B, T, G, 2, D, 20, lengths, n_new, not p8, torch.bfloat16, P=P, p8=p8, seed=P)
+    if T > 1:
+        run(qd, "wide", B, T, G, 2, D, 20, lengths, None, not p8, torch.bfloat16, P=P, p8=p8, seed=P + 1, q_scale=4.0)
+
+
+@pytest.mark.parametrize("q8", [True, False])
+@pytest.mark.parametrize("D,B,T,G,P", [(64, 60, 1, 2, 6000), (128, 60, 1, 2, 6000), (64, 20, 6, 3, 5400)])
+def test_wide_prefix_of_the_caches_format(qd, q8, D, B, T, G, P):
+    """Long enough that the streams do not read it themselves; several chunks a CTA."""
+    lengths = torch.randint(T, 30, (B,), generator=gen(P)).tolist()
+    run(qd, "wide", B, T, G, 3, D, 30, lengths, None, q8, torch.bfloat16, P=P, p8=q8, seed=P)
+
+
+@pytest.mark.parametrize("p8", [True, False])
+@pytest.mark.parametrize("n_new", [None, "some", "none", "one"])
+def test_wide_prefix_of_more_streams_than_it_lists(qd, p8, n_new):
+    """Above 2048 streams unused rows are not left out of the tiles."""
+    B = 2100
+    lengths = torch.randint(0, 4, (B,), generator=gen(5)).tolist()
+    used = {None: None, "some": [b % 2 for b in range(B)], "none": [0] * B, "one": [0] * (B - 1) + [1]}[n_new]
+    run(qd, "wide", B, 1, 1, 1, 64, 4, lengths, used, not p8, torch.bfloat16, P=150, p8=p8, seed=5)
+
+
+@pytest.mark.parametrize("p8", [True, False])
+@pytest.mark.parametrize("n_new", ["none", "one", "last"])
+def test_wide_prefix_with_next_to_no_rows_in_use(qd, p8, n_new):
+    B, T = 30, 2
+    used = {"none": [0] * B, "one": [1] + [0] * (B - 1), "last": [0] * (B - 1) + [2]}[n_new]
+    run(qd, "wide", B, T, 2, 2, 128, 20, [3] * B, used, not p8, torch.bfloat16, P=300, p8=p8, seed=3)
+
+
+@pytest.mark.parametrize("p8", [True, False])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("way,dtype,B,T,G", [("wide", torch.bfloat16, 24, 1, 2), ("wide", torch.bfloat16, 40, 2, 2),
+                                            ("narrow", torch.bfloat16, 4, 1, 2), ("narrow", torch.float32, 30, 1, 2)])
+def test_scores_that_rise_in_steps(qd, p8, D, way, dtype, B, T, G):
+    """The reference has to move between the chunks of a prefix, and in the middle of one, over what that chunk has written
+    already: keys in four levels, each with a quarter of the dims to itself, so that what the earlier levels left
+    stands alone there."""
+    P, jump = 700, 10.0 if p8 else 45.0
+    level = torch.zeros(P + 3)
+    for at in (192, 448, 512):
+        level[at:] += 1
+
+    def steps(dev, kv, pdev, pkv):
+        g = gen(77)
+        d = torch.zeros(D)
+        d[::2] = 1.0                                                        # the direction of the scores; the queries' below
+        k = (level * jump * D ** 0.5 / (D // 2))[:, None] * d + 0.1 * torch.randn((2, P + 3, D), generator=g)
+        v = torch.randn((2, P + 3, D), generator=g)
+        v *= (torch.arange(D) * 4 // D == level[:, None]).float()
+        for i, x in enumerate((k[None], v[None])):
+            if p8:
+                c, s = ref.quantise_rows(x.numpy())
+                pdev[i].copy_(torch.from_numpy(c))
+                pdev[2 + i].copy_(torch.from_numpy(s))
+                pkv[i] = torch.from_numpy(c).double() * torch.from_numpy(s).double()[..., None]
+            else:
+                pdev[i].copy_(x.bfloat16())
+                pkv[i] = x.bfloat16().double()
+
+    def ones(q):
+        q[:] = q[:1, :1, :1]
+        q[..., ::2] = 1.0
+
+    run(qd, way, B, T, G, 2, D, 8, [0] * B, None, not p8, dtype, P=P, p8=p8, seed=B, change=steps, queries=ones)
+
+
+@pytest.mark.parametrize("way,B", [("wide", 64), ("narrow", 4)])
+def test_a_prefix_that_begins_with_hidden_keys(qd, way, B):
+    """Keys of -infinity first, then scores far below zero: the reference comes from the first that count."""
+    g = gen(18)
+    P, D = 300, 128
+    k = torch.zeros((1, 1, P, D))
+    k[0, 0, :, 0] = -500.0 + torch.rand((P,), generator=g)
+    k[0, 0, :150] = -math.inf
+    v, k = torch.randn((1, 1, P, D), generator=g).bfloat16(), k.bfloat16()
+    own, _ = _filled(g, B, 1, 4, D, True)
+    q = torch.zeros((B, 1, 1, D))
+    q[..., 0] = 1.0
+    q = (q + 2.0 ** -100).bfloat16()                                          # nothing times an infinity
+    view, pre = qd.KvCache(*own), qd.KvCache(k.cuda(), v.cuda())
+    assert route(qd, view, pre, P, True, 1, 1) == way
+    out = torch.empty((B, 1, 1, D), dtype=torch.bfloat16, device="cuda")
+    qd.qd_attn_cached(q.cuda(), view, ints([0] * B), out, prefix=pre, scale=1.0)
+    want, mag, spread = ref.attend(q[:1], k[:, :, 150:].double(), v[:, :, 150:].double(), [150], [1], 1.0)
+    assert ((out.cpu().double() - want).abs() <= bound(want, mag, spread, P, D, torch.bfloat16, False)).all()
+
+
+@pytest.mark.parametrize("p8", [True, False])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype,B,T,G,P", [(torch.float32, 5, 1, 2, 3000), (torch.float32, 24, 4, 2, 333), (torch.float32, 9, 3, 3, 17),
+                                           (torch.bfloat16, 5, 1, 3, 4100), (torch.bfloat16, 3, 5, 3, 130)])
+def test_narrow_prefix(qd, p8, D, dtype, B, T, G, P):
+    """Too few rows, or fp32 ones: a few rows of the batch at a time, the positions split over CTAs where they are many."""
+    lengths = torch.randint(0, 40, (B,), generator=gen(P)).tolist()
+    run(qd, "narrow", B, T, G, 2, D, 40, lengths, [min(T, n) for n in lengths], not p8, dtype, P=P, p8=p8, seed=P)
+
+
+@pytest.mark.parametrize("q8", [True, False])
+def test_narrow_prefix_of_the_caches_format(qd, q8):
+    """Rows that fill a quarter or half of a tile stream by stream, and all of it together."""
+    B, P = 64, 21000 if q8 else 10600
+    run(qd, "narrow", B, 1, 1, 2, 64, 6, [b % 7 for b in range(B)], None, q8, torch.float32, P=P, p8=q8, seed=1)
+
+
+@pytest.mark.parametrize("way,dtype,B,T", [("wide", torch.bfloat16, 40, 1), ("narrow", torch.float32, 40, 1)])
+def test_prefix_passes_of_three_streams_at_a_time(qd, way, dtype, B, T):
+    """Eager calls on two streams and a replayed capture on a third, no workspace given: the results stay bit for bit."""
+    g = gen(45)
+    dev, _ = _filled(g, B, 2, 300, 64, True)
+    pdev, _ = _filled(g, 1, 2, 4000, 64, False)
+    view, pre = qd.KvCache(*dev), qd.KvCache(*pdev)
+    assert route(qd, view, pre, 4000, dtype == torch.bfloat16, T, 4) == way
+    ln = ints(torch.randint(1, 300, (B,), generator=g).tolist())
+    qs = [torch.randn((B, T, 4, 64), generator=g).to(dtype).cuda() for _ in range(3)]
+
+    def call(q, out):
+        qd.qd_attn_cached(q, view, ln, out, prefix=pre)
+    want = [torch.empty_like(q) for q in qs]
+    for q, o in zip(qs, want):
+        call(q, o)
+    torch.cuda.synchronize()
+    outs = [torch.zeros_like(q) for q in qs]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(qs[2], outs[2])
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(30):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                call(qs[i], outs[i])
+        with torch.cuda.stream(streams[2]):
+            graph.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
