@@ -397,3 +397,30 @@ def test_prefix_passes_of_three_streams_at_a_time(qd, way, dtype, B, T):
     torch.cuda.synchronize()
     for o, w in zip(outs, want):
         assert torch.equal(o, w)
+
+
+@pytest.mark.parametrize("dtype,D,rows", [(torch.float32, 128, 8), (torch.float32, 64, 16), (torch.bfloat16, 128, 16)])
+def test_narrow_prefix_leaves_out_unused_rows(qd, dtype, D, rows):
+    """A group of `rows` rows of the batch in which none is in use is not worked: its partials, which stand first in the
+    workspace, (ref, sum) of [key head][row of the batch], stay as they were."""
+    B, T, G, H, P, n_new = 5, 4, 2, 2, 20, [4, 0, 1, 0, 0]
+    g = gen(8)
+    q8 = dtype == torch.bfloat16
+    dev, kv = _filled(g, B, H, 8, D, q8)
+    pdev, pkv = _filled(g, 1, H, P, D, not q8)
+    view, pre = qd.KvCache(*dev), qd.KvCache(*pdev)
+    assert route(qd, view, pre, P, q8, T, G * H) == "narrow"
+    ws = torch.full((qd.qd_attn_cached_workspace(view, q8, T, G * H, prefix=pre),), 0xAB, dtype=torch.uint8, device="cuda")
+    q = torch.randn((B, T, G * H, D), generator=g).to(dtype)
+    out = torch.full((B, T, G * H, D), 7.0, dtype=dtype, device="cuda")
+    qd.qd_attn_cached(q.cuda(), view, ints([4] * B), out, n_new=ints(n_new), prefix=pre, workspace=ws)
+    want, mag, spread = ref.attend(q, kv[0], kv[1], [4] * B, n_new, D ** -0.5, pkv[0][0], pkv[1][0])
+    used = ~torch.isnan(want)
+    assert ((out.cpu().double() - want).abs() <= bound(want, mag, spread, P + 4, D, dtype, False))[used].all()
+    assert bool((out.cpu()[~used] == 7.0).all())
+    n = B * T * G
+    notes = ws.cpu()[:H * n * 8].view(H, n, 8)
+    live = torch.tensor([t < n_new[b] for b in range(B) for t in range(T) for _ in range(G)])
+    for r0 in range(0, n, rows):
+        untouched = bool((notes[:, r0:r0 + rows] == 0xAB).all())
+        assert untouched == (not live[r0:r0 + rows].any()), r0

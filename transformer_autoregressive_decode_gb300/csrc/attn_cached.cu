@@ -238,7 +238,7 @@ template <bool Q8, bool F32, int D, int NTX, bool PREFIX> struct WarpPass {
                 rr = r - bb * (a.T * a.G);
             }
             const int tt = rr / a.G, gg = rr - tt * a.G;
-            const bool live = r < a.rows && (PREFIX || tt < nn);
+            const bool live = r < a.rows && tt < (PREFIX ? clamp_new(a, bb) : nn);   // the others are not read
             const uint8_t *src = a.q + bb * a.q_stream + tt * a.q_token + (int64_t)(hk * a.G + gg) * D * (F32 ? 4 : 2);
             constexpr int E = 16 / K::ES;           // dims of a piece
             float x[K::KP * E];
@@ -248,7 +248,7 @@ template <bool Q8, bool F32, int D, int NTX, bool PREFIX> struct WarpPass {
                 for (int e = 0; e < E; e += F32 ? 4 : 8) {
                     const int d = i * 4 * E + t * E + e;
                     uint4 u = make_uint4(0, 0, 0, 0);
-                    if (r < a.rows) u = __ldg(reinterpret_cast<const uint4 *>(src + d * (F32 ? 4 : 2)));
+                    if (live) u = __ldg(reinterpret_cast<const uint4 *>(src + d * (F32 ? 4 : 2)));
                     if constexpr (F32)
                         Elem<float>::unpack(u, x + i * E + e);
                     else
@@ -654,6 +654,10 @@ __global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NTX>::kMinCtas)
     const int len = PREFIX ? a.max_len : clamp_len(__ldg(a.lengths + b), a.max_len);
     const int nn = PREFIX ? a.T : clamp_new(a, b);
     const int r0 = grp * K::RW;
+    if (PREFIX && a.n_new) {                         // a group without a row in use leaves no partials: nothing asks for them
+        const int r = r0 + lane, of = a.T * a.G, bb = r / of;
+        if (!__any_sync(0xffffffffu, lane < K::RW && r < a.rows && (r - bb * of) / a.G < clamp_new(a, bb))) return;
+    }
 
     WarpPass<Q8, F32, D, NTX, PREFIX> w;
     w.init(lane);

@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) attn_prefix_tc_kernel(const Cac
                     b = row / (a.T * a.G), in = row - b * (a.T * a.G);
                 }
                 const int tt = in / a.G, g = in - tt * a.G;
-                src = a.q + b * a.q_stream + tt * a.q_token + (int64_t)(hk * a.G + g) * D * 2;
+                if (tt < clamp_new(a, b)) src = a.q + b * a.q_stream + tt * a.q_token + (int64_t)(hk * a.G + g) * D * 2;
             }
             // the warp's 32 rows, D / 8 lanes a row: whole lines, where a row a thread took a line for every 16 bytes
             float cs = a.scale2;
