@@ -424,3 +424,49 @@ def test_narrow_prefix_leaves_out_unused_rows(qd, dtype, D, rows):
     for r0 in range(0, n, rows):
         untouched = bool((notes[:, r0:r0 + rows] == 0xAB).all())
         assert untouched == (not live[r0:r0 + rows].any()), r0
+
+
+@pytest.mark.parametrize("way,q8,dtype,T", [("wide", True, torch.bfloat16, 1), ("wide", False, torch.bfloat16, 3), ("narrow", True, torch.float32, 2),
+                                            ("narrow", False, torch.float32, 1)])
+@pytest.mark.parametrize("captured", [False, True])
+def test_inputs_written_just_before_a_prefix_of_its_own_pass(qd, way, q8, dtype, T, captured):
+    """Rows, lengths, counts and queries change directly before every call, whose pass over the streams' caches begins
+    while the prefix's runs; the same call on finished inputs gives the same bits."""
+    B, G, H, D, S, P, steps = 40, 2, 4, 128, 130, 2900, 30
+    g = gen(92)
+    dev, _ = _filled(g, B, H, S, D, q8)
+    pdev, _ = _filled(g, 1, H, P, D, not q8)
+    view, pre = qd.KvCache(*dev), qd.KvCache(*pdev)
+    assert route(qd, view, pre, P, dtype == torch.bfloat16, T, G * H) == way
+    rows = torch.randn((steps, 2, B, T, H, D), generator=g).to(dtype).cuda()
+    qs = torch.randn((steps, B, T, G * H, D), generator=g).to(dtype).cuda()
+    counts = torch.randint(0, T + 1, (steps, B), generator=g, dtype=torch.int32).cuda()
+    at, row, q = torch.zeros((1,), dtype=torch.long, device="cuda"), torch.empty_like(rows[0]), torch.empty_like(qs[0])
+    ln, nn = torch.zeros((B,), dtype=torch.int32, device="cuda"), torch.zeros((B,), dtype=torch.int32, device="cuda")
+    out, again = torch.zeros_like(q), torch.zeros_like(q)
+    ws = torch.empty((qd.qd_attn_cached_workspace(view, dtype == torch.bfloat16, T, G * H, prefix=pre),), dtype=torch.uint8, device="cuda")
+
+    def step():
+        row.copy_(rows.index_select(0, at)[0])
+        nn.copy_(counts.index_select(0, at)[0])
+        ln.add_(nn)
+        q.copy_(qs.index_select(0, at)[0])
+        qd.qd_kv_append(view, row[0], row[1], ln, n_new=nn)
+        qd.qd_attn_cached(q, view, ln, out, n_new=nn, prefix=pre, workspace=ws)
+        at.add_(1)
+
+    if captured:
+        step()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        at.zero_()
+        ln.zero_()
+        out.zero_()
+    for i in range(steps):
+        graph.replay() if captured else step()
+        torch.cuda.synchronize()
+        qd.qd_attn_cached(q, view, ln, again, n_new=nn, prefix=pre, workspace=ws)
+        torch.cuda.synchronize()
+        assert torch.equal(out, again), i

@@ -248,7 +248,7 @@ template <bool Q8, bool F32, int D, int NTX, bool PREFIX> struct WarpPass {
                 for (int e = 0; e < E; e += F32 ? 4 : 8) {
                     const int d = i * 4 * E + t * E + e;
                     uint4 u = make_uint4(0, 0, 0, 0);
-                    if (live) u = __ldg(reinterpret_cast<const uint4 *>(src + d * (F32 ? 4 : 2)));
+                    if (live) u = *reinterpret_cast<const uint4 *>(src + d * (F32 ? 4 : 2));
                     if constexpr (F32)
                         Elem<float>::unpack(u, x + i * E + e);
                     else
@@ -620,7 +620,7 @@ template <bool Q8, bool F32, int D, int NTX, bool PREFIX> struct WarpPass {
 
 // A stream's tiles of tp positions (a power of two), its own and then those of a short prefix: none where it has no new token.
 __device__ __forceinline__ int tiles_of(const CachedArgs &a, int b, int tp) {
-    const int len = clamp_len(__ldg(a.lengths + b), a.max_len);
+    const int len = clamp_len(a.lengths[b], a.max_len);
     return clamp_new(a, b) > 0 ? (int)((unsigned)(len + tp - 1) / (unsigned)tp) + a.pre_tiles : 0;
 }
 
@@ -651,7 +651,7 @@ __global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NTX>::kMinCtas)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = blockIdx.x % nsplit, item = blockIdx.x / nsplit;
     const int grp = item % a.groups, hk = (item / a.groups) % a.kvh, b = PREFIX ? 0 : item / a.groups / a.kvh;
-    const int len = PREFIX ? a.max_len : clamp_len(__ldg(a.lengths + b), a.max_len);
+    const int len = PREFIX ? a.max_len : clamp_len(a.lengths[b], a.max_len);
     const int nn = PREFIX ? a.T : clamp_new(a, b);
     const int r0 = grp * K::RW;
     if (PREFIX && a.n_new) {                         // a group without a row in use leaves no partials: nothing asks for them
@@ -821,7 +821,8 @@ __global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NTX>::kMinCtas)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned wid = blockIdx.x * kAcWarps + warp;
     // A prefix's pass before this one let it start when every CTA of that pass had waited for whatever wrote the inputs: those
-    // grids are complete, their results in L2, and the fence keeps loads from anything older.  It needs none of that pass's
+    // grids are complete, their results in L2, and the fence keeps what is read from anything older (plain loads and
+    // cp.async; none of it is read by non-coherent loads, which a fence does not order).  It needs none of that pass's
     // results, so it runs beside it (its idle SMs, its end) and waits at its own end instead, because attn_join_kernel waits
     // for this kernel alone.  (16384 under 96 x 4 x 32 rows 129 us one after the other, 116 so; 4096 under 64 x 16 31.6 and 29.9.)
     const bool beside = a.splits != 0 || a.wide != 0;
@@ -876,7 +877,7 @@ __global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NTX>::kMinCtas)
         const int in = (int)((x - s_b) / tiles), tile0 = (int)(x - s_b - in * tiles);
         const int n = (int)min(tiles - tile0, x1 - x);
         const int hk = in / groups, grp = in - hk * groups;
-        const int len = clamp_len(__ldg(a.lengths + b), a.max_len);
+        const int len = clamp_len(a.lengths[b], a.max_len);
         // its own tiles, then a short prefix's (two copies of the pass: a loop around one held 250 bytes a thread in memory)
         const int own = (int)tiles - a.pre_tiles, cut = min(max(own, tile0), tile0 + n);
         if (tile0 < own)

@@ -67,8 +67,10 @@ template <bool RAW> __device__ __forceinline__ uint32_t codes_f16(uint32_t y, ui
 __device__ __forceinline__ float part_weight(float2 ml, float M) { return ml.y == 0.f ? 0.f : ex2(ml.x - M); }
 
 __device__ __forceinline__ int clamp_len(int len, int most) { return len < 0 ? 0 : len > most ? most : len; }
+// Lengths, counts and queries are read by plain loads, which the fence or wait at a kernel's start orders (attn_share_kernel), not
+// by non-coherent ones, which nothing does.
 __device__ __forceinline__ int clamp_new(const CachedArgs &a, int b) {
-    const int n = a.n_new ? __ldg(a.n_new + b) : a.T;
+    const int n = a.n_new ? a.n_new[b] : a.T;
     return n < 0 ? 0 : n > a.T ? a.T : n;
 }
 // A list of `total` tiles in equal runs, one per worker (warp or CTA).
