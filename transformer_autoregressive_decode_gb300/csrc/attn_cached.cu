@@ -1113,7 +1113,8 @@ cudaError_t launch_ex(F fn, dim3 grid, int threads, int smem, unsigned cluster, 
     return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 
-// kind Cluster or Prefix: `ctas` of clusters of nsplit; kind Share: every CTA the SMs hold, *ctas says how many.
+// kind Cluster or Prefix: `ctas` of clusters of nsplit; kind Share: every CTA the SMs hold, *ctas says how many.  `plan`: only *ctas,
+// for Cluster the CTAs that an SM holds, three at most.
 template <bool Q8, bool F32, int D, int NTX>
 cudaError_t launch(int kind, const CachedArgs &a, unsigned *ctas, int nsplit, int dev, cudaStream_t s, bool plan) {
     using K = AcCfg<Q8, F32, D, NTX>;
@@ -1130,6 +1131,10 @@ cudaError_t launch(int kind, const CachedArgs &a, unsigned *ctas, int nsplit, in
         auto fn = attn_cached_kernel<Q8, F32, D, NTX, true>;
         if ((e = make_ready(&ready[kind][dev], fn, K::kSmem)) != cudaSuccess) return e;
         return launch_ex(fn, *ctas, kAcThreads, K::kSmem, 1, s, a, nsplit);
+    }
+    if (plan) {
+        *ctas = (unsigned)std::min(3, K::kMinCtas);
+        return cudaSuccess;
     }
     auto fn = attn_cached_kernel<Q8, F32, D, NTX, false>;
     const int smem = nsplit > 1 ? K::kSmemCluster : K::kSmem;
@@ -1226,11 +1231,17 @@ qd_status make_plan(const qd_kv_cache *cache, const qd_kv_cache *prefix, int pre
     if (items * tiles > (1ll << 30)) return QD_EUNSUPPORTED;
     // A cluster per item while the grid is one wave, or little more, and a warp's share short; longer or larger batches are
     // shared out.  (72 items, a short prefix: 576 CTAs 13.8 us, 288 10.2; 592 items of one CTA 14.6 us, shared out 18.)
-    // An SM holds three CTAs at least, two of the largest variants.
-    const int wave = ((d == 128 && (!q8 || p->nt == 2)) || (p->nt & 7) == 4 ? 2 : 3) * sms;
+    // The wave is what the SMs hold of this variant (two CTAs of bf16 rows of 64, whose ring is as large as that of 128: 160 items
+    // of up to 700 positions in clusters of two, as if there were room for three, 8.4 us, one CTA each 7.6); the little more goes by the work
+    // of an item (560 items of up to 200 or 700 of those positions, nearly two waves, 8.5 and 13.9 us, shared out 9.6 and 14.2).
+    const CachedArgs none = {};
+    unsigned per_sm = 0;
+    if (dispatch(kPassCluster, q8, f32, d, p->nt, none, &per_sm, 0, dev, nullptr, true) != cudaSuccess) return QD_ECUDA;
+    const int wave = (int)per_sm * sms;
+    const int most = (d == 128 && (!q8 || p->nt == 2)) || (p->nt & 7) == 4 ? wave + wave / 3 : 4 * sms;
     p->nsplit = 1;
     while (p->nsplit < kAcMaxCluster && items * p->nsplit * 2 <= wave && tiles > p->nsplit * kAcWarps) p->nsplit *= 2;
-    if (items * p->nsplit > wave + wave / 3 || tiles > 8 * p->nsplit * kAcWarps) p->nsplit = 0;
+    if (items * p->nsplit > most || tiles > 8 * p->nsplit * kAcWarps) p->nsplit = 0;
     size_t at = 0;
     if (prefix && prefix_length > 0 && !p->inline_prefix) {
         const bool pq8 = prefix->format == QD_KV_Q8;
@@ -1251,7 +1262,6 @@ qd_status make_plan(const qd_kv_cache *cache, const qd_kv_cache *prefix, int pre
         }
     }
     if (!p->nsplit) {
-        const CachedArgs none = {};
         if (dispatch(kPassShare, q8, f32, d, p->nt, none, &p->ctas, 0, dev, nullptr, true) != cudaSuccess) return QD_ECUDA;
         const size_t slots = (size_t)items + (size_t)p->ctas * kAcWarps;
         p->s_ml = at, at = up256(at + slots * p->rw * 8);
