@@ -470,3 +470,24 @@ def test_inputs_written_just_before_a_prefix_of_its_own_pass(qd, way, q8, dtype,
         qd.qd_attn_cached(q, view, ln, again, n_new=nn, prefix=pre, workspace=ws)
         torch.cuda.synchronize()
         assert torch.equal(out, again), i
+
+
+def test_scratch_is_given_back_and_taken_anew(qd):
+    g = gen(46)
+    B = 40
+    dev, _ = _filled(g, B, 2, 8, 64, True)
+    pdev, _ = _filled(g, 1, 2, 600, 64, False)
+    view, pre = qd.KvCache(*dev), qd.KvCache(*pdev)
+    q, ln = torch.randn((B, 1, 4, 64), generator=g).bfloat16().cuda(), ints([8] * B)
+    outs = [torch.zeros_like(q) for _ in range(2)]
+    qd.release_scratch()
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    qd.qd_attn_cached(q, view, ln, outs[0], prefix=pre)
+    assert torch.cuda.memory_allocated() > before
+    qd.release_scratch()                                  # the call may still run: its memory stays the stream's
+    assert torch.cuda.memory_allocated() == before
+    qd.qd_attn_cached(q, view, ln, outs[1], prefix=pre)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], outs[1]) and bool(outs[0].float().abs().sum() > 0)
+    qd.release_scratch()

@@ -178,3 +178,28 @@ def test_a_workspace_that_is_less_than_it_counts(qd):
     for ws in (torch.zeros(1, dtype=torch.uint8).expand(1 << 30), torch.zeros(1 << 12, dtype=torch.uint8)[::2]):
         with pytest.raises(ValueError):
             qd.qd_attn_cached(q, view, torch.zeros(2, dtype=torch.int32), torch.zeros_like(q), workspace=ws)
+
+
+def test_scratch_is_given_back(qd):
+    """All that the binding holds for streams goes at once, and is asked for anew afterwards (no such device)."""
+    import gc
+    import weakref
+
+    class Memory:
+        pass
+
+    ops = qd._setup_ops()
+    held = [Memory() for _ in range(3)]
+    refs = [weakref.ref(x) for x in held]
+    for i, x in enumerate(held):
+        assert ops.keep(98, i, x, A, 256)
+    del held, x
+    gc.collect()
+    assert all(r() is not None for r in refs)
+    qd.release_scratch()
+    gc.collect()
+    assert all(r() is None for r in refs)
+    again = Memory()
+    assert ops.keep(98, 0, again, A, 256)
+    qd.release_scratch()
+    qd.release_scratch()                                  # nothing left: nothing to do

@@ -689,6 +689,13 @@ _ops = None
 _SCRATCH_MOST = 128 << 20
 
 
+def release_scratch():
+    """Give the scratch that qd_attn_cached keeps for the streams it was called on (one tensor each, 128 MB
+    at most) back to torch's allocator; the next call on a stream takes new."""
+    if _ops is not None:
+        _ops.release()
+
+
 def _fresh(need: int, t, stream):
     torch = _T()
     if stream is None:
@@ -731,7 +738,7 @@ def qd_attn_cached(q, cache: KvCache, lengths, out, n_new=None, max_length: Opti
     and shape).  max_length: bound of the lengths (default: the cache's positions); scale:
     default head_dim ** -0.5; prefix_length: default all of the prefix.  workspace: contiguous uint8
     tensor of qd_attn_cached_workspace bytes, of this call alone while it runs; by default the
-    stream's own scratch (in a capture: fresh memory of the graph's)."""
+    stream's own scratch, kept until release_scratch() (in a capture: fresh memory of the graph's)."""
     ops = _ops or _setup_ops()
     args = (q, cache.addr, lengths, out, n_new, max_length, scale, None if prefix is None else prefix.addr, prefix_length)
     if workspace is not None:

@@ -319,6 +319,17 @@ static PyObject *py_keep(PyObject *self, PyObject *args) {
     Py_RETURN_TRUE;
 }
 
+/* release(): gives up the scratch of all streams.  What still runs on one keeps its memory to itself: the allocator hands it to
+ * later work of that stream only. */
+static PyObject *py_release(PyObject *self, PyObject *none) {
+    PyObject *held[64];
+    const int n = n_scratch;
+    for (int i = 0; i < n; ++i) held[i] = scratch[i].tensor;
+    n_scratch = 0;                      /* first: what a tensor's end sets off finds none */
+    for (int i = 0; i < n; ++i) Py_DECREF(held[i]);
+    Py_RETURN_NONE;
+}
+
 /* setup(append, read, attn, workspace, verify: addresses; float32, bfloat16, int32, current raw stream, whether it is being
  * captured: torch's) */
 static PyObject *py_setup(PyObject *self, PyObject *args) {
@@ -335,6 +346,7 @@ static PyObject *py_setup(PyObject *self, PyObject *args) {
 static PyMethodDef methods[] = {{"setup", py_setup, METH_VARARGS, NULL},
                                 {"rows", (PyCFunction)(void (*)(void))py_rows, METH_FASTCALL, NULL},
                                 {"keep", py_keep, METH_VARARGS, NULL},
+                                {"release", py_release, METH_NOARGS, NULL},
                                 {"attn", (PyCFunction)(void (*)(void))py_attn, METH_FASTCALL, NULL},
                                 {"verify", (PyCFunction)(void (*)(void))py_verify, METH_FASTCALL, NULL},
                                 {NULL, NULL, 0, NULL}};
