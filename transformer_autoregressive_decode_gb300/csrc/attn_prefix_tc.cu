@@ -114,10 +114,6 @@ __device__ __forceinline__ void ld32_start(uint32_t taddr, uint32_t *r) {
     tc_ld16_nowait(taddr + 16, r + 16);
 }
 
-__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-           ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
 // Byte of 16-byte piece c (of 8) of row r in a swizzled box.
 __device__ __forceinline__ uint32_t swz(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 
@@ -424,7 +420,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) attn_prefix_tc_kernel(const Cac
         constexpr uint32_t idesc_o = base | (1u << 16) | ((uint32_t)(D >> 3) << 17);
         // descriptors of the first bytes; an offset of n bytes adds n / 16
         const uint64_t dQ = sw128_desc(smem_addr(sm + C::kQ)), dK = sw128_desc(smem_addr(sm + C::kK));
-        const uint64_t dV = desc_mn(smem_addr(sm + C::kV), kWtBox, 1024u);
+        const uint64_t dV = sw128_desc_mn(smem_addr(sm + C::kV), kWtBox, 1024u);
         constexpr uint32_t kBox16 = kWtBox / 16;
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         int kc = 0, seg = 0;

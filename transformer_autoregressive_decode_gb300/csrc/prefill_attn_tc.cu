@@ -60,14 +60,6 @@ template <int HD> struct AtCfg {
     static constexpr size_t kSmem = 1024 + kBar + 32 * 8 + 16;
 };
 
-// Shared-memory descriptor of an MN-major operand with the 128-byte swizzle: rows of
-// 128 bytes along MN (64 bf16), 8-row groups along K `sbo` bytes apart, 64-element MN
-// blocks `lbo` bytes apart.
-__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-           ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-
 // N consecutive fp32 columns of this thread's tensor-memory lane: N / 16 loads, one wait.
 template <int N> __device__ __forceinline__ void ld_cols(uint32_t taddr, float *v) {
     uint32_t r[N];

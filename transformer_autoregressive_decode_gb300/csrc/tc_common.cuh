@@ -82,6 +82,14 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
+// Shared-memory descriptor of an MN-major operand with the 128-byte swizzle: rows of
+// 128 bytes along MN (64 bf16), 8-row groups along K `sbo` bytes apart, 64-element MN
+// blocks `lbo` bytes apart.
+__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
+           ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
 // Instruction descriptor, kind::f16: fp32 accumulator, bf16 A and B, A K-major, B
 // K-major (or MN-major: bit 16), N >> 3 at bit 17, M >> 4 at bit 24.
 template <int M, int N, bool B_MN = false> __device__ __forceinline__ constexpr uint32_t tc_idesc_mn() {
