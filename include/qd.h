@@ -652,7 +652,8 @@ qd_status qd_attn_cached_workspace(const qd_kv_cache *cache, const qd_kv_cache *
  * (below 0 and NaN as 0, above 1 as 1) and gives the first id whose running sum exceeds floor(u *
  * sum) (the product in fp64), so the result does not depend on the order of
  * summation; where every weight is 0 it gives -1.  A drafted id outside [0, vocab)
- * fails.  vocab <= 524288, n_tokens in [1, 64].  Errors: QD_EINVAL, QD_ECUDA. */
+ * fails.  vocab <= 524288, n_tokens in [1, 64].  out_ids and n_accepted lie over none of the other arrays (the
+ * probabilities are not checked for it).  Errors: QD_EINVAL, QD_ECUDA. */
 qd_status qd_verify_drafts(const float *target_probs_dev, int64_t target_stream_stride, int64_t target_row_stride,
                            const float *draft_probs_dev, int64_t draft_stream_stride, int64_t draft_row_stride,
                            const int32_t *draft_ids_dev, const int32_t *n_draft_dev, const float *u_dev, int n_streams,

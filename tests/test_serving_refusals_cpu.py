@@ -203,3 +203,31 @@ def test_scratch_is_given_back(qd):
     assert ops.keep(98, 0, again, A, 256)
     qd.release_scratch()
     qd.release_scratch()                                  # nothing left: nothing to do
+
+
+# ------------------------------------------------------------------------------- verification's arrays
+
+# 3 streams of 4 drafts: ids 48 bytes, u and out_ids 60, n_draft and n_accepted 12
+ARRAYS = [
+    (dict(), False),
+    (dict(acc=6 * A), True),                                 # n_accepted over n_draft: some CTAs would read the new count
+    (dict(out=4 * A), True),                                 # out_ids over draft_ids: rows of another pitch
+    (dict(out=4 * A + 44), True),
+    (dict(out=4 * A + 48), False),
+    (dict(out=4 * A - 56), True),
+    (dict(out=4 * A - 60), False),
+    (dict(out=5 * A), True),
+    (dict(acc=5 * A + 56), True),
+    (dict(acc=5 * A + 60), False),
+    (dict(out=6 * A - 56), True),
+    (dict(acc=7 * A + 56), True),                            # n_accepted in out_ids
+    (dict(acc=7 * A + 60), False),
+    (dict(acc=4 * A + 40), True),
+]
+
+
+@pytest.mark.parametrize("kw,over", ARRAYS)
+def test_verification_over_what_it_reads(qd, accepted, kw, over):
+    f = dict(p=2 * A, ps=40, pr=8, q=3 * A, qs=32, qr=8, ids=4 * A, nd=6 * A, u=5 * A, B=3, T=4, V=8, out=7 * A, acc=8 * A)
+    f.update(kw)
+    check(qd, accepted, qd._lib.qd_verify_drafts(*f.values(), None), over)

@@ -297,6 +297,21 @@ extern "C" qd_status qd_verify_drafts(const float *target_probs_dev, int64_t tar
                            n_draft_dev};
     for (const void *p : ptrs)
         if (!is_aligned(p, 4)) return QD_EINVAL;
+    // a stream's CTAs read the ids, counts and numbers while others write the results
+    struct Ints {
+        const void *at;
+        int64_t n;
+    };
+    const int64_t B = n_streams, T = n_tokens;
+    const Ints out = {out_ids_dev, B * (T + 1)}, acc = {n_accepted_dev, B};
+    const Ints in[3] = {{draft_ids_dev, B * T}, {u_dev, B * (T + 1)}, {n_draft_dev, n_draft_dev ? B : 0}};
+    auto meet = [](const Ints &a, const Ints &b) {
+        const int64_t d = bytes_between(a.at, b.at);
+        return a.n && b.n && (d < 0 ? -d < 4 * b.n : d < 4 * a.n);
+    };
+    if (meet(out, acc)) return QD_EINVAL;
+    for (const Ints &x : in)
+        if (meet(out, x) || meet(acc, x)) return QD_EINVAL;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return QD_ECUDA;
     for (int i = 0; i < 7; ++i)
