@@ -614,7 +614,9 @@ qd_status qd_kv_read(const qd_kv_cache *cache, void *k_rows_dev, void *v_rows_de
  * 16-byte aligned with strides of 16-byte multiples; q and out must not overlap.
  * Scores, softmax and sums are fp32.  fp32 queries and their probabilities keep at least
  * 22 bits through the products; bf16 queries are exact, their probabilities keep 22
- * bits over 8-bit rows and 16 over bf16 rows, whatever the batch.
+ * bits over 8-bit rows and 16 over bf16 rows, whatever the batch.  (Over 8-bit rows a probability times its
+ * value's scale is exact to 2^-35 of the largest at best, 2^-27 over a prefix in a pass of its own, and keeps
+ * fewer bits where all values are below 2^-58.)
  * prefix: one stream of n_kv_heads heads in either format (its strides for streams are
  * unread), read once for the whole batch; NULL or prefix_length 0: none.
  * n_tokens <= 64, max_length in [1, cache->smax] bounds the lengths (it plans the launch).

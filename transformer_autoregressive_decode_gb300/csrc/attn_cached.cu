@@ -824,7 +824,7 @@ __global__ void __launch_bounds__(kAcThreads, AcCfg<Q8, F32, D, NTX>::kMinCtas)
     // grids are complete, their results in L2, and the fence keeps what is read from anything older (plain loads and
     // cp.async; none of it is read by non-coherent loads, which a fence does not order).  It needs none of that pass's
     // results, so it runs beside it (its idle SMs, its end) and waits at its own end instead, because attn_join_kernel waits
-    // for this kernel alone.  (16384 under 96 x 4 x 32 rows 129 us one after the other, 116 so; 4096 under 64 x 16 31.6 and 29.9.)
+    // for this kernel alone.  (16384 under 96 x 4 x 32 rows 153 us one after the other, 141 so; 4096 under 64 x 16 35.8 and 33.2.)
     const bool beside = a.splits != 0 || a.wide != 0;
     if (beside)
         __threadfence();
@@ -1143,11 +1143,15 @@ cudaError_t launch(int kind, const CachedArgs &a, unsigned *ctas, int nsplit, in
 }
 
 // Up to here (tiles that the streams would read between them) a prefix is read by every stream's own pass: a launch and
-// a pipeline's start less, where its positions cost little (64 streams, one token each, 8-bit: 1024 positions, 16384 tiles, 24 us
-// against 32 on the tcgen05 cores; 2048, 32768 tiles, 37 against 33; bf16: 512, 16384 tiles, 24 against 32).
+// a pipeline's start less, where its positions cost little (64 streams, one token each, 8-bit: 1024 positions, 16384 tiles, 28 us
+// against 30 on the tcgen05 cores; 1536, 24576 tiles, 34 against 30; bf16: 512, 16384 tiles, 25 against 30; 1024, 32768 tiles, 36
+// against 32).
 constexpr int64_t kInlineTiles = 20000;
 
-// Rows from which the prefix goes to the tcgen05 cores.
+// Rows from which the prefix goes to the tcgen05 cores (16000 8-bit positions under 32, 48 and 96 rows of 8 key heads: 37.3, 37.3 and
+// 39.1 us there, 37.3, 39.0 and 53.1 a few rows at a time; 8000 bf16 positions under 16, 48 and 96 rows: 21.6, 26.1 and 29.6
+// there, 28.2, 31.2 and 43.1).  Not before, although bf16 prefixes would gain: fewer rows keep the finer spacing of faint weights over 8-bit
+// rows (2^-35 of the largest, 2^-27 there), and the limit is one for both formats.
 constexpr int kWideFrom = 48;
 
 constexpr int tile_positions(bool q8, int d) { return q8 || d == 64 ? 32 : 16; }   // AcCfg::TP

@@ -90,7 +90,12 @@ struct Share {
 // ---- the prefix on the tcgen05 tensor cores (attn_prefix_tc.cu): bf16 rows, many of them
 constexpr int kWideRows = 128;   // rows of a tile
 constexpr int kWideKeys = 128;   // keys of a chunk
-constexpr unsigned kWideMinRun = 4;     // chunks worth a CTA's start and its partial (4096 under 64 x 16 rows: 2, 4, 6, 8: 33.7, 29.9, 34.6, 33.4 us)
+// The shortest run of chunks.  A longer one saves starts and partials; a shorter one takes more SMs, of which the own caches' pass
+// beside it gets the rest.  Both move the time in steps, so no run is best everywhere; 2, 4, 6 and 8 chunks, call in us, 8 key heads: 2048
+// bf16 positions under 64 x 16 rows 30.8, 33.5, 38.6, 39.0; 4096 37.1, 34.2, 39.1, 40.4, next to no own caches 23.2, 21.2,
+// 28.0, 25.9; 8000 47.0, 42.7, 42.9, 45.8; 3000 under 32 x 2 x 16 26.6, 27.6, 30.0, 32.3; 8000 8-bit under 48 x 16
+// 39.1, 38.4, 40.5, 42.4; 2000 under 96 x 4 x 32 90.3, 90.3, 92.2, 97.4.
+constexpr unsigned kWideMinRun = 4;
 constexpr int kWideMaxStreams = 2048;   // up to here the unused rows of a batch are left out
 
 // Rows of the streams before `upto` (unused ones left out where n_new says so), and of all.

@@ -20,10 +20,11 @@
 // tensor memory (the half's previous O product has finished when its next S has) and what the chunk has written so
 // far.  So the scores are usually read once.
 //
-// Measured: 16384 8-bit positions under 768 of 1536 rows and 8 key heads, 52.7 GFLOP (79 with P's second part), 89 us a
-// call with next to no own caches, 71 with one part, which keeps 11 bits (8 of bf16).  A pair of chunks takes some 6000
-// clocks where the products need 3072 and the exponentials' units (16 a clock and SM) 2048: a half's softmax and its
-// two products follow one another, and S and O of two halves fill the tensor memory of head_dim 128.
+// Measured: 16384 8-bit positions under 768 of 1536 rows and 8 key heads, 52.7 GFLOP (79 with P's second part), 85 us, the
+// tensor pipe 44 % of its cycles; 71 us with one part, which keeps 11 bits (8 of bf16).  A pair of chunks needs 3072 clocks of products
+// and 2048 of the exponentials' units (16 a clock and SM) and takes about twice the former: a half's softmax and its two
+// products follow one another, and S and O of two halves fill the tensor memory of head_dim 128.  Not tried: O's products begun on the
+// first keys while the others' weights are formed, and a share of the exponentials on the FMA units.
 //
 // Roles (512 threads): warps 0-3 and 4-7 the softmax of the two halves (a row each, also Q and the results),
 // warps 8-11 load K and V, warp 12 owns the tensor memory and issues the MMAs, warps 13-15 only complete its
