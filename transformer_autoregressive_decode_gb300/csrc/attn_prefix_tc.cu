@@ -591,12 +591,13 @@ __global__ void __launch_bounds__(kWtThreads, 1) attn_prefix_tc_kernel(const Cac
                     tc_wait_ld_u32<32>(x[q][0]);
                     tc_wait_ld_u32<32>(x[q][1]);
                     // a half's first keys set the reference, which is near enough as a rule
-                    bool move = q == 0 && i < 2;
-                    if (!move) {
-                        weigh_all(x[q]);
-                        move = __any_sync(0xffffffffu, top > kWtTop<Q8> || ref == -INFINITY);
+                    const bool first = q == 0 && i < 2;
+                    if (first) {
+                        const float m = fmaxf(largest<Q8>(x[q][0], scq, cs, here), largest<Q8>(x[q][1], scq + 32, cs, here - 32));
+                        if (m - kWtUp<Q8> > ref) ref = m - kWtUp<Q8>;
                     }
-                    if (move) {
+                    weigh_all(x[q]);
+                    if (!first && __any_sync(0xffffffffu, top > kWtTop<Q8> || ref == -INFINITY)) {
                         uint32_t y[2][32];          // the scores again: they stand until their weights are written
                         ld32_start(tq, y[0]);
                         ld32_start(tq + 32u, y[1]);
