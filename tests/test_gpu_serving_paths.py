@@ -491,3 +491,26 @@ def test_scratch_is_given_back_and_taken_anew(qd):
     torch.cuda.synchronize()
     assert torch.equal(outs[0], outs[1]) and bool(outs[0].float().abs().sum() > 0)
     qd.release_scratch()
+
+
+@pytest.mark.parametrize("way,p8,B", [("wide", True, 24), ("wide", False, 24), ("narrow", True, 4), ("narrow", False, 4)])
+def test_prefix_offsets_past_32_bits(qd, way, p8, B):
+    """A prefix whose second head stands more than 2^32 bytes on, and whose rows are far apart."""
+    g = gen(13)
+    H, P, D, G = 2, 200, 128, 2
+    e = 1 if p8 else 2
+    (pdev, pkv), (dev, kv) = _filled(g, 1, H, P, D, p8), _filled(g, B, H, 4, D, not p8)
+    step, row = 2 ** 32 // e + 2 ** 27, 2 ** 20
+    far = []
+    for x in pdev[:2]:
+        y = torch.zeros(step + P * row, dtype=x.dtype, device="cuda").as_strided((1, H, P, D), (0, step, row, 1))
+        far.append(y.copy_(x))
+    view, pre = qd.KvCache(*dev), qd.KvCache(*far, *pdev[2:])
+    q = torch.randn((B, 1, G * H, D), generator=g).bfloat16()
+    out = torch.zeros((B, 1, G * H, D), dtype=torch.bfloat16, device="cuda")
+    assert route(qd, view, pre, P, True, 1, G * H) == way
+    qd.qd_attn_cached(q.cuda(), view, ints([4] * B), out, prefix=pre)
+    want, mag, spread = ref.attend(q, kv[0], kv[1], [4] * B, [1] * B, D ** -0.5, pkv[0][0], pkv[1][0])
+    tol = torch.maximum(bound(want, mag, spread, P + 4, D, torch.bfloat16, p8, way == "wide"),
+                        bound(want, mag, spread, P + 4, D, torch.bfloat16, not p8))
+    assert ((out.cpu().double() - want).abs() <= tol).all()
