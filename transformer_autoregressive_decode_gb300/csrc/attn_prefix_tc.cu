@@ -5,7 +5,7 @@
 // come in chunks of 128.  A CTA has two halves, each with a tile of its own in flight (S, P and O in tensor
 // memory), so that the tensor core works for one half while the other takes its softmax:
 //   S = Q K^T          128 x 128 fp32 in tensor memory; Q and K from shared memory
-//   softmax            thread = row: P = 2^(s - ref) as two 16-bit parts over S's own columns, 32 keys at a time
+//   softmax            thread = row: P = 2^(s - ref) as two 16-bit parts over S's own columns, 64 keys at a time
 //   O += P V           P's parts from tensor memory, V from shared memory (keys x dims: the MN-major operand)
 // With more than 128 rows the halves take two tiles of rows over the same chunks (K and V are shared);
 // otherwise both take the one tile, every other chunk each.  The list (key head, tile pair, chunk) is cut into equal
@@ -16,14 +16,14 @@
 // scores stand in 32 columns, and so do their parts: 16 columns of the first, 16 of the second.
 //
 // 64 keys' probabilities are formed with the reference as it stands and written over their scores when none has outgrown
-// its room (32 keys at a time, a vote each, took 150 us where this takes 142); otherwise the reference moves first, with O in
+// its room (32 keys at a time, a vote each, took 150 us where this takes 140); otherwise the reference moves first, with O in
 // tensor memory (the half's previous O product has finished when its next S has) and what the chunk has written so
 // far.  So the scores are usually read once.
 //
 // Measured: 16384 8-bit positions under 768 of 1536 rows and 8 key heads, 52.7 GFLOP (79 with P's second part), 85 us, the
-// tensor pipe 44 % of its cycles; 71 us with one part, which keeps 11 bits (8 of bf16).  A pair of chunks needs 3072 clocks of products
-// and 2048 of the exponentials' units (16 a clock and SM) and takes about twice the former: a half's softmax and its two
-// products follow one another, and S and O of two halves fill the tensor memory of head_dim 128.  Not tried: O's products begun on the
+// tensor pipe 44 % of its cycles; 71 us with one part, which keeps 11 bits (8 of bf16).  A chunk needs 1536 clocks of products in each
+// half, and 1024 of the exponentials' units (16 a clock and SM), and a pair takes about twice the products' time: a half's softmax
+// and its two products follow one another, and S and O of two halves fill the tensor memory of head_dim 128.  Not tried: O's products begun on the
 // first keys while the others' weights are formed, and a share of the exponentials on the FMA units.
 //
 // Roles (512 threads): warps 0-3 and 4-7 the softmax of the two halves (a row each, also Q and the results),
