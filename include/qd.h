@@ -661,6 +661,62 @@ qd_status qd_verify_drafts(const float *target_probs_dev, int64_t target_stream_
                            const int32_t *draft_ids_dev, const int32_t *n_draft_dev, const float *u_dev, int n_streams,
                            int n_tokens, int vocab, int32_t *out_ids_dev, int32_t *n_accepted_dev, void *cuda_stream);
 
+/* ---- a decoder layer's attention over a cache in pages ----
+ *
+ * For callers that hold their streams' caches in pages of a few positions instead of a
+ * stretch per stream: qd_qk_norm_rope brings a fused projection's rows into queries and
+ * pages, qd_attn_prompt attends over whole prompts, qd_attn_paged over the pages for the
+ * new tokens of a step.
+ *
+ * A cache in pages is a qd_kv_cache whose streams are the pages and whose smax is the
+ * positions of a page (a power of two from 16 to 2^20; QD_EUNSUPPORTED otherwise).  Position j of stream b
+ * is row j % smax of page page_table[b * table_stride + j / smax] (DEVICE int32, at most
+ * table_pages of them a stream, table_pages * smax at most 2^31 - 1025).  The table is read on the device, so
+ * a captured graph serves streams whose pages change.  lengths_dev, n_new_dev, streams and
+ * memory: as for the calls over contiguous caches above. */
+
+/* Rows for qd_qk_norm_rope (plain data, DEVICE pointers).  Element (row n, head h, dim d) of q
+ * is q[n * q_stride + h * head_dim + d], likewise k, v and the results; strides in elements,
+ * multiples of 16 bytes, everything 16-byte aligned.  dtype is that of q, k, v; out_dtype that
+ * of q_out, k_out, v_out. */
+typedef struct {
+    const void *q, *k, *v;                   /* v NULL: none (then no pages) */
+    int64_t q_stride, k_stride, v_stride;
+    void *q_out, *k_out, *v_out;             /* k_out, v_out NULL: not wanted */
+    int64_t q_out_stride, k_out_stride, v_out_stride;
+    int dtype, out_dtype;
+    int n_tokens, n_q_heads, n_kv_heads, head_dim;
+    const float *q_gamma, *k_gamma;          /* fp32 [head_dim]; NULL: not normalised */
+    double eps;
+    const float *cos, *sin;                  /* fp32 [rope_rows][head_dim / 2]; both NULL: not rotated */
+    int rope_rows;
+    const int32_t *positions;                /* int32 [n_tokens], with mrope_h > 0 [3][n_tokens]; NULL: positions in the cache */
+    int mrope_h;                             /* three interleaved position streams: frequency d < 3 * mrope_h takes stream d % 3 */
+    const int32_t *lengths, *offsets, *n_new;   /* int32 [n_streams], [n_streams + 1], [n_streams]; NULL: see below */
+    int n_streams;
+    const qd_kv_cache *pages;                /* NULL: no cache is written */
+    const int32_t *page_table;
+    int64_t table_stride;
+    int table_pages;
+} qd_rope_rows;
+
+/* qd_qk_norm_rope -- per head of q and k: x' = x / sqrt(mean(x^2) + eps) * gamma, then, with c and s the table
+ * row of the token's position and h = head_dim / 2, y[d] = x'[d] c[d] - x'[d + h] s[d] and y[d + h] = x'[d + h] c[d]
+ * + x'[d] s[d]; v stays as it is.  All in fp32, rounded once to q_out, k_out, v_out and, for k and v, into the
+ * stream's pages (bf16, or 8-bit rows as qd_kv_append makes them).
+ * The rows of the streams: with offsets, packed, rows [offsets[b], offsets[b + 1]) are stream b's new tokens; without,
+ * n_tokens / n_streams rows a stream, of which it uses the first n_new[b] (NULL: all).  Row t of a stream with n new
+ * tokens stands at position lengths[b] - n + t of its cache.  lengths NULL: rows without a stream (positions and no
+ * pages).  Rows that no stream uses are neither read nor written.  A position outside the
+ * tables makes the row's rotated results NaN; one outside [0, table_pages * page) or on a page outside the pool is
+ * not written.  Offsets ascend in [0, n_tokens]; rows that they do not give to one stream may be left out.
+ * No two rows of one call may stand at the same place in the cache.
+ * A result may take its own rows' place (same type, stride and address) or stand between rows of other arrays; it lies over
+ * nothing else that the call reads or writes (the pages, tables and arrays of integers are not checked for it).
+ * Errors: QD_EINVAL (arguments, alignment, memory, results that lie over something; a pool whose pages, heads and rows lie over
+ * each other), QD_EUNSUPPORTED (head_dim, page, more than 2^30 tokens or 65536 heads), QD_ECUDA. */
+qd_status qd_qk_norm_rope(const qd_rope_rows *rows, void *cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -45,7 +45,7 @@ EXPORTS = ("qd_create", "qd_destroy", "qd_reset", "qd_prefill", "qd_prefill_mrop
            "qd_batch_set_stream", "qd_batch_decode", "qd_batch_sync", "qd_batch_get_logits", "qd_batch_copy_kv",
            "qd_batch_get_pos", "qd_batch_get_launch_count", "qd_batch_set_graphs", "qd_batch_time_kernel", "qd_batch_prefill",
            "qd_batch_set_sampling", "qd_kv_append", "qd_kv_read", "qd_attn_cached", "qd_attn_cached_workspace",
-           "qd_verify_drafts")
+           "qd_verify_drafts", "qd_qk_norm_rope")
 
 
 class qd_config(ctypes.Structure):
@@ -73,6 +73,17 @@ class qd_kv_cache(ctypes.Structure):
         (n, ctypes.c_int) for n in ("format", "n_streams", "n_kv_heads", "smax", "head_dim")] + [
         (n, ctypes.c_int64) for n in ("stream_stride", "head_stride", "row_stride", "scale_stream_stride",
                                       "scale_head_stride")]
+
+
+class qd_rope_rows(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in "qkv"] + [(n + "_stride", ctypes.c_int64) for n in "qkv"] + \
+        [(n + "_out", ctypes.c_void_p) for n in "qkv"] + [(n + "_out_stride", ctypes.c_int64) for n in "qkv"] + [
+        (n, ctypes.c_int) for n in ("dtype", "out_dtype", "n_tokens", "n_q_heads", "n_kv_heads", "head_dim")] + [
+        ("q_gamma", ctypes.c_void_p), ("k_gamma", ctypes.c_void_p), ("eps", ctypes.c_double),
+        ("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("rope_rows", ctypes.c_int), ("positions", ctypes.c_void_p),
+        ("mrope_h", ctypes.c_int), ("lengths", ctypes.c_void_p), ("offsets", ctypes.c_void_p), ("n_new", ctypes.c_void_p),
+        ("n_streams", ctypes.c_int), ("pages", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+        ("table_stride", ctypes.c_int64), ("table_pages", ctypes.c_int)]
 
 
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t
@@ -130,6 +141,7 @@ _SIGS = {
     "qd_attn_cached": ([_vp, _vp, _i32, _vp, _i64, _i64, _vp, _i64, _i64, _i32, _i32, _i32, ctypes.c_float, _vp, _vp,
                         _i32, _vp, _sz, _vp], _i32),
     "qd_attn_cached_workspace": ([_vp, _vp, _i32, _i32, _i32, _i32, _i32, _P(_sz)], _i32),
+    "qd_qk_norm_rope": ([_vp, _vp], _i32),
     "qd_verify_drafts": ([_vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp], _i32),
 }
 for _name, (_args, _res) in _SIGS.items():
@@ -675,7 +687,7 @@ def _setup_ops():
     from . import _qd_ops
     t = _T()
     _qd_ops.setup(*(ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in (
-        "qd_kv_append", "qd_kv_read", "qd_attn_cached", "qd_attn_cached_workspace", "qd_verify_drafts")),
+        "qd_kv_append", "qd_kv_read", "qd_attn_cached", "qd_attn_cached_workspace", "qd_verify_drafts", "qd_qk_norm_rope")),
         t.float32, t.bfloat16, t.int32, t._C._cuda_getCurrentRawStream, t._C._cuda_isCurrentStreamCapturing)
     _ops = _qd_ops
     return _ops
@@ -766,3 +778,19 @@ def qd_verify_drafts(target_probs, draft_ids, u, out_ids, n_accepted, draft_prob
     st = (_ops or _setup_ops()).verify(target_probs, draft_ids, u, out_ids, n_accepted, draft_probs, n_draft, stream)
     if st != QD_OK:
         raise QDError(st, "qd_verify_drafts failed")
+
+
+def qd_qk_norm_rope(q, k, q_out, cos=None, sin=None, lengths=None, v=None, k_out=None, v_out=None, q_gamma=None, k_gamma=None,
+                    eps: float = 1e-6, offsets=None, n_new=None, positions=None, mrope_h: int = 0,
+                    pages: Optional[KvCache] = None, page_table=None, stream=None):
+    """Normalise the heads of q [tokens, q_heads, head_dim] and k [tokens, kv_heads, head_dim] (fp32 or bf16, slices of a
+    fused projection as they are) by q_gamma, k_gamma (fp32 [head_dim]), rotate them by the tables cos, sin
+    (fp32 [positions, head_dim / 2]) and write them to q_out, k_out (fp32 or bf16), v to v_out, and k and v into the
+    pages (a KvCache of [pages, kv_heads, page, head_dim]) that page_table (int32 [streams, pages of one]) names.
+    The streams' rows stand packed (offsets, int32 [streams + 1]) or tokens / streams each (n_new of them in use);
+    lengths (int32 [streams]) counts them in.  positions (int32 [tokens], or [3, tokens] with mrope_h)
+    rotates by other positions than the cache's."""
+    st = (_ops or _setup_ops()).rope(q, k, v, q_out, k_out, v_out, cos, sin, lengths, offsets, n_new, positions, mrope_h, q_gamma,
+                                     k_gamma, eps, None if pages is None else pages.addr, page_table, stream)
+    if st != QD_OK:
+        raise QDError(st, "qd_qk_norm_rope failed")

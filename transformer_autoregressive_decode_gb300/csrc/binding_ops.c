@@ -18,11 +18,13 @@ typedef qd_status (*attn_fn)(const qd_kv_cache *, const qd_kv_cache *, int, cons
 typedef qd_status (*space_fn)(const qd_kv_cache *, const qd_kv_cache *, int, int, int, int, int, size_t *);
 typedef qd_status (*verify_fn)(const float *, int64_t, int64_t, const float *, int64_t, int64_t, const int32_t *,
                                const int32_t *, const float *, int, int, int, int32_t *, int32_t *, void *);
+typedef qd_status (*rope_fn)(const qd_rope_rows *, void *);
 
 static rows_fn f_append, f_read;
 static attn_fn f_attn;
 static space_fn f_space;
 static verify_fn f_verify;
+static rope_fn f_rope;
 static PyObject *t_f32, *t_bf16, *t_i32;               /* torch's types */
 static PyObject *raw_stream, *capturing;               /* its current raw stream of a device; whether that is being captured */
 static PyObject *s_shape, *s_stride, *s_dtype, *s_ptr, *s_device, *s_stream;
@@ -297,6 +299,118 @@ static PyObject *py_verify(PyObject *self, PyObject *const *a, Py_ssize_t nargs)
                                     (int)B, (int)T, (int)V, (int32_t *)out, (int32_t *)acc, s));
 }
 
+/* A tensor [tokens, heads, head_dim] whose heads are contiguous; tokens < 0: any.  None: a null pointer. */
+static int read_heads(PyObject *o, const char *what, int64_t tokens, int64_t heads, int64_t d, Tensor *t) {
+    memset(t, 0, sizeof *t);
+    if (o == Py_None) return 1;
+    if (!read_tensor(o, t)) return 0;
+    if (t->nd != 3 || (tokens >= 0 && t->shape[0] != tokens) || (heads >= 0 && t->shape[1] != heads) || (d >= 0 && t->shape[2] != d) ||
+        (t->shape[2] > 1 && t->stride[2] != 1) || (t->shape[1] > 1 && t->stride[1] != t->shape[2])) {
+        PyErr_Format(PyExc_ValueError, "%s must be [tokens, heads, head_dim], a token's heads contiguous", what);
+        return 0;
+    }
+    return fits(t);
+}
+static int64_t token_stride(const Tensor *t) { return t->shape[0] > 1 ? t->stride[0] : t->shape[1] * t->shape[2]; }
+
+/* contiguous fp32 values of n columns: a vector (rows NULL) or rows of them; None: a null pointer */
+static int read_floats(PyObject *o, const char *what, int64_t n, int64_t *rows, const float **to) {
+    Tensor t;
+    *to = NULL;
+    if (o == Py_None) return 1;
+    if (!read_tensor(o, &t)) return 0;
+    if (t.type != t_f32 || t.nd != (rows ? 2 : 1) || t.shape[t.nd - 1] != n || t.stride[t.nd - 1] != 1 ||
+        (rows && t.shape[0] > 1 && t.stride[0] != n)) {
+        PyErr_Format(PyExc_ValueError, "%s must be contiguous fp32 of %lld columns", what, (long long)n);
+        return 0;
+    }
+    if (rows) *rows = t.shape[0];
+    *to = (const float *)t.ptr;
+    return fits(&t);
+}
+
+/* page_table: int32 [streams, pages of one], a stream's contiguous */
+static int read_table(PyObject *o, int64_t streams, const int32_t **to, int64_t *stride, int *pages) {
+    Tensor t;
+    if (!read_tensor(o, &t)) return 0;
+    if (t.type != t_i32 || t.nd != 2 || t.shape[0] != streams || (t.shape[1] > 1 && t.stride[1] != 1)) {
+        PyErr_Format(PyExc_ValueError, "page_table must be int32 [%lld, pages], rows contiguous", (long long)streams);
+        return 0;
+    }
+    *to = (const int32_t *)t.ptr, *stride = t.shape[0] > 1 ? t.stride[0] : 0, *pages = (int)t.shape[1];
+    return fits(&t);
+}
+
+/* the values of a one-dimensional int32 tensor, or -1 */
+static int64_t length_of(PyObject *o) {
+    Tensor t;
+    if (!read_tensor(o, &t)) return -1;
+    if (t.nd != 1) {
+        bad("one axis is wanted");
+        return -1;
+    }
+    return t.shape[0];
+}
+
+/* rope(q, k, v, q_out, k_out, v_out, cos, sin, lengths, offsets, n_new, positions, mrope_h, q_gamma, k_gamma, eps, pages, page_table,
+ * stream) */
+static PyObject *py_rope(PyObject *self, PyObject *const *a, Py_ssize_t nargs) {
+    NARGS(19)
+    Tensor q, k, v, qo, ko, vo;
+    qd_rope_rows r;
+    memset(&r, 0, sizeof r);
+    if (a[0] == Py_None || a[1] == Py_None || a[3] == Py_None) {
+        bad("q, k and q_out are wanted");
+        return NULL;
+    }
+    if (!read_heads(a[0], "q", -1, -1, -1, &q)) return NULL;
+    const int64_t N = q.shape[0], D = q.shape[2];
+    if (!read_heads(a[1], "k", N, -1, D, &k)) return NULL;
+    const int64_t H = k.shape[1];
+    if (!read_heads(a[2], "v", N, H, D, &v) || !read_heads(a[3], "q_out", N, q.shape[1], D, &qo) ||
+        !read_heads(a[4], "k_out", N, H, D, &ko) || !read_heads(a[5], "v_out", N, H, D, &vo))
+        return NULL;
+    if (k.type != q.type || (v.ptr && v.type != q.type) || (ko.ptr && ko.type != qo.type) || (vo.ptr && vo.type != qo.type)) {
+        bad("q, k, v are of one type, and their results of one");
+        return NULL;
+    }
+    if (!type_of(&q, &r.dtype) || !type_of(&qo, &r.out_dtype)) return NULL;
+    int64_t n_cos = 0, n_sin = 0;
+    if (!read_floats(a[6], "cos", D / 2, &n_cos, &r.cos) || !read_floats(a[7], "sin", D / 2, &n_sin, &r.sin) ||
+        !read_floats(a[13], "q_gamma", D, NULL, &r.q_gamma) || !read_floats(a[14], "k_gamma", D, NULL, &r.k_gamma))
+        return NULL;
+    if (n_cos != n_sin) {
+        bad("cos and sin have the same rows");
+        return NULL;
+    }
+    int64_t B = 0;
+    if (a[8] != Py_None && (B = length_of(a[8])) < 0) return NULL;
+    if (!read_ints(a[8], B, &r.lengths, "lengths") || !read_ints(a[9], B + 1, &r.offsets, "offsets") ||
+        !read_ints(a[10], B, &r.n_new, "n_new") || !opt_int(a[12], 0, &r.mrope_h) ||
+        !read_ints(a[11], r.mrope_h ? 3 * N : N, &r.positions, "positions"))
+        return NULL;
+    r.eps = PyFloat_AsDouble(a[15]);
+    if (r.eps == -1.0 && PyErr_Occurred()) return NULL;
+    if ((a[16] == Py_None) != (a[17] == Py_None)) {
+        bad("pages and page_table come together");
+        return NULL;
+    }
+    if (a[16] != Py_None) {
+        r.pages = (const qd_kv_cache *)PyLong_AsVoidPtr(a[16]);
+        if (PyErr_Occurred() || !read_table(a[17], B, &r.page_table, &r.table_stride, &r.table_pages)) return NULL;
+    }
+    void *s;
+    long dev;
+    if (!stream_of(a[18], a[0], &s, &dev)) return NULL;
+    if (N == 0) return PyLong_FromLong(QD_OK);
+    r.q = q.ptr, r.k = k.ptr, r.v = v.ptr, r.q_out = qo.ptr, r.k_out = ko.ptr, r.v_out = vo.ptr;
+    r.q_stride = token_stride(&q), r.k_stride = token_stride(&k), r.v_stride = v.ptr ? token_stride(&v) : 0;
+    r.q_out_stride = token_stride(&qo), r.k_out_stride = ko.ptr ? token_stride(&ko) : 0, r.v_out_stride = vo.ptr ? token_stride(&vo) : 0;
+    r.n_tokens = (int)N, r.n_q_heads = (int)q.shape[1], r.n_kv_heads = (int)H, r.head_dim = (int)D;
+    r.rope_rows = (int)n_cos, r.n_streams = (int)B;
+    return PyLong_FromLong(f_rope(&r, s));
+}
+
 /* keep(device, stream, tensor, pointer, bytes): scratch of a stream from now on, where there is room to note it.  Address
  * and tensor change together, so another thread's call between the two cannot leave an address of freed memory. */
 static PyObject *py_keep(PyObject *self, PyObject *args) {
@@ -330,16 +444,17 @@ static PyObject *py_release(PyObject *self, PyObject *none) {
     Py_RETURN_NONE;
 }
 
-/* setup(append, read, attn, workspace, verify: addresses; float32, bfloat16, int32, current raw stream, whether it is being
+/* setup(append, read, attn, workspace, verify, rope: addresses; float32, bfloat16, int32, current raw stream, whether it is being
  * captured: torch's) */
 static PyObject *py_setup(PyObject *self, PyObject *args) {
-    unsigned long long f[5];
-    if (!PyArg_ParseTuple(args, "KKKKKOOOOO", &f[0], &f[1], &f[2], &f[3], &f[4], &t_f32, &t_bf16, &t_i32, &raw_stream,
+    unsigned long long f[6];
+    if (!PyArg_ParseTuple(args, "KKKKKKOOOOO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &t_f32, &t_bf16, &t_i32, &raw_stream,
                           &capturing))
         return NULL;
     Py_INCREF(t_f32), Py_INCREF(t_bf16), Py_INCREF(t_i32), Py_INCREF(raw_stream), Py_INCREF(capturing);
     f_append = (rows_fn)(uintptr_t)f[0], f_read = (rows_fn)(uintptr_t)f[1], f_attn = (attn_fn)(uintptr_t)f[2];
     f_space = (space_fn)(uintptr_t)f[3], f_verify = (verify_fn)(uintptr_t)f[4];
+    f_rope = (rope_fn)(uintptr_t)f[5];
     Py_RETURN_NONE;
 }
 
@@ -349,6 +464,7 @@ static PyMethodDef methods[] = {{"setup", py_setup, METH_VARARGS, NULL},
                                 {"release", py_release, METH_NOARGS, NULL},
                                 {"attn", (PyCFunction)(void (*)(void))py_attn, METH_FASTCALL, NULL},
                                 {"verify", (PyCFunction)(void (*)(void))py_verify, METH_FASTCALL, NULL},
+                                {"rope", (PyCFunction)(void (*)(void))py_rope, METH_FASTCALL, NULL},
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_qd_ops", NULL, -1, methods, NULL, NULL, NULL, NULL};
 

@@ -75,6 +75,20 @@ inline qd_status check_cache(const qd_kv_cache *c, int dev, bool one_stream) {
     return QD_OK;
 }
 
+// The checks of a cache in pages (its streams are the pages, its positions a page's) and of the streams' table of them.
+inline qd_status check_pages(const qd_kv_cache *c, const int32_t *table, int64_t table_stride, int table_pages, int n_streams, int dev,
+                             int *shift) {
+    const qd_status st = check_cache(c, dev, false);
+    if (st != QD_OK) return st;
+    if (c->smax < 16 || (c->smax & (c->smax - 1)) || c->smax > (1 << 20)) return QD_EUNSUPPORTED;
+    if (!table || !is_aligned(table, 4) || table_pages < 1 || n_streams < 1 || table_stride < 0 || table_stride > (int64_t(1) << 40))
+        return QD_EINVAL;
+    if ((int64_t)table_pages * c->smax > INT32_MAX - 1024) return QD_EUNSUPPORTED;
+    if (dev >= 0 && !on_device(table, dev)) return QD_EINVAL;
+    for (*shift = 4; (1 << *shift) < c->smax;) ++*shift;
+    return QD_OK;
+}
+
 // What a call writes must have bytes of its own: pieces of `inner` elements of e bytes at every combination of the
 // axes' steps (in elements), in one array or in two `pair` bytes apart.  From the smallest step on, each has to pass over all that the
 // smaller ones span; axes that interleave without nesting are refused too.
