@@ -717,6 +717,24 @@ typedef struct {
  * each other), QD_EUNSUPPORTED (head_dim, page, more than 2^30 tokens or 65536 heads), QD_ECUDA. */
 qd_status qd_qk_norm_rope(const qd_rope_rows *rows, void *cuda_stream);
 
+/* qd_attn_paged -- attention of every stream's new tokens over its cache in pages:
+ *   out[b][t][h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q[b][t][h] . k_j - max)
+ * over the stream's positions j < lengths[b] - (n_new[b] - 1 - t) (lengths outside [0, max_length] are taken as the
+ * nearest end), with key/value head h / (n_q_heads / n_kv_heads).  Arguments that qd_attn_cached has too, queries that see no position,
+ * unseen places, bits kept, limits and the workspace are as there.  max_length is at most table_pages * page.
+ * Only the table's entries for positions below the length are read.  Where one of them is outside the pool, nothing is read there and
+ * all of the stream's rows in use become NaN.  Several streams (or positions) may share pages.
+ * Errors: as qd_attn_cached, and QD_EINVAL (table), QD_EUNSUPPORTED (page). */
+qd_status qd_attn_paged(const qd_kv_cache *pages, const int32_t *page_table_dev, int64_t table_stride, int table_pages, int n_streams,
+                        const void *q_dev, int64_t q_stream_stride, int64_t q_token_stride, void *out_dev, int64_t out_stream_stride,
+                        int64_t out_token_stride, int dtype, int n_tokens, int n_q_heads, float scale, const int32_t *lengths_dev,
+                        const int32_t *n_new_dev, int max_length, void *workspace_dev, size_t workspace_bytes, void *cuda_stream);
+
+/* Bytes of workspace that qd_attn_paged needs on the current device for these sizes (HOST *bytes); of the pages only the
+ * sizes, strides and formats are looked at.  Errors as qd_attn_paged. */
+qd_status qd_attn_paged_workspace(const qd_kv_cache *pages, int n_streams, int table_pages, int dtype, int n_tokens, int n_q_heads,
+                                  int max_length, size_t *bytes);
+
 #ifdef __cplusplus
 }
 #endif

@@ -124,3 +124,53 @@ def test_rope_marshalling(qd, bad):
           "table": dict(page_table=z(3, 2, dtype=i)), "pages": dict(pages=None), "float lengths": dict(lengths=z(2))}[bad]
     with pytest.raises(ValueError):
         qd.qd_qk_norm_rope(a.pop("q"), a.pop("k"), a.pop("q_out"), **a)
+
+
+def paged(qd, **kw):
+    """4 streams of 2 tokens, 4 query and 2 key heads, fp32."""
+    f = dict(table=9 * A, table_stride=2, table_pages=2, n_streams=4, q=A, qs=512, qt=256, out=2 * A, os=512, ot=256, dtype=0, n_tokens=2,
+             n_q_heads=4, scale=0.125, lengths=8 * A, n_new=None, max_length=32, ws=None, ws_bytes=0)
+    c = pool(qd, **kw.pop("pool", {}))
+    f.update(kw)
+    return qd._lib.qd_attn_paged(ctypes.addressof(c), *f.values(), None)
+
+
+PAGED = [
+    (dict(), OK), (dict(n_new=10 * A), OK), (dict(dtype=1), OK), (dict(max_length=1), OK), (dict(table_stride=0), OK),
+    (dict(table=None), EINVAL), (dict(table=9 * A + 2), EINVAL), (dict(table_pages=0), EINVAL), (dict(table_stride=-2), EINVAL),
+    (dict(n_streams=0), EINVAL), (dict(max_length=33), EINVAL), (dict(max_length=0), EINVAL), (dict(dtype=3), EINVAL),
+    (dict(n_tokens=0), EINVAL), (dict(n_tokens=65), EUNS), (dict(n_q_heads=3), EINVAL), (dict(n_q_heads=1), EINVAL),
+    (dict(scale=float("nan")), EINVAL), (dict(scale=float("inf")), EINVAL),
+    (dict(q=None), EINVAL), (dict(out=None), EINVAL), (dict(lengths=None), EINVAL), (dict(q=A + 8), EINVAL), (dict(qt=258), EINVAL),
+    (dict(out=A), EINVAL), (dict(out=A + 1024), EINVAL), (dict(ot=128), EINVAL), (dict(os=256), EINVAL), (dict(n_new=10 * A + 1), EINVAL),
+    (dict(pool=dict(smax=48)), EUNS), (dict(pool=dict(head_dim=32)), EUNS), (dict(pool=dict(k=None)), EINVAL),
+    (dict(pool=dict(k_scale=None)), EINVAL), (dict(pool=dict(format=2)), EINVAL),
+    (dict(n_streams=(1 << 22) + 1), EUNS),      # 2 tokens x 2 heads of each key head x 2^22 streams are the 2^24 rows allowed
+    (dict(table_pages=1 << 27, max_length=1 << 20), EUNS),
+]
+
+
+@pytest.mark.parametrize("kw, want", PAGED)
+def test_paged_refusals(qd, accepted, kw, want):
+    got = paged(qd, **kw)
+    if want:
+        assert got == getattr(qd, want)
+    elif accepted is not None:
+        assert got == accepted
+
+
+@pytest.mark.parametrize("bad", ["streams", "heads", "table", "type", "lengths", "long", "workspace"])
+def test_paged_marshalling(qd, bad):
+    import torch
+    z, i = torch.zeros, torch.int32
+    c = qd.KvCache(z(4, 2, 16, 64, dtype=torch.bfloat16), z(4, 2, 16, 64, dtype=torch.bfloat16))
+    a = dict(q=z(2, 1, 4, 64), table=z(2, 2, dtype=i), lengths=z(2, dtype=i), out=z(2, 1, 4, 64))
+    more = {}
+    if bad == "workspace":
+        more = dict(workspace=z(1, dtype=torch.uint8).expand(1 << 20))
+    else:
+        a |= {"streams": dict(out=z(3, 1, 4, 64)), "heads": dict(q=z(2, 1, 64, 4).transpose(2, 3)), "table": dict(table=z(2, 2)),
+              "type": dict(out=z(2, 1, 4, 64, dtype=torch.bfloat16)), "lengths": dict(lengths=z(3, dtype=i)),
+              "long": dict(table=z(2, 1, dtype=i).expand(2, 2))}[bad]
+    with pytest.raises(ValueError):
+        qd.qd_attn_paged(a["q"], c, a["table"], a["lengths"], a["out"], **more)

@@ -45,7 +45,7 @@ EXPORTS = ("qd_create", "qd_destroy", "qd_reset", "qd_prefill", "qd_prefill_mrop
            "qd_batch_set_stream", "qd_batch_decode", "qd_batch_sync", "qd_batch_get_logits", "qd_batch_copy_kv",
            "qd_batch_get_pos", "qd_batch_get_launch_count", "qd_batch_set_graphs", "qd_batch_time_kernel", "qd_batch_prefill",
            "qd_batch_set_sampling", "qd_kv_append", "qd_kv_read", "qd_attn_cached", "qd_attn_cached_workspace",
-           "qd_verify_drafts", "qd_qk_norm_rope")
+           "qd_verify_drafts", "qd_qk_norm_rope", "qd_attn_paged", "qd_attn_paged_workspace")
 
 
 class qd_config(ctypes.Structure):
@@ -141,6 +141,9 @@ _SIGS = {
     "qd_attn_cached": ([_vp, _vp, _i32, _vp, _i64, _i64, _vp, _i64, _i64, _i32, _i32, _i32, ctypes.c_float, _vp, _vp,
                         _i32, _vp, _sz, _vp], _i32),
     "qd_attn_cached_workspace": ([_vp, _vp, _i32, _i32, _i32, _i32, _i32, _P(_sz)], _i32),
+    "qd_attn_paged": ([_vp, _vp, _i64, _i32, _i32, _vp, _i64, _i64, _vp, _i64, _i64, _i32, _i32, _i32, ctypes.c_float, _vp, _vp, _i32, _vp,
+                       _sz, _vp], _i32),
+    "qd_attn_paged_workspace": ([_vp, _i32, _i32, _i32, _i32, _i32, _i32, _P(_sz)], _i32),
     "qd_qk_norm_rope": ([_vp, _vp], _i32),
     "qd_verify_drafts": ([_vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp], _i32),
 }
@@ -687,7 +690,8 @@ def _setup_ops():
     from . import _qd_ops
     t = _T()
     _qd_ops.setup(*(ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in (
-        "qd_kv_append", "qd_kv_read", "qd_attn_cached", "qd_attn_cached_workspace", "qd_verify_drafts", "qd_qk_norm_rope")),
+        "qd_kv_append", "qd_kv_read", "qd_attn_cached", "qd_attn_cached_workspace", "qd_verify_drafts", "qd_qk_norm_rope", "qd_attn_paged",
+        "qd_attn_paged_workspace")),
         t.float32, t.bfloat16, t.int32, t._C._cuda_getCurrentRawStream, t._C._cuda_isCurrentStreamCapturing)
     _ops = _qd_ops
     return _ops
@@ -702,7 +706,7 @@ _SCRATCH_MOST = 128 << 20
 
 
 def release_scratch():
-    """Give the scratch that qd_attn_cached keeps for the streams it was called on (one tensor each, 128 MB
+    """Give the scratch that qd_attn_cached and qd_attn_paged keep for the streams it was called on (one tensor each, 128 MB
     at most) back to torch's allocator; the next call on a stream takes new."""
     if _ops is not None:
         _ops.release()
@@ -714,6 +718,23 @@ def _fresh(need: int, t, stream):
         return torch.empty(need, dtype=torch.uint8, device=t.device)
     with torch.cuda.stream(stream):
         return torch.empty(need, dtype=torch.uint8, device=t.device)
+
+
+def _with_scratch(ops, call, args, q, workspace, stream):
+    """call(*args, workspace, its bytes, stream) with the caller's workspace, the stream's own scratch, or fresh memory."""
+    if workspace is not None:
+        if not workspace.is_contiguous():       # an expanded one has fewer bytes than it counts
+            raise ValueError("workspace must be contiguous")
+        return call(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream)
+    st = call(*args, None, 0, stream)
+    if st <= 0:
+        return st
+    need, torch = st, _T()                      # the bytes of scratch that there is none of
+    keep = need <= _SCRATCH_MOST and stream is None and q.is_cuda and not torch._C._cuda_isCurrentStreamCapturing()
+    ws = _fresh(max(need, 1 << 20) if keep else need, q, stream)
+    if keep:
+        ops.keep(q.get_device(), torch._C._cuda_getCurrentRawStream(q.get_device()), ws, ws.data_ptr(), ws.numel())
+    return call(*args, ws.data_ptr(), ws.numel(), stream)
 
 
 def qd_kv_append(cache: KvCache, k_rows, v_rows, lengths, n_new=None, stream=None):
@@ -753,19 +774,7 @@ def qd_attn_cached(q, cache: KvCache, lengths, out, n_new=None, max_length: Opti
     stream's own scratch, kept until release_scratch() (in a capture: fresh memory of the graph's)."""
     ops = _ops or _setup_ops()
     args = (q, cache.addr, lengths, out, n_new, max_length, scale, None if prefix is None else prefix.addr, prefix_length)
-    if workspace is not None:
-        if not workspace.is_contiguous():       # an expanded one has fewer bytes than it counts
-            raise ValueError("workspace must be contiguous")
-        st = ops.attn(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream)
-    else:
-        st = ops.attn(*args, None, 0, stream)
-        if st > 0:                                  # the bytes of scratch that there is none of
-            need, torch = st, _T()
-            keep = need <= _SCRATCH_MOST and stream is None and q.is_cuda and not torch._C._cuda_isCurrentStreamCapturing()
-            ws = _fresh(max(need, 1 << 20) if keep else need, q, stream)
-            if keep:
-                ops.keep(q.get_device(), torch._C._cuda_getCurrentRawStream(q.get_device()), ws, ws.data_ptr(), ws.numel())
-            st = ops.attn(*args, ws.data_ptr(), ws.numel(), stream)
+    st = _with_scratch(ops, ops.attn, args, q, workspace, stream)
     if st != QD_OK:
         raise QDError(st, "qd_attn_cached failed")
 
@@ -794,3 +803,26 @@ def qd_qk_norm_rope(q, k, q_out, cos=None, sin=None, lengths=None, v=None, k_out
                                      k_gamma, eps, None if pages is None else pages.addr, page_table, stream)
     if st != QD_OK:
         raise QDError(st, "qd_qk_norm_rope failed")
+
+
+def qd_attn_paged_workspace(pages: KvCache, n_streams: int, table_pages: int, bf16: bool, n_tokens: int, n_q_heads: int,
+                            max_length: Optional[int] = None) -> int:
+    """Bytes of workspace of a qd_attn_paged call of these sizes (0: none)."""
+    n = ctypes.c_size_t(0)
+    st = _lib.qd_attn_paged_workspace(pages.addr, n_streams, table_pages, QD_BF16 if bf16 else QD_F32, n_tokens, n_q_heads,
+                                      table_pages * pages.shape[2] if max_length is None else int(max_length), ctypes.byref(n))
+    if st != QD_OK:
+        raise QDError(st, "qd_attn_paged_workspace failed")
+    return n.value
+
+
+def qd_attn_paged(q, pages: KvCache, page_table, lengths, out, n_new=None, max_length: Optional[int] = None, scale=None, workspace=None,
+                  stream=None):
+    """Attention of the new tokens q [streams, tokens, q_heads, head_dim] (fp32 or bf16) over each stream's positions in
+    the pages (a KvCache of [pages, kv_heads, page, head_dim]) that page_table (int32 [streams, pages of one]) names, into
+    out (same type and shape).  max_length: bound of the lengths (default: what the table can name); scale and
+    workspace (of qd_attn_paged_workspace bytes) as in qd_attn_cached."""
+    ops = _ops or _setup_ops()
+    st = _with_scratch(ops, ops.paged, (q, pages.addr, page_table, lengths, out, n_new, max_length, scale), q, workspace, stream)
+    if st != QD_OK:
+        raise QDError(st, "qd_attn_paged failed")

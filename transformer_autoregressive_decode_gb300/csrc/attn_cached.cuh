@@ -30,12 +30,19 @@ struct CachedArgs {
     // partials of attn_share_kernel: [slot][rows of a CTA]
     float2 *s_ml;
     float *s_o;
+    // a cache in pages: c's streams are the pages
+    const int32_t *table;
+    int64_t table_stride;
+    int page_shift, n_pages;
 };
 
 // Probabilities stand 2^10 above 1 at the running maximum and may grow to 2^15 before the
 // sums are rescaled: fp16 then keeps 11 (two parts: 22) bits of every weight down to 2^-24
 // (2^-10) of the largest, and small moves of the maximum cost nothing.
 constexpr float kAcUp = 10.f, kAcRoom = 15.f;
+// The largest log2 of a scale: finite rows have 2^121 at most, and the reference has to stay finite for an infinite one, whose
+// weight then is infinite, as the element is.
+constexpr float kScaleMost = 122.f;
 
 __device__ __forceinline__ float ex2(float x) {
     float y;

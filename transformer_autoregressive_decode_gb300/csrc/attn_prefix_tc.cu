@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) attn_prefix_tc_kernel(const Cac
                     store(sm + C::kV + (uint32_t)(st * KB) * kWtBox, uv);
                     // the scales come with V, which is not given up before its softmax is done (K's tile is)
                     float *sc = reinterpret_cast<float *>(sm + C::kSc) + st * 384;
-                    sc[tid] = sk, sc[128 + tid] = sv, sc[256 + tid] = fmaxf(lg2(fabsf(sv)), -60.f);
+                    sc[tid] = sk, sc[128 + tid] = sv, sc[256 + tid] = fminf(fmaxf(lg2(fabsf(sv)), -60.f), kScaleMost);
                     fence_proxy_async_smem();
                     mbar_arrive(&v_full[st]);
                     if (i + 1 < w.n) {

@@ -18,6 +18,9 @@ typedef qd_status (*attn_fn)(const qd_kv_cache *, const qd_kv_cache *, int, cons
 typedef qd_status (*space_fn)(const qd_kv_cache *, const qd_kv_cache *, int, int, int, int, int, size_t *);
 typedef qd_status (*verify_fn)(const float *, int64_t, int64_t, const float *, int64_t, int64_t, const int32_t *,
                                const int32_t *, const float *, int, int, int, int32_t *, int32_t *, void *);
+typedef qd_status (*paged_fn)(const qd_kv_cache *, const int32_t *, int64_t, int, int, const void *, int64_t, int64_t, void *, int64_t,
+                              int64_t, int, int, int, float, const int32_t *, const int32_t *, int, void *, size_t, void *);
+typedef qd_status (*paged_space_fn)(const qd_kv_cache *, int, int, int, int, int, int, size_t *);
 typedef qd_status (*rope_fn)(const qd_rope_rows *, void *);
 
 static rows_fn f_append, f_read;
@@ -25,6 +28,8 @@ static attn_fn f_attn;
 static space_fn f_space;
 static verify_fn f_verify;
 static rope_fn f_rope;
+static paged_fn f_paged;
+static paged_space_fn f_paged_space;
 static PyObject *t_f32, *t_bf16, *t_i32;               /* torch's types */
 static PyObject *raw_stream, *capturing;               /* its current raw stream of a device; whether that is being captured */
 static PyObject *s_shape, *s_stride, *s_dtype, *s_ptr, *s_device, *s_stream;
@@ -187,6 +192,46 @@ static int opt_int(PyObject *o, int otherwise, int *to) {
     return 1;
 }
 
+/* The scratch kept for a stream, where it has `need` bytes and the stream is not being captured (the replays may run beside anything):
+ * *ws NULL otherwise */
+static int find_scratch(long dev, void *stream, size_t need, void **ws, size_t *have) {
+    *ws = NULL, *have = 0;
+    if (dev < 0) return 1;
+    PyObject *cap = PyObject_CallNoArgs(capturing);
+    if (!cap) return 0;
+    const int is = PyObject_IsTrue(cap);
+    Py_DECREF(cap);
+    for (int i = 0; !is && i < n_scratch; ++i)
+        if (scratch[i].dev == dev && scratch[i].stream == stream && scratch[i].size >= need) {
+            *ws = scratch[i].ptr, *have = scratch[i].size;
+            break;
+        }
+    return 1;
+}
+
+/* q and out: [streams, tokens, q_heads, head_dim] of one type, heads contiguous */
+static int read_queries(PyObject *qo, PyObject *oo, int64_t B, int64_t D, Tensor *q, Tensor *o, int *dtype) {
+    if (!read_tensor(qo, q) || !read_tensor(oo, o)) return 0;
+    if (q->nd != 4 || o->nd != 4 || q->type != o->type || q->shape[0] != B || q->shape[3] != D || o->shape[0] != B ||
+        o->shape[1] != q->shape[1] || o->shape[2] != q->shape[2] || o->shape[3] != D) {
+        PyErr_Format(PyExc_ValueError, "q and out must be [%lld, tokens, q_heads, %lld] of one type", (long long)B, (long long)D);
+        return 0;
+    }
+    if (q->stride[3] != 1 || o->stride[3] != 1 || (q->shape[2] > 1 && (q->stride[2] != D || o->stride[2] != D)))
+        return bad("the heads of q and out must be contiguous");
+    return fits(q) && type_of(q, dtype);
+}
+
+static int read_scale(PyObject *o, int64_t d, float *to) {
+    double scale = 1.0 / (d == 64 ? 8.0 : 11.313708498984761);   /* head_dim ** -0.5 */
+    if (o != Py_None) {
+        scale = PyFloat_AsDouble(o);
+        if (scale == -1.0 && PyErr_Occurred()) return 0;
+    }
+    *to = (float)scale;
+    return 1;
+}
+
 /* attn(q, cache, lengths, out, n_new, max_length, scale, prefix, prefix_length, workspace, workspace_bytes, stream):
  * the status; with workspace None and no scratch kept for the stream that is large enough (in a capture: none is used, the
  * replays may run beside anything), the bytes that the call needs instead of making it */
@@ -200,18 +245,9 @@ static PyObject *py_attn(PyObject *self, PyObject *const *a, Py_ssize_t nargs) {
     long dev;
     int dtype, most, plen;
     size_t have = 0;
-    if (PyErr_Occurred() || !read_tensor(a[0], &q) || !read_tensor(a[3], &o)) return NULL;
     const int64_t D = c->head_dim, B = c->n_streams;
-    if (q.nd != 4 || o.nd != 4 || q.type != o.type || q.shape[0] != B || q.shape[3] != D || o.shape[0] != B ||
-        o.shape[1] != q.shape[1] || o.shape[2] != q.shape[2] || o.shape[3] != D) {
-        PyErr_Format(PyExc_ValueError, "q and out must be [%d, tokens, q_heads, %d] of one type", c->n_streams, c->head_dim);
-        return NULL;
-    }
-    if (q.stride[3] != 1 || o.stride[3] != 1 || (q.shape[2] > 1 && (q.stride[2] != D || o.stride[2] != D))) {
-        bad("the heads of q and out must be contiguous");
-        return NULL;
-    }
-    if (!fits(&q) || !type_of(&q, &dtype) || !opt_int(a[5], c->smax, &most) || !opt_int(a[8], p ? p->smax : 0, &plen))
+    if (PyErr_Occurred() || !read_queries(a[0], a[3], B, D, &q, &o, &dtype)) return NULL;
+    if (!opt_int(a[5], c->smax, &most) || !opt_int(a[8], p ? p->smax : 0, &plen))
         return NULL;
     if (p && p->n_streams != 1) {
         bad("the prefix is a cache of one stream");
@@ -222,12 +258,8 @@ static PyObject *py_attn(PyObject *self, PyObject *const *a, Py_ssize_t nargs) {
         return NULL;
     }
     if (plen == 0) p = NULL;
-    double scale = 1.0 / (D == 64 ? 8.0 : 11.313708498984761);   /* head_dim ** -0.5 */
-    if (a[6] != Py_None) {
-        scale = PyFloat_AsDouble(a[6]);
-        if (scale == -1.0 && PyErr_Occurred()) return NULL;
-    }
-    if (!read_ints(a[2], B, &lengths, "lengths") || !read_ints(a[4], B, &n_new, "n_new") || !stream_of(a[11], a[0], &s, &dev))
+    float scale;
+    if (!read_scale(a[6], D, &scale) || !read_ints(a[2], B, &lengths, "lengths") || !read_ints(a[4], B, &n_new, "n_new") || !stream_of(a[11], a[0], &s, &dev))
         return NULL;
     const int T = (int)q.shape[1], QH = (int)q.shape[2];
     if (a[9] != Py_None) {
@@ -239,23 +271,63 @@ static PyObject *py_attn(PyObject *self, PyObject *const *a, Py_ssize_t nargs) {
         const qd_status st = f_space(c, p, plen, dtype, T, QH, most, &need);
         if (st != QD_OK) return PyLong_FromLong(st);
         if (need) {
-            int i = n_scratch;
-            if (dev >= 0) {
-                PyObject *cap = PyObject_CallNoArgs(capturing);
-                if (!cap) return NULL;
-                const int is = PyObject_IsTrue(cap);
-                Py_DECREF(cap);
-                for (i = 0; !is && i < n_scratch; ++i)
-                    if (scratch[i].dev == dev && scratch[i].stream == s && scratch[i].size >= need) break;
-                if (is) i = n_scratch;
-            }
-            if (i == n_scratch) return PyLong_FromSize_t(need);
-            ws = scratch[i].ptr, have = scratch[i].size;
+            if (!find_scratch(dev, s, need, &ws, &have)) return NULL;
+            if (!ws) return PyLong_FromSize_t(need);
         }
     }
     return PyLong_FromLong(f_attn(c, p, plen, q.ptr, B > 1 ? q.stride[0] : 0, T > 1 ? q.stride[1] : 0, o.ptr,
-                                  B > 1 ? o.stride[0] : 0, T > 1 ? o.stride[1] : 0, dtype, T, QH, (float)scale, lengths,
+                                  B > 1 ? o.stride[0] : 0, T > 1 ? o.stride[1] : 0, dtype, T, QH, scale, lengths,
                                   n_new, most, ws, have, s));
+}
+
+/* page_table: int32 [streams, pages of one], a stream's contiguous */
+static int read_table(PyObject *o, int64_t streams, const int32_t **to, int64_t *stride, int *pages) {
+    Tensor t;
+    if (!read_tensor(o, &t)) return 0;
+    if (t.type != t_i32 || t.nd != 2 || t.shape[0] != streams || (t.shape[1] > 1 && t.stride[1] != 1)) {
+        PyErr_Format(PyExc_ValueError, "page_table must be int32 [%lld, pages], rows contiguous", (long long)streams);
+        return 0;
+    }
+    *to = (const int32_t *)t.ptr, *stride = t.shape[0] > 1 ? t.stride[0] : 0, *pages = (int)t.shape[1];
+    return fits(&t);
+}
+
+/* paged(q, pages, page_table, lengths, out, n_new, max_length, scale, workspace, workspace_bytes, stream): as attn */
+static PyObject *py_paged(PyObject *self, PyObject *const *a, Py_ssize_t nargs) {
+    NARGS(11)
+    const qd_kv_cache *c = (const qd_kv_cache *)PyLong_AsVoidPtr(a[1]);
+    Tensor q, o, t;
+    const int32_t *lengths, *n_new, *table;
+    void *s, *ws = NULL;
+    long dev;
+    int dtype, most, per;
+    int64_t table_stride;
+    size_t have = 0;
+    float scale;
+    if (PyErr_Occurred() || !read_tensor(a[0], &t)) return NULL;
+    const int64_t D = c->head_dim, B = t.nd == 4 ? t.shape[0] : 0;
+    if (!read_queries(a[0], a[4], B, D, &q, &o, &dtype) || !read_table(a[2], B, &table, &table_stride, &per)) return NULL;
+    const int64_t named = (int64_t)per * c->smax;
+    if (!opt_int(a[6], named > INT32_MAX ? INT32_MAX : (int)named, &most) || !read_scale(a[7], D, &scale) ||
+        !read_ints(a[3], B, &lengths, "lengths") || !read_ints(a[5], B, &n_new, "n_new") || !stream_of(a[10], a[0], &s, &dev))
+        return NULL;
+    const int T = (int)q.shape[1], QH = (int)q.shape[2];
+    if (a[8] != Py_None) {
+        ws = PyLong_AsVoidPtr(a[8]);
+        have = PyLong_AsSize_t(a[9]);
+        if (PyErr_Occurred()) return NULL;
+    } else {
+        size_t need = 0;
+        const qd_status st = f_paged_space(c, (int)B, per, dtype, T, QH, most, &need);
+        if (st != QD_OK) return PyLong_FromLong(st);
+        if (need) {
+            if (!find_scratch(dev, s, need, &ws, &have)) return NULL;
+            if (!ws) return PyLong_FromSize_t(need);
+        }
+    }
+    return PyLong_FromLong(f_paged(c, table, table_stride, per, (int)B, q.ptr, B > 1 ? q.stride[0] : 0, T > 1 ? q.stride[1] : 0, o.ptr,
+                                   B > 1 ? o.stride[0] : 0, T > 1 ? o.stride[1] : 0, dtype, T, QH, scale, lengths, n_new, most, ws, have,
+                                   s));
 }
 
 /* verify(target_probs, draft_ids, u, out_ids, n_accepted, draft_probs, n_draft, stream) */
@@ -326,18 +398,6 @@ static int read_floats(PyObject *o, const char *what, int64_t n, int64_t *rows, 
     }
     if (rows) *rows = t.shape[0];
     *to = (const float *)t.ptr;
-    return fits(&t);
-}
-
-/* page_table: int32 [streams, pages of one], a stream's contiguous */
-static int read_table(PyObject *o, int64_t streams, const int32_t **to, int64_t *stride, int *pages) {
-    Tensor t;
-    if (!read_tensor(o, &t)) return 0;
-    if (t.type != t_i32 || t.nd != 2 || t.shape[0] != streams || (t.shape[1] > 1 && t.stride[1] != 1)) {
-        PyErr_Format(PyExc_ValueError, "page_table must be int32 [%lld, pages], rows contiguous", (long long)streams);
-        return 0;
-    }
-    *to = (const int32_t *)t.ptr, *stride = t.shape[0] > 1 ? t.stride[0] : 0, *pages = (int)t.shape[1];
     return fits(&t);
 }
 
@@ -444,17 +504,17 @@ static PyObject *py_release(PyObject *self, PyObject *none) {
     Py_RETURN_NONE;
 }
 
-/* setup(append, read, attn, workspace, verify, rope: addresses; float32, bfloat16, int32, current raw stream, whether it is being
+/* setup(append, read, attn, workspace, verify, rope, paged, its workspace: addresses; float32, bfloat16, int32, current raw stream, whether it is being
  * captured: torch's) */
 static PyObject *py_setup(PyObject *self, PyObject *args) {
-    unsigned long long f[6];
-    if (!PyArg_ParseTuple(args, "KKKKKKOOOOO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &t_f32, &t_bf16, &t_i32, &raw_stream,
+    unsigned long long f[8];
+    if (!PyArg_ParseTuple(args, "KKKKKKKKOOOOO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &f[7], &t_f32, &t_bf16, &t_i32, &raw_stream,
                           &capturing))
         return NULL;
     Py_INCREF(t_f32), Py_INCREF(t_bf16), Py_INCREF(t_i32), Py_INCREF(raw_stream), Py_INCREF(capturing);
     f_append = (rows_fn)(uintptr_t)f[0], f_read = (rows_fn)(uintptr_t)f[1], f_attn = (attn_fn)(uintptr_t)f[2];
     f_space = (space_fn)(uintptr_t)f[3], f_verify = (verify_fn)(uintptr_t)f[4];
-    f_rope = (rope_fn)(uintptr_t)f[5];
+    f_rope = (rope_fn)(uintptr_t)f[5], f_paged = (paged_fn)(uintptr_t)f[6], f_paged_space = (paged_space_fn)(uintptr_t)f[7];
     Py_RETURN_NONE;
 }
 
@@ -464,6 +524,7 @@ static PyMethodDef methods[] = {{"setup", py_setup, METH_VARARGS, NULL},
                                 {"release", py_release, METH_NOARGS, NULL},
                                 {"attn", (PyCFunction)(void (*)(void))py_attn, METH_FASTCALL, NULL},
                                 {"verify", (PyCFunction)(void (*)(void))py_verify, METH_FASTCALL, NULL},
+                                {"paged", (PyCFunction)(void (*)(void))py_paged, METH_FASTCALL, NULL},
                                 {"rope", (PyCFunction)(void (*)(void))py_rope, METH_FASTCALL, NULL},
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_qd_ops", NULL, -1, methods, NULL, NULL, NULL, NULL};

@@ -117,6 +117,20 @@ inline int64_t bytes_between(const void *a, const void *b) {
     return (int64_t)(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
 }
 
+// out's rows [B][T] of `row` elements of e bytes must lie neither over each other nor over q's; strides in elements.
+inline bool rows_apart(const void *q, int64_t q_stream, int64_t q_token, const void *out, int64_t out_stream, int64_t out_token, int64_t e,
+                       int64_t B, int64_t T, int64_t row) {
+    const bool alike = (T == 1 || q_token == out_token) && (B == 1 || q_stream == out_stream);
+    if (q == out || !apart(e, row, {{T, out_token}, {B, out_stream}}, alike ? bytes_between(q, out) : 0)) return false;
+    if (!alike) {                                    // rows of two layouts: not in the same stretch of memory
+        const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(out);
+        const uintptr_t q1 = ((uintptr_t)(T - 1) * q_token + (uintptr_t)(B - 1) * q_stream + row) * e;
+        const uintptr_t o1 = ((uintptr_t)(T - 1) * out_token + (uintptr_t)(B - 1) * out_stream + row) * e;
+        if (q0 < o0 ? o0 - q0 < q1 : q0 - o0 < o1) return false;
+    }
+    return true;
+}
+
 inline KvView kv_view(const qd_kv_cache *c) {
     const int64_t e = c->format == QD_KV_Q8 ? 1 : 2;
     return {static_cast<const uint8_t *>(c->k), static_cast<const uint8_t *>(c->v), c->k_scale, c->v_scale,
