@@ -717,6 +717,31 @@ typedef struct {
  * each other), QD_EUNSUPPORTED (head_dim, page, more than 2^30 tokens or 65536 heads), QD_ECUDA. */
 qd_status qd_qk_norm_rope(const qd_rope_rows *rows, void *cuda_stream);
 
+/* qd_attn_prompt -- causal attention over whole prompts, packed one after the other:
+ *   out[i][h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q[i][h] . k_j - max)
+ * Sequence b's queries are rows [offsets[b], offsets[b + 1]) of q and out, its keys and values rows [kv_offsets[b],
+ * kv_offsets[b + 1]) of k and v (DEVICE int32 [n_seqs + 1]; kv_offsets NULL: the same rows, n_kv_tokens == n_tokens).  Its
+ * last query sees all of its keys, each one before it one key less: a prompt's later chunk has more keys
+ * than queries; a query that sees none gives zeros.  Key/value head h / (n_q_heads / n_kv_heads).  What a
+ * query does not see never reaches its result, NaN and infinity included; an infinite value that it does see makes its
+ * dim infinite or NaN.
+ * Element (row n, head h, dim d) of q is q[n * q_stride + h * head_dim + d], likewise k, v, out: bf16, 16-byte aligned,
+ * strides in elements, multiples of 8.  Scores, softmax and sums are fp32; a probability enters the product with V as one bf16
+ * (8 bits).  out lies over none of the inputs (rows of one stride may stand beside each other).
+ * Rows that belong to no sequence are left as they are.  Offsets are taken into [0, n_tokens] ([0, n_kv_tokens]); they ascend: a sequence
+ * whose end is before its beginning is empty, and rows that they give to several sequences may hold any of their results.
+ * workspace_dev: DEVICE, 256-byte aligned, qd_attn_prompt_workspace bytes (0 for small calls: NULL is allowed); scratch
+ * of one call, as for qd_attn_cached.
+ * Errors: QD_EINVAL (arguments, alignment, memory, workspace, an out that lies over something), QD_EUNSUPPORTED (head_dim, more
+ * than 128 query heads a key head or 65536 in all, 2^30 tokens, 2^24 sequences), QD_ECUDA. */
+qd_status qd_attn_prompt(const void *q_dev, int64_t q_stride, const void *k_dev, int64_t k_stride, const void *v_dev, int64_t v_stride,
+                         void *out_dev, int64_t out_stride, int n_tokens, int n_kv_tokens, int n_q_heads, int n_kv_heads, int head_dim,
+                         float scale, const int32_t *offsets_dev, const int32_t *kv_offsets_dev, int n_seqs, void *workspace_dev,
+                         size_t workspace_bytes, void *cuda_stream);
+
+/* Bytes of workspace that qd_attn_prompt needs on the current device for these sizes (HOST *bytes).  Errors as qd_attn_prompt. */
+qd_status qd_attn_prompt_workspace(int n_tokens, int n_kv_tokens, int n_seqs, int n_q_heads, int n_kv_heads, int head_dim, size_t *bytes);
+
 /* qd_attn_paged -- attention of every stream's new tokens over its cache in pages:
  *   out[b][t][h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q[b][t][h] . k_j - max)
  * over the stream's positions j < lengths[b] - (n_new[b] - 1 - t) (lengths outside [0, max_length] are taken as the

@@ -174,3 +174,58 @@ def test_paged_marshalling(qd, bad):
               "long": dict(table=z(2, 1, dtype=i).expand(2, 2))}[bad]
     with pytest.raises(ValueError):
         qd.qd_attn_paged(a["q"], c, a["table"], a["lengths"], a["out"], **more)
+
+
+def attend_prompt(qd, **kw):
+    """100 tokens, 4 query and 2 key heads of 64, slices of a fused projection; results elsewhere."""
+    f = dict(q=A, qs=512, k=A + 512, ks=512, v=A + 768, vs=512, out=2 * A, os=256, n=100, m=100, qh=4, kvh=2, hd=64, scale=0.125,
+             offsets=8 * A, kv_offsets=None, seqs=3, ws=None, ws_bytes=0)
+    f.update(kw)
+    return qd._lib.qd_attn_prompt(*f.values(), None)
+
+
+PROMPT = [
+    (dict(), OK), (dict(kv_offsets=9 * A, m=200, k=3 * A, v=4 * A), OK), (dict(n=1, m=1, qs=0, ks=0, vs=0, os=0), OK), (dict(scale=-1.0), OK),
+    (dict(out=A + 1024 + 512, os=1024, qs=1024, ks=1024, vs=1024), OK),      # between the rows
+    (dict(q=None), EINVAL), (dict(k=None), EINVAL), (dict(v=None), EINVAL), (dict(out=None), EINVAL), (dict(offsets=None), EINVAL),
+    (dict(n=0), EINVAL), (dict(m=0), EINVAL), (dict(seqs=0), EINVAL), (dict(qh=3), EINVAL), (dict(qh=1), EINVAL), (dict(kvh=0), EINVAL),
+    (dict(hd=96), EUNS), (dict(qh=258), EUNS), (dict(m=200), EINVAL), (dict(seqs=(1 << 24) + 1), EUNS),
+    (dict(n=(1 << 30) + 1, m=(1 << 30) + 1), EUNS),
+    (dict(scale=float("inf")), EINVAL), (dict(q=A + 8), EINVAL), (dict(qs=508), EINVAL), (dict(qs=248), EINVAL), (dict(ks=120), EINVAL),
+    (dict(os=128), EINVAL), (dict(qs=-512), EINVAL), (dict(vs=(1 << 37) + 8), EINVAL), (dict(offsets=8 * A + 2), EINVAL),
+    (dict(kv_offsets=8 * A + 1), EINVAL),
+    (dict(out=A), EINVAL), (dict(out=A, os=512), EINVAL), (dict(out=A + 512, os=512), EINVAL), (dict(out=A + 1024 * 10), EINVAL),
+    (dict(out=A + 512, os=512, k=3 * A, v=4 * A, ks=128, vs=128), OK),
+]
+
+
+@pytest.mark.parametrize("kw, want", PROMPT)
+def test_prompt_refusals(qd, accepted, kw, want):
+    got = attend_prompt(qd, **kw)
+    if want:
+        assert got == getattr(qd, want)
+    elif accepted is not None:
+        assert got == accepted
+
+
+@pytest.mark.parametrize("bad", ["type", "heads", "keys", "offsets", "kv", "none", "workspace"])
+def test_prompt_marshalling(qd, bad):
+    import torch
+    z, i, h = torch.zeros, torch.int32, torch.bfloat16
+    a = dict(q=z(4, 4, 64, dtype=h), k=z(4, 2, 64, dtype=h), v=z(4, 2, 64, dtype=h), out=z(4, 4, 64, dtype=h), offsets=z(2, dtype=i))
+    more = {}
+    if bad == "workspace":
+        more = dict(workspace=z(1, dtype=torch.uint8).expand(1 << 20))
+    else:
+        a |= {"type": dict(q=z(4, 4, 64)), "heads": dict(out=z(4, 64, 4, dtype=h).transpose(1, 2)), "keys": dict(v=z(5, 2, 64, dtype=h)),
+              "offsets": dict(offsets=z(2)), "kv": dict(k=z(5, 2, 64, dtype=h), v=z(5, 2, 64, dtype=h)), "none": dict(offsets=None)}[bad]
+    with pytest.raises(ValueError):
+        qd.qd_attn_prompt(*a.values(), **more)
+
+
+def test_prompt_without_rows(qd):
+    """Nothing to do: no call is made (a call on host memory would be refused)."""
+    import torch
+    z, h = torch.zeros, torch.bfloat16
+    qd.qd_attn_prompt(z(0, 4, 64, dtype=h), z(0, 2, 64, dtype=h), z(0, 2, 64, dtype=h), z(0, 4, 64, dtype=h), z(3, dtype=torch.int32))
+    qd.qd_qk_norm_rope(z(0, 4, 64), z(0, 2, 64), z(0, 4, 64), positions=z(0, dtype=torch.int32))

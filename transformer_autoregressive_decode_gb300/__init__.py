@@ -45,7 +45,8 @@ EXPORTS = ("qd_create", "qd_destroy", "qd_reset", "qd_prefill", "qd_prefill_mrop
            "qd_batch_set_stream", "qd_batch_decode", "qd_batch_sync", "qd_batch_get_logits", "qd_batch_copy_kv",
            "qd_batch_get_pos", "qd_batch_get_launch_count", "qd_batch_set_graphs", "qd_batch_time_kernel", "qd_batch_prefill",
            "qd_batch_set_sampling", "qd_kv_append", "qd_kv_read", "qd_attn_cached", "qd_attn_cached_workspace",
-           "qd_verify_drafts", "qd_qk_norm_rope", "qd_attn_paged", "qd_attn_paged_workspace")
+           "qd_verify_drafts", "qd_qk_norm_rope", "qd_attn_paged", "qd_attn_paged_workspace",
+           "qd_attn_prompt", "qd_attn_prompt_workspace")
 
 
 class qd_config(ctypes.Structure):
@@ -144,6 +145,9 @@ _SIGS = {
     "qd_attn_paged": ([_vp, _vp, _i64, _i32, _i32, _vp, _i64, _i64, _vp, _i64, _i64, _i32, _i32, _i32, ctypes.c_float, _vp, _vp, _i32, _vp,
                        _sz, _vp], _i32),
     "qd_attn_paged_workspace": ([_vp, _i32, _i32, _i32, _i32, _i32, _i32, _P(_sz)], _i32),
+    "qd_attn_prompt": ([_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _i32, _i32, _i32, _i32, ctypes.c_float, _vp, _vp, _i32, _vp, _sz,
+                        _vp], _i32),
+    "qd_attn_prompt_workspace": ([_i32, _i32, _i32, _i32, _i32, _i32, _P(_sz)], _i32),
     "qd_qk_norm_rope": ([_vp, _vp], _i32),
     "qd_verify_drafts": ([_vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp], _i32),
 }
@@ -691,7 +695,7 @@ def _setup_ops():
     t = _T()
     _qd_ops.setup(*(ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in (
         "qd_kv_append", "qd_kv_read", "qd_attn_cached", "qd_attn_cached_workspace", "qd_verify_drafts", "qd_qk_norm_rope", "qd_attn_paged",
-        "qd_attn_paged_workspace")),
+        "qd_attn_paged_workspace", "qd_attn_prompt", "qd_attn_prompt_workspace")),
         t.float32, t.bfloat16, t.int32, t._C._cuda_getCurrentRawStream, t._C._cuda_isCurrentStreamCapturing)
     _ops = _qd_ops
     return _ops
@@ -706,7 +710,7 @@ _SCRATCH_MOST = 128 << 20
 
 
 def release_scratch():
-    """Give the scratch that qd_attn_cached and qd_attn_paged keep for the streams it was called on (one tensor each, 128 MB
+    """Give the scratch that qd_attn_cached, qd_attn_paged and qd_attn_prompt keep for the streams it was called on (one tensor each, 128 MB
     at most) back to torch's allocator; the next call on a stream takes new."""
     if _ops is not None:
         _ops.release()
@@ -826,3 +830,23 @@ def qd_attn_paged(q, pages: KvCache, page_table, lengths, out, n_new=None, max_l
     st = _with_scratch(ops, ops.paged, (q, pages.addr, page_table, lengths, out, n_new, max_length, scale), q, workspace, stream)
     if st != QD_OK:
         raise QDError(st, "qd_attn_paged failed")
+
+
+def qd_attn_prompt_workspace(n_tokens: int, n_kv_tokens: int, n_seqs: int, n_q_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    """Bytes of workspace of a qd_attn_prompt call of these sizes (0: none)."""
+    n = ctypes.c_size_t(0)
+    st = _lib.qd_attn_prompt_workspace(n_tokens, n_kv_tokens, n_seqs, n_q_heads, n_kv_heads, head_dim, ctypes.byref(n))
+    if st != QD_OK:
+        raise QDError(st, "qd_attn_prompt_workspace failed")
+    return n.value
+
+
+def qd_attn_prompt(q, k, v, out, offsets, kv_offsets=None, scale=None, workspace=None, stream=None):
+    """Causal attention over whole prompts packed one after the other: q [tokens, q_heads, head_dim], k, v [keys, kv_heads,
+    head_dim] into out (bf16, slices of a fused projection as they are).  offsets (int32 [sequences + 1]): the rows of each
+    sequence; kv_offsets: those of its keys, where they are others (a prompt's later chunk); the last query sees all keys.
+    scale: default head_dim ** -0.5; workspace (of qd_attn_prompt_workspace bytes) as in qd_attn_cached."""
+    ops = _ops or _setup_ops()
+    st = _with_scratch(ops, ops.prompt, (q, k, v, out, offsets, kv_offsets, scale), q, workspace, stream)
+    if st != QD_OK:
+        raise QDError(st, "qd_attn_prompt failed")

@@ -1,0 +1,764 @@
+// Causal attention over whole prompts of different lengths that stand packed one after the other (bf16), on the tcgen05
+// tensor cores.
+//
+//   out[i] = sum_{j < lim_i} 2^(s_ij - ref) v_j / sum_{j < lim_i} 2^(s_ij - ref),   s_ij = log2(e) scale q_i . k_j,   lim_i = past + i + 1
+//
+// The rows of a sequence and key head are its (token, query head of the group) pairs, token by token, so a group's heads share
+// every key that is read, and short prompts of grouped heads still fill tiles.  A tile has the rows of 128 / G whole tokens (the M
+// of an MMA, a few rows unused where G does not divide 128), a CTA works a pair of them against the same chunks of 128 keys, one tile's
+// products under the other's softmax:
+//   S = Q K^T          128 x 128 fp32 in tensor memory; Q and K from shared memory, by TMA
+//   softmax            thread = row; P as bf16 over S's own columns, 64 keys at a time
+//   O += P V           P from tensor memory, V from shared memory (keys x dims: the MN-major operand), 64 keys at a time
+// The reference is the largest of a row's first 64 scores and moves only when the sum of 64 weights passes 2^80 (bf16 weights
+// have fp32's range), so the scores are read once and O stays where it is.
+//
+// P is one bf16 part (a weight keeps 8 bits): a second part takes half as many products again, and its rounding, unbiased and
+// independent from key to key, is below the rounding of a bf16 result (measured against 64 bits, 2-norm: see the tests' bounds).
+// The sum is that of the weights before their rounding, in fp32.
+//
+// What a row does not see never reaches it: scores are selected, not added to a mask, and a V row that is not finite among
+// the chunks that some rows see only in part is zeroed in shared memory and added by the rows that see it (0 x infinity is
+// NaN).  Two warps look those chunks through while their scores are worked out.
+//
+// Pairs differ in length, and only the device knows the lengths.  Up to a pair per SM each CTA finds its own; beyond, attn_prompt_plan_kernel
+// sorts the pairs, longest first, and the CTAs take them from a counter.
+//
+// Roles (384 threads): warps 0-3 and 4-7 the softmax of the two tiles, warp 8 owns the tensor memory and issues the MMAs, warp 9 takes the
+// pairs and loads, warps 10 and 11 look V through.  Every wait is bounded; where one expires the pair's results become NaN and the roles
+// run to their ends.
+#include <cuda.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "attn_cached.cuh"
+#include "qd_internal.h"
+#include "tc_common.cuh"
+
+namespace qd {
+
+namespace {
+
+constexpr int kPtThreads = 384, kPtSoft = 256;
+constexpr int kPtRegsSoft = 208, kPtRegsRest = 88;
+static_assert(kPtSoft * kPtRegsSoft + (kPtThreads - kPtSoft) * kPtRegsRest <= kPtThreads * 168, "registers");
+constexpr uint32_t kPtBox = 128 * 128;        // 128 rows of 128 bytes, 128-byte swizzle
+constexpr uint32_t kPtS = 0, kPtO = 256;      // tensor memory columns: S (and P) of the tiles, O
+constexpr int kPtKeys = 128;                  // of a chunk
+constexpr int kPtStages = 2;                  // of K and of V
+constexpr int kPtSlots = 4;                   // pairs in flight between the roles
+constexpr int kPtUsers = 11;                  // warps that read a slot
+constexpr int kPtBuckets = 1024;              // of the plan's sort
+constexpr float kPtTop = 1.2e24f;             // 2^80
+
+struct PromptArgs {
+    const uint8_t *v;
+    uint8_t *out;
+    int64_t v_token, o_token;                 // bytes
+    const int32_t *offsets, *kv_offsets;      // kv_offsets: may be offsets
+    int N, M, B, G, kvh;                      // tokens, keys
+    int tpt;                                  // tokens of a tile
+    float scale2;                             // softmax scale times log2(e)
+    // the plan: pairs (sequence, pair) longest first, room for `cap`; [0] their number, [1] the next to be taken.  null: a pair per CTA
+    int2 *list;
+    int *count;
+    int cap, cost_shift;
+};
+
+// A pair of tiles, as the roles see it.
+struct Pair {
+    int hk, q0, tokens;                       // key head; first token row, tokens (of both tiles)
+    int k0, lim0;                             // first key row; keys that the first token sees
+    int n[2];                                 // chunks of either tile; hk < 0: no more pairs
+    uint32_t odd;                             // chunks, counted from first_edge(), in which V was not finite
+};
+// The first chunk that the pair's first token does not see all of.
+__device__ __forceinline__ int first_edge(const Pair &p) { return p.lim0 > 0 ? p.lim0 / kPtKeys : 0; }
+
+struct Sequence {
+    int q0, n, k0, m;
+};
+__device__ __forceinline__ Sequence sequence(const PromptArgs &a, int b) {
+    Sequence s;
+    s.q0 = min(max(a.offsets[b], 0), a.N);
+    s.n = min(max(a.offsets[b + 1], s.q0), a.N) - s.q0;
+    s.k0 = min(max(a.kv_offsets[b], 0), a.M);
+    s.m = min(max(a.kv_offsets[b + 1], s.k0), a.M) - s.k0;
+    return s;
+}
+__device__ __forceinline__ int chunks(int keys) { return keys > 0 ? (keys + kPtKeys - 1) / kPtKeys : 0; }
+
+__device__ __forceinline__ Pair pair_of(const PromptArgs &a, int b, int pair, int hk) {
+    const Sequence s = sequence(a, b);
+    const int t0 = pair * 2 * a.tpt;
+    Pair p;
+    p.hk = hk;
+    p.q0 = s.q0 + t0, p.tokens = min(s.n - t0, 2 * a.tpt);
+    p.k0 = s.k0, p.lim0 = s.m - s.n + t0 + 1;
+    const int first = min(p.tokens, a.tpt);
+    p.n[0] = chunks(p.lim0 + first - 1);
+    p.n[1] = p.tokens > first ? chunks(p.lim0 + p.tokens - 1) : 0;
+    p.odd = 0;
+    return p;
+}
+__device__ __forceinline__ int pairs_of(const PromptArgs &a, const Sequence &s) { return (s.n + 2 * a.tpt - 1) / (2 * a.tpt); }
+
+// ---- the plan: one CTA, a counting sort of the pairs by their chunks, longest first
+__global__ void __launch_bounds__(1024) attn_prompt_plan_kernel(const PromptArgs a) {
+    __shared__ int hist[kPtBuckets], sums[32];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    hist[tid] = 0;
+    pdl_wait();
+    pdl_launch_dependents();
+    __syncthreads();
+    // as many threads a sequence as there are, a warp at least
+    int per = 1024;
+    while (per > 32 && a.B * per > 1024) per >>= 1;
+    auto walk = [&](auto &&take) {
+        for (int b = tid / per; b < a.B; b += 1024 / per) {
+            const Sequence s = sequence(a, b);
+            const int pairs = pairs_of(a, s);
+            for (int i = tid % per; i < pairs; i += per) {
+                const int last = min(s.n, (i + 1) * 2 * a.tpt);            // tokens up to the pair's end
+                take(b, i, min(chunks(s.m - s.n + last) >> a.cost_shift, kPtBuckets - 1));
+            }
+        }
+    };
+    walk([&](int, int, int cost) { atomicAdd(&hist[kPtBuckets - 1 - cost], 1); });
+    __syncthreads();
+    // where each bucket begins
+    const int mine = hist[tid];
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    if (lane == 31) sums[warp] = upto;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < 32; ++w) {
+        if (w < warp) before += sums[w];
+        all += sums[w];
+    }
+    hist[tid] = before + upto - mine;
+    __syncthreads();
+    walk([&](int b, int i, int cost) {
+        const int at = atomicAdd(&hist[kPtBuckets - 1 - cost], 1);
+        if (at < a.cap) a.list[at] = make_int2(b, i);                      // (offsets that do not ascend could name more)
+    });
+    if (tid == 0) a.count[0] = min(all, a.cap), a.count[1] = 0;
+}
+
+template <int D> struct PtCfg {
+    static constexpr int KB = D / 64;                         // 64-wide blocks of head_dim
+    static constexpr uint32_t kTile = KB * kPtBox;            // of Q, K or V
+    static constexpr uint32_t kQ = 0;                         // Q [tile]
+    static constexpr uint32_t kK = kQ + 2 * kTile;            // K [stage]
+    static constexpr uint32_t kV = kK + kPtStages * kTile;    // V [stage]
+    static constexpr uint32_t kSlot = kV + kPtStages * kTile;
+    static constexpr uint32_t kBar = kSlot + kPtSlots * sizeof(Pair);
+    static constexpr uint32_t kBars = 48;
+    static constexpr uint32_t kSmem = 1024 + kBar + kBars * 8;
+};
+static_assert(sizeof(Pair) % 8 == 0, "barriers follow");
+
+// 32 scores of a row as weights against its reference, packed; their sum joins l2.  EDGE: the first `left` are seen.
+template <bool EDGE>
+__device__ __forceinline__ void weigh(const uint32_t *x, uint64_t cs2, uint64_t rf2, int left, uint32_t *y, uint64_t &l2) {
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+        const uint64_t x0 = pk(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), x1 = pk(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+        float s0, s1, s2, s3;
+        unpk(fma2(x0, cs2, rf2), s0, s1);
+        unpk(fma2(x1, cs2, rf2), s2, s3);
+        s0 = ex2(s0), s1 = ex2(s1), s2 = ex2(s2), s3 = ex2(s3);
+        if constexpr (EDGE) {
+            s0 = e < left ? s0 : 0.f, s1 = e + 1 < left ? s1 : 0.f;
+            s2 = e + 2 < left ? s2 : 0.f, s3 = e + 3 < left ? s3 : 0.f;
+        }
+        l2 = add2(l2, add2(pk(s0, s1), pk(s2, s3)));
+        y[e / 2] = pack_bf16(s0, s1), y[e / 2 + 1] = pack_bf16(s2, s3);
+    }
+}
+// The largest of the first `left` of 32 scores, in log2 units.
+__device__ __forceinline__ float largest(const uint32_t *x, float cs, int left) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < 32; ++e) m = fmaxf(m, e < left ? __uint_as_float(x[e]) * cs : -INFINITY);
+    return m;
+}
+__device__ __forceinline__ bool not_finite(uint32_t w) { return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u; }
+
+template <int D>
+__global__ void __launch_bounds__(kPtThreads, 1)
+    attn_prompt_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                       const __grid_constant__ CUtensorMap mv, const PromptArgs a) {
+    using C = PtCfg<D>;
+    constexpr int KB = C::KB;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    Pair *slots = reinterpret_cast<Pair *>(sm + C::kSlot);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + C::kBar);
+    uint64_t *slot_full = bars, *slot_empty = bars + 4;                                              // [slot]
+    uint64_t *q_full = bars + 8, *q_empty = bars + 10, *s_full = bars + 12, *o_half = bars + 14;     // [tile]
+    uint64_t *o_full = bars + 16, *o_empty = bars + 18, *p_full = bars + 20;                         // [tile], [tile], [tile][half]
+    uint64_t *k_full = bars + 24, *k_empty = bars + 26, *v_full = bars + 28, *v_empty = bars + 30, *v_clean = bars + 32;   // [stage]
+    uint64_t *drain = bars + 34;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 35);
+    volatile int *bad = reinterpret_cast<volatile int *>(bars + 36);
+
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kPtSlots; ++i) mbar_init(&slot_full[i], 1), mbar_init(&slot_empty[i], kPtUsers);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], 1), mbar_init(&s_full[i], 1), mbar_init(&o_half[i], 1);
+            mbar_init(&o_full[i], 1), mbar_init(&o_empty[i], 4);
+            mbar_init(&p_full[2 * i], 4), mbar_init(&p_full[2 * i + 1], 4);
+        }
+        for (int i = 0; i < kPtStages; ++i) {
+            mbar_init(&k_full[i], 1), mbar_init(&k_empty[i], 1);
+            mbar_init(&v_full[i], 1), mbar_init(&v_empty[i], 1), mbar_init(&v_clean[i], 2);
+        }
+        mbar_init(drain, 1);
+        *bad = 0;
+        fence_barrier_init();
+    }
+    // the predecessor first, the tensor memory then: held while waiting it could be what a predecessor's CTA on this SM waits for
+    pdl_wait();
+    if (warp == 8) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    auto slot_of = [&](int i) -> Pair & { return slots[i % kPtSlots]; };
+    // the i-th pair of this CTA, or none (hk < 0)
+    auto pair_at = [&](int i) {
+        Pair p;
+        p.hk = -1;
+        // (a wait may expire for some lanes alone: all of a warp leave together, here and below)
+        if (__all_sync(0xffffffffu, wt_wait(&slot_full[i % kPtSlots], (uint32_t)(i / kPtSlots) & 1u, bad))) p = slot_of(i);
+        return p;
+    };
+    auto done_with = [&](int i) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&slot_empty[i % kPtSlots]);
+    };
+
+    if (warp == 9) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPtRegsRest));
+        // ---- the pairs, and their loads (the whole warp walks along; one lane issues)
+        int kc = 0, nq[2] = {0, 0}, total = 1, next = 0;
+        bool ok = true;
+        if (a.list) {
+            total = a.count[0] * a.kvh;
+            if (lane == 0) next = atomicAdd(&a.count[1], 1);
+            next = __shfl_sync(0xffffffffu, next, 0);
+        }
+        for (int it = 0; ok; ++it) {
+            Pair p;
+            p.hk = -1;
+            if (a.list) {
+                if (next < total) {
+                    const int2 e = a.list[next / a.kvh];
+                    p = pair_of(a, e.x, e.y, next % a.kvh);
+                }
+            } else if (it == 0) {
+                // pair blockIdx.x / kvh of all sequences' pairs: 32 sequences a step, the running sum across the lanes
+                const int want = (int)blockIdx.x / a.kvh;
+                int sum = 0;
+                for (int b0 = 0; b0 < a.B; b0 += 32) {
+                    int n = 0;
+                    if (b0 + lane < a.B) n = pairs_of(a, sequence(a, b0 + lane));
+                    int upto = n;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+                        if (lane >= o) upto += v;
+                    }
+                    const uint32_t over = __ballot_sync(0xffffffffu, sum + upto > want);
+                    if (over) {
+                        const int at = __ffs(over) - 1;
+                        p = pair_of(a, b0 + at, want - sum - __shfl_sync(0xffffffffu, upto - n, at), (int)blockIdx.x % a.kvh);
+                        break;
+                    }
+                    sum += __shfl_sync(0xffffffffu, upto, 31);
+                }
+            }
+            if (it >= kPtSlots) ok = wt_wait(&slot_empty[it % kPtSlots], (uint32_t)(it / kPtSlots + 1) & 1u, bad);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (lane == 0) {
+                slot_of(it) = p;
+                mbar_arrive(&slot_full[it % kPtSlots]);
+            }
+            __syncwarp();
+            if (p.hk < 0) break;
+            if (a.list && lane == 0) next = atomicAdd(&a.count[1], 1);     // in flight under this pair's loads
+            const int n = max(p.n[0], p.n[1]);
+            for (int c = 0; ok && c < n; ++c, ++kc) {
+                const int st = kc % kPtStages;
+                const uint32_t was = (uint32_t)(kc / kPtStages + 1) & 1u;
+                const int key = p.k0 + c * kPtKeys;
+                auto load = [&](const CUtensorMap *m, uint32_t at, uint64_t *full, uint32_t bytes, int head, int row) {
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(full, bytes);
+#pragma unroll
+                        for (int b = 0; b < KB; ++b) tma_load_3d_plain(sm + at + b * kPtBox, m, 64 * b, head, row, full);
+                    }
+                    __syncwarp();
+                };
+                auto load_q = [&](int h) {
+                    if (p.n[h] == 0) return;
+                    if (nq[h] > 0) ok = ok && wt_wait(&q_empty[h], (uint32_t)(nq[h] + 1) & 1u, bad);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) return;
+                    load(&mq, C::kQ + h * C::kTile, &q_full[h], (uint32_t)(KB * a.tpt * a.G * 128), p.hk * a.G, p.q0 + h * a.tpt);
+                    ++nq[h];
+                };
+                if (c == 0) load_q(p.n[0] ? 0 : 1);
+                if (kc >= kPtStages) ok = ok && wt_wait(&k_empty[st], was, bad);
+                ok = __all_sync(0xffffffffu, ok);
+                if (ok) load(&mk, C::kK + st * C::kTile, &k_full[st], C::kTile, p.hk, key);
+                if (c == 0 && p.n[0]) load_q(1);
+                if (kc >= kPtStages) ok = ok && wt_wait(&v_empty[st], was, bad);
+                ok = __all_sync(0xffffffffu, ok);
+                if (ok) load(&mv, C::kV + st * C::kTile, &v_full[st], C::kTile, p.hk, key);
+            }
+            next = __shfl_sync(0xffffffffu, next, 0);
+        }
+        // copies in flight land before the CTA may end (they have, unless a wait expired)
+        if (!ok) {
+            for (int h = 0; h < 2; ++h)
+                if (nq[h] > 0) (void)mbar_wait_bounded(&q_full[h], (uint32_t)(nq[h] + 1) & 1u, 20000000ull);
+            for (int i = 0; i < kPtStages; ++i) {
+                const int uses = kc / kPtStages + 1;
+                (void)mbar_wait_bounded(&k_full[i], (uint32_t)(uses + 1) & 1u, 20000000ull);
+                (void)mbar_wait_bounded(&v_full[i], (uint32_t)(uses + 1) & 1u, 20000000ull);
+            }
+        }
+    } else if (warp == 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPtRegsRest));
+        // ---- the MMAs: always a tile's O followed by its next S, which may be the next pair's first
+        constexpr uint32_t base = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(128 >> 4) << 24);
+        constexpr uint32_t idesc_s = base | ((uint32_t)(kPtKeys >> 3) << 17);
+        constexpr uint32_t idesc_o = base | (1u << 16) | ((uint32_t)(D >> 3) << 17);
+        const uint64_t dQ = sw128_desc(smem_addr(sm + C::kQ)), dK = sw128_desc(smem_addr(sm + C::kK));
+        const uint64_t dV = sw128_desc_mn(smem_addr(sm + C::kV), kPtBox, 1024u);
+        constexpr uint32_t kBox16 = kPtBox / 16;
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        int kc = 0;                                 // chunks before this pair's
+        uint32_t nq[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0};   // of either tile: pairs, P's, pairs begun in O
+        bool ok = true, begun[2] = {false, false};  // the pair's first S is issued
+        Pair p = pair_at(0);
+        // S of tile h, chunk c of pair x whose first chunk is the kx-th
+        auto issue_s = [&](int h, int c, const Pair &x, int kx) {
+            const int st = (kx + c) % kPtStages;
+            if (c == 0) ok = ok && wt_wait(&q_full[h], nq[h]++ & 1u, bad);
+            ok = ok && wt_wait(&k_full[st], (uint32_t)((kx + c) / kPtStages) & 1u, bad);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) return;
+            tc_fence_after();
+            const uint32_t d = tm + kPtS + 128u * h;
+            const uint64_t q = dQ + h * KB * kBox16, k = dK + st * KB * kBox16;
+            const bool last_k = h == 1 || x.n[1] <= c;      // nobody needs this K after it
+            if (elect_one()) {
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        tc_mma(d, q + kb * kBox16 + 2 * s, k + kb * kBox16 + 2 * s, idesc_s, (kb | s) ? 1u : 0u);
+                tc_commit(&s_full[h]);
+                if (last_k) tc_commit(&k_empty[st]);
+                if (c + 1 == x.n[h]) tc_commit(&q_empty[h]);
+            }
+            __syncwarp();
+        };
+        auto issue_o = [&](int h, int c) {
+            const int st = (kc + c) % kPtStages;
+            const uint32_t ph = (uint32_t)((kc + c) / kPtStages) & 1u;
+            if (c == 0) {
+                if (no[h] > 0) ok = ok && wt_wait(&o_empty[h], (no[h] + 1) & 1u, bad);
+                ++no[h];
+            }
+            const uint32_t d = tm + kPtO + 128u * h, pt = tm + kPtS + 128u * h;
+            const uint64_t v = dV + st * KB * kBox16;
+            ok = ok && wt_wait(&v_full[st], ph, bad) && wt_wait(&v_clean[st], ph, bad);
+            for (int half = 0; half < 2; ++half) {
+                ok = ok && wt_wait(&p_full[2 * h + half], np[h] & 1u, bad);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) return;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        tc_mma_ts(d, pt + 32u * half + 8u * i, v + (4 * half + i) * 128, idesc_o, (c | half | i) ? 1u : 0u);
+                    if (half == 0) {
+                        tc_commit(&o_half[h]);
+                    } else {
+                        if (h == 1 || p.n[1] <= c) tc_commit(&v_empty[st]);
+                        if (c + 1 == p.n[h]) tc_commit(&o_full[h]);
+                    }
+                }
+                __syncwarp();
+            }
+            ++np[h];
+        };
+        for (int it = 0; ok && p.hk >= 0; ++it) {
+            const int n = max(p.n[0], p.n[1]);
+            for (int h = 0; h < 2; ++h)
+                if (ok && !begun[h] && p.n[h] > 0) issue_s(h, 0, p, kc);
+            begun[0] = begun[1] = false;
+            Pair x;
+            x.hk = -2;                              // the next pair: not known yet
+            for (int c = 0; ok && c < n; ++c)
+                for (int h = 0; h < 2; ++h) {
+                    if (!ok || c >= p.n[h]) continue;
+                    issue_o(h, c);
+                    if (!ok) break;
+                    if (c + 1 < p.n[h]) {
+                        issue_s(h, c + 1, p, kc);
+                    } else {
+                        if (x.hk == -2) x = pair_at(it + 1);
+                        if (x.hk >= 0 && x.n[h] > 0) {
+                            issue_s(h, 0, x, kc + n);
+                            begun[h] = true;
+                        }
+                    }
+                }
+            if (x.hk == -2) x = pair_at(it + 1);
+            done_with(it);
+            kc += n;
+            p = x;
+        }
+        // every MMA issued has completed before the tensor memory can be freed
+        if (elect_one()) tc_commit(drain);
+        (void)mbar_wait_bounded(drain, 0u, 20000000ull);
+        __syncwarp();
+    } else if (warp >= 10) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPtRegsRest));
+        // ---- V of chunks that some rows see in part: what is not finite becomes zero, and is noted
+        int kc = 0;
+        bool ok = true;
+        for (int it = 0; ok; ++it) {
+            Pair p = pair_at(it);
+            if (p.hk < 0) break;
+            const int n = max(p.n[0], p.n[1]), edge = first_edge(p);
+            for (int c = 0; ok && c < n; ++c, ++kc) {
+                const int st = kc % kPtStages;
+                ok = wt_wait(&v_full[st], (uint32_t)(kc / kPtStages) & 1u, bad);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (c >= edge) {
+                    uint4 *tile = reinterpret_cast<uint4 *>(sm + C::kV + st * C::kTile);
+                    constexpr int kPieces = KB * 128 * 8;
+                    bool odd = false;
+#pragma unroll 4
+                    for (int i = (warp - 10) * 32 + lane; i < kPieces; i += 64) {
+                        uint4 u = tile[i];
+                        if (not_finite(u.x) || not_finite(u.y) || not_finite(u.z) || not_finite(u.w)) {
+                            odd = true;
+                            auto keep = [](uint32_t w) {
+                                if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+                                if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
+                                return w;
+                            };
+                            tile[i] = make_uint4(keep(u.x), keep(u.y), keep(u.z), keep(u.w));
+                        }
+                    }
+                    if (odd) {
+                        fence_proxy_async_smem();
+                        atomicOr(&slot_of(it).odd, 1u << (c - edge));
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&v_clean[st]);
+            }
+            done_with(it);
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPtRegsSoft));
+        // ---- softmax: tile h, row r of it
+        const int h = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        const uint32_t tS = tmem + kPtS + 128u * h + lanes, tO = tmem + kPtO + 128u * h + lanes;
+        const int token = r / a.G, head = r - token * a.G;
+        const bool in_tile = token < a.tpt;
+        uint32_t ns = 0, no = 0;                    // S's, O's so far
+        bool ok = true;
+        for (int it = 0; ok; ++it) {
+            const Pair p = pair_at(it);
+            if (p.hk < 0) break;
+            const int tt = h * a.tpt + token, n = p.n[h];
+            const bool live = in_tile && tt < p.tokens;
+            // rows without a token see what the tile's last one does
+            const int lim = p.lim0 + (live ? tt : min(p.tokens, (h + 1) * a.tpt) - 1);
+            const int lim_all = __reduce_min_sync(0xffffffffu, lim);        // keys that every row of the warp sees
+            float ref = -INFINITY, l = 0.f;
+            for (int c = 0; c < n; ++c) {
+                ok = ok && wt_wait(&s_full[h], ns & 1u, bad);
+                ++ns;
+                tc_fence_after();
+                const int left = lim - c * kPtKeys;
+                const bool edge = lim_all < (c + 1) * kPtKeys;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int here = left - 64 * q;
+                    uint32_t x[64], y[32];
+                    ld32_start(tS + 64u * q, x);
+                    ld32_start(tS + 64u * q + 32u, x + 32);
+                    tc_wait_ld_u32<64>(x);
+                    const bool first = q == 0 && c == 0;
+                    if (first) ref = fmaxf(largest(x, a.scale2, here), largest(x + 32, a.scale2, here - 32));
+                    float sum;
+                    auto weigh_all = [&](const uint32_t *z) {
+                        const float rf = ref == -INFINITY ? 0.f : -ref;
+                        const uint64_t cs2 = pk(a.scale2, a.scale2), rf2 = pk(rf, rf);
+                        uint64_t l2 = pk(0.f, 0.f);
+                        if (edge) {
+                            weigh<true>(z, cs2, rf2, here, y, l2);
+                            weigh<true>(z + 32, cs2, rf2, here - 32, y + 16, l2);
+                        } else {
+                            weigh<false>(z, cs2, rf2, here, y, l2);
+                            weigh<false>(z + 32, cs2, rf2, here - 32, y + 16, l2);
+                        }
+                        float l0, l1;
+                        unpk(l2, l0, l1);
+                        sum = l0 + l1;
+                    };
+                    weigh_all(x);
+                    if (!first && __any_sync(0xffffffffu, live && (sum > kPtTop || (ref == -INFINITY && here > 0)))) {
+                        uint32_t z[64];             // the scores again: they stand until their weights are written
+                        ld32_start(tS + 64u * q, z);
+                        ld32_start(tS + 64u * q + 32u, z + 32);
+                        tc_wait_ld_u32<64>(z);
+                        const float m = fmaxf(largest(z, a.scale2, here), largest(z + 32, a.scale2, here - 32));
+                        float f = 1.f;
+                        if (m > ref) {
+                            f = ref == -INFINITY ? 0.f : ex2(ref - m);
+                            ref = m;
+                            l *= f;
+                        }
+                        // O holds the chunks before, whose products this S came behind, and this chunk's first half
+                        if (q == 1) {
+                            ok = ok && wt_wait(&o_half[h], (ns - 1) & 1u, bad);
+                            tc_fence_after();
+                        }
+                        if (c > 0 || q > 0) {
+#pragma unroll 1
+                            for (int i = 0; i < D / 32; ++i) {
+                                uint32_t u[32];
+                                ld32_start(tO + 32u * i, u);
+                                tc_wait_ld_u32<32>(u);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * f);
+                                tc_st16(tO + 32u * i, u);
+                                tc_st16(tO + 32u * i + 16u, u + 16);
+                            }
+                        }
+                        weigh_all(z);
+                    }
+                    l += sum;
+                    tc_st16(tS + 32u * q, y);
+                    tc_st16(tS + 32u * q + 16u, y + 16);
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_full[2 * h + q]);
+                }
+            }
+            // ---- the rows' results
+            if (n > 0) {
+                ok = ok && wt_wait(&o_full[h], no & 1u, bad);
+                ++no;
+                tc_fence_after();
+            }
+            ok = __all_sync(0xffffffffu, ok && !*bad);
+            const float fail = ok ? 0.f : __uint_as_float(0x7fc00000u);
+            // no key gives zeros; keys whose scores are all -infinity NaN, as the formula does
+            const float by = (lim <= 0 ? 0.f : l == 0.f ? __uint_as_float(0x7fc00000u) : 1.f / l) + fail;
+            const uint32_t odd = n > 0 ? *reinterpret_cast<volatile uint32_t *>(&slot_of(it).odd) : 0u;
+            uint8_t *dst = a.out + (int64_t)(p.q0 + tt) * a.o_token + (int64_t)(p.hk * a.G + head) * (2 * D);
+#pragma unroll 1
+            for (int i = 0; i < D / 32; ++i) {
+                uint32_t u[32];
+                if (n > 0) {
+                    ld32_start(tO + 32u * i, u);
+                    tc_wait_ld_u32<32>(u);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) u[e] = 0;
+                }
+                if (odd) {
+                    // the values that were taken out, by the rows that see them
+                    for (int k = 0; k < 32; ++k) {
+                        if (!((odd >> k) & 1u)) continue;
+                        const int j0 = (first_edge(p) + k) * kPtKeys, j1 = min(lim, j0 + kPtKeys);
+                        for (int j = j0; live && j < j1; ++j) {
+                            const uint16_t *v = reinterpret_cast<const uint16_t *>(a.v + (int64_t)(p.k0 + j) * a.v_token) + p.hk * D + 32 * i;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const uint32_t w = (uint32_t)v[e] << 16;
+                                if ((w & 0x7f800000u) == 0x7f800000u) u[e] = __float_as_uint(__uint_as_float(u[e]) + __uint_as_float(w));
+                            }
+                        }
+                    }
+                }
+                if (live) {
+                    uint32_t o[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = pack_bf16(__uint_as_float(u[2 * e]) * by, __uint_as_float(u[2 * e + 1]) * by);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        *reinterpret_cast<uint4 *>(dst + 64 * i + 16 * e) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                }
+            }
+            if (n > 0) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&o_empty[h]);
+            }
+            done_with(it);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+template <typename F, typename... A>
+cudaError_t launch_after(F fn, unsigned ctas, int threads, size_t smem, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+
+template <int D> cudaError_t launch(const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v, const PromptArgs &a, unsigned ctas, int dev,
+                                    cudaStream_t s) {
+    static std::atomic<bool> ready[64] = {};
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    auto fn = attn_prompt_kernel<D>;
+    if (!ready[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)PtCfg<D>::kSmem);
+        if (e != cudaSuccess) return e;
+        ready[dev] = true;
+    }
+    if (a.list) {
+        const cudaError_t e = launch_after(attn_prompt_plan_kernel, 1, 1024, 0, s, a);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_after(fn, ctas, kPtThreads, PtCfg<D>::kSmem, s, q, k, v, a);
+}
+
+// How a call runs: the most pairs that the sequences can have, and the CTAs.
+struct PromptPlan {
+    int tpt, cap;
+    bool list;
+    unsigned ctas;
+    size_t bytes;
+};
+qd_status plan_prompt(int n_tokens, int n_kv_tokens, int n_seqs, int n_q_heads, int n_kv_heads, int head_dim, int dev, PromptPlan *p) {
+    if (n_tokens < 1 || n_kv_tokens < 1 || n_seqs < 1 || n_kv_heads < 1 || n_q_heads < n_kv_heads || n_q_heads % n_kv_heads) return QD_EINVAL;
+    if (head_dim != 64 && head_dim != 128) return QD_EUNSUPPORTED;
+    const int G = n_q_heads / n_kv_heads;
+    if (G > 128 || n_q_heads > 65536 || n_tokens > (1 << 30) || n_kv_tokens > (1 << 30) || n_seqs > (1 << 24)) return QD_EUNSUPPORTED;
+    p->tpt = 128 / G;
+    const int64_t pairs = (int64_t)n_tokens / (2 * p->tpt) + std::min(n_seqs, n_tokens);
+    if (pairs * n_kv_heads > (1 << 30)) return QD_EUNSUPPORTED;
+    const int sms = sms_of(dev);
+    p->cap = (int)pairs;
+    p->list = pairs * n_kv_heads > sms;
+    p->ctas = (unsigned)std::min<int64_t>(pairs * n_kv_heads, sms);
+    p->bytes = p->list ? 256 + (size_t)pairs * sizeof(int2) : 0;
+    return QD_OK;
+}
+
+}  // namespace
+
+}  // namespace qd
+
+using namespace qd;
+
+extern "C" {
+
+qd_status qd_attn_prompt_workspace(int n_tokens, int n_kv_tokens, int n_seqs, int n_q_heads, int n_kv_heads, int head_dim, size_t *bytes) {
+    if (!bytes) return QD_EINVAL;
+    *bytes = 0;
+    int dev = 0;
+    PromptPlan p;
+    qd_status st = plan_prompt(n_tokens, n_kv_tokens, n_seqs, n_q_heads, n_kv_heads, head_dim, -1, &p);
+    if (st != QD_OK) return st;
+    if (cudaGetDevice(&dev) != cudaSuccess) return QD_ECUDA;
+    st = plan_prompt(n_tokens, n_kv_tokens, n_seqs, n_q_heads, n_kv_heads, head_dim, dev, &p);
+    *bytes = p.bytes;
+    return st;
+}
+
+qd_status qd_attn_prompt(const void *q_dev, int64_t q_stride, const void *k_dev, int64_t k_stride, const void *v_dev, int64_t v_stride,
+                         void *out_dev, int64_t out_stride, int n_tokens, int n_kv_tokens, int n_q_heads, int n_kv_heads, int head_dim,
+                         float scale, const int32_t *offsets_dev, const int32_t *kv_offsets_dev, int n_seqs, void *workspace_dev,
+                         size_t workspace_bytes, void *cuda_stream) {
+    PromptPlan p;
+    qd_status st = plan_prompt(n_tokens, n_kv_tokens, n_seqs, n_q_heads, n_kv_heads, head_dim, -1, &p);
+    if (st != QD_OK) return st;
+    if (!q_dev || !k_dev || !v_dev || !out_dev || !offsets_dev || !(scale > -3e38f && scale < 3e38f)) return QD_EINVAL;
+    if (!kv_offsets_dev && n_tokens != n_kv_tokens) return QD_EINVAL;
+    for (const void *x : {q_dev, k_dev, v_dev, (const void *)out_dev})
+        if (!is_aligned(x, 16)) return QD_EINVAL;
+    if (!is_aligned(offsets_dev, 4) || !is_aligned(kv_offsets_dev, 4)) return QD_EINVAL;
+    const int64_t q_row = (int64_t)n_q_heads * head_dim, k_row = (int64_t)n_kv_heads * head_dim;
+    for (int64_t x : {q_stride, k_stride, v_stride, out_stride})
+        if (x % 8 || x > (int64_t(1) << 37)) return QD_EINVAL;       // (a tensor map's strides end at 2^40 bytes)
+    if ((n_tokens > 1 && (q_stride < q_row || out_stride < q_row)) || (n_kv_tokens > 1 && (k_stride < k_row || v_stride < k_row))) return QD_EINVAL;
+    // out lies over none of the inputs, but may stand between their rows
+    if (!rows_beside(out_dev, 2, n_tokens, out_stride, q_row, q_dev, 2, n_tokens, q_stride, q_row) ||
+        !rows_beside(out_dev, 2, n_tokens, out_stride, q_row, k_dev, 2, n_kv_tokens, k_stride, k_row) ||
+        !rows_beside(out_dev, 2, n_tokens, out_stride, q_row, v_dev, 2, n_kv_tokens, v_stride, k_row))
+        return QD_EINVAL;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return QD_ECUDA;
+    for (const void *x : {q_dev, k_dev, v_dev, (const void *)out_dev, (const void *)offsets_dev})
+        if (!on_device(x, dev)) return QD_EINVAL;
+    if (kv_offsets_dev && !on_device(kv_offsets_dev, dev)) return QD_EINVAL;
+    if ((st = plan_prompt(n_tokens, n_kv_tokens, n_seqs, n_q_heads, n_kv_heads, head_dim, dev, &p)) != QD_OK) return st;
+    if (p.bytes && (!workspace_dev || workspace_bytes < p.bytes || !is_aligned(workspace_dev, 256) || !on_device(workspace_dev, dev)))
+        return QD_EINVAL;
+
+    PromptArgs a = {};
+    a.v = static_cast<const uint8_t *>(v_dev), a.out = static_cast<uint8_t *>(out_dev);
+    a.v_token = v_stride * 2, a.o_token = out_stride * 2;
+    a.offsets = offsets_dev, a.kv_offsets = kv_offsets_dev ? kv_offsets_dev : offsets_dev;
+    a.N = n_tokens, a.M = n_kv_tokens, a.B = n_seqs, a.G = n_q_heads / n_kv_heads, a.kvh = n_kv_heads;
+    a.tpt = p.tpt, a.scale2 = scale * 1.4426950408889634f;
+    if (p.list) {
+        a.count = static_cast<int *>(workspace_dev);
+        a.list = reinterpret_cast<int2 *>(static_cast<uint8_t *>(workspace_dev) + 256);
+        a.cap = p.cap;
+        while ((n_kv_tokens / kPtKeys + 1) >> a.cost_shift >= kPtBuckets) ++a.cost_shift;
+    }
+    CUtensorMap mq, mk, mv;
+    if (!make_heads_map(&mq, q_dev, head_dim, n_q_heads, n_tokens, n_tokens > 1 ? q_stride : q_row, a.G, a.tpt) ||
+        !make_heads_map(&mk, k_dev, head_dim, n_kv_heads, n_kv_tokens, n_kv_tokens > 1 ? k_stride : k_row, 1, kPtKeys) ||
+        !make_heads_map(&mv, v_dev, head_dim, n_kv_heads, n_kv_tokens, n_kv_tokens > 1 ? v_stride : k_row, 1, kPtKeys))
+        return QD_ECUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+    const cudaError_t e = head_dim == 128 ? launch<128>(mq, mk, mv, a, p.ctas, dev, s) : launch<64>(mq, mk, mv, a, p.ctas, dev, s);
+    return e == cudaSuccess ? QD_OK : QD_ECUDA;
+}
+
+}  // extern "C"

@@ -21,6 +21,9 @@ typedef qd_status (*verify_fn)(const float *, int64_t, int64_t, const float *, i
 typedef qd_status (*paged_fn)(const qd_kv_cache *, const int32_t *, int64_t, int, int, const void *, int64_t, int64_t, void *, int64_t,
                               int64_t, int, int, int, float, const int32_t *, const int32_t *, int, void *, size_t, void *);
 typedef qd_status (*paged_space_fn)(const qd_kv_cache *, int, int, int, int, int, int, size_t *);
+typedef qd_status (*prompt_fn)(const void *, int64_t, const void *, int64_t, const void *, int64_t, void *, int64_t, int, int, int, int, int,
+                               float, const int32_t *, const int32_t *, int, void *, size_t, void *);
+typedef qd_status (*prompt_space_fn)(int, int, int, int, int, int, size_t *);
 typedef qd_status (*rope_fn)(const qd_rope_rows *, void *);
 
 static rows_fn f_append, f_read;
@@ -30,6 +33,8 @@ static verify_fn f_verify;
 static rope_fn f_rope;
 static paged_fn f_paged;
 static paged_space_fn f_paged_space;
+static prompt_fn f_prompt;
+static prompt_space_fn f_prompt_space;
 static PyObject *t_f32, *t_bf16, *t_i32;               /* torch's types */
 static PyObject *raw_stream, *capturing;               /* its current raw stream of a device; whether that is being captured */
 static PyObject *s_shape, *s_stride, *s_dtype, *s_ptr, *s_device, *s_stream;
@@ -471,6 +476,63 @@ static PyObject *py_rope(PyObject *self, PyObject *const *a, Py_ssize_t nargs) {
     return PyLong_FromLong(f_rope(&r, s));
 }
 
+/* prompt(q, k, v, out, offsets, kv_offsets, scale, workspace, workspace_bytes, stream): as attn */
+static PyObject *py_prompt(PyObject *self, PyObject *const *a, Py_ssize_t nargs) {
+    NARGS(10)
+    Tensor q, k, v, o;
+    const int32_t *offsets, *kv_offsets;
+    void *s, *ws = NULL;
+    long dev;
+    size_t have = 0;
+    float scale;
+    for (int i = 0; i < 5; ++i)
+        if (a[i] == Py_None) {
+            bad("q, k, v, out and offsets are wanted");
+            return NULL;
+        }
+    if (!read_heads(a[0], "q", -1, -1, -1, &q)) return NULL;
+    const int64_t N = q.shape[0], QH = q.shape[1], D = q.shape[2];
+    if (!read_heads(a[1], "k", -1, -1, D, &k)) return NULL;
+    const int64_t M = k.shape[0], H = k.shape[1];
+    if (!read_heads(a[2], "v", M, H, D, &v) || !read_heads(a[3], "out", N, QH, D, &o)) return NULL;
+    if (q.type != t_bf16 || k.type != t_bf16 || v.type != t_bf16 || o.type != t_bf16) {
+        bad("q, k, v and out must be bf16");
+        return NULL;
+    }
+    const int64_t B = length_of(a[4]) - 1;
+    if (B < 0) {
+        if (!PyErr_Occurred()) bad("offsets must be [sequences + 1]");
+        return NULL;
+    }
+    if (!read_ints(a[4], B + 1, &offsets, "offsets") || !read_ints(a[5], B + 1, &kv_offsets, "kv_offsets") || !read_scale(a[6], D, &scale) ||
+        !stream_of(a[9], a[0], &s, &dev))
+        return NULL;
+    if (!kv_offsets && M != N) {
+        bad("k has other rows than q: kv_offsets are wanted");
+        return NULL;
+    }
+    if (B > INT32_MAX) {
+        bad("too many sequences");
+        return NULL;
+    }
+    if (N == 0 || B == 0) return PyLong_FromLong(QD_OK);
+    if (a[7] != Py_None) {
+        ws = PyLong_AsVoidPtr(a[7]);
+        have = PyLong_AsSize_t(a[8]);
+        if (PyErr_Occurred()) return NULL;
+    } else {
+        size_t need = 0;
+        const qd_status st = f_prompt_space((int)N, (int)M, (int)B, (int)QH, (int)H, (int)D, &need);
+        if (st != QD_OK) return PyLong_FromLong(st);
+        if (need) {
+            if (!find_scratch(dev, s, need, &ws, &have)) return NULL;
+            if (!ws) return PyLong_FromSize_t(need);
+        }
+    }
+    return PyLong_FromLong(f_prompt(q.ptr, token_stride(&q), k.ptr, token_stride(&k), v.ptr, token_stride(&v), o.ptr, token_stride(&o), (int)N,
+                                    (int)M, (int)QH, (int)H, (int)D, scale, offsets, kv_offsets, (int)B, ws, have, s));
+}
+
 /* keep(device, stream, tensor, pointer, bytes): scratch of a stream from now on, where there is room to note it.  Address
  * and tensor change together, so another thread's call between the two cannot leave an address of freed memory. */
 static PyObject *py_keep(PyObject *self, PyObject *args) {
@@ -504,17 +566,19 @@ static PyObject *py_release(PyObject *self, PyObject *none) {
     Py_RETURN_NONE;
 }
 
-/* setup(append, read, attn, workspace, verify, rope, paged, its workspace: addresses; float32, bfloat16, int32, current raw stream, whether it is being
+/* setup(append, read, attn, workspace, verify, rope, paged, its workspace, prompt, its workspace: addresses; float32, bfloat16, int32, current raw stream, whether it is being
  * captured: torch's) */
 static PyObject *py_setup(PyObject *self, PyObject *args) {
-    unsigned long long f[8];
-    if (!PyArg_ParseTuple(args, "KKKKKKKKOOOOO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &f[7], &t_f32, &t_bf16, &t_i32, &raw_stream,
+    unsigned long long f[10];
+    if (!PyArg_ParseTuple(args, "KKKKKKKKKKOOOOO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &f[7], &f[8],
+                          &f[9], &t_f32, &t_bf16, &t_i32, &raw_stream,
                           &capturing))
         return NULL;
     Py_INCREF(t_f32), Py_INCREF(t_bf16), Py_INCREF(t_i32), Py_INCREF(raw_stream), Py_INCREF(capturing);
     f_append = (rows_fn)(uintptr_t)f[0], f_read = (rows_fn)(uintptr_t)f[1], f_attn = (attn_fn)(uintptr_t)f[2];
     f_space = (space_fn)(uintptr_t)f[3], f_verify = (verify_fn)(uintptr_t)f[4];
     f_rope = (rope_fn)(uintptr_t)f[5], f_paged = (paged_fn)(uintptr_t)f[6], f_paged_space = (paged_space_fn)(uintptr_t)f[7];
+    f_prompt = (prompt_fn)(uintptr_t)f[8], f_prompt_space = (prompt_space_fn)(uintptr_t)f[9];
     Py_RETURN_NONE;
 }
 
@@ -525,6 +589,7 @@ static PyMethodDef methods[] = {{"setup", py_setup, METH_VARARGS, NULL},
                                 {"attn", (PyCFunction)(void (*)(void))py_attn, METH_FASTCALL, NULL},
                                 {"verify", (PyCFunction)(void (*)(void))py_verify, METH_FASTCALL, NULL},
                                 {"paged", (PyCFunction)(void (*)(void))py_paged, METH_FASTCALL, NULL},
+                                {"prompt", (PyCFunction)(void (*)(void))py_prompt, METH_FASTCALL, NULL},
                                 {"rope", (PyCFunction)(void (*)(void))py_rope, METH_FASTCALL, NULL},
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_qd_ops", NULL, -1, methods, NULL, NULL, NULL, NULL};

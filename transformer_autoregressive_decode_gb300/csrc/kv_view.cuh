@@ -131,6 +131,23 @@ inline bool rows_apart(const void *q, int64_t q_stream, int64_t q_token, const v
     return true;
 }
 
+// The stretch of memory that n rows of `inner` elements of e bytes, `stride` elements apart, lie in.
+struct Stretch {
+    uintptr_t from, to;
+    Stretch(const void *p, int64_t e, int64_t n, int64_t stride, int64_t inner)
+        : from(reinterpret_cast<uintptr_t>(p)), to(from + (uintptr_t)(((n - 1) * stride + inner) * e)) {}
+    bool meets(const Stretch &o) const { return from < o.to && o.from < to; }
+};
+// Whether `out`'s rows lie over none of p's: elsewhere, or in the gaps between rows of the same pitch.
+inline bool rows_beside(const void *out, int64_t oe, int64_t on, int64_t os, int64_t oi, const void *p, int64_t pe, int64_t pn, int64_t ps,
+                        int64_t pi) {
+    if (!Stretch(out, oe, on, os, oi).meets(Stretch(p, pe, pn, ps, pi))) return true;
+    const int64_t pitch = on > 1 ? os * oe : pn > 1 ? ps * pe : 0;
+    if (pitch <= 0 || (on > 1 && pn > 1 && ps * pe != pitch)) return false;
+    const int64_t off = (bytes_between(p, out) % pitch + pitch) % pitch;   // out's row begins this far behind one of p's
+    return off >= pi * pe && off + oi * oe <= pitch;
+}
+
 inline KvView kv_view(const qd_kv_cache *c) {
     const int64_t e = c->format == QD_KV_Q8 ? 1 : 2;
     return {static_cast<const uint8_t *>(c->k), static_cast<const uint8_t *>(c->v), c->k_scale, c->v_scale,

@@ -350,6 +350,8 @@ cudaError_t launch_batch_attention(int hd, int B, const BatchAttnArgs &a, const 
 // 32-position tiles, the prefill attention's 128-key chunks); false if the driver
 // refuses it.
 bool make_kv_tile_map(CUtensorMap *m, const void *kv, int hd, int S, long long planes, int box_rows = 32);
+// bf16 [tokens][heads][hd], a token's heads contiguous, tokens `stride` elements apart: box of 64 dims x box_heads x box_tokens
+bool make_heads_map(CUtensorMap *m, const void *rows, int hd, int heads, int tokens, int64_t stride, int box_heads, int box_tokens);
 // TMA map of a row-major bf16 matrix [rows, K], box of 64 elements x box_rows rows with
 // the 128-byte swizzle; false if the driver refuses it.
 bool make_bf16_rows_map(CUtensorMap *m, const void *ptr, int rows, int K, int box_rows);

@@ -222,14 +222,6 @@ template <typename TI, typename TO> RopeFn rope_fn(int d, bool q8) {
     return q8 ? qk_norm_rope_kernel<TI, TO, 128, true, U> : qk_norm_rope_kernel<TI, TO, 128, false, U>;
 }
 
-// The stretch of memory that n rows of `inner` elements of e bytes, `stride` elements apart, lie in.
-struct Stretch {
-    uintptr_t from, to;
-    Stretch(const void *p, int64_t e, int64_t n, int64_t stride, int64_t inner)
-        : from(reinterpret_cast<uintptr_t>(p)), to(p ? from + (uintptr_t)(((n - 1) * stride + inner) * e) : from) {}
-    bool meets(const Stretch &o) const { return from < o.to && o.from < to; }
-};
-
 }  // namespace
 
 }  // namespace qd
@@ -270,12 +262,7 @@ extern "C" qd_status qd_qk_norm_rope(const qd_rope_rows *x, void *cuda_stream) {
             const int64_t pe = j < 3 ? e : oe, ps = j < 3 ? in_stride[j] : out_stride[j - 3];
             const int64_t pi = (int64_t)(j % 3 ? x->n_kv_heads : x->n_q_heads) * d;
             if (j == i && p == out[i] && pe == oe && (N == 1 || ps == out_stride[i])) continue;
-            if (!Stretch(out[i], oe, N, out_stride[i], inner).meets(Stretch(p, pe, N, ps, pi))) continue;
-            // rows of one stride that stand beside each other
-            const int64_t gap = bytes_between(p, out[i]), pitch = ps * pe;
-            if (N < 2 || pitch != out_stride[i] * oe || pitch <= 0) return QD_EINVAL;
-            const int64_t off = ((gap % pitch) + pitch) % pitch;         // out's row begins this far into p's pitch
-            if (off < pi * pe || off + inner * oe > pitch) return QD_EINVAL;
+            if (!rows_beside(out[i], oe, N, out_stride[i], inner, p, pe, N, ps, pi)) return QD_EINVAL;
         }
     }
     for (const void *p : {(const void *)x->q_gamma, (const void *)x->k_gamma, (const void *)x->cos, (const void *)x->sin})

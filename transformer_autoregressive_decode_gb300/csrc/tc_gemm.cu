@@ -556,6 +556,20 @@ bool make_kv_tile_map(CUtensorMap *m, const void *kv, int hd, int S, long long p
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_heads_map(CUtensorMap *m, const void *rows, int hd, int heads, int tokens, int64_t stride, int box_heads, int box_tokens) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn || (reinterpret_cast<uintptr_t>(rows) & 15) || hd % 64 || heads < 1 || tokens < 1 || stride % 8 || box_heads < 1 ||
+        box_heads > 256 || box_tokens < 1 || box_tokens > 256)
+        return false;
+    cuuint64_t dims[3] = {(cuuint64_t)hd, (cuuint64_t)heads, (cuuint64_t)tokens};
+    cuuint64_t strides[2] = {(cuuint64_t)hd * 2, (cuuint64_t)stride * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
+    cuuint32_t es[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(rows), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 constexpr int kMaxSplits = 8;
 
 bool tc_gemm_plan(int R, int K, int T, int num_sms, TcGemmPlan *p) {
