@@ -707,7 +707,7 @@ typedef struct {
  * The rows of the streams: with offsets, packed, rows [offsets[b], offsets[b + 1]) are stream b's new tokens; without,
  * n_tokens / n_streams rows a stream, of which it uses the first n_new[b] (NULL: all).  Row t of a stream with n new
  * tokens stands at position lengths[b] - n + t of its cache.  lengths NULL: rows without a stream (positions and no
- * pages).  Rows that no stream uses are neither read nor written.  A position outside the
+ * pages).  Rows that no stream uses do not matter and are not written.  A position outside the
  * tables makes the row's rotated results NaN; one outside [0, table_pages * page) or on a page outside the pool is
  * not written.  Offsets ascend in [0, n_tokens]; rows that they do not give to one stream may be left out.
  * No two rows of one call may stand at the same place in the cache.

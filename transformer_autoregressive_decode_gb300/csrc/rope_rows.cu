@@ -3,21 +3,28 @@
 //
 //   x' = x / sqrt(mean(x^2) + eps) * gamma,   y[d] = x'[d] c_d - x'[d + h] s_d,   y[d + h] = x'[d + h] c_d + x'[d] s_d   (h = D / 2)
 //
-// Every byte moves once, so HBM bounds it for prompts, and the launch and three dependent loads (length, page and table row,
-// the rows) for a step.  A row stands on D / 8 lanes, each with four elements of the lower half and the four that they are rotated with:
-// nothing but the sum of squares (and the maximum of an 8-bit row) crosses lanes, and a lane that rotates a token's rows
-// keeps its four cosines and sines from head to head.  Everything is fp32 until the result is rounded once.
+// Every byte moves once, so HBM bounds it for prompts (28000 tokens of 32 + 16 heads, 688 MB, 121 us, 0.84 of the measured rate;
+// 3248 fp32 tokens of 16 + 16 heads into 8-bit pages, 73 MB, 16 us, 0.68: the start's loads and the end take the rest), and the launch
+// and three dependent loads (length, page and table row) for a step (64 tokens 3.2 us).  A row stands on D / 16 lanes, each with eight
+// elements of the lower half and the eight that they are rotated with: nothing but the sum of squares (and the maximum of an
+// 8-bit row) crosses lanes, and a lane keeps its eight cosines and sines of a token from head to head.  Everything is fp32 until the
+// result is rounded once.
 #include <algorithm>
 
 #include "kv_view.cuh"
+#include "mma_sync.cuh"
 #include "qd_device.cuh"
 #include "qd_internal.h"
+#include "tc_common.cuh"
 
 namespace qd {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
+// CTAs an SM and rows ahead of a thread, the one at hand among them (16 x 2500 bf16 tokens of 32 + 16 heads, 8 x 512 fp32 tokens of 16 + 16:
+// 4 CTAs 124 and 16.6 us, 5 121 and 15.9, 6 127 and 17.6; a row less 121 and 16.0, one more 122 and 16.9).
+constexpr int kRopeThreads = 128, kRopeCtas = 5;
+template <typename T> constexpr int kRopeAhead = sizeof(T) == 2 ? 4 : 3;
 
 struct RopeArgs {
     const uint8_t *in[3];              // q, k, v rows
@@ -29,197 +36,310 @@ struct RopeArgs {
     const int32_t *pos;                // [N] or [3][N], or null: the positions in the cache
     int rope_rows, mrope3;             // frequencies below mrope3 take stream d % 3
     const int32_t *lengths, *offsets, *n_new;
-    int B, T, N, qh, kvh, heads;
+    int B, T, N, qh, kvh;
     KvView pages;                      // k null: none
     const int32_t *table;
     int64_t table_stride;
     int table_pages, n_pages, page_shift;
-    int hp, tp, run;                   // heads and tokens of a CTA's groups of lanes; tokens of a CTA
+    int units, run;                    // of heads of a token (a warp's rows each); of those of a warp
 };
 
-// Four elements as floats, and back.
-template <typename T> struct Four;
-template <> struct Four<float> {
-    using V = float4;
-    static __device__ __forceinline__ void get(V u, float *x) { x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w; }
-    static __device__ __forceinline__ V put(const float *x) { return make_float4(x[0], x[1], x[2], x[3]); }
-};
-template <> struct Four<__nv_bfloat16> {
-    using V = uint2;
-    static __device__ __forceinline__ void get(V u, float *x) { x[0] = bf16lo(u.x), x[1] = bf16hi(u.x), x[2] = bf16lo(u.y), x[3] = bf16hi(u.y); }
-    static __device__ __forceinline__ V put(const float *x) {
-        const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
-        return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+// A lane's 16 elements of a row of D: eight of the lower half (in chunks of 16 bytes, which are contiguous across the lanes: 32 bytes a lane in two loads
+// took every 32-byte sector twice, 8 x 512 fp32 tokens 24 us) and the eight that they are rotated with.
+template <typename T, int D> struct Sixteen {
+    static constexpr int P = (int)sizeof(T), E = 16 / P;             // chunks, elements of one
+    // chunk i's first element
+    static __device__ __forceinline__ int at(int i, int lane) { return i * (D / P) + E * lane; }
+    static __device__ __forceinline__ void get(const uint4 *u, float *f) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) Elem<T>::unpack(u[i], f + i * E);
     }
 };
-
-// A token's stream, its place among the stream's new rows, how many those are; b < 0: the row is not in use.
-struct Token {
-    int b, t, n;
-};
-__device__ __forceinline__ Token token_of(const RopeArgs &a, int row) {
-    if (!a.offsets) {
-        if (!a.lengths) return {0, row, a.N};
-        const int b = row / a.T, t = row - b * a.T;
-        int n = a.n_new ? a.n_new[b] : a.T;
-        n = n < 0 ? 0 : n > a.T ? a.T : n;
-        return {t < n ? b : -1, t, n};
+// N elements as T, to memory.
+template <typename T, int N> __device__ __forceinline__ void put(uint8_t *to, const float *f) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) *reinterpret_cast<float4 *>(to + 4 * i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+    } else if constexpr (N == 8) {
+        *reinterpret_cast<uint4 *>(to) = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+    } else {
+        *reinterpret_cast<uint2 *>(to) = make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
     }
-    int lo = 0, hi = a.B;                               // the last stream that begins at row or before
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.offsets[mid] <= row)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    const int first = a.offsets[lo], end = min(a.offsets[lo + 1], a.N);
-    return {first >= 0 && first <= row && row < end ? lo : -1, row - first, end - first};
 }
 
-// fp32 bits of |x| order like the magnitudes, NaN above infinity.
-__device__ __forceinline__ uint32_t mag(float x) { return __float_as_uint(x) & 0x7fffffffu; }
-
-template <typename TI, typename TO, int D, bool Q8, int U>
-__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeArgs a) {
-    constexpr int LPR = D / 8, HALF = D / 2;
-    const int lane = threadIdx.x % LPR, slot = threadIdx.x / LPR, in = slot / a.hp, h0 = slot - in * a.hp;
-    const int heads = a.heads;
-    const uint32_t mask = LPR == 16 ? 0xffffu << (threadIdx.x & 16) : 0xffu << (threadIdx.x & 24);
-    if (in >= a.tp) return;
-    const int end = min(a.N, (int)(blockIdx.x + 1) * a.run);
-    for (int row = (int)blockIdx.x * a.run + in; row < end; row += a.tp) {
-        const Token tk = token_of(a, row);
-        if (tk.b < 0) continue;
-        // where the token stands
-        const int at = a.lengths ? max(a.lengths[tk.b], 0) - tk.n + tk.t : -1;
-        int64_t to = -1, to_s = -1;                     // bytes into the pages, of a row of head 0; scales
-        if (a.pages.k && at >= 0 && (at >> a.page_shift) < a.table_pages) {
-            const int page = a.table[tk.b * a.table_stride + (at >> a.page_shift)], r = at & ((1 << a.page_shift) - 1);
-            if ((unsigned)page < (unsigned)a.n_pages) {
-                to = page * a.pages.stream + r * a.pages.row;
-                to_s = page * a.pages.sstream + r;
-            }
+// The stream of the token rows that a warp walks.
+struct Stream {
+    int b, first, end, base;                            // rows [first, end) are the stream's; row r stands at position base + r - first
+    // The last stream that begins at row or before: 32 offsets at a time, coarse to fine.
+    __device__ __forceinline__ void find(const RopeArgs &a, int row) {
+        b = 0, first = 0, end = a.N, base = 0;
+        if (!a.lengths) return;
+        if (!a.offsets) {
+            b = row / a.T;
+            load(a);
+            return;
         }
-        float c[4], s[4];
-        if (a.cos) {
-            const int most = a.rope_rows;
-            if (a.mrope3) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int d = 4 * lane + e, p = a.pos[(int64_t)(d < a.mrope3 ? d % 3 : 0) * a.N + row];
-                    const bool there = (unsigned)p < (unsigned)most;
-                    c[e] = there ? __ldg(a.cos + (int64_t)p * HALF + d) : __uint_as_float(0x7fc00000u);
-                    s[e] = there ? __ldg(a.sin + (int64_t)p * HALF + d) : __uint_as_float(0x7fc00000u);
-                }
-            } else {
-                const int p = a.pos ? a.pos[row] : at;
-                if ((unsigned)p < (unsigned)most) {
-                    Four<float>::get(__ldg(reinterpret_cast<const float4 *>(a.cos + (int64_t)p * HALF) + lane), c);
-                    Four<float>::get(__ldg(reinterpret_cast<const float4 *>(a.sin + (int64_t)p * HALF) + lane), s);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) c[e] = s[e] = __uint_as_float(0x7fc00000u);
-                }
-            }
+        const int lane = threadIdx.x & 31;
+        int n = a.B;
+        while (n > 1) {
+            const int step = (n + 31) / 32, at = lane * step;
+            const bool before = at < n && a.offsets[b + at] <= row;
+            const int k = max(__popc(__ballot_sync(0xffffffffu, before)), 1) - 1;
+            b += k * step, n = min(step, n - k * step);
+        }
+        load(a);
+    }
+    __device__ __forceinline__ void load(const RopeArgs &a) {
+        if (a.offsets) {
+            first = a.offsets[b], end = min(a.offsets[b + 1], a.N);
         } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) c[e] = 1.f, s[e] = 0.f;
+            const int n = a.n_new ? a.n_new[b] : a.T;
+            first = b * a.T, end = first + (n < 0 ? 0 : n > a.T ? a.T : n);
         }
-        for (int h = h0; h < heads; h += U * a.hp) {
-            typename Four<TI>::V lo[U], hi[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int hh = h + u * a.hp;
-                if (hh >= heads) break;
-                const int which = hh < a.qh ? 0 : hh < a.qh + a.kvh ? 1 : 2;
-                const int of = which == 0 ? hh : which == 1 ? hh - a.qh : hh - a.qh - a.kvh;
-                const TI *src = reinterpret_cast<const TI *>(a.in[which] + row * a.in_token[which]) + of * D + 4 * lane;
-                lo[u] = *reinterpret_cast<const typename Four<TI>::V *>(src);
-                hi[u] = *reinterpret_cast<const typename Four<TI>::V *>(src + HALF);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int hh = h + u * a.hp;
-                if (hh >= heads) break;
-                const int which = hh < a.qh ? 0 : hh < a.qh + a.kvh ? 1 : 2;
-                const int of = which == 0 ? hh : which == 1 ? hh - a.qh : hh - a.qh - a.kvh;
-                float x[8];
-                Four<TI>::get(lo[u], x);
-                Four<TI>::get(hi[u], x + 4);
-                if (which < 2) {
-                    const float *gamma = a.gamma[which];
-                    if (gamma) {
-                        float ss = 0.f;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-                        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
-                        const float inv = 1.f / sqrtf(ss / (float)D + a.eps);
-                        float g[8];
-                        Four<float>::get(__ldg(reinterpret_cast<const float4 *>(gamma) + lane), g);
-                        Four<float>::get(__ldg(reinterpret_cast<const float4 *>(gamma + HALF) + lane), g + 4);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * g[e];
-                    }
-                    if (a.cos) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float l = x[e], u2 = x[4 + e];
-                            x[e] = l * c[e] - u2 * s[e];
-                            x[4 + e] = u2 * c[e] + l * s[e];
-                        }
-                    }
-                }
-                if (a.out[which]) {
-                    TO *dst = reinterpret_cast<TO *>(a.out[which] + row * a.out_token[which]) + of * D + 4 * lane;
-                    *reinterpret_cast<typename Four<TO>::V *>(dst) = Four<TO>::put(x);
-                    *reinterpret_cast<typename Four<TO>::V *>(dst + HALF) = Four<TO>::put(x + 4);
-                }
-                if (which && to >= 0) {
-                    uint8_t *dst = const_cast<uint8_t *>(which == 1 ? a.pages.k : a.pages.v) + to + of * a.pages.head;
-                    if constexpr (Q8) {
-                        uint32_t m = 0;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) m = max(m, mag(x[e]));
-#pragma unroll
-                        for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(mask, m, o));
-                        // even lanes take one quotient, odd ones the other
-                        const bool finite = m < 0x7f800000u, zero = m < 0x05800000u;   // below 2^-116
-                        const float top = zero || !finite ? 1.f : __uint_as_float(m);
-                        float quot = lane & 1 ? __fdiv_rn(top, 127.f) : __fdiv_rn(127.f, top);
-                        if (zero) quot = 0.f;
-                        const float by = __shfl_sync(mask, quot, 0, LPR), scale = __shfl_sync(mask, quot, 1, LPR);
-                        uint32_t w[2];
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            uint32_t k[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                k[e] = __float_as_uint(__fadd_rn(__fmul_rn(finite ? x[4 * i + e] : 0.f, by), 12582912.f));
-                            w[i] = __byte_perm(__byte_perm(k[0], k[1], 0x0040), __byte_perm(k[2], k[3], 0x0040), 0x5410);
-                        }
-                        *reinterpret_cast<uint32_t *>(dst + 4 * lane) = w[0];
-                        *reinterpret_cast<uint32_t *>(dst + HALF + 4 * lane) = w[1];
-                        if (lane == 0)
-                            const_cast<float *>(which == 1 ? a.pages.ks : a.pages.vs)[to_s + of * a.pages.shead] =
-                                finite ? scale : __uint_as_float(0x7fc00000u);
-                    } else {
-                        __nv_bfloat16 *row16 = reinterpret_cast<__nv_bfloat16 *>(dst) + 4 * lane;
-                        *reinterpret_cast<uint2 *>(row16) = Four<__nv_bfloat16>::put(x);
-                        *reinterpret_cast<uint2 *>(row16 + HALF) = Four<__nv_bfloat16>::put(x + 4);
-                    }
-                }
-            }
+        base = max(a.lengths[b], 0) - (end - first);
+    }
+    // On to the stream of a later row.
+    __device__ __forceinline__ void go(const RopeArgs &a, int row) {
+        if (row < end || !a.lengths) return;
+        int then = b;
+        if (a.offsets)
+            while (then + 1 < a.B && a.offsets[then + 1] <= row) ++then;
+        else
+            then = row / a.T;
+        if (then != b) {
+            b = then;
+            load(a);
         }
     }
+};
+
+// Where a token goes in the pages, and which rows of the tables it is rotated by.
+struct Place {
+    int page, r;                                        // page -1: not written, -2: the row is not in use
+    int p[3];                                           // its position in every stream of positions
+};
+__device__ __forceinline__ Place place_of(const RopeArgs &a, Stream &s, int row, bool there) {
+    Place x;
+    x.page = -2, x.r = 0, x.p[0] = x.p[1] = x.p[2] = -1;
+    if (!there) return x;
+    s.go(a, row);
+    if (row < s.first || row >= s.end || s.first < 0) return x;
+    x.page = -1;
+    const int at = a.lengths ? s.base + row - s.first : -1;
+    if (a.table && at >= 0 && (at >> a.page_shift) < a.table_pages) {
+        const int page = a.table[s.b * a.table_stride + (at >> a.page_shift)];
+        x.r = at & ((1 << a.page_shift) - 1);
+        if ((unsigned)page < (unsigned)a.n_pages) x.page = page;
+    }
+    if (a.pos) {
+        x.p[0] = a.pos[row];
+        if (a.mrope3) x.p[1] = a.pos[(int64_t)a.N + row], x.p[2] = a.pos[2 * (int64_t)a.N + row];
+    } else {
+        x.p[0] = at;
+    }
+    return x;
+}
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// A warp takes a few heads of one kind (q, k, v) of one token at a time (a row on D / 16 lanes) and walks a run of those, token by token, the same number
+// for every warp, so that whatever goes by the kind or the token is the same for its lanes.  The rows ahead are on their way
+// into shared memory, S of them, each thread's own 16 elements into a place of its own: nothing waits for another thread, and
+// 64 KB an SM are in flight, where as many registers would leave no room (two rows ahead in registers: 16 x 2500 tokens 205 to
+// 310 us).  A token's place is looked up two tokens ahead, its cosines and sines are loaded one ahead.
+template <typename TI, typename TO, int D, bool Q8>
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) qk_norm_rope_kernel(const RopeArgs a) {
+    using X = Sixteen<TI, D>;
+    constexpr int LPR = D / 16, RPW = 32 / LPR, HALF = D / 2, P = X::P, E = X::E, S = kRopeAhead<TI>;
+    __shared__ uint4 ring[S][P][kRopeThreads];
+    const int lane = threadIdx.x % LPR, in = (threadIdx.x & 31) / LPR;    // this lane's share of a row; the row's place among the warp's
+    const int warp = __shfl_sync(0xffffffffu, (int)(blockIdx.x * (kRopeThreads / 32) + threadIdx.x / 32), 0);
+    const int64_t x0 = (int64_t)warp * a.run, left = (int64_t)a.N * a.units - x0;
+    if (left <= 0) return;
+    const int n = left < a.run ? (int)left : a.run;
+    int row = (int)(x0 / a.units), unit = (int)(x0 - (int64_t)row * a.units);
+    const int uq = (a.qh + RPW - 1) / RPW, uk = (a.kvh + RPW - 1) / RPW;   // units of q, of k
+    const int last = row + (n + unit - 1) / a.units;    // the run's last token
+
+    // the copies: of rows that no stream uses, too, which are there all the same
+    int ci = 0, cu = unit, crow = row;                  // units so far; unit and token of the next
+    const uint32_t mine = smem_addr(&ring[0][0][threadIdx.x]);
+    auto copy = [&](int stage) {
+        if (ci < n) {
+            const int kind = cu < uq ? 0 : cu < uq + uk ? 1 : 2, of = (cu - (kind == 0 ? 0 : kind == 1 ? uq : uq + uk)) * RPW + in;
+            const uint8_t *src = a.in[kind] + crow * a.in_token[kind] + (of * D + E * lane) * (int)sizeof(TI);
+            if (of < (kind ? a.kvh : a.qh)) {
+#pragma unroll
+                for (int i = 0; i < P; ++i)
+                    cp16(mine + (uint32_t)((stage * P + i) * kRopeThreads * 16), src + i * (D / P) * (int)sizeof(TI));
+            }
+            ++ci;
+            if (++cu == a.units) cu = 0, ++crow;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    // of a vector in this lane's order: elements 4 i .. of its 16
+    auto four = [&](const float *v, int i) {
+        return __ldg(reinterpret_cast<const ulonglong2 *>(v + X::at(4 * i / E, lane) + 4 * i % E));
+    };
+    struct Angles {
+        uint64_t c[4], s[4];
+    };
+    auto angles = [&](const Place &p) {
+        Angles x;
+        const float nan = __uint_as_float(0x7fc00000u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x.c[i] = x.s[i] = pk(nan, nan);
+        if (!a.cos || p.page == -2) return x;
+        if (a.mrope3) {
+            float c[8], s[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int d = X::at(e / E, lane) + e % E, k = d < a.mrope3 ? d % 3 : 0, q = k == 0 ? p.p[0] : k == 1 ? p.p[1] : p.p[2];
+                const bool there = (unsigned)q < (unsigned)a.rope_rows;
+                c[e] = there ? __ldg(a.cos + (int64_t)q * HALF + d) : nan;
+                s[e] = there ? __ldg(a.sin + (int64_t)q * HALF + d) : nan;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x.c[i] = pk(c[2 * i], c[2 * i + 1]), x.s[i] = pk(s[2 * i], s[2 * i + 1]);
+        } else if ((unsigned)p.p[0] < (unsigned)a.rope_rows) {
+            const float *c = a.cos + (int64_t)p.p[0] * HALF, *s = a.sin + (int64_t)p.p[0] * HALF;
+            const ulonglong2 c0 = four(c, 0), c1 = four(c, 1), s0 = four(s, 0), s1 = four(s, 1);
+            x.c[0] = c0.x, x.c[1] = c0.y, x.c[2] = c1.x, x.c[3] = c1.y;
+            x.s[0] = s0.x, x.s[1] = s0.y, x.s[2] = s1.x, x.s[3] = s1.y;
+        }
+        return x;
+    };
+    const uint64_t minus = pk(-1.f, -1.f);
+    // one unit of a token; every lane comes here (the sums cross lanes), `live` ones write
+    auto finish = [&](const uint4 *in16, const Place &p, int row, int kind, int of, bool live, const Angles &w) {
+        float f[16];
+        X::get(in16, f);
+        if (kind < 2) {
+            uint64_t y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = pk(f[2 * e], f[2 * e + 1]);
+            // the row's mean square crosses lanes while the elements are weighted and rotated; its root multiplies them last
+            float inv = 1.f;
+            const float *g = a.gamma[kind];
+            if (g) {
+                uint64_t sq = mul2(y[0], y[0]), sr = mul2(y[1], y[1]);
+#pragma unroll
+                for (int e = 2; e < 8; e += 2) sq = fma2(y[e], y[e], sq), sr = fma2(y[e + 1], y[e + 1], sr);
+                float s0, s1;
+                unpk(add2(sq, sr), s0, s1);
+                float ss = s0 + s1;
+#pragma unroll
+                for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                inv = rsqrtf(fmaf(ss, 1.f / (float)D, a.eps));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const ulonglong2 v = four(g, i);
+                    y[2 * i] = mul2(y[2 * i], v.x), y[2 * i + 1] = mul2(y[2 * i + 1], v.y);
+                }
+            }
+            if (a.cos) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint64_t l = y[e], u = y[4 + e];
+                    y[e] = fma2(mul2(u, w.s[e]), minus, mul2(l, w.c[e]));
+                    y[4 + e] = fma2(u, w.c[e], mul2(l, w.s[e]));
+                }
+            }
+            const uint64_t inv2 = pk(inv, inv);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) unpk(mul2(y[e], inv2), f[2 * e], f[2 * e + 1]);
+        }
+        if (live && a.out[kind]) {
+            uint8_t *dst = a.out[kind] + row * a.out_token[kind] + (of * D + E * lane) * (int)sizeof(TO);
+#pragma unroll
+            for (int i = 0; i < P; ++i) put<TO, E>(dst + i * (D / P) * (int)sizeof(TO), f + i * E);
+        }
+        if (kind == 0 || p.page < 0) return;
+        const int64_t to = p.page * a.pages.stream + p.r * a.pages.row + of * a.pages.head;
+        uint8_t *dst = const_cast<uint8_t *>(kind == 1 ? a.pages.k : a.pages.v) + to;
+        if constexpr (Q8) {
+            uint64_t z = pk(0.f, 0.f);
+            const uint64_t none = z;
+            float most = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                z = fma2(pk(f[2 * e], f[2 * e + 1]), none, z);   // 0, or NaN where an element is not finite
+                most = fmaxf(most, fmaxf(fabsf(f[2 * e]), fabsf(f[2 * e + 1])));
+            }
+            float z0, z1;
+            unpk(z, z0, z1);
+            uint32_t m = z0 + z1 == 0.f ? __float_as_uint(most) : 0x7fc00000u;
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+            // even lanes take one quotient, odd ones the other
+            const bool finite = m < 0x7f800000u, zero = m < 0x05800000u;   // below 2^-116
+            const float top = zero || !finite ? 1.f : __uint_as_float(m);
+            float quot = __fdiv_rn(lane & 1 ? top : 127.f, lane & 1 ? 127.f : top);
+            if (zero) quot = 0.f;
+            const float by = __shfl_sync(0xffffffffu, quot, 0, LPR), scale = __shfl_sync(0xffffffffu, quot, 1, LPR);
+            const uint64_t magic = pk(12582912.f, 12582912.f);
+            uint32_t q[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                // the low byte is the code (the products singly: a packed product and sum became one fused operation, which rounds once)
+                const uint64_t c0 = add2(pk(__fmul_rn(f[4 * i], by), __fmul_rn(f[4 * i + 1], by)), magic);
+                const uint64_t c1 = add2(pk(__fmul_rn(f[4 * i + 2], by), __fmul_rn(f[4 * i + 3], by)), magic);
+                q[i] = __byte_perm(__byte_perm((uint32_t)c0, (uint32_t)(c0 >> 32), 0x0040), __byte_perm((uint32_t)c1, (uint32_t)(c1 >> 32), 0x0040),
+                                   0x5410);
+                if (!finite) q[i] = 0;
+            }
+            if (live) {
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    if constexpr (E == 8)
+                        *reinterpret_cast<uint2 *>(dst + X::at(i, lane)) = make_uint2(q[2 * i], q[2 * i + 1]);
+                    else
+                        *reinterpret_cast<uint32_t *>(dst + X::at(i, lane)) = q[i];
+                }
+                if (lane == 0)
+                    const_cast<float *>(kind == 1 ? a.pages.ks : a.pages.vs)[p.page * a.pages.sstream + of * a.pages.shead + p.r] =
+                        finite ? scale : __uint_as_float(0x7fc00000u);
+            }
+        } else if (live) {
+#pragma unroll
+            for (int i = 0; i < P; ++i) put<__nv_bfloat16, E>(dst + 2 * X::at(i, lane), f + i * E);
+        }
+    };
+
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) copy(i);
+    Stream s;
+    s.find(a, row);
+    Place p0 = place_of(a, s, row, true), p1 = place_of(a, s, row + 1, row < last);
+    Angles w0 = angles(p0), w1 = angles(p1);
+    Place p2 = place_of(a, s, row + 2, row + 1 < last);
+    int stage = 0;
+    for (int i = 0; i < n; ++i) {
+        copy(stage == 0 ? S - 1 : stage - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+        uint4 u[P];
+#pragma unroll
+        for (int j = 0; j < P; ++j) u[j] = ring[stage][j][threadIdx.x];
+        const int kind = unit < uq ? 0 : unit < uq + uk ? 1 : 2, of = (unit - (kind == 0 ? 0 : kind == 1 ? uq : uq + uk)) * RPW + in;
+        if (p0.page != -2) finish(u, p0, row, kind, of, of < (kind ? a.kvh : a.qh), w0);
+        stage = stage == S - 1 ? 0 : stage + 1;
+        if (++unit == a.units) {
+            unit = 0, ++row;
+            p0 = p1, w0 = w1, p1 = p2;
+            w1 = angles(p1);
+            p2 = place_of(a, s, row + 2, row + 1 < last);
+        }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 typedef void (*RopeFn)(const RopeArgs);
 template <typename TI, typename TO> RopeFn rope_fn(int d, bool q8) {
-    constexpr int U = 2;
-    if (d == 64) return q8 ? qk_norm_rope_kernel<TI, TO, 64, true, U> : qk_norm_rope_kernel<TI, TO, 64, false, U>;
-    return q8 ? qk_norm_rope_kernel<TI, TO, 128, true, U> : qk_norm_rope_kernel<TI, TO, 128, false, U>;
+    if (d == 64) return q8 ? qk_norm_rope_kernel<TI, TO, 64, true> : qk_norm_rope_kernel<TI, TO, 64, false>;
+    return q8 ? qk_norm_rope_kernel<TI, TO, 128, true> : qk_norm_rope_kernel<TI, TO, 128, false>;
 }
 
 }  // namespace
@@ -307,11 +427,13 @@ extern "C" qd_status qd_qk_norm_rope(const qd_rope_rows *x, void *cuda_stream) {
         a.table = x->page_table, a.table_stride = x->table_stride, a.table_pages = x->table_pages;
         a.n_pages = c->n_streams, a.page_shift = shift;
     }
-    const int groups = kRopeThreads / (d / 8), heads = a.qh + (a.in[2] ? 2 : 1) * a.kvh;
-    a.heads = heads, a.hp = std::min(heads, groups), a.tp = groups / a.hp;
-    const int sms = sms_of(dev);
-    a.run = std::max(a.tp, (a.N + sms * 16 - 1) / (sms * 16));
-    const dim3 grid((unsigned)((a.N + a.run - 1) / a.run));
+    // a run for every warp that the SMs hold at once
+    const int rpw = 512 / d, sms = sms_of(dev);
+    a.units = (a.qh + rpw - 1) / rpw + (a.in[2] ? 2 : 1) * ((a.kvh + rpw - 1) / rpw);
+    const int64_t units = (int64_t)a.N * a.units, warps = (int64_t)sms * kRopeCtas * (kRopeThreads / 32);
+    a.run = (int)((units + warps - 1) / warps);
+    const int64_t per = (int64_t)a.run * (kRopeThreads / 32);
+    const dim3 grid((unsigned)((units + per - 1) / per));
     const bool q8 = c && c->format == QD_KV_Q8;
     const RopeFn fn = x->dtype == QD_F32 ? (x->out_dtype == QD_F32 ? rope_fn<float, float>(d, q8) : rope_fn<float, __nv_bfloat16>(d, q8))
                                          : (x->out_dtype == QD_F32 ? rope_fn<__nv_bfloat16, float>(d, q8)
