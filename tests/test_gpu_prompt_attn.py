@@ -84,14 +84,15 @@ def test_values(qd, shape):
 @pytest.mark.parametrize("lens, klens, qh, kvh, hd", [
     ([2000, 1], None, 16, 8, 128), ([512] * 8, None, 16, 8, 128), (list(range(1, 600, 17)), None, 8, 8, 64), ([3000], None, 32, 4, 128),
     ([100] * 70, None, 6, 2, 64), ([700, 300, 1000], [3000, 5000, 1000], 12, 4, 128), ([1] * 400, None, 4, 4, 64),
-    ([4100], None, 4, 4, 64), ([40] * 1500, None, 1, 1, 64), ([9000], None, 6, 6, 128), ([1900, 2000], [2500, 4001], 18, 6, 64)])
+    ([4100], None, 4, 4, 64), ([40] * 1500, None, 1, 1, 64), ([9000], None, 6, 6, 128), ([1900, 2000], [2500, 4001], 18, 6, 64),
+    ([20000, 17, 3000], None, 4, 2, 64), ([5000, 4000], [6000, 4000], 40, 8, 128), ([33] * 300, [33 + i for i in range(300)], 16, 8, 64)])
 def test_many_pairs(qd, lens, klens, qh, kvh, hd):
-    """As many pairs of tiles as SMs, or more: those are taken from the sorted list."""
+    """More pairs of tiles than SMs, dealt out by every CTA for itself or, beyond 256 pairs or 16 an SM, taken from a sorted list."""
     st = make(lens, klens, qh, kvh, hd, slack=3)
     N, M = st["q"].shape[0], st["k"].shape[0]
-    pairs = (N // (2 * (128 // (qh // kvh))) + len(lens)) * kvh
+    pairs = N // (2 * (128 // (qh // kvh))) + len(lens)
     sms = torch.cuda.get_device_properties(0).multi_processor_count
-    assert (qd.qd_attn_prompt_workspace(N, M, len(lens), qh, kvh, hd) > 0) == (pairs > sms)
+    assert (qd.qd_attn_prompt_workspace(N, M, len(lens), qh, kvh, hd) > 0) == (pairs > 256 or len(lens) > 256 or pairs * kvh > 16 * sms)
     call(qd, st)
     check(st)
 
@@ -225,7 +226,7 @@ def test_offsets_that_make_no_sense(qd, offs):
         assert (st["out"].cpu()[~rows] == MARK).all() and st["out"].isfinite().all()
 
 
-@pytest.mark.parametrize("lens", [[64, 30], [700, 900, 300]], ids=["a pair an SM", "list"])
+@pytest.mark.parametrize("lens", [[64, 30], [700, 900, 300], [100] * 260], ids=["a pair an SM", "several", "list"])
 def test_captured_calls(qd, lens):
     """A graph's replays with other lengths and values, and two calls in it."""
     st = make(lens, None, 16, 8, 128)
@@ -249,7 +250,7 @@ def test_captured_calls(qd, lens):
 
 
 def test_streams_and_workspaces(qd):
-    sts = [make([800, 600, 77], None, 16, 8, 128, seed=i) for i in range(2)]
+    sts = [make(lens, None, 16, 8, 128, seed=i) for i, lens in enumerate(([800, 600, 77], [100] * 270))]
     side = [torch.cuda.Stream() for _ in sts]
     torch.cuda.synchronize()
     for _ in range(4):
@@ -260,8 +261,8 @@ def test_streams_and_workspaces(qd):
     torch.cuda.synchronize()
     for st in sts:
         check(st)
-    st = make([800, 600, 77, 900], None, 16, 8, 128)       # (2377 // 128 + 4) * 8 = 176 pairs: more than SMs
-    need = qd.qd_attn_prompt_workspace(2377, 2377, 4, 16, 8, 128)
+    st = make([9000, 20000, 77, 5000], None, 16, 8, 128)   # 34077 // 128 + 4 = 270 pairs: a list
+    need = qd.qd_attn_prompt_workspace(34077, 34077, 4, 16, 8, 128)
     want = call(qd, st).clone()
     call(qd, st, workspace=torch.full((need,), 255, dtype=torch.uint8, device="cuda"))
     assert torch.equal(st["out"], want)

@@ -40,15 +40,15 @@ namespace qd {
 
 namespace {
 
-constexpr int kPtThreads = 384, kPtSoft = 256;
-constexpr int kPtRegsSoft = 208, kPtRegsRest = 88;
-static_assert(kPtSoft * kPtRegsSoft + (kPtThreads - kPtSoft) * kPtRegsRest <= kPtThreads * 168, "registers");
+constexpr int kPtThreads = 640, kPtSoft = 512;
+constexpr int kPtRegsSoft = 104, kPtRegsRest = 64;
+static_assert(kPtSoft * kPtRegsSoft + (kPtThreads - kPtSoft) * kPtRegsRest <= kPtThreads * 96, "registers");
 constexpr uint32_t kPtBox = 128 * 128;        // 128 rows of 128 bytes, 128-byte swizzle
 constexpr uint32_t kPtS = 0, kPtO = 256;      // tensor memory columns: S (and P) of the tiles, O
 constexpr int kPtKeys = 128;                  // of a chunk
 constexpr int kPtStages = 2;                  // of K and of V
 constexpr int kPtSlots = 4;                   // pairs in flight between the roles
-constexpr int kPtUsers = 11;                  // warps that read a slot
+constexpr int kPtUsers = 19;                  // warps that read a slot
 constexpr int kPtBuckets = 1024;              // of the plan's sort
 constexpr float kPtTop = 1.2e24f;             // 2^80
 
@@ -59,19 +59,24 @@ struct PromptArgs {
     const int32_t *offsets, *kv_offsets;      // kv_offsets: may be offsets
     int N, M, B, G, kvh;                      // tokens, keys
     int tpt;                                  // tokens of a tile
+    bool wide_out;                            // out's rows stand at multiples of 32 bytes
     float scale2;                             // softmax scale times log2(e)
-    // the plan: pairs (sequence, pair) longest first, room for `cap`; [0] their number, [1] the next to be taken.  null: a pair per CTA
-    int2 *list;
+    // the list of pairs, longest first, room for `cap`; [0] their number, [1] those taken beyond the first of each CTA.  null: every CTA
+    // finds its own
+    int4 *list;
     int *count;
     int cap, cost_shift;
 };
 
 // A pair of tiles, as the roles see it.
-struct Pair {
-    int hk, q0, tokens;                       // key head; first token row, tokens (of both tiles)
+struct __align__(16) Pair {
+    int q0, tokens;                           // first token row, tokens (of both tiles)
     int k0, lim0;                             // first key row; keys that the first token sees
-    int n[2];                                 // chunks of either tile; hk < 0: no more pairs
+    int n0, n1;                               // chunks of either tile
+    int hk;                                   // key head; below 0: no more pairs
     uint32_t odd;                             // chunks, counted from first_edge(), in which V was not finite
+    __device__ __forceinline__ int n(int h) const { return h ? n1 : n0; }
+    __device__ __forceinline__ int most() const { return max(n0, n1); }
 };
 // The first chunk that the pair's first token does not see all of.
 __device__ __forceinline__ int first_edge(const Pair &p) { return p.lim0 > 0 ? p.lim0 / kPtKeys : 0; }
@@ -89,16 +94,15 @@ __device__ __forceinline__ Sequence sequence(const PromptArgs &a, int b) {
 }
 __device__ __forceinline__ int chunks(int keys) { return keys > 0 ? (keys + kPtKeys - 1) / kPtKeys : 0; }
 
-__device__ __forceinline__ Pair pair_of(const PromptArgs &a, int b, int pair, int hk) {
-    const Sequence s = sequence(a, b);
+__device__ __forceinline__ Pair pair_of(const PromptArgs &a, const Sequence &s, int pair, int hk) {
     const int t0 = pair * 2 * a.tpt;
     Pair p;
     p.hk = hk;
     p.q0 = s.q0 + t0, p.tokens = min(s.n - t0, 2 * a.tpt);
     p.k0 = s.k0, p.lim0 = s.m - s.n + t0 + 1;
     const int first = min(p.tokens, a.tpt);
-    p.n[0] = chunks(p.lim0 + first - 1);
-    p.n[1] = p.tokens > first ? chunks(p.lim0 + p.tokens - 1) : 0;
+    p.n0 = chunks(p.lim0 + first - 1);
+    p.n1 = p.tokens > first ? chunks(p.lim0 + p.tokens - 1) : 0;
     p.odd = 0;
     return p;
 }
@@ -121,11 +125,11 @@ __global__ void __launch_bounds__(1024) attn_prompt_plan_kernel(const PromptArgs
             const int pairs = pairs_of(a, s);
             for (int i = tid % per; i < pairs; i += per) {
                 const int last = min(s.n, (i + 1) * 2 * a.tpt);            // tokens up to the pair's end
-                take(b, i, min(chunks(s.m - s.n + last) >> a.cost_shift, kPtBuckets - 1));
+                take(s, i, min(chunks(s.m - s.n + last) >> a.cost_shift, kPtBuckets - 1));
             }
         }
     };
-    walk([&](int, int, int cost) { atomicAdd(&hist[kPtBuckets - 1 - cost], 1); });
+    walk([&](const Sequence &, int, int cost) { atomicAdd(&hist[kPtBuckets - 1 - cost], 1); });
     __syncthreads();
     // where each bucket begins
     const int mine = hist[tid];
@@ -145,11 +149,86 @@ __global__ void __launch_bounds__(1024) attn_prompt_plan_kernel(const PromptArgs
     }
     hist[tid] = before + upto - mine;
     __syncthreads();
-    walk([&](int b, int i, int cost) {
+    walk([&](const Sequence &s, int i, int cost) {
         const int at = atomicAdd(&hist[kPtBuckets - 1 - cost], 1);
-        if (at < a.cap) a.list[at] = make_int2(b, i);                      // (offsets that do not ascend could name more)
+        if (at >= a.cap) return;                                           // (offsets that do not ascend could name more)
+        const Pair p = pair_of(a, s, i, 0);
+        a.list[2 * at] = make_int4(p.q0, p.tokens, p.k0, p.lim0);
+        a.list[2 * at + 1] = make_int4(p.n0, p.n1, 0, 0);
     });
     if (tid == 0) a.count[0] = min(all, a.cap), a.count[1] = 0;
+}
+
+// ---- or, for few pairs, every CTA by itself: the pairs of all sequences ranked by their chunks (equal ones in order, the same in every CTA),
+// (pair, key head) dealt out there and back.  The CTA's pairs to mine[0 ..], their number to *n.
+constexpr int kPtOwnPairs = 256, kPtOwnRounds = 16;
+struct OwnPlan {
+    int first[kPtOwnPairs + 1];               // of every sequence
+    int cost[kPtOwnPairs];
+    Pair mine[kPtOwnRounds];
+    int n;
+};
+__device__ __forceinline__ void plan_own(const PromptArgs &a, OwnPlan &w) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    Sequence s = {};
+    if (tid < a.B) {
+        s = sequence(a, tid);
+        w.first[tid + 1] = pairs_of(a, s);
+    }
+    if (tid == 0) w.n = 0;
+    __syncthreads();
+    if (tid < 32) {                           // running sums, 8 sequences a lane
+        int v[kPtOwnPairs / 32], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kPtOwnPairs / 32; ++i) {
+            const int b = lane * (kPtOwnPairs / 32) + i;
+            v[i] = sum += b < a.B ? w.first[b + 1] : 0;
+        }
+        int upto = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += x;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kPtOwnPairs / 32; ++i) {
+            const int b = lane * (kPtOwnPairs / 32) + i;
+            if (b < a.B) w.first[b + 1] = upto - sum + v[i];
+        }
+        if (lane == 0) w.first[0] = 0;
+    }
+    __syncthreads();
+    const int total = min(w.first[a.B], kPtOwnPairs);   // (offsets that do not ascend could name more)
+    Pair p = {};
+    if (tid < total) {
+        int lo = 0, hi = a.B;                 // first[lo] <= tid < first[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (w.first[mid] <= tid)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        s = sequence(a, lo);
+        p = pair_of(a, s, tid - w.first[lo], 0);
+        w.cost[tid] = p.most();
+    }
+    __syncthreads();
+    if (tid >= total) return;
+    int rank = tid;
+    const int grid = (int)gridDim.x;
+    if (total * a.kvh > grid) {
+        rank = 0;
+        for (int j = 0; j < total; ++j) rank += w.cost[j] > w.cost[tid] || (w.cost[j] == w.cost[tid] && j < tid);
+    }
+    for (int hk = 0; hk < a.kvh; ++hk) {
+        const int j = rank * a.kvh + hk, round = j / grid, at = j - round * grid;
+        if ((round & 1 ? grid - 1 - at : at) != (int)blockIdx.x || round >= kPtOwnRounds) continue;
+        p.hk = hk;
+        w.mine[round] = p;
+        atomicMax(&w.n, round + 1);           // (no round is left out before the last)
+    }
 }
 
 template <int D> struct PtCfg {
@@ -159,28 +238,29 @@ template <int D> struct PtCfg {
     static constexpr uint32_t kK = kQ + 2 * kTile;            // K [stage]
     static constexpr uint32_t kV = kK + kPtStages * kTile;    // V [stage]
     static constexpr uint32_t kSlot = kV + kPtStages * kTile;
-    static constexpr uint32_t kBar = kSlot + kPtSlots * sizeof(Pair);
+    static constexpr uint32_t kRow = kSlot + kPtSlots * sizeof(Pair);   // rows' maxima, sums [of either][tile][half][128]
+    static constexpr uint32_t kOwn = kRow + 2 * 2 * 2 * 128 * 4;
+    static constexpr uint32_t kBar = kOwn + (sizeof(OwnPlan) + 15) / 16 * 16;
     static constexpr uint32_t kBars = 48;
     static constexpr uint32_t kSmem = 1024 + kBar + kBars * 8;
 };
-static_assert(sizeof(Pair) % 8 == 0, "barriers follow");
+static_assert(sizeof(Pair) == 32, "two loads of 16 bytes");
 
-// 32 scores of a row as weights against its reference, packed; their sum joins l2.  EDGE: the first `left` are seen.
+// 32 scores of a row as weights against its reference, packed; their sums join la and lb.  EDGE: the first `left` are seen.  (Single
+// products and packed sums: 64 scores take one warp of a scheduler 354 clocks, two of them 493, which is the exponentials' 8 a clock;
+// packed products 412 and 543.)
 template <bool EDGE>
-__device__ __forceinline__ void weigh(const uint32_t *x, uint64_t cs2, uint64_t rf2, int left, uint32_t *y, uint64_t &l2) {
+__device__ __forceinline__ void weigh(const uint32_t *x, float cs, float rf, int left, uint32_t *y, uint64_t &la, uint64_t &lb) {
 #pragma unroll
     for (int e = 0; e < 32; e += 4) {
-        const uint64_t x0 = pk(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), x1 = pk(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
-        float s0, s1, s2, s3;
-        unpk(fma2(x0, cs2, rf2), s0, s1);
-        unpk(fma2(x1, cs2, rf2), s2, s3);
-        s0 = ex2(s0), s1 = ex2(s1), s2 = ex2(s2), s3 = ex2(s3);
-        if constexpr (EDGE) {
-            s0 = e < left ? s0 : 0.f, s1 = e + 1 < left ? s1 : 0.f;
-            s2 = e + 2 < left ? s2 : 0.f, s3 = e + 3 < left ? s3 : 0.f;
+        float s[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            s[i] = ex2(fmaf(__uint_as_float(x[e + i]), cs, rf));
+            if constexpr (EDGE) s[i] = e + i < left ? s[i] : 0.f;
         }
-        l2 = add2(l2, add2(pk(s0, s1), pk(s2, s3)));
-        y[e / 2] = pack_bf16(s0, s1), y[e / 2 + 1] = pack_bf16(s2, s3);
+        la = add2(la, pk(s[0], s[1])), lb = add2(lb, pk(s[2], s[3]));
+        y[e / 2] = pack_bf16(s[0], s[1]), y[e / 2 + 1] = pack_bf16(s[2], s[3]);
     }
 }
 // The largest of the first `left` of 32 scores, in log2 units.
@@ -191,6 +271,19 @@ __device__ __forceinline__ float largest(const uint32_t *x, float cs, int left) 
     return m;
 }
 __device__ __forceinline__ bool not_finite(uint32_t w) { return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u; }
+// Two bf16: acc + 0 x w, NaN from the first that is not finite on.
+__device__ __forceinline__ uint32_t add_none(uint32_t w, uint32_t acc) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(w), "r"(0u), "r"(acc));
+    return d;
+}
+
+// 32 bytes at a multiple of 32.
+__device__ __forceinline__ void st32(void *to, const uint32_t *v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
+                 "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
 
 template <int D>
 __global__ void __launch_bounds__(kPtThreads, 1)
@@ -203,8 +296,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     Pair *slots = reinterpret_cast<Pair *>(sm + C::kSlot);
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + C::kBar);
     uint64_t *slot_full = bars, *slot_empty = bars + 4;                                              // [slot]
-    uint64_t *q_full = bars + 8, *q_empty = bars + 10, *s_full = bars + 12, *o_half = bars + 14;     // [tile]
-    uint64_t *o_full = bars + 16, *o_empty = bars + 18, *p_full = bars + 20;                         // [tile], [tile], [tile][half]
+    uint64_t *q_full = bars + 8, *q_empty = bars + 10, *s_full = bars + 12, *p_full = bars + 14;     // [tile]
+    uint64_t *o_full = bars + 16, *o_empty = bars + 18;                                              // [tile]
     uint64_t *k_full = bars + 24, *k_empty = bars + 26, *v_full = bars + 28, *v_empty = bars + 30, *v_clean = bars + 32;   // [stage]
     uint64_t *drain = bars + 34;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 35);
@@ -214,9 +307,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kPtSlots; ++i) mbar_init(&slot_full[i], 1), mbar_init(&slot_empty[i], kPtUsers);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], 1), mbar_init(&s_full[i], 1), mbar_init(&o_half[i], 1);
-            mbar_init(&o_full[i], 1), mbar_init(&o_empty[i], 4);
-            mbar_init(&p_full[2 * i], 4), mbar_init(&p_full[2 * i + 1], 4);
+            mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], 1), mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 8);
+            mbar_init(&o_full[i], 1), mbar_init(&o_empty[i], 8);
         }
         for (int i = 0; i < kPtStages; ++i) {
             mbar_init(&k_full[i], 1), mbar_init(&k_empty[i], 1);
@@ -226,12 +318,18 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         *bad = 0;
         fence_barrier_init();
     }
+    if (warp == 17 && lane < 3) {
+        const CUtensorMap *m = lane == 0 ? &mq : lane == 1 ? &mk : &mv;
+        asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+    }
     // the predecessor first, the tensor memory then: held while waiting it could be what a predecessor's CTA on this SM waits for
     pdl_wait();
-    if (warp == 8) {
+    if (warp == 16) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
+    OwnPlan &own = *reinterpret_cast<OwnPlan *>(sm + C::kOwn);
+    if (!a.list) plan_own(a, own);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -250,46 +348,25 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         if (lane == 0) mbar_arrive(&slot_empty[i % kPtSlots]);
     };
 
-    if (warp == 9) {
+    if (warp == 17) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPtRegsRest));
         // ---- the pairs, and their loads (the whole warp walks along; one lane issues)
-        int kc = 0, nq[2] = {0, 0}, total = 1, next = 0;
+        int kc = 0, nq[2] = {0, 0}, next = (int)blockIdx.x;
+        const int total = a.list ? a.count[0] * a.kvh : own.n;
         bool ok = true;
-        if (a.list) {
-            total = a.count[0] * a.kvh;
-            if (lane == 0) next = atomicAdd(&a.count[1], 1);
-            next = __shfl_sync(0xffffffffu, next, 0);
-        }
-        for (int it = 0; ok; ++it) {
-            Pair p;
+        // pair `i` of the list, or of this CTA's own
+        auto pair_no = [&](int i) {
+            Pair p = {};
             p.hk = -1;
-            if (a.list) {
-                if (next < total) {
-                    const int2 e = a.list[next / a.kvh];
-                    p = pair_of(a, e.x, e.y, next % a.kvh);
-                }
-            } else if (it == 0) {
-                // pair blockIdx.x / kvh of all sequences' pairs: 32 sequences a step, the running sum across the lanes
-                const int want = (int)blockIdx.x / a.kvh;
-                int sum = 0;
-                for (int b0 = 0; b0 < a.B; b0 += 32) {
-                    int n = 0;
-                    if (b0 + lane < a.B) n = pairs_of(a, sequence(a, b0 + lane));
-                    int upto = n;
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const int v = __shfl_up_sync(0xffffffffu, upto, o);
-                        if (lane >= o) upto += v;
-                    }
-                    const uint32_t over = __ballot_sync(0xffffffffu, sum + upto > want);
-                    if (over) {
-                        const int at = __ffs(over) - 1;
-                        p = pair_of(a, b0 + at, want - sum - __shfl_sync(0xffffffffu, upto - n, at), (int)blockIdx.x % a.kvh);
-                        break;
-                    }
-                    sum += __shfl_sync(0xffffffffu, upto, 31);
-                }
-            }
+            if (i >= total) return p;
+            if (!a.list) return own.mine[i];
+            const int4 u = a.list[2 * (i / a.kvh)], v = a.list[2 * (i / a.kvh) + 1];
+            p.q0 = u.x, p.tokens = u.y, p.k0 = u.z, p.lim0 = u.w, p.n0 = v.x, p.n1 = v.y;
+            p.hk = i % a.kvh;
+            return p;
+        };
+        Pair p = pair_no(a.list ? next : 0);
+        for (int it = 0; ok; ++it) {
             if (it >= kPtSlots) ok = wt_wait(&slot_empty[it % kPtSlots], (uint32_t)(it / kPtSlots + 1) & 1u, bad);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
@@ -299,8 +376,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             }
             __syncwarp();
             if (p.hk < 0) break;
-            if (a.list && lane == 0) next = atomicAdd(&a.count[1], 1);     // in flight under this pair's loads
-            const int n = max(p.n[0], p.n[1]);
+            if (a.list && lane == 0) next = (int)gridDim.x + atomicAdd(&a.count[1], 1);     // in flight under this pair's loads
+            const int n = p.most();
             for (int c = 0; ok && c < n; ++c, ++kc) {
                 const int st = kc % kPtStages;
                 const uint32_t was = (uint32_t)(kc / kPtStages + 1) & 1u;
@@ -314,23 +391,24 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     __syncwarp();
                 };
                 auto load_q = [&](int h) {
-                    if (p.n[h] == 0) return;
+                    if (p.n(h) == 0) return;
                     if (nq[h] > 0) ok = ok && wt_wait(&q_empty[h], (uint32_t)(nq[h] + 1) & 1u, bad);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) return;
                     load(&mq, C::kQ + h * C::kTile, &q_full[h], (uint32_t)(KB * a.tpt * a.G * 128), p.hk * a.G, p.q0 + h * a.tpt);
                     ++nq[h];
                 };
-                if (c == 0) load_q(p.n[0] ? 0 : 1);
+                if (c == 0) load_q(p.n0 ? 0 : 1);
                 if (kc >= kPtStages) ok = ok && wt_wait(&k_empty[st], was, bad);
                 ok = __all_sync(0xffffffffu, ok);
                 if (ok) load(&mk, C::kK + st * C::kTile, &k_full[st], C::kTile, p.hk, key);
-                if (c == 0 && p.n[0]) load_q(1);
+                if (c == 0 && p.n0) load_q(1);
                 if (kc >= kPtStages) ok = ok && wt_wait(&v_empty[st], was, bad);
                 ok = __all_sync(0xffffffffu, ok);
                 if (ok) load(&mv, C::kV + st * C::kTile, &v_full[st], C::kTile, p.hk, key);
             }
             next = __shfl_sync(0xffffffffu, next, 0);
+            if (ok) p = pair_no(a.list ? next : it + 1);
         }
         // copies in flight land before the CTA may end (they have, unless a wait expired)
         if (!ok) {
@@ -342,7 +420,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 (void)mbar_wait_bounded(&v_full[i], (uint32_t)(uses + 1) & 1u, 20000000ull);
             }
         }
-    } else if (warp == 8) {
+    } else if (warp == 16) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPtRegsRest));
         // ---- the MMAs: always a tile's O followed by its next S, which may be the next pair's first
         constexpr uint32_t base = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(128 >> 4) << 24);
@@ -366,7 +444,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             tc_fence_after();
             const uint32_t d = tm + kPtS + 128u * h;
             const uint64_t q = dQ + h * KB * kBox16, k = dK + st * KB * kBox16;
-            const bool last_k = h == 1 || x.n[1] <= c;      // nobody needs this K after it
+            const bool last_k = h == 1 || x.n1 <= c;      // nobody needs this K after it
             if (elect_one()) {
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb)
@@ -375,7 +453,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                         tc_mma(d, q + kb * kBox16 + 2 * s, k + kb * kBox16 + 2 * s, idesc_s, (kb | s) ? 1u : 0u);
                 tc_commit(&s_full[h]);
                 if (last_k) tc_commit(&k_empty[st]);
-                if (c + 1 == x.n[h]) tc_commit(&q_empty[h]);
+                if (c + 1 == x.n(h)) tc_commit(&q_empty[h]);
             }
             __syncwarp();
         };
@@ -389,43 +467,38 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             const uint32_t d = tm + kPtO + 128u * h, pt = tm + kPtS + 128u * h;
             const uint64_t v = dV + st * KB * kBox16;
             ok = ok && wt_wait(&v_full[st], ph, bad) && wt_wait(&v_clean[st], ph, bad);
-            for (int half = 0; half < 2; ++half) {
-                ok = ok && wt_wait(&p_full[2 * h + half], np[h] & 1u, bad);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) return;
-                tc_fence_after();
-                if (elect_one()) {
+            ok = ok && wt_wait(&p_full[h], np[h] & 1u, bad);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) return;
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        tc_mma_ts(d, pt + 32u * half + 8u * i, v + (4 * half + i) * 128, idesc_o, (c | half | i) ? 1u : 0u);
-                    if (half == 0) {
-                        tc_commit(&o_half[h]);
-                    } else {
-                        if (h == 1 || p.n[1] <= c) tc_commit(&v_empty[st]);
-                        if (c + 1 == p.n[h]) tc_commit(&o_full[h]);
-                    }
-                }
-                __syncwarp();
+                for (int i = 0; i < kPtKeys / 16; ++i) tc_mma_ts(d, pt + 8u * i + 32u * (i >> 2), v + i * 128, idesc_o, (c | i) ? 1u : 0u);
+                if (h == 1 || p.n1 <= c) tc_commit(&v_empty[st]);
+                if (c + 1 == p.n(h)) tc_commit(&o_full[h]);
             }
+            __syncwarp();
             ++np[h];
         };
         for (int it = 0; ok && p.hk >= 0; ++it) {
-            const int n = max(p.n[0], p.n[1]);
+            const int n = p.most();
+#pragma unroll
             for (int h = 0; h < 2; ++h)
-                if (ok && !begun[h] && p.n[h] > 0) issue_s(h, 0, p, kc);
+                if (ok && !begun[h] && p.n(h) > 0) issue_s(h, 0, p, kc);
             begun[0] = begun[1] = false;
             Pair x;
             x.hk = -2;                              // the next pair: not known yet
             for (int c = 0; ok && c < n; ++c)
+#pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    if (!ok || c >= p.n[h]) continue;
+                    if (!ok || c >= p.n(h)) continue;
                     issue_o(h, c);
-                    if (!ok) break;
-                    if (c + 1 < p.n[h]) {
+                    if (!ok) continue;
+                    if (c + 1 < p.n(h)) {
                         issue_s(h, c + 1, p, kc);
                     } else {
                         if (x.hk == -2) x = pair_at(it + 1);
-                        if (x.hk >= 0 && x.n[h] > 0) {
+                        if (x.hk >= 0 && x.n(h) > 0) {
                             issue_s(h, 0, x, kc + n);
                             begun[h] = true;
                         }
@@ -440,7 +513,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         if (elect_one()) tc_commit(drain);
         (void)mbar_wait_bounded(drain, 0u, 20000000ull);
         __syncwarp();
-    } else if (warp >= 10) {
+    } else if (warp >= 18) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPtRegsRest));
         // ---- V of chunks that some rows see in part: what is not finite becomes zero, and is noted
         int kc = 0;
@@ -448,30 +521,32 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         for (int it = 0; ok; ++it) {
             Pair p = pair_at(it);
             if (p.hk < 0) break;
-            const int n = max(p.n[0], p.n[1]), edge = first_edge(p);
+            const int n = p.most(), edge = first_edge(p);
             for (int c = 0; ok && c < n; ++c, ++kc) {
                 const int st = kc % kPtStages;
                 ok = wt_wait(&v_full[st], (uint32_t)(kc / kPtStages) & 1u, bad);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 if (c >= edge) {
-                    uint4 *tile = reinterpret_cast<uint4 *>(sm + C::kV + st * C::kTile);
+                    uint4 *tile = reinterpret_cast<uint4 *>(sm + C::kV + st * C::kTile) + (warp - 18) * 32 + lane;
                     constexpr int kPieces = KB * 128 * 8;
-                    bool odd = false;
-#pragma unroll 4
-                    for (int i = (warp - 10) * 32 + lane; i < kPieces; i += 64) {
-                        uint4 u = tile[i];
-                        if (not_finite(u.x) || not_finite(u.y) || not_finite(u.z) || not_finite(u.w)) {
-                            odd = true;
+                    uint32_t acc[4] = {0, 0, 0, 0};
+#pragma unroll 8
+                    for (int i = 0; i < kPieces; i += 64) {
+                        const uint4 u = tile[i];
+                        acc[0] = add_none(u.x, acc[0]), acc[1] = add_none(u.y, acc[1]);
+                        acc[2] = add_none(u.z, acc[2]), acc[3] = add_none(u.w, acc[3]);
+                    }
+                    if (not_finite(acc[0]) || not_finite(acc[1]) || not_finite(acc[2]) || not_finite(acc[3])) {
+                        for (int i = 0; i < kPieces; i += 64) {
                             auto keep = [](uint32_t w) {
                                 if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
                                 if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
                                 return w;
                             };
+                            const uint4 u = tile[i];
                             tile[i] = make_uint4(keep(u.x), keep(u.y), keep(u.z), keep(u.w));
                         }
-                    }
-                    if (odd) {
                         fence_proxy_async_smem();
                         atomicOr(&slot_of(it).odd, 1u << (c - edge));
                     }
@@ -483,18 +558,19 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPtRegsSoft));
-        // ---- softmax: tile h, row r of it
-        const int h = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+        // ---- softmax: tile h, row r of it, the keys' half kh of every chunk; the two warps that share rows keep one reference
+        const int h = warp >> 3, kh = (warp >> 2) & 1, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        const uint32_t tS = tmem + kPtS + 128u * h + lanes, tO = tmem + kPtO + 128u * h + lanes;
-        const int token = r / a.G, head = r - token * a.G;
+        const uint32_t tS = tmem + kPtS + 128u * h + 64u * kh + lanes, tO = tmem + kPtO + 128u * h + lanes;
+        const int token = r / a.G, head = r - token * a.G, pair_bar = 1 + h * 4 + quarter;
+        float *row_max = reinterpret_cast<float *>(sm + C::kRow) + (h * 2) * 128 + r, *row_sum = row_max + 4 * 128;
         const bool in_tile = token < a.tpt;
         uint32_t ns = 0, no = 0;                    // S's, O's so far
         bool ok = true;
         for (int it = 0; ok; ++it) {
             const Pair p = pair_at(it);
             if (p.hk < 0) break;
-            const int tt = h * a.tpt + token, n = p.n[h];
+            const int tt = h * a.tpt + token, n = p.n(h);
             const bool live = in_tile && tt < p.tokens;
             // rows without a token see what the tile's last one does
             const int lim = p.lim0 + (live ? tt : min(p.tokens, (h + 1) * a.tpt) - 1);
@@ -504,75 +580,79 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 ok = ok && wt_wait(&s_full[h], ns & 1u, bad);
                 ++ns;
                 tc_fence_after();
-                const int left = lim - c * kPtKeys;
-                const bool edge = lim_all < (c + 1) * kPtKeys;
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int here = left - 64 * q;
-                    uint32_t x[64], y[32];
-                    ld32_start(tS + 64u * q, x);
-                    ld32_start(tS + 64u * q + 32u, x + 32);
-                    tc_wait_ld_u32<64>(x);
-                    const bool first = q == 0 && c == 0;
-                    if (first) ref = fmaxf(largest(x, a.scale2, here), largest(x + 32, a.scale2, here - 32));
-                    float sum;
-                    auto weigh_all = [&](const uint32_t *z) {
-                        const float rf = ref == -INFINITY ? 0.f : -ref;
-                        const uint64_t cs2 = pk(a.scale2, a.scale2), rf2 = pk(rf, rf);
-                        uint64_t l2 = pk(0.f, 0.f);
-                        if (edge) {
-                            weigh<true>(z, cs2, rf2, here, y, l2);
-                            weigh<true>(z + 32, cs2, rf2, here - 32, y + 16, l2);
-                        } else {
-                            weigh<false>(z, cs2, rf2, here, y, l2);
-                            weigh<false>(z + 32, cs2, rf2, here - 32, y + 16, l2);
-                        }
-                        float l0, l1;
-                        unpk(l2, l0, l1);
-                        sum = l0 + l1;
-                    };
-                    weigh_all(x);
-                    if (!first && __any_sync(0xffffffffu, live && (sum > kPtTop || (ref == -INFINITY && here > 0)))) {
-                        uint32_t z[64];             // the scores again: they stand until their weights are written
-                        ld32_start(tS + 64u * q, z);
-                        ld32_start(tS + 64u * q + 32u, z + 32);
-                        tc_wait_ld_u32<64>(z);
-                        const float m = fmaxf(largest(z, a.scale2, here), largest(z + 32, a.scale2, here - 32));
+                const int left = lim - c * kPtKeys - 64 * kh;
+                const bool edge = lim_all < c * kPtKeys + 64 * kh + 64;
+                uint32_t x[64], y[32];
+                float sum;
+                auto largest_all = [&]() { return fmaxf(largest(x, a.scale2, left), largest(x + 32, a.scale2, left - 32)); };
+                // the largest of both warps' scores
+                auto largest_row = [&]() {
+                    const float m = largest_all();
+                    row_max[kh * 128] = m;
+                    named_sync(pair_bar, 64);
+                    return fmaxf(m, row_max[(kh ^ 1) * 128]);
+                };
+                auto weigh_all = [&](bool split) {
+                    const float rf = ref == -INFINITY ? 0.f : -ref;
+                    uint64_t la = pk(0.f, 0.f), lb = la;
+                    if (edge)
+                        weigh<true>(x, a.scale2, rf, left, y, la, lb);
+                    else
+                        weigh<false>(x, a.scale2, rf, left, y, la, lb);
+                    if (split) tc_wait_ld_u32<32>(x + 32);
+                    if (edge)
+                        weigh<true>(x + 32, a.scale2, rf, left - 32, y + 16, la, lb);
+                    else
+                        weigh<false>(x + 32, a.scale2, rf, left, y + 16, la, lb);
+                    float l0, l1;
+                    unpk(add2(la, lb), l0, l1);
+                    sum = l0 + l1;
+                };
+                tc_ld32_nowait(tS, x);
+                tc_wait_ld_u32<32>(x);
+                tc_ld32_nowait(tS + 32u, x + 32);
+                if (c == 0) {
+                    tc_wait_ld_u32<32>(x + 32);
+                    ref = largest_row();
+                    weigh_all(false);
+                } else {
+                    weigh_all(true);
+                    if (named_sync_or(pair_bar, 64, live && (sum > kPtTop || (ref == -INFINITY && left > 0)))) {
+                        tc_ld32_nowait(tS, x);      // the scores again: they stand until their weights are written
+                        tc_ld32_nowait(tS + 32u, x + 32);
+                        tc_wait_ld_u32<64>(x);
+                        const float m = largest_row();
                         float f = 1.f;
                         if (m > ref) {
                             f = ref == -INFINITY ? 0.f : ex2(ref - m);
                             ref = m;
                             l *= f;
                         }
-                        // O holds the chunks before, whose products this S came behind, and this chunk's first half
-                        if (q == 1) {
-                            ok = ok && wt_wait(&o_half[h], (ns - 1) & 1u, bad);
-                            tc_fence_after();
-                        }
-                        if (c > 0 || q > 0) {
+                        // O holds the chunks before, whose products this S came behind; half its columns each
 #pragma unroll 1
-                            for (int i = 0; i < D / 32; ++i) {
-                                uint32_t u[32];
-                                ld32_start(tO + 32u * i, u);
-                                tc_wait_ld_u32<32>(u);
+                        for (int i = 0; i < D / 32; ++i) {
+                            const uint32_t at = tO + (uint32_t)(kh * (D / 2) + 16 * i);
+                            uint32_t u[16];
+                            tc_ld16_nowait(at, u);
+                            tc_wait_ld_u32<16>(u);
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * f);
-                                tc_st16(tO + 32u * i, u);
-                                tc_st16(tO + 32u * i + 16u, u + 16);
-                            }
+                            for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * f);
+                            tc_st16(at, u);
                         }
-                        weigh_all(z);
+                        weigh_all(false);
                     }
-                    l += sum;
-                    tc_st16(tS + 32u * q, y);
-                    tc_st16(tS + 32u * q + 16u, y + 16);
-                    tc_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&p_full[2 * h + q]);
                 }
+                l += sum;
+                tc_st32(tS, y);
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[h]);
             }
-            // ---- the rows' results
+            // ---- the rows' results, half their dims each
+            row_sum[kh * 128] = l;
+            named_sync(pair_bar, 64);
+            l = row_sum[0] + row_sum[128];
             if (n > 0) {
                 ok = ok && wt_wait(&o_full[h], no & 1u, bad);
                 ++no;
@@ -583,12 +663,13 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             // no key gives zeros; keys whose scores are all -infinity NaN, as the formula does
             const float by = (lim <= 0 ? 0.f : l == 0.f ? __uint_as_float(0x7fc00000u) : 1.f / l) + fail;
             const uint32_t odd = n > 0 ? *reinterpret_cast<volatile uint32_t *>(&slot_of(it).odd) : 0u;
-            uint8_t *dst = a.out + (int64_t)(p.q0 + tt) * a.o_token + (int64_t)(p.hk * a.G + head) * (2 * D);
+            uint8_t *dst = a.out + (int64_t)(p.q0 + tt) * a.o_token + (int64_t)(p.hk * a.G + head) * (2 * D) + kh * D;
 #pragma unroll 1
-            for (int i = 0; i < D / 32; ++i) {
+            for (int i = 0; i < D / 64; ++i) {
+                const int d0 = kh * (D / 2) + 32 * i;
                 uint32_t u[32];
                 if (n > 0) {
-                    ld32_start(tO + 32u * i, u);
+                    tc_ld32_nowait(tO + (uint32_t)d0, u);
                     tc_wait_ld_u32<32>(u);
                 } else {
 #pragma unroll
@@ -600,7 +681,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                         if (!((odd >> k) & 1u)) continue;
                         const int j0 = (first_edge(p) + k) * kPtKeys, j1 = min(lim, j0 + kPtKeys);
                         for (int j = j0; live && j < j1; ++j) {
-                            const uint16_t *v = reinterpret_cast<const uint16_t *>(a.v + (int64_t)(p.k0 + j) * a.v_token) + p.hk * D + 32 * i;
+                            const uint16_t *v = reinterpret_cast<const uint16_t *>(a.v + (int64_t)(p.k0 + j) * a.v_token) + p.hk * D + d0;
 #pragma unroll
                             for (int e = 0; e < 32; ++e) {
                                 const uint32_t w = (uint32_t)v[e] << 16;
@@ -613,9 +694,14 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     uint32_t o[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) o[e] = pack_bf16(__uint_as_float(u[2 * e]) * by, __uint_as_float(u[2 * e + 1]) * by);
+                    if (a.wide_out) {               // whole sectors
+                        st32(dst + 64 * i, o);
+                        st32(dst + 64 * i + 32, o + 8);
+                    } else {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        *reinterpret_cast<uint4 *>(dst + 64 * i + 16 * e) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        for (int e = 0; e < 4; ++e)
+                            *reinterpret_cast<uint4 *>(dst + 64 * i + 16 * e) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    }
                 }
             }
             if (n > 0) {
@@ -629,7 +715,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 8) tmem_dealloc(tmem, 512);
+    if (warp == 16) tmem_dealloc(tmem, 512);
 }
 
 template <typename F, typename... A>
@@ -682,9 +768,9 @@ qd_status plan_prompt(int n_tokens, int n_kv_tokens, int n_seqs, int n_q_heads, 
     if (pairs * n_kv_heads > (1 << 30)) return QD_EUNSUPPORTED;
     const int sms = sms_of(dev);
     p->cap = (int)pairs;
-    p->list = pairs * n_kv_heads > sms;
+    p->list = pairs > kPtOwnPairs || n_seqs > kPtOwnPairs || pairs * n_kv_heads > (int64_t)kPtOwnRounds * sms;
     p->ctas = (unsigned)std::min<int64_t>(pairs * n_kv_heads, sms);
-    p->bytes = p->list ? 256 + (size_t)pairs * sizeof(int2) : 0;
+    p->bytes = p->list ? 256 + (size_t)pairs * 32 : 0;
     return QD_OK;
 }
 
@@ -744,10 +830,11 @@ qd_status qd_attn_prompt(const void *q_dev, int64_t q_stride, const void *k_dev,
     a.v_token = v_stride * 2, a.o_token = out_stride * 2;
     a.offsets = offsets_dev, a.kv_offsets = kv_offsets_dev ? kv_offsets_dev : offsets_dev;
     a.N = n_tokens, a.M = n_kv_tokens, a.B = n_seqs, a.G = n_q_heads / n_kv_heads, a.kvh = n_kv_heads;
+    a.wide_out = is_aligned(out_dev, 32) && (n_tokens == 1 || out_stride % 16 == 0);
     a.tpt = p.tpt, a.scale2 = scale * 1.4426950408889634f;
     if (p.list) {
         a.count = static_cast<int *>(workspace_dev);
-        a.list = reinterpret_cast<int2 *>(static_cast<uint8_t *>(workspace_dev) + 256);
+        a.list = reinterpret_cast<int4 *>(static_cast<uint8_t *>(workspace_dev) + 256);
         a.cap = p.cap;
         while ((n_kv_tokens / kPtKeys + 1) >> a.cost_shift >= kPtBuckets) ++a.cost_shift;
     }
