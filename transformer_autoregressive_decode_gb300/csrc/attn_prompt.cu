@@ -163,8 +163,9 @@ __global__ void __launch_bounds__(1024) attn_prompt_plan_kernel(const PromptArgs
 // (pair, key head) dealt out there and back.  The CTA's pairs to mine[0 ..], their number to *n.
 constexpr int kPtOwnPairs = 256, kPtOwnRounds = 16;
 struct OwnPlan {
+    int cost[kPtOwnPairs];                    // read 16 at a time
     int first[kPtOwnPairs + 1];               // of every sequence
-    int cost[kPtOwnPairs];
+    int pad[3];
     Pair mine[kPtOwnRounds];
     int n;
 };
@@ -176,6 +177,7 @@ __device__ __forceinline__ void plan_own(const PromptArgs &a, OwnPlan &w) {
         w.first[tid + 1] = pairs_of(a, s);
     }
     if (tid == 0) w.n = 0;
+    if (tid < kPtOwnPairs) w.cost[tid] = -1;
     __syncthreads();
     if (tid < 32) {                           // running sums, 8 sequences a lane
         int v[kPtOwnPairs / 32], sum = 0;
@@ -220,14 +222,23 @@ __device__ __forceinline__ void plan_own(const PromptArgs &a, OwnPlan &w) {
     const int grid = (int)gridDim.x;
     if (total * a.kvh > grid) {
         rank = 0;
-        for (int j = 0; j < total; ++j) rank += w.cost[j] > w.cost[tid] || (w.cost[j] == w.cost[tid] && j < tid);
+        const int own = p.most();
+        const int4 *cost = reinterpret_cast<const int4 *>(w.cost);
+#pragma unroll 4
+        for (int j = 0; j < total; j += 4) {  // (what stands past `total` is below every cost)
+            const int4 c = cost[j / 4];
+            rank += (c.x > own || (c.x == own && j < tid)) + (c.y > own || (c.y == own && j + 1 < tid)) +
+                    (c.z > own || (c.z == own && j + 2 < tid)) + (c.w > own || (c.w == own && j + 3 < tid));
+        }
     }
+    int round = rank * a.kvh / grid, at = rank * a.kvh - round * grid;
     for (int hk = 0; hk < a.kvh; ++hk) {
-        const int j = rank * a.kvh + hk, round = j / grid, at = j - round * grid;
-        if ((round & 1 ? grid - 1 - at : at) != (int)blockIdx.x || round >= kPtOwnRounds) continue;
-        p.hk = hk;
-        w.mine[round] = p;
-        atomicMax(&w.n, round + 1);           // (no round is left out before the last)
+        if ((round & 1 ? grid - 1 - at : at) == (int)blockIdx.x && round < kPtOwnRounds) {
+            p.hk = hk;
+            w.mine[round] = p;
+            atomicMax(&w.n, round + 1);       // (no round is left out before the last)
+        }
+        if (++at == grid) at = 0, ++round;
     }
 }
 
@@ -263,11 +274,11 @@ __device__ __forceinline__ void weigh(const uint32_t *x, float cs, float rf, int
         y[e / 2] = pack_bf16(s[0], s[1]), y[e / 2 + 1] = pack_bf16(s[2], s[3]);
     }
 }
-// The largest of the first `left` of 32 scores, in log2 units.
-__device__ __forceinline__ float largest(const uint32_t *x, float cs, int left) {
+// The largest of the first `left` of N scores, in log2 units.
+template <int N> __device__ __forceinline__ float largest(const uint32_t *x, float cs, int left) {
     float m = -INFINITY;
 #pragma unroll
-    for (int e = 0; e < 32; ++e) m = fmaxf(m, e < left ? __uint_as_float(x[e]) * cs : -INFINITY);
+    for (int e = 0; e < N; ++e) m = fmaxf(m, e < left ? __uint_as_float(x[e]) * cs : -INFINITY);
     return m;
 }
 __device__ __forceinline__ bool not_finite(uint32_t w) { return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u; }
@@ -584,10 +595,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 const bool edge = lim_all < c * kPtKeys + 64 * kh + 64;
                 uint32_t x[64], y[32];
                 float sum;
-                auto largest_all = [&]() { return fmaxf(largest(x, a.scale2, left), largest(x + 32, a.scale2, left - 32)); };
-                // the largest of both warps' scores
-                auto largest_row = [&]() {
-                    const float m = largest_all();
+                // the larger of both warps' largest scores
+                auto of_row = [&](float m) {
                     row_max[kh * 128] = m;
                     named_sync(pair_bar, 64);
                     return fmaxf(m, row_max[(kh ^ 1) * 128]);
@@ -611,17 +620,15 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 tc_ld32_nowait(tS, x);
                 tc_wait_ld_u32<32>(x);
                 tc_ld32_nowait(tS + 32u, x + 32);
-                if (c == 0) {
-                    tc_wait_ld_u32<32>(x + 32);
-                    ref = largest_row();
-                    weigh_all(false);
-                } else {
+                // the first chunk: 16 scores of either warp set the reference, which is near enough as a rule
+                if (c == 0) ref = of_row(largest<16>(x, a.scale2, left));
+                {
                     weigh_all(true);
                     if (named_sync_or(pair_bar, 64, live && (sum > kPtTop || (ref == -INFINITY && left > 0)))) {
                         tc_ld32_nowait(tS, x);      // the scores again: they stand until their weights are written
                         tc_ld32_nowait(tS + 32u, x + 32);
                         tc_wait_ld_u32<64>(x);
-                        const float m = largest_row();
+                        const float m = of_row(largest<64>(x, a.scale2, left));
                         float f = 1.f;
                         if (m > ref) {
                             f = ref == -INFINITY ? 0.f : ex2(ref - m);
@@ -630,7 +637,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                         }
                         // O holds the chunks before, whose products this S came behind; half its columns each
 #pragma unroll 1
-                        for (int i = 0; i < D / 32; ++i) {
+                        for (int i = 0; c > 0 && i < D / 32; ++i) {
                             const uint32_t at = tO + (uint32_t)(kh * (D / 2) + 16 * i);
                             uint32_t u[16];
                             tc_ld16_nowait(at, u);
@@ -664,36 +671,40 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             const float by = (lim <= 0 ? 0.f : l == 0.f ? __uint_as_float(0x7fc00000u) : 1.f / l) + fail;
             const uint32_t odd = n > 0 ? *reinterpret_cast<volatile uint32_t *>(&slot_of(it).odd) : 0u;
             uint8_t *dst = a.out + (int64_t)(p.q0 + tt) * a.o_token + (int64_t)(p.hk * a.G + head) * (2 * D) + kh * D;
+            uint32_t u[D / 2];
+            if (n > 0) {
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) tc_ld32_nowait(tO + (uint32_t)(kh * (D / 2) + 32 * i), u + 32 * i);
+                tc_wait_ld_u32<D / 2>(u);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&o_empty[h]);        // the next pair's products may begin
+            } else {
+#pragma unroll
+                for (int e = 0; e < D / 2; ++e) u[e] = 0;
+            }
+            if (odd) {
+                // the values that were taken out, by the rows that see them
 #pragma unroll 1
-            for (int i = 0; i < D / 64; ++i) {
-                const int d0 = kh * (D / 2) + 32 * i;
-                uint32_t u[32];
-                if (n > 0) {
-                    tc_ld32_nowait(tO + (uint32_t)d0, u);
-                    tc_wait_ld_u32<32>(u);
-                } else {
+                for (int k = 0; k < 32; ++k) {
+                    if (!((odd >> k) & 1u)) continue;
+                    const int j0 = (first_edge(p) + k) * kPtKeys, j1 = min(lim, j0 + kPtKeys);
+                    for (int j = j0; live && j < j1; ++j) {
+                        const uint16_t *v = reinterpret_cast<const uint16_t *>(a.v + (int64_t)(p.k0 + j) * a.v_token) + p.hk * D + kh * (D / 2);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) u[e] = 0;
-                }
-                if (odd) {
-                    // the values that were taken out, by the rows that see them
-                    for (int k = 0; k < 32; ++k) {
-                        if (!((odd >> k) & 1u)) continue;
-                        const int j0 = (first_edge(p) + k) * kPtKeys, j1 = min(lim, j0 + kPtKeys);
-                        for (int j = j0; live && j < j1; ++j) {
-                            const uint16_t *v = reinterpret_cast<const uint16_t *>(a.v + (int64_t)(p.k0 + j) * a.v_token) + p.hk * D + d0;
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const uint32_t w = (uint32_t)v[e] << 16;
-                                if ((w & 0x7f800000u) == 0x7f800000u) u[e] = __float_as_uint(__uint_as_float(u[e]) + __uint_as_float(w));
-                            }
+                        for (int e = 0; e < D / 2; ++e) {
+                            const uint32_t w = (uint32_t)v[e] << 16;
+                            if ((w & 0x7f800000u) == 0x7f800000u) u[e] = __float_as_uint(__uint_as_float(u[e]) + __uint_as_float(w));
                         }
                     }
                 }
-                if (live) {
+            }
+            if (live) {
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) {
                     uint32_t o[16];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = pack_bf16(__uint_as_float(u[2 * e]) * by, __uint_as_float(u[2 * e + 1]) * by);
+                    for (int e = 0; e < 16; ++e) o[e] = pack_bf16(__uint_as_float(u[32 * i + 2 * e]) * by, __uint_as_float(u[32 * i + 2 * e + 1]) * by);
                     if (a.wide_out) {               // whole sectors
                         st32(dst + 64 * i, o);
                         st32(dst + 64 * i + 32, o + 8);
@@ -703,11 +714,6 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                             *reinterpret_cast<uint4 *>(dst + 64 * i + 16 * e) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                     }
                 }
-            }
-            if (n > 0) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&o_empty[h]);
             }
             done_with(it);
         }
