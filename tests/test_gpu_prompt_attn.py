@@ -92,9 +92,41 @@ def test_many_pairs(qd, lens, klens, qh, kvh, hd):
     N, M = st["q"].shape[0], st["k"].shape[0]
     pairs = N // (2 * (128 // (qh // kvh))) + len(lens)
     sms = torch.cuda.get_device_properties(0).multi_processor_count
-    assert (qd.qd_attn_prompt_workspace(N, M, len(lens), qh, kvh, hd) > 0) == (pairs > 256 or len(lens) > 256 or pairs * kvh > 16 * sms)
+    listed = pairs > 256 or len(lens) > 256 or pairs * kvh > 16 * sms
+    cut = not listed and pairs * kvh <= sms + sms // 4 and M >= 2048 * len(lens)      # may be cut into pieces
+    assert (qd.qd_attn_prompt_workspace(N, M, len(lens), qh, kvh, hd) > 0) == (listed or cut)
     call(qd, st)
     check(st)
+
+
+@pytest.mark.parametrize("lens, klens, qh, kvh, hd", [
+    ([3000], None, 1, 1, 128), ([5000], None, 2, 2, 64), ([1], [9000], 4, 2, 64), ([300], [7000], 8, 2, 128), ([128, 256], [4000, 8000], 3, 3, 64),
+    ([1, 64, 0, 700], [4097, 6400, 10, 5000], 4, 4, 128), ([2300, 40, 1], None, 6, 2, 64), ([600] * 6, [3600] * 6, 8, 8, 128), ([250], [3000], 100, 1, 64),
+    ([50], [3], 1, 1, 64)])
+def test_pieces(qd, lens, klens, qh, kvh, hd):
+    """Few pairs over long keys: cut into equal runs of chunks, joined."""
+    st = make(lens, klens, qh, kvh, hd, slack=2)
+    call(qd, st)
+    check(st)
+    if klens and sum(klens) > 3000:             # pieces in which a row sees nothing, and rising scores between them
+        st["k"][:, :, :] *= 0.2
+        at = st["koffs"][-1] - 1
+        st["k"][at] = st["q"][st["offs"][-1] - 1, ::qh // kvh] * 5.0
+        call(qd, st)
+        check(st, norm=False)
+
+
+def test_pieces_and_values_that_are_not_finite(qd):
+    st = make([300], [7000], 8, 2, 128, slack=60)
+    want = call(qd, st).clone()
+    st["v"][7000:], st["v"][6900, 1, 5] = float("nan"), float("inf")
+    st["out"].fill_(MARK)
+    call(qd, st)
+    got = st["out"]
+    mask = torch.zeros(got.shape, dtype=torch.bool, device="cuda")
+    mask[200:300, 4:, 5] = True                 # query i sees keys up to 6700 + i
+    assert not got[mask].isfinite().any() and (got[300:] == MARK).all()
+    assert torch.equal(got[:300][~mask[:300]], want[:300][~mask[:300]])
 
 
 @pytest.mark.parametrize("hd", [64, 128])
@@ -279,3 +311,14 @@ def test_the_same_whatever_the_batch(qd):
         out = torch.empty_like(want[i0:i1])
         qd.qd_attn_prompt(st["q"][i0:i1], st["k"][i0:i1], st["v"][i0:i1], out, torch.tensor([0, i1 - i0], dtype=torch.int32).cuda())
         assert torch.equal(out, want[i0:i1])
+
+
+def test_pairs_whose_first_tile_has_no_keys(qd):
+    """Tiles that see nothing beside ones that do, pair after pair in the same CTA: many sequences of more queries than keys."""
+    lens = [200 + 3 * i for i in range(60)]
+    klens = [70 + i for i in range(60)]
+    st = make(lens, klens, 32, 16, 128)
+    for _ in range(3):
+        st["out"].fill_(MARK)
+        call(qd, st)
+        check(st)

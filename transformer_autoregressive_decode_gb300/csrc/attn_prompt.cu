@@ -66,6 +66,16 @@ struct PromptArgs {
     int4 *list;
     int *count;
     int cap, cost_shift;
+    // room for pieces of pairs, two a CTA; null: pairs stay whole
+    struct Join *join;
+    float2 *p_ml;                             // [piece][256] reference, sum
+    float *p_o;                               // [piece][256][D]
+};
+
+// A pair whose chunks several CTAs have worked: pieces 2 first + second of the first CTA's, then 2 w of the `more` that follow.  more 0: none.
+struct Join {
+    int q0, tokens, hk, lim0;
+    int first, second, more, pad;
 };
 
 // A pair of tiles, as the roles see it.
@@ -73,8 +83,10 @@ struct __align__(16) Pair {
     int q0, tokens;                           // first token row, tokens (of both tiles)
     int k0, lim0;                             // first key row; keys that the first token sees
     int n0, n1;                               // chunks of either tile
-    int hk;                                   // key head; below 0: no more pairs
+    int hk;                                   // key head, and above it (1 + the piece's place) << 20 for a piece; below 0: no more pairs
     uint32_t odd;                             // chunks, counted from first_edge(), in which V was not finite
+    __device__ __forceinline__ int head() const { return hk & 0xfffff; }
+    __device__ __forceinline__ int piece() const { return (hk >> 20) - 1; }
     __device__ __forceinline__ int n(int h) const { return h ? n1 : n0; }
     __device__ __forceinline__ int most() const { return max(n0, n1); }
 };
@@ -161,14 +173,120 @@ __global__ void __launch_bounds__(1024) attn_prompt_plan_kernel(const PromptArgs
 
 // ---- or, for few pairs, every CTA by itself: the pairs of all sequences ranked by their chunks (equal ones in order, the same in every CTA),
 // (pair, key head) dealt out there and back.  The CTA's pairs to mine[0 ..], their number to *n.
-constexpr int kPtOwnPairs = 256, kPtOwnRounds = 16;
+constexpr int kPtOwnPairs = 256, kPtOwnRounds = 16, kPtMaxCtas = 512;
+// Pairs are cut into pieces, equal runs of chunks for all CTAs, where that takes as many chunks off the one that has most (3 x 700 to 1000 queries
+// over up to 6000 keys, 12 of 4 heads: 47 chunks in 104 CTAs, 31 in all; the pieces' way through memory and the joining kernel
+// take about 8 us, a chunk 1.4).
+constexpr int kPtWorthCutting = 8;
+constexpr int kPtMinRun = 4;
 struct OwnPlan {
     int cost[kPtOwnPairs];                    // read 16 at a time
     int first[kPtOwnPairs + 1];               // of every sequence
     int pad[3];
     Pair mine[kPtOwnRounds];
     int n;
+    int most;                                 // chunks of the CTA that has most, were the pairs dealt out whole
+    int load[kPtMaxCtas];
+    int sums[8];
+    // where the pairs are cut: all of them, the chunks of one key head before each, and this CTA's run
+    Pair pairs[kPtOwnPairs];
+    int before[kPtOwnPairs + 1];
+    int total, x0, x1;
+    unsigned run, more;                       // of the Share
+    bool cut;
 };
+__device__ __forceinline__ int rank_of(const PromptArgs &a, const OwnPlan &w, const Pair &p, int total) {
+    const int tid = threadIdx.x;
+    if (total * a.kvh <= (int)gridDim.x) return tid;
+    int rank = 0;
+    const int own = p.most();
+    const int4 *cost = reinterpret_cast<const int4 *>(w.cost);
+#pragma unroll 4
+    for (int j = 0; j < total; j += 4) {      // (what stands past `total` is below every cost)
+        const int4 c = cost[j / 4];
+        rank += (c.x > own || (c.x == own && j < tid)) + (c.y > own || (c.y == own && j + 1 < tid)) +
+                (c.z > own || (c.z == own && j + 2 < tid)) + (c.w > own || (c.w == own && j + 3 < tid));
+    }
+    return rank;
+}
+// Every thread of the CTA: whether the pairs are cut, and then this CTA's pieces.  p: pair threadIdx.x, with key head 0.
+__device__ __noinline__ bool cut_pairs(const PromptArgs &a, OwnPlan &w, const Pair &p, int total) {
+    const int tid = threadIdx.x, lane = tid & 31, grid = (int)gridDim.x, own = tid < total ? p.most() : 0;
+    if (tid < total) {
+        const int rank = rank_of(a, w, p, total);
+        int round = rank * a.kvh / grid, at = rank * a.kvh - round * grid;
+        for (int hk = 0; hk < a.kvh; ++hk) {
+            atomicAdd(&w.load[round & 1 ? grid - 1 - at : at], own);
+            if (++at == grid) at = 0, ++round;
+        }
+    }
+    // chunks before this pair, of one key head
+    int upto = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    if (lane == 31 && tid < kPtOwnPairs) w.sums[tid / 32] = upto;
+    __syncthreads();
+    int before = upto - own, all = 0;
+#pragma unroll
+    for (int i = 0; i < kPtOwnPairs / 32; ++i) {
+        if (i < tid / 32) before += w.sums[i];
+        all += w.sums[i];
+    }
+    int most = 0;
+    for (int i = tid; i < grid; i += kPtThreads) most = max(most, w.load[i]);
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) atomicMax(&w.most, most);
+    __syncthreads();
+    const unsigned work = (unsigned)all * (unsigned)a.kvh;
+    Share sh;
+    const int ctas = (int)min((unsigned)grid, max(1u, work / kPtMinRun));
+    sh.use(work, (unsigned)ctas);
+    const bool cut = w.most >= (int)sh.run + kPtWorthCutting;
+    Join *join = a.join + 2 * blockIdx.x;
+    if (tid < 2) join[tid].more = 0;
+    if (!cut) return false;
+    if (tid < kPtOwnPairs) w.pairs[tid] = p, w.before[tid] = before;
+    if (tid == 0) {
+        w.before[kPtOwnPairs] = all, w.total = total, w.cut = true, w.run = sh.run, w.more = sh.more;
+        w.x0 = (int)blockIdx.x < ctas ? (int)sh.first(blockIdx.x) : 0;
+        w.x1 = (int)blockIdx.x < ctas ? (int)sh.first(blockIdx.x + 1) : 0;
+    }
+    return true;
+}
+// The piece that begins at chunk x of the list (pair after pair, head after head); x moves on to the next.
+__device__ __forceinline__ Pair piece_at(const PromptArgs &a, const OwnPlan &w, int &x) {
+    Pair q = {};
+    q.hk = -1;
+    if (x >= w.x1) return q;
+    int lo = 0, hi = kPtOwnPairs;             // before[lo] kvh <= x < before[hi] kvh
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (w.before[mid] * a.kvh <= x)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const Pair p = w.pairs[lo];
+    const int own = p.most(), y = x - w.before[lo] * a.kvh, hk = y / own, c0 = y - hk * own, c1 = min(own, c0 + w.x1 - x);
+    // a piece's place among the two that a CTA can have: its run begins with it, or ends
+    const int place = x == w.x0 ? 0 : 1;
+    q = p;
+    q.hk = hk;
+    if (c0 > 0 || c1 < own) q.hk |= (1 + 2 * (int)blockIdx.x + place) << 20;
+    q.k0 += c0 * kPtKeys, q.lim0 -= c0 * kPtKeys;
+    q.n0 = max(0, min(p.n0, c1) - c0), q.n1 = max(0, min(p.n1, c1) - c0);
+    if (c0 == 0 && c1 < own && (threadIdx.x & 31) == 0) {
+        Share sh;
+        sh.run = w.run, sh.more = w.more;
+        a.join[2 * blockIdx.x + place] = {p.q0, p.tokens, hk, p.lim0, (int)blockIdx.x, place,
+                                          (int)sh.owner((unsigned)(x + own) - 1u) - (int)blockIdx.x, 0};
+    }
+    x += c1 - c0;
+    return q;
+}
 __device__ __forceinline__ void plan_own(const PromptArgs &a, OwnPlan &w) {
     const int tid = threadIdx.x, lane = tid & 31;
     Sequence s = {};
@@ -176,8 +294,9 @@ __device__ __forceinline__ void plan_own(const PromptArgs &a, OwnPlan &w) {
         s = sequence(a, tid);
         w.first[tid + 1] = pairs_of(a, s);
     }
-    if (tid == 0) w.n = 0;
+    if (tid == 0) w.n = 0, w.most = 0, w.cut = false;
     if (tid < kPtOwnPairs) w.cost[tid] = -1;
+    if (a.join && tid < kPtMaxCtas) w.load[tid] = 0;
     __syncthreads();
     if (tid < 32) {                           // running sums, 8 sequences a lane
         int v[kPtOwnPairs / 32], sum = 0;
@@ -217,20 +336,13 @@ __device__ __forceinline__ void plan_own(const PromptArgs &a, OwnPlan &w) {
         w.cost[tid] = p.most();
     }
     __syncthreads();
-    if (tid >= total) return;
-    int rank = tid;
     const int grid = (int)gridDim.x;
-    if (total * a.kvh > grid) {
-        rank = 0;
-        const int own = p.most();
-        const int4 *cost = reinterpret_cast<const int4 *>(w.cost);
-#pragma unroll 4
-        for (int j = 0; j < total; j += 4) {  // (what stands past `total` is below every cost)
-            const int4 c = cost[j / 4];
-            rank += (c.x > own || (c.x == own && j < tid)) + (c.y > own || (c.y == own && j + 1 < tid)) +
-                    (c.z > own || (c.z == own && j + 2 < tid)) + (c.w > own || (c.w == own && j + 3 < tid));
-        }
+    if (a.join) {
+        // the CTAs' loads, and the chunks before every pair (over cost[], which the ranks have been read from)
+        if (cut_pairs(a, w, p, total)) return;
     }
+    if (tid >= total) return;
+    const int rank = rank_of(a, w, p, total);
     int round = rank * a.kvh / grid, at = rank * a.kvh - round * grid;
     for (int hk = 0; hk < a.kvh; ++hk) {
         if ((round & 1 ? grid - 1 - at : at) == (int)blockIdx.x && round < kPtOwnRounds) {
@@ -363,14 +475,15 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPtRegsRest));
         // ---- the pairs, and their loads (the whole warp walks along; one lane issues)
         int kc = 0, nq[2] = {0, 0}, next = (int)blockIdx.x;
-        const int total = a.list ? a.count[0] * a.kvh : own.n;
+        const int total = a.list ? a.count[0] * a.kvh : min(own.n, kPtOwnRounds);
+        int x = own.x0;                             // where the pairs are cut: the next chunk
         bool ok = true;
         // pair `i` of the list, or of this CTA's own
         auto pair_no = [&](int i) {
             Pair p = {};
             p.hk = -1;
-            if (i >= total) return p;
-            if (!a.list) return own.mine[i];
+            if (i >= total && (a.list || !own.cut)) return p;
+            if (!a.list) return own.cut ? piece_at(a, own, x) : own.mine[i];
             const int4 u = a.list[2 * (i / a.kvh)], v = a.list[2 * (i / a.kvh) + 1];
             p.q0 = u.x, p.tokens = u.y, p.k0 = u.z, p.lim0 = u.w, p.n0 = v.x, p.n1 = v.y;
             p.hk = i % a.kvh;
@@ -406,17 +519,17 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     if (nq[h] > 0) ok = ok && wt_wait(&q_empty[h], (uint32_t)(nq[h] + 1) & 1u, bad);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) return;
-                    load(&mq, C::kQ + h * C::kTile, &q_full[h], (uint32_t)(KB * a.tpt * a.G * 128), p.hk * a.G, p.q0 + h * a.tpt);
+                    load(&mq, C::kQ + h * C::kTile, &q_full[h], (uint32_t)(KB * a.tpt * a.G * 128), p.head() * a.G, p.q0 + h * a.tpt);
                     ++nq[h];
                 };
                 if (c == 0) load_q(p.n0 ? 0 : 1);
                 if (kc >= kPtStages) ok = ok && wt_wait(&k_empty[st], was, bad);
                 ok = __all_sync(0xffffffffu, ok);
-                if (ok) load(&mk, C::kK + st * C::kTile, &k_full[st], C::kTile, p.hk, key);
+                if (ok) load(&mk, C::kK + st * C::kTile, &k_full[st], C::kTile, p.head(), key);
                 if (c == 0 && p.n0) load_q(1);
                 if (kc >= kPtStages) ok = ok && wt_wait(&v_empty[st], was, bad);
                 ok = __all_sync(0xffffffffu, ok);
-                if (ok) load(&mv, C::kV + st * C::kTile, &v_full[st], C::kTile, p.hk, key);
+                if (ok) load(&mv, C::kV + st * C::kTile, &v_full[st], C::kTile, p.head(), key);
             }
             next = __shfl_sync(0xffffffffu, next, 0);
             if (ok) p = pair_no(a.list ? next : it + 1);
@@ -445,8 +558,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         uint32_t nq[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0};   // of either tile: pairs, P's, pairs begun in O
         bool ok = true, begun[2] = {false, false};  // the pair's first S is issued
         Pair p = pair_at(0);
-        // S of tile h, chunk c of pair x whose first chunk is the kx-th
-        auto issue_s = [&](int h, int c, const Pair &x, int kx) {
+        // S of tile h, chunk c of pair x whose first chunk is the kx-th; `other`: the other tile's S of that chunk is issued, or none is wanted
+        auto issue_s = [&](int h, int c, const Pair &x, int kx, bool other) {
             const int st = (kx + c) % kPtStages;
             if (c == 0) ok = ok && wt_wait(&q_full[h], nq[h]++ & 1u, bad);
             ok = ok && wt_wait(&k_full[st], (uint32_t)((kx + c) / kPtStages) & 1u, bad);
@@ -455,7 +568,6 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             tc_fence_after();
             const uint32_t d = tm + kPtS + 128u * h;
             const uint64_t q = dQ + h * KB * kBox16, k = dK + st * KB * kBox16;
-            const bool last_k = h == 1 || x.n1 <= c;      // nobody needs this K after it
             if (elect_one()) {
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb)
@@ -463,7 +575,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     for (int s = 0; s < 4; ++s)
                         tc_mma(d, q + kb * kBox16 + 2 * s, k + kb * kBox16 + 2 * s, idesc_s, (kb | s) ? 1u : 0u);
                 tc_commit(&s_full[h]);
-                if (last_k) tc_commit(&k_empty[st]);
+                if (other) tc_commit(&k_empty[st]);
                 if (c + 1 == x.n(h)) tc_commit(&q_empty[h]);
             }
             __syncwarp();
@@ -495,7 +607,10 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             const int n = p.most();
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                if (ok && !begun[h] && p.n(h) > 0) issue_s(h, 0, p, kc);
+                if (ok && !begun[h] && p.n(h) > 0) {
+                    issue_s(h, 0, p, kc, begun[1 - h] || p.n(1 - h) == 0);
+                    begun[h] = true;
+                }
             begun[0] = begun[1] = false;
             Pair x;
             x.hk = -2;                              // the next pair: not known yet
@@ -506,11 +621,12 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     issue_o(h, c);
                     if (!ok) continue;
                     if (c + 1 < p.n(h)) {
-                        issue_s(h, c + 1, p, kc);
+                        issue_s(h, c + 1, p, kc, h == 1 || p.n1 <= c + 1);
                     } else {
                         if (x.hk == -2) x = pair_at(it + 1);
                         if (x.hk >= 0 && x.n(h) > 0) {
-                            issue_s(h, 0, x, kc + n);
+                            // (the second tile's may come first: where this pair had no first)
+                            issue_s(h, 0, x, kc + n, begun[1 - h] || x.n(1 - h) == 0);
                             begun[h] = true;
                         }
                     }
@@ -670,7 +786,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             // no key gives zeros; keys whose scores are all -infinity NaN, as the formula does
             const float by = (lim <= 0 ? 0.f : l == 0.f ? __uint_as_float(0x7fc00000u) : 1.f / l) + fail;
             const uint32_t odd = n > 0 ? *reinterpret_cast<volatile uint32_t *>(&slot_of(it).odd) : 0u;
-            uint8_t *dst = a.out + (int64_t)(p.q0 + tt) * a.o_token + (int64_t)(p.hk * a.G + head) * (2 * D) + kh * D;
+            uint8_t *dst = a.out + (int64_t)(p.q0 + tt) * a.o_token + (int64_t)(p.head() * a.G + head) * (2 * D) + kh * D;
             uint32_t u[D / 2];
             if (n > 0) {
 #pragma unroll
@@ -690,7 +806,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     if (!((odd >> k) & 1u)) continue;
                     const int j0 = (first_edge(p) + k) * kPtKeys, j1 = min(lim, j0 + kPtKeys);
                     for (int j = j0; live && j < j1; ++j) {
-                        const uint16_t *v = reinterpret_cast<const uint16_t *>(a.v + (int64_t)(p.k0 + j) * a.v_token) + p.hk * D + kh * (D / 2);
+                        const uint16_t *v = reinterpret_cast<const uint16_t *>(a.v + (int64_t)(p.k0 + j) * a.v_token) + p.head() * D + kh * (D / 2);
 #pragma unroll
                         for (int e = 0; e < D / 2; ++e) {
                             const uint32_t w = (uint32_t)v[e] << 16;
@@ -699,7 +815,16 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     }
                 }
             }
-            if (live) {
+            if (p.piece() >= 0) {
+                // a piece: the products as they are, with the reference and the sum
+                const int64_t at = (int64_t)p.piece() * 256 + h * 128 + r;
+                if (live) {
+                    float *to = a.p_o + at * D + kh * (D / 2);
+#pragma unroll
+                    for (int e = 0; e < D / 2; e += 8) st32(to + e, u + e);
+                    if (kh == 0) a.p_ml[at] = make_float2(ref, l + fail);
+                }
+            } else if (live) {
 #pragma unroll
                 for (int i = 0; i < D / 64; ++i) {
                     uint32_t o[16];
@@ -724,10 +849,40 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     if (warp == 16) tmem_dealloc(tmem, 512);
 }
 
+// The pieces of a pair that several CTAs worked, weighted to their largest reference: blockIdx.x the pair's first piece, blockIdx.y 16 of
+// its 256 rows; D / 8 threads a row.
+constexpr int kPtJoinRows = 16;
+template <int D> __global__ void __launch_bounds__(kPtJoinRows * D / 8) attn_prompt_join_kernel(const PromptArgs a) {
+    pdl_wait();
+    const Join j = a.join[blockIdx.x];
+    if (j.more == 0) return;
+    const int row = blockIdx.y * kPtJoinRows + threadIdx.x / (D / 8), d = threadIdx.x % (D / 8) * 8;
+    const int h = row >> 7, r = row & 127, token = r / a.G, head = r - token * a.G, tt = h * a.tpt + token;
+    if (token >= a.tpt || tt >= j.tokens) return;
+    auto piece = [&](int i) { return (int64_t)(i == 0 ? 2 * j.first + j.second : 2 * (j.first + i)) * 256 + row; };
+    float M = -INFINITY;
+    for (int i = 0; i <= j.more; ++i) M = fmaxf(M, a.p_ml[piece(i)].x);
+    float sum = 0.f, acc[8] = {};
+    for (int i = 0; i <= j.more; ++i) {
+        const float2 e = a.p_ml[piece(i)];
+        if (e.y == 0.f) continue;                   // nothing seen there
+        const float f = ex2(e.x - M);
+        sum = fmaf(f, e.y, sum);
+        const float4 *o = reinterpret_cast<const float4 *>(a.p_o + piece(i) * D + d);
+        const float4 x = o[0], y = o[1];
+        acc[0] = fmaf(f, x.x, acc[0]), acc[1] = fmaf(f, x.y, acc[1]), acc[2] = fmaf(f, x.z, acc[2]), acc[3] = fmaf(f, x.w, acc[3]);
+        acc[4] = fmaf(f, y.x, acc[4]), acc[5] = fmaf(f, y.y, acc[5]), acc[6] = fmaf(f, y.z, acc[6]), acc[7] = fmaf(f, y.w, acc[7]);
+    }
+    const float by = j.lim0 + tt <= 0 ? 0.f : sum == 0.f ? __uint_as_float(0x7fc00000u) : 1.f / sum;
+    *reinterpret_cast<uint4 *>(a.out + (int64_t)(j.q0 + tt) * a.o_token + ((int64_t)(j.hk * a.G + head) * D + d) * 2) =
+        make_uint4(pack_bf16(acc[0] * by, acc[1] * by), pack_bf16(acc[2] * by, acc[3] * by), pack_bf16(acc[4] * by, acc[5] * by),
+                   pack_bf16(acc[6] * by, acc[7] * by));
+}
+
 template <typename F, typename... A>
-cudaError_t launch_after(F fn, unsigned ctas, int threads, size_t smem, cudaStream_t s, A... args) {
+cudaError_t launch_after(F fn, dim3 ctas, int threads, size_t smem, cudaStream_t s, A... args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas);
+    cfg.gridDim = ctas;
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -754,16 +909,22 @@ template <int D> cudaError_t launch(const CUtensorMap &q, const CUtensorMap &k, 
         const cudaError_t e = launch_after(attn_prompt_plan_kernel, 1, 1024, 0, s, a);
         if (e != cudaSuccess) return e;
     }
-    return launch_after(fn, ctas, kPtThreads, PtCfg<D>::kSmem, s, q, k, v, a);
+    const cudaError_t e = launch_after(fn, ctas, kPtThreads, PtCfg<D>::kSmem, s, q, k, v, a);
+    if (e != cudaSuccess || !a.join) return e;
+    return launch_after(attn_prompt_join_kernel<D>, dim3(2 * ctas, 256 / kPtJoinRows), kPtJoinRows * D / 8, 0, s, a);
 }
 
 // How a call runs: the most pairs that the sequences can have, and the CTAs.
 struct PromptPlan {
     int tpt, cap;
-    bool list;
+    bool list, join;
     unsigned ctas;
-    size_t bytes;
+    size_t p_ml, p_o, bytes;
 };
+// Keys a sequence, in the mean, from which few pairs may be cut into pieces: below, none is long enough to gain by it (kPtWorthCutting), and the
+// joining kernel's launch, which the lengths decide about too late, costs 2 us.
+constexpr int64_t kPtCutKeys = 16 * kPtKeys;
+
 qd_status plan_prompt(int n_tokens, int n_kv_tokens, int n_seqs, int n_q_heads, int n_kv_heads, int head_dim, int dev, PromptPlan *p) {
     if (n_tokens < 1 || n_kv_tokens < 1 || n_seqs < 1 || n_kv_heads < 1 || n_q_heads < n_kv_heads || n_q_heads % n_kv_heads) return QD_EINVAL;
     if (head_dim != 64 && head_dim != 128) return QD_EUNSUPPORTED;
@@ -776,7 +937,16 @@ qd_status plan_prompt(int n_tokens, int n_kv_tokens, int n_seqs, int n_q_heads, 
     p->cap = (int)pairs;
     p->list = pairs > kPtOwnPairs || n_seqs > kPtOwnPairs || pairs * n_kv_heads > (int64_t)kPtOwnRounds * sms;
     p->ctas = (unsigned)std::min<int64_t>(pairs * n_kv_heads, sms);
+    // few pairs of long sequences: every SM has a CTA, and room for two pieces
+    p->join = !p->list && pairs * n_kv_heads <= sms + sms / 4 && n_kv_tokens >= kPtCutKeys * n_seqs && sms <= kPtMaxCtas;
     p->bytes = p->list ? 256 + (size_t)pairs * 32 : 0;
+    if (p->join) {
+        p->ctas = (unsigned)sms;
+        const size_t pieces = 2 * (size_t)sms;
+        p->p_ml = (pieces * sizeof(Join) + 255) / 256 * 256;
+        p->p_o = p->p_ml + pieces * 256 * sizeof(float2);
+        p->bytes = p->p_o + pieces * 256 * head_dim * sizeof(float);
+    }
     return QD_OK;
 }
 
@@ -843,6 +1013,11 @@ qd_status qd_attn_prompt(const void *q_dev, int64_t q_stride, const void *k_dev,
         a.list = reinterpret_cast<int4 *>(static_cast<uint8_t *>(workspace_dev) + 256);
         a.cap = p.cap;
         while ((n_kv_tokens / kPtKeys + 1) >> a.cost_shift >= kPtBuckets) ++a.cost_shift;
+    }
+    if (p.join) {
+        uint8_t *ws = static_cast<uint8_t *>(workspace_dev);
+        a.join = reinterpret_cast<Join *>(ws);
+        a.p_ml = reinterpret_cast<float2 *>(ws + p.p_ml), a.p_o = reinterpret_cast<float *>(ws + p.p_o);
     }
     CUtensorMap mq, mk, mv;
     if (!make_heads_map(&mq, q_dev, head_dim, n_q_heads, n_tokens, n_tokens > 1 ? q_stride : q_row, a.G, a.tpt) ||
