@@ -44,9 +44,8 @@ constexpr int kPtThreads = 640, kPtSoft = 512;
 constexpr int kPtRegsSoft = 104, kPtRegsRest = 64;
 static_assert(kPtSoft * kPtRegsSoft + (kPtThreads - kPtSoft) * kPtRegsRest <= kPtThreads * 96, "registers");
 constexpr uint32_t kPtBox = 128 * 128;        // 128 rows of 128 bytes, 128-byte swizzle
-constexpr uint32_t kPtS = 0, kPtO = 256;      // tensor memory columns: S (and P) of the tiles, O
+constexpr uint32_t kPtS = 0;                  // tensor memory columns: S of the tiles, then O
 constexpr int kPtKeys = 128;                  // of a chunk
-constexpr int kPtStages = 2;                  // of K and of V
 constexpr int kPtSlots = 4;                   // pairs in flight between the roles
 constexpr int kPtUsers = 19;                  // warps that read a slot
 constexpr int kPtBuckets = 1024;              // of the plan's sort
@@ -356,11 +355,16 @@ __device__ __forceinline__ void plan_own(const PromptArgs &a, OwnPlan &w) {
 
 template <int D> struct PtCfg {
     static constexpr int KB = D / 64;                         // 64-wide blocks of head_dim
+    static constexpr int kStages = 4 / KB;                    // of K and of V
+    // Heads of 64 leave columns for P beside S and O, so that the next S need not wait for P's product
+    static constexpr bool kOwnP = D == 64;
+    static constexpr uint32_t kP = kOwnP ? 384 : kPtS, kPHalf = kOwnP ? 32 : 64, kPTile = kOwnP ? 64 : 128;   // columns; of a half, of a tile
+    static constexpr uint32_t kO = 256, kOTile = kOwnP ? 64 : 128;
     static constexpr uint32_t kTile = KB * kPtBox;            // of Q, K or V
     static constexpr uint32_t kQ = 0;                         // Q [tile]
     static constexpr uint32_t kK = kQ + 2 * kTile;            // K [stage]
-    static constexpr uint32_t kV = kK + kPtStages * kTile;    // V [stage]
-    static constexpr uint32_t kSlot = kV + kPtStages * kTile;
+    static constexpr uint32_t kV = kK + kStages * kTile;    // V [stage]
+    static constexpr uint32_t kSlot = kV + kStages * kTile;
     static constexpr uint32_t kRow = kSlot + kPtSlots * sizeof(Pair);   // rows' maxima, sums [of either][tile][half][128]
     static constexpr uint32_t kOwn = kRow + 2 * 2 * 2 * 128 * 4;
     static constexpr uint32_t kBar = kOwn + (sizeof(OwnPlan) + 15) / 16 * 16;
@@ -369,28 +373,28 @@ template <int D> struct PtCfg {
 };
 static_assert(sizeof(Pair) == 32, "two loads of 16 bytes");
 
-// 32 scores of a row as weights against its reference, packed; their sums join la and lb.  EDGE: the first `left` are seen.  (Single
-// products and packed sums: 64 scores take one warp of a scheduler 354 clocks, two of them 493, which is the exponentials' 8 a clock;
-// packed products 412 and 543.)
-template <bool EDGE>
-__device__ __forceinline__ void weigh(const uint32_t *x, float cs, float rf, int left, uint32_t *y, uint64_t &la, uint64_t &lb) {
+// 32 scores of a row as weights against its reference, packed; their sums join la and lb.  (Single products and packed sums: 64 scores take one
+// warp of a scheduler 349 clocks, two of them 566, near the exponentials' 8 a clock; packed products 328 and 556.)
+__device__ __forceinline__ void weigh(const uint32_t *x, float cs, float rf, uint32_t *y, uint64_t &la, uint64_t &lb) {
 #pragma unroll
     for (int e = 0; e < 32; e += 4) {
         float s[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            s[i] = ex2(fmaf(__uint_as_float(x[e + i]), cs, rf));
-            if constexpr (EDGE) s[i] = e + i < left ? s[i] : 0.f;
-        }
+        for (int i = 0; i < 4; ++i) s[i] = ex2(fmaf(__uint_as_float(x[e + i]), cs, rf));
         la = add2(la, pk(s[0], s[1])), lb = add2(lb, pk(s[2], s[3]));
         y[e / 2] = pack_bf16(s[0], s[1]), y[e / 2 + 1] = pack_bf16(s[2], s[3]);
     }
 }
-// The largest of the first `left` of N scores, in log2 units.
-template <int N> __device__ __forceinline__ float largest(const uint32_t *x, float cs, int left) {
+// Scores past the first `left` of 32 become `none`, whose weight is zero whatever stood there.
+__device__ __forceinline__ void hide(uint32_t *x, int left, uint32_t none) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) x[e] = e < left ? x[e] : none;
+}
+// The largest of N scores, in log2 units.
+template <int N> __device__ __forceinline__ float largest(const uint32_t *x, float cs) {
     float m = -INFINITY;
 #pragma unroll
-    for (int e = 0; e < N; ++e) m = fmaxf(m, e < left ? __uint_as_float(x[e]) * cs : -INFINITY);
+    for (int e = 0; e < N; ++e) m = fmaxf(m, __uint_as_float(x[e]) * cs);
     return m;
 }
 __device__ __forceinline__ bool not_finite(uint32_t w) { return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u; }
@@ -421,19 +425,20 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     uint64_t *slot_full = bars, *slot_empty = bars + 4;                                              // [slot]
     uint64_t *q_full = bars + 8, *q_empty = bars + 10, *s_full = bars + 12, *p_full = bars + 14;     // [tile]
     uint64_t *o_full = bars + 16, *o_empty = bars + 18;                                              // [tile]
-    uint64_t *k_full = bars + 24, *k_empty = bars + 26, *v_full = bars + 28, *v_empty = bars + 30, *v_clean = bars + 32;   // [stage]
-    uint64_t *drain = bars + 34;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 35);
-    volatile int *bad = reinterpret_cast<volatile int *>(bars + 36);
+    uint64_t *s_empty = bars + 20;                                                                   // [tile]
+    uint64_t *k_full = bars + 22, *k_empty = bars + 26, *v_full = bars + 30, *v_empty = bars + 34, *v_clean = bars + 38;   // [stage]
+    uint64_t *drain = bars + 42, *p_empty = bars + 45;                                               // p_empty: [tile]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 43);
+    volatile int *bad = reinterpret_cast<volatile int *>(bars + 44);
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kPtSlots; ++i) mbar_init(&slot_full[i], 1), mbar_init(&slot_empty[i], kPtUsers);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], 1), mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 8);
-            mbar_init(&o_full[i], 1), mbar_init(&o_empty[i], 8);
+            mbar_init(&o_full[i], 1), mbar_init(&o_empty[i], 8), mbar_init(&s_empty[i], 8), mbar_init(&p_empty[i], 1);
         }
-        for (int i = 0; i < kPtStages; ++i) {
+        for (int i = 0; i < C::kStages; ++i) {
             mbar_init(&k_full[i], 1), mbar_init(&k_empty[i], 1);
             mbar_init(&v_full[i], 1), mbar_init(&v_empty[i], 1), mbar_init(&v_clean[i], 2);
         }
@@ -451,6 +456,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
+    pdl_launch_dependents();                  // the whole grid is resident, so what follows may be placed as SMs fall free
     OwnPlan &own = *reinterpret_cast<OwnPlan *>(sm + C::kOwn);
     if (!a.list) plan_own(a, own);
     tc_fence_before();
@@ -503,8 +509,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             if (a.list && lane == 0) next = (int)gridDim.x + atomicAdd(&a.count[1], 1);     // in flight under this pair's loads
             const int n = p.most();
             for (int c = 0; ok && c < n; ++c, ++kc) {
-                const int st = kc % kPtStages;
-                const uint32_t was = (uint32_t)(kc / kPtStages + 1) & 1u;
+                const int st = kc % C::kStages;
+                const uint32_t was = (uint32_t)(kc / C::kStages + 1) & 1u;
                 const int key = p.k0 + c * kPtKeys;
                 auto load = [&](const CUtensorMap *m, uint32_t at, uint64_t *full, uint32_t bytes, int head, int row) {
                     if (elect_one()) {
@@ -523,11 +529,11 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     ++nq[h];
                 };
                 if (c == 0) load_q(p.n0 ? 0 : 1);
-                if (kc >= kPtStages) ok = ok && wt_wait(&k_empty[st], was, bad);
+                if (kc >= C::kStages) ok = ok && wt_wait(&k_empty[st], was, bad);
                 ok = __all_sync(0xffffffffu, ok);
                 if (ok) load(&mk, C::kK + st * C::kTile, &k_full[st], C::kTile, p.head(), key);
                 if (c == 0 && p.n0) load_q(1);
-                if (kc >= kPtStages) ok = ok && wt_wait(&v_empty[st], was, bad);
+                if (kc >= C::kStages) ok = ok && wt_wait(&v_empty[st], was, bad);
                 ok = __all_sync(0xffffffffu, ok);
                 if (ok) load(&mv, C::kV + st * C::kTile, &v_full[st], C::kTile, p.head(), key);
             }
@@ -538,8 +544,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         if (!ok) {
             for (int h = 0; h < 2; ++h)
                 if (nq[h] > 0) (void)mbar_wait_bounded(&q_full[h], (uint32_t)(nq[h] + 1) & 1u, 20000000ull);
-            for (int i = 0; i < kPtStages; ++i) {
-                const int uses = kc / kPtStages + 1;
+            for (int i = 0; i < C::kStages; ++i) {
+                const int uses = kc / C::kStages + 1;
                 (void)mbar_wait_bounded(&k_full[i], (uint32_t)(uses + 1) & 1u, 20000000ull);
                 (void)mbar_wait_bounded(&v_full[i], (uint32_t)(uses + 1) & 1u, 20000000ull);
             }
@@ -555,14 +561,18 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         constexpr uint32_t kBox16 = kPtBox / 16;
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         int kc = 0;                                 // chunks before this pair's
-        uint32_t nq[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0};   // of either tile: pairs, P's, pairs begun in O
+        uint32_t nq[2] = {0, 0}, n_s[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0};   // of either tile: pairs, S's, P's, pairs begun in O
         bool ok = true, begun[2] = {false, false};  // the pair's first S is issued
         Pair p = pair_at(0);
         // S of tile h, chunk c of pair x whose first chunk is the kx-th; `other`: the other tile's S of that chunk is issued, or none is wanted
         auto issue_s = [&](int h, int c, const Pair &x, int kx, bool other) {
-            const int st = (kx + c) % kPtStages;
+            const int st = (kx + c) % C::kStages;
             if (c == 0) ok = ok && wt_wait(&q_full[h], nq[h]++ & 1u, bad);
-            ok = ok && wt_wait(&k_full[st], (uint32_t)((kx + c) / kPtStages) & 1u, bad);
+            if constexpr (C::kOwnP) {
+                if (n_s[h] > 0) ok = ok && wt_wait(&s_empty[h], (n_s[h] + 1) & 1u, bad);
+                ++n_s[h];
+            }
+            ok = ok && wt_wait(&k_full[st], (uint32_t)((kx + c) / C::kStages) & 1u, bad);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) return;
             tc_fence_after();
@@ -581,13 +591,13 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             __syncwarp();
         };
         auto issue_o = [&](int h, int c) {
-            const int st = (kc + c) % kPtStages;
-            const uint32_t ph = (uint32_t)((kc + c) / kPtStages) & 1u;
+            const int st = (kc + c) % C::kStages;
+            const uint32_t ph = (uint32_t)((kc + c) / C::kStages) & 1u;
             if (c == 0) {
                 if (no[h] > 0) ok = ok && wt_wait(&o_empty[h], (no[h] + 1) & 1u, bad);
                 ++no[h];
             }
-            const uint32_t d = tm + kPtO + 128u * h, pt = tm + kPtS + 128u * h;
+            const uint32_t d = tm + C::kO + C::kOTile * h, pt = tm + C::kP + C::kPTile * h;
             const uint64_t v = dV + st * KB * kBox16;
             ok = ok && wt_wait(&v_full[st], ph, bad) && wt_wait(&v_clean[st], ph, bad);
             ok = ok && wt_wait(&p_full[h], np[h] & 1u, bad);
@@ -596,7 +606,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
-                for (int i = 0; i < kPtKeys / 16; ++i) tc_mma_ts(d, pt + 8u * i + 32u * (i >> 2), v + i * 128, idesc_o, (c | i) ? 1u : 0u);
+                for (int i = 0; i < kPtKeys / 16; ++i) tc_mma_ts(d, pt + 8u * (i & 3) + C::kPHalf * (i >> 2), v + i * 128, idesc_o, (c | i) ? 1u : 0u);
+                if constexpr (C::kOwnP) tc_commit(&p_empty[h]);
                 if (h == 1 || p.n1 <= c) tc_commit(&v_empty[st]);
                 if (c + 1 == p.n(h)) tc_commit(&o_full[h]);
             }
@@ -618,10 +629,11 @@ __global__ void __launch_bounds__(kPtThreads, 1)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     if (!ok || c >= p.n(h)) continue;
-                    issue_o(h, c);
+                    if (C::kOwnP && c + 1 < p.n(h)) issue_s(h, c + 1, p, kc, h == 1 || p.n1 <= c + 1);
+                    if (ok) issue_o(h, c);
                     if (!ok) continue;
                     if (c + 1 < p.n(h)) {
-                        issue_s(h, c + 1, p, kc, h == 1 || p.n1 <= c + 1);
+                        if (!C::kOwnP) issue_s(h, c + 1, p, kc, h == 1 || p.n1 <= c + 1);
                     } else {
                         if (x.hk == -2) x = pair_at(it + 1);
                         if (x.hk >= 0 && x.n(h) > 0) {
@@ -650,8 +662,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             if (p.hk < 0) break;
             const int n = p.most(), edge = first_edge(p);
             for (int c = 0; ok && c < n; ++c, ++kc) {
-                const int st = kc % kPtStages;
-                ok = wt_wait(&v_full[st], (uint32_t)(kc / kPtStages) & 1u, bad);
+                const int st = kc % C::kStages;
+                ok = wt_wait(&v_full[st], (uint32_t)(kc / C::kStages) & 1u, bad);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 if (c >= edge) {
@@ -688,10 +700,12 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         // ---- softmax: tile h, row r of it, the keys' half kh of every chunk; the two warps that share rows keep one reference
         const int h = warp >> 3, kh = (warp >> 2) & 1, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        const uint32_t tS = tmem + kPtS + 128u * h + 64u * kh + lanes, tO = tmem + kPtO + 128u * h + lanes;
+        const uint32_t tS = tmem + kPtS + 128u * h + 64u * kh + lanes, tO = tmem + C::kO + C::kOTile * h + lanes;
+        const uint32_t tP = tmem + C::kP + C::kPTile * h + C::kPHalf * kh + lanes;
         const int token = r / a.G, head = r - token * a.G, pair_bar = 1 + h * 4 + quarter;
         float *row_max = reinterpret_cast<float *>(sm + C::kRow) + (h * 2) * 128 + r, *row_sum = row_max + 4 * 128;
         const bool in_tile = token < a.tpt;
+        const uint32_t none = a.scale2 < 0.f ? 0x7f800000u : 0xff800000u;       // -infinity once it is scaled
         uint32_t ns = 0, no = 0;                    // S's, O's so far
         bool ok = true;
         for (int it = 0; ok; ++it) {
@@ -703,6 +717,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             const int lim = p.lim0 + (live ? tt : min(p.tokens, (h + 1) * a.tpt) - 1);
             const int lim_all = __reduce_min_sync(0xffffffffu, lim);        // keys that every row of the warp sees
             float ref = -INFINITY, l = 0.f;
+            bool ref_wanted = true;
             for (int c = 0; c < n; ++c) {
                 ok = ok && wt_wait(&s_full[h], ns & 1u, bad);
                 ++ns;
@@ -711,62 +726,70 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 const bool edge = lim_all < c * kPtKeys + 64 * kh + 64;
                 uint32_t x[64], y[32];
                 float sum;
+                bool all_none = false;
                 // the larger of both warps' largest scores
                 auto of_row = [&](float m) {
                     row_max[kh * 128] = m;
                     named_sync(pair_bar, 64);
                     return fmaxf(m, row_max[(kh ^ 1) * 128]);
                 };
-                auto weigh_all = [&](bool split) {
+                // one pass as a rule; another where a weight has outgrown its room
+#pragma unroll 1
+                while (true) {
+                    tc_ld32_nowait(tS, x);
+                    tc_wait_ld_u32<32>(x);
+                    tc_ld32_nowait(tS + 32u, x + 32);           // arrives under the work on the first
+                    if (edge) hide(x, left, none);
+                    // the first chunk: 16 scores of either warp set the reference, which is near enough as a rule
+                    if (ref_wanted) ref = of_row(largest<16>(x, a.scale2)), ref_wanted = false;
                     const float rf = ref == -INFINITY ? 0.f : -ref;
                     uint64_t la = pk(0.f, 0.f), lb = la;
-                    if (edge)
-                        weigh<true>(x, a.scale2, rf, left, y, la, lb);
-                    else
-                        weigh<false>(x, a.scale2, rf, left, y, la, lb);
-                    if (split) tc_wait_ld_u32<32>(x + 32);
-                    if (edge)
-                        weigh<true>(x + 32, a.scale2, rf, left - 32, y + 16, la, lb);
-                    else
-                        weigh<false>(x + 32, a.scale2, rf, left, y + 16, la, lb);
+                    weigh(x, a.scale2, rf, y, la, lb);
+                    tc_wait_ld_u32<32>(x + 32);
+                    if (edge) hide(x + 32, left - 32, none);
+                    weigh(x + 32, a.scale2, rf, y + 16, la, lb);
                     float l0, l1;
                     unpk(add2(la, lb), l0, l1);
                     sum = l0 + l1;
-                };
-                tc_ld32_nowait(tS, x);
-                tc_wait_ld_u32<32>(x);
-                tc_ld32_nowait(tS + 32u, x + 32);
-                // the first chunk: 16 scores of either warp set the reference, which is near enough as a rule
-                if (c == 0) ref = of_row(largest<16>(x, a.scale2, left));
-                {
-                    weigh_all(true);
-                    if (named_sync_or(pair_bar, 64, live && (sum > kPtTop || (ref == -INFINITY && left > 0)))) {
-                        tc_ld32_nowait(tS, x);      // the scores again: they stand until their weights are written
-                        tc_ld32_nowait(tS + 32u, x + 32);
-                        tc_wait_ld_u32<64>(x);
-                        const float m = of_row(largest<64>(x, a.scale2, left));
-                        float f = 1.f;
-                        if (m > ref) {
-                            f = ref == -INFINITY ? 0.f : ex2(ref - m);
-                            ref = m;
-                            l *= f;
-                        }
-                        // O holds the chunks before, whose products this S came behind; half its columns each
+                    if (!named_sync_or(pair_bar, 64, live && (sum > kPtTop || (ref == -INFINITY && left > 0 && !all_none)))) break;
+                    // the scores again: they stand until their weights are written
+                    tc_ld32_nowait(tS, x);
+                    tc_ld32_nowait(tS + 32u, x + 32);
+                    tc_wait_ld_u32<64>(x);
+                    if (edge) hide(x, left, none), hide(x + 32, left - 32, none);
+                    const float m = of_row(largest<64>(x, a.scale2));
+                    all_none = m == -INFINITY;      // (scores of -infinity alone: the reference stays)
+                    if constexpr (C::kOwnP) {
+                        if (ns > 1) ok = ok && wt_wait(&p_empty[h], ns & 1u, bad);
+                        tc_fence_after();
+                    }
+                    float f = 1.f;
+                    if (m > ref) {
+                        f = ref == -INFINITY ? 0.f : ex2(ref - m);
+                        ref = m;
+                        l *= f;
+                    }
+                    // O holds the chunks before, whose products are done (this S came behind them); half its columns each
 #pragma unroll 1
-                        for (int i = 0; c > 0 && i < D / 32; ++i) {
-                            const uint32_t at = tO + (uint32_t)(kh * (D / 2) + 16 * i);
-                            uint32_t u[16];
-                            tc_ld16_nowait(at, u);
-                            tc_wait_ld_u32<16>(u);
+                    for (int i = 0; c > 0 && i < D / 32; ++i) {
+                        const uint32_t at = tO + (uint32_t)(kh * (D / 2) + 16 * i);
+                        uint32_t u[16];
+                        tc_ld16_nowait(at, u);
+                        tc_wait_ld_u32<16>(u);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * f);
-                            tc_st16(at, u);
-                        }
-                        weigh_all(false);
+                        for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * f);
+                        tc_st16(at, u);
                     }
                 }
                 l += sum;
-                tc_st32(tS, y);
+                if constexpr (C::kOwnP) {           // the scores are done with
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s_empty[h]);
+                    if (ns > 1) ok = ok && wt_wait(&p_empty[h], ns & 1u, bad);   // the last P's product
+                    tc_fence_after();
+                }
+                tc_st32(tP, y);
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -1007,7 +1030,8 @@ qd_status qd_attn_prompt(const void *q_dev, int64_t q_stride, const void *k_dev,
     a.offsets = offsets_dev, a.kv_offsets = kv_offsets_dev ? kv_offsets_dev : offsets_dev;
     a.N = n_tokens, a.M = n_kv_tokens, a.B = n_seqs, a.G = n_q_heads / n_kv_heads, a.kvh = n_kv_heads;
     a.wide_out = is_aligned(out_dev, 32) && (n_tokens == 1 || out_stride % 16 == 0);
-    a.tpt = p.tpt, a.scale2 = scale * 1.4426950408889634f;
+    a.tpt = p.tpt;
+    a.scale2 = scale == 0.f ? 1e-30f : scale * 1.4426950408889634f;   // (hidden scores are infinite: 0 times them would be NaN)
     if (p.list) {
         a.count = static_cast<int *>(workspace_dev);
         a.list = reinterpret_cast<int4 *>(static_cast<uint8_t *>(workspace_dev) + 256);

@@ -88,8 +88,8 @@ static int read_tensor(PyObject *t, Tensor *o) {
     return !PyErr_Occurred();
 }
 
-/* n contiguous int32 values, or None */
-static int read_ints(PyObject *t, int64_t n, const int32_t **to, const char *what) {
+/* n contiguous int32 values (any number, where n is below 0: *found then), or None */
+static int read_some_ints(PyObject *t, int64_t n, int64_t *found, const int32_t **to, const char *what) {
     *to = NULL;
     if (t == Py_None) return 1;
     Tensor x;
@@ -100,13 +100,18 @@ static int read_ints(PyObject *t, int64_t n, const int32_t **to, const char *wha
         if (x.shape[i] != 1 && x.stride[i] != count) ok = 0;
         count *= x.shape[i];
     }
+    if (n < 0 && x.nd == 1) n = *found = count;
     if (!ok || count != n) {
-        PyErr_Format(PyExc_ValueError, "%s must be %lld contiguous int32 values", what, (long long)n);
+        if (n < 0)
+            PyErr_Format(PyExc_ValueError, "%s must be one axis of contiguous int32 values", what);
+        else
+            PyErr_Format(PyExc_ValueError, "%s must be %lld contiguous int32 values", what, (long long)n);
         return 0;
     }
     *to = (const int32_t *)x.ptr;
     return 1;
 }
+static int read_ints(PyObject *t, int64_t n, const int32_t **to, const char *what) { return read_some_ints(t, n, NULL, to, what); }
 
 static int type_of(const Tensor *t, int *dtype) {
     if (t->type == t_bf16)
@@ -406,17 +411,6 @@ static int read_floats(PyObject *o, const char *what, int64_t n, int64_t *rows, 
     return fits(&t);
 }
 
-/* the values of a one-dimensional int32 tensor, or -1 */
-static int64_t length_of(PyObject *o) {
-    Tensor t;
-    if (!read_tensor(o, &t)) return -1;
-    if (t.nd != 1) {
-        bad("one axis is wanted");
-        return -1;
-    }
-    return t.shape[0];
-}
-
 /* rope(q, k, v, q_out, k_out, v_out, cos, sin, lengths, offsets, n_new, positions, mrope_h, q_gamma, k_gamma, eps, pages, page_table,
  * stream) */
 static PyObject *py_rope(PyObject *self, PyObject *const *a, Py_ssize_t nargs) {
@@ -449,8 +443,7 @@ static PyObject *py_rope(PyObject *self, PyObject *const *a, Py_ssize_t nargs) {
         return NULL;
     }
     int64_t B = 0;
-    if (a[8] != Py_None && (B = length_of(a[8])) < 0) return NULL;
-    if (!read_ints(a[8], B, &r.lengths, "lengths") || !read_ints(a[9], B + 1, &r.offsets, "offsets") ||
+    if (!read_some_ints(a[8], -1, &B, &r.lengths, "lengths") || !read_ints(a[9], B + 1, &r.offsets, "offsets") ||
         !read_ints(a[10], B, &r.n_new, "n_new") || !opt_int(a[12], 0, &r.mrope_h) ||
         !read_ints(a[11], r.mrope_h ? 3 * N : N, &r.positions, "positions"))
         return NULL;
@@ -499,12 +492,13 @@ static PyObject *py_prompt(PyObject *self, PyObject *const *a, Py_ssize_t nargs)
         bad("q, k, v and out must be bf16");
         return NULL;
     }
-    const int64_t B = length_of(a[4]) - 1;
-    if (B < 0) {
-        if (!PyErr_Occurred()) bad("offsets must be [sequences + 1]");
+    int64_t B = 0;
+    if (!read_some_ints(a[4], -1, &B, &offsets, "offsets")) return NULL;
+    if (--B < 0) {
+        bad("offsets must be [sequences + 1]");
         return NULL;
     }
-    if (!read_ints(a[4], B + 1, &offsets, "offsets") || !read_ints(a[5], B + 1, &kv_offsets, "kv_offsets") || !read_scale(a[6], D, &scale) ||
+    if ( !read_ints(a[5], B + 1, &kv_offsets, "kv_offsets") || !read_scale(a[6], D, &scale) ||
         !stream_of(a[9], a[0], &s, &dev))
         return NULL;
     if (!kv_offsets && M != N) {

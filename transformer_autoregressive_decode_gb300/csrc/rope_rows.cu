@@ -155,6 +155,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) qk_norm_rope_kernel(c
     constexpr int LPR = D / 16, RPW = 32 / LPR, HALF = D / 2, P = X::P, E = X::E, S = kRopeAhead<TI>;
     __shared__ uint4 ring[S][P][kRopeThreads];
     const int lane = threadIdx.x % LPR, in = (threadIdx.x & 31) / LPR;    // this lane's share of a row; the row's place among the warp's
+    pdl_wait();                                         // whatever wrote the rows
+    pdl_launch_dependents();                            // (they wait for the whole grid before they read)
     const int warp = __shfl_sync(0xffffffffu, (int)(blockIdx.x * (kRopeThreads / 32) + threadIdx.x / 32), 0);
     const int64_t x0 = (int64_t)warp * a.run, left = (int64_t)a.N * a.units - x0;
     if (left <= 0) return;
@@ -438,6 +440,15 @@ extern "C" qd_status qd_qk_norm_rope(const qd_rope_rows *x, void *cuda_stream) {
     const RopeFn fn = x->dtype == QD_F32 ? (x->out_dtype == QD_F32 ? rope_fn<float, float>(d, q8) : rope_fn<float, __nv_bfloat16>(d, q8))
                                          : (x->out_dtype == QD_F32 ? rope_fn<__nv_bfloat16, float>(d, q8)
                                                                    : rope_fn<__nv_bfloat16, __nv_bfloat16>(d, q8));
-    fn<<<grid, kRopeThreads, 0, static_cast<cudaStream_t>(cuda_stream)>>>(a);
-    return cudaGetLastError() == cudaSuccess ? QD_OK : QD_ECUDA;
+    // placed while a predecessor that allows it ends
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kRopeThreads);
+    cfg.stream = static_cast<cudaStream_t>(cuda_stream);
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, a) == cudaSuccess ? QD_OK : QD_ECUDA;
 }
