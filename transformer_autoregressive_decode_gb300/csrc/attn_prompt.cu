@@ -44,7 +44,7 @@ constexpr int kPtThreads = 640, kPtSoft = 512;
 constexpr int kPtRegsSoft = 104, kPtRegsRest = 64;
 static_assert(kPtSoft * kPtRegsSoft + (kPtThreads - kPtSoft) * kPtRegsRest <= kPtThreads * 96, "registers");
 constexpr uint32_t kPtBox = 128 * 128;        // 128 rows of 128 bytes, 128-byte swizzle
-constexpr uint32_t kPtS = 0;                  // tensor memory columns: S of the tiles, then O
+constexpr uint32_t kPtS = 0, kPtO = 256;      // tensor memory columns: S of the tiles (P of 64 keys over the first half of theirs), O
 constexpr int kPtKeys = 128;                  // of a chunk
 constexpr int kPtSlots = 4;                   // pairs in flight between the roles
 constexpr int kPtUsers = 19;                  // warps that read a slot
@@ -92,7 +92,7 @@ struct __align__(16) Pair {
 // The first chunk that the pair's first token does not see all of.
 __device__ __forceinline__ int first_edge(const Pair &p) { return p.lim0 > 0 ? p.lim0 / kPtKeys : 0; }
 
-struct Sequence {
+struct __align__(16) Sequence {
     int q0, n, k0, m;
 };
 __device__ __forceinline__ Sequence sequence(const PromptArgs &a, int b) {
@@ -188,7 +188,10 @@ struct OwnPlan {
     int load[kPtMaxCtas];
     int sums[8];
     // where the pairs are cut: all of them, the chunks of one key head before each, and this CTA's run
-    Pair pairs[kPtOwnPairs];
+    union {
+        Pair pairs[kPtOwnPairs];
+        Sequence seqs[kPtOwnPairs];           // until then
+    };
     int before[kPtOwnPairs + 1];
     int total, x0, x1;
     unsigned run, more;                       // of the Share
@@ -288,10 +291,11 @@ __device__ __forceinline__ Pair piece_at(const PromptArgs &a, const OwnPlan &w, 
 }
 __device__ __forceinline__ void plan_own(const PromptArgs &a, OwnPlan &w) {
     const int tid = threadIdx.x, lane = tid & 31;
-    Sequence s = {};
+    Sequence s;
     if (tid < a.B) {
         s = sequence(a, tid);
         w.first[tid + 1] = pairs_of(a, s);
+        w.seqs[tid] = s;
     }
     if (tid == 0) w.n = 0, w.most = 0, w.cut = false;
     if (tid < kPtOwnPairs) w.cost[tid] = -1;
@@ -330,8 +334,7 @@ __device__ __forceinline__ void plan_own(const PromptArgs &a, OwnPlan &w) {
             else
                 hi = mid;
         }
-        s = sequence(a, lo);
-        p = pair_of(a, s, tid - w.first[lo], 0);
+        p = pair_of(a, w.seqs[lo], tid - w.first[lo], 0);
         w.cost[tid] = p.most();
     }
     __syncthreads();
@@ -342,24 +345,20 @@ __device__ __forceinline__ void plan_own(const PromptArgs &a, OwnPlan &w) {
     }
     if (tid >= total) return;
     const int rank = rank_of(a, w, p, total);
-    int round = rank * a.kvh / grid, at = rank * a.kvh - round * grid;
-    for (int hk = 0; hk < a.kvh; ++hk) {
-        if ((round & 1 ? grid - 1 - at : at) == (int)blockIdx.x && round < kPtOwnRounds) {
-            p.hk = hk;
-            w.mine[round] = p;
-            atomicMax(&w.n, round + 1);       // (no round is left out before the last)
-        }
-        if (++at == grid) at = 0, ++round;
+    // this CTA's place in the rounds that the pair's key heads fall into
+    const int j0 = rank * a.kvh, j1 = j0 + a.kvh;
+    for (int round = j0 / grid; round * grid < j1 && round < kPtOwnRounds; ++round) {
+        const int j = round * grid + (round & 1 ? grid - 1 - (int)blockIdx.x : (int)blockIdx.x);
+        if (j < j0 || j >= j1) continue;
+        p.hk = j - j0;
+        w.mine[round] = p;
+        atomicMax(&w.n, round + 1);           // (no round is left out before the last)
     }
 }
 
 template <int D> struct PtCfg {
     static constexpr int KB = D / 64;                         // 64-wide blocks of head_dim
     static constexpr int kStages = 4 / KB;                    // of K and of V
-    // Heads of 64 leave columns for P beside S and O, so that the next S need not wait for P's product
-    static constexpr bool kOwnP = D == 64;
-    static constexpr uint32_t kP = kOwnP ? 384 : kPtS, kPHalf = kOwnP ? 32 : 64, kPTile = kOwnP ? 64 : 128;   // columns; of a half, of a tile
-    static constexpr uint32_t kO = 256, kOTile = kOwnP ? 64 : 128;
     static constexpr uint32_t kTile = KB * kPtBox;            // of Q, K or V
     static constexpr uint32_t kQ = 0;                         // Q [tile]
     static constexpr uint32_t kK = kQ + 2 * kTile;            // K [stage]
@@ -425,9 +424,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     uint64_t *slot_full = bars, *slot_empty = bars + 4;                                              // [slot]
     uint64_t *q_full = bars + 8, *q_empty = bars + 10, *s_full = bars + 12, *p_full = bars + 14;     // [tile]
     uint64_t *o_full = bars + 16, *o_empty = bars + 18;                                              // [tile]
-    uint64_t *s_empty = bars + 20;                                                                   // [tile]
     uint64_t *k_full = bars + 22, *k_empty = bars + 26, *v_full = bars + 30, *v_empty = bars + 34, *v_clean = bars + 38;   // [stage]
-    uint64_t *drain = bars + 42, *p_empty = bars + 45;                                               // p_empty: [tile]
+    uint64_t *drain = bars + 42;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 43);
     volatile int *bad = reinterpret_cast<volatile int *>(bars + 44);
 
@@ -436,7 +434,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         for (int i = 0; i < kPtSlots; ++i) mbar_init(&slot_full[i], 1), mbar_init(&slot_empty[i], kPtUsers);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], 1), mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 8);
-            mbar_init(&o_full[i], 1), mbar_init(&o_empty[i], 8), mbar_init(&s_empty[i], 8), mbar_init(&p_empty[i], 1);
+            mbar_init(&o_full[i], 1), mbar_init(&o_empty[i], 8);
         }
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(&k_full[i], 1), mbar_init(&k_empty[i], 1);
@@ -561,17 +559,13 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         constexpr uint32_t kBox16 = kPtBox / 16;
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         int kc = 0;                                 // chunks before this pair's
-        uint32_t nq[2] = {0, 0}, n_s[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0};   // of either tile: pairs, S's, P's, pairs begun in O
+        uint32_t nq[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0};   // of either tile: pairs, P's, pairs begun in O
         bool ok = true, begun[2] = {false, false};  // the pair's first S is issued
         Pair p = pair_at(0);
         // S of tile h, chunk c of pair x whose first chunk is the kx-th; `other`: the other tile's S of that chunk is issued, or none is wanted
         auto issue_s = [&](int h, int c, const Pair &x, int kx, bool other) {
             const int st = (kx + c) % C::kStages;
             if (c == 0) ok = ok && wt_wait(&q_full[h], nq[h]++ & 1u, bad);
-            if constexpr (C::kOwnP) {
-                if (n_s[h] > 0) ok = ok && wt_wait(&s_empty[h], (n_s[h] + 1) & 1u, bad);
-                ++n_s[h];
-            }
             ok = ok && wt_wait(&k_full[st], (uint32_t)((kx + c) / C::kStages) & 1u, bad);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) return;
@@ -597,7 +591,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 if (no[h] > 0) ok = ok && wt_wait(&o_empty[h], (no[h] + 1) & 1u, bad);
                 ++no[h];
             }
-            const uint32_t d = tm + C::kO + C::kOTile * h, pt = tm + C::kP + C::kPTile * h;
+            const uint32_t d = tm + kPtO + 128u * h, pt = tm + kPtS + 128u * h;
             const uint64_t v = dV + st * KB * kBox16;
             ok = ok && wt_wait(&v_full[st], ph, bad) && wt_wait(&v_clean[st], ph, bad);
             ok = ok && wt_wait(&p_full[h], np[h] & 1u, bad);
@@ -606,8 +600,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
-                for (int i = 0; i < kPtKeys / 16; ++i) tc_mma_ts(d, pt + 8u * (i & 3) + C::kPHalf * (i >> 2), v + i * 128, idesc_o, (c | i) ? 1u : 0u);
-                if constexpr (C::kOwnP) tc_commit(&p_empty[h]);
+                for (int i = 0; i < kPtKeys / 16; ++i) tc_mma_ts(d, pt + 8u * i + 32u * (i >> 2), v + i * 128, idesc_o, (c | i) ? 1u : 0u);
                 if (h == 1 || p.n1 <= c) tc_commit(&v_empty[st]);
                 if (c + 1 == p.n(h)) tc_commit(&o_full[h]);
             }
@@ -629,11 +622,10 @@ __global__ void __launch_bounds__(kPtThreads, 1)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     if (!ok || c >= p.n(h)) continue;
-                    if (C::kOwnP && c + 1 < p.n(h)) issue_s(h, c + 1, p, kc, h == 1 || p.n1 <= c + 1);
-                    if (ok) issue_o(h, c);
+                    issue_o(h, c);
                     if (!ok) continue;
                     if (c + 1 < p.n(h)) {
-                        if (!C::kOwnP) issue_s(h, c + 1, p, kc, h == 1 || p.n1 <= c + 1);
+                        issue_s(h, c + 1, p, kc, h == 1 || p.n1 <= c + 1);
                     } else {
                         if (x.hk == -2) x = pair_at(it + 1);
                         if (x.hk >= 0 && x.n(h) > 0) {
@@ -700,8 +692,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         // ---- softmax: tile h, row r of it, the keys' half kh of every chunk; the two warps that share rows keep one reference
         const int h = warp >> 3, kh = (warp >> 2) & 1, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        const uint32_t tS = tmem + kPtS + 128u * h + 64u * kh + lanes, tO = tmem + C::kO + C::kOTile * h + lanes;
-        const uint32_t tP = tmem + C::kP + C::kPTile * h + C::kPHalf * kh + lanes;
+        const uint32_t tS = tmem + kPtS + 128u * h + 64u * kh + lanes, tO = tmem + kPtO + 128u * h + lanes;
         const int token = r / a.G, head = r - token * a.G, pair_bar = 1 + h * 4 + quarter;
         float *row_max = reinterpret_cast<float *>(sm + C::kRow) + (h * 2) * 128 + r, *row_sum = row_max + 4 * 128;
         const bool in_tile = token < a.tpt;
@@ -759,10 +750,6 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     if (edge) hide(x, left, none), hide(x + 32, left - 32, none);
                     const float m = of_row(largest<64>(x, a.scale2));
                     all_none = m == -INFINITY;      // (scores of -infinity alone: the reference stays)
-                    if constexpr (C::kOwnP) {
-                        if (ns > 1) ok = ok && wt_wait(&p_empty[h], ns & 1u, bad);
-                        tc_fence_after();
-                    }
                     float f = 1.f;
                     if (m > ref) {
                         f = ref == -INFINITY ? 0.f : ex2(ref - m);
@@ -782,14 +769,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     }
                 }
                 l += sum;
-                if constexpr (C::kOwnP) {           // the scores are done with
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&s_empty[h]);
-                    if (ns > 1) ok = ok && wt_wait(&p_empty[h], ns & 1u, bad);   // the last P's product
-                    tc_fence_after();
-                }
-                tc_st32(tP, y);
+                tc_st32(tS, y);
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
