@@ -8,25 +8,34 @@
 // of an MMA, a few rows unused where G does not divide 128), a CTA works a pair of them against the same chunks of 128 keys, one tile's
 // products under the other's softmax:
 //   S = Q K^T          128 x 128 fp32 in tensor memory; Q and K from shared memory, by TMA
-//   softmax            thread = row; P as bf16 over S's own columns, 64 keys at a time
-//   O += P V           P from tensor memory, V from shared memory (keys x dims: the MN-major operand), 64 keys at a time
-// The reference is the largest of a row's first 64 scores and moves only when the sum of 64 weights passes 2^80 (bf16 weights
-// have fp32's range), so the scores are read once and O stays where it is.
+//   softmax            two threads a row, 64 keys each; P as bf16 over the first half of those keys' S columns
+//   O += P V           P from tensor memory, V from shared memory (keys x dims: the MN-major operand)
+// The reference comes from 32 of a row's first scores and moves only when the sum of 64 weights passes 2^40 (bf16 weights have
+// fp32's range; 2^40 leaves V as much as 2^87), so the scores are read once and O stays where it is.
 //
 // P is one bf16 part (a weight keeps 8 bits): a second part takes half as many products again, and its rounding, unbiased and
-// independent from key to key, is below the rounding of a bf16 result (measured against 64 bits, 2-norm: see the tests' bounds).
-// The sum is that of the weights before their rounding, in fp32.
+// independent from key to key, adds to that of a bf16 result about as much again (2-norm against 64 bits: 1.8e-3 to 2.3e-3, the result's own
+// rounding 1.6e-3).  The sum is that of the weights before their rounding, in fp32.
 //
-// What a row does not see never reaches it: scores are selected, not added to a mask, and a V row that is not finite among
+// What a row does not see never reaches it: hidden scores are replaced, not added to, and a V row that is not finite among
 // the chunks that some rows see only in part is zeroed in shared memory and added by the rows that see it (0 x infinity is
 // NaN).  Two warps look those chunks through while their scores are worked out.
 //
-// Pairs differ in length, and only the device knows the lengths.  Up to a pair per SM each CTA finds its own; beyond, attn_prompt_plan_kernel
-// sorts the pairs, longest first, and the CTAs take them from a counter.
+// Pairs differ in length, and only the device knows the lengths.  Few pairs (OwnPlan) every CTA ranks for itself, longest first, and takes those of
+// its place in each round, there and back; or, where few pairs are long, all CTAs take equal runs of chunks, the pieces of a pair going
+// through memory to attn_prompt_join_kernel.  Many are sorted by attn_prompt_plan_kernel, and the CTAs take them from a counter.
 //
-// Roles (384 threads): warps 0-3 and 4-7 the softmax of the two tiles, warp 8 owns the tensor memory and issues the MMAs, warp 9 takes the
-// pairs and loads, warps 10 and 11 look V through.  Every wait is bounded; where one expires the pair's results become NaN and the roles
-// run to their ends.
+// Measured: one prompt of 8192 under 32 heads, 550 GFLOP, 355 us (1550 TFLOP/s, 0.81 of the measured peak): a pair of tiles takes about 2700 clocks
+// a chunk where its products take 2048, because a tile's softmax (1200: 64 exponentials a thread are 512 at the unit's rate, the rest
+// issue slots, the way from and to tensor memory and the vote of a row's two warps) and its two products (1024, and 400 until they
+// have begun and been noticed) follow one another, and S and O of two tiles fill the tensor memory of head_dim 128.  Heads of 64
+// leave columns for P beside S, so that the next S need not wait for P's product: 288 us where this form takes 267 (both tiles' softmaxes
+// then meet on the same units).  8 x 512 tokens, 16 of 8 heads, 50 MB, 20 us: the start (plan 1.2 us, first loads 1.2), 4 chunks a CTA, the
+// results' way out (4 us).
+//
+// Roles (640 threads): warps 0-7 and 8-15 the softmax of the two tiles, warp 16 owns the tensor memory and issues the MMAs, warp 17 takes the
+// pairs and loads, warps 18 and 19 look V through.  Registers a thread: 96 at launch, then 104 and 64.  Every wait is bounded; where one
+// expires the pair's results become NaN and the roles run to their ends.
 #include <cuda.h>
 
 #include <algorithm>
@@ -49,7 +58,7 @@ constexpr int kPtKeys = 128;                  // of a chunk
 constexpr int kPtSlots = 4;                   // pairs in flight between the roles
 constexpr int kPtUsers = 19;                  // warps that read a slot
 constexpr int kPtBuckets = 1024;              // of the plan's sort
-constexpr float kPtTop = 1.2e24f;             // 2^80
+constexpr float kPtTop = 1.0995116e12f;       // 2^40
 
 struct PromptArgs {
     const uint8_t *v;
@@ -367,7 +376,7 @@ template <int D> struct PtCfg {
     static constexpr uint32_t kRow = kSlot + kPtSlots * sizeof(Pair);   // rows' maxima, sums [of either][tile][half][128]
     static constexpr uint32_t kOwn = kRow + 2 * 2 * 2 * 128 * 4;
     static constexpr uint32_t kBar = kOwn + (sizeof(OwnPlan) + 15) / 16 * 16;
-    static constexpr uint32_t kBars = 48;
+    static constexpr uint32_t kBars = 56;
     static constexpr uint32_t kSmem = 1024 + kBar + kBars * 8;
 };
 static_assert(sizeof(Pair) == 32, "two loads of 16 bytes");
@@ -442,6 +451,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         }
         mbar_init(drain, 1);
         *bad = 0;
+        for (int i = 0; i < 16; ++i) reinterpret_cast<int *>(bars + 46)[i] = 0;
         fence_barrier_init();
     }
     if (warp == 17 && lane < 3) {
@@ -693,7 +703,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         const int h = warp >> 3, kh = (warp >> 2) & 1, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const uint32_t tS = tmem + kPtS + 128u * h + 64u * kh + lanes, tO = tmem + kPtO + 128u * h + lanes;
-        const int token = r / a.G, head = r - token * a.G, pair_bar = 1 + h * 4 + quarter;
+        const int token = r / a.G, head = r - token * a.G, pair_bar = 1 + h * 4 + quarter;   // (every meeting there is of one kind)
         float *row_max = reinterpret_cast<float *>(sm + C::kRow) + (h * 2) * 128 + r, *row_sum = row_max + 4 * 128;
         const bool in_tile = token < a.tpt;
         const uint32_t none = a.scale2 < 0.f ? 0x7f800000u : 0xff800000u;       // -infinity once it is scaled
@@ -721,7 +731,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 // the larger of both warps' largest scores
                 auto of_row = [&](float m) {
                     row_max[kh * 128] = m;
-                    named_sync(pair_bar, 64);
+                    (void)named_sync_or(pair_bar, 64, false);
                     return fmaxf(m, row_max[(kh ^ 1) * 128]);
                 };
                 // one pass as a rule; another where a weight has outgrown its room
@@ -777,7 +787,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             }
             // ---- the rows' results, half their dims each
             row_sum[kh * 128] = l;
-            named_sync(pair_bar, 64);
+            (void)named_sync_or(pair_bar, 64, false);
             l = row_sum[0] + row_sum[128];
             if (n > 0) {
                 ok = ok && wt_wait(&o_full[h], no & 1u, bad);
@@ -845,6 +855,15 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             }
             done_with(it);
         }
+        // The two warps of a row meet at barriers that wait for both.  One that leaves early, because a wait has expired, meets the other
+        // until that one has left, too; each one's leaving is one arrival more, which frees the other if it waits there.
+        volatile int *left = reinterpret_cast<volatile int *>(bars + 46);
+        if (lane == 0) left[warp] = 1;
+        __threadfence_block();
+        __syncwarp();
+        asm volatile("bar.arrive %0, 64;" ::"r"(pair_bar) : "memory");
+        if (__any_sync(0xffffffffu, *bad != 0))
+            while (__any_sync(0xffffffffu, left[warp ^ 4] == 0)) (void)named_sync_or(pair_bar, 64, false);
     }
     tc_fence_before();
     __syncthreads();
@@ -941,7 +960,8 @@ qd_status plan_prompt(int n_tokens, int n_kv_tokens, int n_seqs, int n_q_heads, 
     p->list = pairs > kPtOwnPairs || n_seqs > kPtOwnPairs || pairs * n_kv_heads > (int64_t)kPtOwnRounds * sms;
     p->ctas = (unsigned)std::min<int64_t>(pairs * n_kv_heads, sms);
     // few pairs of long sequences: every SM has a CTA, and room for two pieces
-    p->join = !p->list && pairs * n_kv_heads <= sms + sms / 4 && n_kv_tokens >= kPtCutKeys * n_seqs && sms <= kPtMaxCtas;
+    p->join = !p->list && pairs * n_kv_heads <= sms + sms / 4 && n_kv_tokens >= kPtCutKeys * n_seqs && sms <= kPtMaxCtas &&
+              pairs * n_kv_heads * (n_kv_tokens / kPtKeys + 1) < (int64_t(1) << 30);   // (the chunks are counted in an int)
     p->bytes = p->list ? 256 + (size_t)pairs * 32 : 0;
     if (p->join) {
         p->ctas = (unsigned)sms;

@@ -219,9 +219,10 @@ static int find_scratch(long dev, void *stream, size_t need, void **ws, size_t *
     return 1;
 }
 
-/* q and out: [streams, tokens, q_heads, head_dim] of one type, heads contiguous */
+/* q and out: [streams, tokens, q_heads, head_dim] of one type, heads contiguous; B < 0: any number of streams */
 static int read_queries(PyObject *qo, PyObject *oo, int64_t B, int64_t D, Tensor *q, Tensor *o, int *dtype) {
     if (!read_tensor(qo, q) || !read_tensor(oo, o)) return 0;
+    if (B < 0) B = q->nd == 4 ? q->shape[0] : 0;
     if (q->nd != 4 || o->nd != 4 || q->type != o->type || q->shape[0] != B || q->shape[3] != D || o->shape[0] != B ||
         o->shape[1] != q->shape[1] || o->shape[2] != q->shape[2] || o->shape[3] != D) {
         PyErr_Format(PyExc_ValueError, "q and out must be [%lld, tokens, q_heads, %lld] of one type", (long long)B, (long long)D);
@@ -306,7 +307,7 @@ static int read_table(PyObject *o, int64_t streams, const int32_t **to, int64_t 
 static PyObject *py_paged(PyObject *self, PyObject *const *a, Py_ssize_t nargs) {
     NARGS(11)
     const qd_kv_cache *c = (const qd_kv_cache *)PyLong_AsVoidPtr(a[1]);
-    Tensor q, o, t;
+    Tensor q, o;
     const int32_t *lengths, *n_new, *table;
     void *s, *ws = NULL;
     long dev;
@@ -314,9 +315,11 @@ static PyObject *py_paged(PyObject *self, PyObject *const *a, Py_ssize_t nargs) 
     int64_t table_stride;
     size_t have = 0;
     float scale;
-    if (PyErr_Occurred() || !read_tensor(a[0], &t)) return NULL;
-    const int64_t D = c->head_dim, B = t.nd == 4 ? t.shape[0] : 0;
-    if (!read_queries(a[0], a[4], B, D, &q, &o, &dtype) || !read_table(a[2], B, &table, &table_stride, &per)) return NULL;
+    if (PyErr_Occurred()) return NULL;
+    const int64_t D = c->head_dim;
+    if (!read_queries(a[0], a[4], -1, D, &q, &o, &dtype)) return NULL;
+    const int64_t B = q.shape[0];
+    if (!read_table(a[2], B, &table, &table_stride, &per)) return NULL;
     const int64_t named = (int64_t)per * c->smax;
     if (!opt_int(a[6], named > INT32_MAX ? INT32_MAX : (int)named, &most) || !read_scale(a[7], D, &scale) ||
         !read_ints(a[3], B, &lengths, "lengths") || !read_ints(a[5], B, &n_new, "n_new") || !stream_of(a[10], a[0], &s, &dev))

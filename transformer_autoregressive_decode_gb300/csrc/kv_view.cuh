@@ -141,6 +141,8 @@ struct Stretch {
 // Whether `out`'s rows lie over none of p's: elsewhere, or in the gaps between rows of the same pitch.
 inline bool rows_beside(const void *out, int64_t oe, int64_t on, int64_t os, int64_t oi, const void *p, int64_t pe, int64_t pn, int64_t ps,
                         int64_t pi) {
+    constexpr int64_t kMost = int64_t(1) << 60;   // no address is as far
+    if ((on > 1 && os > kMost / oe / (on - 1)) || (pn > 1 && ps > kMost / pe / (pn - 1))) return false;
     if (!Stretch(out, oe, on, os, oi).meets(Stretch(p, pe, pn, ps, pi))) return true;
     const int64_t pitch = on > 1 ? os * oe : pn > 1 ? ps * pe : 0;
     if (pitch <= 0 || (on > 1 && pn > 1 && ps * pe != pitch)) return false;
