@@ -8,9 +8,9 @@
 // of an MMA, a few rows unused where G does not divide 128), a CTA works a pair of them against the same chunks of 128 keys, one tile's
 // products under the other's softmax:
 //   S = Q K^T          128 x 128 fp32 in tensor memory; Q and K from shared memory, by TMA
-//   softmax            two threads a row, 64 keys each; P as bf16 over the first half of those keys' S columns
+//   softmax            thread = row; P as bf16 over S's own columns, 64 keys' in the first half of theirs
 //   O += P V           P from tensor memory, V from shared memory (keys x dims: the MN-major operand)
-// The reference comes from 32 of a row's first scores and moves only when the sum of 64 weights passes 2^40 (bf16 weights have
+// The reference comes from a row's first 32 scores and moves only when the sum of 128 weights passes 2^40 (bf16 weights have
 // fp32's range; 2^40 leaves V as much as 2^87), so the scores are read once and O stays where it is.
 //
 // P is one bf16 part (a weight keeps 8 bits): a second part takes half as many products again, and its rounding, unbiased and
@@ -25,16 +25,17 @@
 // its place in each round, there and back; or, where few pairs are long, all CTAs take equal runs of chunks, the pieces of a pair going
 // through memory to attn_prompt_join_kernel.  Many are sorted by attn_prompt_plan_kernel, and the CTAs take them from a counter.
 //
-// Measured: one prompt of 8192 under 32 heads, 550 GFLOP, 355 us (1550 TFLOP/s, 0.81 of the measured peak): a pair of tiles takes about 2700 clocks
-// a chunk where its products take 2048, because a tile's softmax (1200: 64 exponentials a thread are 512 at the unit's rate, the rest
-// issue slots, the way from and to tensor memory and the vote of a row's two warps) and its two products (1024, and 400 until they
-// have begun and been noticed) follow one another, and S and O of two tiles fill the tensor memory of head_dim 128.  Heads of 64
-// leave columns for P beside S, so that the next S need not wait for P's product: 288 us where this form takes 267 (both tiles' softmaxes
-// then meet on the same units).  8 x 512 tokens, 16 of 8 heads, 50 MB, 20 us: the start (plan 1.2 us, first loads 1.2), 4 chunks a CTA, the
-// results' way out (4 us).
+// Measured: one prompt of 8192 under 32 heads, 550 GFLOP, 346 us (1590 TFLOP/s, 0.83 of the measured peak): a pair of tiles takes about 2650 clocks
+// a chunk where its products take 2048, because a tile's softmax (1150: 128 exponentials a thread are 512 at the unit's rate, the rest
+// issue slots, the way from and to tensor memory and the vote) and its two products (1024, and 400 until they have begun and been
+// noticed) follow one another, and S and O of two tiles fill the tensor memory of head_dim 128.  Not better: two warps a tile's rows, 64 keys each, which
+// have to agree on the reference (357 us; short prompts 1 to 2 % faster); the product of the first 64 keys begun while the others are
+// weighed (397); for heads of 64, P in columns of its own, so that the next S need not wait for P's product (288 us where this form
+// takes 266: both tiles' softmaxes then meet on the same units).  8 x 512 tokens, 16 of 8 heads, 50 MB, 20.8 us: the start (plan 1.2 us, first
+// loads 1.2), 4 chunks a CTA, the results' way out (4 us).
 //
-// Roles (640 threads): warps 0-7 and 8-15 the softmax of the two tiles, warp 16 owns the tensor memory and issues the MMAs, warp 17 takes the
-// pairs and loads, warps 18 and 19 look V through.  Registers a thread: 96 at launch, then 104 and 64.  Every wait is bounded; where one
+// Roles (384 threads): warps 0-3 and 4-7 the softmax of the two tiles, warp 8 owns the tensor memory and issues the MMAs, warp 9 takes the
+// pairs and loads, warps 10 and 11 look V through.  Registers a thread: 168 at launch, then 208 and 88.  Every wait is bounded; where one
 // expires the pair's results become NaN and the roles run to their ends.
 #include <cuda.h>
 
@@ -49,14 +50,14 @@ namespace qd {
 
 namespace {
 
-constexpr int kPtThreads = 640, kPtSoft = 512;
-constexpr int kPtRegsSoft = 104, kPtRegsRest = 64;
-static_assert(kPtSoft * kPtRegsSoft + (kPtThreads - kPtSoft) * kPtRegsRest <= kPtThreads * 96, "registers");
+constexpr int kPtThreads = 384, kPtSoft = 256;
+constexpr int kPtRegsSoft = 208, kPtRegsRest = 88;
+static_assert(kPtSoft * kPtRegsSoft + (kPtThreads - kPtSoft) * kPtRegsRest <= kPtThreads * 168, "registers");
 constexpr uint32_t kPtBox = 128 * 128;        // 128 rows of 128 bytes, 128-byte swizzle
 constexpr uint32_t kPtS = 0, kPtO = 256;      // tensor memory columns: S of the tiles (P of 64 keys over the first half of theirs), O
 constexpr int kPtKeys = 128;                  // of a chunk
 constexpr int kPtSlots = 4;                   // pairs in flight between the roles
-constexpr int kPtUsers = 19;                  // warps that read a slot
+constexpr int kPtUsers = 11;                  // warps that read a slot
 constexpr int kPtBuckets = 1024;              // of the plan's sort
 constexpr float kPtTop = 1.0995116e12f;       // 2^40
 
@@ -308,7 +309,7 @@ __device__ __forceinline__ void plan_own(const PromptArgs &a, OwnPlan &w) {
     }
     if (tid == 0) w.n = 0, w.most = 0, w.cut = false;
     if (tid < kPtOwnPairs) w.cost[tid] = -1;
-    if (a.join && tid < kPtMaxCtas) w.load[tid] = 0;
+    for (int i = tid; a.join && i < kPtMaxCtas; i += kPtThreads) w.load[i] = 0;
     __syncthreads();
     if (tid < 32) {                           // running sums, 8 sequences a lane
         int v[kPtOwnPairs / 32], sum = 0;
@@ -373,10 +374,9 @@ template <int D> struct PtCfg {
     static constexpr uint32_t kK = kQ + 2 * kTile;            // K [stage]
     static constexpr uint32_t kV = kK + kStages * kTile;    // V [stage]
     static constexpr uint32_t kSlot = kV + kStages * kTile;
-    static constexpr uint32_t kRow = kSlot + kPtSlots * sizeof(Pair);   // rows' maxima, sums [of either][tile][half][128]
-    static constexpr uint32_t kOwn = kRow + 2 * 2 * 2 * 128 * 4;
+    static constexpr uint32_t kOwn = kSlot + kPtSlots * sizeof(Pair);
     static constexpr uint32_t kBar = kOwn + (sizeof(OwnPlan) + 15) / 16 * 16;
-    static constexpr uint32_t kBars = 56;
+    static constexpr uint32_t kBars = 46;
     static constexpr uint32_t kSmem = 1024 + kBar + kBars * 8;
 };
 static_assert(sizeof(Pair) == 32, "two loads of 16 bytes");
@@ -442,8 +442,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kPtSlots; ++i) mbar_init(&slot_full[i], 1), mbar_init(&slot_empty[i], kPtUsers);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], 1), mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 8);
-            mbar_init(&o_full[i], 1), mbar_init(&o_empty[i], 8);
+            mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], 1), mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 4);
+            mbar_init(&o_full[i], 1), mbar_init(&o_empty[i], 4);
         }
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(&k_full[i], 1), mbar_init(&k_empty[i], 1);
@@ -451,16 +451,15 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         }
         mbar_init(drain, 1);
         *bad = 0;
-        for (int i = 0; i < 16; ++i) reinterpret_cast<int *>(bars + 46)[i] = 0;
         fence_barrier_init();
     }
-    if (warp == 17 && lane < 3) {
+    if (warp == 9 && lane < 3) {
         const CUtensorMap *m = lane == 0 ? &mq : lane == 1 ? &mk : &mv;
         asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
     }
     // the predecessor first, the tensor memory then: held while waiting it could be what a predecessor's CTA on this SM waits for
     pdl_wait();
-    if (warp == 16) {
+    if (warp == 8) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
@@ -485,7 +484,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         if (lane == 0) mbar_arrive(&slot_empty[i % kPtSlots]);
     };
 
-    if (warp == 17) {
+    if (warp == 9) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPtRegsRest));
         // ---- the pairs, and their loads (the whole warp walks along; one lane issues)
         int kc = 0, nq[2] = {0, 0}, next = (int)blockIdx.x;
@@ -558,7 +557,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 (void)mbar_wait_bounded(&v_full[i], (uint32_t)(uses + 1) & 1u, 20000000ull);
             }
         }
-    } else if (warp == 16) {
+    } else if (warp == 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPtRegsRest));
         // ---- the MMAs: always a tile's O followed by its next S, which may be the next pair's first
         constexpr uint32_t base = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(128 >> 4) << 24);
@@ -654,7 +653,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         if (elect_one()) tc_commit(drain);
         (void)mbar_wait_bounded(drain, 0u, 20000000ull);
         __syncwarp();
-    } else if (warp >= 18) {
+    } else if (warp >= 10) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPtRegsRest));
         // ---- V of chunks that some rows see in part: what is not finite becomes zero, and is noted
         int kc = 0;
@@ -669,7 +668,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 if (c >= edge) {
-                    uint4 *tile = reinterpret_cast<uint4 *>(sm + C::kV + st * C::kTile) + (warp - 18) * 32 + lane;
+                    uint4 *tile = reinterpret_cast<uint4 *>(sm + C::kV + st * C::kTile) + (warp - 10) * 32 + lane;
                     constexpr int kPieces = KB * 128 * 8;
                     uint32_t acc[4] = {0, 0, 0, 0};
 #pragma unroll 8
@@ -699,12 +698,11 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPtRegsSoft));
-        // ---- softmax: tile h, row r of it, the keys' half kh of every chunk; the two warps that share rows keep one reference
-        const int h = warp >> 3, kh = (warp >> 2) & 1, quarter = warp & 3, r = quarter * 32 + lane;
+        // ---- softmax: tile h, row r of it
+        const int h = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        const uint32_t tS = tmem + kPtS + 128u * h + 64u * kh + lanes, tO = tmem + kPtO + 128u * h + lanes;
-        const int token = r / a.G, head = r - token * a.G, pair_bar = 1 + h * 4 + quarter;   // (every meeting there is of one kind)
-        float *row_max = reinterpret_cast<float *>(sm + C::kRow) + (h * 2) * 128 + r, *row_sum = row_max + 4 * 128;
+        const uint32_t tS = tmem + kPtS + 128u * h + lanes, tO = tmem + kPtO + 128u * h + lanes;
+        const int token = r / a.G, head = r - token * a.G;
         const bool in_tile = token < a.tpt;
         const uint32_t none = a.scale2 < 0.f ? 0x7f800000u : 0xff800000u;       // -infinity once it is scaled
         uint32_t ns = 0, no = 0;                    // S's, O's so far
@@ -723,42 +721,38 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 ok = ok && wt_wait(&s_full[h], ns & 1u, bad);
                 ++ns;
                 tc_fence_after();
-                const int left = lim - c * kPtKeys - 64 * kh;
-                const bool edge = lim_all < c * kPtKeys + 64 * kh + 64;
-                uint32_t x[64], y[32];
+                const int left = lim - c * kPtKeys;
+                const bool edge = lim_all < (c + 1) * kPtKeys;
+                uint32_t x[128], y[64];
                 float sum;
                 bool all_none = false;
-                // the larger of both warps' largest scores
-                auto of_row = [&](float m) {
-                    row_max[kh * 128] = m;
-                    (void)named_sync_or(pair_bar, 64, false);
-                    return fmaxf(m, row_max[(kh ^ 1) * 128]);
-                };
                 // one pass as a rule; another where a weight has outgrown its room
 #pragma unroll 1
                 while (true) {
                     tc_ld32_nowait(tS, x);
                     tc_wait_ld_u32<32>(x);
-                    tc_ld32_nowait(tS + 32u, x + 32);           // arrives under the work on the first
+#pragma unroll
+                    for (int i = 1; i < 4; ++i) tc_ld32_nowait(tS + 32u * i, x + 32 * i);           // arrive under the work on the first
                     if (edge) hide(x, left, none);
-                    // the first chunk: 16 scores of either warp set the reference, which is near enough as a rule
-                    if (ref_wanted) ref = of_row(largest<16>(x, a.scale2)), ref_wanted = false;
+                    // the first chunk: 32 scores set the reference, which is near enough as a rule
+                    if (ref_wanted) ref = largest<32>(x, a.scale2), ref_wanted = false;
                     const float rf = ref == -INFINITY ? 0.f : -ref;
                     uint64_t la = pk(0.f, 0.f), lb = la;
                     weigh(x, a.scale2, rf, y, la, lb);
-                    tc_wait_ld_u32<32>(x + 32);
-                    if (edge) hide(x + 32, left - 32, none);
-                    weigh(x + 32, a.scale2, rf, y + 16, la, lb);
+                    tc_wait_ld_u32<96>(x + 32);
+                    if (edge) hide(x + 32, left - 32, none), hide(x + 64, left - 64, none), hide(x + 96, left - 96, none);
+#pragma unroll
+                    for (int i = 1; i < 4; ++i) weigh(x + 32 * i, a.scale2, rf, y + 16 * i, la, lb);
                     float l0, l1;
                     unpk(add2(la, lb), l0, l1);
                     sum = l0 + l1;
-                    if (!named_sync_or(pair_bar, 64, live && (sum > kPtTop || (ref == -INFINITY && left > 0 && !all_none)))) break;
+                    if (!__any_sync(0xffffffffu, live && (sum > kPtTop || (ref == -INFINITY && left > 0 && !all_none)))) break;
                     // the scores again: they stand until their weights are written
-                    tc_ld32_nowait(tS, x);
-                    tc_ld32_nowait(tS + 32u, x + 32);
-                    tc_wait_ld_u32<64>(x);
-                    if (edge) hide(x, left, none), hide(x + 32, left - 32, none);
-                    const float m = of_row(largest<64>(x, a.scale2));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) tc_ld32_nowait(tS + 32u * i, x + 32 * i);
+                    tc_wait_ld_u32<128>(x);
+                    if (edge) hide(x, left, none), hide(x + 32, left - 32, none), hide(x + 64, left - 64, none), hide(x + 96, left - 96, none);
+                    const float m = largest<128>(x, a.scale2);
                     all_none = m == -INFINITY;      // (scores of -infinity alone: the reference stays)
                     float f = 1.f;
                     if (m > ref) {
@@ -766,10 +760,10 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                         ref = m;
                         l *= f;
                     }
-                    // O holds the chunks before, whose products are done (this S came behind them); half its columns each
+                    // O holds the chunks before, whose products are done (this S came behind them)
 #pragma unroll 1
-                    for (int i = 0; c > 0 && i < D / 32; ++i) {
-                        const uint32_t at = tO + (uint32_t)(kh * (D / 2) + 16 * i);
+                    for (int i = 0; c > 0 && i < D / 16; ++i) {
+                        const uint32_t at = tO + (uint32_t)(16 * i);
                         uint32_t u[16];
                         tc_ld16_nowait(at, u);
                         tc_wait_ld_u32<16>(u);
@@ -779,16 +773,14 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     }
                 }
                 l += sum;
-                tc_st32(tS, y);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tc_st16(tS + 64u * (i >> 1) + 16u * (i & 1), y + 16 * i);
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[h]);
             }
-            // ---- the rows' results, half their dims each
-            row_sum[kh * 128] = l;
-            (void)named_sync_or(pair_bar, 64, false);
-            l = row_sum[0] + row_sum[128];
+            // ---- the rows' results
             if (n > 0) {
                 ok = ok && wt_wait(&o_full[h], no & 1u, bad);
                 ++no;
@@ -799,18 +791,18 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             // no key gives zeros; keys whose scores are all -infinity NaN, as the formula does
             const float by = (lim <= 0 ? 0.f : l == 0.f ? __uint_as_float(0x7fc00000u) : 1.f / l) + fail;
             const uint32_t odd = n > 0 ? *reinterpret_cast<volatile uint32_t *>(&slot_of(it).odd) : 0u;
-            uint8_t *dst = a.out + (int64_t)(p.q0 + tt) * a.o_token + (int64_t)(p.head() * a.G + head) * (2 * D) + kh * D;
-            uint32_t u[D / 2];
+            uint8_t *dst = a.out + (int64_t)(p.q0 + tt) * a.o_token + (int64_t)(p.head() * a.G + head) * (2 * D);
+            uint32_t u[D];
             if (n > 0) {
 #pragma unroll
-                for (int i = 0; i < D / 64; ++i) tc_ld32_nowait(tO + (uint32_t)(kh * (D / 2) + 32 * i), u + 32 * i);
-                tc_wait_ld_u32<D / 2>(u);
+                for (int i = 0; i < D / 32; ++i) tc_ld32_nowait(tO + 32u * i, u + 32 * i);
+                tc_wait_ld_u32<D>(u);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&o_empty[h]);        // the next pair's products may begin
             } else {
 #pragma unroll
-                for (int e = 0; e < D / 2; ++e) u[e] = 0;
+                for (int e = 0; e < D; ++e) u[e] = 0;
             }
             if (odd) {
                 // the values that were taken out, by the rows that see them
@@ -819,9 +811,9 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     if (!((odd >> k) & 1u)) continue;
                     const int j0 = (first_edge(p) + k) * kPtKeys, j1 = min(lim, j0 + kPtKeys);
                     for (int j = j0; live && j < j1; ++j) {
-                        const uint16_t *v = reinterpret_cast<const uint16_t *>(a.v + (int64_t)(p.k0 + j) * a.v_token) + p.head() * D + kh * (D / 2);
+                        const uint16_t *v = reinterpret_cast<const uint16_t *>(a.v + (int64_t)(p.k0 + j) * a.v_token) + p.head() * D;
 #pragma unroll
-                        for (int e = 0; e < D / 2; ++e) {
+                        for (int e = 0; e < D; ++e) {
                             const uint32_t w = (uint32_t)v[e] << 16;
                             if ((w & 0x7f800000u) == 0x7f800000u) u[e] = __float_as_uint(__uint_as_float(u[e]) + __uint_as_float(w));
                         }
@@ -832,14 +824,14 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 // a piece: the products as they are, with the reference and the sum
                 const int64_t at = (int64_t)p.piece() * 256 + h * 128 + r;
                 if (live) {
-                    float *to = a.p_o + at * D + kh * (D / 2);
+                    float *to = a.p_o + at * D;
 #pragma unroll
-                    for (int e = 0; e < D / 2; e += 8) st32(to + e, u + e);
-                    if (kh == 0) a.p_ml[at] = make_float2(ref, l + fail);
+                    for (int e = 0; e < D; e += 8) st32(to + e, u + e);
+                    a.p_ml[at] = make_float2(ref, l + fail);
                 }
             } else if (live) {
 #pragma unroll
-                for (int i = 0; i < D / 64; ++i) {
+                for (int i = 0; i < D / 32; ++i) {
                     uint32_t o[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) o[e] = pack_bf16(__uint_as_float(u[32 * i + 2 * e]) * by, __uint_as_float(u[32 * i + 2 * e + 1]) * by);
@@ -855,20 +847,11 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             }
             done_with(it);
         }
-        // The two warps of a row meet at barriers that wait for both.  One that leaves early, because a wait has expired, meets the other
-        // until that one has left, too; each one's leaving is one arrival more, which frees the other if it waits there.
-        volatile int *left = reinterpret_cast<volatile int *>(bars + 46);
-        if (lane == 0) left[warp] = 1;
-        __threadfence_block();
-        __syncwarp();
-        asm volatile("bar.arrive %0, 64;" ::"r"(pair_bar) : "memory");
-        if (__any_sync(0xffffffffu, *bad != 0))
-            while (__any_sync(0xffffffffu, left[warp ^ 4] == 0)) (void)named_sync_or(pair_bar, 64, false);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 16) tmem_dealloc(tmem, 512);
+    if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
 // The pieces of a pair that several CTAs worked, weighted to their largest reference: blockIdx.x the pair's first piece, blockIdx.y 16 of
