@@ -299,8 +299,29 @@ __device__ __forceinline__ Pair piece_at(const PromptArgs &a, const OwnPlan &w, 
     x += c1 - c0;
     return q;
 }
+// Pair p's key heads, the pair's rank given, to the CTAs there and back: this CTA's to w.mine.
+__device__ __forceinline__ void deal(const PromptArgs &a, OwnPlan &w, Pair p, int rank) {
+    const int grid = (int)gridDim.x;
+    // this CTA's place in the rounds that the pair's key heads fall into
+    const int j0 = rank * a.kvh, j1 = j0 + a.kvh;
+    for (int round = j0 / grid; round * grid < j1 && round < kPtOwnRounds; ++round) {
+        const int j = round * grid + (round & 1 ? grid - 1 - (int)blockIdx.x : (int)blockIdx.x);
+        if (j < j0 || j >= j1) continue;
+        p.hk = j - j0;
+        w.mine[round] = p;
+        atomicMax(&w.n, round + 1);           // (no round is left out before the last)
+    }
+}
 __device__ __forceinline__ void plan_own(const PromptArgs &a, OwnPlan &w) {
     const int tid = threadIdx.x, lane = tid & 31;
+    if (a.B == 1 && !a.join) {                // one prompt: the later a pair, the longer
+        const Sequence s = sequence(a, 0);
+        if (tid == 0) w.n = 0, w.cut = false;
+        __syncthreads();
+        const int total = min(pairs_of(a, s), kPtOwnPairs);
+        if (tid < total) deal(a, w, pair_of(a, s, tid, 0), total - 1 - tid);
+        return;
+    }
     Sequence s;
     if (tid < a.B) {
         s = sequence(a, tid);
@@ -348,22 +369,9 @@ __device__ __forceinline__ void plan_own(const PromptArgs &a, OwnPlan &w) {
         w.cost[tid] = p.most();
     }
     __syncthreads();
-    const int grid = (int)gridDim.x;
-    if (a.join) {
-        // the CTAs' loads, and the chunks before every pair (over cost[], which the ranks have been read from)
-        if (cut_pairs(a, w, p, total)) return;
-    }
+    if (a.join && cut_pairs(a, w, p, total)) return;
     if (tid >= total) return;
-    const int rank = rank_of(a, w, p, total);
-    // this CTA's place in the rounds that the pair's key heads fall into
-    const int j0 = rank * a.kvh, j1 = j0 + a.kvh;
-    for (int round = j0 / grid; round * grid < j1 && round < kPtOwnRounds; ++round) {
-        const int j = round * grid + (round & 1 ? grid - 1 - (int)blockIdx.x : (int)blockIdx.x);
-        if (j < j0 || j >= j1) continue;
-        p.hk = j - j0;
-        w.mine[round] = p;
-        atomicMax(&w.n, round + 1);           // (no round is left out before the last)
-    }
+    deal(a, w, p, rank_of(a, w, p, total));
 }
 
 template <int D> struct PtCfg {
