@@ -102,7 +102,7 @@ def test_many_pairs(qd, lens, klens, qh, kvh, hd):
 @pytest.mark.parametrize("lens, klens, qh, kvh, hd", [
     ([3000], None, 1, 1, 128), ([5000], None, 2, 2, 64), ([1], [9000], 4, 2, 64), ([300], [7000], 8, 2, 128), ([128, 256], [4000, 8000], 3, 3, 64),
     ([1, 64, 0, 700], [4097, 6400, 10, 5000], 4, 4, 128), ([2300, 40, 1], None, 6, 2, 64), ([600] * 6, [3600] * 6, 8, 8, 128), ([250], [3000], 100, 1, 64),
-    ([50], [3], 1, 1, 64)])
+    ([50], [3], 1, 1, 64), ([600, 300], [100, 9000], 2, 2, 64), ([897, 400, 30], [141, 8000, 0], 3, 1, 128)])
 def test_pieces(qd, lens, klens, qh, kvh, hd):
     """Few pairs over long keys: cut into equal runs of chunks, joined."""
     st = make(lens, klens, qh, kvh, hd, slack=2)

@@ -98,6 +98,7 @@ struct __align__(16) Pair {
     __device__ __forceinline__ int piece() const { return (hk >> 20) - 1; }
     __device__ __forceinline__ int n(int h) const { return h ? n1 : n0; }
     __device__ __forceinline__ int most() const { return max(n0, n1); }
+    __device__ __forceinline__ int work() const { return max(1, most()); }   // a pair that sees nothing is written all the same
 };
 // The first chunk that the pair's first token does not see all of.
 __device__ __forceinline__ int first_edge(const Pair &p) { return p.lim0 > 0 ? p.lim0 / kPtKeys : 0; }
@@ -223,7 +224,7 @@ __device__ __forceinline__ int rank_of(const PromptArgs &a, const OwnPlan &w, co
 }
 // Every thread of the CTA: whether the pairs are cut, and then this CTA's pieces.  p: pair threadIdx.x, with key head 0.
 __device__ __noinline__ bool cut_pairs(const PromptArgs &a, OwnPlan &w, const Pair &p, int total) {
-    const int tid = threadIdx.x, lane = tid & 31, grid = (int)gridDim.x, own = tid < total ? p.most() : 0;
+    const int tid = threadIdx.x, lane = tid & 31, grid = (int)gridDim.x, own = tid < total ? p.work() : 0;
     if (tid < total) {
         const int rank = rank_of(a, w, p, total);
         int round = rank * a.kvh / grid, at = rank * a.kvh - round * grid;
@@ -282,7 +283,7 @@ __device__ __forceinline__ Pair piece_at(const PromptArgs &a, const OwnPlan &w, 
             hi = mid;
     }
     const Pair p = w.pairs[lo];
-    const int own = p.most(), y = x - w.before[lo] * a.kvh, hk = y / own, c0 = y - hk * own, c1 = min(own, c0 + w.x1 - x);
+    const int own = p.work(), y = x - w.before[lo] * a.kvh, hk = y / own, c0 = y - hk * own, c1 = min(own, c0 + w.x1 - x);
     // a piece's place among the two that a CTA can have: its run begins with it, or ends
     const int place = x == w.x0 ? 0 : 1;
     q = p;
